@@ -70,6 +70,13 @@ typedef enum pa_status {
 #define PA_DEV_BAD_SLOT 0x4       /* a slot >= num_blocks * block_size */
 #define PA_DEV_BAD_PAIR 0x8       /* a copy pair outside [0, num_blocks) */
 #define PA_DEV_TIMEOUT 0x10       /* a bounded wait inside a kernel gave up */
+#define PA_DEV_NO_BLOCKS 0x20     /* the free ring holds fewer blocks than a step needs */
+
+/* Element type of the calls that take one (2 bytes each). */
+typedef enum pa_dtype {
+    PA_F16 = 0, /* IEEE binary16 */
+    PA_BF16 = 1 /* bfloat16 */
+} pa_dtype;
 
 /* Human-readable name of a status code (static storage). */
 const char *pa_status_string(pa_status s);
@@ -417,6 +424,111 @@ pa_status pa_block_copy(pa_half *k_cache, pa_half *v_cache,
                         const int64_t *pairs, int N, int H, int D,
                         int block_size, int num_blocks, int32_t *status,
                         pa_stream_t stream);
+
+/* ===========================================================================
+ * One serving step with grouped K/V heads.
+ *
+ * The calls below serve models whose H query heads share Hkv <= H key/value
+ * heads (query head h reads K/V head h / (H / Hkv); H a multiple of Hkv), in
+ * fp16 or bf16 (pa_dtype), with the step's new tokens packed: sequence b's
+ * tokens are rows q_offsets[b] .. q_offsets[b+1]-1 of [T, heads, D] arrays,
+ * no padding between sequences.  They are, in the order a step uses them:
+ * the plan (blocks, slots and positions from the lengths), the rotation of
+ * queries and keys with the cache write, and attention of new prompts, of
+ * chunks over the cache, and of single tokens.  The cache is the pool of the
+ * calls above with Hkv heads: [num_blocks, block_size, Hkv, D].
+ *
+ * Packed q, k, v may be views of one projection's output: a token's heads
+ * are contiguous and 16-byte aligned, *_stride is the distance between
+ * tokens in elements, a multiple of 8 and at least heads * D.  Outputs of
+ * attention are contiguous.  None of these calls keeps anything between
+ * calls, so they may run on several streams and be captured; a workspace
+ * belongs to one call at a time.
+ * ========================================================================= */
+
+/* ---------------------------------------------------------------------------
+ * Step plan: block tables, slots and positions from the sequences' lengths.
+ *
+ * Sequence b has cached_lens[b] tokens in the cache and new_lens[b] more in
+ * this step (0: it does not run).  With have = ceil(cached / block_size) and
+ * want = ceil((cached + new) / block_size), entries have .. want-1 of its
+ * table row are filled with blocks from the free list, first in, first out,
+ * sequences in order (tutorial, "Block管理策略": Block Table, Free List, growth
+ * into new blocks); the others are left as they were.  Written besides:
+ *   context_lens [B]    int32  cached + new
+ *   q_offsets    [B+1]  int32  first packed row of each sequence, then the total
+ *   slot_mapping [T_max] int64 slot of each packed token (as pa_kv_cache_write
+ *                              takes it), -1 in the rows behind the last one
+ *   positions    [T_max] int32 its position, 0 behind the last one
+ *
+ * The free list is a ring: free_blocks [num_blocks] int32, free_state [2]
+ * int64 = blocks taken and blocks put so far, so it holds free_state[1] -
+ * free_state[0] blocks, the next one at index free_state[0] mod num_blocks.
+ * free_state_out [2] receives the state after the step and may be free_state
+ * itself; a caller returns a block by writing its id at free_state[1] mod
+ * num_blocks and adding one to free_state[1].
+ *
+ * All or nothing: when the blocks needed exceed those held
+ * (PA_DEV_NO_BLOCKS) or the new tokens exceed T_max (PA_DEV_BAD_CONTEXT), no
+ * block is taken and the step is empty: context_lens = cached, offsets 0,
+ * slots -1.  A sequence with a negative length, or that outgrows its table
+ * row, is flagged PA_DEV_BAD_CONTEXT, adds nothing and gets context 0.  An id
+ * outside [0, num_blocks), in the ring or in the block that new tokens
+ * continue, is flagged PA_DEV_BAD_BLOCK_ID: its tokens get slot -1 (and a
+ * fresh entry -1).
+ *
+ * block_size in {4, 8, 16, 32}; B at most 16384 (else PA_ERR_UNSUPPORTED);
+ * max_blocks_per_seq * block_size below 2^31 - 64.
+ * ------------------------------------------------------------------------- */
+pa_status pa_step_plan(const int32_t *cached_lens, const int32_t *new_lens, int B,
+                       int block_size, int num_blocks, int max_blocks_per_seq, int T_max,
+                       const int32_t *free_blocks, const int64_t *free_state,
+                       int32_t *block_tables, int32_t *context_lens, int32_t *q_offsets,
+                       int64_t *slot_mapping, int32_t *positions, int64_t *free_state_out,
+                       int32_t *status, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions with several axes, with the cache write.
+ *
+ * Pair i (of rotary_dim / 2) of every query and key head turns by
+ * angle = positions[axis(i)][t] * inv_freq(i):
+ *     x' = x cos(angle) - y sin(angle),  y' = y cos(angle) + x sin(angle)
+ * where (x, y) = (dims i, i + rotary_dim / 2), or (2i, 2i + 1) with
+ * interleaved != 0; dims from rotary_dim on pass unchanged.  One axis is the
+ * usual position of text, three are time, height and width of image and
+ * video tokens.  Sines and products are fp32 and exact to fp32 at every int32
+ * position (negative ones too); results are rounded once, to nearest even.
+ *
+ * Rotated q goes to q_out, rotated k to k_out unless that is NULL, and to
+ * k_cache at slot_mapping[t]; v is copied to v_cache there.  Negative slots
+ * skip the cache write (q_out and k_out are still written); a slot past the
+ * pool is flagged PA_DEV_BAD_SLOT and skipped; two tokens with the same slot:
+ * undefined which one lands.  k_cache, v_cache, v and slot_mapping may all be
+ * NULL: rotation only, k_out is then required.  q_out may be q and k_out may
+ * be k (the same pointer and stride), no other overlap is allowed.
+ *
+ * q [T, H, D], k and v [T, Hkv, D] with their strides; q_out, k_out likewise
+ * positions [n_axes, T] int32, n_axes 1..4
+ * table [rotary_dim / 2] from pa_rope_table, on the device, its axes below
+ *       n_axes (a larger one reads the last axis)
+ * D in {64, 128}, block_size in {4, 8, 16, 32}; rotary_dim a multiple of 16,
+ * 16 .. D.
+ *
+ * pa_rope_table (host): table[i] = inv_freq[i] / 2 pi as a 64-bit fraction of
+ * a turn, axes[i] (0..3; NULL: all 0) in its two low bits.  inv_freq in radians
+ * a position, finite and below 2^50 in magnitude; PA_ERR_INVALID otherwise.
+ * ------------------------------------------------------------------------- */
+pa_status pa_rope_table(const double *inv_freq, const int32_t *axes, int n, uint64_t *table);
+
+pa_status pa_rope_cache_write(const void *q, const void *k, const void *v,
+                              const int32_t *positions, const uint64_t *table,
+                              const int64_t *slot_mapping, int T, int H, int Hkv, int D,
+                              int rotary_dim, int n_axes, int interleaved, pa_dtype dtype,
+                              int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              int block_size, int num_blocks, void *q_out,
+                              int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                              void *k_cache, void *v_cache, int32_t *status,
+                              pa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,7 @@ PA_DEV_BAD_CONTEXT = 0x2
 PA_DEV_BAD_SLOT = 0x4
 PA_DEV_BAD_PAIR = 0x8
 PA_DEV_TIMEOUT = 0x10
+PA_DEV_NO_BLOCKS = 0x20
 
 # Every symbol include/pagedkv.h declares.
 EXPORTS = (
@@ -29,6 +30,7 @@ EXPORTS = (
     "pa_decode_static",
     "pa_decode_append", "pa_decode_shared_prefix", "pa_shared_prefix_groups",
     "pa_kv_cache_write_fp8", "pa_decode_fp8",
+    "pa_step_plan", "pa_rope_table", "pa_rope_cache_write",
 )
 
 # Size of the fixed scratch array behind pa_decode_static (PA_DECODE_STATIC_SCRATCH_BYTES).
@@ -45,6 +47,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
 
 
 def _bind(lib):
@@ -93,6 +96,13 @@ def _bind(lib):
     lib.pa_decode_fp8.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                                   ctypes.c_float, _P, _P, _SZ, _P, _P]
     lib.pa_decode_fp8.restype = _I
+    lib.pa_step_plan.argtypes = [_P, _P, _I, _I, _I, _I, _I] + [_P] * 10
+    lib.pa_step_plan.restype = _I
+    lib.pa_rope_table.argtypes = [_P, _P, _I, _P]
+    lib.pa_rope_table.restype = _I
+    lib.pa_rope_cache_write.argtypes = [_P] * 6 + [_I] * 8 + [_L] * 3 + [
+        _I, _I, _P, _L, _P, _L, _P, _P, _P, _P]
+    lib.pa_rope_cache_write.restype = _I
     return lib
 
 

@@ -146,4 +146,42 @@ size_t prefill_workspace_bytes(int B, int H, int Lq, int D);
 cudaError_t launch_prefill(const PrefillArgs& a, const void* k_cache, const void* v_cache,
                            cudaStream_t stream);
 
+// ---- one serving step with grouped K/V heads --------------------------------
+
+struct StepPlanArgs {
+  const int32_t* cached_lens;
+  const int32_t* new_lens;
+  const int32_t* free_blocks;  // ring of num_blocks ids
+  const int64_t* free_state;   // [2] blocks taken and put so far
+  int32_t* block_tables;
+  int32_t* context_lens;
+  int32_t* q_offsets;
+  int64_t* slot_mapping;
+  int32_t* positions;
+  int64_t* free_state_out;
+  int32_t* status;
+  int B, T_max, bs_log2, num_blocks, max_blocks;
+};
+int step_plan_max_batch();
+cudaError_t launch_step_plan(const StepPlanArgs& a, cudaStream_t stream);
+
+struct RopeArgs {
+  const void* q;  // [T, H, D] and [T, Hkv, D] rows, strides in elements between tokens
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  const int32_t* positions;        // [n_axes, T]
+  const unsigned long long* table;  // [R / 2] turns per position, axis in the low two bits
+  const int64_t* slots;
+  void* q_out;
+  void* k_out;    // may be null
+  void* k_cache;  // both null: rotation only
+  void* v_cache;
+  int32_t* status;
+  long long n_slots;
+  int T, H, Hkv, D, R, n_axes;
+  bool bf16, interleaved;
+};
+cudaError_t launch_rope_write(const RopeArgs& a, cudaStream_t stream);
+
 }  // namespace pk
