@@ -530,6 +530,81 @@ pa_status pa_rope_cache_write(const void *q, const void *k, const void *v,
                               void *k_cache, void *v_cache, int32_t *status,
                               pa_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention over whole prompts (packed, causal, grouped heads).
+ *
+ * Token i of sequence b attends to tokens 0 .. i of its own sequence, K and V
+ * being packed rows like q (no cache is read):
+ *     s_j = scale * q[t,h,:] . k[j,h/G,:],  out[t,h,:] = softmax(s) v[.,h/G,:]
+ * with G = H / Hkv, scores and sums in fp32; the softmax weights are rounded to
+ * the 16-bit type for their product with v, the result once more, to nearest
+ * even.  Rows before q_offsets[0] and behind q_offsets[B] are left as they
+ * were.  Other sequences' rows, NaN included, never reach a result.
+ *
+ * q [T, H, D], k and v [T, Hkv, D] with their strides; out [T, H, D]
+ * q_offsets [B+1] int32, rising, within [0, T]: a sequence breaking that is
+ *           flagged PA_DEV_BAD_CONTEXT and not computed (offsets that make
+ *           sequences overlap leave their rows undefined)
+ * D in {64, 128}; H / Hkv at most 128 (else PA_ERR_UNSUPPORTED); scale > 0.
+ * ------------------------------------------------------------------------- */
+pa_status pa_prompt_attention(const void *q, const void *k, const void *v,
+                              const int32_t *q_offsets, int B, int T, int H, int Hkv, int D,
+                              pa_dtype dtype, int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, float scale, void *out, int32_t *status,
+                              pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of packed chunks over the paged cache (grouped heads).
+ *
+ * Sequence b's q_len = q_offsets[b+1] - q_offsets[b] queries are its last
+ * positions: query i is at n - q_len + i, n = context_lens[b], and attends to
+ * keys 0 .. n - q_len + i of the cache (which holds the chunk's own K/V
+ * already).  Otherwise as pa_prompt_attention; the cache as in pa_decode with
+ * Hkv heads.  A context outside [q_len, min(max_context_len,
+ * max_blocks_per_seq * block_size)] is flagged PA_DEV_BAD_CONTEXT and its rows
+ * are zeros; a bad block id reads as zeros, flagged PA_DEV_BAD_BLOCK_ID.
+ *
+ * D in {64, 128}; block_size in {8, 16, 32}; max_context_len at most
+ * max_blocks_per_seq * block_size; (num_blocks + 1) * block_size * Hkv below
+ * 2^31.  workspace (16-byte aligned, may be NULL): with at least
+ * pa_chunk_attention_workspace_size(...) bytes, few and long chunks are cut
+ * into key ranges merged by log-sum-exp, which fills the GPU; without it every
+ * unit runs whole (same result up to rounding).  Smaller and not NULL:
+ * PA_ERR_WORKSPACE.
+ * ------------------------------------------------------------------------- */
+size_t pa_chunk_attention_workspace_size(int B, int T, int H, int Hkv, int D,
+                                         int max_context_len);
+
+pa_status pa_chunk_attention(const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *block_tables, const int32_t *context_lens,
+                             const int32_t *q_offsets, int B, int T, int H, int Hkv, int D,
+                             pa_dtype dtype, int64_t q_stride, int block_size, int num_blocks,
+                             int max_blocks_per_seq, int max_context_len, float scale,
+                             void *out, void *workspace, size_t workspace_bytes,
+                             int32_t *status, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Decode with grouped heads: one query token per sequence.
+ *
+ * pa_decode's result where G = H / Hkv query heads read each K/V head, which
+ * comes from memory once for all of them (up to 16; more take it once for
+ * every 16).  Arguments, errors and the workspace rule as for pa_decode, with
+ * q and out [B, H, D] and the cache [num_blocks, block_size, Hkv, D] in dtype;
+ * a context past max_context_len is flagged PA_DEV_BAD_CONTEXT and cut to it, a
+ * negative one gives zeros.  partition_tokens: a multiple of 64 up to 2048, or
+ * 0 to choose.  D in {64, 128}; block_size in {8, 16, 32}; B at most 65535;
+ * any finite scale; (num_blocks + 1) * block_size * Hkv below 2^31.
+ * ------------------------------------------------------------------------- */
+size_t pa_decode_grouped_workspace_size(int B, int H, int Hkv, int D, int block_size,
+                                        int max_context_len, int partition_tokens);
+
+pa_status pa_decode_grouped(const void *q, const void *k_cache, const void *v_cache,
+                            const int32_t *block_tables, const int32_t *context_lens, int B,
+                            int H, int Hkv, int D, pa_dtype dtype, int block_size,
+                            int num_blocks, int max_blocks_per_seq, int max_context_len,
+                            int partition_tokens, float scale, void *out, void *workspace,
+                            size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

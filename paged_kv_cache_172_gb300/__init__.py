@@ -15,5 +15,7 @@ from ._lib import (  # noqa: F401
     pa_prefill_chunk, pa_prefill_chunk_varlen, pa_prefill_workspace_size, status_string,
 )
 from .grouped import (  # noqa: F401
-    StepPlan, pa_rope_cache_write, pa_rope_table, pa_step_plan,
+    StepPlan, pa_chunk_attention, pa_chunk_attention_workspace_size, pa_decode_grouped,
+    pa_decode_grouped_workspace_size, pa_prompt_attention, pa_rope_cache_write, pa_rope_table,
+    pa_step_plan,
 )

@@ -30,7 +30,9 @@ EXPORTS = (
     "pa_decode_static",
     "pa_decode_append", "pa_decode_shared_prefix", "pa_shared_prefix_groups",
     "pa_kv_cache_write_fp8", "pa_decode_fp8",
-    "pa_step_plan", "pa_rope_table", "pa_rope_cache_write",
+    "pa_step_plan", "pa_rope_table", "pa_rope_cache_write", "pa_prompt_attention",
+    "pa_chunk_attention_workspace_size", "pa_chunk_attention",
+    "pa_decode_grouped_workspace_size", "pa_decode_grouped",
 )
 
 # Size of the fixed scratch array behind pa_decode_static (PA_DECODE_STATIC_SCRATCH_BYTES).
@@ -103,6 +105,18 @@ def _bind(lib):
     lib.pa_rope_cache_write.argtypes = [_P] * 6 + [_I] * 8 + [_L] * 3 + [
         _I, _I, _P, _L, _P, _L, _P, _P, _P, _P]
     lib.pa_rope_cache_write.restype = _I
+    lib.pa_prompt_attention.argtypes = [_P] * 4 + [_I] * 6 + [_L] * 3 + [ctypes.c_float, _P, _P,
+                                                                        _P]
+    lib.pa_prompt_attention.restype = _I
+    lib.pa_chunk_attention_workspace_size.argtypes = [_I] * 6
+    lib.pa_chunk_attention_workspace_size.restype = _SZ
+    lib.pa_chunk_attention.argtypes = [_P] * 6 + [_I] * 6 + [_L] + [_I] * 4 + [
+        ctypes.c_float, _P, _P, _SZ, _P, _P]
+    lib.pa_chunk_attention.restype = _I
+    lib.pa_decode_grouped_workspace_size.argtypes = [_I] * 7
+    lib.pa_decode_grouped_workspace_size.restype = _SZ
+    lib.pa_decode_grouped.argtypes = [_P] * 5 + [_I] * 10 + [ctypes.c_float, _P, _P, _SZ, _P, _P]
+    lib.pa_decode_grouped.restype = _I
     return lib
 
 

@@ -145,4 +145,189 @@ pa_status pa_rope_cache_write(const void* q, const void* k, const void* v,
   return launched(pk::launch_rope_write(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Shared checks of the attention calls; PA_OK to go on.
+static pa_status attention_args(int B, int H, int Hkv, int D, int dtype) {
+  if (B < 0 || !heads_ok(H, Hkv) || !dtype_ok(dtype)) return PA_ERR_INVALID;
+  if (D != 64 && D != 128) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+static pa_status cache_args(const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                            const int32_t* context_lens, int Hkv, int block_size, int num_blocks,
+                            int max_blocks, int max_context) {
+  if (!k_cache || !v_cache || !block_tables || !context_lens || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !pool_ok(num_blocks, block_size, Hkv) || max_blocks <= 0 ||
+      max_context < 0 || (long long)max_context > (long long)max_blocks * block_size)
+    return PA_ERR_INVALID;
+  return PA_OK;
+}
+
+static bool paged_block(int bs) { return bs == 8 || bs == 16 || bs == 32; }
+
+// Prompts (block_tables null) and chunks.
+static pa_status packed_impl(pk::GroupedArgs& a, const void* q, const void* k, const void* v,
+                             int64_t qs, int64_t ks, int64_t vs, float scale, int max_keys,
+                             pa_stream_t stream) {
+  if (!isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID;
+  a.G = a.H / a.Hkv;
+  a.span = pk::grouped_span(a.G);
+  if (a.span == 0) return PA_ERR_UNSUPPORTED;
+  if (a.B == 0 || a.T == 0) return PA_OK;
+  if (!a.q_offsets || !a.out || !aligned16(a.out) || !rows_ok(q, qs, a.H, a.D))
+    return PA_ERR_INVALID;
+  a.min_part_tiles = pk::kGroupedMinPartTiles;
+  // A sequence whose context is bad still has its ql <= T rows in the plan.
+  a.max_tiles = (int)(((long long)(max_keys > a.T ? max_keys : a.T) + 127) / 128);
+  const long long units = (long long)a.T / a.span + a.B;
+  if (units * a.Hkv * a.split >= (1LL << 31)) return PA_ERR_INVALID;
+  a.max_units = (int)units;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  const cudaError_t e =
+      pk::launch_grouped(a, q, k, v, qs, ks, vs, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaErrorInvalidValue ? PA_ERR_INVALID : launched(e);
+}
+
+pa_status pa_prompt_attention(const void* q, const void* k, const void* v,
+                              const int32_t* q_offsets, int B, int T, int H, int Hkv, int D,
+                              pa_dtype dtype, int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, float scale, void* out, int32_t* status,
+                              pa_stream_t stream) {
+  const pa_status st = attention_args(B, H, Hkv, D, dtype);
+  if (st != PA_OK) return st;
+  if (T < 0) return PA_ERR_INVALID;
+  if (B > 0 && T > 0 && (!rows_ok(k, k_stride, Hkv, D) || !rows_ok(v, v_stride, Hkv, D)))
+    return PA_ERR_INVALID;
+  pk::GroupedArgs a = {};
+  a.q_offsets = q_offsets;
+  a.out = out;
+  a.status = status;
+  a.B = B;
+  a.T = T;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.split = 1;
+  a.bf16 = dtype == PA_BF16;
+  return packed_impl(a, q, k, v, q_stride, k_stride, v_stride, scale, T, stream);
+}
+
+size_t pa_chunk_attention_workspace_size(int B, int T, int H, int Hkv, int D,
+                                         int max_context_len) {
+  if (B <= 0 || T <= 0 || !heads_ok(H, Hkv) || (D != 64 && D != 128) || max_context_len <= 0)
+    return 0;
+  return pk::grouped_workspace_bytes(B, T, H, Hkv, D, max_context_len);
+}
+
+pa_status pa_chunk_attention(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, const int32_t* context_lens,
+                             const int32_t* q_offsets, int B, int T, int H, int Hkv, int D,
+                             pa_dtype dtype, int64_t q_stride, int block_size, int num_blocks,
+                             int max_blocks_per_seq, int max_context_len, float scale, void* out,
+                             void* workspace, size_t workspace_bytes, int32_t* status,
+                             pa_stream_t stream) {
+  pa_status st = attention_args(B, H, Hkv, D, dtype);
+  if (st != PA_OK) return st;
+  if (!paged_block(block_size)) return PA_ERR_UNSUPPORTED;
+  if (T < 0) return PA_ERR_INVALID;
+  pk::GroupedArgs a = {};
+  a.split = 1;
+  if (B > 0 && T > 0) {
+    st = cache_args(k_cache, v_cache, block_tables, context_lens, Hkv, block_size, num_blocks,
+                    max_blocks_per_seq, max_context_len);
+    if (st != PA_OK) return st;
+    if (workspace != nullptr) {
+      if (!aligned16(workspace)) return PA_ERR_INVALID;
+      if (workspace_bytes <
+          pk::grouped_workspace_bytes(B, T, H, Hkv, D, max_context_len))
+        return PA_ERR_WORKSPACE;
+      a.split = pk::grouped_split(B, T, H, Hkv, max_context_len);
+    }
+  }
+  a.q_offsets = q_offsets;
+  a.context_lens = context_lens;
+  a.block_tables = block_tables;
+  a.out = out;
+  a.ws = static_cast<float*>(workspace);
+  a.status = status;
+  a.B = B;
+  a.T = T;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_context = max_context_len;
+  a.bf16 = dtype == PA_BF16;
+  return packed_impl(a, q, k_cache, v_cache, q_stride, 0, 0, scale, max_context_len, stream);
+}
+
+static int decode_partition(int B, int H, int Hkv, int max_context, int partition_tokens) {
+  if (max_context < 1) max_context = 1;  // every row is empty: one partition
+  return partition_tokens > 0 ? partition_tokens
+                              : pk::grouped_decode_partition(B, H, Hkv, max_context);
+}
+
+size_t pa_decode_grouped_workspace_size(int B, int H, int Hkv, int D, int block_size,
+                                        int max_context_len, int partition_tokens) {
+  if (B <= 0 || !heads_ok(H, Hkv) || (D != 64 && D != 128) || !paged_block(block_size) ||
+      max_context_len <= 0 || partition_tokens < 0)
+    return 0;
+  const int pt = decode_partition(B, H, Hkv, max_context_len, partition_tokens);
+  const long long parts = ((long long)max_context_len + pt - 1) / pt;
+  return parts <= 1 ? 0 : (size_t)B * H * parts * (D + 2) * sizeof(float);
+}
+
+pa_status pa_decode_grouped(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, const int32_t* context_lens, int B,
+                            int H, int Hkv, int D, pa_dtype dtype, int block_size, int num_blocks,
+                            int max_blocks_per_seq, int max_context_len, int partition_tokens,
+                            float scale, void* out, void* workspace, size_t workspace_bytes,
+                            int32_t* status, pa_stream_t stream) {
+  pa_status st = attention_args(B, H, Hkv, D, dtype);
+  if (st != PA_OK) return st;
+  if (!paged_block(block_size)) return PA_ERR_UNSUPPORTED;
+  if (B > 65535 || !isfinite(scale) || partition_tokens < 0 || partition_tokens % 64 != 0 ||
+      partition_tokens > 2048)
+    return PA_ERR_INVALID;
+  if (B == 0) return PA_OK;
+  st = cache_args(k_cache, v_cache, block_tables, context_lens, Hkv, block_size, num_blocks,
+                  max_blocks_per_seq, max_context_len);
+  if (st != PA_OK) return st;
+  if (!q || !out || !aligned16(q) || !aligned16(out)) return PA_ERR_INVALID;
+  pk::GroupedDecodeArgs a = {};
+  a.part_tokens = decode_partition(B, H, Hkv, max_context_len, partition_tokens);
+  const long long parts =
+      ((long long)(max_context_len > 0 ? max_context_len : 1) + a.part_tokens - 1) /
+      a.part_tokens;
+  if (parts > 65535) return PA_ERR_INVALID;
+  a.num_parts = (int)parts;
+  if (parts > 1) {
+    const size_t need = (size_t)B * H * parts * (D + 2) * sizeof(float);
+    if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PA_ERR_INVALID;
+    a.ws_o = static_cast<float*>(workspace);
+    a.ws_ml = a.ws_o + (size_t)B * H * parts * D;
+  }
+  a.q = q;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.out = out;
+  a.status = status;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.G = H / Hkv;
+  a.D = D;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_context = max_context_len;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.bf16 = dtype == PA_BF16;
+  const cudaError_t e = pk::launch_grouped_decode(a, k_cache, v_cache,
+                                                  reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaErrorInvalidValue ? PA_ERR_INVALID : launched(e);
+}
+
 }  // extern "C"

@@ -1,0 +1,521 @@
+// grouped_decode.cu -- decode attention with grouped K/V heads over the paged
+// cache: one query token per sequence, G = H / Hkv query heads reading the same
+// K/V head, fp16 or bf16.
+//
+//     s_jg = scale * q_g . k_j,  out_g = sum_j 2^(..) v_j / sum_j 2^(..)
+//
+// Bound: HBM.  A K and a V row of D values serve G heads, so the work per byte
+// is G times that of one head per K/V head: 2 G multiply-adds a byte, too much
+// for scalar arithmetic at 8 TB/s beyond two or three heads, and far too little
+// to fill the tcgen05 tiles of 128 rows.  Warp MMAs (m16n8k16) sit between:
+// with the keys as the 16 rows and the heads as the 8 columns,
+//     S^T [16 keys x 8 heads] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16] P^T,
+// a group of up to 8 heads wastes no rows on padding to 16 (two column tiles
+// serve up to 16 heads, more heads take more CTAs), K is the row operand as it
+// lies in the cache, V^T comes from transposing ldmatrix loads, and the
+// accumulators of S^T become the column operand of the second product by one
+// 8 x 8 transposition in registers (movmatrix).
+//
+// One CTA takes one partition of a sequence's keys for one K/V head; its four
+// warps take every fourth stage of 16 keys, each through its own ring of TMA
+// boxes (K and V, 8 KB a stage at D = 128), with its own running maximum and
+// sums, and merge through shared memory at the end.  Three CTAs share an SM
+// (72 KB of shared memory each), 192 KB of loads in flight.  Contexts longer
+// than a partition leave (o, m, l) in the workspace, merged by log-sum-exp in a
+// second, dependent launch.
+//
+// Rounding: scores, maxima, sums and outputs in fp32; the weights 2^(s - m) <= 1
+// are rounded to the cache's type for the second product, the result once more.
+#include <cuda_bf16.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "pk_common.cuh"
+#include "pk_internal.h"
+
+namespace pk {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kKeys = 16;   // keys of a stage
+constexpr int kRing = 2;    // stages in flight per warp
+constexpr int kSpan = kWarps * kKeys;   // keys the CTA takes a round
+constexpr int kMaxPart = 32 * kSpan;    // a warp's table entries sit one per lane
+
+template <int D>
+struct DCfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int GROUP = HALVES * 1024;  // 8 keys: the atoms of dims 0-63, 64-127
+  static constexpr int TILE = 2 * GROUP;       // K (or V) of a stage
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int RING_BYTES = kWarps * kRing * STAGE;
+};
+
+// Shared memory: the rings (reused for the merge of the warps), then per warp
+// and head (m, l), then the barriers.
+template <int D, int NT>
+constexpr int merge_bytes() { return kWarps * NT * 8 * D * 4; }
+template <int D, int NT>
+constexpr int smem_bytes() {
+  const int ring = DCfg<D>::RING_BYTES, mrg = merge_bytes<D, NT>();
+  return (ring > mrg ? ring : mrg) + kWarps * NT * 8 * 8 + kWarps * kRing * 8 + 1024;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Transposes an 8 x 8 matrix of 16-bit values held two per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T round_to(float x) {
+  if constexpr (std::is_same<T, __half>::value)
+    return __float2half_rn(x);
+  else
+    return __float2bfloat16_rn(x);
+}
+
+// NT column tiles of 8 heads; grid (Hkv * head chunks, B, partitions).
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads)
+    grouped_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+                          const __grid_constant__ CUtensorMap vmap, const GroupedDecodeArgs a) {
+  using C = DCfg<D>;
+  constexpr int HEADS = NT * 8;
+  constexpr int KS = D / 16;  // 16-dim steps of either product
+  extern __shared__ uint8_t smem_dyn[];
+  const uint32_t raw = smem_u32(smem_dyn);
+  uint8_t* smem = smem_dyn + (((raw + 1023u) & ~1023u) - raw);
+  constexpr int kRoom =
+      C::RING_BYTES > merge_bytes<D, NT>() ? C::RING_BYTES : merge_bytes<D, NT>();
+  float* s_o = reinterpret_cast<float*>(smem);                  // [warp][head][D], after the rings
+  float2* s_ml = reinterpret_cast<float2*>(smem + kRoom);       // [warp][head]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRoom + kWarps * HEADS * 8);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (a.G + HEADS - 1) / HEADS;
+  const int hkv = blockIdx.x / chunks, g0 = (blockIdx.x % chunks) * HEADS;
+  const int heads = min(HEADS, a.G - g0);  // live columns
+  const int h0 = hkv * a.G + g0;           // first query head
+  const int b = blockIdx.y, part = blockIdx.z;
+  uint64_t* bar = bars + warp * kRing;
+
+  pdl_wait();
+  pdl_launch_dependents();
+  int n = a.context_lens[b];
+  if (n < 0 || n > a.max_context) {
+    if (threadIdx.x == 0 && part == 0) flag_status(a.status, PA_DEV_BAD_CONTEXT);
+    n = n < 0 ? 0 : a.max_context;
+  }
+  const int k0 = part * a.part_tokens;
+  if (k0 >= n) {
+    if (part == 0)  // an empty context: zero rows
+      for (int i = threadIdx.x; i < heads * D; i += kThreads)
+        static_cast<T*>(a.out)[((size_t)b * a.H + h0) * D + i] = round_to<T>(0.f);
+    return;
+  }
+  const int k1 = min(n, k0 + a.part_tokens);
+  const bool alone = n <= a.part_tokens;  // the only partition of its sequence
+  // This warp's stages: keys k0 + (warp + 4 i) * 16 ...
+  const int n_st = (k1 - k0 + kKeys - 1) / kKeys;
+  const int mine = n_st > warp ? (n_st - warp + kWarps - 1) / kWarps : 0;
+
+  // Lane i holds the pool row of the first slot of the warp's i-th stage, and
+  // for 8-token blocks that of its second half.
+  const int bs = a.block_size;
+  int row_lo = 0, row_hi = 0;
+  if (lane < mine) {
+    const int key = k0 + (warp + kWarps * lane) * kKeys;
+    auto pool_row = [&](int j) {
+      if (j >= n) return a.num_blocks * bs * a.Hkv;  // past the sequence: outside the map
+      int phys = a.block_tables[(size_t)b * a.max_blocks + j / bs];
+      if (phys < 0 || phys >= a.num_blocks) {
+        flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+        phys = a.num_blocks;
+      }
+      return phys * bs * a.Hkv;
+    };
+    row_lo = pool_row(key);
+    if (bs < kKeys) row_hi = pool_row(key + 8);
+  }
+  if (lane == 0) {
+    for (int s = 0; s < kRing; ++s) mbar_init(&bar[s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+
+  uint8_t* ring = smem + warp * kRing * C::STAGE;
+  auto request = [&](int i) {
+    const int lo = __shfl_sync(kAll, row_lo, i), hi = __shfl_sync(kAll, row_hi, i);
+    if (lane == 0) {
+      uint8_t* st = ring + (i % kRing) * C::STAGE;
+      uint64_t* full = &bar[i % kRing];
+      mbar_arrive_expect_tx(full, C::STAGE);
+      if (bs >= kKeys) {  // a box of two key groups, from the stage's place in the block
+        const int grp = ((k0 + (warp + kWarps * i) * kKeys) % bs) / 8;
+        tma_load_5d(st, &kmap, 0, 0, 0, grp, lo + hkv, full);
+        tma_load_5d(st + C::TILE, &vmap, 0, 0, 0, grp, lo + hkv, full);
+      } else {  // two blocks of one key group
+        tma_load_5d(st, &kmap, 0, 0, 0, 0, lo + hkv, full);
+        tma_load_5d(st + C::GROUP, &kmap, 0, 0, 0, 0, hi + hkv, full);
+        tma_load_5d(st + C::TILE, &vmap, 0, 0, 0, 0, lo + hkv, full);
+        tma_load_5d(st + C::TILE + C::GROUP, &vmap, 0, 0, 0, 0, hi + hkv, full);
+      }
+    }
+  };
+  for (int i = 0; i < kRing && i < mine; ++i) request(i);
+
+  // Q^T as the column operand: lane holds head lane / 4, dims 2 (lane % 4) + {0, 1}
+  // and those + 8 of each 16-dim step.
+  const int col = lane >> 2, two = 2 * (lane & 3);
+  uint32_t qf[NT][KS][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int g = t * 8 + col;
+    const T* qr = static_cast<const T*>(a.q) + ((size_t)b * a.H + h0 + g) * D + two;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qf[t][ks][e] =
+            g < heads ? *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 8 * e) : 0u;
+  }
+
+  float o[NT][KS][4];  // O^T: dims lane / 4 (+ 8), heads two, two + 1
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) o[t][ks][0] = o[t][ks][1] = o[t][ks][2] = o[t][ks][3] = 0.f;
+  float m[NT][2], l[NT][2];  // heads two, two + 1; l: this lane's keys only
+#pragma unroll
+  for (int t = 0; t < NT; ++t) m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
+  const float sl2 = a.scale_log2;
+  const int mi = lane >> 3, rr = lane & 7;  // ldmatrix: matrix and row of this lane
+  bool ok = true;
+  int done = 0;
+  for (; done < mine; ++done) {
+    if (!__all_sync(kAll, mbar_wait(&bar[done % kRing], (done / kRing) & 1))) {
+      ok = false;
+      break;
+    }
+    uint8_t* st = ring + (done % kRing) * C::STAGE;
+    const uint32_t kb = smem_u32(st), vb = kb + C::TILE;
+    const int key0 = k0 + (warp + kWarps * done) * kKeys;
+    const int live = k1 - key0;  // keys of this stage, if below 16
+    if (live < kKeys) {
+      // V rows past the keys hold anything, and 0 * NaN is NaN: zero them.
+      for (int i = lane; i < (kKeys - live) * (D / 8); i += 32) {
+        const int r = live + i / (D / 8), c = i % (D / 8);
+        *reinterpret_cast<uint4*>(st + C::TILE + (r >> 3) * C::GROUP + (c >> 3) * 1024 +
+                                  (r & 7) * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncwarp();
+    }
+    // 16-byte chunk c of key r: chunk c ^ (r & 7) of the row in its swizzled atom
+    float s[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int c = 2 * ks + (mi >> 1);
+      uint32_t kf[4];  // keys 0-7 / 8-15 (mi & 1), dims 0-7 / 8-15 (mi >> 1)
+      ldsm4(kb + (mi & 1) * C::GROUP + (c >> 3) * 1024 + rr * 128 + (((c & 7) ^ rr) << 4), kf);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma<T>(s[t], kf, qf[t][ks][0], qf[t][ks][1]);
+    }
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      // scaled before they are masked: any finite scale, 0 and below included
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] *= sl2;
+      if (live < kKeys) {
+        if (col >= live) s[t][0] = s[t][1] = -INFINITY;
+        if (col + 8 >= live) s[t][2] = s[t][3] = -INFINITY;
+      }
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(s[t][e], s[t][2 + e]);
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+        const float m_new = fmaxf(m[t][e], mx);  // key 0 of a stage is never masked
+        const float alpha = ex2_approx(m[t][e] - m_new);
+        m[t][e] = m_new;
+        p[e] = ex2_approx(s[t][e] - m_new);
+        p[2 + e] = ex2_approx(s[t][2 + e] - m_new);
+        l[t][e] = l[t][e] * alpha + (p[e] + p[2 + e]);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          o[t][ks][e] *= alpha;
+          o[t][ks][2 + e] *= alpha;
+        }
+      }
+      pf[t][0] = transpose8(pack<T>(p[0], p[1]));  // keys 0-7: now two keys of head lane / 4
+      pf[t][1] = transpose8(pack<T>(p[2], p[3]));
+    }
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int c = 2 * ks + (mi & 1);
+      uint32_t vf[4];  // dims 0-7 / 8-15 (mi & 1), keys 0-7 / 8-15 (mi >> 1), transposed
+      ldsm4_t(vb + (mi >> 1) * C::GROUP + (c >> 3) * 1024 + rr * 128 + (((c & 7) ^ rr) << 4), vf);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma<T>(o[t][ks], vf, pf[t][0], pf[t][1]);
+    }
+    __syncwarp();
+    if (done + kRing < mine) {
+      if (lane == 0) fence_proxy_async_smem();  // this stage's reads before its refill
+      request(done + kRing);
+    }
+  }
+  if (!ok) {
+    if (lane == 0) flag_status(a.status, PA_DEV_TIMEOUT);
+    for (int i = done; i < mine && i < done + kRing; ++i)
+      mbar_wait(&bar[i % kRing], (i / kRing) & 1);
+  }
+  // Sums over the lanes that share a head.
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = l[t][e];
+      x += __shfl_xor_sync(kAll, x, 4);
+      x += __shfl_xor_sync(kAll, x, 8);
+      x += __shfl_xor_sync(kAll, x, 16);
+      l[t][e] = x;
+    }
+  __syncthreads();  // every warp's stages are read: their room takes the outputs
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int g = t * 8 + two + e;
+      float* dst = s_o + ((size_t)warp * HEADS + g) * D + col;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        dst[ks * 16] = o[t][ks][e];
+        dst[ks * 16 + 8] = o[t][ks][2 + e];
+      }
+      if (col == 0) s_ml[warp * HEADS + g] = make_float2(m[t][e], l[t][e]);
+    }
+  }
+  __syncthreads();
+  // Thread: one dim pair of every (kThreads / (D / 2))-th head.
+  constexpr int kPairs = D / 2, kStep = kThreads / kPairs;
+  const int d = 2 * (threadIdx.x % kPairs);
+  for (int g = threadIdx.x / kPairs; g < heads; g += kStep) {
+    float2 ml[kWarps];
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      ml[w] = s_ml[w * HEADS + g];
+      if (ml[w].y != 0.f) M = fmaxf(M, ml[w].x);
+    }
+    float L = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (ml[w].y == 0.f) continue;  // a warp without stages
+      const float wgt = ex2_approx(ml[w].x - M);
+      const float2 v = *reinterpret_cast<const float2*>(s_o + ((size_t)w * HEADS + g) * D + d);
+      L += wgt * ml[w].y;
+      x += wgt * v.x;
+      y += wgt * v.y;
+    }
+    const size_t row = (size_t)b * a.H + h0 + g;
+    if (alone) {
+      const float inv = L != 0.f ? 1.f / L : 0.f;
+      *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D + d) =
+          pack<T>(x * inv, y * inv);
+    } else {
+      const size_t pr = row * a.num_parts + part;
+      *reinterpret_cast<float2*>(a.ws_o + pr * D + d) = make_float2(x, y);
+      if (d == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * pr) = make_float2(M, L);
+    }
+  }
+}
+
+// Merges the partitions of a (sequence, head): W warps take every W-th one.
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(32 * W) grouped_decode_merge(const GroupedDecodeArgs a) {
+  constexpr int EPL = D / 32;
+  __shared__ float s_o[W][D];
+  __shared__ float2 s_ml[W];
+  pdl_wait();
+  pdl_launch_dependents();
+  const size_t row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = min(max(a.context_lens[row / a.H], 0), a.max_context);
+  if (n <= a.part_tokens) return;  // written by its only partition (or empty)
+  const int parts = (n + a.part_tokens - 1) / a.part_tokens;
+  float M = -INFINITY, L = 0.f, o[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+  constexpr int kAhead = 4;  // partitions whose loads are in flight together
+  for (int p0 = warp; p0 < parts; p0 += kAhead * W) {
+    float2 ml[kAhead];
+    float v[kAhead][EPL];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int p = p0 + k * W;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (p < parts) {
+        const size_t pr = row * a.num_parts + p;
+        ml[k] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * pr);
+#pragma unroll
+        for (int e = 0; e < EPL; e += 2) {
+          const float2 f = *reinterpret_cast<const float2*>(a.ws_o + pr * D + lane * EPL + e);
+          v[k][e] = f.x, v[k][e + 1] = f.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (ml[k].y == 0.f) continue;
+      const float m_new = fmaxf(M, ml[k].x);
+      const float keep = ex2_approx(M - m_new), take = ex2_approx(ml[k].x - m_new);
+      M = m_new;
+      L = L * keep + ml[k].y * take;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] = o[e] * keep + v[k][e] * take;
+    }
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) s_o[warp][lane * EPL + e] = o[e];
+    if (lane == 0) s_ml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (warp > 0) return;
+    float mx = M;
+#pragma unroll
+    for (int w = 1; w < W; ++w)
+      if (s_ml[w].y != 0.f) mx = fmaxf(mx, s_ml[w].x);
+    float keep = L != 0.f ? ex2_approx(M - mx) : 0.f;
+    L *= keep;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] *= keep;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      if (s_ml[w].y == 0.f) continue;
+      const float take = ex2_approx(s_ml[w].x - mx);
+      L += s_ml[w].y * take;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] += s_o[w][lane * EPL + e] * take;
+    }
+  }
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  T* dst = static_cast<T*>(a.out) + row * D + lane * EPL;
+#pragma unroll
+  for (int e = 0; e < EPL; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack<T>(o[e] * inv, o[e + 1] * inv);
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_t(const GroupedDecodeArgs& a, const void* k_cache, const void* v_cache,
+                     cudaStream_t stream) {
+  using C = DCfg<D>;
+  using u64 = unsigned long long;
+  CUtensorMap kmap, vmap;
+  // Rows (slot, head) of D values; inside a block (64 dims, 8 keys, halves, key
+  // groups), at its first slot's row.
+  const u64 rowb = (u64)D * 2, tok = rowb * a.Hkv;
+  const u64 dims[5] = {64, 8, (u64)C::HALVES, (u64)a.block_size / 8,
+                       (u64)a.num_blocks * a.block_size * a.Hkv};
+  const u64 st[4] = {tok, 128, 8 * tok, rowb};
+  const unsigned box[5] = {64, 8, (unsigned)C::HALVES, a.block_size >= kKeys ? 2u : 1u, 1};
+  cudaError_t e = make_map_5d(&kmap, k_cache, dims, st, box, true);
+  if (e == cudaSuccess) e = make_map_5d(&vmap, v_cache, dims, st, box, true);
+  if (e != cudaSuccess) return e;
+  constexpr auto kern = grouped_decode_kernel<T, D, NT>;
+  constexpr int smem = smem_bytes<D, NT>();
+  e = ensure_dynamic_smem<kern>(smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.Hkv * ((a.G + 8 * NT - 1) / (8 * NT)), a.B, a.num_parts);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, a);
+  if (e != cudaSuccess || a.num_parts == 1) return e;
+  cfg.gridDim = dim3(a.B * a.H);
+  cfg.dynamicSmemBytes = 0;
+  if (a.num_parts <= 16) {
+    cfg.blockDim = dim3(32);
+    return cudaLaunchKernelEx(&cfg, grouped_decode_merge<T, D, 1>, a);
+  }
+  cfg.blockDim = dim3(32 * 8);
+  return cudaLaunchKernelEx(&cfg, grouped_decode_merge<T, D, 8>, a);
+}
+
+}  // namespace
+
+int grouped_decode_partition(int B, int H, int Hkv, int max_context) {
+  const int G = H / Hkv;
+  const long long ctas = (long long)B * Hkv * (G <= 8 ? 1 : (G + 15) / 16);
+  // About four rounds of the 3 CTAs an SM holds, so that sequences of
+  // different lengths even out; partitions of 64 to 2,048 keys.
+  const int nsm = sm_count() > 0 ? sm_count() : 152;
+  const long long parts = (12LL * nsm + ctas - 1) / ctas;
+  long long p = (max_context + parts - 1) / parts;
+  p = (p + kSpan - 1) / kSpan * kSpan;
+  return (int)(p < kSpan ? kSpan : p > kMaxPart ? kMaxPart : p);
+}
+
+cudaError_t launch_grouped_decode(const GroupedDecodeArgs& a, const void* k_cache,
+                                  const void* v_cache, cudaStream_t stream) {
+#define PK_GD(TT, DD)                                                  \
+  (a.G <= 8 ? launch_t<TT, DD, 1>(a, k_cache, v_cache, stream)         \
+            : launch_t<TT, DD, 2>(a, k_cache, v_cache, stream))
+  if (a.bf16) return a.D == 128 ? PK_GD(__nv_bfloat16, 128) : PK_GD(__nv_bfloat16, 64);
+  return a.D == 128 ? PK_GD(__half, 128) : PK_GD(__half, 64);
+#undef PK_GD
+}
+
+}  // namespace pk

@@ -1,0 +1,859 @@
+// grouped_prompt.cu -- causal attention of packed new tokens with grouped K/V
+// heads on the sm_103a tensor cores (tcgen05, accumulators in tensor memory):
+// whole prompts over their own K/V (contiguous rows) and chunks over a paged
+// cache.
+//
+// Query i of a sequence with ql new tokens and n keys sits at position
+// n - ql + i and sees keys 0 .. n - ql + i (a prompt has n = ql):
+//     out_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale * q_i . k_j - max).
+//
+// Tiles.  The G = H / Hkv query heads that share a K/V head go into one tile:
+// its 128 rows are floor(128 / G) consecutive tokens x G heads, row r = token
+// r / G, head r mod G (the order in which one TMA box of a packed [T, H, D]
+// array lands).  A key tile then serves all heads of the group, and a chunk of
+// a few tokens still fills rows instead of leaving a tile of 128 tokens to
+// each head.  A CTA takes two such tiles A and B, one after the other in the
+// sequence, of one K/V head, and walks the visible keys in tiles of 128:
+//   warps 0-3, 4-7  softmax of tile A, B: one row per thread (TMEM lane = row);
+//   warp 8          producer: Q, then K_0, K_1, V_0, K_2, V_1, ... into a ring;
+//   warp 9          issues S = Q K^T (one thread), owns the tensor memory;
+//   warp 10         issues O += P V (one thread).
+// Tensor memory: S [0, 128) shared by both tiles, P_A [128, 192), P_B
+// [192, 256) as 16-bit pairs, O_A, O_B from column 256 (D columns each).  Q
+// stays in shared memory (A operand of the S products) and P in tensor memory
+// (A operand of the P V products): the placement that asks least of the shared
+// memory's bandwidth, as in the fp16 chunk kernel of this library.
+//
+// Scheduling.  Lengths live on the device, so the grid is an upper bound
+// (T / (2 * tokens per tile) + B units for each K/V head) and each CTA finds
+// its unit itself: units are ranked by the number of key tiles they read,
+// longest first, so that the last CTAs to start are the short ones.  The rank
+// needs no sort: how many units of a sequence read at least t key tiles has a
+// closed form, and a search over t (eleven candidates a round, one per warp)
+// with sums over the sequences finds the unit.  Few units with many keys: each
+// is cut into up to `split` key ranges whose (o, m, l) rows go to the workspace
+// and are merged by log-sum-exp.
+//
+// Rounding: scores, maxima, sums and O are fp32; P is rounded to the 16-bit
+// type of the inputs (the tensor core's operand; its values are at most 2^8
+// before scaling, since O is rescaled only when the maximum grew by more than
+// that), the result once more at the end.
+//
+// Bound: the tensor pipe by intensity; see the notes at launch_grouped.
+#include <cuda_bf16.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "pk_common.cuh"
+#include "pk_internal.h"
+#include "pk_tcgen05.cuh"
+
+namespace pk {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kTile = 128;               // query rows of a tile, keys of a key tile
+constexpr int kSlab = 128 * 128;         // 128 rows x 64 dims (128 bytes)
+constexpr int kQRoom = 2 * kSlab;        // a Q tile's room, up to 128 dims
+constexpr int kThreadsG = 352;           // 8 softmax warps, producer, 2 MMA issuers
+constexpr int kWarps = kThreadsG / 32;
+constexpr int kWarpLoad = 8, kWarpS = 9, kWarpPv = 10;
+constexpr int kCols = 512;               // tensor memory columns
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
+constexpr int kWindow = 256;             // block-table entries staged at a time
+constexpr int kMaxRing = 8;
+constexpr int kBars = 1 + 2 * kMaxRing + 8 + 1;
+constexpr float kLazy = 8.0f;            // log2 of the growth that forces a rescale
+
+// Layout of a K or V tile in shared memory.  Paged: key groups of 8 keys x D
+// dims, each the 1 KB atoms of dims 0-63 and 64-127 (the order in which a
+// block's box lands).  Contiguous rows: two slabs of 128 keys x 64 dims.
+template <int D, bool PAGED>
+struct Cfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE_BYTES = kTile * D * 2;
+  static constexpr int RING = D == 128 ? 5 : 8;
+  static_assert(RING <= kMaxRing, "barriers");
+  static constexpr int GROUP = PAGED ? 8 * D * 2 : 1024;  // 8 keys
+  static constexpr int HALF = PAGED ? 1024 : kSlab;       // from dims 0-63 to dims 64-127
+  static constexpr int OFF_KV = 2 * kQRoom;
+  static constexpr int OFF_BAR = OFF_KV + RING * TILE_BYTES;
+  static constexpr int OFF_MISC = OFF_BAR + kBars * 8;  // TMEM address, issue counters, search
+  static constexpr int OFF_TBL = (OFF_MISC + 128 + 15) / 16 * 16;
+  static constexpr int SMEM = OFF_TBL + (PAGED ? kWindow * 4 : 0) + 1024;
+  static_assert(SMEM <= 232448, "shared memory per CTA");
+  static constexpr int PART = D + 4;  // floats of a partial row: o[D], m, l, pad
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// Instruction descriptors: idesc_f16_f32 with the operand type (1: bf16).
+template <typename T>
+__host__ __device__ constexpr uint32_t operand_type() {
+  return std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
+}
+
+// A sequence of the packed step, as every CTA sees it.
+struct Seq {
+  int start, ql, n;  // first packed row, new tokens, keys
+  bool bad;          // its rows are zeros
+  bool lost;         // its rows do not exist: nothing to write
+};
+
+template <bool PAGED>
+__device__ __forceinline__ Seq sequence(const GroupedArgs& a, int b) {
+  Seq s;
+  s.start = a.q_offsets[b];
+  const int end = a.q_offsets[b + 1];
+  s.ql = end - s.start;
+  s.lost = s.start < 0 || end < s.start || end > a.T;
+  if (s.lost) s.ql = 0;
+  s.n = s.ql;
+  s.bad = s.lost;
+  if (PAGED && s.ql > 0) {
+    const int n = a.context_lens[b];
+    if (n < s.ql || n > a.max_context)
+      s.bad = true;
+    else
+      s.n = n;
+  }
+  return s;
+}
+
+// Key tiles that unit i (tokens i * span .. ) of a sequence reads.
+__device__ __forceinline__ int unit_tiles(const Seq& s, int span, int i) {
+  return (s.n - s.ql + min((i + 1) * span, s.ql) + kTile - 1) / kTile;
+}
+
+// Units of a sequence that read at least t (>= 1) key tiles: the last ones.
+__device__ __forceinline__ int units_from(const Seq& s, int span, int t) {
+  const int k = (t - 1) * kTile + 1;  // keys such a unit needs at least
+  if (s.ql <= 0 || s.n < k) return 0;
+  const int nu = (s.ql + span - 1) / span;
+  const int over = k - (s.n - s.ql);  // its tokens needed at least
+  const int first = over <= 0 ? 0 : (over + span - 1) / span - 1;
+  return nu - min(first, nu - 1);
+}
+
+// Key ranges a unit of that many key tiles is cut into.
+__device__ __forceinline__ int unit_parts(int tiles, int split, int min_tiles) {
+  return max(1, min(split, tiles / min_tiles));
+}
+
+__device__ __forceinline__ int warp_sum(int x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
+  return x;
+}
+
+// The unit of a rank (units by key tiles, longest first): true and (b, i), or
+// false behind the last unit.  All threads of the CTA call it.
+template <bool PAGED>
+__device__ __forceinline__ bool find_unit(const GroupedArgs& a, int rank, int* s_cnt, int& b_out,
+                                          int& i_out) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // units with >= lo tiles: more than rank (lo = 0: taken as such); >= hi: at most rank
+  int lo = 0, hi = a.max_tiles + 1, above = 0;  // above: units with >= hi tiles
+  while (hi - lo > 1) {
+    const int gap = hi - lo;
+    const int t = lo + 1 + (int)((long long)warp * (gap - 1) / kWarps);
+    int c = 0;
+    for (int b = lane; b < a.B; b += 32) c += units_from(sequence<PAGED>(a, b), a.span, t);
+    c = warp_sum(c);
+    if (lane == 0) s_cnt[warp] = c;
+    __syncthreads();
+    int nlo = lo, nhi = hi, nabove = above;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {  // candidates rise with w, counts fall
+      const int tw = lo + 1 + (int)((long long)w * (gap - 1) / kWarps);
+      if (s_cnt[w] > rank)
+        nlo = tw;
+      else if (tw < nhi) {
+        nhi = tw;
+        nabove = s_cnt[w];
+      }
+    }
+    lo = nlo;
+    hi = nhi;
+    above = nabove;
+    __syncthreads();
+  }
+  if (lo == 0) return false;
+  // The units that read exactly lo tiles, sequences in order: the (rank - above)-th.
+  if (warp == 0) {
+    int left = rank - above;
+    bool found = false;
+    for (int base = 0; base < a.B && !found; base += 32) {
+      const int b = base + lane;
+      int c = 0, upper = 0, nu = 0;
+      if (b < a.B) {
+        const Seq s = sequence<PAGED>(a, b);
+        upper = units_from(s, a.span, lo + 1);
+        c = units_from(s, a.span, lo) - upper;
+        nu = (s.ql + a.span - 1) / a.span;
+      }
+      int x = c;  // inclusive scan
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(kAll, x, d);
+        if (lane >= d) x += y;
+      }
+      const unsigned hit = __ballot_sync(kAll, x > left);
+      if (hit != 0) {
+        found = true;
+        if (lane == __ffs(hit) - 1) {
+          s_cnt[0] = b;
+          s_cnt[1] = nu - 1 - upper - (left - (x - c));
+        }
+      } else {
+        left -= __shfl_sync(kAll, x, 31);
+      }
+    }
+  }
+  __syncthreads();
+  b_out = s_cnt[0];
+  i_out = s_cnt[1];
+  return true;
+}
+
+// Wait until the S issuer has issued `n` products of a tile.
+__device__ __forceinline__ bool wait_count(volatile int* cnt, int n) {
+  if (*cnt >= n) return true;
+  const long long t0 = clock64();
+  while (*cnt < n) {
+    __nanosleep(32);
+    if (clock64() - t0 > kWaitLimitCycles) return false;
+  }
+  return true;
+}
+
+// Ring index of K_t and V_t among n_kv key tiles (K_0, then K_{t+1}, V_t).
+__device__ __forceinline__ int ring_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int ring_v(int t, int n_kv) {
+  return t + 1 < n_kv ? 2 * t + 2 : 2 * t + 1;
+}
+
+template <typename T, int D, bool PAGED>
+__global__ void __launch_bounds__(kThreadsG, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap qmap,
+                   const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap omap, const GroupedArgs a) {
+  using C = Cfg<D, PAGED>;
+  constexpr int kRing = C::RING;
+  constexpr uint32_t kIdS = tc::idesc_f16_f32(kTile, kTile, false, false) | operand_type<T>();
+  constexpr uint32_t kIdO = tc::idesc_f16_f32(kTile, D, false, true) | operand_type<T>();
+  extern __shared__ uint8_t smem_dyn[];
+  const uint32_t raw = smem_u32(smem_dyn);
+  uint8_t* smem = smem_dyn + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + C::OFF_KV;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* kv_full = bars + 1;
+  uint64_t* kv_empty = kv_full + kRing;
+  uint64_t* s_full = kv_empty + kRing;  // [2] per tile: S(j) computed
+  uint64_t* s_free = s_full + 2;        // [2]: its softmax holds S in registers
+  uint64_t* p_full = s_free + 2;        // [2]: P(j) stored
+  uint64_t* pv_done = p_full + 2;       // [2]: O += P(j) V_j completed
+  uint64_t* drain = pv_done + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* s_issued = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // [2]
+  int* s_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);                      // [11]
+  int32_t* tbl = reinterpret_cast<int32_t*>(smem + C::OFF_TBL);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = blockIdx.x % a.split;
+  const int hkv = (blockIdx.x / a.split) % a.Hkv;
+  const int rank = blockIdx.x / (a.split * a.Hkv);
+
+  pdl_wait();
+  pdl_launch_dependents();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.B; i += kThreadsG)
+      if (sequence<PAGED>(a, i).lost) flag_status(a.status, PA_DEV_BAD_CONTEXT);
+  int b, unit;
+  if (!find_unit<PAGED>(a, rank, s_cnt, b, unit)) return;
+  const Seq sq = sequence<PAGED>(a, b);
+  const int tok0 = unit * a.span;  // first token of tile A in its sequence
+  if (sq.bad) {                    // zero rows (its rows exist: ql > 0)
+    if (part != 0) return;
+    if (threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_CONTEXT);
+    const int rows = min(a.span, sq.ql - tok0);
+    const int per_tok = a.G * D / 8;  // 16-byte chunks
+    for (int i = threadIdx.x; i < rows * per_tok; i += kThreadsG)
+      reinterpret_cast<uint4*>(static_cast<T*>(a.out) +
+                               ((size_t)(sq.start + tok0 + i / per_tok) * a.H + hkv * a.G) * D)
+          [i % per_tok] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  // Key tiles of the unit, and this CTA's range of them.
+  const int all_tiles = unit_tiles(sq, a.span, unit);
+  const int parts = unit_parts(all_tiles, a.split, a.min_part_tiles);
+  if (part >= parts) return;
+  const int kt0 = (int)((long long)part * all_tiles / parts);
+  const int n_kv = (int)((long long)(part + 1) * all_tiles / parts) - kt0;
+  const int tpt = a.span / 2;  // tokens of a tile
+  const int toks_a = min(tpt, sq.ql - tok0), toks_b = max(0, min(tpt, sq.ql - tok0 - tpt));
+  const int pos_a = sq.n - sq.ql + tok0, pos_b = pos_a + tpt;  // first positions
+  auto tiles_of = [&](int pos, int toks) {
+    const int all = toks > 0 ? (pos + toks - 1) / kTile + 1 : 0;
+    return min(max(all - kt0, 0), n_kv);
+  };
+  const int ntile_a = tiles_of(pos_a, toks_a), ntile_b = tiles_of(pos_b, toks_b);
+  const int row0 = sq.start + tok0;  // packed row of tile A's first token
+
+  if (threadIdx.x == 0) {
+    s_issued[0] = 0;
+    s_issued[1] = 0;
+    mbar_init(q_full, 1);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);  // one arrival per softmax warp
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(drain, 2);
+    fence_mbar_init();
+    // Q first: it heads the start-up path.  A box is tpt tokens x G heads x 64
+    // dims; tokens past the packed rows read as zeros.
+    mbar_arrive_expect_tx(q_full, 2 * C::HALVES * tpt * a.G * 128);
+    for (int x = 0; x < 2; ++x)
+      for (int hf = 0; hf < C::HALVES; ++hf)
+        tma_load_3d(sQ + x * kQRoom + hf * kSlab, &qmap, 64 * hf, hkv * a.G, row0 + x * tpt,
+                    q_full);
+  }
+  if (warp == kWarpS) {
+    tc::tmem_alloc(tmem_at, kCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_at;
+  bool ok = true;
+  int issued = 0;  // ring tiles requested
+
+  if (warp == kWarpLoad) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tmap(&kmap);
+      prefetch_tmap(&vmap);
+    }
+    const int bpt = PAGED ? kTile / a.block_size : 1;  // blocks of a key tile
+    const int nblk = PAGED ? (sq.n + a.block_size - 1) / a.block_size : 0;
+    int win = -kWindow;
+    auto load_tile = [&](int t, bool v, int u) {
+      const int lb0 = (kt0 + t) * bpt;
+      if (PAGED && (lb0 < win || lb0 + bpt > win + kWindow)) {
+        // K_t is requested before V_{t-1}: the window starts one tile early.
+        win = (!v && t > 0) ? lb0 - bpt : lb0;
+        __syncwarp();
+        int ent[kWindow / 32];
+#pragma unroll
+        for (int k = 0; k < kWindow / 32; ++k) {
+          const int lb = win + lane + 32 * k;
+          ent[k] = lb < nblk ? __ldg(a.block_tables + (size_t)b * a.max_blocks + lb)
+                             : a.num_blocks;  // past the sequence: zeros
+        }
+#pragma unroll
+        for (int k = 0; k < kWindow / 32; ++k) {
+          int phys = ent[k];
+          if (phys < 0 || phys > a.num_blocks ||
+              (phys == a.num_blocks && win + lane + 32 * k < nblk)) {
+            flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+            phys = a.num_blocks;
+          }
+          tbl[lane + 32 * k] = phys;
+        }
+        __syncwarp();
+      }
+      const int st = u % kRing;
+      if (lane == 0) {
+        ok = mbar_wait(&kv_empty[st], ((u / kRing) & 1) ^ 1);
+        if (ok) mbar_arrive_expect_tx(&kv_full[st], C::TILE_BYTES);
+      }
+      ok = __shfl_sync(kAll, ok, 0);
+      if (!ok) return;
+      uint8_t* dst = sKV + st * C::TILE_BYTES;
+      if constexpr (PAGED) {
+        // One box per block, from lane to lane: (64 dims, 8 keys, halves, key
+        // groups) at row (block * block_size * Hkv + head) of the pool.
+        for (int i = lane; i < bpt; i += 32)
+          tma_load_5d(dst + i * (a.block_size / 8) * C::GROUP, v ? &vmap : &kmap, 0, 0, 0, 0,
+                      tbl[lb0 - win + i] * a.block_size * a.Hkv + hkv, &kv_full[st]);
+      } else if (lane == 0) {
+        // 128 tokens of one head, both halves; rows past the array read as zeros.
+        tma_load_4d(dst, v ? &vmap : &kmap, 0, sq.start + (kt0 + t) * kTile, 0, hkv,
+                    &kv_full[st]);
+      }
+      if (lane == 0) ++issued;
+    };
+    int u = 0;
+    if (n_kv > 0) load_tile(0, false, u++);
+    for (int j = 0; j < n_kv && ok; ++j) {
+      if (j + 1 < n_kv) load_tile(j + 1, false, u++);
+      if (ok) load_tile(j, true, u++);
+    }
+  } else if (warp == kWarpS) {
+    // ------------------------------------------------------------ S = Q K^T
+    if (lane == 0) {
+      const int nt[2] = {ntile_a, ntile_b};
+      const uint64_t dk = tc::smem_desc(smem_u32(sKV), 16, C::GROUP, tc::kSwizzle128B);
+      const uint64_t dq = tc::smem_desc(smem_u32(sQ), 16, 1024, tc::kSwizzle128B);
+      bool q_there = false;
+      int last_x = -1, last_t = 0;
+      for (int t = 0; t < n_kv && ok; ++t) {
+        const int u = ring_k(t);
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (t >= nt[x]) continue;
+          if (!q_there && !(ok = q_there = mbar_wait(q_full, 0))) break;
+          if (last_x >= 0 && !(ok = mbar_wait(&s_free[last_x], last_t & 1))) break;
+          if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) break;
+          tc::fence_after_sync();
+          const uint64_t db = dk + (u % kRing) * (C::TILE_BYTES >> 4);
+          const uint64_t da = dq + x * (kQRoom >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_f16(tmem + kColS, da + (((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
+                        db + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+          tc::commit(&s_full[x]);
+          s_issued[x] = t + 1;  // a scheduling hint to the P V issuer
+          last_x = x;
+          last_t = t;
+        }
+        if (ok) tc::commit(&kv_empty[u % kRing]);
+      }
+    }
+    ok = __shfl_sync(kAll, ok, 0);
+  } else if (warp == kWarpPv) {
+    // ------------------------------------------------------------ O += P V
+    const int nt[2] = {ntile_a, ntile_b};
+    const uint64_t dv = tc::smem_desc(smem_u32(sKV), C::HALF, C::GROUP, tc::kSwizzle128B);
+    auto issue_pv = [&](int t) {  // lane 0
+      const int u = ring_v(t, n_kv);
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (t >= nt[x]) continue;
+        if (!(ok = mbar_wait(&p_full[x], t & 1))) break;
+        if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) break;
+        // Behind S(t + 1) in the tensor core's queue, so that never waits for this.
+        if (t + 1 < nt[x] && !(ok = wait_count(s_issued + x, t + 2))) break;
+        tc::fence_after_sync();
+        const uint32_t ta = tmem + kColP + x * (kTile / 2);
+        const uint64_t db = dv + (u % kRing) * (C::TILE_BYTES >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          tc::mma_f16_ts(tmem + kColO + x * D, ta + kk * 8, db + ((kk * 2 * C::GROUP) >> 4), kIdO,
+                         t > 0 || kk > 0);
+        tc::commit(&pv_done[x]);
+      }
+      if (ok) tc::commit(&kv_empty[u % kRing]);
+    };
+    if (lane == 0)
+      for (int t = 0; t + 1 < n_kv && ok; ++t) issue_pv(t);
+    ok = __shfl_sync(kAll, ok, 0);
+    if (ok && n_kv > 0) {
+      // Rows of the last key tile past the sequence's keys hold whatever the
+      // block's tail, or the next sequence's rows, hold: 0 * NaN is NaN, so the
+      // warp zeroes them once V has landed.
+      const int live = sq.n - (kt0 + n_kv - 1) * kTile;
+      if (live < kTile) {
+        const int u = ring_v(n_kv - 1, n_kv);
+        if (lane == 0) ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1);
+        ok = __shfl_sync(kAll, ok, 0);
+        if (ok) {
+          uint8_t* vt = sKV + (u % kRing) * C::TILE_BYTES;
+          constexpr int kChunks = D / 8;
+          for (int i = lane; i < (kTile - live) * kChunks; i += 32) {
+            const int r = live + i / kChunks, c = i % kChunks;
+            *reinterpret_cast<uint4*>(vt + (r >> 3) * C::GROUP + (c >> 3) * C::HALF +
+                                      (r & 7) * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+      }
+      if (ok && lane == 0) issue_pv(n_kv - 1);
+    }
+    ok = __shfl_sync(kAll, ok, 0);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
+    const uint32_t t_s = tmem + t_lane + kColS, t_o = tmem + t_lane + kColO + x * D;
+    const int pos0 = x ? pos_b : pos_a, toks = x ? toks_b : toks_a;
+    const int ntile = x ? ntile_b : ntile_a;
+    const int my_tok = row / a.G;
+    const bool live = my_tok < toks;  // a row of this sequence
+    const int pos = pos0 + my_tok;
+    const float sl2 = a.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    ok = __all_sync(kAll, mbar_wait(q_full, 0));
+    for (int j = 0; j < ntile && ok; ++j) {
+      if (!(ok = __all_sync(kAll, mbar_wait(&s_full[x], j & 1)))) break;
+      tc::fence_after_sync();
+      const int kbase = (kt0 + j) * kTile;
+      uint32_t r[4][32];
+      float cm[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::ld_32x32_max(t_s + c * 32, r[c], cm[c]);
+      tc::wait_ld();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[x]);
+      float mt = max3f(cm[0], cm[1], fmaxf(cm[2], cm[3]));
+      if (kbase + kTile - 1 > pos0) {  // keys past some row's position
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (kbase + c * 32 + i > pos) r[c][i] = __float_as_uint(-INFINITY);
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mx[(i >> 1) & 7] = max3f(mx[(i >> 1) & 7], __uint_as_float(r[c][i]),
+                                     __uint_as_float(r[c][i + 1]));
+        mt = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+      }
+      mt *= sl2;
+      const float m_new = fmaxf(m, mt);
+      const bool resc = live && m_new > m + kLazy;
+      float alpha = 1.f;
+      if (resc) {
+        alpha = ex2_approx(m - m_new);
+        m = m_new;
+        l *= alpha;
+      }
+      // A row that has seen masked keys alone (a part whose range starts past
+      // its position) has m = -inf, and -inf + inf is NaN: taken with maximum 0
+      // its weights are all zero and its partial row is empty.
+      const float neg_m = m == -INFINITY ? 0.f : -m;
+      float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float y0, y1;
+          fma_f32x2(y0, y1, __uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1]), sl2,
+                    sl2, neg_m, neg_m);
+          const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+          const int k = 2 * (e & 3);
+          add_f32x2(rs[k], rs[k + 1], rs[k], rs[k + 1], p0, p1);
+          r[c][e] = pack2<T>(p0, p1);
+        }
+      l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+      if (j > 0) {  // P V of the tile before done: P is free, O stands still
+        if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (j - 1) & 1)))) break;
+        tc::fence_after_sync();
+      }
+      if (j > 0 && __any_sync(kAll, resc)) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tc::ld_32x32(t_o + c * 32, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tc::st_32x32(t_o + c * 32, o);
+        }
+        tc::wait_st();
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t pw[32];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          pw[e] = r[2 * hf][e];
+          pw[16 + e] = r[2 * hf + 1][e];
+        }
+        tc::st_32x32(tmem + t_lane + kColP + x * (kTile / 2) + hf * 32, pw);
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[x]);
+    }
+    if (ok && ntile > 0) ok = __all_sync(kAll, mbar_wait(&pv_done[x], (ntile - 1) & 1));
+    // One decision for the tile: a wait that gave up in one warp must not leave
+    // the others at the barrier below.
+    ok = named_bar_and(1 + x, 128, ok);
+    if (ntile > 0) tc::fence_after_sync();
+    const int my_row = row0 + x * tpt + my_tok, my_head = hkv * a.G + row % a.G;
+    if (ok && parts > 1) {
+      // A part: the unnormalised row (o, m, l) for the merge.
+      float* wrow = a.ws + (((size_t)part * a.T + my_row) * a.H + my_head) * C::PART;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (ntile > 0) {
+          tc::ld_32x32(t_o + c * 32, o);
+          tc::wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (live) {
+          float4* dst = reinterpret_cast<float4*>(wrow + c * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        }
+      }
+      if (live) {
+        wrow[D] = m;
+        wrow[D + 1] = l;
+      }
+    } else if (ok && toks > 0) {
+      // The tile goes through Q's room (every S product of it is done), in the
+      // swizzled rows of the TMA boxes.  A whole tile of this sequence leaves by
+      // TMA; a tile that ends inside leaves by 16-byte stores of its live rows
+      // alone, since the next packed rows are another sequence's.
+      uint8_t* qrow = sQ + x * kQRoom + row * 128;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tc::ld_32x32(t_o + c * 32, o);
+        tc::wait_ld();
+        uint32_t hv[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          hv[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+        uint8_t* slab = qrow + (c >> 1) * kSlab;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(slab + ((((c & 1) << 2) + q) ^ (row & 7)) * 16) =
+              make_uint4(hv[4 * q], hv[4 * q + 1], hv[4 * q + 2], hv[4 * q + 3]);
+      }
+      const bool whole = toks == tpt;
+      if (whole) fence_proxy_async_smem();
+      named_bar_sync(1 + x, 128);
+      if (whole) {
+        if (quarter == 0 && lane == 0) {
+#pragma unroll
+          for (int hf = 0; hf < C::HALVES; ++hf)
+            tma_store_3d(&omap, sQ + x * kQRoom + hf * kSlab, 64 * hf, hkv * a.G,
+                         row0 + x * tpt);
+          bulk_commit_group();
+          bulk_wait_all();
+        }
+      } else {
+        constexpr int kChunks = D / 8;
+        for (int i = row; i < toks * a.G * kChunks; i += 128) {
+          const int r = i / kChunks, c = i % kChunks;
+          const uint4 w = *reinterpret_cast<const uint4*>(
+              sQ + x * kQRoom + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) * 16));
+          *reinterpret_cast<uint4*>(
+              static_cast<T*>(a.out) +
+              ((size_t)(row0 + x * tpt + r / a.G) * a.H + hkv * a.G + r % a.G) * D + c * 8) = w;
+        }
+      }
+    }
+  }
+
+  // All roles meet.  After a wait that gave up, the producer lets its copies
+  // land and the issuers their MMAs end (both bounded) before the CTA leaves.
+  tc::fence_before_sync();
+  if (__syncthreads_or(!ok)) {
+    if (threadIdx.x == 0) flag_status(a.status, PA_DEV_TIMEOUT);
+    if (warp == kWarpLoad && lane == 0) {
+      mbar_wait(q_full, 0);
+      for (int u = max(0, issued - kRing); u < issued; ++u)
+        mbar_wait(&kv_full[u % kRing], (u / kRing) & 1);
+    }
+    if ((warp == kWarpS || warp == kWarpPv) && lane == 0) {
+      tc::commit(drain);
+      mbar_wait(drain, 0);
+    }
+    __syncthreads();
+  }
+  if (warp == kWarpS) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kCols);
+  }
+}
+
+// Merges the parts of a split unit's rows by log-sum-exp (m, l in the log2
+// domain): one warp per (token, head), lane l owns D / 32 dims.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) grouped_merge_kernel(const GroupedArgs a) {
+  constexpr int EPL = D / 32, kPart = D + 4;
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (w >= (long long)a.T * a.H) return;
+  const int t = (int)(w / a.H), h = (int)(w % a.H);
+  // The sequence that holds row t: offsets rise (else the row is nobody's).
+  int lo = 0, hi = a.B;
+  if (a.B <= 0 || t < a.q_offsets[0] || t >= a.q_offsets[a.B]) return;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.q_offsets[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const Seq s = sequence<true>(a, lo);
+  if (s.bad || t < s.start || t >= s.start + s.ql) return;
+  const int parts =
+      unit_parts(unit_tiles(s, a.span, (t - s.start) / a.span), a.split, a.min_part_tiles);
+  if (parts <= 1) return;  // written by its only part
+  constexpr int kMax = 8;
+  float ms[kMax], ls[kMax], ov[kMax][EPL];
+#pragma unroll
+  for (int p = 0; p < kMax; ++p) {
+    ms[p] = -INFINITY;
+    ls[p] = 0.f;
+    if (p < parts) {
+      const float* row = a.ws + (((size_t)p * a.T + t) * a.H + h) * kPart;
+      ms[p] = row[D];
+      ls[p] = row[D + 1];
+      if constexpr (EPL == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(row + lane * 4);
+        ov[p][0] = f.x, ov[p][1] = f.y, ov[p][2] = f.z, ov[p][3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(row + lane * 2);
+        ov[p][0] = f.x, ov[p][1] = f.y;
+      }
+    }
+  }
+  float M = -INFINITY;
+#pragma unroll
+  for (int p = 0; p < kMax; ++p)
+    if (ls[p] != 0.f) M = fmaxf(M, ms[p]);
+  float L = 0.f, o[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) o[e] = 0.f;
+#pragma unroll
+  for (int p = 0; p < kMax; ++p)
+    if (ls[p] != 0.f) {
+      const float wgt = ex2_approx(ms[p] - M);
+      L += ls[p] * wgt;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] += wgt * ov[p][e];
+    }
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  T* dst = static_cast<T*>(a.out) + ((size_t)t * a.H + h) * D + lane * EPL;
+#pragma unroll
+  for (int e = 0; e < EPL; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack2<T>(o[e] * inv, o[e + 1] * inv);
+}
+
+template <typename T, int D, bool PAGED>
+cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const void* v,
+                     long long q_stride, long long k_stride, long long v_stride,
+                     cudaStream_t stream) {
+  using C = Cfg<D, PAGED>;
+  using u64 = unsigned long long;
+  CUtensorMap qmap, kmap, vmap, omap;
+  const unsigned tpt = a.span / 2;
+  {
+    const u64 dims[3] = {(u64)D, (u64)a.H, (u64)a.T};
+    const u64 qs[2] = {(u64)D * 2, (u64)q_stride * 2}, os[2] = {(u64)D * 2, (u64)a.H * D * 2};
+    const unsigned box[3] = {64, (unsigned)a.G, tpt};
+    cudaError_t e = make_map_3d(&qmap, q, dims, qs, box, true);
+    if (e == cudaSuccess) e = make_map_3d(&omap, a.out, dims, os, box, true);
+    if (e != cudaSuccess) return e;
+  }
+  for (int i = 0; i < 2; ++i) {
+    CUtensorMap* map = i ? &vmap : &kmap;
+    cudaError_t e;
+    if constexpr (PAGED) {
+      // Rows (slot, head) of D values; inside a block (64 dims, 8 keys, halves,
+      // key groups), at its first slot's row.
+      const u64 rowb = (u64)D * 2, tok = rowb * a.Hkv;
+      const u64 dims[5] = {64, 8, (u64)C::HALVES, (u64)a.block_size / 8,
+                           (u64)a.num_blocks * a.block_size * a.Hkv};
+      const u64 st[4] = {tok, 128, 8 * tok, rowb};
+      const unsigned box[5] = {64, 8, (unsigned)C::HALVES, (unsigned)a.block_size / 8, 1};
+      e = make_map_5d(map, i ? v : k, dims, st, box, true);
+    } else {
+      const u64 dims[4] = {64, (u64)a.T, (u64)C::HALVES, (u64)a.Hkv};
+      const u64 st[3] = {(u64)(i ? v_stride : k_stride) * 2, 128, (u64)D * 2};
+      const unsigned box[4] = {64, kTile, (unsigned)C::HALVES, 1};
+      e = make_map_4d(map, i ? v : k, dims, st, box, true);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  constexpr auto kern = grouped_kernel<T, D, PAGED>;
+  cudaError_t e = ensure_dynamic_smem<kern>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.max_units * a.Hkv * a.split));
+  cfg.blockDim = dim3(kThreadsG);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, qmap, kmap, vmap, omap, a);
+  if constexpr (PAGED) {
+    if (e != cudaSuccess || a.split == 1) return e;
+    cudaLaunchConfig_t cm = cfg;
+    cm.gridDim = dim3((unsigned)(((long long)a.T * a.H * 32 + 255) / 256));
+    cm.blockDim = dim3(256);
+    cm.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cm, grouped_merge_kernel<T, D>, a);
+  }
+  return e;
+}
+
+}  // namespace
+
+int grouped_span(int G) { return G <= kTile ? 2 * (kTile / G) : 0; }
+
+int grouped_split(int B, int T, int H, int Hkv, int max_context) {
+  const int span = grouped_span(H / Hkv);
+  const int nsm = sm_count();
+  if (span == 0 || nsm <= 0) return 1;
+  const long long ctas = ((long long)T / span + B) * Hkv;
+  const long long tiles = ((long long)max_context + kTile - 1) / kTile;
+  // Fewer CTAs than four for each SM: more key ranges even out sequences of
+  // different lengths; none shorter than kMinPartTiles.
+  long long s = 4LL * nsm / (ctas > 0 ? ctas : 1);
+  if (s > tiles / kGroupedMinPartTiles) s = tiles / kGroupedMinPartTiles;
+  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
+}
+
+size_t grouped_workspace_bytes(int B, int T, int H, int Hkv, int D, int max_context) {
+  const int s = grouped_split(B, T, H, Hkv, max_context);
+  return s <= 1 ? 0 : (size_t)s * T * H * (D + 4) * sizeof(float);
+}
+
+cudaError_t launch_grouped(const GroupedArgs& a, const void* q, const void* k, const void* v,
+                           long long q_stride, long long k_stride, long long v_stride,
+                           cudaStream_t stream) {
+#define PK_GROUPED(TT, DD)                                                                     \
+  (a.block_tables != nullptr                                                                   \
+       ? launch_t<TT, DD, true>(a, q, k, v, q_stride, k_stride, v_stride, stream)              \
+       : launch_t<TT, DD, false>(a, q, k, v, q_stride, k_stride, v_stride, stream))
+  if (a.bf16) return a.D == 128 ? PK_GROUPED(__nv_bfloat16, 128) : PK_GROUPED(__nv_bfloat16, 64);
+  return a.D == 128 ? PK_GROUPED(__half, 128) : PK_GROUPED(__half, 64);
+#undef PK_GROUPED
+}
+
+}  // namespace pk

@@ -129,6 +129,17 @@ __device__ __forceinline__ bool named_bar_and(int id, int nthreads, bool pred) {
   return r != 0;
 }
 
+// 4-D tiled TMA load (coordinates innermost first).
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, int c0,
+                                            int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 5-D tiled TMA load (coordinates innermost first).
 __device__ __forceinline__ void tma_load_5d(void* smem_dst, const CUtensorMap* map, int c0,
                                             int c1, int c2, int c3, int c4, uint64_t* bar) {

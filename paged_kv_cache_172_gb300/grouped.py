@@ -188,3 +188,134 @@ def pa_rope_cache_write(q, k, v, positions, table, slot_mapping, k_cache=None, v
          positions.shape[0], int(bool(interleaved)), _DTYPE[dt], qs, ks, vs, bs, NB, _ptr(q_out),
          qos, _ptr(k_out), kos, _ptr(k_cache), _ptr(v_cache), _status(status))
     return q_out, k_out
+
+
+def pa_prompt_attention(q, k, v, q_offsets, scale, out=None, status=None, stream=None):
+    """Causal attention of packed prompts over their own rows.  q [T,H,D], k and
+    v [T,Hkv,D] (views of one projection's output are fine), q_offsets [B+1]
+    int32: sequence b is rows q_offsets[b] .. q_offsets[b+1]-1.  Returns ``out``
+    [T,H,D]; rows outside the sequences are left as they were (undefined when
+    ``out`` is allocated here)."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dt = q.dtype
+    qs = _rows(q, dt, "q", -1, -1, -1)
+    T, H, D = q.shape
+    ks = _rows(k, dt, "k", T, -1, D)
+    Hkv = k.shape[1]
+    vs = _rows(v, dt, "v", T, Hkv, D)
+    _dense(q_offsets, torch.int32, "q_offsets", -1)
+    B = q_offsets.shape[0] - 1
+    if out is None:
+        out = torch.empty((T, H, D), dtype=dt, device=q.device)
+    else:
+        _dense(out, dt, "out", T, H, D)
+    dev = _same_device("pa_prompt_attention", q, k, v, q_offsets, out, status)
+    _run(lib().pa_prompt_attention, "pa_prompt_attention", dev, stream, _ptr(q), _ptr(k),
+         _ptr(v), _ptr(q_offsets), B, T, H, Hkv, D, _DTYPE[dt], qs, ks, vs, float(scale),
+         _ptr(out), _status(status))
+    return out
+
+
+def _cache(dt, D, k_cache, v_cache, block_tables, context_lens, B):
+    """(num_blocks, block_size, Hkv, max_blocks) of a checked paged cache."""
+    _dense(k_cache, dt, "k_cache", -1, -1, -1, D)
+    NB, bs, Hkv, _ = k_cache.shape
+    _dense(v_cache, dt, "v_cache", NB, bs, Hkv, D)
+    _dense(block_tables, torch.int32, "block_tables", B, -1)
+    _dense(context_lens, torch.int32, "context_lens", B)
+    return NB, bs, Hkv, block_tables.shape[1]
+
+
+def _workspace(workspace, nbytes, device):
+    """(tensor, bytes) of the given workspace, or of a new one where one is needed."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def pa_chunk_attention_workspace_size(B, T, H, Hkv, D, max_context_len):
+    """Bytes of workspace pa_chunk_attention uses on the current device."""
+    return lib().pa_chunk_attention_workspace_size(B, T, H, Hkv, D, max_context_len)
+
+
+def pa_chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offsets, scale,
+                       max_context_len=None, out=None, workspace=None, split=True, status=None,
+                       stream=None):
+    """Attention of packed chunks over the paged cache with grouped heads.  q
+    [T,H,D]; caches [NB,bs,Hkv,D]; sequence b's rows q_offsets[b] ..
+    q_offsets[b+1]-1 are its last positions of context_lens[b] and attend to
+    everything up to themselves.  ``max_context_len`` bounds the contexts (None:
+    what the tables hold).  A workspace for the split of long contexts is
+    allocated when not given; split=False passes none.  Returns ``out``
+    [T,H,D]; rows outside the sequences are left as they were."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dt = q.dtype
+    qs = _rows(q, dt, "q", -1, -1, -1)
+    T, H, D = q.shape
+    _dense(q_offsets, torch.int32, "q_offsets", -1)
+    B = q_offsets.shape[0] - 1
+    NB, bs, Hkv, M = _cache(dt, D, k_cache, v_cache, block_tables, context_lens, B)
+    cap = M * bs if max_context_len is None else int(max_context_len)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=dt, device=q.device)
+    else:
+        _dense(out, dt, "out", T, H, D)
+    dev = _same_device("pa_chunk_attention", q, k_cache, v_cache, block_tables, context_lens,
+                       q_offsets, out, workspace, status)
+    ws, ws_bytes = None, 0
+    if split:
+        need = 0
+        if workspace is None:
+            with torch.cuda.device(dev):
+                need = pa_chunk_attention_workspace_size(B, T, H, Hkv, D, cap)
+        ws, ws_bytes = _workspace(workspace, need, dev)
+    _run(lib().pa_chunk_attention, "pa_chunk_attention", dev, stream, _ptr(q), _ptr(k_cache),
+         _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(q_offsets), B, T, H, Hkv, D,
+         _DTYPE[dt], qs, bs, NB, M, cap, float(scale), _ptr(out), _ptr(ws), ws_bytes,
+         _status(status))
+    return out
+
+
+def pa_decode_grouped_workspace_size(B, H, Hkv, D, block_size, max_context_len,
+                                     partition_tokens=0):
+    """Bytes of workspace pa_decode_grouped needs on the current device."""
+    return lib().pa_decode_grouped_workspace_size(B, H, Hkv, D, block_size, max_context_len,
+                                                  partition_tokens)
+
+
+def pa_decode_grouped(q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
+                      out=None, partition_tokens=0, workspace=None, status=None, stream=None):
+    """Paged decode attention with grouped heads: q [B,H,D] (fp16 or bf16), caches
+    [NB,bs,Hkv,D] of the same type, ``max_context_len`` a host-side bound on
+    context_lens.  Returns ``out`` [B,H,D]."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dt = q.dtype
+    if dt not in _DTYPE:
+        raise TypeError(f"q must be fp16 or bf16, got {dt}")
+    _dense(q, dt, "q", -1, -1, -1)
+    B, H, D = q.shape
+    NB, bs, Hkv, M = _cache(dt, D, k_cache, v_cache, block_tables, context_lens, B)
+    cap = int(max_context_len)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _dense(out, dt, "out", B, H, D)
+    dev = _same_device("pa_decode_grouped", q, k_cache, v_cache, block_tables, context_lens, out,
+                       workspace, status)
+    need = 0
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = pa_decode_grouped_workspace_size(B, H, Hkv, D, bs, cap, partition_tokens)
+    ws, ws_bytes = _workspace(workspace, need, dev)
+    _run(lib().pa_decode_grouped, "pa_decode_grouped", dev, stream, _ptr(q), _ptr(k_cache),
+         _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), B, H, Hkv, D, _DTYPE[dt], bs, NB,
+         M, cap, int(partition_tokens), float(scale), _ptr(out), _ptr(ws), ws_bytes,
+         _status(status))
+    return out
