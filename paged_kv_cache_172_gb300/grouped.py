@@ -3,17 +3,20 @@ step plan, rotary cache write, prompt attention, chunk attention and grouped
 decode, on packed tokens in fp16 or bf16.
 
 Argument marshalling only, as in ``_lib``: every step runs in the library's
-CUDA kernels.  Single-token calls are as short as their launches, so the
-checks here are kept to plain attribute reads.
+CUDA kernels.  The kernels of a single-token step take 2 to 6 us, less than
+a call's argument checks written out one by one (about 20 us of host time), so
+each call tests all its arguments in one expression and looks for the one to
+complain about only when that fails.
 """
-import ctypes
 from typing import NamedTuple
 
 import torch
 
-from ._lib import _check, _ptr, _stream, lib
+from ._lib import _check, _ptr, lib
 
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1}  # pa_dtype
+# The current stream's handle without a torch.cuda.Stream object around it.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class StepPlan(NamedTuple):
@@ -33,65 +36,87 @@ class StepPlan(NamedTuple):
                    new(2, torch.int64))
 
 
-def _same_device(name, first, *rest):
-    dev = first.device
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on different devices: {dev}, {t.device}")
-    return dev
-
-
 def _run(fn, name, dev, stream, *args):
     """Calls the library with the tensors' device current (its launches go to the
     current device) on ``stream`` or that device's current stream."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"{name}: stream on {stream.device}, tensors on {dev}")
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream, dev))
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"{name}: stream on {stream.device}, tensors on cuda:{dev}")
+        handle = stream.cuda_stream
     else:
-        rc = fn(*args, _stream(stream, dev))
+        handle = _raw_stream(dev)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
     if rc:
         _check(rc, name)
 
 
-def _dense(t, dtype, name, *shape):
-    """A contiguous CUDA tensor of that type; -1 in ``shape`` takes any size."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.dim() != len(shape) or any(n not in (-1, m) for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be {list(shape)} (-1: any), got {list(t.shape)}")
+def _dense(t, dtype, shape, dev):
+    """Whether t is a contiguous tensor of that type and shape on device dev."""
+    return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev)
 
 
-def _rows(t, dtype, name, *shape):
-    """A [T, heads, D] CUDA tensor whose tokens' heads are contiguous; the
-    distance between tokens in elements."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or dtype not in _DTYPE:
-        raise TypeError(f"{name} must be {dtype if dtype in _DTYPE else 'fp16 or bf16'}, "
-                        f"got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() != 3 or any(n not in (-1, m) for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be {list(shape)} (-1: any), got {list(t.shape)}")
-    T, heads, D = t.shape
+def _rows(t, dtype, shape, dev):
+    """Whether t is [T, heads, D] on device dev with a token's heads contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        return False
     st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != D):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return st[0] if T > 1 else heads * D
+    return st[2] == 1 and (st[1] == shape[2] or shape[1] == 1)
 
 
-def _status(status):
-    if status is not None and (status.dtype != torch.int32 or not status.is_cuda):
-        raise TypeError("status must be a CUDA int32 tensor")
-    return _ptr(status)
+def _stride(t):
+    """Distance between tokens in elements (any for a single token)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _status_ok(status, dev):
+    return status is None or (status.dtype is torch.int32 and status.get_device() == dev)
+
+
+def _shaped(name, *tensors):
+    """The tensors' dimensions, before anything is read off them: (name, tensor, dims)."""
+    for what, t, dims in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: {what} must be a torch.Tensor")
+        if t.dim() != dims:
+            raise ValueError(f"{name}: {what} must have {dims} dims, got {list(t.shape)}")
+
+
+def _complain(name, dev, dense, rows=(), status=None):
+    """Raises the error of the first argument that a call's test found wrong.
+    dense, rows: (name, tensor or None, dtype, shape)."""
+    for strided, group in ((False, dense), (True, rows)):
+        for what, t, dtype, shape in group:
+            if t is None:
+                continue
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: {what} must be a torch.Tensor")
+            if t.dtype != dtype:
+                raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
+            if not t.is_cuda:
+                raise ValueError(f"{name}: {what} must be on a CUDA device")
+            if t.get_device() != dev:
+                raise ValueError(f"{name}: {what} is on {t.device}, others on cuda:{dev}")
+            if tuple(t.shape) != tuple(shape):
+                raise ValueError(f"{name}: {what} must be {list(shape)}, got {list(t.shape)}")
+            if not strided and not t.is_contiguous():
+                raise ValueError(f"{name}: {what} must be contiguous")
+            if strided and not _rows(t, dtype, shape, dev):
+                raise ValueError(f"{name}: a token's heads must be contiguous in {what}")
+    if not _status_ok(status, dev):
+        raise TypeError(f"{name}: status must be int32 on the tensors' device")
+    raise ValueError(f"{name}: bad arguments")
+
+
+def _float16(name, q):
+    """pa_dtype of q, the tensor that sets a call's type."""
+    if q.dtype not in _DTYPE:
+        raise TypeError(f"{name}: q must be fp16 or bf16, got {q.dtype}")
+    return _DTYPE[q.dtype]
 
 
 def pa_step_plan(cached_lens, new_lens, block_tables, free_blocks, free_state, block_size,
@@ -106,28 +131,34 @@ def pa_step_plan(cached_lens, new_lens, block_tables, free_blocks, free_state, b
     slot_mapping and positions [max_tokens] (-1 and 0 behind the last token) and
     the new free_state (out's may be the one passed in).  A step that does not fit
     the ring (PA_DEV_NO_BLOCKS) or max_tokens (PA_DEV_BAD_CONTEXT) plans nothing."""
-    _dense(cached_lens, torch.int32, "cached_lens", -1)
-    B = cached_lens.shape[0]
-    _dense(new_lens, torch.int32, "new_lens", B)
-    _dense(block_tables, torch.int32, "block_tables", B, -1)
-    _dense(free_blocks, torch.int32, "free_blocks", -1)
-    _dense(free_state, torch.int64, "free_state", 2)
-    max_tokens = int(max_tokens)
+    i32, i64 = torch.int32, torch.int64
+    _shaped("pa_step_plan", ("cached_lens", cached_lens, 1), ("block_tables", block_tables, 2),
+            ("free_blocks", free_blocks, 1))
+    B, M, NB, T = (cached_lens.shape[0], block_tables.shape[1], free_blocks.shape[0],
+                   int(max_tokens))
+    dev = cached_lens.get_device()
     if out is None:
-        out = StepPlan.empty(B, max_tokens, cached_lens.device)
-    else:
-        _dense(out.context_lens, torch.int32, "out.context_lens", B)
-        _dense(out.q_offsets, torch.int32, "out.q_offsets", B + 1)
-        _dense(out.slot_mapping, torch.int64, "out.slot_mapping", max_tokens)
-        _dense(out.positions, torch.int32, "out.positions", max_tokens)
-        _dense(out.free_state, torch.int64, "out.free_state", 2)
-    dev = _same_device("pa_step_plan", cached_lens, new_lens, block_tables, free_blocks,
-                       free_state, *out, status)
-    _run(lib().pa_step_plan, "pa_step_plan", dev, stream, _ptr(cached_lens), _ptr(new_lens), B,
-         int(block_size), free_blocks.shape[0], block_tables.shape[1], max_tokens,
-         _ptr(free_blocks), _ptr(free_state), _ptr(block_tables), _ptr(out.context_lens),
-         _ptr(out.q_offsets), _ptr(out.slot_mapping), _ptr(out.positions), _ptr(out.free_state),
-         _status(status))
+        out = StepPlan.empty(B, T, cached_lens.device)
+    ctx, offs, slots, pos, state = out
+    one = (B,)
+    if not (dev >= 0 and _dense(cached_lens, i32, one, dev) and _dense(new_lens, i32, one, dev)
+            and _dense(block_tables, i32, (B, M), dev) and _dense(free_blocks, i32, (NB,), dev)
+            and _dense(free_state, i64, (2,), dev) and _dense(ctx, i32, one, dev)
+            and _dense(offs, i32, (B + 1,), dev) and _dense(slots, i64, (T,), dev)
+            and _dense(pos, i32, (T,), dev) and _dense(state, i64, (2,), dev)
+            and _status_ok(status, dev)):
+        _complain("pa_step_plan", dev,
+                  (("cached_lens", cached_lens, i32, one), ("new_lens", new_lens, i32, one),
+                   ("block_tables", block_tables, i32, (B, M)),
+                   ("free_blocks", free_blocks, i32, (NB,)), ("free_state", free_state, i64, (2,)),
+                   ("out.context_lens", ctx, i32, one), ("out.q_offsets", offs, i32, (B + 1,)),
+                   ("out.slot_mapping", slots, i64, (T,)), ("out.positions", pos, i32, (T,)),
+                   ("out.free_state", state, i64, (2,))), status=status)
+    _run(lib().pa_step_plan, "pa_step_plan", dev, stream, cached_lens.data_ptr(),
+         new_lens.data_ptr(), B, int(block_size), NB, M, T, free_blocks.data_ptr(),
+         free_state.data_ptr(), block_tables.data_ptr(), ctx.data_ptr(), offs.data_ptr(),
+         slots.data_ptr(), pos.data_ptr(), state.data_ptr(),
+         None if status is None else status.data_ptr())
     return out
 
 
@@ -153,40 +184,49 @@ def pa_rope_cache_write(q, k, v, positions, table, slot_mapping, k_cache=None, v
     may be views of one projection's output (a token's heads contiguous).  Returns
     (q_out, k_out); q_out is allocated when not given and may be q; k_out, given
     or with no cache allocated, receives the rotated keys and may be k."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    dt = q.dtype
-    qs = _rows(q, dt, "q", -1, -1, -1)
-    T, H, D = q.shape
-    ks = _rows(k, dt, "k", T, -1, D)
-    Hkv = k.shape[1]
-    if positions.dim() == 1:
-        positions = positions[None]
-    _dense(positions, torch.int32, "positions", -1, T)
-    _dense(table, torch.int64, "table", -1)
-    NB = bs = vs = 0
-    if (k_cache is None) != (v_cache is None):
-        raise ValueError("k_cache and v_cache are given together")
-    if k_cache is not None:
-        vs = _rows(v, dt, "v", T, Hkv, D)
-        _dense(k_cache, dt, "k_cache", -1, -1, Hkv, D)
+    name = "pa_rope_cache_write"
+    _shaped(name, ("q", q, 3), ("k", k, 3), ("table", table, 1))
+    code, dt, dev = _float16(name, q), q.dtype, q.get_device()
+    (T, H, D), Hkv, n = q.shape, k.shape[1], table.shape[0]
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    pos_shape = (T,) if positions.dim() == 1 else (axes, T)
+    kv, caches = (T, Hkv, D), ()
+    NB = bs = 0
+    if k_cache is not None or v_cache is not None:
+        _shaped(name, ("k_cache", k_cache, 4), ("v", v, 3))
         NB, bs = k_cache.shape[:2]
-        _dense(v_cache, dt, "v_cache", NB, bs, Hkv, D)
-        _dense(slot_mapping, torch.int64, "slot_mapping", T)
+        caches = (NB, bs, Hkv, D)
     else:
         v = slot_mapping = None
         if k_out is None:
-            k_out = torch.empty((T, Hkv, D), dtype=dt, device=q.device)
+            k_out = torch.empty(kv, dtype=dt, device=q.device)
     if q_out is None:
         q_out = torch.empty((T, H, D), dtype=dt, device=q.device)
-    qos = _rows(q_out, dt, "q_out", T, H, D)
-    kos = 0 if k_out is None else _rows(k_out, dt, "k_out", T, Hkv, D)
-    dev = _same_device("pa_rope_cache_write", q, k, v, positions, table, slot_mapping, k_cache,
-                       v_cache, q_out, k_out, status)
-    _run(lib().pa_rope_cache_write, "pa_rope_cache_write", dev, stream, _ptr(q), _ptr(k), _ptr(v),
-         _ptr(positions), _ptr(table), _ptr(slot_mapping), T, H, Hkv, D, 2 * table.shape[0],
-         positions.shape[0], int(bool(interleaved)), _DTYPE[dt], qs, ks, vs, bs, NB, _ptr(q_out),
-         qos, _ptr(k_out), kos, _ptr(k_cache), _ptr(v_cache), _status(status))
+    if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _rows(k, dt, kv, dev)
+            and _dense(positions, torch.int32, pos_shape, dev)
+            and _dense(table, torch.int64, (n,), dev) and _rows(q_out, dt, (T, H, D), dev)
+            and (k_out is None or _rows(k_out, dt, kv, dev))
+            and (not caches or (_rows(v, dt, kv, dev) and _dense(k_cache, dt, caches, dev)
+                                and v_cache is not None and _dense(v_cache, dt, caches, dev)
+                                and slot_mapping is not None
+                                and _dense(slot_mapping, torch.int64, (T,), dev)))
+            and _status_ok(status, dev)):
+        if caches and (v_cache is None or slot_mapping is None):
+            raise ValueError(f"{name}: the cache write needs k_cache, v_cache and slot_mapping")
+        _complain(name, dev,
+                  (("positions", positions, torch.int32, pos_shape),
+                   ("table", table, torch.int64, (n,)), ("k_cache", k_cache, dt, caches),
+                   ("v_cache", v_cache, dt, caches),
+                   ("slot_mapping", slot_mapping, torch.int64, (T,))),
+                  (("q", q, dt, (T, H, D)), ("k", k, dt, kv), ("v", v, dt, kv),
+                   ("q_out", q_out, dt, (T, H, D)), ("k_out", k_out, dt, kv)), status)
+    _run(lib().pa_rope_cache_write, name, dev, stream, q.data_ptr(), k.data_ptr(),
+         v.data_ptr() if caches else None, positions.data_ptr(), table.data_ptr(),
+         slot_mapping.data_ptr() if caches else None, T, H, Hkv, D, 2 * n, axes,
+         1 if interleaved else 0, code, _stride(q), _stride(k), _stride(v) if caches else 0, bs,
+         NB, q_out.data_ptr(), _stride(q_out), None if k_out is None else k_out.data_ptr(),
+         0 if k_out is None else _stride(k_out), k_cache.data_ptr() if caches else None,
+         v_cache.data_ptr() if caches else None, None if status is None else status.data_ptr())
     return q_out, k_out
 
 
@@ -196,46 +236,42 @@ def pa_prompt_attention(q, k, v, q_offsets, scale, out=None, status=None, stream
     int32: sequence b is rows q_offsets[b] .. q_offsets[b+1]-1.  Returns ``out``
     [T,H,D]; rows outside the sequences are left as they were (undefined when
     ``out`` is allocated here)."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    dt = q.dtype
-    qs = _rows(q, dt, "q", -1, -1, -1)
-    T, H, D = q.shape
-    ks = _rows(k, dt, "k", T, -1, D)
-    Hkv = k.shape[1]
-    vs = _rows(v, dt, "v", T, Hkv, D)
-    _dense(q_offsets, torch.int32, "q_offsets", -1)
-    B = q_offsets.shape[0] - 1
+    name = "pa_prompt_attention"
+    _shaped(name, ("q", q, 3), ("k", k, 3), ("v", v, 3), ("q_offsets", q_offsets, 1))
+    code, dt, dev = _float16(name, q), q.dtype, q.get_device()
+    (T, H, D), Hkv, n = q.shape, k.shape[1], q_offsets.shape[0]
     if out is None:
         out = torch.empty((T, H, D), dtype=dt, device=q.device)
-    else:
-        _dense(out, dt, "out", T, H, D)
-    dev = _same_device("pa_prompt_attention", q, k, v, q_offsets, out, status)
-    _run(lib().pa_prompt_attention, "pa_prompt_attention", dev, stream, _ptr(q), _ptr(k),
-         _ptr(v), _ptr(q_offsets), B, T, H, Hkv, D, _DTYPE[dt], qs, ks, vs, float(scale),
-         _ptr(out), _status(status))
+    if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _rows(k, dt, (T, Hkv, D), dev)
+            and _rows(v, dt, (T, Hkv, D), dev) and _dense(q_offsets, torch.int32, (n,), dev)
+            and _dense(out, dt, (T, H, D), dev) and _status_ok(status, dev)):
+        _complain(name, dev, (("q_offsets", q_offsets, torch.int32, (n,)),
+                              ("out", out, dt, (T, H, D))),
+                  (("q", q, dt, (T, H, D)), ("k", k, dt, (T, Hkv, D)),
+                   ("v", v, dt, (T, Hkv, D))), status)
+    _run(lib().pa_prompt_attention, name, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         q_offsets.data_ptr(), n - 1, T, H, Hkv, D, code, _stride(q), _stride(k), _stride(v),
+         scale, out.data_ptr(), None if status is None else status.data_ptr())
     return out
 
 
-def _cache(dt, D, k_cache, v_cache, block_tables, context_lens, B):
-    """(num_blocks, block_size, Hkv, max_blocks) of a checked paged cache."""
-    _dense(k_cache, dt, "k_cache", -1, -1, -1, D)
-    NB, bs, Hkv, _ = k_cache.shape
-    _dense(v_cache, dt, "v_cache", NB, bs, Hkv, D)
-    _dense(block_tables, torch.int32, "block_tables", B, -1)
-    _dense(context_lens, torch.int32, "context_lens", B)
-    return NB, bs, Hkv, block_tables.shape[1]
-
-
-def _workspace(workspace, nbytes, device):
-    """(tensor, bytes) of the given workspace, or of a new one where one is needed."""
+def _workspace(name, workspace, nbytes, dev):
+    """(address, bytes, owner) of the given workspace, or of a new one of nbytes."""
     if workspace is None:
         if nbytes == 0:
-            return None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace, workspace.numel() * workspace.element_size()
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"{name}: workspace must be contiguous and on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _sized(fn, dev, *args):
+    """A workspace size, which depends on the device, with that device current."""
+    if dev == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def pa_chunk_attention_workspace_size(B, T, H, Hkv, D, max_context_len):
@@ -253,32 +289,34 @@ def pa_chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offset
     what the tables hold).  A workspace for the split of long contexts is
     allocated when not given; split=False passes none.  Returns ``out``
     [T,H,D]; rows outside the sequences are left as they were."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    dt = q.dtype
-    qs = _rows(q, dt, "q", -1, -1, -1)
-    T, H, D = q.shape
-    _dense(q_offsets, torch.int32, "q_offsets", -1)
-    B = q_offsets.shape[0] - 1
-    NB, bs, Hkv, M = _cache(dt, D, k_cache, v_cache, block_tables, context_lens, B)
+    name = "pa_chunk_attention"
+    _shaped(name, ("q", q, 3), ("k_cache", k_cache, 4), ("block_tables", block_tables, 2),
+            ("q_offsets", q_offsets, 1))
+    code, dt, dev = _float16(name, q), q.dtype, q.get_device()
+    (T, H, D), (NB, bs, Hkv, _), n = q.shape, k_cache.shape, q_offsets.shape[0]
+    B, M, pool = n - 1, block_tables.shape[1], (NB, bs, Hkv, D)
     cap = M * bs if max_context_len is None else int(max_context_len)
     if out is None:
         out = torch.empty((T, H, D), dtype=dt, device=q.device)
-    else:
-        _dense(out, dt, "out", T, H, D)
-    dev = _same_device("pa_chunk_attention", q, k_cache, v_cache, block_tables, context_lens,
-                       q_offsets, out, workspace, status)
+    if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _dense(k_cache, dt, pool, dev)
+            and _dense(v_cache, dt, pool, dev) and _dense(block_tables, torch.int32, (B, M), dev)
+            and _dense(context_lens, torch.int32, (B,), dev)
+            and _dense(q_offsets, torch.int32, (n,), dev) and _dense(out, dt, (T, H, D), dev)
+            and _status_ok(status, dev)):
+        _complain(name, dev, (("k_cache", k_cache, dt, pool), ("v_cache", v_cache, dt, pool),
+                              ("block_tables", block_tables, torch.int32, (B, M)),
+                              ("context_lens", context_lens, torch.int32, (B,)),
+                              ("q_offsets", q_offsets, torch.int32, (n,)),
+                              ("out", out, dt, (T, H, D))), (("q", q, dt, (T, H, D)),), status)
     ws, ws_bytes = None, 0
     if split:
-        need = 0
-        if workspace is None:
-            with torch.cuda.device(dev):
-                need = pa_chunk_attention_workspace_size(B, T, H, Hkv, D, cap)
-        ws, ws_bytes = _workspace(workspace, need, dev)
-    _run(lib().pa_chunk_attention, "pa_chunk_attention", dev, stream, _ptr(q), _ptr(k_cache),
-         _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), _ptr(q_offsets), B, T, H, Hkv, D,
-         _DTYPE[dt], qs, bs, NB, M, cap, float(scale), _ptr(out), _ptr(ws), ws_bytes,
-         _status(status))
+        need = 0 if workspace is not None else _sized(pa_chunk_attention_workspace_size, dev, B,
+                                                      T, H, Hkv, D, cap)
+        ws, ws_bytes, workspace = _workspace(name, workspace, need, dev)
+    _run(lib().pa_chunk_attention, name, dev, stream, q.data_ptr(), k_cache.data_ptr(),
+         v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+         q_offsets.data_ptr(), B, T, H, Hkv, D, code, _stride(q), bs, NB, M, cap, scale,
+         out.data_ptr(), ws, ws_bytes, None if status is None else status.data_ptr())
     return out
 
 
@@ -294,28 +332,27 @@ def pa_decode_grouped(q, k_cache, v_cache, block_tables, context_lens, scale, ma
     """Paged decode attention with grouped heads: q [B,H,D] (fp16 or bf16), caches
     [NB,bs,Hkv,D] of the same type, ``max_context_len`` a host-side bound on
     context_lens.  Returns ``out`` [B,H,D]."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    dt = q.dtype
-    if dt not in _DTYPE:
-        raise TypeError(f"q must be fp16 or bf16, got {dt}")
-    _dense(q, dt, "q", -1, -1, -1)
-    B, H, D = q.shape
-    NB, bs, Hkv, M = _cache(dt, D, k_cache, v_cache, block_tables, context_lens, B)
-    cap = int(max_context_len)
+    name = "pa_decode_grouped"
+    _shaped(name, ("q", q, 3), ("k_cache", k_cache, 4), ("block_tables", block_tables, 2))
+    code, dt, dev = _float16(name, q), q.dtype, q.get_device()
+    (B, H, D), (NB, bs, Hkv, _) = q.shape, k_cache.shape
+    M, pool, cap = block_tables.shape[1], (NB, bs, Hkv, D), int(max_context_len)
     if out is None:
-        out = torch.empty_like(q)
-    else:
-        _dense(out, dt, "out", B, H, D)
-    dev = _same_device("pa_decode_grouped", q, k_cache, v_cache, block_tables, context_lens, out,
-                       workspace, status)
-    need = 0
-    if workspace is None:
-        with torch.cuda.device(dev):
-            need = pa_decode_grouped_workspace_size(B, H, Hkv, D, bs, cap, partition_tokens)
-    ws, ws_bytes = _workspace(workspace, need, dev)
-    _run(lib().pa_decode_grouped, "pa_decode_grouped", dev, stream, _ptr(q), _ptr(k_cache),
-         _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), B, H, Hkv, D, _DTYPE[dt], bs, NB,
-         M, cap, int(partition_tokens), float(scale), _ptr(out), _ptr(ws), ws_bytes,
-         _status(status))
+        out = torch.empty((B, H, D), dtype=dt, device=q.device)
+    if not (dev >= 0 and _dense(q, dt, (B, H, D), dev) and _dense(k_cache, dt, pool, dev)
+            and _dense(v_cache, dt, pool, dev) and _dense(block_tables, torch.int32, (B, M), dev)
+            and _dense(context_lens, torch.int32, (B,), dev) and _dense(out, dt, (B, H, D), dev)
+            and _status_ok(status, dev)):
+        _complain(name, dev, (("q", q, dt, (B, H, D)), ("k_cache", k_cache, dt, pool),
+                              ("v_cache", v_cache, dt, pool),
+                              ("block_tables", block_tables, torch.int32, (B, M)),
+                              ("context_lens", context_lens, torch.int32, (B,)),
+                              ("out", out, dt, (B, H, D))), (), status)
+    need = 0 if workspace is not None else _sized(pa_decode_grouped_workspace_size, dev, B, H,
+                                                  Hkv, D, bs, cap, partition_tokens)
+    ws, ws_bytes, workspace = _workspace(name, workspace, need, dev)
+    _run(lib().pa_decode_grouped, name, dev, stream, q.data_ptr(), k_cache.data_ptr(),
+         v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, H, Hkv, D, code,
+         bs, NB, M, cap, partition_tokens, scale, out.data_ptr(), ws, ws_bytes,
+         None if status is None else status.data_ptr())
     return out
