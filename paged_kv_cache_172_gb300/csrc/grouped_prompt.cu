@@ -57,14 +57,14 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTile = 128;               // query rows of a tile, keys of a key tile
 constexpr int kSlab = 128 * 128;         // 128 rows x 64 dims (128 bytes)
 constexpr int kQRoom = 2 * kSlab;        // a Q tile's room, up to 128 dims
-constexpr int kThreadsG = 352;           // 8 softmax warps, producer, 2 MMA issuers
-constexpr int kWarps = kThreadsG / 32;
-constexpr int kWarpLoad = 8, kWarpS = 9, kWarpPv = 10;
+constexpr int kThreadsG = 384;           // 8 softmax warps, K/V loads, 2 MMA issuers, scheduler
+constexpr int kWarpLoad = 8, kWarpS = 9, kWarpPv = 10, kWarpSched = 11;
+constexpr int kItems = 3;                // items posted ahead
 constexpr int kCols = 512;               // tensor memory columns
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr int kWindow = 256;             // block-table entries staged at a time
 constexpr int kMaxRing = 8;
-constexpr int kBars = 1 + 2 * kMaxRing + 8 + 1;
+constexpr int kBars = 2 * kMaxRing + 15 + 2 * kItems + 1;
 constexpr float kLazy = 8.0f;            // log2 of the growth that forces a rescale
 
 // Layout of a K or V tile in shared memory.  Paged: key groups of 8 keys x D
@@ -80,8 +80,8 @@ struct Cfg {
   static constexpr int HALF = PAGED ? 1024 : kSlab;       // from dims 0-63 to dims 64-127
   static constexpr int OFF_KV = 2 * kQRoom;
   static constexpr int OFF_BAR = OFF_KV + RING * TILE_BYTES;
-  static constexpr int OFF_MISC = OFF_BAR + kBars * 8;  // TMEM address, issue counters, search
-  static constexpr int OFF_TBL = (OFF_MISC + 128 + 15) / 16 * 16;
+  static constexpr int OFF_MISC = OFF_BAR + kBars * 8;  // TMEM address, issue counters, items
+  static constexpr int OFF_TBL = (OFF_MISC + 16 + kItems * 64 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_TBL + (PAGED ? kWindow * 4 : 0) + 1024;
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static constexpr int PART = D + 4;  // floats of a partial row: o[D], m, l, pad
@@ -157,44 +157,48 @@ __device__ __forceinline__ int warp_sum(int x) {
   return x;
 }
 
-// The unit of a rank (units by key tiles, longest first): true and (b, i), or
-// false behind the last unit.  All threads of the CTA call it.
+// Walks the units by key tiles, longest first (one warp, all lanes alike).
 template <bool PAGED>
-__device__ __forceinline__ bool find_unit(const GroupedArgs& a, int rank, int* s_cnt, int& b_out,
-                                          int& i_out) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // units with >= lo tiles: more than rank (lo = 0: taken as such); >= hi: at most rank
-  int lo = 0, hi = a.max_tiles + 1, above = 0;  // above: units with >= hi tiles
-  while (hi - lo > 1) {
-    const int gap = hi - lo;
-    const int t = lo + 1 + (int)((long long)warp * (gap - 1) / kWarps);
-    int c = 0;
-    for (int b = lane; b < a.B; b += 32) c += units_from(sequence<PAGED>(a, b), a.span, t);
-    c = warp_sum(c);
-    if (lane == 0) s_cnt[warp] = c;
-    __syncthreads();
-    int nlo = lo, nhi = hi, nabove = above;
+struct Units {
+  const GroupedArgs& a;
+  int bound, above;  // no unit asked for later reads `bound` key tiles or more; how many do
+
+  __device__ Units(const GroupedArgs& args) : a(args), bound(args.max_tiles + 1), above(0) {}
+
+  // The unit of a rank: (b, i), or false behind the last unit.  Ranks rise from
+  // call to call.
+  __device__ bool find(int rank, int& b_out, int& i_out) {
+    const int lane = threadIdx.x & 31;
+    // units with >= lo tiles: more than rank (lo = 0: taken as such); >= hi: at most rank
+    int lo = 0, hi = bound, over = above;
+    while (hi - lo > 1) {  // three candidates a pass over the sequences
+      const int gap = hi - lo;
+      int t[3], c[3] = {0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {  // candidates rise with w, counts fall
-      const int tw = lo + 1 + (int)((long long)w * (gap - 1) / kWarps);
-      if (s_cnt[w] > rank)
-        nlo = tw;
-      else if (tw < nhi) {
-        nhi = tw;
-        nabove = s_cnt[w];
+      for (int k = 0; k < 3; ++k) t[k] = lo + 1 + (int)((long long)(k + 1) * (gap - 2) / 4);
+#pragma unroll 1
+      for (int b = lane; b < a.B; b += 32) {
+        const Seq s = sequence<PAGED>(a, b);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) c[k] += units_from(s, a.span, t[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {  // candidates rise, counts fall
+        c[k] = warp_sum(c[k]);
+        if (c[k] > rank)
+          lo = t[k];
+        else if (t[k] < hi) {
+          hi = t[k];
+          over = c[k];
+        }
       }
     }
-    lo = nlo;
-    hi = nhi;
-    above = nabove;
-    __syncthreads();
-  }
-  if (lo == 0) return false;
-  // The units that read exactly lo tiles, sequences in order: the (rank - above)-th.
-  if (warp == 0) {
-    int left = rank - above;
-    bool found = false;
-    for (int base = 0; base < a.B && !found; base += 32) {
+    bound = hi;
+    above = over;
+    if (lo == 0) return false;
+    // The units that read exactly lo tiles, sequences in order: the (rank - over)-th.
+    int left = rank - over;
+    for (int base = 0; base < a.B; base += 32) {
       const int b = base + lane;
       int c = 0, upper = 0, nu = 0;
       if (b < a.B) {
@@ -211,21 +215,16 @@ __device__ __forceinline__ bool find_unit(const GroupedArgs& a, int rank, int* s
       }
       const unsigned hit = __ballot_sync(kAll, x > left);
       if (hit != 0) {
-        found = true;
-        if (lane == __ffs(hit) - 1) {
-          s_cnt[0] = b;
-          s_cnt[1] = nu - 1 - upper - (left - (x - c));
-        }
-      } else {
-        left -= __shfl_sync(kAll, x, 31);
+        const int src = __ffs(hit) - 1;
+        b_out = base + src;
+        i_out = __shfl_sync(kAll, nu - 1 - upper - (left - (x - c)), src);
+        return true;
       }
+      left -= __shfl_sync(kAll, x, 31);
     }
+    return false;
   }
-  __syncthreads();
-  b_out = s_cnt[0];
-  i_out = s_cnt[1];
-  return true;
-}
+};
 
 // Wait until the S issuer has issued `n` products of a tile.
 __device__ __forceinline__ bool wait_count(volatile int* cnt, int n) {
@@ -238,11 +237,43 @@ __device__ __forceinline__ bool wait_count(volatile int* cnt, int n) {
   return true;
 }
 
+// The registers of a thread: the softmax warps hold a row of S, the others next
+// to nothing (128 * (2 * 200 + 104) = 384 * 168, what the block is launched with).
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+}
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+}
+
+// A wait that is not on the chain of products: polled rarely.
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    __nanosleep(200);
+    if (clock64() - t0 > kWaitLimitCycles) return false;
+  }
+  return true;
+}
+
 // Ring index of K_t and V_t among n_kv key tiles (K_0, then K_{t+1}, V_t).
 __device__ __forceinline__ int ring_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int ring_v(int t, int n_kv) {
   return t + 1 < n_kv ? 2 * t + 2 : 2 * t + 1;
 }
+
+// What the scheduler posts of a work item: a unit, or one of its key ranges.
+static_assert(kThreadsG == 384, "register split");
+struct Item {
+  int valid;             // 0: no more items
+  int row0, hkv;         // packed row of tile A's first token; K/V head
+  int toks_a, toks_b;    // tokens of the tiles in this sequence
+  int pos_a;             // position of tile A's first token
+  int kt0, n_kv;         // first key tile, key tiles
+  int ntile_a, ntile_b;  // of those, the ones each tile reads
+  int parts, part;
+  int b, n;              // sequence and its keys
+};
 
 template <typename T, int D, bool PAGED>
 __global__ void __launch_bounds__(kThreadsG, 1)
@@ -260,349 +291,515 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + C::OFF_KV;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* q_full = bars;
-  uint64_t* kv_full = bars + 1;
+  uint64_t* kv_full = bars;
   uint64_t* kv_empty = kv_full + kRing;
-  uint64_t* s_full = kv_empty + kRing;  // [2] per tile: S(j) computed
+  uint64_t* q_full = kv_empty + kRing;  // [2] per tile: Q of the item landed
+  uint64_t* q_free = q_full + 2;        // [2]: the item's S products are done with it
+  uint64_t* s_full = q_free + 2;        // [2]: an S product computed
   uint64_t* s_free = s_full + 2;        // [2]: its softmax holds S in registers
-  uint64_t* p_full = s_free + 2;        // [2]: P(j) stored
-  uint64_t* pv_done = p_full + 2;       // [2]: O += P(j) V_j completed
-  uint64_t* drain = pv_done + 2;
+  uint64_t* p_full = s_free + 2;        // [2]: P stored
+  uint64_t* pv_done = p_full + 2;       // [2]: O += P V completed
+  uint64_t* out_full = pv_done + 2;     // [2]: the item's output tile is staged
+  uint64_t* stage_b = out_full + 2;     // tile A's output has left the stage
+  uint64_t* it_full = stage_b + 1;      // [kItems]: an item is posted
+  uint64_t* it_empty = it_full + kItems;  // [kItems]: every role has copied it
+  uint64_t* drain = it_empty + kItems;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* s_issued = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // [2]
-  int* s_cnt = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);                      // [11]
+  Item* items = reinterpret_cast<Item*>(smem + C::OFF_MISC + 16);
   int32_t* tbl = reinterpret_cast<int32_t*>(smem + C::OFF_TBL);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = blockIdx.x % a.split;
-  const int hkv = (blockIdx.x / a.split) % a.Hkv;
-  const int rank = blockIdx.x / (a.split * a.Hkv);
-
-  pdl_wait();
-  pdl_launch_dependents();
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.B; i += kThreadsG)
-      if (sequence<PAGED>(a, i).lost) flag_status(a.status, PA_DEV_BAD_CONTEXT);
-  int b, unit;
-  if (!find_unit<PAGED>(a, rank, s_cnt, b, unit)) return;
-  const Seq sq = sequence<PAGED>(a, b);
-  const int tok0 = unit * a.span;  // first token of tile A in its sequence
-  if (sq.bad) {                    // zero rows (its rows exist: ql > 0)
-    if (part != 0) return;
-    if (threadIdx.x == 0) flag_status(a.status, PA_DEV_BAD_CONTEXT);
-    const int rows = min(a.span, sq.ql - tok0);
-    const int per_tok = a.G * D / 8;  // 16-byte chunks
-    for (int i = threadIdx.x; i < rows * per_tok; i += kThreadsG)
-      reinterpret_cast<uint4*>(static_cast<T*>(a.out) +
-                               ((size_t)(sq.start + tok0 + i / per_tok) * a.H + hkv * a.G) * D)
-          [i % per_tok] = make_uint4(0u, 0u, 0u, 0u);
-    return;
-  }
-  // Key tiles of the unit, and this CTA's range of them.
-  const int all_tiles = unit_tiles(sq, a.span, unit);
-  const int parts = unit_parts(all_tiles, a.split, a.min_part_tiles);
-  if (part >= parts) return;
-  const int kt0 = (int)((long long)part * all_tiles / parts);
-  const int n_kv = (int)((long long)(part + 1) * all_tiles / parts) - kt0;
   const int tpt = a.span / 2;  // tokens of a tile
-  const int toks_a = min(tpt, sq.ql - tok0), toks_b = max(0, min(tpt, sq.ql - tok0 - tpt));
-  const int pos_a = sq.n - sq.ql + tok0, pos_b = pos_a + tpt;  // first positions
-  auto tiles_of = [&](int pos, int toks) {
-    const int all = toks > 0 ? (pos + toks - 1) / kTile + 1 : 0;
-    return min(max(all - kt0, 0), n_kv);
-  };
-  const int ntile_a = tiles_of(pos_a, toks_a), ntile_b = tiles_of(pos_b, toks_b);
-  const int row0 = sq.start + tok0;  // packed row of tile A's first token
 
   if (threadIdx.x == 0) {
     s_issued[0] = 0;
     s_issued[1] = 0;
-    mbar_init(q_full, 1);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 4);  // one arrival per softmax warp
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&out_full[i], 4);
+    }
+    mbar_init(stage_b, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], kWarpSched);  // every other warp
     }
     mbar_init(drain, 2);
     fence_mbar_init();
-    // Q first: it heads the start-up path.  A box is tpt tokens x G heads x 64
-    // dims; tokens past the packed rows read as zeros.
-    mbar_arrive_expect_tx(q_full, 2 * C::HALVES * tpt * a.G * 128);
-    for (int x = 0; x < 2; ++x)
-      for (int hf = 0; hf < C::HALVES; ++hf)
-        tma_load_3d(sQ + x * kQRoom + hf * kSlab, &qmap, 64 * hf, hkv * a.G, row0 + x * tpt,
-                    q_full);
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+    prefetch_tmap(&omap);
   }
   if (warp == kWarpS) {
     tc::tmem_alloc(tmem_at, kCols);
     tc::tmem_relinquish();
   }
+  pdl_wait();
+  pdl_launch_dependents();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_at;
   bool ok = true;
-  int issued = 0;  // ring tiles requested
+  int issued = 0;  // ring tiles, or Q loads, requested
 
-  if (warp == kWarpLoad) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      prefetch_tmap(&kmap);
-      prefetch_tmap(&vmap);
-    }
-    const int bpt = PAGED ? kTile / a.block_size : 1;  // blocks of a key tile
-    const int nblk = PAGED ? (sq.n + a.block_size - 1) / a.block_size : 0;
-    int win = -kWindow;
-    auto load_tile = [&](int t, bool v, int u) {
-      const int lb0 = (kt0 + t) * bpt;
-      if (PAGED && (lb0 < win || lb0 + bpt > win + kWindow)) {
-        // K_t is requested before V_{t-1}: the window starts one tile early.
-        win = (!v && t > 0) ? lb0 - bpt : lb0;
-        __syncwarp();
-        int ent[kWindow / 32];
-#pragma unroll
-        for (int k = 0; k < kWindow / 32; ++k) {
-          const int lb = win + lane + 32 * k;
-          ent[k] = lb < nblk ? __ldg(a.block_tables + (size_t)b * a.max_blocks + lb)
-                             : a.num_blocks;  // past the sequence: zeros
-        }
-#pragma unroll
-        for (int k = 0; k < kWindow / 32; ++k) {
-          int phys = ent[k];
-          if (phys < 0 || phys > a.num_blocks ||
-              (phys == a.num_blocks && win + lane + 32 * k < nblk)) {
-            flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
-            phys = a.num_blocks;
+  // The k-th item of this CTA, copied; the scheduler may then reuse its room.
+  auto take = [&](int k, Item& it) {
+    if (!(ok = __all_sync(kAll, mbar_wait(&it_full[k % kItems], (k / kItems) & 1)))) return false;
+    it = items[k % kItems];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&it_empty[k % kItems]);
+    return it.valid != 0;
+  };
+
+  if (warp == kWarpSched) {
+    // ------------------------------------------------------------ scheduler, Q loads
+    reg_dec();
+    if (blockIdx.x == 0)
+      for (int i = lane; i < a.B; i += 32)
+        if (sequence<PAGED>(a, i).lost) flag_status(a.status, PA_DEV_BAD_CONTEXT);
+    Units<PAGED> units(a);
+    const long long n_items = (long long)a.max_units * a.Hkv * a.split;
+    int round = 0, last_rank = -1, b = 0, unit = 0;
+    bool more = true;
+    // Items are dealt in rounds, every other one backwards, so that no CTA
+    // gets the longest of every round.
+    auto next = [&](Item& it) {
+      it.valid = 0;
+      while (more) {
+        const int at = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+        const long long idx = (long long)round * gridDim.x + at;
+        ++round;
+        if (!(more = idx < n_items)) break;
+        it.part = (int)(idx % a.split);
+        it.hkv = (int)(idx / a.split % a.Hkv);
+        const int rank = (int)(idx / ((long long)a.split * a.Hkv));
+        if (rank != last_rank && !(more = units.find(rank, b, unit))) break;
+        last_rank = rank;
+        const Seq s = sequence<PAGED>(a, b);
+        const int tok0 = unit * a.span;
+        const int all = unit_tiles(s, a.span, unit);
+        it.parts = unit_parts(all, a.split, a.min_part_tiles);
+        if (it.part >= it.parts) continue;
+        it.valid = 1;
+        it.b = b;
+        it.n = s.n;
+        it.row0 = s.start + tok0;
+        it.toks_a = min(tpt, s.ql - tok0);
+        it.toks_b = max(0, min(tpt, s.ql - tok0 - tpt));
+        it.pos_a = s.n - s.ql + tok0;
+        it.kt0 = (int)((long long)it.part * all / it.parts);
+        it.n_kv = (int)((long long)(it.part + 1) * all / it.parts) - it.kt0;
+        auto reads = [&](int pos, int toks) {
+          const int t = toks > 0 ? (pos + toks - 1) / kTile + 1 : 0;
+          return min(max(t - it.kt0, 0), it.n_kv);
+        };
+        it.ntile_a = reads(it.pos_a, it.toks_a);
+        it.ntile_b = reads(it.pos_a + tpt, it.toks_b);
+        if (s.bad) {  // no keys: zero rows, written by the first part
+          if (lane == 0) flag_status(a.status, PA_DEV_BAD_CONTEXT);
+          if (it.part > 0) {
+            it.valid = 0;
+            continue;
           }
-          tbl[lane + 32 * k] = phys;
+          it.parts = 1;
+          it.kt0 = it.n_kv = it.ntile_a = it.ntile_b = 0;
+        }
+        break;
+      }
+    };
+    auto post = [&](int k, const Item& it) {
+      if (!(ok = __all_sync(kAll, wait_slow(&it_empty[k % kItems], ((k / kItems) & 1) ^ 1))))
+        return;
+      if (lane == 0) {
+        items[k % kItems] = it;
+        mbar_arrive(&it_full[k % kItems]);  // (release: the stores above are seen)
+      }
+      __syncwarp();
+    };
+    // The output tiles of an item leave the ring slot it staged them in: a whole
+    // tile by TMA, one that ends inside a sequence by 16-byte copies of its rows
+    // alone, since the next packed rows are another sequence's.
+    int staged = 0, stage_u = 0;  // items stored so far; ring index of the item's stage
+    auto store = [&](const Item& it) {
+      stage_u += 2 * it.n_kv;
+      if (it.parts > 1) return;
+      uint8_t* stage = sKV + (stage_u % kRing) * C::TILE_BYTES;
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (!(ok = __all_sync(kAll, wait_slow(&out_full[x], staged & 1)))) return;
+        const int toks = x ? it.toks_b : it.toks_a, row = it.row0 + x * tpt;
+        if (toks == tpt) {
+          if (lane == 0) {
+            for (int hf = 0; hf < C::HALVES; ++hf)
+              tma_store_3d(&omap, stage + hf * kSlab, 64 * hf, it.hkv * a.G, row);
+            bulk_commit_group();
+            bulk_wait_read();
+          }
+        } else {
+          constexpr int kChunks = D / 8;
+          for (int i = lane; i < toks * a.G * kChunks; i += 32) {
+            const int r = i / kChunks, c = i % kChunks;
+            const uint4 w = *reinterpret_cast<const uint4*>(
+                stage + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) * 16));
+            *reinterpret_cast<uint4*>(
+                static_cast<T*>(a.out) +
+                ((size_t)(row + r / a.G) * a.H + it.hkv * a.G + r % a.G) * D + c * 8) = w;
+          }
         }
         __syncwarp();
+        if (lane == 0) {
+          // (the next writer of the slot may be TMA: order the generic reads first)
+          fence_proxy_async_smem();
+          mbar_arrive(x == 0 ? stage_b : &kv_empty[stage_u % kRing]);
+        }
       }
-      const int st = u % kRing;
-      if (lane == 0) {
-        ok = mbar_wait(&kv_empty[st], ((u / kRing) & 1) ^ 1);
-        if (ok) mbar_arrive_expect_tx(&kv_full[st], C::TILE_BYTES);
-      }
-      ok = __shfl_sync(kAll, ok, 0);
-      if (!ok) return;
-      uint8_t* dst = sKV + st * C::TILE_BYTES;
-      if constexpr (PAGED) {
-        // One box per block, from lane to lane: (64 dims, 8 keys, halves, key
-        // groups) at row (block * block_size * Hkv + head) of the pool.
-        for (int i = lane; i < bpt; i += 32)
-          tma_load_5d(dst + i * (a.block_size / 8) * C::GROUP, v ? &vmap : &kmap, 0, 0, 0, 0,
-                      tbl[lb0 - win + i] * a.block_size * a.Hkv + hkv, &kv_full[st]);
-      } else if (lane == 0) {
-        // 128 tokens of one head, both halves; rows past the array read as zeros.
-        tma_load_4d(dst, v ? &vmap : &kmap, 0, sq.start + (kt0 + t) * kTile, 0, hkv,
-                    &kv_full[st]);
-      }
-      if (lane == 0) ++issued;
+      ++staged;
+      ++stage_u;
     };
-    int u = 0;
-    if (n_kv > 0) load_tile(0, false, u++);
-    for (int j = 0; j < n_kv && ok; ++j) {
-      if (j + 1 < n_kv) load_tile(j + 1, false, u++);
-      if (ok) load_tile(j, true, u++);
+    Item cur, nxt, prev;
+    prev.valid = 0;
+    next(cur);
+    post(0, cur);
+    for (int k = 0; ok && cur.valid; ++k) {
+      next(nxt);
+      post(k + 1, nxt);
+      if (!ok) break;
+      // Q of item k, tile by tile as the products of item k - 1 let go of it:
+      // boxes of tpt tokens x G heads x 64 dims; rows past the array read as zeros.
+      if (lane == 0)
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (!(ok = mbar_wait(&q_free[x], (k & 1) ^ 1))) break;
+          mbar_arrive_expect_tx(&q_full[x], C::HALVES * tpt * a.G * 128);
+          for (int hf = 0; hf < C::HALVES; ++hf)
+            tma_load_3d(sQ + x * kQRoom + hf * kSlab, &qmap, 64 * hf, cur.hkv * a.G,
+                        cur.row0 + x * tpt, &q_full[x]);
+          ++issued;
+        }
+      if (!(ok = __shfl_sync(kAll, ok, 0))) break;
+      if (prev.valid) store(prev);
+      prev = cur;
+      cur = nxt;
+    }
+    if (ok && prev.valid) store(prev);
+    if (lane == 0) bulk_wait_all();
+  } else if (warp == kWarpLoad) {
+    // ------------------------------------------------------------ K and V
+    reg_dec();
+    const int bpt = PAGED ? kTile / a.block_size : 1;  // blocks of a key tile
+    int u = 0;  // ring index, over all items
+    Item it;
+    for (int k = 0; take(k, it); ++k) {
+      const int nblk = PAGED ? (it.n + a.block_size - 1) / a.block_size : 0;
+      const int row = PAGED ? 0 : it.row0 - it.pos_a;  // first packed row of the sequence
+      int win = -kWindow;
+      auto load_tile = [&](int t, bool v) {
+        const int lb0 = (it.kt0 + t) * bpt;
+        if (PAGED && (lb0 < win || lb0 + bpt > win + kWindow)) {
+          // K_t is requested before V_{t-1}: the window starts one tile early.
+          win = (!v && t > 0) ? lb0 - bpt : lb0;
+          __syncwarp();
+          int ent[kWindow / 32];
+#pragma unroll
+          for (int e = 0; e < kWindow / 32; ++e) {
+            const int lb = win + lane + 32 * e;
+            ent[e] = lb < nblk ? __ldg(a.block_tables + (size_t)it.b * a.max_blocks + lb)
+                               : a.num_blocks;  // past the sequence: zeros
+          }
+#pragma unroll
+          for (int e = 0; e < kWindow / 32; ++e) {
+            int phys = ent[e];
+            if (phys < 0 || phys > a.num_blocks ||
+                (phys == a.num_blocks && win + lane + 32 * e < nblk)) {
+              flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+              phys = a.num_blocks;
+            }
+            tbl[lane + 32 * e] = phys;
+          }
+          __syncwarp();
+        }
+        const int st = u % kRing;
+        if (lane == 0) {
+          ok = mbar_wait(&kv_empty[st], ((u / kRing) & 1) ^ 1);
+          if (ok) mbar_arrive_expect_tx(&kv_full[st], C::TILE_BYTES);
+        }
+        ok = __shfl_sync(kAll, ok, 0);
+        if (!ok) return;
+        uint8_t* dst = sKV + st * C::TILE_BYTES;
+        if constexpr (PAGED) {
+          // One box per block, from lane to lane: (64 dims, 8 keys, halves, key
+          // groups) at row (block * block_size * Hkv + head) of the pool.
+          for (int i = lane; i < bpt; i += 32)
+            tma_load_5d(dst + i * (a.block_size / 8) * C::GROUP, v ? &vmap : &kmap, 0, 0, 0, 0,
+                        tbl[lb0 - win + i] * a.block_size * a.Hkv + it.hkv, &kv_full[st]);
+        } else if (lane == 0) {
+          // 128 tokens of one head, both halves; rows past the array read as zeros.
+          tma_load_4d(dst, v ? &vmap : &kmap, 0, row + (it.kt0 + t) * kTile, 0, it.hkv,
+                      &kv_full[st]);
+        }
+        issued = ++u;
+      };
+      if (it.n_kv > 0) load_tile(0, false);
+      for (int j = 0; j < it.n_kv && ok; ++j) {
+        if (j + 1 < it.n_kv) load_tile(j + 1, false);
+        if (ok) load_tile(j, true);
+      }
+      // One slot of the ring is the item's output stage.
+      if (ok && it.parts == 1) {
+        const int st = u % kRing;
+        if (lane == 0) {
+          ok = mbar_wait(&kv_empty[st], ((u / kRing) & 1) ^ 1);
+          if (ok) mbar_arrive(&kv_full[st]);
+        }
+        ok = __shfl_sync(kAll, ok, 0);
+        if (ok) issued = ++u;
+      }
+      if (!ok) break;
     }
   } else if (warp == kWarpS) {
     // ------------------------------------------------------------ S = Q K^T
-    if (lane == 0) {
-      const int nt[2] = {ntile_a, ntile_b};
-      const uint64_t dk = tc::smem_desc(smem_u32(sKV), 16, C::GROUP, tc::kSwizzle128B);
-      const uint64_t dq = tc::smem_desc(smem_u32(sQ), 16, 1024, tc::kSwizzle128B);
-      bool q_there = false;
-      int last_x = -1, last_t = 0;
-      for (int t = 0; t < n_kv && ok; ++t) {
-        const int u = ring_k(t);
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (t >= nt[x]) continue;
-          if (!q_there && !(ok = q_there = mbar_wait(q_full, 0))) break;
-          if (last_x >= 0 && !(ok = mbar_wait(&s_free[last_x], last_t & 1))) break;
-          if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) break;
-          tc::fence_after_sync();
-          const uint64_t db = dk + (u % kRing) * (C::TILE_BYTES >> 4);
-          const uint64_t da = dq + x * (kQRoom >> 4);
+    reg_dec();
+    const uint64_t dk = tc::smem_desc(smem_u32(sKV), 16, C::GROUP, tc::kSwizzle128B);
+    const uint64_t dq = tc::smem_desc(smem_u32(sQ), 16, 1024, tc::kSwizzle128B);
+    // (The loops over the two tiles are unrolled: an array indexed at run time
+    // would sit in local memory, on the chain from one S product to the next.)
+    int u0 = 0, done[2] = {0, 0};   // ring tiles and products of the items before
+    uint64_t* last_free = nullptr;  // s_free of the product issued last, its phase
+    int last_phase = 0;
+    Item it;
+    for (int k = 0; take(k, it); ++k) {
+      const int nt[2] = {it.ntile_a, it.ntile_b};
+      if (lane == 0) {
+        bool q_there[2] = {false, false};
+        for (int t = 0; t < it.n_kv && ok; ++t) {
+          const int u = u0 + ring_k(t);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_f16(tmem + kColS, da + (((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
-                        db + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4), kIdS, kk > 0);
-          tc::commit(&s_full[x]);
-          s_issued[x] = t + 1;  // a scheduling hint to the P V issuer
-          last_x = x;
-          last_t = t;
+          for (int x = 0; x < 2; ++x) {
+            if (t >= nt[x] || !ok) continue;
+            if (!q_there[x] && !(ok = q_there[x] = mbar_wait(&q_full[x], k & 1))) continue;
+            // S is free once the softmax of the product before has loaded it.
+            if (last_free != nullptr && !(ok = mbar_wait(last_free, last_phase))) continue;
+            if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) continue;
+            tc::fence_after_sync();
+            const uint64_t db = dk + (u % kRing) * (C::TILE_BYTES >> 4);
+            const uint64_t da = dq + x * (kQRoom >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_f16(tmem + kColS, da + (((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
+                          db + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4), kIdS, kk > 0);
+            tc::commit(&s_full[x]);
+            if (t + 1 == nt[x]) tc::commit(&q_free[x]);
+            last_free = &s_free[x];
+            last_phase = done[x] & 1;
+            s_issued[x] = ++done[x];  // a scheduling hint to the P V issuer
+          }
+          if (ok) tc::commit(&kv_empty[u % kRing]);
         }
-        if (ok) tc::commit(&kv_empty[u % kRing]);
+        // A tile that read nothing lets its Q go, once it has landed.
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (ok && nt[x] == 0 && (ok = mbar_wait(&q_full[x], k & 1))) mbar_arrive(&q_free[x]);
+        u0 += 2 * it.n_kv + (it.parts == 1);
       }
+      if (!(ok = __shfl_sync(kAll, ok, 0))) break;
     }
-    ok = __shfl_sync(kAll, ok, 0);
   } else if (warp == kWarpPv) {
     // ------------------------------------------------------------ O += P V
-    const int nt[2] = {ntile_a, ntile_b};
+    reg_dec();
     const uint64_t dv = tc::smem_desc(smem_u32(sKV), C::HALF, C::GROUP, tc::kSwizzle128B);
-    auto issue_pv = [&](int t) {  // lane 0
-      const int u = ring_v(t, n_kv);
-      for (int x = 0; x < 2 && ok; ++x) {
-        if (t >= nt[x]) continue;
-        if (!(ok = mbar_wait(&p_full[x], t & 1))) break;
-        if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) break;
-        // Behind S(t + 1) in the tensor core's queue, so that never waits for this.
-        if (t + 1 < nt[x] && !(ok = wait_count(s_issued + x, t + 2))) break;
-        tc::fence_after_sync();
-        const uint32_t ta = tmem + kColP + x * (kTile / 2);
-        const uint64_t db = dv + (u % kRing) * (C::TILE_BYTES >> 4);
+    int u0 = 0, done[2] = {0, 0};
+    Item it;
+    for (int k = 0; take(k, it); ++k) {
+      const int nt[2] = {it.ntile_a, it.ntile_b};
+      auto issue_pv = [&](int t) {  // lane 0
+        const int u = u0 + ring_v(t, it.n_kv);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          tc::mma_f16_ts(tmem + kColO + x * D, ta + kk * 8, db + ((kk * 2 * C::GROUP) >> 4), kIdO,
-                         t > 0 || kk > 0);
-        tc::commit(&pv_done[x]);
+        for (int x = 0; x < 2; ++x) {
+          if (t >= nt[x] || !ok) continue;
+          // (P of an item's first tile is stored behind the item before's last
+          // read of O by the same warps: O may then be overwritten.)
+          if (!(ok = mbar_wait(&p_full[x], done[x] & 1))) continue;
+          if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) continue;
+          // Behind S(t + 1) in the tensor core's queue, so that never waits for this.
+          if (t + 1 < nt[x] && !(ok = wait_count(s_issued + x, done[x] + 2))) continue;
+          tc::fence_after_sync();
+          const uint32_t ta = tmem + kColP + x * (kTile / 2);
+          const uint64_t db = dv + (u % kRing) * (C::TILE_BYTES >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc::mma_f16_ts(tmem + kColO + x * D, ta + kk * 8, db + ((kk * 2 * C::GROUP) >> 4),
+                           kIdO, t > 0 || kk > 0);
+          tc::commit(&pv_done[x]);
+          ++done[x];
+        }
+        if (ok) tc::commit(&kv_empty[u % kRing]);
+      };
+      if (lane == 0)
+        for (int t = 0; t + 1 < it.n_kv && ok; ++t) issue_pv(t);
+      if (!(ok = __shfl_sync(kAll, ok, 0))) break;
+      if (it.n_kv == 0) {
+        u0 += it.parts == 1;
+        continue;
       }
-      if (ok) tc::commit(&kv_empty[u % kRing]);
-    };
-    if (lane == 0)
-      for (int t = 0; t + 1 < n_kv && ok; ++t) issue_pv(t);
-    ok = __shfl_sync(kAll, ok, 0);
-    if (ok && n_kv > 0) {
       // Rows of the last key tile past the sequence's keys hold whatever the
       // block's tail, or the next sequence's rows, hold: 0 * NaN is NaN, so the
       // warp zeroes them once V has landed.
-      const int live = sq.n - (kt0 + n_kv - 1) * kTile;
+      const int live = it.n - (it.kt0 + it.n_kv - 1) * kTile;
       if (live < kTile) {
-        const int u = ring_v(n_kv - 1, n_kv);
+        const int u = u0 + ring_v(it.n_kv - 1, it.n_kv);
         if (lane == 0) ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1);
-        ok = __shfl_sync(kAll, ok, 0);
-        if (ok) {
-          uint8_t* vt = sKV + (u % kRing) * C::TILE_BYTES;
-          constexpr int kChunks = D / 8;
-          for (int i = lane; i < (kTile - live) * kChunks; i += 32) {
-            const int r = live + i / kChunks, c = i % kChunks;
-            *reinterpret_cast<uint4*>(vt + (r >> 3) * C::GROUP + (c >> 3) * C::HALF +
-                                      (r & 7) * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
+        if (!(ok = __shfl_sync(kAll, ok, 0))) break;
+        uint8_t* vt = sKV + (u % kRing) * C::TILE_BYTES;
+        constexpr int kChunks = D / 8;
+        for (int i = lane; i < (kTile - live) * kChunks; i += 32) {
+          const int r = live + i / kChunks, c = i % kChunks;
+          *reinterpret_cast<uint4*>(vt + (r >> 3) * C::GROUP + (c >> 3) * C::HALF +
+                                    (r & 7) * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
+        fence_proxy_async_smem();
         __syncwarp();
       }
-      if (ok && lane == 0) issue_pv(n_kv - 1);
+      if (lane == 0) issue_pv(it.n_kv - 1);
+      if (!(ok = __shfl_sync(kAll, ok, 0))) break;
+      u0 += 2 * it.n_kv + (it.parts == 1);
     }
-    ok = __shfl_sync(kAll, ok, 0);
   } else {
     // ------------------------------------------------------------ softmax
+    reg_inc();
     const int x = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
+    const int my_tok = row / a.G, my_g = row % a.G;
     const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_s = tmem + t_lane + kColS, t_o = tmem + t_lane + kColO + x * D;
-    const int pos0 = x ? pos_b : pos_a, toks = x ? toks_b : toks_a;
-    const int ntile = x ? ntile_b : ntile_a;
-    const int my_tok = row / a.G;
-    const bool live = my_tok < toks;  // a row of this sequence
-    const int pos = pos0 + my_tok;
     const float sl2 = a.scale_log2;
-    float m = -INFINITY, l = 0.f;
-    ok = __all_sync(kAll, mbar_wait(q_full, 0));
-    for (int j = 0; j < ntile && ok; ++j) {
-      if (!(ok = __all_sync(kAll, mbar_wait(&s_full[x], j & 1)))) break;
-      tc::fence_after_sync();
-      const int kbase = (kt0 + j) * kTile;
-      uint32_t r[4][32];
-      float cm[4];
+    int done = 0;    // key tiles of the items before and of this one
+    int u0 = 0;      // ring tiles of the items before
+    int staged = 0;  // output tiles staged so far
+    Item it;
+    for (int k = 0; take(k, it); ++k) {
+      const int pos0 = it.pos_a + (x ? tpt : 0);
+      const int ntile = x ? it.ntile_b : it.ntile_a;
+      const bool live = my_tok < (x ? it.toks_b : it.toks_a);  // a row of this sequence
+      const int pos = pos0 + my_tok;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < ntile; ++j, ++done) {
+        if (!(ok = __all_sync(kAll, mbar_wait(&s_full[x], done & 1)))) break;
+        tc::fence_after_sync();
+        const int kbase = (it.kt0 + j) * kTile;
+        uint32_t r[4][32];
+        float cm[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc::ld_32x32_max(t_s + c * 32, r[c], cm[c]);
-      tc::wait_ld();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[x]);
-      float mt = max3f(cm[0], cm[1], fmaxf(cm[2], cm[3]));
-      if (kbase + kTile - 1 > pos0) {  // keys past some row's position
+        for (int c = 0; c < 4; ++c) tc::ld_32x32_max(t_s + c * 32, r[c], cm[c]);
+        tc::wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[x]);
+        float mt = max3f(cm[0], cm[1], fmaxf(cm[2], cm[3]));
+        if (kbase + kTile - 1 > pos0) {  // keys past some row's position
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const int seen = pos - (kbase + c * 32);  // last key of these 32 it sees
+            const uint32_t hide = seen < 0 ? ~0u : seen >= 31 ? 0u : ~0u << (seen + 1);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (kbase + c * 32 + i > pos) r[c][i] = __float_as_uint(-INFINITY);
-        float mx[8];
+            for (int i = 0; i < 32; ++i)
+              if ((hide >> i) & 1) r[c][i] = __float_as_uint(-INFINITY);
+          }
+          float mx[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+          for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mx[(i >> 1) & 7] = max3f(mx[(i >> 1) & 7], __uint_as_float(r[c][i]),
-                                     __uint_as_float(r[c][i + 1]));
-        mt = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-      }
-      mt *= sl2;
-      const float m_new = fmaxf(m, mt);
-      const bool resc = live && m_new > m + kLazy;
-      float alpha = 1.f;
-      if (resc) {
-        alpha = ex2_approx(m - m_new);
-        m = m_new;
-        l *= alpha;
-      }
-      // A row that has seen masked keys alone (a part whose range starts past
-      // its position) has m = -inf, and -inf + inf is NaN: taken with maximum 0
-      // its weights are all zero and its partial row is empty.
-      const float neg_m = m == -INFINITY ? 0.f : -m;
-      float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float y0, y1;
-          fma_f32x2(y0, y1, __uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1]), sl2,
-                    sl2, neg_m, neg_m);
-          const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
-          const int k = 2 * (e & 3);
-          add_f32x2(rs[k], rs[k + 1], rs[k], rs[k + 1], p0, p1);
-          r[c][e] = pack2<T>(p0, p1);
+            for (int i = 0; i < 32; i += 2)
+              mx[(i >> 1) & 7] = max3f(mx[(i >> 1) & 7], __uint_as_float(r[c][i]),
+                                       __uint_as_float(r[c][i + 1]));
+          mt = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]),
+                     fmaxf(mx[6], mx[7]));
         }
-      l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
-      if (j > 0) {  // P V of the tile before done: P is free, O stands still
-        if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (j - 1) & 1)))) break;
+        mt *= sl2;
+        const float m_new = fmaxf(m, mt);
+        const bool resc = live && m_new > m + kLazy;
+        float alpha = 1.f;
+        if (resc) {
+          alpha = ex2_approx(m - m_new);
+          m = m_new;
+          l *= alpha;
+        }
+        // A row that has seen masked keys alone (a part whose range starts past
+        // its position) has m = -inf, and -inf + inf is NaN: taken with maximum 0
+        // its weights are all zero and its partial row is empty.
+        const float neg_m = m == -INFINITY ? 0.f : -m;
+        float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float y0, y1;
+            fma_f32x2(y0, y1, __uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1]),
+                      sl2, sl2, neg_m, neg_m);
+            const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+            const int q = 2 * (e & 3);
+            add_f32x2(rs[q], rs[q + 1], rs[q], rs[q + 1], p0, p1);
+            r[c][e] = pack2<T>(p0, p1);
+          }
+        l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+        if (j > 0) {  // P V of the tile before done: P is free, O stands still
+          if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
+          tc::fence_after_sync();
+          if (__any_sync(kAll, resc)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc::ld_32x32(t_o + c * 32, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tc::st_32x32(t_o + c * 32, o);
+            }
+            tc::wait_st();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)  // the packed pairs as they lie in the registers
+          tc::st_32x16(tmem + t_lane + kColP + x * (kTile / 2) + c * 16, r[c]);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      if (ntile > 0) {  // the last P V
+        if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
         tc::fence_after_sync();
       }
-      if (j > 0 && __any_sync(kAll, resc)) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tc::ld_32x32(t_o + c * 32, o);
-          tc::wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tc::st_32x32(t_o + c * 32, o);
-        }
-        tc::wait_st();
+      // The output: of a whole unit through the ring slot granted to the item,
+      // tile A first and B once A's has left it; of a part its unnormalised row.
+      const bool whole = it.parts == 1;
+      const int stage_u = u0 + 2 * it.n_kv;
+      if (whole) {
+        if (!(ok = __all_sync(kAll, x ? mbar_wait(stage_b, staged & 1)
+                                      : mbar_wait(&kv_full[stage_u % kRing],
+                                                  (stage_u / kRing) & 1))))
+          break;
+        ++staged;
       }
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t pw[32];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          pw[e] = r[2 * hf][e];
-          pw[16 + e] = r[2 * hf + 1][e];
-        }
-        tc::st_32x32(tmem + t_lane + kColP + x * (kTile / 2) + hf * 32, pw);
-      }
-      tc::wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[x]);
-    }
-    if (ok && ntile > 0) ok = __all_sync(kAll, mbar_wait(&pv_done[x], (ntile - 1) & 1));
-    // One decision for the tile: a wait that gave up in one warp must not leave
-    // the others at the barrier below.
-    ok = named_bar_and(1 + x, 128, ok);
-    if (ntile > 0) tc::fence_after_sync();
-    const int my_row = row0 + x * tpt + my_tok, my_head = hkv * a.G + row % a.G;
-    if (ok && parts > 1) {
-      // A part: the unnormalised row (o, m, l) for the merge.
-      float* wrow = a.ws + (((size_t)part * a.T + my_row) * a.H + my_head) * C::PART;
-#pragma unroll
+      u0 = stage_u + whole;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      uint8_t* srow = sKV + (stage_u % kRing) * C::TILE_BYTES + row * 128;
+      float* wrow = a.ws + (((size_t)it.part * a.T + it.row0 + (x ? tpt : 0) + my_tok) * a.H +
+                            it.hkv * a.G + my_g) * C::PART;
+      // (Rolled: the code of the hot loop above and of the other roles has to
+      // stay in the instruction cache.)
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         if (ntile > 0) {
@@ -612,7 +809,17 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-        if (live) {
+        if (whole) {  // swizzled rows of 64 dims, as the TMA boxes have them
+          uint32_t hv[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            hv[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+          uint8_t* slab = srow + (c >> 1) * kSlab;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(slab + ((((c & 1) << 2) + q) ^ (row & 7)) * 16) =
+                make_uint4(hv[4 * q], hv[4 * q + 1], hv[4 * q + 2], hv[4 * q + 3]);
+        } else if (live) {
           float4* dst = reinterpret_cast<float4*>(wrow + c * 32);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -620,68 +827,28 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                                  __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
       }
-      if (live) {
+      tc::fence_before_sync();  // O is read before the next item's P V overwrites it
+      if (whole) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&out_full[x]);
+      } else if (live) {
         wrow[D] = m;
         wrow[D + 1] = l;
-      }
-    } else if (ok && toks > 0) {
-      // The tile goes through Q's room (every S product of it is done), in the
-      // swizzled rows of the TMA boxes.  A whole tile of this sequence leaves by
-      // TMA; a tile that ends inside leaves by 16-byte stores of its live rows
-      // alone, since the next packed rows are another sequence's.
-      uint8_t* qrow = sQ + x * kQRoom + row * 128;
-      const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tc::ld_32x32(t_o + c * 32, o);
-        tc::wait_ld();
-        uint32_t hv[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          hv[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-        uint8_t* slab = qrow + (c >> 1) * kSlab;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(slab + ((((c & 1) << 2) + q) ^ (row & 7)) * 16) =
-              make_uint4(hv[4 * q], hv[4 * q + 1], hv[4 * q + 2], hv[4 * q + 3]);
-      }
-      const bool whole = toks == tpt;
-      if (whole) fence_proxy_async_smem();
-      named_bar_sync(1 + x, 128);
-      if (whole) {
-        if (quarter == 0 && lane == 0) {
-#pragma unroll
-          for (int hf = 0; hf < C::HALVES; ++hf)
-            tma_store_3d(&omap, sQ + x * kQRoom + hf * kSlab, 64 * hf, hkv * a.G,
-                         row0 + x * tpt);
-          bulk_commit_group();
-          bulk_wait_all();
-        }
-      } else {
-        constexpr int kChunks = D / 8;
-        for (int i = row; i < toks * a.G * kChunks; i += 128) {
-          const int r = i / kChunks, c = i % kChunks;
-          const uint4 w = *reinterpret_cast<const uint4*>(
-              sQ + x * kQRoom + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) * 16));
-          *reinterpret_cast<uint4*>(
-              static_cast<T*>(a.out) +
-              ((size_t)(row0 + x * tpt + r / a.G) * a.H + hkv * a.G + r % a.G) * D + c * 8) = w;
-        }
       }
     }
   }
 
-  // All roles meet.  After a wait that gave up, the producer lets its copies
-  // land and the issuers their MMAs end (both bounded) before the CTA leaves.
+  // All roles meet.  After a wait that gave up, the loaders let their copies
+  // land and the issuers their MMAs end (all bounded) before the CTA leaves.
   tc::fence_before_sync();
   if (__syncthreads_or(!ok)) {
     if (threadIdx.x == 0) flag_status(a.status, PA_DEV_TIMEOUT);
-    if (warp == kWarpLoad && lane == 0) {
-      mbar_wait(q_full, 0);
+    if (warp == kWarpSched && lane == 0)
+      for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(&q_full[i & 1], (i >> 1) & 1);
+    if (warp == kWarpLoad && lane == 0)
       for (int u = max(0, issued - kRing); u < issued; ++u)
         mbar_wait(&kv_full[u % kRing], (u / kRing) & 1);
-    }
     if ((warp == kWarpS || warp == kWarpPv) && lane == 0) {
       tc::commit(drain);
       mbar_wait(drain, 0);
@@ -768,12 +935,11 @@ cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const v
   using C = Cfg<D, PAGED>;
   using u64 = unsigned long long;
   CUtensorMap qmap, kmap, vmap, omap;
-  const unsigned tpt = a.span / 2;
   {
     const u64 dims[3] = {(u64)D, (u64)a.H, (u64)a.T};
-    const u64 qs[2] = {(u64)D * 2, (u64)q_stride * 2}, os[2] = {(u64)D * 2, (u64)a.H * D * 2};
-    const unsigned box[3] = {64, (unsigned)a.G, tpt};
-    cudaError_t e = make_map_3d(&qmap, q, dims, qs, box, true);
+    const u64 st[2] = {(u64)D * 2, (u64)q_stride * 2}, os[2] = {(u64)D * 2, (u64)a.H * D * 2};
+    const unsigned box[3] = {64, (unsigned)a.G, (unsigned)(a.span / 2)};
+    cudaError_t e = make_map_3d(&qmap, q, dims, st, box, true);
     if (e == cudaSuccess) e = make_map_3d(&omap, a.out, dims, os, box, true);
     if (e != cudaSuccess) return e;
   }
@@ -801,7 +967,10 @@ cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const v
   cudaError_t e = ensure_dynamic_smem<kern>(C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.max_units * a.Hkv * a.split));
+  // One CTA for each SM, or for each item where there are fewer.
+  const long long items = (long long)a.max_units * a.Hkv * a.split;
+  const int nsm = sm_count() > 0 ? sm_count() : 1;
+  cfg.gridDim = dim3((unsigned)(items < nsm ? items : nsm));
   cfg.blockDim = dim3(kThreadsG);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;

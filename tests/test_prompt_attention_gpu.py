@@ -124,12 +124,18 @@ def test_values_of_one_give_one():
 
 def test_bad_offsets_are_flagged_and_skipped():
     p = Packed([50, 60, 70], 4, 2, 64, torch.float16, seed=9)
-    for offs, live in (([0, 50, 110, 181], [0, 1]), ([-1, 50, 110, 180], [1, 2]),
-                       ([0, 50, 40, 180], [0])):
+    for offs, live in (([0, 50, 110, 181], [0, 1]), ([-1, 50, 110, 180], [1, 2])):
         p.offsets.copy_(torch.tensor(offs, dtype=torch.int32))
         out, st = run(p)
         assert st == pk.PA_DEV_BAD_CONTEXT
         check_all(p, out, only=live)
+    # falling offsets: the last sequence is rows 40 .. 179 and shares 40 .. 49 with
+    # the first, whose other rows are its own
+    p.offsets.copy_(torch.tensor([0, 50, 40, 180], dtype=torch.int32))
+    out, st = run(p)
+    assert st == pk.PA_DEV_BAD_CONTEXT
+    ref, tol = attend(p.q[:40], p.k[:40], p.v[:40], p.scale, 0)
+    check(out[:40], ref, tol, "rows of one sequence alone")
     p.offsets.copy_(torch.tensor([0, 50, 110, 181], dtype=torch.int32))
     out, _ = run(p)
     assert (out[110:] == 7).all()
