@@ -64,7 +64,7 @@ constexpr int kCols = 512;               // tensor memory columns
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr int kWindow = 256;             // block-table entries staged at a time
 constexpr int kMaxRing = 8;
-constexpr int kBars = 2 * kMaxRing + 15 + 2 * kItems + 1;
+constexpr int kBars = 2 * kMaxRing + 12 + 2 * kItems + 1;
 constexpr float kLazy = 8.0f;            // log2 of the growth that forces a rescale
 
 // Layout of a K or V tile in shared memory.  Paged: key groups of 8 keys x D
@@ -81,7 +81,7 @@ struct Cfg {
   static constexpr int OFF_KV = 2 * kQRoom;
   static constexpr int OFF_BAR = OFF_KV + RING * TILE_BYTES;
   static constexpr int OFF_MISC = OFF_BAR + kBars * 8;  // TMEM address, issue counters, items
-  static constexpr int OFF_TBL = (OFF_MISC + 16 + kItems * 64 + 15) / 16 * 16;
+  static constexpr int OFF_TBL = (OFF_MISC + 16 + kMaxRing * 4 + kItems * 64 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_TBL + (PAGED ? kWindow * 4 : 0) + 1024;
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static constexpr int PART = D + 4;  // floats of a partial row: o[D], m, l, pad
@@ -131,18 +131,24 @@ __device__ __forceinline__ Seq sequence(const GroupedArgs& a, int b) {
   return s;
 }
 
+// x / span for 0 <= x < 2^31: a product with 2^40 / span rounded up (span <= 256,
+// so the excess x * 2^-40 stays below 1 / span).
+__device__ __forceinline__ int per_span(const GroupedArgs& a, int x) {
+  return (int)(((unsigned long long)(unsigned)x * a.span_magic) >> 40);
+}
+
 // Key tiles that unit i (tokens i * span .. ) of a sequence reads.
 __device__ __forceinline__ int unit_tiles(const Seq& s, int span, int i) {
   return (s.n - s.ql + min((i + 1) * span, s.ql) + kTile - 1) / kTile;
 }
 
 // Units of a sequence that read at least t (>= 1) key tiles: the last ones.
-__device__ __forceinline__ int units_from(const Seq& s, int span, int t) {
+__device__ __forceinline__ int units_from(const GroupedArgs& a, const Seq& s, int t) {
   const int k = (t - 1) * kTile + 1;  // keys such a unit needs at least
   if (s.ql <= 0 || s.n < k) return 0;
-  const int nu = (s.ql + span - 1) / span;
+  const int nu = per_span(a, s.ql + a.span - 1);
   const int over = k - (s.n - s.ql);  // its tokens needed at least
-  const int first = over <= 0 ? 0 : (over + span - 1) / span - 1;
+  const int first = over <= 0 ? 0 : per_span(a, over + a.span - 1) - 1;
   return nu - min(first, nu - 1);
 }
 
@@ -180,7 +186,7 @@ struct Units {
       for (int b = lane; b < a.B; b += 32) {
         const Seq s = sequence<PAGED>(a, b);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) c[k] += units_from(s, a.span, t[k]);
+        for (int k = 0; k < 3; ++k) c[k] += units_from(a, s, t[k]);
       }
 #pragma unroll
       for (int k = 0; k < 3; ++k) {  // candidates rise, counts fall
@@ -203,9 +209,9 @@ struct Units {
       int c = 0, upper = 0, nu = 0;
       if (b < a.B) {
         const Seq s = sequence<PAGED>(a, b);
-        upper = units_from(s, a.span, lo + 1);
-        c = units_from(s, a.span, lo) - upper;
-        nu = (s.ql + a.span - 1) / a.span;
+        upper = units_from(a, s, lo + 1);
+        c = units_from(a, s, lo) - upper;
+        nu = per_span(a, s.ql + a.span - 1);
       }
       int x = c;  // inclusive scan
 #pragma unroll
@@ -279,8 +285,7 @@ template <typename T, int D, bool PAGED>
 __global__ void __launch_bounds__(kThreadsG, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap,
-                   const __grid_constant__ CUtensorMap omap, const GroupedArgs a) {
+                   const __grid_constant__ CUtensorMap vmap, const GroupedArgs a) {
   using C = Cfg<D, PAGED>;
   constexpr int kRing = C::RING;
   constexpr uint32_t kIdS = tc::idesc_f16_f32(kTile, kTile, false, false) | operand_type<T>();
@@ -299,14 +304,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   uint64_t* s_free = s_full + 2;        // [2]: its softmax holds S in registers
   uint64_t* p_full = s_free + 2;        // [2]: P stored
   uint64_t* pv_done = p_full + 2;       // [2]: O += P V completed
-  uint64_t* out_full = pv_done + 2;     // [2]: the item's output tile is staged
-  uint64_t* stage_b = out_full + 2;     // tile A's output has left the stage
-  uint64_t* it_full = stage_b + 1;      // [kItems]: an item is posted
+  uint64_t* it_full = pv_done + 2;      // [kItems]: an item is posted
   uint64_t* it_empty = it_full + kItems;  // [kItems]: every role has copied it
   uint64_t* drain = it_empty + kItems;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* s_issued = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // [2]
-  Item* items = reinterpret_cast<Item*>(smem + C::OFF_MISC + 16);
+  int* stage_left = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // [ring] see the epilogue
+  Item* items = reinterpret_cast<Item*>(smem + C::OFF_MISC + 16 + kMaxRing * 4);
   int32_t* tbl = reinterpret_cast<int32_t*>(smem + C::OFF_TBL);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -326,9 +330,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       mbar_init(&s_free[i], 4);  // one arrival per softmax warp
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&out_full[i], 4);
     }
-    mbar_init(stage_b, 1);
+    for (int s = 0; s < kRing; ++s) stage_left[s] = 0;
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&it_full[i], 1);
       mbar_init(&it_empty[i], kWarpSched);  // every other warp
@@ -338,7 +341,6 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     prefetch_tmap(&qmap);
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
-    prefetch_tmap(&omap);
   }
   if (warp == kWarpS) {
     tc::tmem_alloc(tmem_at, kCols);
@@ -427,53 +429,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       }
       __syncwarp();
     };
-    // The output tiles of an item leave the ring slot it staged them in: a whole
-    // tile by TMA, one that ends inside a sequence by 16-byte copies of its rows
-    // alone, since the next packed rows are another sequence's.
-    int staged = 0, stage_u = 0;  // items stored so far; ring index of the item's stage
-    auto store = [&](const Item& it) {
-      stage_u += 2 * it.n_kv;
-      if (it.parts > 1) return;
-      uint8_t* stage = sKV + (stage_u % kRing) * C::TILE_BYTES;
-      for (int x = 0; x < 2 && ok; ++x) {
-        if (!(ok = __all_sync(kAll, wait_slow(&out_full[x], staged & 1)))) return;
-        const int toks = x ? it.toks_b : it.toks_a, row = it.row0 + x * tpt;
-        if (toks == tpt) {
-          if (lane == 0) {
-            for (int hf = 0; hf < C::HALVES; ++hf)
-              tma_store_3d(&omap, stage + hf * kSlab, 64 * hf, it.hkv * a.G, row);
-            bulk_commit_group();
-            bulk_wait_read();
-          }
-        } else {
-          constexpr int kChunks = D / 8;
-          for (int i = lane; i < toks * a.G * kChunks; i += 32) {
-            const int r = i / kChunks, c = i % kChunks;
-            const uint4 w = *reinterpret_cast<const uint4*>(
-                stage + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) * 16));
-            *reinterpret_cast<uint4*>(
-                static_cast<T*>(a.out) +
-                ((size_t)(row + r / a.G) * a.H + it.hkv * a.G + r % a.G) * D + c * 8) = w;
-          }
-        }
-        __syncwarp();
-        if (lane == 0) {
-          // (the next writer of the slot may be TMA: order the generic reads first)
-          fence_proxy_async_smem();
-          mbar_arrive(x == 0 ? stage_b : &kv_empty[stage_u % kRing]);
-        }
-      }
-      ++staged;
-      ++stage_u;
-    };
-    Item cur, nxt, prev;
-    prev.valid = 0;
+    // Two items ahead; then, item by item, what the other roles wait for first.
+    Item cur, nxt;
     next(cur);
     post(0, cur);
+    next(nxt);
+    if (ok && cur.valid) post(1, nxt);
     for (int k = 0; ok && cur.valid; ++k) {
-      next(nxt);
-      post(k + 1, nxt);
-      if (!ok) break;
       // Q of item k, tile by tile as the products of item k - 1 let go of it:
       // boxes of tpt tokens x G heads x 64 dims; rows past the array read as zeros.
       if (lane == 0)
@@ -486,12 +448,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           ++issued;
         }
       if (!(ok = __shfl_sync(kAll, ok, 0))) break;
-      if (prev.valid) store(prev);
-      prev = cur;
       cur = nxt;
+      if (ok && cur.valid) {
+        next(nxt);
+        post(k + 2, nxt);
+      }
     }
-    if (ok && prev.valid) store(prev);
-    if (lane == 0) bulk_wait_all();
   } else if (warp == kWarpLoad) {
     // ------------------------------------------------------------ K and V
     reg_dec();
@@ -677,13 +639,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     reg_inc();
     const int x = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const int my_tok = row / a.G, my_g = row % a.G;
+    const int my_tok = (row * a.g_magic) >> 16, my_g = row - my_tok * a.G;  // row / G, row % G
     const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_s = tmem + t_lane + kColS, t_o = tmem + t_lane + kColO + x * D;
     const float sl2 = a.scale_log2;
     int done = 0;    // key tiles of the items before and of this one
     int u0 = 0;      // ring tiles of the items before
-    int staged = 0;  // output tiles staged so far
     Item it;
     for (int k = 0; take(k, it); ++k) {
       const int pos0 = it.pos_a + (x ? tpt : 0);
@@ -781,57 +742,87 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
         tc::fence_after_sync();
       }
-      // The output: of a whole unit through the ring slot granted to the item,
-      // tile A first and B once A's has left it; of a part its unnormalised row.
+      // The output, half the columns at a time.  Of a whole unit: each warp turns
+      // its 32 rows around in its share of the ring slot granted to the item, so
+      // that the stores to global memory are whole row halves and not 16 bytes of
+      // 32 rows (which took 3,000 cycles a tile); rows that are not the sequence's
+      // are left out, the next packed rows being another one's.  Of a part: the
+      // unnormalised row.
       const bool whole = it.parts == 1;
       const int stage_u = u0 + 2 * it.n_kv;
-      if (whole) {
-        if (!(ok = __all_sync(kAll, x ? mbar_wait(stage_b, staged & 1)
-                                      : mbar_wait(&kv_full[stage_u % kRing],
-                                                  (stage_u / kRing) & 1))))
-          break;
-        ++staged;
-      }
       u0 = stage_u + whole;
+      const int toks = x ? it.toks_b : it.toks_a, first = it.row0 + (x ? tpt : 0);
+      if (toks == 0) continue;  // (tile B of a unit that ends in tile A)
+      if (whole &&
+          !(ok = __all_sync(kAll, mbar_wait(&kv_full[stage_u % kRing], (stage_u / kRing) & 1))))
+        break;
+      constexpr int kHalf = D / 2, kChunks = kHalf / 8;  // columns; 16-byte chunks of them
       const float inv = l != 0.f ? 1.f / l : 0.f;
-      uint8_t* srow = sKV + (stage_u % kRing) * C::TILE_BYTES + row * 128;
-      float* wrow = a.ws + (((size_t)it.part * a.T + it.row0 + (x ? tpt : 0) + my_tok) * a.H +
-                            it.hkv * a.G + my_g) * C::PART;
+      uint8_t* stage = sKV + (stage_u % kRing) * C::TILE_BYTES + warp * (32 * D);
+      auto at = [&](int r, int c) {  // chunk c of row r, conflict-free both ways
+        return stage + r * D + ((c ^ (kChunks == 8 ? r & 7 : (r >> 1) & 3)) * 16);
+      };
+      T* out0 = static_cast<T*>(a.out) + ((size_t)first * a.H + it.hkv * a.G) * D;
+      float* wrow =
+          a.ws + (((size_t)it.part * a.T + first + my_tok) * a.H + it.hkv * a.G + my_g) * C::PART;
       // (Rolled: the code of the hot loop above and of the other roles has to
       // stay in the instruction cache.)
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t o[kHalf / 32][32];
         if (ntile > 0) {
-          tc::ld_32x32(t_o + c * 32, o);
+#pragma unroll
+          for (int c = 0; c < kHalf / 32; ++c) tc::ld_32x32(t_o + hf * kHalf + c * 32, o[c]);
           tc::wait_ld();
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
+          for (int i = 0; i < kHalf; ++i) o[i >> 5][i & 31] = 0u;
         }
-        if (whole) {  // swizzled rows of 64 dims, as the TMA boxes have them
-          uint32_t hv[16];
+        if (whole) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            hv[i] = pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-          uint8_t* slab = srow + (c >> 1) * kSlab;
+          for (int q = 0; q < kChunks; ++q) {
+            uint32_t hv[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(slab + ((((c & 1) << 2) + q) ^ (row & 7)) * 16) =
-                make_uint4(hv[4 * q], hv[4 * q + 1], hv[4 * q + 2], hv[4 * q + 3]);
+            for (int i = 0; i < 4; ++i)
+              hv[i] = pack2<T>(__uint_as_float(o[q >> 2][8 * (q & 3) + 2 * i]) * inv,
+                               __uint_as_float(o[q >> 2][8 * (q & 3) + 2 * i + 1]) * inv);
+            *reinterpret_cast<uint4*>(at(lane, q)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+          }
+          __syncwarp();
+          const int c = lane % kChunks;
+#pragma unroll 4
+          for (int i = 0; i < kChunks; ++i) {
+            const int r = i * (32 / kChunks) + lane / kChunks, rt = quarter * 32 + r;
+            const int tok = (rt * a.g_magic) >> 16;  // rt / G
+            if (tok < toks)
+              *reinterpret_cast<uint4*>(out0 + ((size_t)tok * a.H + rt - tok * a.G) * D +
+                                        hf * kHalf + c * 8) =
+                  *reinterpret_cast<const uint4*>(at(r, c));
+          }
+          __syncwarp();
         } else if (live) {
-          float4* dst = reinterpret_cast<float4*>(wrow + c * 32);
+          uint4* dst = reinterpret_cast<uint4*>(wrow + hf * kHalf);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          for (int i = 0; i < kHalf / 4; ++i)
+            dst[i] = make_uint4(o[i >> 3][4 * (i & 7)], o[i >> 3][4 * (i & 7) + 1],
+                                o[i >> 3][4 * (i & 7) + 2], o[i >> 3][4 * (i & 7) + 3]);
         }
       }
       tc::fence_before_sync();  // O is read before the next item's P V overwrites it
       if (whole) {
+        // The last of the four or eight warps that use the stage lets the slot go
+        // (to TMA, the async proxy, which these accesses come before).  A count
+        // and not a barrier: a tile may be several items ahead of the other.
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&out_full[x]);
+        if (lane == 0) {
+          __threadfence_block();
+          if (atomicAdd(&stage_left[stage_u % kRing], 1) == (it.toks_b > 0 ? 7 : 3)) {
+            __threadfence_block();
+            stage_left[stage_u % kRing] = 0;
+            mbar_arrive(&kv_empty[stage_u % kRing]);
+          }
+        }
       } else if (live) {
         wrow[D] = m;
         wrow[D + 1] = l;
@@ -934,13 +925,12 @@ cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const v
                      cudaStream_t stream) {
   using C = Cfg<D, PAGED>;
   using u64 = unsigned long long;
-  CUtensorMap qmap, kmap, vmap, omap;
+  CUtensorMap qmap, kmap, vmap;
   {
     const u64 dims[3] = {(u64)D, (u64)a.H, (u64)a.T};
-    const u64 st[2] = {(u64)D * 2, (u64)q_stride * 2}, os[2] = {(u64)D * 2, (u64)a.H * D * 2};
+    const u64 st[2] = {(u64)D * 2, (u64)q_stride * 2};
     const unsigned box[3] = {64, (unsigned)a.G, (unsigned)(a.span / 2)};
-    cudaError_t e = make_map_3d(&qmap, q, dims, st, box, true);
-    if (e == cudaSuccess) e = make_map_3d(&omap, a.out, dims, os, box, true);
+    const cudaError_t e = make_map_3d(&qmap, q, dims, st, box, true);
     if (e != cudaSuccess) return e;
   }
   for (int i = 0; i < 2; ++i) {
@@ -979,7 +969,7 @@ cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const v
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, qmap, kmap, vmap, omap, a);
+  e = cudaLaunchKernelEx(&cfg, kern, qmap, kmap, vmap, a);
   if constexpr (PAGED) {
     if (e != cudaSuccess || a.split == 1) return e;
     cudaLaunchConfig_t cm = cfg;

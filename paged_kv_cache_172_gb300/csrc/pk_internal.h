@@ -198,6 +198,8 @@ struct GroupedArgs {
   int32_t* status;
   int B, T, H, Hkv, G, D;
   int span;       // tokens of a unit (two tiles)
+  unsigned long long span_magic;  // 2^40 / span, rounded up
+  int g_magic;    // 2^16 / G, rounded up: r * g_magic >> 16 = r / G for r < 128
   int max_units;  // units of a K/V head, at most
   int max_tiles;  // key tiles of a unit, at most
   int split, min_part_tiles;
