@@ -84,7 +84,6 @@ struct Cfg {
   static constexpr int OFF_TBL = (OFF_MISC + 16 + kMaxRing * 4 + kItems * 64 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_TBL + (PAGED ? kWindow * 4 : 0) + 1024;
   static_assert(SMEM <= 232448, "shared memory per CTA");
-  static constexpr int PART = D + 4;  // floats of a partial row: o[D], m, l, pad
 };
 
 template <typename T>
@@ -266,6 +265,17 @@ __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ int ring_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int ring_v(int t, int n_kv) {
   return t + 1 < n_kv ? 2 * t + 2 : 2 * t + 1;
+}
+
+// Parts in the workspace.  Row r of a K/V head's packed rows (token r / G, head r
+// mod G; a tile's rows are consecutive) has its D outputs as D / 4 groups of four,
+// group c of all rows together: [part][Hkv][D / 4][T * G] float4, so that a warp's
+// 32 rows store and load whole lines.  Behind them (max, normaliser) as
+// [part][Hkv][T * G] float2.
+__device__ __forceinline__ float2* part_ml(const GroupedArgs& a, int D, int part, int hkv) {
+  const size_t plane = (size_t)a.T * a.G;
+  return reinterpret_cast<float2*>(a.ws + (size_t)a.split * a.Hkv * plane * D) +
+         (size_t)(part * a.Hkv + hkv) * plane;
 }
 
 // What the scheduler posts of a work item: a unit, or one of its key ranges.
@@ -639,7 +649,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     reg_inc();
     const int x = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const int my_tok = (row * a.g_magic) >> 16, my_g = row - my_tok * a.G;  // row / G, row % G
+    const int my_tok = (row * a.g_magic) >> 16;  // row / G
     const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_s = tmem + t_lane + kColS, t_o = tmem + t_lane + kColO + x * D;
     const float sl2 = a.scale_log2;
@@ -763,8 +773,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         return stage + r * D + ((c ^ (kChunks == 8 ? r & 7 : (r >> 1) & 3)) * 16);
       };
       T* out0 = static_cast<T*>(a.out) + ((size_t)first * a.H + it.hkv * a.G) * D;
-      float* wrow =
-          a.ws + (((size_t)it.part * a.T + first + my_tok) * a.H + it.hkv * a.G + my_g) * C::PART;
+      const size_t prow = (size_t)first * a.G + row, plane = (size_t)a.T * a.G;  // see part_ml
+      float4* part_o =
+          reinterpret_cast<float4*>(a.ws) + (size_t)(it.part * a.Hkv + it.hkv) * (D / 4) * plane;
       // (Rolled: the code of the hot loop above and of the other roles has to
       // stay in the instruction cache.)
 #pragma unroll 1
@@ -801,11 +812,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           }
           __syncwarp();
         } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(wrow + hf * kHalf);
+          float4* dst = part_o + hf * (kHalf / 4) * plane + prow;
 #pragma unroll
-          for (int i = 0; i < kHalf / 4; ++i)
-            dst[i] = make_uint4(o[i >> 3][4 * (i & 7)], o[i >> 3][4 * (i & 7) + 1],
-                                o[i >> 3][4 * (i & 7) + 2], o[i >> 3][4 * (i & 7) + 3]);
+          for (int i = 0; i < kHalf / 4; ++i, dst += plane)
+            *dst = make_float4(__uint_as_float(o[i >> 3][4 * (i & 7)]),
+                               __uint_as_float(o[i >> 3][4 * (i & 7) + 1]),
+                               __uint_as_float(o[i >> 3][4 * (i & 7) + 2]),
+                               __uint_as_float(o[i >> 3][4 * (i & 7) + 3]));
         }
       }
       tc::fence_before_sync();  // O is read before the next item's P V overwrites it
@@ -824,8 +837,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           }
         }
       } else if (live) {
-        wrow[D] = m;
-        wrow[D + 1] = l;
+        part_ml(a, D, it.part, it.hkv)[prow] = make_float2(m, l);
       }
     }
   }
@@ -852,71 +864,109 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   }
 }
 
-// Merges the parts of a split unit's rows by log-sum-exp (m, l in the log2
-// domain): one warp per (token, head), lane l owns D / 32 dims.
+// Merges the parts of split units by log-sum-exp (m, l in the log2 domain).  A
+// block takes 32 consecutive rows of a K/V head, a lane each; its warps first
+// take the parts' (m, l) in turn and leave every part's weight in shared memory,
+// then D / 8 columns each, four parts' loads in flight.  (One thread to a row
+// with all its parts one after the other: 64 us for 32 parts, all latency.)
+constexpr int kMergeWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(256) grouped_merge_kernel(const GroupedArgs a) {
-  constexpr int EPL = D / 32, kPart = D + 4;
+__global__ void __launch_bounds__(32 * kMergeWarps) grouped_merge_kernel(const GroupedArgs a) {
+  constexpr int kC = D / 4 / kMergeWarps;  // groups of four columns of a warp
+  __shared__ float s_w[kGroupedMaxSplit][32];     // m, then the weight of a part
+  __shared__ float s_m[kMergeWarps][32], s_l[kMergeWarps][32];
+  __shared__ uint2 s_out[32][D / 4 + 1];
   pdl_wait();
   pdl_launch_dependents();
-  const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w >= (long long)a.T * a.H) return;
-  const int t = (int)(w / a.H), h = (int)(w % a.H);
-  // The sequence that holds row t: offsets rise (else the row is nobody's).
-  int lo = 0, hi = a.B;
-  if (a.B <= 0 || t < a.q_offsets[0] || t >= a.q_offsets[a.B]) return;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.q_offsets[mid] <= t)
-      lo = mid;
-    else
-      hi = mid;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hkv = blockIdx.y;
+  const size_t plane = (size_t)a.T * a.G, row0 = (size_t)blockIdx.x * 32, r = row0 + lane;
+  int parts = 0;  // of this lane's row; 0: nothing to merge
+  if (r < plane) {
+    const int t = (int)(r / a.G);
+    if (t >= a.q_offsets[0] && t < a.q_offsets[a.B]) {
+      int lo = 0, hi = a.B;  // the sequence that holds row t: offsets rise
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.q_offsets[mid] <= t)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const Seq s = sequence<true>(a, lo);
+      if (!s.bad && t >= s.start && t < s.start + s.ql)
+        parts = unit_parts(unit_tiles(s, a.span, per_span(a, t - s.start)), a.split,
+                           a.min_part_tiles);
+      if (parts == 1) parts = 0;  // (written by its only part)
+    }
   }
-  const Seq s = sequence<true>(a, lo);
-  if (s.bad || t < s.start || t >= s.start + s.ql) return;
-  const int parts =
-      unit_parts(unit_tiles(s, a.span, (t - s.start) / a.span), a.split, a.min_part_tiles);
-  if (parts <= 1) return;  // written by its only part
-  constexpr int kMax = 8;
-  float ms[kMax], ls[kMax], ov[kMax][EPL];
+  const int most = __reduce_max_sync(kAll, parts);
+  if (most == 0) return;  // (alike in all warps)
+  float M = -INFINITY;
+  float m[kGroupedMaxSplit / kMergeWarps], l[kGroupedMaxSplit / kMergeWarps];
 #pragma unroll
-  for (int p = 0; p < kMax; ++p) {
-    ms[p] = -INFINITY;
-    ls[p] = 0.f;
+  for (int i = 0; i < kGroupedMaxSplit / kMergeWarps; ++i) {
+    const int p = warp + i * kMergeWarps;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
     if (p < parts) {
-      const float* row = a.ws + (((size_t)p * a.T + t) * a.H + h) * kPart;
-      ms[p] = row[D];
-      ls[p] = row[D + 1];
-      if constexpr (EPL == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(row + lane * 4);
-        ov[p][0] = f.x, ov[p][1] = f.y, ov[p][2] = f.z, ov[p][3] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(row + lane * 2);
-        ov[p][0] = f.x, ov[p][1] = f.y;
+      const float2 ml = part_ml(a, D, p, hkv)[r];
+      m[i] = ml.x;
+      l[i] = ml.y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kGroupedMaxSplit / kMergeWarps; ++i)
+    if (l[i] != 0.f) M = fmaxf(M, m[i]);
+  s_m[warp][lane] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, s_m[w][lane]);
+  float L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kGroupedMaxSplit / kMergeWarps; ++i) {
+    // an empty part's row is no number: weight 0 stands for leaving it out
+    const float w = l[i] != 0.f ? ex2_approx(m[i] - M) : 0.f;
+    s_w[warp + i * kMergeWarps][lane] = w;
+    if (l[i] != 0.f) L += w * l[i];
+  }
+  s_l[warp][lane] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) L += s_l[w][lane];
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  float4 acc[kC];
+#pragma unroll
+  for (int c = 0; c < kC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* src =
+      reinterpret_cast<const float4*>(a.ws) + ((size_t)hkv * (D / 4) + warp * kC) * plane + r;
+  const size_t step = (size_t)a.Hkv * (D / 4) * plane;  // to the next part
+#pragma unroll 4
+  for (int p = 0; p < most; ++p) {
+    const float w = s_w[p][lane];
+    if (p < parts && w != 0.f) {
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        const float4 v = src[p * step + c * plane];
+        acc[c].x += w * v.x;
+        acc[c].y += w * v.y;
+        acc[c].z += w * v.z;
+        acc[c].w += w * v.w;
       }
     }
   }
-  float M = -INFINITY;
 #pragma unroll
-  for (int p = 0; p < kMax; ++p)
-    if (ls[p] != 0.f) M = fmaxf(M, ms[p]);
-  float L = 0.f, o[EPL];
-#pragma unroll
-  for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-#pragma unroll
-  for (int p = 0; p < kMax; ++p)
-    if (ls[p] != 0.f) {
-      const float wgt = ex2_approx(ms[p] - M);
-      L += ls[p] * wgt;
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) o[e] += wgt * ov[p][e];
-    }
-  const float inv = L != 0.f ? 1.f / L : 0.f;
-  T* dst = static_cast<T*>(a.out) + ((size_t)t * a.H + h) * D + lane * EPL;
-#pragma unroll
-  for (int e = 0; e < EPL; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack2<T>(o[e] * inv, o[e + 1] * inv);
+  for (int c = 0; c < kC; ++c)
+    s_out[lane][warp * kC + c] = make_uint2(pack2<T>(acc[c].x * inv, acc[c].y * inv),
+                                            pack2<T>(acc[c].z * inv, acc[c].w * inv));
+  __syncthreads();
+  // Whole rows, a warp one at a time (lane q's count says whether row q is merged).
+  for (int q = warp; q < 32; q += kMergeWarps) {
+    if (__shfl_sync(kAll, parts, q) == 0) continue;
+    const size_t rr = row0 + q, t = rr / a.G;
+    T* dst = static_cast<T*>(a.out) + (t * a.H + hkv * a.G + (rr - t * a.G)) * D;
+    for (int c = lane; c < D / 4; c += 32) reinterpret_cast<uint2*>(dst)[c] = s_out[q][c];
+  }
 }
 
 template <typename T, int D, bool PAGED>
@@ -973,8 +1023,8 @@ cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const v
   if constexpr (PAGED) {
     if (e != cudaSuccess || a.split == 1) return e;
     cudaLaunchConfig_t cm = cfg;
-    cm.gridDim = dim3((unsigned)(((long long)a.T * a.H * 32 + 255) / 256));
-    cm.blockDim = dim3(256);
+    cm.gridDim = dim3((unsigned)(((long long)a.T * a.G + 31) / 32), a.Hkv);
+    cm.blockDim = dim3(32 * kMergeWarps);
     cm.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cm, grouped_merge_kernel<T, D>, a);
   }
@@ -989,18 +1039,32 @@ int grouped_split(int B, int T, int H, int Hkv, int max_context) {
   const int span = grouped_span(H / Hkv);
   const int nsm = sm_count();
   if (span == 0 || nsm <= 0) return 1;
-  const long long ctas = ((long long)T / span + B) * Hkv;
-  const long long tiles = ((long long)max_context + kTile - 1) / kTile;
-  // Fewer CTAs than four for each SM: more key ranges even out sequences of
-  // different lengths; none shorter than kMinPartTiles.
-  long long s = 4LL * nsm / (ctas > 0 ? ctas : 1);
-  if (s > tiles / kGroupedMinPartTiles) s = tiles / kGroupedMinPartTiles;
-  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
+  // Lengths are on the device: every sequence is taken to run, with half a unit
+  // lost at its end and contexts of 0.6 of the longest on average.  Time in key
+  // tiles, with s parts to a unit: the longest part, or all parts spread over the
+  // SMs; a part costs kPartCost tiles besides its own.
+  constexpr double kMean = 0.6, kPartCost = 4.0;
+  double units = (double)T / span + 0.5 * B;
+  if (units < B) units = B;
+  units *= Hkv;
+  const double tiles = ((double)max_context + kTile - 1) / kTile;
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= kGroupedMaxSplit && (s == 1 || s * kGroupedMinPartTiles <= tiles); ++s) {
+    const double longest = tiles / s + (s > 1 ? kPartCost : 0.0);
+    const double spread = units * s * (kMean * tiles / s + (s > 1 ? kPartCost : 0.0)) / nsm;
+    const double t = longest > spread ? longest : spread;
+    if (s == 1 || t < least) {
+      best = s;
+      least = t;
+    }
+  }
+  return best;
 }
 
 size_t grouped_workspace_bytes(int B, int T, int H, int Hkv, int D, int max_context) {
   const int s = grouped_split(B, T, H, Hkv, max_context);
-  return s <= 1 ? 0 : (size_t)s * T * H * (D + 4) * sizeof(float);
+  return s <= 1 ? 0 : (size_t)s * T * H * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_grouped(const GroupedArgs& a, const void* q, const void* k, const void* v,

@@ -194,7 +194,7 @@ struct GroupedArgs {
   const int32_t* context_lens;  // [B], paged
   const int32_t* block_tables;  // [B, max_blocks], paged
   void* out;                    // [T, H, D]
-  float* ws;                    // [split, T, H, D + 4] parts of split units
+  float* ws;                    // parts of split units, split * T * H * (D + 2) floats
   int32_t* status;
   int B, T, H, Hkv, G, D;
   int span;       // tokens of a unit (two tiles)
@@ -208,6 +208,7 @@ struct GroupedArgs {
   bool bf16;
 };
 constexpr int kGroupedMinPartTiles = 4;  // key tiles of a part, at least
+constexpr int kGroupedMaxSplit = 32;     // parts of a unit, at most
 int grouped_span(int G);  // tokens of a work unit; 0: unsupported
 int grouped_split(int B, int T, int H, int Hkv, int max_context);
 size_t grouped_workspace_bytes(int B, int T, int H, int Hkv, int D, int max_context);
