@@ -264,10 +264,11 @@ pa_status pa_chunk_attention(const void* q, const void* k_cache, const void* v_c
   return packed_impl(a, q, k_cache, v_cache, q_stride, 0, 0, scale, max_context_len, stream);
 }
 
-static int decode_partition(int B, int H, int Hkv, int max_context, int partition_tokens) {
+static int decode_partition(int B, int H, int Hkv, int D, int max_context,
+                            int partition_tokens) {
   if (max_context < 1) max_context = 1;  // every row is empty: one partition
   return partition_tokens > 0 ? partition_tokens
-                              : pk::grouped_decode_partition(B, H, Hkv, max_context);
+                              : pk::grouped_decode_partition(B, H, Hkv, D, max_context);
 }
 
 size_t pa_decode_grouped_workspace_size(int B, int H, int Hkv, int D, int block_size,
@@ -275,7 +276,7 @@ size_t pa_decode_grouped_workspace_size(int B, int H, int Hkv, int D, int block_
   if (B <= 0 || !heads_ok(H, Hkv) || (D != 64 && D != 128) || !paged_block(block_size) ||
       max_context_len <= 0 || partition_tokens < 0)
     return 0;
-  const int pt = decode_partition(B, H, Hkv, max_context_len, partition_tokens);
+  const int pt = decode_partition(B, H, Hkv, D, max_context_len, partition_tokens);
   const long long parts = ((long long)max_context_len + pt - 1) / pt;
   return parts <= 1 ? 0 : (size_t)B * H * parts * (D + 2) * sizeof(float);
 }
@@ -298,7 +299,7 @@ pa_status pa_decode_grouped(const void* q, const void* k_cache, const void* v_ca
   if (st != PA_OK) return st;
   if (!q || !out || !aligned16(q) || !aligned16(out)) return PA_ERR_INVALID;
   pk::GroupedDecodeArgs a = {};
-  a.part_tokens = decode_partition(B, H, Hkv, max_context_len, partition_tokens);
+  a.part_tokens = decode_partition(B, H, Hkv, D, max_context_len, partition_tokens);
   const long long parts =
       ((long long)(max_context_len > 0 ? max_context_len : 1) + a.part_tokens - 1) /
       a.part_tokens;

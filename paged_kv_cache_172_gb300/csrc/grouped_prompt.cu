@@ -15,24 +15,27 @@
 // each head.  A CTA takes two such tiles A and B, one after the other in the
 // sequence, of one K/V head, and walks the visible keys in tiles of 128:
 //   warps 0-3, 4-7  softmax of tile A, B: one row per thread (TMEM lane = row);
-//   warp 8          producer: Q, then K_0, K_1, V_0, K_2, V_1, ... into a ring;
+//   warp 8          requests K_0, K_1, V_0, K_2, V_1, ... into a ring;
 //   warp 9          issues S = Q K^T (one thread), owns the tensor memory;
-//   warp 10         issues O += P V (one thread).
+//   warp 10         issues O += P V (one thread);
+//   warp 11         schedules, and requests Q.
 // Tensor memory: S [0, 128) shared by both tiles, P_A [128, 192), P_B
 // [192, 256) as 16-bit pairs, O_A, O_B from column 256 (D columns each).  Q
 // stays in shared memory (A operand of the S products) and P in tensor memory
 // (A operand of the P V products): the placement that asks least of the shared
 // memory's bandwidth, as in the fp16 chunk kernel of this library.
 //
-// Scheduling.  Lengths live on the device, so the grid is an upper bound
-// (T / (2 * tokens per tile) + B units for each K/V head) and each CTA finds
-// its unit itself: units are ranked by the number of key tiles they read,
-// longest first, so that the last CTAs to start are the short ones.  The rank
-// needs no sort: how many units of a sequence read at least t key tiles has a
-// closed form, and a search over t (eleven candidates a round, one per warp)
-// with sums over the sequences finds the unit.  Few units with many keys: each
-// is cut into up to `split` key ranges whose (o, m, l) rows go to the workspace
-// and are merged by log-sum-exp.
+// Scheduling.  One persistent CTA for each SM.  Lengths live on the device, so
+// the host knows only a bound on the units of two tiles (T / tokens of a unit + B
+// for each K/V head); warp 11 ranks them by the number of key tiles they read,
+// longest first, deals them to the CTAs in rounds and posts each CTA's next two in
+// shared memory.  The rank needs no sort: how many units of a sequence read at
+// least t key tiles has a closed form, and a binary search over t with sums over
+// the sequences finds the unit.  K/V loads run on into the next item, Q is
+// requested tile by tile as the S products of the item before let go of it, and
+// the output leaves through a slot of the K/V ring.  Few units with many keys:
+// each is cut into up to `split` key ranges whose (o, m, l) rows go to the
+// workspace and are merged by log-sum-exp.
 //
 // Rounding: scores, maxima, sums and O are fp32; P is rounded to the 16-bit
 // type of the inputs (the tensor core's operand; its values are at most 2^8
@@ -156,19 +159,15 @@ __device__ __forceinline__ int unit_parts(int tiles, int split, int min_tiles) {
   return max(1, min(split, tiles / min_tiles));
 }
 
-__device__ __forceinline__ int warp_sum(int x) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
-  return x;
-}
-
 // Walks the units by key tiles, longest first (one warp, all lanes alike).
 template <bool PAGED>
 struct Units {
   const GroupedArgs& a;
   int bound, above;  // no unit asked for later reads `bound` key tiles or more; how many do
+  int tiles, base0, before;  // where the last scan ended: sequences from base0, units before
 
-  __device__ Units(const GroupedArgs& args) : a(args), bound(args.max_tiles + 1), above(0) {}
+  __device__ Units(const GroupedArgs& args)
+      : a(args), bound(args.max_tiles + 1), above(0), tiles(0), base0(0), before(0) {}
 
   // The unit of a rank: (b, i), or false behind the last unit.  Ranks rise from
   // call to call.
@@ -176,34 +175,33 @@ struct Units {
     const int lane = threadIdx.x & 31;
     // units with >= lo tiles: more than rank (lo = 0: taken as such); >= hi: at most rank
     int lo = 0, hi = bound, over = above;
-    while (hi - lo > 1) {  // three candidates a pass over the sequences
-      const int gap = hi - lo;
-      int t[3], c[3] = {0, 0, 0};
-#pragma unroll
-      for (int k = 0; k < 3; ++k) t[k] = lo + 1 + (int)((long long)(k + 1) * (gap - 2) / 4);
+    // (A short loop: the first search of a launch runs from a cold instruction
+    // cache, where a longer body cost more than the passes it saved.)
 #pragma unroll 1
-      for (int b = lane; b < a.B; b += 32) {
-        const Seq s = sequence<PAGED>(a, b);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) c[k] += units_from(a, s, t[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {  // candidates rise, counts fall
-        c[k] = warp_sum(c[k]);
-        if (c[k] > rank)
-          lo = t[k];
-        else if (t[k] < hi) {
-          hi = t[k];
-          over = c[k];
-        }
+    while (hi - lo > 1) {
+      const int t = (lo + hi) >> 1;
+      int c = 0;
+#pragma unroll 1
+      for (int b = lane; b < a.B; b += 32) c += units_from(a, sequence<PAGED>(a, b), t);
+      c = __reduce_add_sync(kAll, c);
+      if (c > rank) {
+        lo = t;
+      } else {
+        hi = t;
+        over = c;
       }
     }
     bound = hi;
     above = over;
     if (lo == 0) return false;
     // The units that read exactly lo tiles, sequences in order: the (rank - over)-th.
-    int left = rank - over;
-    for (int base = 0; base < a.B; base += 32) {
+    if (lo != tiles) {
+      tiles = lo;
+      base0 = before = 0;
+    }
+    int left = rank - over - before;
+#pragma unroll 1
+    for (int base = base0; base < a.B; base += 32) {
       const int b = base + lane;
       int c = 0, upper = 0, nu = 0;
       if (b < a.B) {
@@ -221,6 +219,8 @@ struct Units {
       const unsigned hit = __ballot_sync(kAll, x > left);
       if (hit != 0) {
         const int src = __ffs(hit) - 1;
+        base0 = base;
+        before = rank - over - left;
         b_out = base + src;
         i_out = __shfl_sync(kAll, nu - 1 - upper - (left - (x - c)), src);
         return true;

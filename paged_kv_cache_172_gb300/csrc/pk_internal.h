@@ -230,7 +230,7 @@ struct GroupedDecodeArgs {
   float scale_log2;
   bool bf16;
 };
-int grouped_decode_partition(int B, int H, int Hkv, int max_context);
+int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context);
 cudaError_t launch_grouped_decode(const GroupedDecodeArgs& a, const void* k_cache,
                                   const void* v_cache, cudaStream_t stream);
 
