@@ -77,14 +77,16 @@ pa_status pa_rope_table(const double* inv_freq, const int32_t* axes, int n, uint
     // inv_freq / 2 pi as an unevaluated sum: 1 / 2 pi in two doubles, and the
     // first product's rounding error recovered by a fused multiply-add.
     constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
-    double hi = inv_freq[i] * kHi;
-    const double lo = fma(inv_freq[i], kHi, -hi) + inv_freq[i] * kLo;
-    hi -= floor(hi);  // exact; whole turns drop out
+    const double f0 = fabs(inv_freq[i]);
+    double hi = f0 * kHi;
+    const double lo = fma(f0, kHi, -hi) + f0 * kLo;
+    hi -= floor(hi);  // exact, as hi >= 0; whole turns drop out
     // 2^62 steps (the two low bits stay free), modulo one turn; |lo| is far
     // below one turn for any inv_freq below 2^50
-    if (fabs(inv_freq[i]) >= 1125899906842624.0) return PA_ERR_INVALID;
+    if (f0 >= 1125899906842624.0) return PA_ERR_INVALID;
     constexpr double kSteps = 4611686018427387904.0;
-    const uint64_t f = ((uint64_t)(hi * kSteps) + (uint64_t)llrint(lo * kSteps)) << 2;
+    uint64_t f = ((uint64_t)(hi * kSteps) + (uint64_t)llrint(lo * kSteps)) << 2;
+    if (inv_freq[i] < 0.0) f = 0 - f;  // the other way round (its low bits stay zero)
     table[i] = f | (uint64_t)(axes ? axes[i] : 0);
   }
   return PA_OK;

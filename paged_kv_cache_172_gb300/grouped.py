@@ -15,8 +15,10 @@ import torch
 from ._lib import _check, _ptr, lib
 
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1}  # pa_dtype
-# The current stream's handle without a torch.cuda.Stream object around it.
+# The current stream's handle without a torch.cuda.Stream object around it, and
+# the current device (tensors on one exist: CUDA is initialised).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 class StepPlan(NamedTuple):
@@ -45,7 +47,7 @@ def _run(fn, name, dev, stream, *args):
         handle = stream.cuda_stream
     else:
         handle = _raw_stream(dev)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -77,13 +79,14 @@ def _status_ok(status, dev):
     return status is None or (status.dtype is torch.int32 and status.get_device() == dev)
 
 
-def _shaped(name, *tensors):
-    """The tensors' dimensions, before anything is read off them: (name, tensor, dims)."""
+def _misshaped(name, *tensors):
+    """The error behind sizes that could not be read off: (name, tensor, dims)."""
     for what, t, dims in tensors:
         if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: {what} must be a torch.Tensor")
+            return TypeError(f"{name}: {what} must be a torch.Tensor")
         if t.dim() != dims:
-            raise ValueError(f"{name}: {what} must have {dims} dims, got {list(t.shape)}")
+            return ValueError(f"{name}: {what} must have {dims} dims, got {list(t.shape)}")
+    return ValueError(f"{name}: bad shapes")
 
 
 def _complain(name, dev, dense, rows=(), status=None):
@@ -132,10 +135,13 @@ def pa_step_plan(cached_lens, new_lens, block_tables, free_blocks, free_state, b
     the new free_state (out's may be the one passed in).  A step that does not fit
     the ring (PA_DEV_NO_BLOCKS) or max_tokens (PA_DEV_BAD_CONTEXT) plans nothing."""
     i32, i64 = torch.int32, torch.int64
-    _shaped("pa_step_plan", ("cached_lens", cached_lens, 1), ("block_tables", block_tables, 2),
-            ("free_blocks", free_blocks, 1))
-    B, M, NB, T = (cached_lens.shape[0], block_tables.shape[1], free_blocks.shape[0],
-                   int(max_tokens))
+    try:
+        (B,), (_, M), (NB,), T = (cached_lens.shape, block_tables.shape, free_blocks.shape,
+                                  int(max_tokens))
+    except (AttributeError, ValueError):
+        raise _misshaped("pa_step_plan", ("cached_lens", cached_lens, 1),
+                         ("block_tables", block_tables, 2),
+                         ("free_blocks", free_blocks, 1)) from None
     dev = cached_lens.get_device()
     if out is None:
         out = StepPlan.empty(B, T, cached_lens.device)
@@ -185,16 +191,20 @@ def pa_rope_cache_write(q, k, v, positions, table, slot_mapping, k_cache=None, v
     (q_out, k_out); q_out is allocated when not given and may be q; k_out, given
     or with no cache allocated, receives the rotated keys and may be k."""
     name = "pa_rope_cache_write"
-    _shaped(name, ("q", q, 3), ("k", k, 3), ("table", table, 1))
+    try:
+        (T, H, D), (_, Hkv, _), (n,) = q.shape, k.shape, table.shape
+    except (AttributeError, ValueError):
+        raise _misshaped(name, ("q", q, 3), ("k", k, 3), ("table", table, 1)) from None
     code, dt, dev = _float16(name, q), q.dtype, q.get_device()
-    (T, H, D), Hkv, n = q.shape, k.shape[1], table.shape[0]
     axes = 1 if positions.dim() == 1 else positions.shape[0]
     pos_shape = (T,) if positions.dim() == 1 else (axes, T)
     kv, caches = (T, Hkv, D), ()
     NB = bs = 0
     if k_cache is not None or v_cache is not None:
-        _shaped(name, ("k_cache", k_cache, 4), ("v", v, 3))
-        NB, bs = k_cache.shape[:2]
+        try:
+            (NB, bs, _, _), (_, _, _) = k_cache.shape, v.shape
+        except (AttributeError, ValueError):
+            raise _misshaped(name, ("k_cache", k_cache, 4), ("v", v, 3)) from None
         caches = (NB, bs, Hkv, D)
     else:
         v = slot_mapping = None
@@ -237,9 +247,12 @@ def pa_prompt_attention(q, k, v, q_offsets, scale, out=None, status=None, stream
     [T,H,D]; rows outside the sequences are left as they were (undefined when
     ``out`` is allocated here)."""
     name = "pa_prompt_attention"
-    _shaped(name, ("q", q, 3), ("k", k, 3), ("v", v, 3), ("q_offsets", q_offsets, 1))
+    try:
+        (T, H, D), (_, Hkv, _), (_, _, _), (n,) = q.shape, k.shape, v.shape, q_offsets.shape
+    except (AttributeError, ValueError):
+        raise _misshaped(name, ("q", q, 3), ("k", k, 3), ("v", v, 3),
+                         ("q_offsets", q_offsets, 1)) from None
     code, dt, dev = _float16(name, q), q.dtype, q.get_device()
-    (T, H, D), Hkv, n = q.shape, k.shape[1], q_offsets.shape[0]
     if out is None:
         out = torch.empty((T, H, D), dtype=dt, device=q.device)
     if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _rows(k, dt, (T, Hkv, D), dev)
@@ -268,7 +281,7 @@ def _workspace(name, workspace, nbytes, dev):
 
 def _sized(fn, dev, *args):
     """A workspace size, which depends on the device, with that device current."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)
@@ -290,11 +303,14 @@ def pa_chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offset
     allocated when not given; split=False passes none.  Returns ``out``
     [T,H,D]; rows outside the sequences are left as they were."""
     name = "pa_chunk_attention"
-    _shaped(name, ("q", q, 3), ("k_cache", k_cache, 4), ("block_tables", block_tables, 2),
-            ("q_offsets", q_offsets, 1))
+    try:
+        (T, H, D), (NB, bs, Hkv, _), (_, M), (n,) = (q.shape, k_cache.shape, block_tables.shape,
+                                                     q_offsets.shape)
+    except (AttributeError, ValueError):
+        raise _misshaped(name, ("q", q, 3), ("k_cache", k_cache, 4),
+                         ("block_tables", block_tables, 2), ("q_offsets", q_offsets, 1)) from None
     code, dt, dev = _float16(name, q), q.dtype, q.get_device()
-    (T, H, D), (NB, bs, Hkv, _), n = q.shape, k_cache.shape, q_offsets.shape[0]
-    B, M, pool = n - 1, block_tables.shape[1], (NB, bs, Hkv, D)
+    B, pool = n - 1, (NB, bs, Hkv, D)
     cap = M * bs if max_context_len is None else int(max_context_len)
     if out is None:
         out = torch.empty((T, H, D), dtype=dt, device=q.device)
@@ -333,10 +349,13 @@ def pa_decode_grouped(q, k_cache, v_cache, block_tables, context_lens, scale, ma
     [NB,bs,Hkv,D] of the same type, ``max_context_len`` a host-side bound on
     context_lens.  Returns ``out`` [B,H,D]."""
     name = "pa_decode_grouped"
-    _shaped(name, ("q", q, 3), ("k_cache", k_cache, 4), ("block_tables", block_tables, 2))
+    try:
+        (B, H, D), (NB, bs, Hkv, _), (_, M) = q.shape, k_cache.shape, block_tables.shape
+    except (AttributeError, ValueError):
+        raise _misshaped(name, ("q", q, 3), ("k_cache", k_cache, 4),
+                         ("block_tables", block_tables, 2)) from None
     code, dt, dev = _float16(name, q), q.dtype, q.get_device()
-    (B, H, D), (NB, bs, Hkv, _) = q.shape, k_cache.shape
-    M, pool, cap = block_tables.shape[1], (NB, bs, Hkv, D), int(max_context_len)
+    pool, cap = (NB, bs, Hkv, D), int(max_context_len)
     if out is None:
         out = torch.empty((B, H, D), dtype=dt, device=q.device)
     if not (dev >= 0 and _dense(q, dt, (B, H, D), dev) and _dense(k_cache, dt, pool, dev)
