@@ -83,7 +83,7 @@ struct Cfg {
   static constexpr int HALF = PAGED ? 1024 : kSlab;       // from dims 0-63 to dims 64-127
   static constexpr int OFF_KV = 2 * kQRoom;
   static constexpr int OFF_BAR = OFF_KV + RING * TILE_BYTES;
-  static constexpr int OFF_MISC = OFF_BAR + kBars * 8;  // TMEM address, issue counters, items
+  static constexpr int OFF_MISC = OFF_BAR + kBars * 8;  // TMEM address, stage counters, items
   static constexpr int OFF_TBL = (OFF_MISC + 16 + kMaxRing * 4 + kItems * 64 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_TBL + (PAGED ? kWindow * 4 : 0) + 1024;
   static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -231,17 +231,6 @@ struct Units {
   }
 };
 
-// Wait until the S issuer has issued `n` products of a tile.
-__device__ __forceinline__ bool wait_count(volatile int* cnt, int n) {
-  if (*cnt >= n) return true;
-  const long long t0 = clock64();
-  while (*cnt < n) {
-    __nanosleep(32);
-    if (clock64() - t0 > kWaitLimitCycles) return false;
-  }
-  return true;
-}
-
 // The registers of a thread: the softmax warps hold a row of S, the others next
 // to nothing (128 * (2 * 200 + 104) = 384 * 168, what the block is launched with).
 __device__ __forceinline__ void reg_inc() {
@@ -318,7 +307,6 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   uint64_t* it_empty = it_full + kItems;  // [kItems]: every role has copied it
   uint64_t* drain = it_empty + kItems;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
-  volatile int* s_issued = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // [2]
   int* stage_left = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // [ring] see the epilogue
   Item* items = reinterpret_cast<Item*>(smem + C::OFF_MISC + 16 + kMaxRing * 4);
   int32_t* tbl = reinterpret_cast<int32_t*>(smem + C::OFF_TBL);
@@ -327,8 +315,6 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   const int tpt = a.span / 2;  // tokens of a tile
 
   if (threadIdx.x == 0) {
-    s_issued[0] = 0;
-    s_issued[1] = 0;
     for (int s = 0; s < kRing; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
@@ -572,7 +558,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             if (t + 1 == nt[x]) tc::commit(&q_free[x]);
             last_free = &s_free[x];
             last_phase = done[x] & 1;
-            s_issued[x] = ++done[x];  // a scheduling hint to the P V issuer
+            ++done[x];
           }
           if (ok) tc::commit(&kv_empty[u % kRing]);
         }
@@ -601,8 +587,6 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           // read of O by the same warps: O may then be overwritten.)
           if (!(ok = mbar_wait(&p_full[x], done[x] & 1))) continue;
           if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) continue;
-          // Behind S(t + 1) in the tensor core's queue, so that never waits for this.
-          if (t + 1 < nt[x] && !(ok = wait_count(s_issued + x, done[x] + 2))) continue;
           tc::fence_after_sync();
           const uint32_t ta = tmem + kColP + x * (kTile / 2);
           const uint64_t db = dv + (u % kRing) * (C::TILE_BYTES >> 4);
@@ -676,6 +660,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         if (lane == 0) mbar_arrive(&s_free[x]);
         float mt = max3f(cm[0], cm[1], fmaxf(cm[2], cm[3]));
         if (kbase + kTile - 1 > pos0) {  // keys past some row's position
+          // (By chunks, with a warp's fully seen and fully hidden ones told apart
+          // by branches, this took fewer instructions and spilled: 30 % slower.)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int seen = pos - (kbase + c * 32);  // last key of these 32 it sees

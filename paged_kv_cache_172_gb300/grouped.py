@@ -56,6 +56,15 @@ def _run(fn, name, dev, stream, *args):
         _check(rc, name)
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor from the pool of the stream that the call runs on: one of
+    another stream's pool could still be in use there, or be handed out again."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dense(t, dtype, shape, dev):
     """Whether t is a contiguous tensor of that type and shape on device dev."""
     return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
@@ -144,7 +153,8 @@ def pa_step_plan(cached_lens, new_lens, block_tables, free_blocks, free_state, b
                          ("free_blocks", free_blocks, 1)) from None
     dev = cached_lens.get_device()
     if out is None:
-        out = StepPlan.empty(B, T, cached_lens.device)
+        with torch.cuda.stream(stream):  # (None: the current one)
+            out = StepPlan.empty(B, T, cached_lens.device)
     ctx, offs, slots, pos, state = out
     one = (B,)
     if not (dev >= 0 and _dense(cached_lens, i32, one, dev) and _dense(new_lens, i32, one, dev)
@@ -209,9 +219,9 @@ def pa_rope_cache_write(q, k, v, positions, table, slot_mapping, k_cache=None, v
     else:
         v = slot_mapping = None
         if k_out is None:
-            k_out = torch.empty(kv, dtype=dt, device=q.device)
+            k_out = _empty(kv, dt, q.device, stream)
     if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=dt, device=q.device)
+        q_out = _empty((T, H, D), dt, q.device, stream)
     if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _rows(k, dt, kv, dev)
             and _dense(positions, torch.int32, pos_shape, dev)
             and _dense(table, torch.int64, (n,), dev) and _rows(q_out, dt, (T, H, D), dev)
@@ -254,7 +264,7 @@ def pa_prompt_attention(q, k, v, q_offsets, scale, out=None, status=None, stream
                          ("q_offsets", q_offsets, 1)) from None
     code, dt, dev = _float16(name, q), q.dtype, q.get_device()
     if out is None:
-        out = torch.empty((T, H, D), dtype=dt, device=q.device)
+        out = _empty((T, H, D), dt, q.device, stream)
     if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _rows(k, dt, (T, Hkv, D), dev)
             and _rows(v, dt, (T, Hkv, D), dev) and _dense(q_offsets, torch.int32, (n,), dev)
             and _dense(out, dt, (T, H, D), dev) and _status_ok(status, dev)):
@@ -268,12 +278,12 @@ def pa_prompt_attention(q, k, v, q_offsets, scale, out=None, status=None, stream
     return out
 
 
-def _workspace(name, workspace, nbytes, dev):
+def _workspace(name, workspace, nbytes, dev, stream):
     """(address, bytes, owner) of the given workspace, or of a new one of nbytes."""
     if workspace is None:
         if nbytes == 0:
             return None, 0, None
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+        workspace = _empty(nbytes, torch.uint8, f"cuda:{dev}", stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"{name}: workspace must be contiguous and on cuda:{dev}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -313,7 +323,7 @@ def pa_chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offset
     B, pool = n - 1, (NB, bs, Hkv, D)
     cap = M * bs if max_context_len is None else int(max_context_len)
     if out is None:
-        out = torch.empty((T, H, D), dtype=dt, device=q.device)
+        out = _empty((T, H, D), dt, q.device, stream)
     if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _dense(k_cache, dt, pool, dev)
             and _dense(v_cache, dt, pool, dev) and _dense(block_tables, torch.int32, (B, M), dev)
             and _dense(context_lens, torch.int32, (B,), dev)
@@ -328,7 +338,7 @@ def pa_chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offset
     if split:
         need = 0 if workspace is not None else _sized(pa_chunk_attention_workspace_size, dev, B,
                                                       T, H, Hkv, D, cap)
-        ws, ws_bytes, workspace = _workspace(name, workspace, need, dev)
+        ws, ws_bytes, workspace = _workspace(name, workspace, need, dev, stream)
     _run(lib().pa_chunk_attention, name, dev, stream, q.data_ptr(), k_cache.data_ptr(),
          v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
          q_offsets.data_ptr(), B, T, H, Hkv, D, code, _stride(q), bs, NB, M, cap, scale,
@@ -357,7 +367,7 @@ def pa_decode_grouped(q, k_cache, v_cache, block_tables, context_lens, scale, ma
     code, dt, dev = _float16(name, q), q.dtype, q.get_device()
     pool, cap = (NB, bs, Hkv, D), int(max_context_len)
     if out is None:
-        out = torch.empty((B, H, D), dtype=dt, device=q.device)
+        out = _empty((B, H, D), dt, q.device, stream)
     if not (dev >= 0 and _dense(q, dt, (B, H, D), dev) and _dense(k_cache, dt, pool, dev)
             and _dense(v_cache, dt, pool, dev) and _dense(block_tables, torch.int32, (B, M), dev)
             and _dense(context_lens, torch.int32, (B,), dev) and _dense(out, dt, (B, H, D), dev)
@@ -369,7 +379,7 @@ def pa_decode_grouped(q, k_cache, v_cache, block_tables, context_lens, scale, ma
                               ("out", out, dt, (B, H, D))), (), status)
     need = 0 if workspace is not None else _sized(pa_decode_grouped_workspace_size, dev, B, H,
                                                   Hkv, D, bs, cap, partition_tokens)
-    ws, ws_bytes, workspace = _workspace(name, workspace, need, dev)
+    ws, ws_bytes, workspace = _workspace(name, workspace, need, dev, stream)
     _run(lib().pa_decode_grouped, name, dev, stream, q.data_ptr(), k_cache.data_ptr(),
          v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, H, Hkv, D, code,
          bs, NB, M, cap, partition_tokens, scale, out.data_ptr(), ws, ws_bytes,

@@ -152,6 +152,25 @@ def test_two_streams_share_nothing_and_a_graph_follows_lengths():
     check_all(a, oa)
 
 
+def test_own_buffers_come_from_the_stream_of_the_call():
+    # out and workspace left to the call on another stream, while the current one
+    # keeps taking and dropping blocks of the same size
+    p = Paged([4000, 900], [10, 40], 8, 2, 128, 16, torch.bfloat16, seed=12)
+    want = run(p)[0]
+    side = torch.cuda.Stream()
+    n = pk.pa_chunk_attention_workspace_size(2, 50, 8, 2, 128, p.tables.shape[1] * 16)
+    assert n > 0
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        outs.append(pk.pa_chunk_attention(p.q, p.k_cache, p.v_cache, p.tables, p.context,
+                                          p.offsets, p.scale, stream=side))
+        for size in (n, want.numel() * 2):  # scribbles on whatever the pool hands out
+            torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 def test_refusals():
     p = Paged([100], [10], 4, 2, 64, 16, torch.float16)
     with pytest.raises(pk.PagedKVError):
