@@ -367,21 +367,23 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       for (int i = lane; i < a.B; i += 32)
         if (sequence<PAGED>(a, i).lost) flag_status(a.status, PA_DEV_BAD_CONTEXT);
     Units<PAGED> units(a);
-    const long long n_items = (long long)a.max_units * a.Hkv * a.split;
-    int round = 0, last_rank = -1, b = 0, unit = 0;
+    const unsigned n_items = (unsigned)a.max_units * a.Hkv * a.split;  // below 2^31
+    unsigned round = 0;
+    int last_rank = -1, b = 0, unit = 0;
     bool more = true;
     // Items are dealt in rounds, every other one backwards, so that no CTA
     // gets the longest of every round.
     auto next = [&](Item& it) {
       it.valid = 0;
       while (more) {
-        const int at = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-        const long long idx = (long long)round * gridDim.x + at;
+        const unsigned at = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+        const unsigned idx = round * gridDim.x + at;
         ++round;
         if (!(more = idx < n_items)) break;
-        it.part = (int)(idx % a.split);
-        it.hkv = (int)(idx / a.split % a.Hkv);
-        const int rank = (int)(idx / ((long long)a.split * a.Hkv));
+        const unsigned unit_head = idx / a.split;
+        const int rank = (int)(unit_head / a.Hkv);
+        it.part = (int)(idx - unit_head * a.split);
+        it.hkv = (int)(unit_head - rank * a.Hkv);
         if (rank != last_rank && !(more = units.find(rank, b, unit))) break;
         last_rank = rank;
         const Seq s = sequence<PAGED>(a, b);
@@ -425,30 +427,27 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       }
       __syncwarp();
     };
-    // Two items ahead; then, item by item, what the other roles wait for first.
-    Item cur, nxt;
-    next(cur);
-    post(0, cur);
-    next(nxt);
-    if (ok && cur.valid) post(1, nxt);
-    for (int k = 0; ok && cur.valid; ++k) {
-      // Q of item k, tile by tile as the products of item k - 1 let go of it:
-      // boxes of tpt tokens x G heads x 64 dims; rows past the array read as zeros.
-      if (lane == 0)
+    // Item k is posted ahead of the Q loads of item k - 1.
+    Item cur, prev;
+    prev.valid = 0;
+    for (int k = 0; ok; ++k) {
+      next(cur);
+      post(k, cur);
+      // Q of the item before, tile by tile as the products of the one before that
+      // let go of it: boxes of tpt tokens x G heads x 64 dims; rows past the array
+      // read as zeros.
+      if (ok && lane == 0 && prev.valid)
         for (int x = 0; x < 2 && ok; ++x) {
-          if (!(ok = mbar_wait(&q_free[x], (k & 1) ^ 1))) break;
+          if (!(ok = mbar_wait(&q_free[x], k & 1))) break;
           mbar_arrive_expect_tx(&q_full[x], C::HALVES * tpt * a.G * 128);
           for (int hf = 0; hf < C::HALVES; ++hf)
-            tma_load_3d(sQ + x * kQRoom + hf * kSlab, &qmap, 64 * hf, cur.hkv * a.G,
-                        cur.row0 + x * tpt, &q_full[x]);
+            tma_load_3d(sQ + x * kQRoom + hf * kSlab, &qmap, 64 * hf, prev.hkv * a.G,
+                        prev.row0 + x * tpt, &q_full[x]);
           ++issued;
         }
-      if (!(ok = __shfl_sync(kAll, ok, 0))) break;
-      cur = nxt;
-      if (ok && cur.valid) {
-        next(nxt);
-        post(k + 2, nxt);
-      }
+      ok = __shfl_sync(kAll, ok, 0);
+      if (!cur.valid) break;
+      prev = cur;
     }
   } else if (warp == kWarpLoad) {
     // ------------------------------------------------------------ K and V
@@ -578,54 +577,53 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     Item it;
     for (int k = 0; take(k, it); ++k) {
       const int nt[2] = {it.ntile_a, it.ntile_b};
-      auto issue_pv = [&](int t) {  // lane 0
-        const int u = u0 + ring_v(t, it.n_kv);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (t >= nt[x] || !ok) continue;
-          // (P of an item's first tile is stored behind the item before's last
-          // read of O by the same warps: O may then be overwritten.)
-          if (!(ok = mbar_wait(&p_full[x], done[x] & 1))) continue;
-          if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) continue;
-          tc::fence_after_sync();
-          const uint32_t ta = tmem + kColP + x * (kTile / 2);
-          const uint64_t db = dv + (u % kRing) * (C::TILE_BYTES >> 4);
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            tc::mma_f16_ts(tmem + kColO + x * D, ta + kk * 8, db + ((kk * 2 * C::GROUP) >> 4),
-                           kIdO, t > 0 || kk > 0);
-          tc::commit(&pv_done[x]);
-          ++done[x];
-        }
-        if (ok) tc::commit(&kv_empty[u % kRing]);
-      };
-      if (lane == 0)
-        for (int t = 0; t + 1 < it.n_kv && ok; ++t) issue_pv(t);
-      if (!(ok = __shfl_sync(kAll, ok, 0))) break;
-      if (it.n_kv == 0) {
-        u0 += it.parts == 1;
-        continue;
-      }
       // Rows of the last key tile past the sequence's keys hold whatever the
       // block's tail, or the next sequence's rows, hold: 0 * NaN is NaN, so the
       // warp zeroes them once V has landed.
+      // (Two rounds through one copy of the code: the tiles up to it, by one lane
+      // without meeting the others, and it alone.)
       const int live = it.n - (it.kt0 + it.n_kv - 1) * kTile;
-      if (live < kTile) {
-        const int u = u0 + ring_v(it.n_kv - 1, it.n_kv);
-        if (lane == 0) ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1);
-        if (!(ok = __shfl_sync(kAll, ok, 0))) break;
-        uint8_t* vt = sKV + (u % kRing) * C::TILE_BYTES;
-        constexpr int kChunks = D / 8;
-        for (int i = lane; i < (kTile - live) * kChunks; i += 32) {
-          const int r = live + i / kChunks, c = i % kChunks;
-          *reinterpret_cast<uint4*>(vt + (r >> 3) * C::GROUP + (c >> 3) * C::HALF +
-                                    (r & 7) * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      const int whole = it.n_kv - (it.n_kv > 0 && live < kTile ? 1 : 0);
+      for (int t0 = 0, t1 = whole; t0 < it.n_kv; t0 = t1, t1 = it.n_kv) {
+        if (t0 == whole) {
+          const int u = u0 + ring_v(t0, it.n_kv);
+          if (lane == 0) ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1);
+          if (!(ok = __shfl_sync(kAll, ok, 0))) break;
+          uint8_t* vt = sKV + (u % kRing) * C::TILE_BYTES;
+          constexpr int kChunks = D / 8;
+          for (int i = lane; i < (kTile - live) * kChunks; i += 32) {
+            const int r = live + i / kChunks, c = i % kChunks;
+            *reinterpret_cast<uint4*>(vt + (r >> 3) * C::GROUP + (c >> 3) * C::HALF +
+                                      (r & 7) * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        fence_proxy_async_smem();
-        __syncwarp();
+        if (lane == 0)
+          for (int t = t0; t < t1 && ok; ++t) {
+            const int u = u0 + ring_v(t, it.n_kv);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (t >= nt[x] || !ok) continue;
+              // (P of an item's first tile is stored behind the item before's last
+              // read of O by the same warps: O may then be overwritten.)
+              if (!(ok = mbar_wait(&p_full[x], done[x] & 1))) continue;
+              if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) continue;
+              tc::fence_after_sync();
+              const uint32_t ta = tmem + kColP + x * (kTile / 2);
+              const uint64_t db = dv + (u % kRing) * (C::TILE_BYTES >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                tc::mma_f16_ts(tmem + kColO + x * D, ta + kk * 8,
+                               db + ((kk * 2 * C::GROUP) >> 4), kIdO, t > 0 || kk > 0);
+              tc::commit(&pv_done[x]);
+              ++done[x];
+            }
+            if (ok) tc::commit(&kv_empty[u % kRing]);
+          }
+        if (!(ok = __shfl_sync(kAll, ok, 0))) break;
       }
-      if (lane == 0) issue_pv(it.n_kv - 1);
-      if (!(ok = __shfl_sync(kAll, ok, 0))) break;
+      if (!ok) break;
       u0 += 2 * it.n_kv + (it.parts == 1);
     }
   } else {
