@@ -360,7 +360,205 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     return it.valid != 0;
   };
 
-  if (warp == kWarpSched) {
+  if (warp < kWarpLoad) {
+    // ------------------------------------------------------------ softmax
+    reg_inc();
+    const int x = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const int my_tok = (row * a.g_magic) >> 16;  // row / G
+    const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
+    const uint32_t t_s = tmem + t_lane + kColS, t_o = tmem + t_lane + kColO + x * D;
+    const float sl2 = a.scale_log2;
+    int done = 0;    // key tiles of the items before and of this one
+    int u0 = 0;      // ring tiles of the items before
+    Item it;
+    for (int k = 0; take(k, it); ++k) {
+      const int pos0 = it.pos_a + (x ? tpt : 0);
+      const int ntile = x ? it.ntile_b : it.ntile_a;
+      const bool live = my_tok < (x ? it.toks_b : it.toks_a);  // a row of this sequence
+      const int pos = pos0 + my_tok;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < ntile; ++j, ++done) {
+        if (!(ok = __all_sync(kAll, mbar_wait(&s_full[x], done & 1)))) break;
+        tc::fence_after_sync();
+        const int kbase = (it.kt0 + j) * kTile;
+        uint32_t r[4][32];
+        float cm[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::ld_32x32_max(t_s + c * 32, r[c], cm[c]);
+        tc::wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[x]);
+        float mt = max3f(cm[0], cm[1], fmaxf(cm[2], cm[3]));
+        if (kbase + kTile - 1 > pos0) {  // keys past some row's position
+          // (By chunks, with a warp's fully seen and fully hidden ones told apart
+          // by branches, this took fewer instructions and spilled: 30 % slower.)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int seen = pos - (kbase + c * 32);  // last key of these 32 it sees
+            const uint32_t hide = seen < 0 ? ~0u : seen >= 31 ? 0u : ~0u << (seen + 1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((hide >> i) & 1) r[c][i] = __float_as_uint(-INFINITY);
+          }
+          float mx[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mx[(i >> 1) & 7] = max3f(mx[(i >> 1) & 7], __uint_as_float(r[c][i]),
+                                       __uint_as_float(r[c][i + 1]));
+          mt = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]),
+                     fmaxf(mx[6], mx[7]));
+        }
+        mt *= sl2;
+        const float m_new = fmaxf(m, mt);
+        const bool resc = live && m_new > m + kLazy;
+        float alpha = 1.f;
+        if (resc) {
+          alpha = ex2_approx(m - m_new);
+          m = m_new;
+          l *= alpha;
+        }
+        // A row that has seen masked keys alone (a part whose range starts past
+        // its position) has m = -inf, and -inf + inf is NaN: taken with maximum 0
+        // its weights are all zero and its partial row is empty.
+        const float neg_m = m == -INFINITY ? 0.f : -m;
+        float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float y0, y1;
+            fma_f32x2(y0, y1, __uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1]),
+                      sl2, sl2, neg_m, neg_m);
+            const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+            const int q = 2 * (e & 3);
+            add_f32x2(rs[q], rs[q + 1], rs[q], rs[q + 1], p0, p1);
+            r[c][e] = pack2<T>(p0, p1);
+          }
+        l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+        if (j > 0) {  // P V of the tile before done: P is free, O stands still
+          if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
+          tc::fence_after_sync();
+          if (__any_sync(kAll, resc)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc::ld_32x32(t_o + c * 32, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tc::st_32x32(t_o + c * 32, o);
+            }
+            tc::wait_st();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)  // the packed pairs as they lie in the registers
+          tc::st_32x16(tmem + t_lane + kColP + x * (kTile / 2) + c * 16, r[c]);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      if (ntile > 0) {  // the last P V
+        if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
+        tc::fence_after_sync();
+      }
+      // The output, half the columns at a time.  Of a whole unit: each warp turns
+      // its 32 rows around in its share of the ring slot granted to the item, so
+      // that the stores to global memory are whole row halves and not 16 bytes of
+      // 32 rows (which took 3,000 cycles a tile); rows that are not the sequence's
+      // are left out, the next packed rows being another one's.  Of a part: the
+      // unnormalised row.
+      const bool whole = it.parts == 1;
+      const int stage_u = u0 + 2 * it.n_kv;
+      u0 = stage_u + whole;
+      const int toks = x ? it.toks_b : it.toks_a, first = it.row0 + (x ? tpt : 0);
+      if (toks == 0) continue;  // (tile B of a unit that ends in tile A)
+      if (whole &&
+          !(ok = __all_sync(kAll, mbar_wait(&kv_full[stage_u % kRing], (stage_u / kRing) & 1))))
+        break;
+      constexpr int kHalf = D / 2, kChunks = kHalf / 8;  // columns; 16-byte chunks of them
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      uint8_t* stage = sKV + (stage_u % kRing) * C::TILE_BYTES + warp * (32 * D);
+      auto at = [&](int r, int c) {  // chunk c of row r, conflict-free both ways
+        return stage + r * D + ((c ^ (kChunks == 8 ? r & 7 : (r >> 1) & 3)) * 16);
+      };
+      T* out0 = static_cast<T*>(a.out) + ((size_t)first * a.H + it.hkv * a.G) * D;
+      const size_t prow = (size_t)first * a.G + row, plane = (size_t)a.T * a.G;  // see part_ml
+      float4* part_o =
+          reinterpret_cast<float4*>(a.ws) + (size_t)(it.part * a.Hkv + it.hkv) * (D / 4) * plane;
+      // (Rolled: the code of the hot loop above and of the other roles has to
+      // stay in the instruction cache.)
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t o[kHalf / 32][32];
+        if (ntile > 0) {
+#pragma unroll
+          for (int c = 0; c < kHalf / 32; ++c) tc::ld_32x32(t_o + hf * kHalf + c * 32, o[c]);
+          tc::wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) o[i >> 5][i & 31] = 0u;
+        }
+        if (whole) {
+#pragma unroll
+          for (int q = 0; q < kChunks; ++q) {
+            uint32_t hv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              hv[i] = pack2<T>(__uint_as_float(o[q >> 2][8 * (q & 3) + 2 * i]) * inv,
+                               __uint_as_float(o[q >> 2][8 * (q & 3) + 2 * i + 1]) * inv);
+            *reinterpret_cast<uint4*>(at(lane, q)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+          }
+          __syncwarp();
+          const int c = lane % kChunks;
+#pragma unroll 4
+          for (int i = 0; i < kChunks; ++i) {
+            const int r = i * (32 / kChunks) + lane / kChunks, rt = quarter * 32 + r;
+            const int tok = (rt * a.g_magic) >> 16;  // rt / G
+            if (tok < toks)
+              *reinterpret_cast<uint4*>(out0 + ((size_t)tok * a.H + rt - tok * a.G) * D +
+                                        hf * kHalf + c * 8) =
+                  *reinterpret_cast<const uint4*>(at(r, c));
+          }
+          __syncwarp();
+        } else if (live) {
+          float4* dst = part_o + hf * (kHalf / 4) * plane + prow;
+#pragma unroll
+          for (int i = 0; i < kHalf / 4; ++i, dst += plane)
+            *dst = make_float4(__uint_as_float(o[i >> 3][4 * (i & 7)]),
+                               __uint_as_float(o[i >> 3][4 * (i & 7) + 1]),
+                               __uint_as_float(o[i >> 3][4 * (i & 7) + 2]),
+                               __uint_as_float(o[i >> 3][4 * (i & 7) + 3]));
+        }
+      }
+      tc::fence_before_sync();  // O is read before the next item's P V overwrites it
+      if (whole) {
+        // The last of the four or eight warps that use the stage lets the slot go
+        // (to TMA, the async proxy, which these accesses come before).  A count
+        // and not a barrier: a tile may be several items ahead of the other.
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence_block();
+          if (atomicAdd(&stage_left[stage_u % kRing], 1) == (it.toks_b > 0 ? 7 : 3)) {
+            __threadfence_block();
+            stage_left[stage_u % kRing] = 0;
+            mbar_arrive(&kv_empty[stage_u % kRing]);
+          }
+        }
+      } else if (live) {
+        part_ml(a, D, it.part, it.hkv)[prow] = make_float2(m, l);
+      }
+    }
+  } else if (warp == kWarpSched) {
     // ------------------------------------------------------------ scheduler, Q loads
     reg_dec();
     if (blockIdx.x == 0)
@@ -569,7 +767,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       }
       if (!(ok = __shfl_sync(kAll, ok, 0))) break;
     }
-  } else if (warp == kWarpPv) {
+  } else {  // kWarpPv
     // ------------------------------------------------------------ O += P V
     reg_dec();
     const uint64_t dv = tc::smem_desc(smem_u32(sKV), C::HALF, C::GROUP, tc::kSwizzle128B);
@@ -625,204 +823,6 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       }
       if (!ok) break;
       u0 += 2 * it.n_kv + (it.parts == 1);
-    }
-  } else {
-    // ------------------------------------------------------------ softmax
-    reg_inc();
-    const int x = warp >> 2, quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    const int my_tok = (row * a.g_magic) >> 16;  // row / G
-    const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_s = tmem + t_lane + kColS, t_o = tmem + t_lane + kColO + x * D;
-    const float sl2 = a.scale_log2;
-    int done = 0;    // key tiles of the items before and of this one
-    int u0 = 0;      // ring tiles of the items before
-    Item it;
-    for (int k = 0; take(k, it); ++k) {
-      const int pos0 = it.pos_a + (x ? tpt : 0);
-      const int ntile = x ? it.ntile_b : it.ntile_a;
-      const bool live = my_tok < (x ? it.toks_b : it.toks_a);  // a row of this sequence
-      const int pos = pos0 + my_tok;
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < ntile; ++j, ++done) {
-        if (!(ok = __all_sync(kAll, mbar_wait(&s_full[x], done & 1)))) break;
-        tc::fence_after_sync();
-        const int kbase = (it.kt0 + j) * kTile;
-        uint32_t r[4][32];
-        float cm[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::ld_32x32_max(t_s + c * 32, r[c], cm[c]);
-        tc::wait_ld();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[x]);
-        float mt = max3f(cm[0], cm[1], fmaxf(cm[2], cm[3]));
-        if (kbase + kTile - 1 > pos0) {  // keys past some row's position
-          // (By chunks, with a warp's fully seen and fully hidden ones told apart
-          // by branches, this took fewer instructions and spilled: 30 % slower.)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int seen = pos - (kbase + c * 32);  // last key of these 32 it sees
-            const uint32_t hide = seen < 0 ? ~0u : seen >= 31 ? 0u : ~0u << (seen + 1);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((hide >> i) & 1) r[c][i] = __float_as_uint(-INFINITY);
-          }
-          float mx[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mx[(i >> 1) & 7] = max3f(mx[(i >> 1) & 7], __uint_as_float(r[c][i]),
-                                       __uint_as_float(r[c][i + 1]));
-          mt = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]),
-                     fmaxf(mx[6], mx[7]));
-        }
-        mt *= sl2;
-        const float m_new = fmaxf(m, mt);
-        const bool resc = live && m_new > m + kLazy;
-        float alpha = 1.f;
-        if (resc) {
-          alpha = ex2_approx(m - m_new);
-          m = m_new;
-          l *= alpha;
-        }
-        // A row that has seen masked keys alone (a part whose range starts past
-        // its position) has m = -inf, and -inf + inf is NaN: taken with maximum 0
-        // its weights are all zero and its partial row is empty.
-        const float neg_m = m == -INFINITY ? 0.f : -m;
-        float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float y0, y1;
-            fma_f32x2(y0, y1, __uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1]),
-                      sl2, sl2, neg_m, neg_m);
-            const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
-            const int q = 2 * (e & 3);
-            add_f32x2(rs[q], rs[q + 1], rs[q], rs[q + 1], p0, p1);
-            r[c][e] = pack2<T>(p0, p1);
-          }
-        l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
-        if (j > 0) {  // P V of the tile before done: P is free, O stands still
-          if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
-          tc::fence_after_sync();
-          if (__any_sync(kAll, resc)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tc::ld_32x32(t_o + c * 32, o);
-              tc::wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tc::st_32x32(t_o + c * 32, o);
-            }
-            tc::wait_st();
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)  // the packed pairs as they lie in the registers
-          tc::st_32x16(tmem + t_lane + kColP + x * (kTile / 2) + c * 16, r[c]);
-        tc::wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
-      }
-      if (!ok) break;
-      if (ntile > 0) {  // the last P V
-        if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
-        tc::fence_after_sync();
-      }
-      // The output, half the columns at a time.  Of a whole unit: each warp turns
-      // its 32 rows around in its share of the ring slot granted to the item, so
-      // that the stores to global memory are whole row halves and not 16 bytes of
-      // 32 rows (which took 3,000 cycles a tile); rows that are not the sequence's
-      // are left out, the next packed rows being another one's.  Of a part: the
-      // unnormalised row.
-      const bool whole = it.parts == 1;
-      const int stage_u = u0 + 2 * it.n_kv;
-      u0 = stage_u + whole;
-      const int toks = x ? it.toks_b : it.toks_a, first = it.row0 + (x ? tpt : 0);
-      if (toks == 0) continue;  // (tile B of a unit that ends in tile A)
-      if (whole &&
-          !(ok = __all_sync(kAll, mbar_wait(&kv_full[stage_u % kRing], (stage_u / kRing) & 1))))
-        break;
-      constexpr int kHalf = D / 2, kChunks = kHalf / 8;  // columns; 16-byte chunks of them
-      const float inv = l != 0.f ? 1.f / l : 0.f;
-      uint8_t* stage = sKV + (stage_u % kRing) * C::TILE_BYTES + warp * (32 * D);
-      auto at = [&](int r, int c) {  // chunk c of row r, conflict-free both ways
-        return stage + r * D + ((c ^ (kChunks == 8 ? r & 7 : (r >> 1) & 3)) * 16);
-      };
-      T* out0 = static_cast<T*>(a.out) + ((size_t)first * a.H + it.hkv * a.G) * D;
-      const size_t prow = (size_t)first * a.G + row, plane = (size_t)a.T * a.G;  // see part_ml
-      float4* part_o =
-          reinterpret_cast<float4*>(a.ws) + (size_t)(it.part * a.Hkv + it.hkv) * (D / 4) * plane;
-      // (Rolled: the code of the hot loop above and of the other roles has to
-      // stay in the instruction cache.)
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t o[kHalf / 32][32];
-        if (ntile > 0) {
-#pragma unroll
-          for (int c = 0; c < kHalf / 32; ++c) tc::ld_32x32(t_o + hf * kHalf + c * 32, o[c]);
-          tc::wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < kHalf; ++i) o[i >> 5][i & 31] = 0u;
-        }
-        if (whole) {
-#pragma unroll
-          for (int q = 0; q < kChunks; ++q) {
-            uint32_t hv[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              hv[i] = pack2<T>(__uint_as_float(o[q >> 2][8 * (q & 3) + 2 * i]) * inv,
-                               __uint_as_float(o[q >> 2][8 * (q & 3) + 2 * i + 1]) * inv);
-            *reinterpret_cast<uint4*>(at(lane, q)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-          }
-          __syncwarp();
-          const int c = lane % kChunks;
-#pragma unroll 4
-          for (int i = 0; i < kChunks; ++i) {
-            const int r = i * (32 / kChunks) + lane / kChunks, rt = quarter * 32 + r;
-            const int tok = (rt * a.g_magic) >> 16;  // rt / G
-            if (tok < toks)
-              *reinterpret_cast<uint4*>(out0 + ((size_t)tok * a.H + rt - tok * a.G) * D +
-                                        hf * kHalf + c * 8) =
-                  *reinterpret_cast<const uint4*>(at(r, c));
-          }
-          __syncwarp();
-        } else if (live) {
-          float4* dst = part_o + hf * (kHalf / 4) * plane + prow;
-#pragma unroll
-          for (int i = 0; i < kHalf / 4; ++i, dst += plane)
-            *dst = make_float4(__uint_as_float(o[i >> 3][4 * (i & 7)]),
-                               __uint_as_float(o[i >> 3][4 * (i & 7) + 1]),
-                               __uint_as_float(o[i >> 3][4 * (i & 7) + 2]),
-                               __uint_as_float(o[i >> 3][4 * (i & 7) + 3]));
-        }
-      }
-      tc::fence_before_sync();  // O is read before the next item's P V overwrites it
-      if (whole) {
-        // The last of the four or eight warps that use the stage lets the slot go
-        // (to TMA, the async proxy, which these accesses come before).  A count
-        // and not a barrier: a tile may be several items ahead of the other.
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          __threadfence_block();
-          if (atomicAdd(&stage_left[stage_u % kRing], 1) == (it.toks_b > 0 ? 7 : 3)) {
-            __threadfence_block();
-            stage_left[stage_u % kRing] = 0;
-            mbar_arrive(&kv_empty[stage_u % kRing]);
-          }
-        }
-      } else if (live) {
-        part_ml(a, D, it.part, it.hkv)[prow] = make_float2(m, l);
-      }
     }
   }
 
