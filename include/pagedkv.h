@@ -539,7 +539,9 @@ pa_status pa_rope_cache_write(const void *q, const void *k, const void *v,
  * with G = H / Hkv, scores and sums in fp32; the softmax weights are rounded to
  * the 16-bit type for their product with v, the result once more, to nearest
  * even.  Rows before q_offsets[0] and behind q_offsets[B] are left as they
- * were.  Other sequences' rows, NaN included, never reach a result.
+ * were.  Other sequences' rows, NaN included, never reach a result, nor does a
+ * later token's k; a later token's v must be finite (its weight is an exact zero,
+ * and a zero times an infinity or NaN in the same 128 keys is NaN).
  *
  * q [T, H, D], k and v [T, Hkv, D] with their strides; out [T, H, D]
  * q_offsets [B+1] int32, rising, within [0, T]: a sequence breaking that is
@@ -560,7 +562,7 @@ pa_status pa_prompt_attention(const void *q, const void *k, const void *v,
  * positions: query i is at n - q_len + i, n = context_lens[b], and attends to
  * keys 0 .. n - q_len + i of the cache (which holds the chunk's own K/V
  * already).  Otherwise as pa_prompt_attention; the cache as in pa_decode with
- * Hkv heads.  A context outside [q_len, min(max_context_len,
+ * Hkv heads.  Slots past a sequence's length may hold anything.  A context outside [q_len, min(max_context_len,
  * max_blocks_per_seq * block_size)] is flagged PA_DEV_BAD_CONTEXT and its rows
  * are zeros; a bad block id reads as zeros, flagged PA_DEV_BAD_BLOCK_ID.
  *
@@ -592,7 +594,9 @@ pa_status pa_chunk_attention(const void *q, const void *k_cache, const void *v_c
  * q and out [B, H, D] and the cache [num_blocks, block_size, Hkv, D] in dtype;
  * a context past max_context_len is flagged PA_DEV_BAD_CONTEXT and cut to it, a
  * negative one gives zeros.  partition_tokens: a multiple of 64 up to 2048, or
- * 0 to choose.  D in {64, 128}; block_size in {8, 16, 32}; B at most 65535;
+ * 0 to choose.  The workspace size depends on the SM count of the current device;
+ * it is 0 where one partition holds the longest context or all partitions fit
+ * the GPU at once (they then merge inside the launch).  D in {64, 128}; block_size in {8, 16, 32}; B at most 65535;
  * any finite scale; (num_blocks + 1) * block_size * Hkv below 2^31.
  * ------------------------------------------------------------------------- */
 size_t pa_decode_grouped_workspace_size(int B, int H, int Hkv, int D, int block_size,

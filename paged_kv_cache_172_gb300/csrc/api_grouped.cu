@@ -280,7 +280,9 @@ size_t pa_decode_grouped_workspace_size(int B, int H, int Hkv, int D, int block_
     return 0;
   const int pt = decode_partition(B, H, Hkv, D, max_context_len, partition_tokens);
   const long long parts = ((long long)max_context_len + pt - 1) / pt;
-  return parts <= 1 ? 0 : (size_t)B * H * parts * (D + 2) * sizeof(float);
+  return pk::grouped_decode_in_cluster(B, H, Hkv, parts)
+             ? 0
+             : (size_t)B * H * parts * (D + 2) * sizeof(float);
 }
 
 pa_status pa_decode_grouped(const void* q, const void* k_cache, const void* v_cache,
@@ -307,7 +309,7 @@ pa_status pa_decode_grouped(const void* q, const void* k_cache, const void* v_ca
       a.part_tokens;
   if (parts > 65535) return PA_ERR_INVALID;
   a.num_parts = (int)parts;
-  if (parts > 1) {
+  if (!pk::grouped_decode_in_cluster(B, H, Hkv, parts)) {
     const size_t need = (size_t)B * H * parts * (D + 2) * sizeof(float);
     if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PA_ERR_INVALID;

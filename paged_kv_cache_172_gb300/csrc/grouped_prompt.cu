@@ -42,7 +42,17 @@
 // before scaling, since O is rescaled only when the maximum grew by more than
 // that), the result once more at the end.
 //
-// Bound: the tensor pipe by intensity; see the notes at launch_grouped.
+// Bound: the tensor pipe by intensity; in the steady state the chain from one S
+// product to the next through the one S region (2 x 1,320 cycles per pair of
+// tiles, where four products take 2,048), and over long prompts the power cap.
+// Besides that a unit costs about 4,000 cycles around its end (last P V product,
+// output, next Q).  Measured (GB300, 32 heads on 8, D = 128, bf16): one prompt of
+// 16,001 tokens 1,279 us, 1,640 TFLOP/s, 0.85 of the measured burst rate and 0.94
+// of the sustained one; eight of 500-4,096 350 us, 1,437 TFLOP/s (0.74); chunks
+// of 512 on 3,584 (40 on 8, fp16) 277 us, 1,163 TFLOP/s (0.60: 704 units on 152
+// SMs are five rounds where 4.6 would do, 125 rows of 128 are used, and 16-token
+// blocks arrive in boxes of 32 rows, which bounds the ring); 16 chunks of 1-48 on
+// up to 8,192 keys 79 us, 3.8 TB/s.
 #include <cuda_bf16.h>
 #include <string.h>
 

@@ -231,6 +231,8 @@ struct GroupedDecodeArgs {
   bool bf16;
 };
 int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context);
+// Whether that many partitions merge inside the launch, without a workspace.
+bool grouped_decode_in_cluster(int B, int H, int Hkv, long long parts);
 cudaError_t launch_grouped_decode(const GroupedDecodeArgs& a, const void* k_cache,
                                   const void* v_cache, cudaStream_t stream);
 

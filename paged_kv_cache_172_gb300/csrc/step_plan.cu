@@ -20,7 +20,8 @@
 // be updated in place.  The work is a few hundred kilobytes at most: the call
 // is bound by its launch and by two trips to memory (lengths, then ring
 // entries), and one launch instead of a scan and a fill is what counts.
-// Measured: see launch_step_plan.
+// Measured (GB300): 38 single tokens 3.8 us, 200 sequences with 11,000 new tokens
+// 5.9 us, of which the launch of an empty kernel is about two thirds.
 #include <cooperative_groups.h>
 
 #include "pk_common.cuh"
