@@ -9,7 +9,7 @@
 
 #include <mutex>
 
-#include "pk_internal.h"
+#include "pk_grouped.h"
 
 namespace {
 

@@ -3,7 +3,7 @@
 // No entry point allocates memory or synchronises.
 #include <math.h>
 
-#include "pk_internal.h"
+#include "pk_grouped.h"
 
 namespace {
 

@@ -44,7 +44,7 @@
 #include <type_traits>
 
 #include "pk_common.cuh"
-#include "pk_internal.h"
+#include "pk_grouped.h"
 
 namespace pk {
 

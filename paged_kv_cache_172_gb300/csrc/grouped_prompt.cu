@@ -59,8 +59,7 @@
 #include <type_traits>
 
 #include "pk_common.cuh"
-#include "pk_internal.h"
-#include "pk_tcgen05.cuh"
+#include "pk_grouped.h"
 
 namespace pk {
 

@@ -86,11 +86,8 @@ cudaError_t make_map_3d(CUtensorMap* map, const void* base, const unsigned long 
                         bool swizzle128,
                         CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
 
-// 4-D and 5-D tiled tensor maps over 16-bit data (same conventions, strides of dims 1 and
-// up in bytes, in any order).
-cudaError_t make_map_4d(CUtensorMap* map, const void* base, const unsigned long long dims[4],
-                        const unsigned long long strides[3], const unsigned box[4],
-                        bool swizzle128);
+// 5-D tiled tensor map over fp16 data (same conventions, strides of dims 1..4
+// in bytes, in any order).
 cudaError_t make_map_5d(CUtensorMap* map, const void* base, const unsigned long long dims[5],
                         const unsigned long long strides[4], const unsigned box[5],
                         bool swizzle128);
@@ -148,92 +145,5 @@ bool prefill_supported(int D, int block_size);
 size_t prefill_workspace_bytes(int B, int H, int Lq, int D);
 cudaError_t launch_prefill(const PrefillArgs& a, const void* k_cache, const void* v_cache,
                            cudaStream_t stream);
-
-// ---- one serving step with grouped K/V heads --------------------------------
-
-struct StepPlanArgs {
-  const int32_t* cached_lens;
-  const int32_t* new_lens;
-  const int32_t* free_blocks;  // ring of num_blocks ids
-  const int64_t* free_state;   // [2] blocks taken and put so far
-  int32_t* block_tables;
-  int32_t* context_lens;
-  int32_t* q_offsets;
-  int64_t* slot_mapping;
-  int32_t* positions;
-  int64_t* free_state_out;
-  int32_t* status;
-  int B, T_max, bs_log2, num_blocks, max_blocks;
-};
-int step_plan_max_batch();
-cudaError_t launch_step_plan(const StepPlanArgs& a, cudaStream_t stream);
-
-struct RopeArgs {
-  const void* q;  // [T, H, D] and [T, Hkv, D] rows, strides in elements between tokens
-  const void* k;
-  const void* v;
-  long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
-  const int32_t* positions;        // [n_axes, T]
-  const unsigned long long* table;  // [R / 2] turns per position, axis in the low two bits
-  const int64_t* slots;
-  void* q_out;
-  void* k_out;    // may be null
-  void* k_cache;  // both null: rotation only
-  void* v_cache;
-  int32_t* status;
-  long long n_slots;
-  int T, H, Hkv, D, R, n_axes;
-  bool bf16, interleaved;
-};
-cudaError_t launch_rope_write(const RopeArgs& a, cudaStream_t stream);
-
-// Attention of packed new tokens (grouped_prompt.cu): prompts over their own
-// rows (block_tables null) or chunks over the paged cache.
-struct GroupedArgs {
-  const int32_t* q_offsets;     // [B + 1]
-  const int32_t* context_lens;  // [B], paged
-  const int32_t* block_tables;  // [B, max_blocks], paged
-  void* out;                    // [T, H, D]
-  float* ws;                    // parts of split units, split * T * H * (D + 2) floats
-  int32_t* status;
-  int B, T, H, Hkv, G, D;
-  int span;       // tokens of a unit (two tiles)
-  unsigned long long span_magic;  // 2^40 / span, rounded up
-  int g_magic;    // 2^16 / G, rounded up: r * g_magic >> 16 = r / G for r < 128
-  int max_units;  // units of a K/V head, at most
-  int max_tiles;  // key tiles of a unit, at most
-  int split, min_part_tiles;
-  int block_size, num_blocks, max_blocks, max_context;
-  float scale_log2;
-  bool bf16;
-};
-constexpr int kGroupedMinPartTiles = 4;  // key tiles of a part, at least
-constexpr int kGroupedMaxSplit = 32;     // parts of a unit, at most
-int grouped_span(int G);  // tokens of a work unit; 0: unsupported
-int grouped_split(int B, int T, int H, int Hkv, int max_context);
-size_t grouped_workspace_bytes(int B, int T, int H, int Hkv, int D, int max_context);
-cudaError_t launch_grouped(const GroupedArgs& a, const void* q, const void* k, const void* v,
-                           long long q_stride, long long k_stride, long long v_stride,
-                           cudaStream_t stream);
-
-// Grouped decode (grouped_decode.cu): one query token per sequence.
-struct GroupedDecodeArgs {
-  const void* q;  // [B, H, D]
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  void* out;
-  float* ws_o;   // [B, H, num_parts, D] unnormalised outputs of the parts
-  float* ws_ml;  // [B, H, num_parts, 2] their (max, normaliser), log2 domain
-  int32_t* status;
-  int B, H, Hkv, G, D, block_size, num_blocks, max_blocks, max_context;
-  int part_tokens, num_parts;
-  float scale_log2;
-  bool bf16;
-};
-int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context);
-// Whether that many partitions merge inside the launch, without a workspace.
-bool grouped_decode_in_cluster(int B, int H, int Hkv, long long parts);
-cudaError_t launch_grouped_decode(const GroupedDecodeArgs& a, const void* k_cache,
-                                  const void* v_cache, cudaStream_t stream);
 
 }  // namespace pk

@@ -27,7 +27,7 @@
 #include <cuda_bf16.h>
 
 #include "pk_common.cuh"
-#include "pk_internal.h"
+#include "pk_grouped.h"
 
 namespace pk {
 

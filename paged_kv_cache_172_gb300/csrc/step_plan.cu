@@ -25,7 +25,7 @@
 #include <cooperative_groups.h>
 
 #include "pk_common.cuh"
-#include "pk_internal.h"
+#include "pk_grouped.h"
 
 namespace pk {
 
