@@ -2,7 +2,8 @@
 
 Each ``csrc/*.cu`` is compiled in parallel with nvcc for
 ``-gencode arch=compute_103a,code=sm_103a`` and linked with a static CUDA
-runtime into ``paged_kv_cache_172_gb300/libpagedkv.so``.  Objects go to
+runtime into ``paged_kv_cache_172_gb300/libpagedkv.so``, and ``csrc/py_grouped.cpp``
+with g++ into ``_grouped.so`` beside it.  Objects go to
 ``paged_kv_cache_172_gb300/_build/``.  Rebuilds only what changed.
 """
 import glob
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
+BINDING = os.path.join(PKG, "_grouped.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-I", INCLUDE, "-I", CSRC]
@@ -49,11 +52,52 @@ def _compile(src, extra, obj_dir):
     return obj, r.stderr if "warning" in r.stderr.lower() else None
 
 
+def _torch_dir():
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_binding(obj_dir):
+    """The Python binding of the grouped-head calls: host C++ against torch's and
+    Python's headers."""
+    src = os.path.join(CSRC, "py_grouped.cpp")
+    obj = os.path.join(obj_dir, "py_grouped.o")
+    if (os.path.exists(obj) and os.path.getmtime(obj) >= os.path.getmtime(src)
+            and os.path.getmtime(obj) >= _headers_mtime()):
+        return obj, None
+    tdir = os.path.join(_torch_dir(), "include")
+    system = [tdir, os.path.join(tdir, "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"],
+              os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE,
+           *(x for d in system for x in ("-isystem", d)), "-c", src, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        return obj, f"error: $ {' '.join(cmd)}\n{r.stdout}\n{r.stderr}"
+    return obj, None
+
+
+def _link_binding(obj, lib):
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(obj),
+                                                                    os.path.getmtime(lib)):
+        return
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, "-L",
+           os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-L", PKG, "-l:" + os.path.basename(lib), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n$ {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, extra_flags=(), out=None, sources=None) -> str:
-    """Compile and link.  ``extra_flags`` (e.g. -D tuning macros) build a
-    variant with its own object directory; ``out`` names its library path;
-    ``sources`` (file names in csrc/) limits a variant to those files."""
+    """Compile and link the library, and the binding of its grouped-head calls.
+    ``extra_flags`` (e.g. -D tuning macros) build a variant with its own object
+    directory; ``out`` names its library path; ``sources`` (file names in csrc/)
+    limits a variant to those files; a variant has no binding."""
     extra_flags = tuple(extra_flags)
+    product = not extra_flags and out is None and sources is None
     lib = out or LIB
     obj_dir = OBJ_DIR
     if extra_flags:
@@ -64,9 +108,15 @@ def build(verbose: bool = False, extra_flags=(), out=None, sources=None) -> str:
         srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     else:
         srcs = [os.path.join(CSRC, s) for s in sources]
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    binding = None
+    with ThreadPoolExecutor(max_workers=min(os.cpu_count() or 8, len(srcs) + 1)) as ex:
+        if product:
+            binding = ex.submit(_compile_binding, obj_dir)
         results = list(ex.map(lambda s: _compile(s, list(extra_flags), obj_dir), srcs))
-    errors = [msg for _, msg in results if msg and "error" in msg.lower()]
+    if binding is not None:
+        binding = binding.result()
+    errors = [msg for _, msg in results + ([binding] if binding else [])
+              if msg and "error" in msg.lower()]
     if errors:
         raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
     if verbose:
@@ -76,6 +126,8 @@ def build(verbose: bool = False, extra_flags=(), out=None, sources=None) -> str:
     objs = [o for o, _ in results]
     if (os.path.exists(lib)
             and all(os.path.getmtime(lib) >= os.path.getmtime(o) for o in objs)):
+        if binding is not None:
+            _link_binding(binding[0], lib)
         return lib
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -83,6 +135,8 @@ def build(verbose: bool = False, extra_flags=(), out=None, sources=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n$ {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    if binding is not None:
+        _link_binding(binding[0], lib)
     return lib
 
 

@@ -20,8 +20,8 @@
 // be updated in place.  The work is a few hundred kilobytes at most: the call
 // is bound by its launch and by two trips to memory (lengths, then ring
 // entries), and one launch instead of a scan and a fill is what counts.
-// Measured (GB300): 38 single tokens 3.8 us, 200 sequences with 11,000 new tokens
-// 5.9 us, of which the launch of an empty kernel is about two thirds.
+// Measured (GB300): 64 sequences with a token each 3.5 us, 200 sequences with 11,000
+// new tokens 5.8 us, of which the launch of an empty kernel is about two thirds.
 #include <cooperative_groups.h>
 
 #include "pk_common.cuh"
@@ -31,7 +31,6 @@ namespace pk {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr unsigned kFullMask = 0xffffffffu;
 
 // Two running sums carried together: new tokens and fresh blocks.
@@ -55,6 +54,7 @@ __device__ __forceinline__ int owner(const int32_t* sums, int B, int x) {
   return lo;
 }
 
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanArgs a) {
   extern __shared__ int32_t plan_smem[];
   int32_t* s_tok = plan_smem;              // [B + 1] prefix sums of the new tokens
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
   const long long held =
       (head >= 0 && tail >= head && tail - head <= a.num_blocks) ? tail - head : 0;
 
-  // ---- both prefix sums, 1024 sequences a round
+  // ---- both prefix sums, kPlanThreads sequences a round
   if (tid == 0) s_total = {0, 0};
   __syncthreads();
   for (int base = 0; base < a.B; base += kPlanThreads) {
@@ -101,13 +101,13 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
     const Pair carried = s_total;
     __syncthreads();
     if (warp == 0) {
-      Pair w = s_warp[lane];
+      Pair w = lane < kPlanThreads / 32 ? s_warp[lane] : Pair{0, 0};
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const Pair y = {__shfl_up_sync(kFullMask, w.tok, d), __shfl_up_sync(kFullMask, w.blk, d)};
         if (lane >= d) w = add(w, y);
       }
-      s_warp[lane] = w;
+      if (lane < kPlanThreads / 32) s_warp[lane] = w;
     }
     __syncthreads();
     Pair before = add(carried, {x.tok - v.tok, x.blk - v.blk});
@@ -196,16 +196,14 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
 
 int step_plan_max_batch() { return 16384; }
 
-cudaError_t launch_step_plan(const StepPlanArgs& a, cudaStream_t stream) {
+template <int kPlanThreads>
+static cudaError_t launch_t(const StepPlanArgs& a, int ranks, cudaStream_t stream) {
   const int smem = 2 * (a.B + 1) * (int)sizeof(int32_t);
   if (smem > 40 * 1024) {
-    const cudaError_t e =
-        ensure_dynamic_smem<step_plan_kernel>(2 * (step_plan_max_batch() + 1) * 4);
+    const cudaError_t e = ensure_dynamic_smem<step_plan_kernel<kPlanThreads>>(
+        2 * (step_plan_max_batch() + 1) * 4);
     if (e != cudaSuccess) return e;
   }
-  // One CTA while its threads take at most two rounds over the tokens; the
-  // cluster's launch costs more than it saves below that.
-  const int ranks = a.T_max <= 2 * kPlanThreads && a.B <= 2 * kPlanThreads ? 1 : 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);
   cfg.blockDim = dim3(kPlanThreads);
@@ -217,8 +215,21 @@ cudaError_t launch_step_plan(const StepPlanArgs& a, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {(unsigned)ranks, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, step_plan_kernel, a);
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, step_plan_kernel<kPlanThreads>, a);
+}
+
+// Threads and blocks of the cluster, by the sequences and the tokens to place.  Up to 256 of
+// each a block of 256 threads does it in one round, and its barriers cost less than those of
+// 1024 (64 sequences with a token each 3.5 us against 3.9, 200 sequences 3.8 against 4.1; 1000
+// sequences would take 7.0 against 4.8).  Up to 1024 one block of 1024 is as quick as eight
+// (1000 sequences 4.8 against 5.0, one chunk of 500 tokens 3.3 against 3.6), and above that
+// the tokens are what takes the time and eight blocks share them (2304 tokens 4.1 us against
+// 4.8, 16,512 tokens 5.8 against 16.5).
+cudaError_t launch_step_plan(const StepPlanArgs& a, cudaStream_t stream) {
+  const int n = a.T_max > a.B ? a.T_max : a.B;
+  if (n <= 256) return launch_t<256>(a, 1, stream);
+  return launch_t<1024>(a, n <= 1024 ? 1 : 8, stream);
 }
 
 }  // namespace pk

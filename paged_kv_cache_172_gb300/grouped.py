@@ -1,24 +1,22 @@
-"""ctypes binding of a serving step with grouped K/V heads (include/pagedkv.h):
-step plan, rotary cache write, prompt attention, chunk attention and grouped
-decode, on packed tokens in fp16 or bf16.
+"""A serving step with grouped K/V heads (include/pagedkv.h): step plan, rotary
+cache write, prompt attention, chunk attention and grouped decode, on packed
+tokens in fp16 or bf16.
 
 Argument marshalling only, as in ``_lib``: every step runs in the library's
 CUDA kernels.  The kernels of a single-token step take 2 to 6 us, less than
-a call's argument checks written out one by one (about 20 us of host time), so
-each call tests all its arguments in one expression and looks for the one to
-complain about only when that fails.
+checking and passing ten to seventeen tensors from Python (7 to 9 us), so these
+calls go through a compiled binding (``csrc/py_grouped.cpp``) that checks the
+arguments and makes the call; the functions here allocate what was left out and
+say which argument did not fit.
 """
 from typing import NamedTuple
 
 import torch
 
-from ._lib import _check, _ptr, lib
+from ._lib import PA_ERR_WORKSPACE, _check, _ptr, lib
 
-_DTYPE = {torch.float16: 0, torch.bfloat16: 1}  # pa_dtype
-# The current stream's handle without a torch.cuda.Stream object around it, and
-# the current device (tensors on one exist: CUDA is initialised).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_HALF = (torch.float16, torch.bfloat16)
+_UNFIT = -1  # the binding found an argument that does not fit
 
 
 class StepPlan(NamedTuple):
@@ -38,22 +36,30 @@ class StepPlan(NamedTuple):
                    new(2, torch.int64))
 
 
-def _run(fn, name, dev, stream, *args):
-    """Calls the library with the tensors' device current (its launches go to the
-    current device) on ``stream`` or that device's current stream."""
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError(f"{name}: stream on {stream.device}, tensors on cuda:{dev}")
-        handle = stream.cuda_stream
-    else:
-        handle = _raw_stream(dev)
-    if dev == _current_device():
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, handle)
-    if rc:
-        _check(rc, name)
+_grouped = None
+
+
+def _binding():
+    """The compiled binding; raises if the library has not been built."""
+    global _grouped
+    if _grouped is None:
+        lib()
+        try:
+            from . import _grouped as module
+        except ImportError as e:
+            raise RuntimeError("the grouped binding is not built: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        _grouped = module
+    return _grouped
+
+
+def _handle(name, stream, tensor):
+    """What the binding takes for a stream: its handle, or None for the current one."""
+    if stream is None:
+        return None
+    if isinstance(tensor, torch.Tensor) and stream.device != tensor.device:
+        raise ValueError(f"{name}: stream on {stream.device}, tensors on {tensor.device}")
+    return stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -65,70 +71,39 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _dense(t, dtype, shape, dev):
-    """Whether t is a contiguous tensor of that type and shape on device dev."""
-    return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == dev)
-
-
-def _rows(t, dtype, shape, dev):
-    """Whether t is [T, heads, D] on device dev with a token's heads contiguous."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        return False
-    st = t.stride()
-    return st[2] == 1 and (st[1] == shape[2] or shape[1] == 1)
-
-
-def _stride(t):
-    """Distance between tokens in elements (any for a single token)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _status_ok(status, dev):
-    return status is None or (status.dtype is torch.int32 and status.get_device() == dev)
-
-
-def _misshaped(name, *tensors):
-    """The error behind sizes that could not be read off: (name, tensor, dims)."""
-    for what, t, dims in tensors:
-        if not isinstance(t, torch.Tensor):
-            return TypeError(f"{name}: {what} must be a torch.Tensor")
-        if t.dim() != dims:
-            return ValueError(f"{name}: {what} must have {dims} dims, got {list(t.shape)}")
-    return ValueError(f"{name}: bad shapes")
-
-
-def _complain(name, dev, dense, rows=(), status=None):
-    """Raises the error of the first argument that a call's test found wrong.
-    dense, rows: (name, tensor or None, dtype, shape)."""
-    for strided, group in ((False, dense), (True, rows)):
+def _failed(rc, name, q, dense, strided=(), status=None):
+    """Raises the error behind a call's return code.  dense, strided: (name, tensor,
+    dtype or None for q's, shape; None: any size) of the arguments in order; q:
+    the tensor that the others go by, first of its list."""
+    if rc != _UNFIT:
+        _check(rc, name)
+    for is_strided, group in ((True, strided), (False, dense)):
         for what, t, dtype, shape in group:
-            if t is None:
-                continue
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name}: {what} must be a torch.Tensor")
-            if t.dtype != dtype:
-                raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
+            if dtype is None and q.dtype not in _HALF:
+                raise TypeError(f"{name}: {what} must be fp16 or bf16, got {q.dtype}")
+            if t.dtype != (dtype or q.dtype):
+                raise TypeError(f"{name}: {what} must be {dtype or q.dtype}, got {t.dtype}")
             if not t.is_cuda:
                 raise ValueError(f"{name}: {what} must be on a CUDA device")
-            if t.get_device() != dev:
-                raise ValueError(f"{name}: {what} is on {t.device}, others on cuda:{dev}")
-            if tuple(t.shape) != tuple(shape):
-                raise ValueError(f"{name}: {what} must be {list(shape)}, got {list(t.shape)}")
-            if not strided and not t.is_contiguous():
+            if t.device != q.device:
+                raise ValueError(f"{name}: {what} is on {t.device}, others on {q.device}")
+            if t.dim() != len(shape) or any(n not in (None, m) for n, m in zip(shape, t.shape)):
+                raise ValueError(f"{name}: {what} must be {list(shape)} (None: any), got "
+                                 f"{list(t.shape)}")
+            if not is_strided and not t.is_contiguous():
                 raise ValueError(f"{name}: {what} must be contiguous")
-            if strided and not _rows(t, dtype, shape, dev):
+            if is_strided and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
                 raise ValueError(f"{name}: a token's heads must be contiguous in {what}")
-    if not _status_ok(status, dev):
+    if status is not None and (status.dtype != torch.int32 or status.device != q.device):
         raise TypeError(f"{name}: status must be int32 on the tensors' device")
     raise ValueError(f"{name}: bad arguments")
 
 
-def _float16(name, q):
-    """pa_dtype of q, the tensor that sets a call's type."""
-    if q.dtype not in _DTYPE:
-        raise TypeError(f"{name}: q must be fp16 or bf16, got {q.dtype}")
-    return _DTYPE[q.dtype]
+def _size(t, dim):
+    """A size that other arguments go by, None where there is none to read."""
+    return t.shape[dim] if isinstance(t, torch.Tensor) and t.dim() > dim else None
 
 
 def pa_step_plan(cached_lens, new_lens, block_tables, free_blocks, free_state, block_size,
@@ -143,38 +118,26 @@ def pa_step_plan(cached_lens, new_lens, block_tables, free_blocks, free_state, b
     slot_mapping and positions [max_tokens] (-1 and 0 behind the last token) and
     the new free_state (out's may be the one passed in).  A step that does not fit
     the ring (PA_DEV_NO_BLOCKS) or max_tokens (PA_DEV_BAD_CONTEXT) plans nothing."""
-    i32, i64 = torch.int32, torch.int64
-    try:
-        (B,), (_, M), (NB,), T = (cached_lens.shape, block_tables.shape, free_blocks.shape,
-                                  int(max_tokens))
-    except (AttributeError, ValueError):
-        raise _misshaped("pa_step_plan", ("cached_lens", cached_lens, 1),
-                         ("block_tables", block_tables, 2),
-                         ("free_blocks", free_blocks, 1)) from None
-    dev = cached_lens.get_device()
+    name = "pa_step_plan"
     if out is None:
+        if not isinstance(cached_lens, torch.Tensor):
+            raise TypeError(f"{name}: cached_lens must be a torch.Tensor")
         with torch.cuda.stream(stream):  # (None: the current one)
-            out = StepPlan.empty(B, T, cached_lens.device)
-    ctx, offs, slots, pos, state = out
-    one = (B,)
-    if not (dev >= 0 and _dense(cached_lens, i32, one, dev) and _dense(new_lens, i32, one, dev)
-            and _dense(block_tables, i32, (B, M), dev) and _dense(free_blocks, i32, (NB,), dev)
-            and _dense(free_state, i64, (2,), dev) and _dense(ctx, i32, one, dev)
-            and _dense(offs, i32, (B + 1,), dev) and _dense(slots, i64, (T,), dev)
-            and _dense(pos, i32, (T,), dev) and _dense(state, i64, (2,), dev)
-            and _status_ok(status, dev)):
-        _complain("pa_step_plan", dev,
-                  (("cached_lens", cached_lens, i32, one), ("new_lens", new_lens, i32, one),
-                   ("block_tables", block_tables, i32, (B, M)),
-                   ("free_blocks", free_blocks, i32, (NB,)), ("free_state", free_state, i64, (2,)),
-                   ("out.context_lens", ctx, i32, one), ("out.q_offsets", offs, i32, (B + 1,)),
-                   ("out.slot_mapping", slots, i64, (T,)), ("out.positions", pos, i32, (T,)),
-                   ("out.free_state", state, i64, (2,))), status=status)
-    _run(lib().pa_step_plan, "pa_step_plan", dev, stream, cached_lens.data_ptr(),
-         new_lens.data_ptr(), B, int(block_size), NB, M, T, free_blocks.data_ptr(),
-         free_state.data_ptr(), block_tables.data_ptr(), ctx.data_ptr(), offs.data_ptr(),
-         slots.data_ptr(), pos.data_ptr(), state.data_ptr(),
-         None if status is None else status.data_ptr())
+            out = StepPlan.empty(cached_lens.numel(), int(max_tokens), cached_lens.device)
+    rc = _binding().step_plan(cached_lens, new_lens, block_tables, free_blocks, free_state, *out,
+                              status, block_size, max_tokens, _handle(name, stream, free_state))
+    if rc:
+        i32, i64, B = torch.int32, torch.int64, _size(cached_lens, 0)
+        _failed(rc, name, cached_lens,
+                (("cached_lens", cached_lens, i32, (None,)), ("new_lens", new_lens, i32, (B,)),
+                 ("block_tables", block_tables, i32, (B, None)),
+                 ("free_blocks", free_blocks, i32, (None,)),
+                 ("free_state", free_state, i64, (2,)),
+                 ("out.context_lens", out[0], i32, (B,)),
+                 ("out.q_offsets", out[1], i32, (None if B is None else B + 1,)),
+                 ("out.slot_mapping", out[2], i64, (max_tokens,)),
+                 ("out.positions", out[3], i32, (max_tokens,)),
+                 ("out.free_state", out[4], i64, (2,))), status=status)
     return out
 
 
@@ -201,52 +164,34 @@ def pa_rope_cache_write(q, k, v, positions, table, slot_mapping, k_cache=None, v
     (q_out, k_out); q_out is allocated when not given and may be q; k_out, given
     or with no cache allocated, receives the rotated keys and may be k."""
     name = "pa_rope_cache_write"
-    try:
-        (T, H, D), (_, Hkv, _), (n,) = q.shape, k.shape, table.shape
-    except (AttributeError, ValueError):
-        raise _misshaped(name, ("q", q, 3), ("k", k, 3), ("table", table, 1)) from None
-    code, dt, dev = _float16(name, q), q.dtype, q.get_device()
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    pos_shape = (T,) if positions.dim() == 1 else (axes, T)
-    kv, caches = (T, Hkv, D), ()
-    NB = bs = 0
-    if k_cache is not None or v_cache is not None:
-        try:
-            (NB, bs, _, _), (_, _, _) = k_cache.shape, v.shape
-        except (AttributeError, ValueError):
-            raise _misshaped(name, ("k_cache", k_cache, 4), ("v", v, 3)) from None
-        caches = (NB, bs, Hkv, D)
-    else:
+    cache = k_cache is not None or v_cache is not None
+    if q_out is None:
+        if not isinstance(q, torch.Tensor):
+            raise TypeError(f"{name}: q must be a torch.Tensor")
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    if not cache:
         v = slot_mapping = None
         if k_out is None:
-            k_out = _empty(kv, dt, q.device, stream)
-    if q_out is None:
-        q_out = _empty((T, H, D), dt, q.device, stream)
-    if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _rows(k, dt, kv, dev)
-            and _dense(positions, torch.int32, pos_shape, dev)
-            and _dense(table, torch.int64, (n,), dev) and _rows(q_out, dt, (T, H, D), dev)
-            and (k_out is None or _rows(k_out, dt, kv, dev))
-            and (not caches or (_rows(v, dt, kv, dev) and _dense(k_cache, dt, caches, dev)
-                                and v_cache is not None and _dense(v_cache, dt, caches, dev)
-                                and slot_mapping is not None
-                                and _dense(slot_mapping, torch.int64, (T,), dev)))
-            and _status_ok(status, dev)):
-        if caches and (v_cache is None or slot_mapping is None):
-            raise ValueError(f"{name}: the cache write needs k_cache, v_cache and slot_mapping")
-        _complain(name, dev,
-                  (("positions", positions, torch.int32, pos_shape),
-                   ("table", table, torch.int64, (n,)), ("k_cache", k_cache, dt, caches),
-                   ("v_cache", v_cache, dt, caches),
-                   ("slot_mapping", slot_mapping, torch.int64, (T,))),
-                  (("q", q, dt, (T, H, D)), ("k", k, dt, kv), ("v", v, dt, kv),
-                   ("q_out", q_out, dt, (T, H, D)), ("k_out", k_out, dt, kv)), status)
-    _run(lib().pa_rope_cache_write, name, dev, stream, q.data_ptr(), k.data_ptr(),
-         v.data_ptr() if caches else None, positions.data_ptr(), table.data_ptr(),
-         slot_mapping.data_ptr() if caches else None, T, H, Hkv, D, 2 * n, axes,
-         1 if interleaved else 0, code, _stride(q), _stride(k), _stride(v) if caches else 0, bs,
-         NB, q_out.data_ptr(), _stride(q_out), None if k_out is None else k_out.data_ptr(),
-         0 if k_out is None else _stride(k_out), k_cache.data_ptr() if caches else None,
-         v_cache.data_ptr() if caches else None, None if status is None else status.data_ptr())
+            if not isinstance(k, torch.Tensor):
+                raise TypeError(f"{name}: k must be a torch.Tensor")
+            k_out = _empty(k.shape, k.dtype, k.device, stream)
+    rc = _binding().rope_cache_write(q, k, v, positions, table, slot_mapping, k_cache, v_cache,
+                                     q_out, k_out, status, interleaved, _handle(name, stream, q))
+    if rc:
+        T, D, Hkv = _size(q, 0), _size(q, 2), _size(k, 1)
+        one = isinstance(positions, torch.Tensor) and positions.dim() == 1
+        dense = [("positions", positions, torch.int32, (T,) if one else (None, T)),
+                 ("table", table, torch.int64, (None,))]
+        strided = [("q", q, None, (None, None, None)), ("k", k, None, (T, None, D)),
+                   ("q_out", q_out, None, (T, _size(q, 1), D))]
+        if k_out is not None:
+            strided.append(("k_out", k_out, None, (T, Hkv, D)))
+        if cache:
+            pool = (_size(k_cache, 0), _size(k_cache, 1), Hkv, D)
+            strided.append(("v", v, None, (T, Hkv, D)))
+            dense += [("k_cache", k_cache, None, pool), ("v_cache", v_cache, None, pool),
+                      ("slot_mapping", slot_mapping, torch.int64, (T,))]
+        _failed(rc, name, q, dense, strided, status)
     return q_out, k_out
 
 
@@ -257,43 +202,26 @@ def pa_prompt_attention(q, k, v, q_offsets, scale, out=None, status=None, stream
     [T,H,D]; rows outside the sequences are left as they were (undefined when
     ``out`` is allocated here)."""
     name = "pa_prompt_attention"
-    try:
-        (T, H, D), (_, Hkv, _), (_, _, _), (n,) = q.shape, k.shape, v.shape, q_offsets.shape
-    except (AttributeError, ValueError):
-        raise _misshaped(name, ("q", q, 3), ("k", k, 3), ("v", v, 3),
-                         ("q_offsets", q_offsets, 1)) from None
-    code, dt, dev = _float16(name, q), q.dtype, q.get_device()
     if out is None:
-        out = _empty((T, H, D), dt, q.device, stream)
-    if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _rows(k, dt, (T, Hkv, D), dev)
-            and _rows(v, dt, (T, Hkv, D), dev) and _dense(q_offsets, torch.int32, (n,), dev)
-            and _dense(out, dt, (T, H, D), dev) and _status_ok(status, dev)):
-        _complain(name, dev, (("q_offsets", q_offsets, torch.int32, (n,)),
-                              ("out", out, dt, (T, H, D))),
-                  (("q", q, dt, (T, H, D)), ("k", k, dt, (T, Hkv, D)),
-                   ("v", v, dt, (T, Hkv, D))), status)
-    _run(lib().pa_prompt_attention, name, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-         q_offsets.data_ptr(), n - 1, T, H, Hkv, D, code, _stride(q), _stride(k), _stride(v),
-         scale, out.data_ptr(), None if status is None else status.data_ptr())
+        if not isinstance(q, torch.Tensor):
+            raise TypeError(f"{name}: q must be a torch.Tensor")
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    rc = _binding().prompt_attention(q, k, v, q_offsets, out, status, scale,
+                                     _handle(name, stream, q))
+    if rc:
+        T, H, D, Hkv = _size(q, 0), _size(q, 1), _size(q, 2), _size(k, 1)
+        _failed(rc, name, q, (("q_offsets", q_offsets, torch.int32, (None,)),
+                              ("out", out, None, (T, H, D))),
+                (("q", q, None, (None, None, None)), ("k", k, None, (T, None, D)),
+                 ("v", v, None, (T, Hkv, D))), status)
     return out
 
 
-def _workspace(name, workspace, nbytes, dev, stream):
-    """(address, bytes, owner) of the given workspace, or of a new one of nbytes."""
-    if workspace is None:
-        if nbytes == 0:
-            return None, 0, None
-        workspace = _empty(nbytes, torch.uint8, f"cuda:{dev}", stream)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"{name}: workspace must be contiguous and on cuda:{dev}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _sized(fn, dev, *args):
+def _sized(fn, device, *args):
     """A workspace size, which depends on the device, with that device current."""
-    if dev == _current_device():
+    if device.index == torch.cuda.current_device():
         return fn(*args)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(device):
         return fn(*args)
 
 
@@ -313,37 +241,44 @@ def pa_chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offset
     allocated when not given; split=False passes none.  Returns ``out``
     [T,H,D]; rows outside the sequences are left as they were."""
     name = "pa_chunk_attention"
-    try:
-        (T, H, D), (NB, bs, Hkv, _), (_, M), (n,) = (q.shape, k_cache.shape, block_tables.shape,
-                                                     q_offsets.shape)
-    except (AttributeError, ValueError):
-        raise _misshaped(name, ("q", q, 3), ("k_cache", k_cache, 4),
-                         ("block_tables", block_tables, 2), ("q_offsets", q_offsets, 1)) from None
-    code, dt, dev = _float16(name, q), q.dtype, q.get_device()
-    B, pool = n - 1, (NB, bs, Hkv, D)
-    cap = M * bs if max_context_len is None else int(max_context_len)
+    if not isinstance(q, torch.Tensor):
+        raise TypeError(f"{name}: q must be a torch.Tensor")
+    if max_context_len is None:
+        max_context_len = (_size(block_tables, 1) or 0) * (_size(k_cache, 1) or 0)
     if out is None:
-        out = _empty((T, H, D), dt, q.device, stream)
-    if not (dev >= 0 and _rows(q, dt, (T, H, D), dev) and _dense(k_cache, dt, pool, dev)
-            and _dense(v_cache, dt, pool, dev) and _dense(block_tables, torch.int32, (B, M), dev)
-            and _dense(context_lens, torch.int32, (B,), dev)
-            and _dense(q_offsets, torch.int32, (n,), dev) and _dense(out, dt, (T, H, D), dev)
-            and _status_ok(status, dev)):
-        _complain(name, dev, (("k_cache", k_cache, dt, pool), ("v_cache", v_cache, dt, pool),
-                              ("block_tables", block_tables, torch.int32, (B, M)),
-                              ("context_lens", context_lens, torch.int32, (B,)),
-                              ("q_offsets", q_offsets, torch.int32, (n,)),
-                              ("out", out, dt, (T, H, D))), (("q", q, dt, (T, H, D)),), status)
-    ws, ws_bytes = None, 0
-    if split:
-        need = 0 if workspace is not None else _sized(pa_chunk_attention_workspace_size, dev, B,
-                                                      T, H, Hkv, D, cap)
-        ws, ws_bytes, workspace = _workspace(name, workspace, need, dev, stream)
-    _run(lib().pa_chunk_attention, name, dev, stream, q.data_ptr(), k_cache.data_ptr(),
-         v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-         q_offsets.data_ptr(), B, T, H, Hkv, D, code, _stride(q), bs, NB, M, cap, scale,
-         out.data_ptr(), ws, ws_bytes, None if status is None else status.data_ptr())
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    if not split:
+        workspace = None
+    elif workspace is None and q.is_cuda and q.dim() == 3 and q.shape[0] > 0:
+        need = _sized(pa_chunk_attention_workspace_size, q.device, (_size(q_offsets, 0) or 1) - 1,
+                      q.shape[0], q.shape[1], _size(k_cache, 2) or 0, q.shape[2],
+                      max_context_len)
+        if need:
+            workspace = _empty(need, torch.uint8, q.device, stream)
+    rc = _binding().chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offsets,
+                                    out, workspace, status, max_context_len, scale,
+                                    _handle(name, stream, q))
+    if rc:
+        B = None if _size(q_offsets, 0) is None else q_offsets.shape[0] - 1
+        _failed(rc, name, q,
+                (("q_offsets", q_offsets, torch.int32, (None,)),
+                 *_cache_args(q, k_cache, v_cache, block_tables, context_lens, B),
+                 ("out", out, None, tuple(q.shape)), *_workspace_arg(workspace)),
+                (("q", q, None, (None, None, None)),), status)
     return out
+
+
+def _cache_args(q, k_cache, v_cache, block_tables, context_lens, B):
+    pool = (_size(k_cache, 0), _size(k_cache, 1), _size(k_cache, 2), _size(q, 2))
+    return (("k_cache", k_cache, None, pool), ("v_cache", v_cache, None, pool),
+            ("block_tables", block_tables, torch.int32, (B, None)),
+            ("context_lens", context_lens, torch.int32, (B,)))
+
+
+def _workspace_arg(workspace):
+    if workspace is None:
+        return ()
+    return (("workspace", workspace, workspace.dtype, tuple(workspace.shape)),)
 
 
 def pa_decode_grouped_workspace_size(B, H, Hkv, D, block_size, max_context_len,
@@ -359,29 +294,25 @@ def pa_decode_grouped(q, k_cache, v_cache, block_tables, context_lens, scale, ma
     [NB,bs,Hkv,D] of the same type, ``max_context_len`` a host-side bound on
     context_lens.  Returns ``out`` [B,H,D]."""
     name = "pa_decode_grouped"
-    try:
-        (B, H, D), (NB, bs, Hkv, _), (_, M) = q.shape, k_cache.shape, block_tables.shape
-    except (AttributeError, ValueError):
-        raise _misshaped(name, ("q", q, 3), ("k_cache", k_cache, 4),
-                         ("block_tables", block_tables, 2)) from None
-    code, dt, dev = _float16(name, q), q.dtype, q.get_device()
-    pool, cap = (NB, bs, Hkv, D), int(max_context_len)
     if out is None:
-        out = _empty((B, H, D), dt, q.device, stream)
-    if not (dev >= 0 and _dense(q, dt, (B, H, D), dev) and _dense(k_cache, dt, pool, dev)
-            and _dense(v_cache, dt, pool, dev) and _dense(block_tables, torch.int32, (B, M), dev)
-            and _dense(context_lens, torch.int32, (B,), dev) and _dense(out, dt, (B, H, D), dev)
-            and _status_ok(status, dev)):
-        _complain(name, dev, (("q", q, dt, (B, H, D)), ("k_cache", k_cache, dt, pool),
-                              ("v_cache", v_cache, dt, pool),
-                              ("block_tables", block_tables, torch.int32, (B, M)),
-                              ("context_lens", context_lens, torch.int32, (B,)),
-                              ("out", out, dt, (B, H, D))), (), status)
-    need = 0 if workspace is not None else _sized(pa_decode_grouped_workspace_size, dev, B, H,
-                                                  Hkv, D, bs, cap, partition_tokens)
-    ws, ws_bytes, workspace = _workspace(name, workspace, need, dev, stream)
-    _run(lib().pa_decode_grouped, name, dev, stream, q.data_ptr(), k_cache.data_ptr(),
-         v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), B, H, Hkv, D, code,
-         bs, NB, M, cap, partition_tokens, scale, out.data_ptr(), ws, ws_bytes,
-         None if status is None else status.data_ptr())
+        if not isinstance(q, torch.Tensor):
+            raise TypeError(f"{name}: q must be a torch.Tensor")
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    handle = _handle(name, stream, q)
+    call = _binding().decode_grouped
+    rc = call(q, k_cache, v_cache, block_tables, context_lens, out, workspace, status,
+              max_context_len, partition_tokens, scale, handle)
+    if rc == PA_ERR_WORKSPACE and workspace is None:  # (most plans need none)
+        need = _sized(pa_decode_grouped_workspace_size, q.device, q.shape[0], q.shape[1],
+                      k_cache.shape[2], q.shape[2], k_cache.shape[1], max_context_len,
+                      partition_tokens)
+        workspace = _empty(need, torch.uint8, q.device, stream)
+        rc = call(q, k_cache, v_cache, block_tables, context_lens, out, workspace, status,
+                  max_context_len, partition_tokens, scale, handle)
+    if rc:
+        _failed(rc, name, q,
+                (("q", q, None, (None, None, None)),
+                 *_cache_args(q, k_cache, v_cache, block_tables, context_lens, _size(q, 0)),
+                 ("out", out, None, tuple(_size(q, i) for i in range(3))),
+                 *_workspace_arg(workspace)), (), status)
     return out
