@@ -464,8 +464,8 @@ pa_status pa_block_copy(pa_half *k_cache, pa_half *v_cache,
  * The free list is a ring: free_blocks [num_blocks] int32, free_state [2]
  * int64 = blocks taken and blocks put so far, so it holds free_state[1] -
  * free_state[0] blocks, the next one at index free_state[0] mod num_blocks.
- * free_state_out [2] receives the state after the step and may be free_state
- * itself; a caller returns a block by writing its id at free_state[1] mod
+ * context_lens may be cached_lens itself.  free_state_out [2] receives the
+ * state after the step and may be free_state itself; a caller returns a block by writing its id at free_state[1] mod
  * num_blocks and adding one to free_state[1].
  *
  * All or nothing: when the blocks needed exceed those held
@@ -478,7 +478,7 @@ pa_status pa_block_copy(pa_half *k_cache, pa_half *v_cache,
  * fresh entry -1).
  *
  * block_size in {4, 8, 16, 32}; B at most 16384 (else PA_ERR_UNSUPPORTED);
- * max_blocks_per_seq * block_size below 2^31 - 64.
+ * max_blocks_per_seq * block_size below 2^31 - 64, T_max below 2^31 - 32768.
  * ------------------------------------------------------------------------- */
 pa_status pa_step_plan(const int32_t *cached_lens, const int32_t *new_lens, int B,
                        int block_size, int num_blocks, int max_blocks_per_seq, int T_max,
@@ -502,8 +502,8 @@ pa_status pa_step_plan(const int32_t *cached_lens, const int32_t *new_lens, int 
  * Rotated q goes to q_out, rotated k to k_out unless that is NULL, and to
  * k_cache at slot_mapping[t]; v is copied to v_cache there.  Negative slots
  * skip the cache write (q_out and k_out are still written); a slot past the
- * pool is flagged PA_DEV_BAD_SLOT and skipped; two tokens with the same slot:
- * undefined which one lands.  k_cache, v_cache, v and slot_mapping may all be
+ * pool is flagged PA_DEV_BAD_SLOT and skipped; what a slot
+ * that two tokens share receives is undefined.  k_cache, v_cache, v and slot_mapping may all be
  * NULL: rotation only, k_out is then required.  q_out may be q and k_out may
  * be k (the same pointer and stride), no other overlap is allowed.
  *
@@ -562,12 +562,12 @@ pa_status pa_prompt_attention(const void *q, const void *k, const void *v,
  * positions: query i is at n - q_len + i, n = context_lens[b], and attends to
  * keys 0 .. n - q_len + i of the cache (which holds the chunk's own K/V
  * already).  Otherwise as pa_prompt_attention; the cache as in pa_decode with
- * Hkv heads.  Slots past a sequence's length may hold anything.  A context outside [q_len, min(max_context_len,
- * max_blocks_per_seq * block_size)] is flagged PA_DEV_BAD_CONTEXT and its rows
+ * Hkv heads.  Slots past a sequence's length may hold anything.  A context
+ * outside [q_len, max_context_len] is flagged PA_DEV_BAD_CONTEXT and its rows
  * are zeros; a bad block id reads as zeros, flagged PA_DEV_BAD_BLOCK_ID.
  *
  * D in {64, 128}; block_size in {8, 16, 32}; max_context_len at most
- * max_blocks_per_seq * block_size; (num_blocks + 1) * block_size * Hkv below
+ * max_blocks_per_seq * block_size and below 2^31 - 32768; (num_blocks + 1) * block_size * Hkv below
  * 2^31.  workspace (16-byte aligned, may be NULL): with at least
  * pa_chunk_attention_workspace_size(...) bytes, few and long chunks are cut
  * into key ranges merged by log-sum-exp, which fills the GPU; without it every

@@ -25,6 +25,10 @@ bool rows_ok(const void* p, int64_t stride, int heads, int D) {
          stride < (1LL << 36);
 }
 
+// Tokens of a call or of a context: the kernels round them up to tiles and step
+// past them by their threads in 32 bits.
+constexpr int kMaxCount = INT32_MAX - 32768;
+
 int log2_block(int bs) { return bs == 4 ? 2 : bs == 8 ? 3 : bs == 16 ? 4 : bs == 32 ? 5 : -1; }
 
 bool pool_ok(int num_blocks, int block_size, int Hkv) {
@@ -43,6 +47,7 @@ pa_status pa_step_plan(const int32_t* cached_lens, const int32_t* new_lens, int 
                        int64_t* slot_mapping, int32_t* positions, int64_t* free_state_out,
                        int32_t* status, pa_stream_t stream) {
   if (B < 0 || T_max < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0) return PA_ERR_INVALID;
+  if (T_max > kMaxCount) return PA_ERR_INVALID;
   const int lg = log2_block(block_size);
   if (lg < 0 || B > pk::step_plan_max_batch()) return PA_ERR_UNSUPPORTED;
   if ((long long)max_blocks_per_seq * block_size >= (1LL << 31) - 64) return PA_ERR_INVALID;
@@ -159,7 +164,8 @@ static pa_status cache_args(const void* k_cache, const void* v_cache, const int3
                             int max_blocks, int max_context) {
   if (!k_cache || !v_cache || !block_tables || !context_lens || !aligned16(k_cache) ||
       !aligned16(v_cache) || !pool_ok(num_blocks, block_size, Hkv) || max_blocks <= 0 ||
-      max_context < 0 || (long long)max_context > (long long)max_blocks * block_size)
+      max_context < 0 || max_context > kMaxCount ||
+      (long long)max_context > (long long)max_blocks * block_size)
     return PA_ERR_INVALID;
   return PA_OK;
 }

@@ -311,11 +311,14 @@ __global__ void __launch_bounds__(kThreads)
         mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
-        const float m_new = fmaxf(m[t][e], mx);  // key 0 of a stage is never masked
-        const float alpha = ex2_approx(m[t][e] - m_new);
+        const float m_new = fmaxf(m[t][e], mx);
+        // Scores of -inf alone so far (infinite keys): -inf + inf is NaN, so their
+        // weights, all zero, are taken with maximum 0.
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = ex2_approx(m[t][e] - ref);
         m[t][e] = m_new;
-        p[e] = ex2_approx(s[t][e] - m_new);
-        p[2 + e] = ex2_approx(s[t][2 + e] - m_new);
+        p[e] = ex2_approx(s[t][e] - ref);
+        p[2 + e] = ex2_approx(s[t][2 + e] - ref);
         l[t][e] = l[t][e] * alpha + (p[e] + p[2 + e]);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {

@@ -16,8 +16,8 @@
 // memory, so no CTA waits for another before it can place its share of the
 // tokens and of the fresh table entries by binary search; a token in a fresh
 // block takes the id from the ring, not from the table another CTA may still
-// be writing.  The ring's state is written behind a cluster barrier, so it may
-// be updated in place.  The work is a few hundred kilobytes at most: the call
+// be writing.  The ring's state is written behind a cluster barrier, as the
+// lengths are, so both may be updated in place.  The work is a few hundred kilobytes at most: the call
 // is bound by its launch and by two trips to memory (lengths, then ring
 // entries), and one launch instead of a scan and a fill is what counts.
 // Measured (GB300): 64 sequences with a token each 3.5 us, 200 sequences with 11,000
@@ -134,14 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
 
   const int first = rank * kPlanThreads + tid, step = ranks * kPlanThreads;
   // ---- per sequence
-  for (int b = first; b <= a.B; b += step) {
-    a.q_offsets[b] = fits ? s_tok[b] : 0;
-    if (b < a.B) {
-      const long long c = a.cached_lens[b], n = a.new_lens[b];
-      const bool bad = c < 0 || n < 0 || c + n > cap;
-      a.context_lens[b] = bad ? 0 : (int32_t)(fits ? c + n : c);
-    }
-  }
+  for (int b = first; b <= a.B; b += step) a.q_offsets[b] = fits ? s_tok[b] : 0;
   const int h0 = held > 0 ? (int)(head % a.num_blocks) : 0;
   auto ring_id = [&](int i) {  // i-th fresh block of the step; -1 if the entry is bad
     int at = h0 + i;           // h0, i < num_blocks
@@ -181,11 +174,18 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
     a.slot_mapping[t] = slot;
     a.positions[t] = pos;
   }
-  // Every CTA has read the ring's state: it may be replaced, in place too.
+  // Every CTA has read the ring's state and the other sequences' lengths: both may
+  // be replaced, in place too (context_lens over cached_lens, an entry by the one
+  // thread that still reads it).
   if (ranks > 1)
     cluster.sync();
   else
     __syncthreads();
+  for (int b = first; b < a.B; b += step) {
+    const long long c = a.cached_lens[b], n = a.new_lens[b];
+    const bool bad = c < 0 || n < 0 || c + n > cap;
+    a.context_lens[b] = bad ? 0 : (int32_t)(fits ? c + n : c);
+  }
   if (rank == 0 && tid == 0) {
     a.free_state_out[0] = head + fresh;
     a.free_state_out[1] = tail;

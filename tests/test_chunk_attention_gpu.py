@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import paged_kv_cache_172_gb300 as pk
-from grouped_ref import Paged, check
+from grouped_ref import Paged, attend, check
 from pk_testutil import zero_status
 
 pytestmark = pytest.mark.gpu
@@ -187,3 +187,21 @@ def test_refusals():
     with pytest.raises(ValueError):
         pk.pa_chunk_attention(p.q, p.k_cache, p.v_cache, p.tables, p.context[:0], p.offsets,
                               p.scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("gone", [range(0, 128), range(0, 1300), range(512, 3000)])
+def test_infinite_scores_weigh_nothing(dtype, gone):
+    p = Paged([3100, 600], [40, 9], 8, 2, 128, 16, dtype, seed=12)
+    p.q[..., 5] = p.q[..., 5].abs() + 0.5
+    gone = range(gone.start, min(gone.stop, p.ctx[0] - 40))
+    p.keys[0][gone.start:gone.stop, :, 5] = -float("inf")  # whole key tiles and ranges of them
+    p.store(0)
+    kept = torch.tensor([j for j in range(p.ctx[0]) if j not in gone], device=DEV)
+    ref, tol = attend(p.q[p.rows(0)], p.keys[0][kept], p.values[0][kept], p.scale,
+                      len(kept) - 40)
+    for split in (True, False):
+        out, st = run(p, split=split)
+        assert st == 0
+        check(out[p.rows(0)], ref, tol, f"split {split}")
+        check_all(p, out, only=[1])

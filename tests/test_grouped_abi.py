@@ -185,3 +185,10 @@ def test_bindings_reject_cpu_tensors_and_wrong_types():
         pk.pa_prompt_attention(None, q, q, i32, 0.1)
     with pytest.raises(ValueError):
         pk.pa_prompt_attention(q[0], q, q, i32, 0.1)
+
+
+def test_counts_that_32_bits_cannot_step_past_are_refused(lib):
+    for T in (2 ** 31 - 32768, 2 ** 31 - 1):
+        assert plan(lib, T=T) == pk.PA_ERR_INVALID
+        assert chunk(lib, mb=2 ** 27, cap=T) == pk.PA_ERR_INVALID
+        assert decode(lib, mb=2 ** 27, cap=T) == pk.PA_ERR_INVALID

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import paged_kv_cache_172_gb300 as pk
-from grouped_ref import Paged, check
+from grouped_ref import Paged, attend, check
 from pk_testutil import zero_status
 
 pytestmark = pytest.mark.gpu
@@ -178,3 +178,19 @@ def test_refusals():
     empty = pk.pa_decode_grouped(p.q[:0], p.k_cache, p.v_cache, p.tables[:0], p.context[:0], 0.1,
                                  9)
     assert empty.shape[0] == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("gone", [range(0, 16), range(0, 64), range(64, 128), range(16, 300)])
+def test_infinite_scores_weigh_nothing(dtype, gone):
+    p = batch([300, 300], 8, 2, 128, 16, dtype, seed=9)
+    p.q[..., 5] = p.q[..., 5].abs() + 0.5
+    p.keys[0][gone.start:gone.stop, :, 5] = -float("inf")  # scores of -inf, whole stages of them
+    p.store(0)
+    kept = torch.tensor([j for j in range(300) if j not in gone], device=DEV)
+    ref, tol = attend(p.q[:1], p.keys[0][kept], p.values[0][kept], p.scale, len(kept) - 1)
+    for pt in (0, 64, 2048):
+        out, st = run(p, partition_tokens=pt)
+        assert st == 0
+        check(out[:1], ref, tol, f"partition {pt}")
+        check_all(p, out, only=[1])

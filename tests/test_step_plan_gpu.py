@@ -215,3 +215,22 @@ def test_empty_step():
     h = make([5], [0], 16, 1, 4, 0)
     g, p, st = call(h)
     assert st == 0 and p.q_offsets.tolist() == [0, 0] and p.context_lens.tolist() == [5]
+
+
+@pytest.mark.parametrize("B,hi,qhi", [(3, 90, 40), (200, 60, 1), (700, 90, 3), (64, 900, 200),
+                                      (4000, 100, 2)])
+def test_context_lengths_may_replace_the_cached_ones(B, hi, qhi):
+    rng = np.random.default_rng(B)
+    cached, new = rng.integers(0, hi + 1, B), rng.integers(0, qhi + 1, B)
+    M = (hi + qhi + 7) // 8 + 1
+    T = int(new.sum()) + 5
+    h = make(cached, new, 8, M, B * M, T, seed=B)
+    g = {k: torch.from_numpy(np.ascontiguousarray(h[k])).to(DEV) for k in ("bt", "ring", "state")}
+    lens = torch.from_numpy(cached.astype(np.int32)).to(DEV)
+    out = pk.StepPlan.empty(B, T, DEV)._replace(context_lens=lens, free_state=g["state"])
+    status = zero_status(DEV)
+    p = pk.pa_step_plan(lens, torch.from_numpy(new.astype(np.int32)).to(DEV), g["bt"], g["ring"],
+                        g["state"], 8, T, out=out, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    check(h, g, p)
