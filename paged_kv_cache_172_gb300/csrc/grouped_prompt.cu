@@ -660,6 +660,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     // ------------------------------------------------------------ K and V
     reg_dec();
     const int bpt = PAGED ? kTile / a.block_size : 1;  // blocks of a key tile
+    const int bbytes = C::TILE_BYTES / bpt;
     int u = 0;  // ring index, over all items
     Item it;
     for (int k = 0; take(k, it); ++k) {
@@ -687,7 +688,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
               flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
               phys = a.num_blocks;
             }
-            tbl[lane + 32 * e] = phys;
+            tbl[lane + 32 * e] = phys * a.block_size * a.Hkv + it.hkv;  // the box's row
           }
           __syncwarp();
         }
@@ -702,9 +703,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         if constexpr (PAGED) {
           // One box per block, from lane to lane: (64 dims, 8 keys, halves, key
           // groups) at row (block * block_size * Hkv + head) of the pool.
-          for (int i = lane; i < bpt; i += 32)
-            tma_load_5d(dst + i * (a.block_size / 8) * C::GROUP, v ? &vmap : &kmap, 0, 0, 0, 0,
-                        tbl[lb0 - win + i] * a.block_size * a.Hkv + it.hkv, &kv_full[st]);
+          if (lane < bpt)
+            tma_load_5d(dst + lane * bbytes, v ? &vmap : &kmap, 0, 0, 0, 0, tbl[lb0 - win + lane],
+                        &kv_full[st]);
         } else if (lane == 0) {
           // 128 tokens of one head, both halves; rows past the array read as zeros.
           tma_load_4d(dst, v ? &vmap : &kmap, 0, row + (it.kt0 + t) * kTile, 0, it.hkv,
@@ -712,10 +713,22 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         }
         issued = ++u;
       };
-      if (it.n_kv > 0) load_tile(0, false);
-      for (int j = 0; j < it.n_kv && ok; ++j) {
-        if (j + 1 < it.n_kv) load_tile(j + 1, false);
-        if (ok) load_tile(j, true);
+      // K_0, then K_{t+1} and V_t in turn (see ring_k).
+      if constexpr (PAGED) {
+        // One copy of the code: three took half of the warp's time in missed
+        // instructions, and of the softmax's with it (16 x 2,048 keys 517 -> 474 us).
+#pragma unroll 1
+        for (int i = 0; i < 2 * it.n_kv && ok; ++i) {
+          const int half = (i + 1) >> 1;
+          const bool v = i > 0 && (!(i & 1) || half == it.n_kv);
+          load_tile(v ? half - 1 : half, v);
+        }
+      } else {
+        if (it.n_kv > 0) load_tile(0, false);
+        for (int j = 0; j < it.n_kv && ok; ++j) {
+          if (j + 1 < it.n_kv) load_tile(j + 1, false);
+          if (ok) load_tile(j, true);
+        }
       }
       // One slot of the ring is the item's output stage.
       if (ok && it.parts == 1) {
