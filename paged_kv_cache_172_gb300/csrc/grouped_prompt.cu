@@ -76,7 +76,7 @@ constexpr int kCols = 512;               // tensor memory columns
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr int kWindow = 256;             // block-table entries staged at a time
 constexpr int kMaxRing = 8;
-constexpr int kBars = 2 * kMaxRing + 12 + 2 * kItems + 1;
+constexpr int kBars = 2 * kMaxRing + 14 + 2 * kItems + 1;
 constexpr float kLazy = 8.0f;            // log2 of the growth that forces a rescale
 
 // Layout of a K or V tile in shared memory.  Paged: key groups of 8 keys x D
@@ -249,6 +249,19 @@ __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
 }
 
+// One lane of a converged warp, the same each time.  (elect.sync and not lane == 0:
+// the compiler then knows that one thread issues the copies and products behind it
+// and does not wrap each in a loop over the lanes that might.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // A wait that is not on the chain of products: polled rarely.
 __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -296,6 +309,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                    const __grid_constant__ CUtensorMap vmap, const GroupedArgs a) {
   using C = Cfg<D, PAGED>;
   constexpr int kRing = C::RING;
+  // P is handed over in halves for contiguous rows, so that its product with V starts
+  // 64 keys early (one prompt of 8,192 353 -> 343 us); with the paged loader's code
+  // beside it the longer loops cost more than that (16 x 2,048 keys 457 -> 470 us).
+  constexpr int kHalves = PAGED ? 1 : 2;
   constexpr uint32_t kIdS = tc::idesc_f16_f32(kTile, kTile, false, false) | operand_type<T>();
   constexpr uint32_t kIdO = tc::idesc_f16_f32(kTile, D, false, true) | operand_type<T>();
   extern __shared__ uint8_t smem_dyn[];
@@ -310,7 +327,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   uint64_t* q_free = q_full + 2;        // [2]: the item's S products are done with it
   uint64_t* s_full = q_free + 2;        // [2]: an S product computed
   uint64_t* s_free = s_full + 2;        // [2]: its softmax holds S in registers
-  uint64_t* p_full = s_free + 2;        // [2]: P stored
+  uint64_t* p_half = s_free + 2;        // [2]: P of the first 64 keys stored
+  uint64_t* p_full = p_half + 2;        // [2]: all of P stored
   uint64_t* pv_done = p_full + 2;       // [2]: O += P V completed
   uint64_t* it_full = pv_done + 2;      // [kItems]: an item is posted
   uint64_t* it_empty = it_full + kItems;  // [kItems]: every role has copied it
@@ -333,6 +351,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       mbar_init(&q_free[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 4);  // one arrival per softmax warp
+      mbar_init(&p_half[i], 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
@@ -438,41 +457,46 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         const float neg_m = m == -INFINITY ? 0.f : -m;
         float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int h = 0; h < kHalves; ++h) {
+          constexpr int kC = 4 / kHalves;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float y0, y1;
-            fma_f32x2(y0, y1, __uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1]),
-                      sl2, sl2, neg_m, neg_m);
-            const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
-            const int q = 2 * (e & 3);
-            add_f32x2(rs[q], rs[q + 1], rs[q], rs[q + 1], p0, p1);
-            r[c][e] = pack2<T>(p0, p1);
-          }
-        l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
-        if (j > 0) {  // P V of the tile before done: P is free, O stands still
-          if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
-          tc::fence_after_sync();
-          if (__any_sync(kAll, resc)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tc::ld_32x32(t_o + c * 32, o);
-              tc::wait_ld();
+          for (int c = kC * h; c < kC * h + kC; ++c)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tc::st_32x32(t_o + c * 32, o);
+            for (int e = 0; e < 16; ++e) {
+              float y0, y1;
+              fma_f32x2(y0, y1, __uint_as_float(r[c][2 * e]), __uint_as_float(r[c][2 * e + 1]),
+                        sl2, sl2, neg_m, neg_m);
+              const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+              const int q = 2 * (e & 3);
+              add_f32x2(rs[q], rs[q + 1], rs[q], rs[q + 1], p0, p1);
+              r[c][e] = pack2<T>(p0, p1);
             }
-            tc::wait_st();
-          }
-        }
+          if (h == 0 && j > 0) {  // P V of the tile before done: P is free, O stands still
+            if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
+            tc::fence_after_sync();
+            if (__any_sync(kAll, resc)) {
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tc::ld_32x32(t_o + c * 32, o);
+                tc::wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c)  // the packed pairs as they lie in the registers
-          tc::st_32x16(tmem + t_lane + kColP + x * (kTile / 2) + c * 16, r[c]);
-        tc::wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tc::st_32x32(t_o + c * 32, o);
+              }
+              tc::wait_st();
+            }
+          }
+#pragma unroll
+          for (int c = kC * h; c < kC * h + kC; ++c)  // the packed pairs as they lie in the registers
+            tc::st_32x16(tmem + t_lane + kColP + x * (kTile / 2) + c * 16, r[c]);
+          tc::wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(h + 1 == kHalves ? &p_full[x] : &p_half[x]);
+        }
+        if (!ok) break;
+        l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
       }
       if (!ok) break;
       if (ntile > 0) {  // the last P V
@@ -755,7 +779,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     Item it;
     for (int k = 0; take(k, it); ++k) {
       const int nt[2] = {it.ntile_a, it.ntile_b};
-      if (lane == 0) {
+      if (elect_one()) {
         bool q_there[2] = {false, false};
         for (int t = 0; t < it.n_kv && ok; ++t) {
           const int u = u0 + ring_k(t);
@@ -787,7 +811,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           if (ok && nt[x] == 0 && (ok = mbar_wait(&q_full[x], k & 1))) mbar_arrive(&q_free[x]);
         u0 += 2 * it.n_kv + (it.parts == 1);
       }
-      if (!(ok = __shfl_sync(kAll, ok, 0))) break;
+      if (!(ok = __all_sync(kAll, ok))) break;
     }
   } else {  // kWarpPv
     // ------------------------------------------------------------ O += P V
@@ -819,7 +843,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0)
+        if (elect_one())
           for (int t = t0; t < t1 && ok; ++t) {
             const int u = u0 + ring_v(t, it.n_kv);
 #pragma unroll
@@ -827,21 +851,27 @@ __global__ void __launch_bounds__(kThreadsG, 1)
               if (t >= nt[x] || !ok) continue;
               // (P of an item's first tile is stored behind the item before's last
               // read of O by the same warps: O may then be overwritten.)
-              if (!(ok = mbar_wait(&p_full[x], done[x] & 1))) continue;
+              if (!(ok = mbar_wait(kHalves > 1 ? &p_half[x] : &p_full[x], done[x] & 1))) continue;
               if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) continue;
               tc::fence_after_sync();
               const uint32_t ta = tmem + kColP + x * (kTile / 2);
               const uint64_t db = dv + (u % kRing) * (C::TILE_BYTES >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
+              for (int kk = 0; kk < kTile / 16; ++kk) {
+                if (kHalves > 1 && kk == kTile / 32) {
+                  if (!(ok = mbar_wait(&p_full[x], done[x] & 1))) break;
+                  tc::fence_after_sync();
+                }
                 tc::mma_f16_ts(tmem + kColO + x * D, ta + kk * 8,
                                db + ((kk * 2 * C::GROUP) >> 4), kIdO, t > 0 || kk > 0);
+              }
+              if (!ok) continue;
               tc::commit(&pv_done[x]);
               ++done[x];
             }
             if (ok) tc::commit(&kv_empty[u % kRing]);
           }
-        if (!(ok = __shfl_sync(kAll, ok, 0))) break;
+        if (!(ok = __all_sync(kAll, ok))) break;
       }
       if (!ok) break;
       u0 += 2 * it.n_kv + (it.parts == 1);
@@ -858,7 +888,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     if (warp == kWarpLoad && lane == 0)
       for (int u = max(0, issued - kRing); u < issued; ++u)
         mbar_wait(&kv_full[u % kRing], (u / kRing) & 1);
-    if ((warp == kWarpS || warp == kWarpPv) && lane == 0) {
+    if ((warp == kWarpS || warp == kWarpPv) && elect_one()) {  // (who issued them)
       tc::commit(drain);
       mbar_wait(drain, 0);
     }
