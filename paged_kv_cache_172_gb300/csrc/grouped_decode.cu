@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads)
   uint8_t* ring = smem + warp * kRing * C::STAGE;
   auto request = [&](int i) {
     const int lo = __shfl_sync(kAll, row_lo, i), hi = __shfl_sync(kAll, row_hi, i);
-    if (lane == 0) {
+    if (elect_one()) {
       uint8_t* st = ring + (i % kRing) * C::STAGE;
       uint64_t* full = &bar[i % kRing];
       mbar_arrive_expect_tx(full, C::STAGE);
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncwarp();
     if (done + kRing < mine) {
-      if (lane == 0) fence_proxy_async_smem();  // this stage's reads before its refill
+      if (elect_one()) fence_proxy_async_smem();  // this stage's reads before its refill
       request(done + kRing);
     }
   }

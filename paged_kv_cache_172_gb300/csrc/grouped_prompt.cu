@@ -249,19 +249,6 @@ __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
 }
 
-// One lane of a converged warp, the same each time.  (elect.sync and not lane == 0:
-// the compiler then knows that one thread issues the copies and products behind it
-// and does not wrap each in a loop over the lanes that might.)
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
-}
-
 // A wait that is not on the chain of products: polled rarely.
 __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -717,11 +704,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           __syncwarp();
         }
         const int st = u % kRing;
-        if (lane == 0) {
+        if (elect_one()) {
           ok = mbar_wait(&kv_empty[st], ((u / kRing) & 1) ^ 1);
           if (ok) mbar_arrive_expect_tx(&kv_full[st], C::TILE_BYTES);
         }
-        ok = __shfl_sync(kAll, ok, 0);
+        ok = __all_sync(kAll, ok);
         if (!ok) return;
         uint8_t* dst = sKV + st * C::TILE_BYTES;
         if constexpr (PAGED) {
@@ -730,7 +717,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           if (lane < bpt)
             tma_load_5d(dst + lane * bbytes, v ? &vmap : &kmap, 0, 0, 0, 0, tbl[lb0 - win + lane],
                         &kv_full[st]);
-        } else if (lane == 0) {
+        } else if (elect_one()) {
           // 128 tokens of one head, both halves; rows past the array read as zeros.
           tma_load_4d(dst, v ? &vmap : &kmap, 0, row + (it.kt0 + t) * kTile, 0, it.hkv,
                       &kv_full[st]);

@@ -102,6 +102,19 @@ cudaError_t launch_grouped_decode(const GroupedDecodeArgs& a, const void* k_cach
                                   const void* v_cache, cudaStream_t stream);
 
 #ifdef __CUDACC__
+// One lane of a converged warp, the same each time.  (elect.sync and not lane == 0:
+// the compiler then knows that one thread issues the copies and products behind it
+// and does not wrap each in a loop over the lanes that might.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // 4-D tiled TMA load (coordinates innermost first).
 __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, int c0,
                                             int c1, int c2, int c3, uint64_t* bar) {
