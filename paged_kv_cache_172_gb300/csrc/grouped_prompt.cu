@@ -712,11 +712,15 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         if (!ok) return;
         uint8_t* dst = sKV + st * C::TILE_BYTES;
         if constexpr (PAGED) {
-          // One box per block, from lane to lane: (64 dims, 8 keys, halves, key
-          // groups) at row (block * block_size * Hkv + head) of the pool.
-          if (lane < bpt)
-            tma_load_5d(dst + lane * bbytes, v ? &vmap : &kmap, 0, 0, 0, 0, tbl[lb0 - win + lane],
-                        &kv_full[st]);
+          // One box per block: (64 dims, 8 keys, halves, key groups) at row
+          // (block * block_size * Hkv + head) of the pool.
+          if (elect_one()) {
+            const CUtensorMap* map = v ? &vmap : &kmap;
+const int32_t* rows = tbl + lb0 - win;
+#pragma unroll 2
+            for (int j = 0; j < bpt; ++j, dst += bbytes)
+              tma_load_5d(dst, map, 0, 0, 0, 0, rows[j], &kv_full[st]);
+          }
         } else if (elect_one()) {
           // 128 tokens of one head, both halves; rows past the array read as zeros.
           tma_load_4d(dst, v ? &vmap : &kmap, 0, row + (it.kt0 + t) * kTile, 0, it.hkv,
