@@ -716,10 +716,16 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           // (block * block_size * Hkv + head) of the pool.
           if (elect_one()) {
             const CUtensorMap* map = v ? &vmap : &kmap;
-const int32_t* rows = tbl + lb0 - win;
-#pragma unroll 2
-            for (int j = 0; j < bpt; ++j, dst += bbytes)
-              tma_load_5d(dst, map, 0, 0, 0, 0, rows[j], &kv_full[st]);
+            // (Four at a time: 8 x 512 tokens on 3,584 in 8-token blocks 246 us, 264 from
+            // lane to lane and 286 one by one; in larger blocks alike.)
+#pragma unroll 1
+            for (int j = 0; j < bpt; j += 4, dst += 4 * bbytes) {
+              const int4 r = *reinterpret_cast<const int4*>(tbl + lb0 - win + j);
+              tma_load_5d(dst, map, 0, 0, 0, 0, r.x, &kv_full[st]);
+              tma_load_5d(dst + bbytes, map, 0, 0, 0, 0, r.y, &kv_full[st]);
+              tma_load_5d(dst + 2 * bbytes, map, 0, 0, 0, 0, r.z, &kv_full[st]);
+              tma_load_5d(dst + 3 * bbytes, map, 0, 0, 0, 0, r.w, &kv_full[st]);
+            }
           }
         } else if (elect_one()) {
           // 128 tokens of one head, both halves; rows past the array read as zeros.
