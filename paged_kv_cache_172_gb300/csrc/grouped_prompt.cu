@@ -54,6 +54,7 @@
 // blocks arrive in boxes of 32 rows, which bounds the ring); 16 chunks of 1-48 on
 // up to 8,192 keys 79 us, 3.8 TB/s.
 #include <cuda_bf16.h>
+#include <math.h>
 #include <string.h>
 
 #include <type_traits>
@@ -1072,11 +1073,16 @@ int grouped_split(int B, int T, int H, int Hkv, int max_context) {
   const int span = grouped_span(H / Hkv);
   const int nsm = sm_count();
   if (span == 0 || nsm <= 0) return 1;
-  // Lengths are on the device: every sequence is taken to run, with half a unit
-  // lost at its end and contexts of 0.6 of the longest on average.  Time in key
-  // tiles, with s parts to a unit: the longest part, or all parts spread over the
-  // SMs; a part costs kPartCost tiles besides its own.
-  constexpr double kMean = 0.6, kPartCost = 4.0;
+  // Lengths are on the device, so the cost of s parts to a unit is a weighted sum of
+  // two guesses, in key tiles, a part costing kPartCost tiles besides its own.  All
+  // sequences alike: whole rounds of equal parts over the SMs.  Ragged ones, where
+  // there are several (half a unit lost at each one's end, contexts of 0.7 of the
+  // longest on average): the longest part, or all of them spread over the SMs.
+  // Fitted to sweeps of s on twenty batches: 4 x 64 tokens on 16,384 keys 67 us (99
+  // with the spread alone), 2 x 128 on 8,192 41 (55), 16 on 65,536 66 (85, the least
+  // 61); furthest from its least is 16 x 16 on 4,096 with 60 of 50, taken for ragged.
+  constexpr double kMean = 0.7, kPartCost = 3.0, kRagged = 2.5;
+  const double alike = (double)B * (((T + B - 1) / B + span - 1) / span) * Hkv;
   double units = (double)T / span + 0.5 * B;
   if (units < B) units = B;
   units *= Hkv;
@@ -1084,9 +1090,13 @@ int grouped_split(int B, int T, int H, int Hkv, int max_context) {
   int best = 1;
   double least = 0.0;
   for (int s = 1; s <= kGroupedMaxSplit && (s == 1 || s * kGroupedMinPartTiles <= tiles); ++s) {
-    const double longest = tiles / s + (s > 1 ? kPartCost : 0.0);
-    const double spread = units * s * (kMean * tiles / s + (s > 1 ? kPartCost : 0.0)) / nsm;
-    const double t = longest > spread ? longest : spread;
+    const double cost = s > 1 ? kPartCost : 0.0;
+    const double longest = tiles / s + cost;
+    double t = ceil(alike * s / nsm) * longest;
+    if (B > 1) {
+      const double spread = units * s * (kMean * tiles / s + cost) / nsm;
+      t += kRagged * (longest > spread ? longest : spread);
+    }
     if (s == 1 || t < least) {
       best = s;
       least = t;
