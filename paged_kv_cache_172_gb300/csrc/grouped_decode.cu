@@ -454,11 +454,13 @@ __global__ void __launch_bounds__(32 * W) grouped_decode_merge(const GroupedDeco
   constexpr int EPL = D / 32;
   __shared__ float s_o[W][D];
   __shared__ float2 s_ml[W];
-  pdl_wait();
-  pdl_launch_dependents();
   const size_t row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The lengths come from before the first kernel, which let this one start only when
+  // all its blocks had waited for them: they are read while it still runs.
   const int n = min(max(a.context_lens[row / a.H], 0), a.max_context);
+  pdl_wait();
+  pdl_launch_dependents();
   if (n <= a.part_tokens) return;  // written by its only partition (or empty)
   const int parts = (n + a.part_tokens - 1) / a.part_tokens;
   float M = -INFINITY, L = 0.f, o[EPL];

@@ -910,10 +910,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) grouped_merge_kernel(const G
   __shared__ float s_w[kGroupedMaxSplit][32];     // m, then the weight of a part
   __shared__ float s_m[kMergeWarps][32], s_l[kMergeWarps][32];
   __shared__ uint2 s_out[32][D / 4 + 1];
-  pdl_wait();
-  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hkv = blockIdx.y;
   const size_t plane = (size_t)a.T * a.G, row0 = (size_t)blockIdx.x * 32, r = row0 + lane;
+  // The lengths come from before the attention kernel, which let this one start only
+  // when all its blocks had waited for them: they are read while it still runs.
   int parts = 0;  // of this lane's row; 0: nothing to merge
   if (r < plane) {
     const int t = (int)(r / a.G);
@@ -933,6 +933,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) grouped_merge_kernel(const G
       if (parts == 1) parts = 0;  // (written by its only part)
     }
   }
+  pdl_wait();
+  pdl_launch_dependents();
   const int most = __reduce_max_sync(kAll, parts);
   if (most == 0) return;  // (alike in all warps)
   float M = -INFINITY;
@@ -1082,7 +1084,7 @@ int grouped_split(int B, int T, int H, int Hkv, int max_context) {
   // with the spread alone), 2 x 128 on 8,192 41 (55), 16 on 65,536 66 (85, the least
   // 61); furthest from its least is 16 x 16 on 4,096 with 60 of 50, taken for ragged.
   constexpr double kMean = 0.7, kPartCost = 3.0, kRagged = 2.5;
-  const double alike = (double)B * (((T + B - 1) / B + span - 1) / span) * Hkv;
+  const double alike = (double)B * ((((long long)T + B - 1) / B + span - 1) / span) * Hkv;
   double units = (double)T / span + 0.5 * B;
   if (units < B) units = B;
   units *= Hkv;
