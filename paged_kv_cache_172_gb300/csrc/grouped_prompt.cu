@@ -173,11 +173,27 @@ __device__ __forceinline__ int unit_parts(int tiles, int split, int min_tiles) {
 template <bool PAGED>
 struct Units {
   const GroupedArgs& a;
+  Seq mine;          // the lane's among the first 32 sequences, read once
   int bound, above;  // no unit asked for later reads `bound` key tiles or more; how many do
   int tiles, base0, before;  // where the last scan ended: sequences from base0, units before
 
   __device__ Units(const GroupedArgs& args)
-      : a(args), bound(args.max_tiles + 1), above(0), tiles(0), base0(0), before(0) {}
+      : a(args), bound(args.max_tiles + 1), above(0), tiles(0), base0(0), before(0) {
+    const int lane = threadIdx.x & 31;
+    mine = lane < a.B ? sequence<PAGED>(a, lane) : Seq{0, 0, 0, true, true};
+  }
+
+  // Sequence b, the same for all lanes.
+  __device__ Seq get(int b) const {
+    if (b >= 32) return sequence<PAGED>(a, b);
+    Seq s;
+    s.start = __shfl_sync(kAll, mine.start, b);
+    s.ql = __shfl_sync(kAll, mine.ql, b);
+    s.n = __shfl_sync(kAll, mine.n, b);
+    s.bad = __shfl_sync(kAll, (int)mine.bad, b);
+    s.lost = false;  // (a lost one has no units)
+    return s;
+  }
 
   // The unit of a rank: (b, i), or false behind the last unit.  Ranks rise from
   // call to call.
@@ -192,7 +208,11 @@ struct Units {
       const int t = (lo + hi) >> 1;
       int c = 0;
 #pragma unroll 1
-      for (int b = lane; b < a.B; b += 32) c += units_from(a, sequence<PAGED>(a, b), t);
+      for (int b = lane; b < a.B; b += 32) {
+        Seq s = mine;
+        if (b >= 32) s = sequence<PAGED>(a, b);
+        c += units_from(a, s, t);
+      }
       c = __reduce_add_sync(kAll, c);
       if (c > rank) {
         lo = t;
@@ -215,7 +235,8 @@ struct Units {
       const int b = base + lane;
       int c = 0, upper = 0, nu = 0;
       if (b < a.B) {
-        const Seq s = sequence<PAGED>(a, b);
+        Seq s = mine;
+        if (b >= 32) s = sequence<PAGED>(a, b);
         upper = units_from(a, s, lo + 1);
         c = units_from(a, s, lo) - upper;
         nu = per_span(a, s.ql + a.span - 1);
@@ -582,9 +603,6 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   } else if (warp == kWarpSched) {
     // ------------------------------------------------------------ scheduler, Q loads
     reg_dec();
-    if (blockIdx.x == 0)
-      for (int i = lane; i < a.B; i += 32)
-        if (sequence<PAGED>(a, i).lost) flag_status(a.status, PA_DEV_BAD_CONTEXT);
     Units<PAGED> units(a);
     const unsigned n_items = (unsigned)a.max_units * a.Hkv * a.split;  // below 2^31
     unsigned round = 0;
@@ -605,7 +623,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         it.hkv = (int)(unit_head - rank * a.Hkv);
         if (rank != last_rank && !(more = units.find(rank, b, unit))) break;
         last_rank = rank;
-        const Seq s = sequence<PAGED>(a, b);
+        const Seq s = units.get(b);
         const int tok0 = unit * a.span;
         const int all = unit_tiles(s, a.span, unit);
         it.parts = unit_parts(all, a.split, a.min_part_tiles);
@@ -646,28 +664,42 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       }
       __syncwarp();
     };
-    // Item k is posted ahead of the Q loads of item k - 1.
-    Item cur, prev;
-    prev.valid = 0;
+    // Item k is posted ahead of the Q loads of item k - 1; the first item's Q goes with
+    // it (behind the second one, the first products waited 3,000 cycles for it).
+    Item cur;
+    int q_row = 0, q_hkv = 0;
+    bool q_due = false;
     for (int k = 0; ok; ++k) {
       next(cur);
       post(k, cur);
-      // Q of the item before, tile by tile as the products of the one before that
-      // let go of it: boxes of tpt tokens x G heads x 64 dims; rows past the array
-      // read as zeros.
-      if (ok && lane == 0 && prev.valid)
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (!(ok = mbar_wait(&q_free[x], k & 1))) break;
-          mbar_arrive_expect_tx(&q_full[x], C::HALVES * tpt * a.G * 128);
-          for (int hf = 0; hf < C::HALVES; ++hf)
-            tma_load_3d(sQ + x * kQRoom + hf * kSlab, &qmap, 64 * hf, prev.hkv * a.G,
-                        prev.row0 + x * tpt, &q_full[x]);
-          ++issued;
+      if (k != 1) {
+        const int j = k == 0 ? 0 : k - 1;  // the item whose Q is due
+        if (k == 0) {
+          q_due = cur.valid;
+          q_row = cur.row0;
+          q_hkv = cur.hkv;
         }
+        // Tile by tile as the products of the item before that let go of it: boxes of
+        // tpt tokens x G heads x 64 dims; rows past the array read as zeros.
+        if (ok && lane == 0 && q_due)
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (!(ok = mbar_wait(&q_free[x], (j & 1) ^ 1))) break;
+            mbar_arrive_expect_tx(&q_full[x], C::HALVES * tpt * a.G * 128);
+            for (int hf = 0; hf < C::HALVES; ++hf)
+              tma_load_3d(sQ + x * kQRoom + hf * kSlab, &qmap, 64 * hf, q_hkv * a.G,
+                          q_row + x * tpt, &q_full[x]);
+            ++issued;
+          }
+      }
       ok = __shfl_sync(kAll, ok, 0);
       if (!cur.valid) break;
-      prev = cur;
+      q_due = k > 0;
+      q_row = cur.row0;
+      q_hkv = cur.hkv;
     }
+    if (blockIdx.x == 0)
+      for (int i = lane; i < a.B; i += 32)
+        if (sequence<PAGED>(a, i).lost) flag_status(a.status, PA_DEV_BAD_CONTEXT);
   } else if (warp == kWarpLoad) {
     // ------------------------------------------------------------ K and V
     reg_dec();
