@@ -180,12 +180,13 @@ static pa_status packed_impl(pk::GroupedArgs& a, const void* q, const void* k, c
   a.G = a.H / a.Hkv;
   a.span = pk::grouped_span(a.G);
   if (a.span == 0) return PA_ERR_UNSUPPORTED;
-  a.span_magic = ((1ull << 40) + a.span - 1) / a.span;
+  a.by_span = pk::div_by(a.span);
+  a.by_split = pk::div_by(a.split);
+  a.by_hkv = pk::div_by(a.Hkv);
   a.g_magic = (65536 + a.G - 1) / a.G;
   if (a.B == 0 || a.T == 0) return PA_OK;
   if (!a.q_offsets || !a.out || !aligned16(a.out) || !rows_ok(q, qs, a.H, a.D))
     return PA_ERR_INVALID;
-  a.min_part_tiles = pk::kGroupedMinPartTiles;
   // A sequence whose context is bad still has its ql <= T rows in the plan.
   a.max_tiles = (int)(((long long)(max_keys > a.T ? max_keys : a.T) + 127) / 128);
   const long long units = (long long)a.T / a.span + a.B;

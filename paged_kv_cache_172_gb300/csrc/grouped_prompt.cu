@@ -119,9 +119,14 @@ __host__ __device__ constexpr uint32_t operand_type() {
 // A sequence of the packed step, as every CTA sees it.
 struct Seq {
   int start, ql, n;  // first packed row, new tokens, keys
+  int nu;            // units
   bool bad;          // its rows are zeros
   bool lost;         // its rows do not exist: nothing to write
 };
+
+__device__ __forceinline__ int divide(int x, DivBy d) {
+  return (int)(((unsigned long long)(unsigned)x * d.m) >> (31 + d.s));
+}
 
 template <bool PAGED>
 __device__ __forceinline__ Seq sequence(const GroupedArgs& a, int b) {
@@ -140,33 +145,27 @@ __device__ __forceinline__ Seq sequence(const GroupedArgs& a, int b) {
     else
       s.n = n;
   }
+  s.nu = divide(s.ql + a.span - 1, a.by_span);
   return s;
-}
-
-// x / span for 0 <= x < 2^31: a product with 2^40 / span rounded up (span <= 256,
-// so the excess x * 2^-40 stays below 1 / span).
-__device__ __forceinline__ int per_span(const GroupedArgs& a, int x) {
-  return (int)(((unsigned long long)(unsigned)x * a.span_magic) >> 40);
 }
 
 // Key tiles that unit i (tokens i * span .. ) of a sequence reads.
 __device__ __forceinline__ int unit_tiles(const Seq& s, int span, int i) {
-  return (s.n - s.ql + min((i + 1) * span, s.ql) + kTile - 1) / kTile;
+  return (int)((unsigned)(s.n - s.ql + min((i + 1) * span, s.ql) + kTile - 1) / kTile);
 }
 
 // Units of a sequence that read at least t (>= 1) key tiles: the last ones.
 __device__ __forceinline__ int units_from(const GroupedArgs& a, const Seq& s, int t) {
   const int k = (t - 1) * kTile + 1;  // keys such a unit needs at least
-  if (s.ql <= 0 || s.n < k) return 0;
-  const int nu = per_span(a, s.ql + a.span - 1);
+  if (s.n < k) return 0;  // (an empty sequence too)
   const int over = k - (s.n - s.ql);  // its tokens needed at least
-  const int first = over <= 0 ? 0 : per_span(a, over + a.span - 1) - 1;
-  return nu - min(first, nu - 1);
+  const int first = over <= 0 ? 0 : divide(over - 1, a.by_span);
+  return s.nu - min(first, s.nu - 1);
 }
 
 // Key ranges a unit of that many key tiles is cut into.
-__device__ __forceinline__ int unit_parts(int tiles, int split, int min_tiles) {
-  return max(1, min(split, tiles / min_tiles));
+__device__ __forceinline__ int unit_parts(int tiles, int split) {
+  return max(1, min(split, (int)((unsigned)tiles / kGroupedMinPartTiles)));
 }
 
 // Walks the units by key tiles, longest first (one warp, all lanes alike).
@@ -180,7 +179,7 @@ struct Units {
   __device__ Units(const GroupedArgs& args)
       : a(args), bound(args.max_tiles + 1), above(0), tiles(0), base0(0), before(0) {
     const int lane = threadIdx.x & 31;
-    mine = lane < a.B ? sequence<PAGED>(a, lane) : Seq{0, 0, 0, true, true};
+    mine = lane < a.B ? sequence<PAGED>(a, lane) : Seq{0, 0, 0, 0, true, true};
   }
 
   // Sequence b, the same for all lanes.
@@ -190,6 +189,7 @@ struct Units {
     s.start = __shfl_sync(kAll, mine.start, b);
     s.ql = __shfl_sync(kAll, mine.ql, b);
     s.n = __shfl_sync(kAll, mine.n, b);
+    s.nu = 0;  // (not asked for)
     s.bad = __shfl_sync(kAll, (int)mine.bad, b);
     s.lost = false;  // (a lost one has no units)
     return s;
@@ -239,7 +239,7 @@ struct Units {
         if (b >= 32) s = sequence<PAGED>(a, b);
         upper = units_from(a, s, lo + 1);
         c = units_from(a, s, lo) - upper;
-        nu = per_span(a, s.ql + a.span - 1);
+        nu = s.nu;
       }
       int x = c;  // inclusive scan
 #pragma unroll
@@ -617,8 +617,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         const unsigned idx = round * gridDim.x + at;
         ++round;
         if (!(more = idx < n_items)) break;
-        const unsigned unit_head = idx / a.split;
-        const int rank = (int)(unit_head / a.Hkv);
+        const unsigned unit_head = divide((int)idx, a.by_split);
+        const int rank = divide((int)unit_head, a.by_hkv);
         it.part = (int)(idx - unit_head * a.split);
         it.hkv = (int)(unit_head - rank * a.Hkv);
         if (rank != last_rank && !(more = units.find(rank, b, unit))) break;
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         const Seq s = units.get(b);
         const int tok0 = unit * a.span;
         const int all = unit_tiles(s, a.span, unit);
-        it.parts = unit_parts(all, a.split, a.min_part_tiles);
+        it.parts = unit_parts(all, a.split);
         if (it.part >= it.parts) continue;
         it.valid = 1;
         it.b = b;
@@ -635,10 +635,15 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         it.toks_a = min(tpt, s.ql - tok0);
         it.toks_b = max(0, min(tpt, s.ql - tok0 - tpt));
         it.pos_a = s.n - s.ql + tok0;
-        it.kt0 = (int)((long long)it.part * all / it.parts);
-        it.n_kv = (int)((long long)(it.part + 1) * all / it.parts) - it.kt0;
+        it.kt0 = 0;
+        it.n_kv = all;
+        if (it.parts > 1) {  // (at most 32 parts of 2^24 tiles)
+          const unsigned at = (unsigned)it.part * all, parts = it.parts;
+          it.kt0 = (int)(at / parts);
+          it.n_kv = (int)((at + all) / parts) - it.kt0;
+        }
         auto reads = [&](int pos, int toks) {
-          const int t = toks > 0 ? (pos + toks - 1) / kTile + 1 : 0;
+          const int t = toks > 0 ? (int)((unsigned)(pos + toks - 1) / kTile) + 1 : 0;
           return min(max(t - it.kt0, 0), it.n_kv);
         };
         it.ntile_a = reads(it.pos_a, it.toks_a);
@@ -960,8 +965,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) grouped_merge_kernel(const G
       }
       const Seq s = sequence<true>(a, lo);
       if (!s.bad && t >= s.start && t < s.start + s.ql)
-        parts = unit_parts(unit_tiles(s, a.span, per_span(a, t - s.start)), a.split,
-                           a.min_part_tiles);
+        parts = unit_parts(unit_tiles(s, a.span, divide(t - s.start, a.by_span)), a.split);
       if (parts == 1) parts = 0;  // (written by its only part)
     }
   }

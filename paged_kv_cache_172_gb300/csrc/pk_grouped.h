@@ -52,6 +52,18 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_write(const RopeArgs& a, cudaStream_t stream);
 
+// x / n for 0 <= x < 2^31 by a product with 2^(31 + s) / n rounded up, 2^s the power
+// of two from n on: the excess, x * 2^s at most, stays below 2^(31 + s) / n * n.
+struct DivBy {
+  unsigned m;
+  int s;
+};
+inline DivBy div_by(int n) {
+  int s = 0;
+  while ((1ll << s) < n) ++s;
+  return {(unsigned)(((1ull << (31 + s)) + n - 1) / n), s};
+}
+
 // Attention of packed new tokens (grouped_prompt.cu): prompts over their own
 // rows (block_tables null) or chunks over the paged cache.
 struct GroupedArgs {
@@ -63,11 +75,11 @@ struct GroupedArgs {
   int32_t* status;
   int B, T, H, Hkv, G, D;
   int span;       // tokens of a unit (two tiles)
-  unsigned long long span_magic;  // 2^40 / span, rounded up
   int g_magic;    // 2^16 / G, rounded up: r * g_magic >> 16 = r / G for r < 128
   int max_units;  // units of a K/V head, at most
   int max_tiles;  // key tiles of a unit, at most
-  int split, min_part_tiles;
+  int split;      // parts of a unit, at most
+  DivBy by_span, by_split, by_hkv;
   int block_size, num_blocks, max_blocks, max_context;
   float scale_log2;
   bool bf16;
