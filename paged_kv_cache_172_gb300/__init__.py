@@ -1,4 +1,4 @@
-"""GB300-native paged-KV attention: ctypes binding of libpagedkv.
+"""GB300-native paged-KV attention: Python binding of libpagedkv.
 
 The compute path is the C-ABI CUDA library (include/pagedkv.h, sources in
 csrc/); this package only marshals torch tensors into it.  Importing the

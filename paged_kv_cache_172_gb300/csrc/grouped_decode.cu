@@ -29,9 +29,9 @@
 // grid fits at once, otherwise through the workspace in a second, dependent
 // launch.
 //
-// Measured (GB300): 4 x 60-131 thousand keys, 64 heads on 8, bf16: 246 us, 6.87
-// TB/s of keys and values, 1.03 of the measured copy rate; 38 sequences of
-// 128-2,048 keys, 40 on 8, fp16: 32.7 us, 5.3 TB/s (the start, the last CTAs and
+// Measured (GB300): 4 x 60-131 thousand keys, 64 heads on 8, bf16: 249 us, 6.78
+// TB/s of keys and values, 1.01 of the measured copy rate; 38 sequences of
+// 128-2,048 keys, 40 on 8, fp16: 32.8 us, 5.3 TB/s (the start, the last CTAs and
 // the merge are 8 us of it); one of 1,000 keys, 32 on 8: 5.0 us, of which a launch
 // and four trips to memory are all.
 //

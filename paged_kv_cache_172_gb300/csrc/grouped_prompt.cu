@@ -47,12 +47,14 @@
 // tiles, where four products take 2,048), and over long prompts the power cap.
 // Besides that a unit costs about 4,000 cycles around its end (last P V product,
 // output, next Q).  Measured (GB300, 32 heads on 8, D = 128, bf16): one prompt of
-// 16,001 tokens 1,279 us, 1,640 TFLOP/s, 0.85 of the measured burst rate and 0.94
-// of the sustained one; eight of 500-4,096 350 us, 1,437 TFLOP/s (0.74); chunks
-// of 512 on 3,584 (40 on 8, fp16) 277 us, 1,163 TFLOP/s (0.60: 704 units on 152
-// SMs are five rounds where 4.6 would do, 125 rows of 128 are used, and 16-token
-// blocks arrive in boxes of 32 rows, which bounds the ring); 16 chunks of 1-48 on
-// up to 8,192 keys 79 us, 3.8 TB/s.
+// 16,001 tokens 1,258 us, 1,667 TFLOP/s, 0.86 of the measured burst rate and 0.95
+// of the sustained one; eight of 500-4,096 345 us, 1,459 TFLOP/s (0.75); chunks
+// of 512 on 3,584 (40 on 8, fp16) 273 us, 1,179 TFLOP/s (0.61: 704 units on 152
+// SMs are five rounds where 4.6 would do, 125 rows of 128 are used, and with
+// all keys in L2 they are 1.5 % quicker); 16 chunks of 1-48 on up to 8,192 keys
+// 76 us, 3.9 TB/s (bound by the chain above over 32 key tiles, not by HBM).  A
+// launch reaches its first S product after 8,000 to 13,000 cycles: the search for
+// the first unit and the code of every role run from a cold instruction cache.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>

@@ -21,9 +21,9 @@
 // of a CTA's tokens are computed once, by all its threads, into shared memory and
 // serve all H + Hkv heads; each thread's first rows are loaded before the barrier,
 // so that loads and sines overlap.  Measured: 16,001 tokens, 32 heads on 8, three
-// axes, bf16: 68.8 us, 6.19 TB/s, 0.93 of the measured copy rate (one token to a
+// axes, bf16: 68.2 us, 6.25 TB/s, 0.93 of the measured copy rate (one token to a
 // CTA: 92 us, half of the time at the barrier behind too few sines); 38 tokens, 40
-// heads on 8: 2.5 us.
+// heads on 8: 2.3 us.
 #include <cuda_bf16.h>
 
 #include "pk_common.cuh"

@@ -20,8 +20,8 @@
 // lengths are, so both may be updated in place.  The work is a few hundred kilobytes at most: the call
 // is bound by its launch and by two trips to memory (lengths, then ring
 // entries), and one launch instead of a scan and a fill is what counts.
-// Measured (GB300): 64 sequences with a token each 3.5 us, 200 sequences with 11,000
-// new tokens 5.8 us, of which the launch of an empty kernel is about two thirds.
+// Measured (GB300): 38 single tokens 3.4 us, 200 sequences with 11,000 new tokens
+// 6.1 us, of which the launch of an empty kernel is about two thirds.
 #include <cooperative_groups.h>
 
 #include "pk_common.cuh"
@@ -221,7 +221,7 @@ static cudaError_t launch_t(const StepPlanArgs& a, int ranks, cudaStream_t strea
 
 // Threads and blocks of the cluster, by the sequences and the tokens to place.  Up to 256 of
 // each a block of 256 threads does it in one round, and its barriers cost less than those of
-// 1024 (64 sequences with a token each 3.5 us against 3.9, 200 sequences 3.8 against 4.1; 1000
+// 1024 (38 sequences with a token each 3.5 us against 3.9, 200 sequences 3.8 against 4.1; 1000
 // sequences would take 7.0 against 4.8).  Up to 1024 one block of 1024 is as quick as eight
 // (1000 sequences 4.8 against 5.0, one chunk of 500 tokens 3.3 against 3.6), and above that
 // the tokens are what takes the time and eight blocks share them (2304 tokens 4.1 us against
