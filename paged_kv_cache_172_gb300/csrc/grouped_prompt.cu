@@ -79,7 +79,7 @@ constexpr int kCols = 512;               // tensor memory columns
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr int kWindow = 256;             // block-table entries staged at a time
 constexpr int kMaxRing = 8;
-constexpr int kBars = 2 * kMaxRing + 14 + 2 * kItems + 1;
+constexpr int kBars = 4 * kMaxRing + 14 + 2 * kItems + 1;
 constexpr float kLazy = 8.0f;            // log2 of the growth that forces a rescale
 
 // Layout of a K or V tile in shared memory.  Paged: key groups of 8 keys x D
@@ -332,8 +332,15 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + C::OFF_KV;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* kv_full = bars;
-  uint64_t* kv_empty = kv_full + kRing;
+  // The slots of the ring are given out in one order (K_0, K_1, V_0, ..., an item's
+  // stage) and let go one by one, but what lands in them is told by kind, the i-th K,
+  // V or stage at [i % ring]: whoever waits there takes every one of its kind in turn,
+  // so a wait can never see the phase of two rounds before (of a slot that another
+  // role has yet to wait for) and pass too early.
+  uint64_t* k_full = bars;
+  uint64_t* v_full = k_full + kRing;
+  uint64_t* st_full = v_full + kRing;
+  uint64_t* kv_empty = st_full + kRing;
   uint64_t* q_full = kv_empty + kRing;  // [2] per tile: Q of the item landed
   uint64_t* q_free = q_full + 2;        // [2]: the item's S products are done with it
   uint64_t* s_full = q_free + 2;        // [2]: an S product computed
@@ -354,7 +361,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(&kv_full[s], 1);
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&st_full[s], 1);
       mbar_init(&kv_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_at;
   bool ok = true;
-  int issued = 0;  // ring tiles, or Q loads, requested
+  int issued = 0, issued_v = 0;  // K tiles, or Q loads, requested; V tiles
 
   // The k-th item of this CTA, copied; the scheduler may then reuse its room.
   auto take = [&](int k, Item& it) {
@@ -409,7 +418,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     const uint32_t t_s = tmem + t_lane + kColS, t_o = tmem + t_lane + kColO + x * D;
     const float sl2 = a.scale_log2;
     int done = 0;    // key tiles of the items before and of this one
-    int u0 = 0;      // ring tiles of the items before
+    int u0 = 0;      // ring slots of the items before
+    int stages = 0;  // of those, stages
     Item it;
     for (int k = 0; take(k, it); ++k) {
       const int pos0 = it.pos_a + (x ? tpt : 0);
@@ -522,11 +532,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       // unnormalised row.
       const bool whole = it.parts == 1;
       const int stage_u = u0 + 2 * it.n_kv;
+      const int stage_i = stages;
       u0 = stage_u + whole;
+      stages += whole;
       const int toks = x ? it.toks_b : it.toks_a, first = it.row0 + (x ? tpt : 0);
       if (toks == 0) continue;  // (tile B of a unit that ends in tile A)
       if (whole &&
-          !(ok = __all_sync(kAll, mbar_wait(&kv_full[stage_u % kRing], (stage_u / kRing) & 1))))
+          !(ok = __all_sync(kAll, mbar_wait(&st_full[stage_i % kRing], (stage_i / kRing) & 1))))
         break;
       constexpr int kHalf = D / 2, kChunks = kHalf / 8;  // columns; 16-byte chunks of them
       const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -712,7 +724,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     reg_dec();
     const int bpt = PAGED ? kTile / a.block_size : 1;  // blocks of a key tile
     const int bbytes = C::TILE_BYTES / bpt;
-    int u = 0;  // ring index, over all items
+    int u = 0, stages = 0;  // ring slots and stages, over all items
     Item it;
     for (int k = 0; take(k, it); ++k) {
       const int nblk = PAGED ? (it.n + a.block_size - 1) / a.block_size : 0;
@@ -744,9 +756,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           __syncwarp();
         }
         const int st = u % kRing;
+        uint64_t* full = v ? &v_full[issued_v % kRing] : &k_full[issued % kRing];
         if (elect_one()) {
           ok = mbar_wait(&kv_empty[st], ((u / kRing) & 1) ^ 1);
-          if (ok) mbar_arrive_expect_tx(&kv_full[st], C::TILE_BYTES);
+          if (ok) mbar_arrive_expect_tx(full, C::TILE_BYTES);
         }
         ok = __all_sync(kAll, ok);
         if (!ok) return;
@@ -761,18 +774,19 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 #pragma unroll 1
             for (int j = 0; j < bpt; j += 4, dst += 4 * bbytes) {
               const int4 r = *reinterpret_cast<const int4*>(tbl + lb0 - win + j);
-              tma_load_5d(dst, map, 0, 0, 0, 0, r.x, &kv_full[st]);
-              tma_load_5d(dst + bbytes, map, 0, 0, 0, 0, r.y, &kv_full[st]);
-              tma_load_5d(dst + 2 * bbytes, map, 0, 0, 0, 0, r.z, &kv_full[st]);
-              tma_load_5d(dst + 3 * bbytes, map, 0, 0, 0, 0, r.w, &kv_full[st]);
+              tma_load_5d(dst, map, 0, 0, 0, 0, r.x, full);
+              tma_load_5d(dst + bbytes, map, 0, 0, 0, 0, r.y, full);
+              tma_load_5d(dst + 2 * bbytes, map, 0, 0, 0, 0, r.z, full);
+              tma_load_5d(dst + 3 * bbytes, map, 0, 0, 0, 0, r.w, full);
             }
           }
         } else if (elect_one()) {
           // 128 tokens of one head, both halves; rows past the array read as zeros.
           tma_load_4d(dst, v ? &vmap : &kmap, 0, row + (it.kt0 + t) * kTile, 0, it.hkv,
-                      &kv_full[st]);
+                      full);
         }
-        issued = ++u;
+        ++u;
+        ++(v ? issued_v : issued);
       };
       // K_0, then K_{t+1} and V_t in turn (see ring_k).
       if constexpr (PAGED) {
@@ -796,10 +810,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         const int st = u % kRing;
         if (lane == 0) {
           ok = mbar_wait(&kv_empty[st], ((u / kRing) & 1) ^ 1);
-          if (ok) mbar_arrive(&kv_full[st]);
+          if (ok) mbar_arrive(&st_full[stages % kRing]);
         }
         ok = __shfl_sync(kAll, ok, 0);
-        if (ok) issued = ++u;
+        ++u;
+        ++stages;
       }
       if (!ok) break;
     }
@@ -810,7 +825,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     const uint64_t dq = tc::smem_desc(smem_u32(sQ), 16, 1024, tc::kSwizzle128B);
     // (The loops over the two tiles are unrolled: an array indexed at run time
     // would sit in local memory, on the chain from one S product to the next.)
-    int u0 = 0, done[2] = {0, 0};   // ring tiles and products of the items before
+    int u0 = 0, k0 = 0, done[2] = {0, 0};  // ring slots, K tiles and products before
     uint64_t* last_free = nullptr;  // s_free of the product issued last, its phase
     int last_phase = 0;
     Item it;
@@ -819,17 +834,19 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       if (elect_one()) {
         bool q_there[2] = {false, false};
         for (int t = 0; t < it.n_kv && ok; ++t) {
-          const int u = u0 + ring_k(t);
+          // K and the addresses first: nothing but the product stands behind the
+          // wait for S, which is on the chain from one product to the next.
+          const int st = (u0 + ring_k(t)) % kRing, ki = k0 + t;
+          const uint64_t db = dk + st * (C::TILE_BYTES >> 4);
+          if (!(ok = mbar_wait(&k_full[ki % kRing], (ki / kRing) & 1))) break;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (t >= nt[x] || !ok) continue;
             if (!q_there[x] && !(ok = q_there[x] = mbar_wait(&q_full[x], k & 1))) continue;
+            const uint64_t da = dq + x * (kQRoom >> 4);
             // S is free once the softmax of the product before has loaded it.
             if (last_free != nullptr && !(ok = mbar_wait(last_free, last_phase))) continue;
-            if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) continue;
             tc::fence_after_sync();
-            const uint64_t db = dk + (u % kRing) * (C::TILE_BYTES >> 4);
-            const uint64_t da = dq + x * (kQRoom >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               tc::mma_f16(tmem + kColS, da + (((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
@@ -840,13 +857,14 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             last_phase = done[x] & 1;
             ++done[x];
           }
-          if (ok) tc::commit(&kv_empty[u % kRing]);
+          if (ok) tc::commit(&kv_empty[st]);
         }
         // A tile that read nothing lets its Q go, once it has landed.
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (ok && nt[x] == 0 && (ok = mbar_wait(&q_full[x], k & 1))) mbar_arrive(&q_free[x]);
         u0 += 2 * it.n_kv + (it.parts == 1);
+        k0 += it.n_kv;
       }
       if (!(ok = __all_sync(kAll, ok))) break;
     }
@@ -854,7 +872,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     // ------------------------------------------------------------ O += P V
     reg_dec();
     const uint64_t dv = tc::smem_desc(smem_u32(sKV), C::HALF, C::GROUP, tc::kSwizzle128B);
-    int u0 = 0, done[2] = {0, 0};
+    int u0 = 0, v0 = 0, done[2] = {0, 0};  // ring slots, V tiles and products before
     Item it;
     for (int k = 0; take(k, it); ++k) {
       const int nt[2] = {it.ntile_a, it.ntile_b};
@@ -867,10 +885,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       const int whole = it.n_kv - (it.n_kv > 0 && live < kTile ? 1 : 0);
       for (int t0 = 0, t1 = whole; t0 < it.n_kv; t0 = t1, t1 = it.n_kv) {
         if (t0 == whole) {
-          const int u = u0 + ring_v(t0, it.n_kv);
-          if (lane == 0) ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1);
+          const int st = (u0 + ring_v(t0, it.n_kv)) % kRing, vi = v0 + t0;
+          if (lane == 0) ok = mbar_wait(&v_full[vi % kRing], (vi / kRing) & 1);
           if (!(ok = __shfl_sync(kAll, ok, 0))) break;
-          uint8_t* vt = sKV + (u % kRing) * C::TILE_BYTES;
+          uint8_t* vt = sKV + st * C::TILE_BYTES;
           constexpr int kChunks = D / 8;
           for (int i = lane; i < (kTile - live) * kChunks; i += 32) {
             const int r = live + i / kChunks, c = i % kChunks;
@@ -882,17 +900,17 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         }
         if (elect_one())
           for (int t = t0; t < t1 && ok; ++t) {
-            const int u = u0 + ring_v(t, it.n_kv);
+            const int st = (u0 + ring_v(t, it.n_kv)) % kRing, vi = v0 + t;
+            const uint64_t db = dv + st * (C::TILE_BYTES >> 4);
+            if (!(ok = mbar_wait(&v_full[vi % kRing], (vi / kRing) & 1))) break;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               if (t >= nt[x] || !ok) continue;
+              const uint32_t ta = tmem + kColP + x * (kTile / 2);
               // (P of an item's first tile is stored behind the item before's last
               // read of O by the same warps: O may then be overwritten.)
               if (!(ok = mbar_wait(kHalves > 1 ? &p_half[x] : &p_full[x], done[x] & 1))) continue;
-              if (!(ok = mbar_wait(&kv_full[u % kRing], (u / kRing) & 1))) continue;
               tc::fence_after_sync();
-              const uint32_t ta = tmem + kColP + x * (kTile / 2);
-              const uint64_t db = dv + (u % kRing) * (C::TILE_BYTES >> 4);
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk) {
                 if (kHalves > 1 && kk == kTile / 32) {
@@ -906,12 +924,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
               tc::commit(&pv_done[x]);
               ++done[x];
             }
-            if (ok) tc::commit(&kv_empty[u % kRing]);
+            if (ok) tc::commit(&kv_empty[st]);
           }
         if (!(ok = __all_sync(kAll, ok))) break;
       }
       if (!ok) break;
       u0 += 2 * it.n_kv + (it.parts == 1);
+      v0 += it.n_kv;
     }
   }
 
@@ -922,9 +941,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     if (threadIdx.x == 0) flag_status(a.status, PA_DEV_TIMEOUT);
     if (warp == kWarpSched && lane == 0)
       for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(&q_full[i & 1], (i >> 1) & 1);
-    if (warp == kWarpLoad && lane == 0)
-      for (int u = max(0, issued - kRing); u < issued; ++u)
-        mbar_wait(&kv_full[u % kRing], (u / kRing) & 1);
+    if (warp == kWarpLoad && lane == 0) {
+      for (int i = max(0, issued - kRing); i < issued; ++i)
+        mbar_wait(&k_full[i % kRing], (i / kRing) & 1);
+      for (int i = max(0, issued_v - kRing); i < issued_v; ++i)
+        mbar_wait(&v_full[i % kRing], (i / kRing) & 1);
+    }
     if ((warp == kWarpS || warp == kWarpPv) && elect_one()) {  // (who issued them)
       tc::commit(drain);
       mbar_wait(drain, 0);

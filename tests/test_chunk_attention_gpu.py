@@ -205,3 +205,26 @@ def test_infinite_scores_weigh_nothing(dtype, gone):
         assert st == 0
         check(out[p.rows(0)], ref, tol, f"split {split}")
         check_all(p, out, only=[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n_bad", [1, 2, 3, 5])
+def test_bad_sequences_among_short_ones(D, n_bad):
+    # rows of zeros take a place in the ring, but no product: units of one to three key
+    # tiles before and behind up to five of them
+    ctx, good = [], []
+    for i in range(80):
+        good.append(len(ctx))
+        ctx += [[130, 200, 256, 300, 100, 3, 384][i % 7]] + [60] * n_bad
+    p = Paged(ctx, [1 + b % 3 for b in range(len(ctx))], 8, 4, D, 16, torch.bfloat16, seed=n_bad)
+    bad = [b for b in range(len(ctx)) if b not in good]
+    p.context[bad] = 1 << 20
+    first = None
+    for _ in range(5):
+        out, st = run(p, split=False)
+        assert st == pk.PA_DEV_BAD_CONTEXT
+        check_all(p, out, only=good)
+        for b in bad:
+            assert (out[p.rows(b)] == 0).all()
+        first = out if first is None else first
+        assert torch.equal(out, first)
