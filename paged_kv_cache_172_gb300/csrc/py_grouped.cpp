@@ -10,6 +10,7 @@
 // (grouped.py) then looks for the one to complain about.
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
@@ -250,10 +251,11 @@ struct Cache {
   }
 };
 
+// A workspace argument: a tensor, or None.
 bool workspace_fits(PyObject* o, int device, void** p, size_t* bytes) {
   *p = nullptr;
   *bytes = 0;
-  if (o == Py_None) return true;
+  if (o == Py_None || o == Py_True) return true;
   const at::Tensor* t = tensor(o);
   if (t == nullptr || !t->is_cuda() || t->get_device() != device || !t->is_contiguous())
     return false;
@@ -262,8 +264,20 @@ bool workspace_fits(PyObject* o, int device, void** p, size_t* bytes) {
   return true;
 }
 
-// q, k_cache, v_cache, block_tables, context_lens, q_offsets, out, workspace,
-// status, max_context_len, scale, stream
+// A workspace for one call, from the pool of the stream that the call runs on: one
+// of another stream's pool could still be in use there, or be handed out again
+// before the call is done.
+at::Tensor workspace_for(size_t bytes, int device, PyObject* given, pa_stream_t s) {
+  const at::TensorOptions options =
+      at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)device);
+  if (given == Py_None) return at::empty({(int64_t)bytes}, options);
+  const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(
+      static_cast<cudaStream_t>(s), (c10::DeviceIndex)device));
+  return at::empty({(int64_t)bytes}, options);
+}
+
+// q, k_cache, v_cache, block_tables, context_lens, q_offsets, out, workspace (True:
+// one is allocated for the call), status, max_context_len, scale, stream
 PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> int {
     const at::Tensor *q = tensor(a[0]), *off = tensor(a[5]), *out = tensor(a[6]);
@@ -288,6 +302,14 @@ PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !stream_of(a[11], dev, &s))
       return kUnfit;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    at::Tensor own;
+    if (a[7] == Py_True) {
+      ws_bytes = pa_chunk_attention_workspace_size((int)B, (int)T, (int)H, (int)c.Hkv, (int)D, cap);
+      if (ws_bytes > 0) {
+        own = workspace_for(ws_bytes, dev, a[11], s);
+        ws = own.data_ptr();
+      }
+    }
     return pa_chunk_attention(data<void>(q), data<void>(c.k), data<void>(c.v),
                               data<int32_t>(c.bt), data<int32_t>(c.ctx), data<int32_t>(off),
                               (int)B, (int)T, (int)H, (int)c.Hkv, (int)D, type, stride(q),
@@ -296,8 +318,9 @@ PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// q, k_cache, v_cache, block_tables, context_lens, out, workspace, status,
-// max_context_len, partition_tokens, scale, stream
+// q, k_cache, v_cache, block_tables, context_lens, out, workspace (None: one is
+// allocated where the call needs it), status, max_context_len, partition_tokens,
+// scale, stream
 PyObject* decode_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> int {
     const at::Tensor *q = tensor(a[0]), *out = tensor(a[5]);
@@ -313,16 +336,26 @@ PyObject* decode_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dev = q->get_device();
     const ScalarType t = q->scalar_type();
     const int64_t B = q->size(0), H = q->size(1), D = q->size(2);
-    if (B > INT32_MAX || H > INT32_MAX || D > INT32_MAX || !dense(q, t, dev, {B, H, D}) ||
+    if (a[6] == Py_True || B > INT32_MAX || H > INT32_MAX || D > INT32_MAX ||
+        !dense(q, t, dev, {B, H, D}) ||
         !c.fits(a + 1, t, dev, B, D) || !dense(out, t, dev, {B, H, D}) ||
         !workspace_fits(a[6], dev, &ws, &ws_bytes) || !status_fits(a[7], dev) ||
         !stream_of(a[11], dev, &s))
       return kUnfit;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-    return pa_decode_grouped(data<void>(q), data<void>(c.k), data<void>(c.v),
-                             data<int32_t>(c.bt), data<int32_t>(c.ctx), (int)B, (int)H,
-                             (int)c.Hkv, (int)D, type, (int)c.bs, (int)c.NB, (int)c.M, cap, pt,
-                             scale, data<void>(out), ws, ws_bytes, status_of(a[7]), s);
+    auto call = [&]() {
+      return pa_decode_grouped(data<void>(q), data<void>(c.k), data<void>(c.v),
+                               data<int32_t>(c.bt), data<int32_t>(c.ctx), (int)B, (int)H,
+                               (int)c.Hkv, (int)D, type, (int)c.bs, (int)c.NB, (int)c.M, cap, pt,
+                               scale, data<void>(out), ws, ws_bytes, status_of(a[7]), s);
+    };
+    const int rc = call();
+    if (rc != PA_ERR_WORKSPACE || a[6] != Py_None) return rc;
+    ws_bytes = pa_decode_grouped_workspace_size((int)B, (int)H, (int)c.Hkv, (int)D, (int)c.bs, cap,
+                                                pt);
+    const at::Tensor own = workspace_for(ws_bytes, dev, a[11], s);
+    ws = own.data_ptr();
+    return call();
   });
 }
 

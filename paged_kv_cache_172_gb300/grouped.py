@@ -6,14 +6,14 @@ Argument marshalling only, as in ``_lib``: every step runs in the library's
 CUDA kernels.  The kernels of a single-token step take 2 to 6 us, less than
 checking and passing ten to seventeen tensors from Python (7 to 9 us), so these
 calls go through a compiled binding (``csrc/py_grouped.cpp``) that checks the
-arguments and makes the call; the functions here allocate what was left out and
-say which argument did not fit.
+arguments, allocates a workspace that was left out and makes the call; the
+functions here allocate outputs and say which argument did not fit.
 """
 from typing import NamedTuple
 
 import torch
 
-from ._lib import PA_ERR_WORKSPACE, _check, _ptr, lib
+from ._lib import _check, _ptr, lib
 
 _HALF = (torch.float16, torch.bfloat16)
 _UNFIT = -1  # the binding found an argument that does not fit
@@ -217,14 +217,6 @@ def pa_prompt_attention(q, k, v, q_offsets, scale, out=None, status=None, stream
     return out
 
 
-def _sized(fn, device, *args):
-    """A workspace size, which depends on the device, with that device current."""
-    if device.index == torch.cuda.current_device():
-        return fn(*args)
-    with torch.cuda.device(device):
-        return fn(*args)
-
-
 def pa_chunk_attention_workspace_size(B, T, H, Hkv, D, max_context_len):
     """Bytes of workspace pa_chunk_attention uses on the current device."""
     return lib().pa_chunk_attention_workspace_size(B, T, H, Hkv, D, max_context_len)
@@ -247,16 +239,11 @@ def pa_chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offset
         max_context_len = (_size(block_tables, 1) or 0) * (_size(k_cache, 1) or 0)
     if out is None:
         out = _empty(q.shape, q.dtype, q.device, stream)
+    own = split and workspace is None  # (allocated by the binding)
     if not split:
         workspace = None
-    elif workspace is None and q.is_cuda and q.dim() == 3 and q.shape[0] > 0:
-        need = _sized(pa_chunk_attention_workspace_size, q.device, (_size(q_offsets, 0) or 1) - 1,
-                      q.shape[0], q.shape[1], _size(k_cache, 2) or 0, q.shape[2],
-                      max_context_len)
-        if need:
-            workspace = _empty(need, torch.uint8, q.device, stream)
     rc = _binding().chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offsets,
-                                    out, workspace, status, max_context_len, scale,
+                                    out, own or workspace, status, max_context_len, scale,
                                     _handle(name, stream, q))
     if rc:
         B = None if _size(q_offsets, 0) is None else q_offsets.shape[0] - 1
@@ -278,6 +265,8 @@ def _cache_args(q, k_cache, v_cache, block_tables, context_lens, B):
 def _workspace_arg(workspace):
     if workspace is None:
         return ()
+    if not isinstance(workspace, torch.Tensor):
+        return (("workspace", workspace, None, ()),)
     return (("workspace", workspace, workspace.dtype, tuple(workspace.shape)),)
 
 
@@ -298,17 +287,9 @@ def pa_decode_grouped(q, k_cache, v_cache, block_tables, context_lens, scale, ma
         if not isinstance(q, torch.Tensor):
             raise TypeError(f"{name}: q must be a torch.Tensor")
         out = _empty(q.shape, q.dtype, q.device, stream)
-    handle = _handle(name, stream, q)
-    call = _binding().decode_grouped
-    rc = call(q, k_cache, v_cache, block_tables, context_lens, out, workspace, status,
-              max_context_len, partition_tokens, scale, handle)
-    if rc == PA_ERR_WORKSPACE and workspace is None:  # (most plans need none)
-        need = _sized(pa_decode_grouped_workspace_size, q.device, q.shape[0], q.shape[1],
-                      k_cache.shape[2], q.shape[2], k_cache.shape[1], max_context_len,
-                      partition_tokens)
-        workspace = _empty(need, torch.uint8, q.device, stream)
-        rc = call(q, k_cache, v_cache, block_tables, context_lens, out, workspace, status,
-                  max_context_len, partition_tokens, scale, handle)
+    rc = _binding().decode_grouped(q, k_cache, v_cache, block_tables, context_lens, out,
+                                   workspace, status, max_context_len, partition_tokens, scale,
+                                   _handle(name, stream, q))
     if rc:
         _failed(rc, name, q,
                 (("q", q, None, (None, None, None)),
