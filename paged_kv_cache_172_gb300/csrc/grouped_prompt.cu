@@ -48,11 +48,11 @@
 // Besides that a unit costs about 4,000 cycles around its end (last P V product,
 // output, next Q).  Measured (GB300, 32 heads on 8, D = 128, bf16): one prompt of
 // 16,001 tokens 1,258 us, 1,667 TFLOP/s, 0.86 of the measured burst rate and 0.95
-// of the sustained one; eight of 500-4,096 345 us, 1,459 TFLOP/s (0.75); chunks
-// of 512 on 3,584 (40 on 8, fp16) 273 us, 1,179 TFLOP/s (0.61: 704 units on 152
+// of the sustained one; eight of 500-4,096 349 us, 1,443 TFLOP/s (0.75); chunks
+// of 512 on 3,584 (40 on 8, fp16) 263 us, 1,225 TFLOP/s (0.63: 704 units on 152
 // SMs are five rounds where 4.6 would do, 125 rows of 128 are used, and with
 // all keys in L2 they are 1.5 % quicker); 16 chunks of 1-48 on up to 8,192 keys
-// 76 us, 3.9 TB/s (bound by the chain above over 32 key tiles, not by HBM).  A
+// 75 us, 4.0 TB/s (bound by the chain above over 32 key tiles, not by HBM).  A
 // launch reaches its first S product after 8,000 to 13,000 cycles: the search for
 // the first unit and the code of every role run from a cold instruction cache.
 #include <cuda_bf16.h>
