@@ -580,17 +580,18 @@ cudaError_t launch_t(const GroupedDecodeArgs& a, const void* k_cache, const void
 
 // Partition length where the caller leaves it open, 64 to 2,048 keys: the one of
 // least cost, the cost in microseconds over the traffic itself being that of the
-// last CTAs (0.0045 a key, 0.0073 at D = 64, whose keys take the same round trips
-// for half the bytes) and that of starting, ending and merging the grid's CTAs
-// (4.5 for each round of them, three to an SM).  Fitted to sweeps of eight
-// batches; measured against the least of each sweep: 38 ragged sequences of up
-// to 2,048 tokens (40 heads on 8) 33.1 us of 32.9, eight of 2,000-4,000 24.2 of
-// 23.8, one of 32,768 26.3 of 26.2, 38 at D = 64 14.3 of 14.3.
+// last CTAs (0.0045 a key, 0.0052 with two column tiles, 0.0073 at D = 64, whose keys
+// take the same round trips for half the bytes) and that of starting, ending and merging the grid's CTAs
+// (4.5 for each round of them, three to an SM).  Over sweeps of 81 batches 6 % above
+// the least on average: 38 ragged sequences of up to 2,048 tokens 32.7 us of 31.5 (40
+// heads on 2: 18.7 of 16.4), four of 60-131 thousand 257.2 of 257.1, one of 2,000 6.5 of
+// 5.6; furthest off where all sequences are alike and fill a round and a bit (64 x
+// 1,500 with 64 heads on 4: 50 of 37), which for ragged ones is right (26.2 of 25.8).
 int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context) {
   const int G = H / Hkv;
   const double pairs = (double)B * Hkv * (G <= 8 ? 1 : (G + 15) / 16);
   const int nsm = sm_count() > 0 ? sm_count() : 152;
-  const double per_key = D == 128 ? 0.0045 : 0.0073, per_cta = 4.5 / (3.0 * nsm);
+  const double per_key = D == 64 ? 0.0073 : G > 8 ? 0.0052 : 0.0045, per_cta = 4.5 / (3.0 * nsm);
   int best = kSpan;
   double least = 0.0;
   for (int p = kSpan; p <= kMaxPart; p += kSpan) {
