@@ -39,6 +39,7 @@
 // are rounded to the cache's type for the second product, the result once more.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <math.h>
 #include <string.h>
 
 #include <type_traits>
@@ -581,21 +582,32 @@ cudaError_t launch_t(const GroupedDecodeArgs& a, const void* k_cache, const void
 // Partition length where the caller leaves it open, 64 to 2,048 keys: the one of
 // least cost, the cost in microseconds over the traffic itself being that of the
 // last CTAs (0.0045 a key, 0.0052 with two column tiles, 0.0073 at D = 64, whose keys
-// take the same round trips for half the bytes) and that of starting, ending and merging the grid's CTAs
-// (4.5 for each round of them, three to an SM).  Over sweeps of 81 batches 6 % above
+// take the same round trips for half the bytes) and that of starting, ending and
+// merging the grid's CTAs (4.5 for each round of them, three to an SM).  Over sweeps of
+// 81 batches 4 % above
 // the least on average: 38 ragged sequences of up to 2,048 tokens 32.7 us of 31.5 (40
-// heads on 2: 18.7 of 16.4), four of 60-131 thousand 257.2 of 257.1, one of 2,000 6.5 of
-// 5.6; furthest off where all sequences are alike and fill a round and a bit (64 x
+// heads on 2: 18.7 of 16.4), four of 60-131 thousand 257.2 of 257.1; furthest off where all sequences are alike and fill a round and a bit (64 x
 // 1,500 with 64 heads on 4: 50 of 37), which for ragged ones is right (26.2 of 25.8).
+// A single sequence is as long as it may be and seldom fills the GPU: its keys count
+// more, its CTAs only past a quarter of those that run at once, and the merge with
+// them (2,000 keys 6.5 -> 6.1 us, with 64 heads on 4 7.6 -> 6.4, at D = 64 5.9 -> 4.6).
 int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context) {
   const int G = H / Hkv;
   const double pairs = (double)B * Hkv * (G <= 8 ? 1 : (G + 15) / 16);
   const int nsm = sm_count() > 0 ? sm_count() : 152;
   const double per_key = D == 64 ? 0.0073 : G > 8 ? 0.0052 : 0.0045, per_cta = 4.5 / (3.0 * nsm);
+  const double slots = (D == 128 ? 3.0 : 6.0) * nsm;  // CTAs at once
   int best = kSpan;
   double least = 0.0;
   for (int p = kSpan; p <= kMaxPart; p += kSpan) {
-    const double cost = per_key * p + per_cta * pairs * ((max_context + p - 1) / p);
+    const int parts = (max_context + p - 1) / p;
+    const double ctas = pairs * parts;
+    double cost = per_key * p + per_cta * ctas;
+    if (B == 1) {
+      cost = 0.0075 * p * (ctas > slots ? 0.7 : 1.0) + ceil(ctas / slots);
+      if (ctas > 0.25 * slots) cost += 6.0 * (ctas / slots - 0.25);
+      if (parts > 1) cost += grouped_decode_in_cluster(B, H, Hkv, parts) ? 0.8 : 2.0;
+    }
     if (p == kSpan || cost < least) {
       best = p;
       least = cost;
