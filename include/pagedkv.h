@@ -465,8 +465,9 @@ pa_status pa_block_copy(pa_half *k_cache, pa_half *v_cache,
  * int64 = blocks taken and blocks put so far, so it holds free_state[1] -
  * free_state[0] blocks, the next one at index free_state[0] mod num_blocks.
  * context_lens may be cached_lens itself.  free_state_out [2] receives the
- * state after the step and may be free_state itself; a caller returns a block by writing its id at free_state[1] mod
- * num_blocks and adding one to free_state[1].
+ * state after the step and may be free_state itself; a caller returns a block
+ * by writing its id at free_state[1] mod num_blocks and adding one to
+ * free_state[1].
  *
  * All or nothing: when the blocks needed exceed those held
  * (PA_DEV_NO_BLOCKS) or the new tokens exceed T_max (PA_DEV_BAD_CONTEXT), no
@@ -503,8 +504,8 @@ pa_status pa_step_plan(const int32_t *cached_lens, const int32_t *new_lens, int 
  * k_cache at slot_mapping[t]; v is copied to v_cache there.  Negative slots
  * skip the cache write (q_out and k_out are still written); a slot past the
  * pool is flagged PA_DEV_BAD_SLOT and skipped; what a slot
- * that two tokens share receives is undefined.  k_cache, v_cache, v and slot_mapping may all be
- * NULL: rotation only, k_out is then required.  q_out may be q and k_out may
+ * that two tokens share receives is undefined.  k_cache, v_cache, v and
+ * slot_mapping may all be NULL: rotation only, k_out is then required.  q_out may be q and k_out may
  * be k (the same pointer and stride), no other overlap is allowed.
  *
  * q [T, H, D], k and v [T, Hkv, D] with their strides; q_out, k_out likewise
@@ -567,8 +568,8 @@ pa_status pa_prompt_attention(const void *q, const void *k, const void *v,
  * are zeros; a bad block id reads as zeros, flagged PA_DEV_BAD_BLOCK_ID.
  *
  * D in {64, 128}; block_size in {8, 16, 32}; max_context_len at most
- * max_blocks_per_seq * block_size and below 2^31 - 32768; (num_blocks + 1) * block_size * Hkv below
- * 2^31.  workspace (16-byte aligned, may be NULL): with at least
+ * max_blocks_per_seq * block_size and below 2^31 - 32768; (num_blocks + 1) *
+ * block_size * Hkv below 2^31.  workspace (16-byte aligned, may be NULL): with at least
  * pa_chunk_attention_workspace_size(...) bytes, few and long chunks are cut
  * into key ranges merged by log-sum-exp, which fills the GPU; without it every
  * unit runs whole (same result up to rounding).  Smaller and not NULL:
@@ -596,7 +597,8 @@ pa_status pa_chunk_attention(const void *q, const void *k_cache, const void *v_c
  * negative one gives zeros.  partition_tokens: a multiple of 64 up to 2048, or
  * 0 to choose.  The workspace size depends on the SM count of the current device;
  * it is 0 where one partition holds the longest context or all partitions fit
- * the GPU at once (they then merge inside the launch).  D in {64, 128}; block_size in {8, 16, 32}; B at most 65535;
+ * the GPU at once (they then merge inside the launch).  D in {64, 128};
+ * block_size in {8, 16, 32}; B at most 65535;
  * any finite scale; (num_blocks + 1) * block_size * Hkv below 2^31.
  * ------------------------------------------------------------------------- */
 size_t pa_decode_grouped_workspace_size(int B, int H, int Hkv, int D, int block_size,

@@ -584,10 +584,10 @@ cudaError_t launch_t(const GroupedDecodeArgs& a, const void* k_cache, const void
 // last CTAs (0.0045 a key, 0.0052 with two column tiles, 0.0073 at D = 64, whose keys
 // take the same round trips for half the bytes) and that of starting, ending and
 // merging the grid's CTAs (4.5 for each round of them, three to an SM).  Over sweeps of
-// 81 batches 4 % above
-// the least on average: 38 ragged sequences of up to 2,048 tokens 32.7 us of 31.5 (40
-// heads on 2: 18.7 of 16.4), four of 60-131 thousand 257.2 of 257.1; furthest off where all sequences are alike and fill a round and a bit (64 x
-// 1,500 with 64 heads on 4: 50 of 37), which for ragged ones is right (26.2 of 25.8).
+// 81 batches 4 % above the least on average: 38 ragged sequences of up to 2,048 tokens
+// 32.7 us of 31.5 (40 heads on 2: 18.7 of 16.4), four of 60-131 thousand 257.2 of 257.1;
+// furthest off where all sequences are alike and fill a round and a bit (64 x 1,500 with
+// 64 heads on 4: 50 of 37), which for ragged ones is right (26.2 of 25.8).
 // A single sequence is as long as it may be and seldom fills the GPU: its keys count
 // more, its CTAs only past a quarter of those that run at once, and the merge with
 // them (2,000 keys 6.5 -> 6.1 us, with 64 heads on 4 7.6 -> 6.4, at D = 64 5.9 -> 4.6).

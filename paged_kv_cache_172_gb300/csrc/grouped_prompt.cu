@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             }
           }
 #pragma unroll
-          for (int c = kC * h; c < kC * h + kC; ++c)  // the packed pairs as they lie in the registers
+          for (int c = kC * h; c < kC * h + kC; ++c)  // the packed pairs, as in the registers
             tc::st_32x16(tmem + t_lane + kColP + x * (kTile / 2) + c * 16, r[c]);
           tc::wait_st();
           tc::fence_before_sync();

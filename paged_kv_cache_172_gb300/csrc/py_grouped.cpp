@@ -124,8 +124,8 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
 // max_tokens, stream
 PyObject* step_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 14, [&]() -> int {
-    const at::Tensor *c = tensor(a[0]), *nw = tensor(a[1]), *bt = tensor(a[2]), *ring = tensor(a[3]),
-                     *st = tensor(a[4]), *ctx = tensor(a[5]), *off = tensor(a[6]),
+    const at::Tensor *c = tensor(a[0]), *nw = tensor(a[1]), *bt = tensor(a[2]),
+                     *ring = tensor(a[3]), *st = tensor(a[4]), *ctx = tensor(a[5]), *off = tensor(a[6]),
                      *slot = tensor(a[7]), *pos = tensor(a[8]), *so = tensor(a[9]);
     int bs, T;
     pa_stream_t s;

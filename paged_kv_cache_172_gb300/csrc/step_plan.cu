@@ -17,9 +17,10 @@
 // tokens and of the fresh table entries by binary search; a token in a fresh
 // block takes the id from the ring, not from the table another CTA may still
 // be writing.  The ring's state is written behind a cluster barrier, as the
-// lengths are, so both may be updated in place.  The work is a few hundred kilobytes at most: the call
-// is bound by its launch and by two trips to memory (lengths, then ring
-// entries), and one launch instead of a scan and a fill is what counts.
+// lengths are, so both may be updated in place.  The work is a few hundred
+// kilobytes at most: the call is bound by its launch and by two trips to memory
+// (lengths, then ring entries), and one launch instead of a scan and a fill is
+// what counts.
 // Measured (GB300): 38 single tokens 3.4 us, 200 sequences with 11,000 new tokens
 // 6.1 us, of which the launch of an empty kernel is about two thirds.
 #include <cooperative_groups.h>
