@@ -978,36 +978,31 @@ __global__ void __launch_bounds__(32 * kMergeWarps) grouped_merge_kernel(const G
   // The lengths come from before the attention kernel, which let this one start only
   // when all its blocks had waited for them: they are read while it still runs.
   int parts = 0;  // of this lane's row; 0: nothing to merge
-  // The sequence that holds a row is found by halving where the offsets rise.  Where
-  // some do not, the sequences that they belong to are not computed, but the others
-  // are, and a row's one is found by looking at them all.
-  int falls = 0;
-  for (int b = lane; b < a.B; b += 32) falls |= a.q_offsets[b] > a.q_offsets[b + 1];
-  const bool rising = !__any_sync(kAll, falls);
-  if (r < plane) {
-    const int t = (int)(r / a.G);
-    int lo = 0;
-    if (!rising) {
-      while (lo < a.B - 1) {
-        const Seq s = sequence<true>(a, lo);
-        if (!s.lost && t >= s.start && t < s.start + s.ql) break;
-        ++lo;
-      }
-    } else if (t >= a.q_offsets[0] && t < a.q_offsets[a.B]) {
-      int hi = a.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_offsets[mid] <= t)
-          lo = mid;
-        else
-          hi = mid;
-      }
+  const int t = r < plane ? (int)(r / a.G) : -1;
+  Seq s = {0, 0, 0, 0, true, true};  // the sequence that holds row t
+  auto holds = [&]() { return !s.lost && t >= s.start && t < s.start + s.ql; };
+  if (t >= 0) {  // by halving, as offsets rise
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.q_offsets[mid] <= t)
+        lo = mid;
+      else
+        hi = mid;
     }
-    const Seq s = sequence<true>(a, lo);
-    if (!s.bad && t >= s.start && t < s.start + s.ql)
-      parts = unit_parts(unit_tiles(s, a.span, divide(t - s.start, a.by_span)), a.split);
-    if (parts == 1) parts = 0;  // (written by its only part)
+    s = sequence<true>(a, lo);
   }
+  // A row of no sequence, or one beside offsets that fall: the sequences that these
+  // belong to are not computed, but the others are, and looking at all finds theirs.
+  if (__any_sync(kAll, t >= 0 && !holds())) {
+    int falls = 0;
+    for (int b = lane; b < a.B; b += 32) falls |= a.q_offsets[b] > a.q_offsets[b + 1];
+    if (__any_sync(kAll, falls) && t >= 0)
+      for (int b = 0; b < a.B && !holds(); ++b) s = sequence<true>(a, b);
+  }
+  if (t >= 0 && !s.bad && holds())
+    parts = unit_parts(unit_tiles(s, a.span, divide(t - s.start, a.by_span)), a.split);
+  if (parts == 1) parts = 0;  // (written by its only part)
   pdl_wait();
   pdl_launch_dependents();
   const int most = __reduce_max_sync(kAll, parts);
