@@ -136,10 +136,10 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
   const int first = rank * kPlanThreads + tid, step = ranks * kPlanThreads;
   // ---- per sequence
   for (int b = first; b <= a.B; b += step) a.q_offsets[b] = fits ? s_tok[b] : 0;
-  const int h0 = held > 0 ? (int)(head % a.num_blocks) : 0;
+  const unsigned h0 = held > 0 ? (unsigned)(head % a.num_blocks) : 0;
   auto ring_id = [&](int i) {  // i-th fresh block of the step; -1 if the entry is bad
-    int at = h0 + i;           // h0, i < num_blocks
-    if (at >= a.num_blocks) at -= a.num_blocks;
+    unsigned at = h0 + (unsigned)i;  // h0, i < num_blocks, their sum below 2^32
+    if (at >= (unsigned)a.num_blocks) at -= (unsigned)a.num_blocks;
     const int id = a.free_blocks[at];
     if (id >= 0 && id < a.num_blocks) return id;
     flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
