@@ -443,7 +443,7 @@ pa_status pa_block_copy(pa_half *k_cache, pa_half *v_cache,
  * tokens in elements, a multiple of 8 and at least heads * D.  Outputs of
  * attention are contiguous.  None of these calls keeps anything between
  * calls, so they may run on several streams and be captured; a workspace
- * belongs to one call at a time.
+ * belongs to one call at a time.  T is below 2^31 - 32768.
  * ========================================================================= */
 
 /* ---------------------------------------------------------------------------

@@ -105,7 +105,8 @@ pa_status pa_rope_cache_write(const void* q, const void* k, const void* v,
                               int block_size, int num_blocks, void* q_out, int64_t q_out_stride,
                               void* k_out, int64_t k_out_stride, void* k_cache, void* v_cache,
                               int32_t* status, pa_stream_t stream) {
-  if (T < 0 || !heads_ok(H, Hkv) || !dtype_ok(dtype) || n_axes < 1 || n_axes > 4)
+  if (T < 0 || T > kMaxCount || !heads_ok(H, Hkv) || !dtype_ok(dtype) || n_axes < 1 ||
+      n_axes > 4)
     return PA_ERR_INVALID;
   if (D != 64 && D != 128) return PA_ERR_UNSUPPORTED;
   if (rotary_dim < 16 || rotary_dim > D || rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
@@ -209,7 +210,7 @@ pa_status pa_prompt_attention(const void* q, const void* k, const void* v,
                               pa_stream_t stream) {
   const pa_status st = attention_args(B, H, Hkv, D, dtype);
   if (st != PA_OK) return st;
-  if (T < 0) return PA_ERR_INVALID;
+  if (T < 0 || T > kMaxCount) return PA_ERR_INVALID;
   if (B > 0 && T > 0 && (!rows_ok(k, k_stride, Hkv, D) || !rows_ok(v, v_stride, Hkv, D)))
     return PA_ERR_INVALID;
   pk::GroupedArgs a = {};
@@ -243,7 +244,7 @@ pa_status pa_chunk_attention(const void* q, const void* k_cache, const void* v_c
   pa_status st = attention_args(B, H, Hkv, D, dtype);
   if (st != PA_OK) return st;
   if (!paged_block(block_size)) return PA_ERR_UNSUPPORTED;
-  if (T < 0) return PA_ERR_INVALID;
+  if (T < 0 || T > kMaxCount) return PA_ERR_INVALID;
   pk::GroupedArgs a = {};
   a.split = 1;
   if (B > 0 && T > 0) {
