@@ -229,7 +229,8 @@ pa_status pa_prompt_attention(const void* q, const void* k, const void* v,
 
 size_t pa_chunk_attention_workspace_size(int B, int T, int H, int Hkv, int D,
                                          int max_context_len) {
-  if (B <= 0 || T <= 0 || !heads_ok(H, Hkv) || (D != 64 && D != 128) || max_context_len <= 0)
+  if (B <= 0 || T <= 0 || T > kMaxCount || !heads_ok(H, Hkv) || (D != 64 && D != 128) ||
+      max_context_len <= 0 || max_context_len > kMaxCount)
     return 0;
   return pk::grouped_workspace_bytes(B, T, H, Hkv, D, max_context_len);
 }
@@ -288,7 +289,7 @@ static int decode_partition(int B, int H, int Hkv, int D, int max_context,
 size_t pa_decode_grouped_workspace_size(int B, int H, int Hkv, int D, int block_size,
                                         int max_context_len, int partition_tokens) {
   if (B <= 0 || !heads_ok(H, Hkv) || (D != 64 && D != 128) || !paged_block(block_size) ||
-      max_context_len <= 0 || partition_tokens < 0)
+      max_context_len <= 0 || max_context_len > kMaxCount || partition_tokens < 0)
     return 0;
   const int pt = decode_partition(B, H, Hkv, D, max_context_len, partition_tokens);
   const long long parts = ((long long)max_context_len + pt - 1) / pt;
