@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 #pragma unroll
           for (int e = 0; e < kWindow / 32; ++e) {
             const int lb = win + lane + 32 * e;
-            ent[e] = lb < nblk ? __ldg(a.block_tables + (size_t)it.b * a.max_blocks + lb)
+            ent[e] = lb < nblk ? a.block_tables[(size_t)it.b * a.max_blocks + lb]
                                : a.num_blocks;  // past the sequence: zeros
           }
 #pragma unroll
