@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
       const int lb = kt0 * BPT + lane + 32 * k;
-      ent0[k] = lb < nblk_seq ? __ldg(a.block_tables + (size_t)b * a.max_blocks + lb)
+      ent0[k] = lb < nblk_seq ? a.block_tables[(size_t)b * a.max_blocks + lb]
                               : a.num_blocks;
     }
   }
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kPerLane; ++k) {
             const int lb = win + lane + 32 * k;
-            ent[k] = lb < nblk_seq ? __ldg(a.block_tables + (size_t)b * a.max_blocks + lb)
+            ent[k] = lb < nblk_seq ? a.block_tables[(size_t)b * a.max_blocks + lb]
                                    : a.num_blocks;  // past the sequence: zeros
           }
         }

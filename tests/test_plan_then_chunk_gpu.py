@@ -65,3 +65,37 @@ def test_fresh_entries_are_seen(B, captured):
             at = torch.as_tensor(j % bs, device=DEV)
             ref, tol = attend(q[b * n:(b + 1) * n], kc[blk, at], vc[blk, at], D ** -0.5, ctx - n)
             check(outs[i][b * n:(b + 1) * n], ref, tol, f"step {i} sequence {b}")
+
+
+@pytest.mark.parametrize("bs", [4, 16])
+def test_fresh_entries_are_seen_by_padded_chunks(bs):
+    # pa_prefill_chunk, directly behind the plan: one K/V head a query head, padded rows
+    B, H, D, n, steps = 12, 2, 64, 9, 12
+    M = 128 // bs
+    NB = B * M
+    g = torch.Generator(device=DEV).manual_seed(bs)
+    kc, vc = (torch.randn(NB, bs, H, D, generator=g, device=DEV).half() for _ in range(2))
+    q = torch.randn(B, H, n, D, generator=g, device=DEV).half()
+    ring = torch.randperm(NB, generator=g, device=DEV).int()
+    tables = torch.full((B, M), -1, dtype=torch.int32, device=DEV)
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+    state = torch.tensor([0, NB], dtype=torch.int64, device=DEV)
+    new = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    plan = pk.StepPlan.empty(B, B * n, DEV)._replace(context_lens=lens, free_state=state)
+    status = zero_status(DEV)
+    outs = []
+    for _ in range(steps):
+        p = pk.pa_step_plan(lens, new, tables, ring, state, bs, B * n, out=plan, status=status)
+        outs.append(pk.pa_prefill_chunk(q, kc, vc, tables, p.context_lens, D ** -0.5,
+                                        status=status))
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    rows = tables.long().cpu().numpy()
+    for i in range(0, steps, 3):
+        for b in range(0, B, 5):
+            ctx = (i + 1) * n
+            j = np.arange(ctx)
+            blk = torch.as_tensor(rows[b, j // bs], device=DEV)
+            at = torch.as_tensor(j % bs, device=DEV)
+            ref, tol = attend(q[b].transpose(0, 1), kc[blk, at], vc[blk, at], D ** -0.5, ctx - n)
+            check(outs[i][b].transpose(0, 1), ref, tol, f"step {i} sequence {b}")
