@@ -473,7 +473,10 @@ pa_status pa_block_copy(pa_half *k_cache, pa_half *v_cache,
  * (PA_DEV_NO_BLOCKS) or the new tokens exceed T_max (PA_DEV_BAD_CONTEXT), no
  * block is taken and the step is empty: context_lens = cached, offsets 0,
  * slots -1.  A sequence with a negative length, or that outgrows its table
- * row, is flagged PA_DEV_BAD_CONTEXT, adds nothing and gets context 0.  An id
+ * row, is flagged PA_DEV_BAD_CONTEXT, adds nothing and gets context 0; where
+ * context_lens is cached_lens its length stays as it was, so that it is flagged
+ * again in the next step and its blocks are not taken for a new sequence's (with
+ * lengths in two buffers that is the caller's to see to).  An id
  * outside [0, num_blocks), in the ring or in the block that new tokens
  * continue, is flagged PA_DEV_BAD_BLOCK_ID: its tokens get slot -1 (and a
  * fresh entry -1).

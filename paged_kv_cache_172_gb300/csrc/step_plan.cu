@@ -185,7 +185,10 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
   for (int b = first; b < a.B; b += step) {
     const long long c = a.cached_lens[b], n = a.new_lens[b];
     const bool bad = c < 0 || n < 0 || c + n > cap;
-    a.context_lens[b] = bad ? 0 : (int32_t)(fits ? c + n : c);
+    // (In place a bad sequence keeps its length: as 0 it would be a new sequence to the
+    // next step, which would fill its row with fresh blocks and flag nothing.)
+    if (!bad || a.context_lens != a.cached_lens)
+      a.context_lens[b] = bad ? 0 : (int32_t)(fits ? c + n : c);
   }
   if (rank == 0 && tid == 0) {
     a.free_state_out[0] = head + fresh;

@@ -116,7 +116,9 @@ def pa_step_plan(cached_lens, new_lens, block_tables, free_blocks, free_state, b
     taken and put so far; the ring itself is only read).  Returns a StepPlan, in
     ``out`` when given (``StepPlan.empty``): context_lens [B], q_offsets [B+1],
     slot_mapping and positions [max_tokens] (-1 and 0 behind the last token) and
-    the new free_state (out's may be the one passed in).  A step that does not fit
+    the new free_state (out's may be the one passed in, as context_lens may be
+    cached_lens).  A bad sequence (a negative length, or one past its table row) is
+    flagged PA_DEV_BAD_CONTEXT and gets context 0, or keeps its length in place.  A step that does not fit
     the ring (PA_DEV_NO_BLOCKS) or max_tokens (PA_DEV_BAD_CONTEXT) plans nothing."""
     name = "pa_step_plan"
     if out is None:
