@@ -592,7 +592,9 @@ pa_status pa_chunk_attention(const void *q, const void *k_cache, const void *v_c
 /* ---------------------------------------------------------------------------
  * Decode with grouped heads: one query token per sequence.
  *
- * pa_decode's result where G = H / Hkv query heads read each K/V head, which
+ * pa_decode's result (the softmax weights enter their product with v to 2^-15 in
+ * bf16 and 2^-21 in fp16, the result is rounded once) where G = H / Hkv query heads
+ * read each K/V head, which
  * comes from memory once for all of them (up to 16; more take it once for
  * every 16).  Arguments, errors and the workspace rule as for pa_decode, with
  * q and out [B, H, D] and the cache [num_blocks, block_size, Hkv, D] in dtype;
