@@ -594,9 +594,8 @@ pa_status pa_chunk_attention(const void *q, const void *k_cache, const void *v_c
  *
  * pa_decode's result (the softmax weights enter their product with v to 2^-15 in
  * bf16 and 2^-21 in fp16, the result is rounded once) where G = H / Hkv query heads
- * read each K/V head, which
- * comes from memory once for all of them (up to 16; more take it once for
- * every 16).  Arguments, errors and the workspace rule as for pa_decode, with
+ * read each K/V head, which comes from memory once for all of them (up to 16; more
+ * take it once for every 16).  Arguments, errors and the workspace rule as for pa_decode, with
  * q and out [B, H, D] and the cache [num_blocks, block_size, Hkv, D] in dtype;
  * a context past max_context_len is flagged PA_DEV_BAD_CONTEXT and cut to it, a
  * negative one gives zeros.  partition_tokens: a multiple of 64 up to 2048, or
