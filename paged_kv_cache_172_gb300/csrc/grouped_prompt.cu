@@ -40,7 +40,8 @@
 // Rounding: scores, maxima, sums and O are fp32; P is rounded to the 16-bit
 // type of the inputs (the tensor core's operand; its values are at most 2^8
 // before scaling, since O is rescaled only when the maximum grew by more than
-// that), the result once more at the end.
+// that; in fp16 times 2^6, so that many small weights are not lost below its
+// smallest step), the result once more at the end.
 //
 // Bound: the tensor pipe by intensity; in the steady state the chain from one S
 // product to the next through the one S region (2 x 1,320 cycles per pair of
@@ -81,6 +82,11 @@ constexpr int kWindow = 256;             // block-table entries staged at a time
 constexpr int kMaxRing = 8;
 constexpr int kBars = 4 * kMaxRing + 14 + 2 * kItems + 1;
 constexpr float kLazy = 8.0f;            // log2 of the growth that forces a rescale
+// log2 of what weights are multiplied by (which the quotient drops): fp16 holds them in
+// steps of 2^-24 at least, and 2^6 makes that 2^-30 of the largest.  (The largest is then
+// 2^14, far enough below 2^16 for an exponent that rounding raises.)
+template <typename T>
+constexpr float kRaiseLog2 = std::is_same<T, __half>::value ? 6.0f : 0.0f;
 
 // Layout of a K or V tile in shared memory.  Paged: key groups of 8 keys x D
 // dims, each the 1 KB atoms of dims 0-63 and 64-127 (the order in which a
@@ -324,6 +330,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   // 64 keys early (one prompt of 8,192 353 -> 343 us); with the paged loader's code
   // beside it the longer loops cost more than that (16 x 2,048 keys 457 -> 470 us).
   constexpr int kHalves = PAGED ? 1 : 2;
+  constexpr float kRaise = kRaiseLog2<T>;
   constexpr uint32_t kIdS = tc::idesc_f16_f32(kTile, kTile, false, false) | operand_type<T>();
   constexpr uint32_t kIdO = tc::idesc_f16_f32(kTile, D, false, true) | operand_type<T>();
   extern __shared__ uint8_t smem_dyn[];
@@ -475,7 +482,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         // A row that has seen masked keys alone (a part whose range starts past
         // its position) has m = -inf, and -inf + inf is NaN: taken with maximum 0
         // its weights are all zero and its partial row is empty.
-        const float neg_m = m == -INFINITY ? 0.f : -m;
+        const float neg_m = m == -INFINITY ? 0.f : kRaise - m;
         float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
