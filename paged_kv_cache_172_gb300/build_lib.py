@@ -8,6 +8,7 @@ with g++ into ``_grouped.so`` beside it.  Objects go to
 """
 import glob
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -53,8 +54,9 @@ def _compile(src, extra, obj_dir):
 
 
 def _torch_dir():
-    import torch
-    return os.path.dirname(torch.__file__)
+    """Where torch is installed, None where it is not."""
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None else os.path.dirname(spec.origin)
 
 
 def _compile_binding(obj_dir):
@@ -64,7 +66,7 @@ def _compile_binding(obj_dir):
     obj = os.path.join(obj_dir, "py_grouped.o")
     if (os.path.exists(obj) and os.path.getmtime(obj) >= os.path.getmtime(src)
             and os.path.getmtime(obj) >= _headers_mtime()):
-        return obj, None
+        return obj
     tdir = os.path.join(_torch_dir(), "include")
     system = [tdir, os.path.join(tdir, "torch", "csrc", "api", "include"),
               sysconfig.get_paths()["include"],
@@ -73,8 +75,8 @@ def _compile_binding(obj_dir):
            *(x for d in system for x in ("-isystem", d)), "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        return obj, f"error: $ {' '.join(cmd)}\n{r.stdout}\n{r.stderr}"
-    return obj, None
+        raise RuntimeError(f"g++ failed:\n$ {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
 
 
 def _link_binding(obj, lib):
@@ -92,7 +94,8 @@ def _link_binding(obj, lib):
 
 
 def build(verbose: bool = False, extra_flags=(), out=None, sources=None) -> str:
-    """Compile and link the library, and the binding of its grouped-head calls.
+    """Compile and link the library, then the binding of its grouped-head calls (left
+    out where torch is not installed; an error of its own, with the library in place).
     ``extra_flags`` (e.g. -D tuning macros) build a variant with its own object
     directory; ``out`` names its library path; ``sources`` (file names in csrc/)
     limits a variant to those files; a variant has no binding."""
@@ -108,15 +111,14 @@ def build(verbose: bool = False, extra_flags=(), out=None, sources=None) -> str:
         srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     else:
         srcs = [os.path.join(CSRC, s) for s in sources]
-    binding = None
+    with_binding = product and _torch_dir() is not None
+    if product and not with_binding:
+        print("torch is not installed: the library is built without the Python binding of its "
+              "grouped-head calls", file=sys.stderr)
     with ThreadPoolExecutor(max_workers=min(os.cpu_count() or 8, len(srcs) + 1)) as ex:
-        if product:
-            binding = ex.submit(_compile_binding, obj_dir)
+        binding = ex.submit(_compile_binding, obj_dir) if with_binding else None
         results = list(ex.map(lambda s: _compile(s, list(extra_flags), obj_dir), srcs))
-    if binding is not None:
-        binding = binding.result()
-    errors = [msg for _, msg in results + ([binding] if binding else [])
-              if msg and "error" in msg.lower()]
+    errors = [msg for _, msg in results if msg and "error" in msg.lower()]
     if errors:
         raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
     if verbose:
@@ -124,19 +126,21 @@ def build(verbose: bool = False, extra_flags=(), out=None, sources=None) -> str:
             if msg:
                 print(msg, file=sys.stderr)
     objs = [o for o, _ in results]
-    if (os.path.exists(lib)
+    if not (os.path.exists(lib)
             and all(os.path.getmtime(lib) >= os.path.getmtime(o) for o in objs)):
-        if binding is not None:
-            _link_binding(binding[0], lib)
-        return lib
-    tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n$ {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, lib)
-    if binding is not None:
-        _link_binding(binding[0], lib)
+        tmp = lib + f".tmp{os.getpid()}"
+        cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n$ {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, lib)
+    if binding is not None:  # the library stands whatever becomes of it
+        try:
+            _link_binding(binding.result(), lib)
+        except RuntimeError:
+            if os.path.exists(BINDING):  # of other sources
+                os.remove(BINDING)
+            raise
     return lib
 
 
