@@ -61,22 +61,37 @@ def _torch_dir():
 
 def _compile_binding(obj_dir):
     """The Python binding of the grouped-head calls: host C++ against torch's and
-    Python's headers."""
+    Python's headers.  Kept while its source, the headers, the command, torch and
+    Python are those it was compiled with."""
     src = os.path.join(CSRC, "py_grouped.cpp")
     obj = os.path.join(obj_dir, "py_grouped.o")
-    if (os.path.exists(obj) and os.path.getmtime(obj) >= os.path.getmtime(src)
-            and os.path.getmtime(obj) >= _headers_mtime()):
-        return obj
-    tdir = os.path.join(_torch_dir(), "include")
+    torch_dir = _torch_dir()
+    tdir = os.path.join(torch_dir, "include")
     system = [tdir, os.path.join(tdir, "torch", "csrc", "api", "include"),
               sysconfig.get_paths()["include"],
               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE,
            *(x for d in system for x in ("-isystem", d)), "-c", src, "-o", obj]
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        made_with = "\n".join([sys.version, " ".join(cmd), f.read()])
+    stamp = obj + ".made_with"
+    if (os.path.exists(obj) and os.path.getmtime(obj) >= os.path.getmtime(src)
+            and os.path.getmtime(obj) >= _headers_mtime() and _read(stamp) == made_with):
+        return obj
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed:\n$ {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(made_with)
     return obj
+
+
+def _read(path):
+    """A file's text, None where there is none."""
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
 
 
 def _link_binding(obj, lib):

@@ -61,3 +61,23 @@ def test_library_is_linked_where_the_binding_does_not_compile(tree):
     assert "g++" in r.stderr and "broken on purpose" in r.stderr and "nvcc failed" not in r.stderr
     check_library(tree)
     assert not (tree / "_grouped.so").exists()  # a binding of other sources does not stay
+
+
+def test_binding_follows_torch(tree):
+    # the same place, another version: what was compiled against the older one is not kept
+    real = os.path.dirname(importlib.util.find_spec("torch").origin)
+    fake = tree / "site" / "torch"
+    (fake / "include").mkdir(parents=True)
+    (fake / "lib").symlink_to(os.path.join(real, "lib"))
+    (fake / "__init__.py").write_text("")
+    obj = tree / "_build" / "py_grouped.o"
+    before = "sys.path.insert(0, os.path.join(at, 'site'))"
+    times = []
+    for version in ("2.9.1", "2.9.1", "2.11.0"):
+        (fake / "version.py").write_text(f"__version__ = {version!r}\n")
+        r = run(tree, before=before)
+        assert r.returncode == 0, r.stderr
+        times.append((obj.stat().st_mtime_ns, (tree / "_grouped.so").stat().st_mtime_ns))
+    assert times[0] == times[1]
+    assert times[2][0] > times[1][0] and times[2][1] > times[1][1]
+    check_library(tree)
