@@ -29,10 +29,10 @@
 // grid fits at once, otherwise through the workspace in a second, dependent
 // launch.
 //
-// Measured (GB300): 4 x 60-131 thousand keys, 64 heads on 8, bf16: 249 us, 6.78
+// Measured (GB300): 4 x 60-131 thousand keys, 64 heads on 8, bf16: 250 us, 6.76
 // TB/s of keys and values, 1.01 of the measured copy rate; 38 sequences of
-// 128-2,048 keys, 40 on 8, fp16: 32.8 us, 5.3 TB/s (the start, the last CTAs and
-// the merge are 8 us of it); one of 1,000 keys, 32 on 8: 5.0 us, of which a launch
+// 128-2,048 keys, 40 on 8, fp16: 33.5 us, 5.2 TB/s (the start, the last CTAs and
+// the merge are 8 us of it); one of 1,000 keys, 32 on 8: 5.3 us, of which a launch
 // and four trips to memory are all.
 //
 // Rounding: scores, maxima, sums and outputs in fp32; the weights 2^(s - m) <= 1
@@ -619,20 +619,24 @@ cudaError_t launch_t(const GroupedDecodeArgs& a, const void* k_cache, const void
 // least cost, the cost in microseconds over the traffic itself being that of the
 // last CTAs (0.0045 a key, 0.0052 with two column tiles, 0.0073 at D = 64, whose keys
 // take the same round trips for half the bytes) and that of starting, ending and
-// merging the grid's CTAs (4.5 for each round of them, three to an SM).  Over sweeps of
-// 81 batches 4 % above the least on average: 38 ragged sequences of up to 2,048 tokens
-// 32.7 us of 31.5 (40 heads on 2: 18.7 of 16.4), four of 60-131 thousand 257.2 of 257.1;
-// furthest off where all sequences are alike and fill a round and a bit (64 x 1,500 with
-// 64 heads on 4: 50 of 37), which for ragged ones is right (26.2 of 25.8).
+// merging the grid's CTAs (4.5 for each round of them, three to an SM).  Fitted over
+// sweeps of 81 batches, 4 % above the least on average, with weights of one rounding;
+// now 38 ragged sequences of up to 2,048 tokens 33.4 us of 32.5 (40 heads on 2: 22.5 of
+// 19.1), four of 60-131 thousand 244.6 of 244.4; furthest off where all sequences are
+// alike and fill a round and a bit (64 x 1,500 with 64 heads on 4: 51.7 of 39.1), which
+// for ragged ones is right (27.6 of 26.5).
 // A single sequence is as long as it may be and seldom fills the GPU: its keys count
 // more, its CTAs only past a quarter of those that run at once, and the merge with
-// them (2,000 keys 6.5 -> 6.1 us, with 64 heads on 4 7.6 -> 6.4, at D = 64 5.9 -> 4.6).
+// them (2,000 keys 6.5 -> 6.1 us, with 64 heads on 4 7.6 -> 6.4, at D = 64 5.9 -> 4.6
+// with weights of one rounding; now 6.6, 6.8 and 4.9, the least 5.9, 6.8 and 4.9).
 int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context) {
   const int G = H / Hkv;
   const double pairs = (double)B * Hkv * (G <= 8 ? 1 : (G + 15) / 16);
   const int nsm = sm_count() > 0 ? sm_count() : 152;
   const double per_key = D == 64 ? 0.0073 : G > 8 ? 0.0052 : 0.0045, per_cta = 4.5 / (3.0 * nsm);
-  const double slots = (D == 128 ? 3.0 : 6.0) * nsm;  // CTAs at once
+  // CTAs at once, as fitted (by shared memory; with two column tiles at D = 64 the
+  // registers of the kernel without clusters leave room for four)
+  const double slots = (D == 128 ? 3.0 : 6.0) * nsm;
   int best = kSpan;
   double least = 0.0;
   for (int p = kSpan; p <= kMaxPart; p += kSpan) {
@@ -658,7 +662,7 @@ int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context) {
 // them until the last is done: worth it while the whole grid does, with room to
 // place the clusters (at most 2.6 CTAs an SM of the 3 it holds).  One sequence of
 // 1,000 tokens 5.7 -> 5.0 us, eight of 2,000-4,000 in 384 CTAs 23.6 -> 22.2; past
-// that 38 ragged sequences in 608 CTAs 33.1 -> 38.1.
+// that 38 ragged sequences in 608 CTAs 33.1 -> 38.1 (weights of one rounding).
 bool grouped_decode_in_cluster(int B, int H, int Hkv, long long parts) {
   const int G = H / Hkv, nsm = sm_count() > 0 ? sm_count() : 152;
   const double ctas = (double)B * Hkv * (G <= 8 ? 1 : (G + 15) / 16) * parts;

@@ -47,15 +47,19 @@
 // product to the next through the one S region (2 x 1,320 cycles per pair of
 // tiles, where four products take 2,048), and over long prompts the power cap.
 // Besides that a unit costs about 4,000 cycles around its end (last P V product,
-// output, next Q).  Measured (GB300, 32 heads on 8, D = 128, bf16): one prompt of
-// 16,001 tokens 1,258 us, 1,667 TFLOP/s, 0.86 of the measured burst rate and 0.95
-// of the sustained one; eight of 500-4,096 349 us, 1,443 TFLOP/s (0.75); chunks
-// of 512 on 3,584 (40 on 8, fp16) 263 us, 1,225 TFLOP/s (0.63: 704 units on 152
-// SMs are five rounds where 4.6 would do, 125 rows of 128 are used, and with
-// all keys in L2 they are 1.5 % quicker); 16 chunks of 1-48 on up to 8,192 keys
-// 75 us, 4.0 TB/s (bound by the chain above over 32 key tiles, not by HBM).  A
+// output, next Q).  Measured (GB300, 32 heads on 8, D = 128, bf16), by call among
+// many and so under the power cap: one prompt of 16,001 tokens 1,315 us, 1,595
+// TFLOP/s, 0.82 of the measured burst rate and 0.91 of the sustained one; eight of
+// 500-4,096 384 us, 1,312 TFLOP/s (0.68; 350 in a short run, at a clock that is
+// higher by as much); chunks of 512 on 3,584 (40 on 8, fp16) 277 us, 1,163 TFLOP/s
+// (0.60, 262 in a short run: 704 units on 152 SMs are five rounds where 4.6 would
+// do, 125 rows of 128 are used, and with all keys in L2 they are 1.5 % quicker); 16
+// chunks of 1-48 on up to 8,192 keys 70 us, 4.3 TB/s (bound by the chain above over
+// 32 key tiles, not by HBM).  A
 // launch reaches its first S product after 8,000 to 13,000 cycles: the search for
-// the first unit and the code of every role run from a cold instruction cache.
+// the first unit and the code of every role run from a cold instruction cache.  A
+// search looks at all sequences, past the first 32 in memory: 256 prompts of 1-60
+// tokens 73 us, 1,000 416, 4,000 5,819.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
