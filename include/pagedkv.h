@@ -443,7 +443,9 @@ pa_status pa_block_copy(pa_half *k_cache, pa_half *v_cache,
  * tokens in elements, a multiple of 8 and at least heads * D.  Outputs of
  * attention are contiguous.  None of these calls keeps anything between
  * calls, so they may run on several streams and be captured; a workspace
- * belongs to one call at a time.  T is below 2^31 - 32768.
+ * belongs to one call at a time.  T is below 2^31 - 32768.  The attention of prompts
+ * and chunks is made for some hundreds of sequences a call: past that its time grows
+ * with their square (1,000 short prompts 0.4 ms, 4,000 5.8 ms).
  * ========================================================================= */
 
 /* ---------------------------------------------------------------------------
