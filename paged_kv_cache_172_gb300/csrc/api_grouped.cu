@@ -193,10 +193,6 @@ static pa_status packed_impl(pk::GroupedArgs& a, const void* q, const void* k, c
   const long long units = (long long)a.T / a.span + a.B;
   if (units * a.Hkv * a.split >= (1LL << 31)) return PA_ERR_INVALID;
   a.max_units = (int)units;
-  // Sequences that overlap have more units than that: up to those of T rows each.
-  const long long all = ((long long)a.T + a.span - 1) / a.span * a.B;
-  const long long most = INT32_MAX / ((long long)a.Hkv * a.split);
-  a.max_items = (int)((all < most ? all : most) * a.Hkv * a.split);
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   const cudaError_t e =
       pk::launch_grouped(a, q, k, v, qs, ks, vs, reinterpret_cast<cudaStream_t>(stream));

@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     // ------------------------------------------------------------ scheduler, Q loads
     reg_dec();
     Units<PAGED> units(a);
-    const unsigned n_items = (unsigned)a.max_items;
+    const unsigned n_items = (unsigned)a.max_units * a.Hkv * a.split;  // below 2^31
     unsigned round = 0;
     int last_rank = -1, b = 0, unit = 0;
     bool more = true;
@@ -1124,8 +1124,7 @@ cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const v
   cudaError_t e = ensure_dynamic_smem<kern>(C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  // One CTA for each SM, or for each item where there are fewer (the bound of
-  // sequences that share no rows).
+  // One CTA for each SM, or for each item where there are fewer.
   const long long items = (long long)a.max_units * a.Hkv * a.split;
   const int nsm = sm_count() > 0 ? sm_count() : 1;
   cfg.gridDim = dim3((unsigned)(items < nsm ? items : nsm));

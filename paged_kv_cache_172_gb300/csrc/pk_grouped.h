@@ -76,8 +76,7 @@ struct GroupedArgs {
   int B, T, H, Hkv, G, D;
   int span;       // tokens of a unit (two tiles)
   int g_magic;    // 2^16 / G, rounded up: r * g_magic >> 16 = r / G for r < 128
-  int max_units;  // units of a K/V head, at most, of sequences that share no rows
-  int max_items;  // parts of units of all heads, whatever the offsets
+  int max_units;  // units of a K/V head, at most
   int max_tiles;  // key tiles of a unit, at most
   int split;      // parts of a unit, at most
   DivBy by_span, by_split, by_hkv;

@@ -46,29 +46,3 @@ def test_split_rows_beside_bad_offsets_are_merged(offsets, good, D):
         check(out[rows], ref, tol, f"split {split}")
         out[rows] = 7.0
         assert (out == 7).all()  # nobody else's rows are touched
-
-
-@pytest.mark.parametrize("paged", [False, True])
-def test_overlapping_sequences_cost_no_other_its_rows(paged):
-    # many sequences over the same rows make more units than T rows can hold; the short
-    # sequence before them has the fewest keys, so its unit is the last to be handed out
-    T, n, H, Hkv, D = 3000, 40, 8, 2, 64
-    offsets = [0, n] + [T, n] * 6
-    g = torch.Generator(device=DEV).manual_seed(3)
-    q, k, v = (torch.randn(T, h, D, generator=g, device=DEV).half() for h in (H, Hkv, Hkv))
-    ref, tol = attend(q[:n], k[:n], v[:n], D ** -0.5, 0)
-    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
-    status = zero_status(DEV)
-    out = torch.full_like(q, 7.0)
-    if paged:  # every sequence on the same blocks
-        bs, M = 8, T // 8
-        tables = torch.arange(M, dtype=torch.int32, device=DEV).repeat(len(offsets) - 1, 1)
-        context = torch.full((len(offsets) - 1,), T, dtype=torch.int32, device=DEV)
-        context[0] = n
-        pk.pa_chunk_attention(q, k.view(M, bs, Hkv, D), v.view(M, bs, Hkv, D), tables, context, off,
-                              D ** -0.5, out=out, status=status)
-    else:
-        pk.pa_prompt_attention(q, k, v, off, D ** -0.5, out=out, status=status)
-    torch.cuda.synchronize()
-    assert int(status.item()) == pk.PA_DEV_BAD_CONTEXT
-    check(out[:n], ref, tol)
