@@ -551,8 +551,9 @@ pa_status pa_rope_cache_write(const void *q, const void *k, const void *v,
  *
  * q [T, H, D], k and v [T, Hkv, D] with their strides; out [T, H, D]
  * q_offsets [B+1] int32, rising, within [0, T]: a sequence breaking that is
- *           flagged PA_DEV_BAD_CONTEXT and not computed (offsets that make
- *           sequences overlap leave their rows undefined)
+ *           flagged PA_DEV_BAD_CONTEXT and not computed.  (Offsets that fall and
+ *           so make sequences overlap leave all rows undefined: the work of a
+ *           call is bounded by that of T rows, the longest units first.)
  * D in {64, 128}; H / Hkv at most 128 (else PA_ERR_UNSUPPORTED); scale > 0.
  * ------------------------------------------------------------------------- */
 pa_status pa_prompt_attention(const void *q, const void *k, const void *v,

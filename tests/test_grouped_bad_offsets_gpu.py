@@ -46,3 +46,30 @@ def test_split_rows_beside_bad_offsets_are_merged(offsets, good, D):
         check(out[rows], ref, tol, f"split {split}")
         out[rows] = 7.0
         assert (out == 7).all()  # nobody else's rows are touched
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_overlapping_sequences_are_flagged_and_bounded(paged):
+    # sequences over the same rows have more units than T rows can: the call ends (with what
+    # it leaves in their rows undefined), keeps to its rows and harms no later call
+    T, n, H, Hkv, D, bs = 3000, 40, 8, 2, 64, 8
+    M = T // bs
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q, k, v = (torch.randn(T, h, D, generator=g, device=DEV).half() for h in (H, Hkv, Hkv))
+    for offsets in ([n] + [T, n] * 50, [0, n]):
+        off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+        B = len(offsets) - 1
+        status = zero_status(DEV)
+        out = torch.full_like(q, 7.0)
+        if paged:  # every sequence on the same blocks
+            tables = torch.arange(M, dtype=torch.int32, device=DEV).repeat(B, 1)
+            context = torch.full((B,), T if B > 1 else n, dtype=torch.int32, device=DEV)
+            pk.pa_chunk_attention(q, k.view(M, bs, Hkv, D), v.view(M, bs, Hkv, D), tables, context,
+                                  off, D ** -0.5, out=out, status=status)
+        else:
+            pk.pa_prompt_attention(q, k, v, off, D ** -0.5, out=out, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == (pk.PA_DEV_BAD_CONTEXT if B > 1 else 0)
+        assert (out[:n] == 7).all() if B > 1 else (out[n:] == 7).all()
+    ref, tol = attend(q[:n], k[:n], v[:n], D ** -0.5, 0)
+    check(out[:n], ref, tol)
