@@ -39,7 +39,7 @@
 // enter the second product as a high and a low half in the cache's type, so that they
 // keep 16 bits and more, as pa_decode's do, and the result is rounded once.  (One
 // rounded weight would be off by as much as the result's own rounding; the halves cost
-// 1 to 2 % in ragged batches, 5 % where 64 sequences of 1,500 keys fill every SM alike,
+// 1 to 3 % in ragged batches, 5 % where 64 sequences of 1,500 keys fill every SM alike,
 // and up to 14 % with two column tiles at D = 64.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
