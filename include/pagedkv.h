@@ -593,6 +593,46 @@ pa_status pa_chunk_attention(const void *q, const void *k_cache, const void *v_c
                              int32_t *status, pa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Cross attention: packed queries over other rows, with no causal mask.
+ *
+ * Request b's queries are the packed rows q_offsets[b] .. q_offsets[b+1]-1; its
+ * keys and values are rows kv_starts[b] .. kv_starts[b] + kv_lens[b] - 1 of k and
+ * v, an encoder's states of another length, and every query sees all of them:
+ *     out[t,h,:] = softmax_j(scale * q[t,h,:] . k[j,h/G,:]) v[j,h/G,:]
+ * otherwise as pa_prompt_attention.  The rows of the requests may be packed,
+ * padded to one length or slots of a pool, in any order and shared between requests.
+ * The beams of a request are queries of it, so its states are read once for all of
+ * them.  With k, v and offsets of the queries' own rows it is the attention of an
+ * encoder.  A request with no keys gets zero rows.  Rows outside the requests are left
+ * as they were.  What other rows of k and v hold, NaN included, never reaches a result.
+ *
+ * q [T, H, D], k and v [Tk, Hkv, D] with their strides; out [T, H, D]
+ * q_offsets [B+1] int32 as for pa_prompt_attention; kv_starts, kv_lens [B] int32
+ * max_q_len, max_kv_len  host-side bounds on the requests' lengths: a request past one
+ *           of them, or whose keys leave [0, Tk), is flagged PA_DEV_BAD_CONTEXT and its
+ *           rows are zeros (max_q_len above T counts as T)
+ * D in {64, 128}; scale > 0.  With max_q_len * H / Hkv at most 16 (and B at most 65535)
+ * the kernel of pa_decode_grouped serves the call, to its precision; otherwise that of
+ * pa_prompt_attention, to its, and H / Hkv is at most 128 (else PA_ERR_UNSUPPORTED).
+ *
+ * workspace (16-byte aligned, may be NULL): with at least
+ * pa_cross_attention_workspace_size(...) bytes few queries over many keys are cut into
+ * key ranges merged by log-sum-exp; without it they run whole (same result up to
+ * rounding).  Smaller and not NULL: PA_ERR_WORKSPACE.  The size depends on the SM count
+ * of the current device and may be 0.
+ * ------------------------------------------------------------------------- */
+size_t pa_cross_attention_workspace_size(int B, int T, int H, int Hkv, int D, int max_q_len,
+                                         int max_kv_len);
+
+pa_status pa_cross_attention(const void *q, const void *k, const void *v,
+                             const int32_t *q_offsets, const int32_t *kv_starts,
+                             const int32_t *kv_lens, int B, int T, int Tk, int H, int Hkv,
+                             int D, pa_dtype dtype, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, int max_q_len, int max_kv_len, float scale,
+                             void *out, void *workspace, size_t workspace_bytes,
+                             int32_t *status, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Decode with grouped heads: one query token per sequence.
  *
  * pa_decode's result (the softmax weights enter their product with v to 2^-15 in

@@ -33,6 +33,7 @@ EXPORTS = (
     "pa_step_plan", "pa_rope_table", "pa_rope_cache_write", "pa_prompt_attention",
     "pa_chunk_attention_workspace_size", "pa_chunk_attention",
     "pa_decode_grouped_workspace_size", "pa_decode_grouped",
+    "pa_cross_attention_workspace_size", "pa_cross_attention",
 )
 
 # Size of the fixed scratch array behind pa_decode_static (PA_DECODE_STATIC_SCRATCH_BYTES).
@@ -117,6 +118,11 @@ def _bind(lib):
     lib.pa_decode_grouped_workspace_size.restype = _SZ
     lib.pa_decode_grouped.argtypes = [_P] * 5 + [_I] * 10 + [ctypes.c_float, _P, _P, _SZ, _P, _P]
     lib.pa_decode_grouped.restype = _I
+    lib.pa_cross_attention_workspace_size.argtypes = [_I] * 7
+    lib.pa_cross_attention_workspace_size.restype = _SZ
+    lib.pa_cross_attention.argtypes = [_P] * 6 + [_I] * 7 + [_L] * 3 + [_I] * 2 + [
+        ctypes.c_float, _P, _P, _SZ, _P, _P]
+    lib.pa_cross_attention.restype = _I
     return lib
 
 

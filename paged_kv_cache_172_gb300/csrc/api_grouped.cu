@@ -275,6 +275,126 @@ pa_status pa_chunk_attention(const void* q, const void* k_cache, const void* v_c
   return packed_impl(a, q, k_cache, v_cache, q_stride, 0, 0, scale, max_context_len, stream);
 }
 
+// Cross attention: whether a request's rows, max_q_len * G to a K/V head, go to the kernel
+// of single tokens, which reads the keys once for every 16 of them.
+static bool cross_few(int B, int T, int H, int Hkv, int max_q) {
+  return (long long)max_q * (H / Hkv) <= pk::kCrossFewColumns && B <= 65535 &&
+         (long long)T * H < (1LL << 31);
+}
+
+static long long cross_parts(int B, int H, int Hkv, int D, int max_q, int max_kv, int* partition) {
+  const int kv = max_kv > 0 ? max_kv : 1;
+  // (a request's queries are further heads of the group)
+  *partition = pk::grouped_decode_partition(B, H * max_q, Hkv, D, kv);
+  const long long parts = ((long long)kv + *partition - 1) / *partition;
+  if (parts <= 65535) return parts;
+  *partition = (int)(((long long)kv / 65535 + 64) / 64 * 64);  // (a bound far above the lengths)
+  return ((long long)kv + *partition - 1) / *partition;
+}
+
+size_t pa_cross_attention_workspace_size(int B, int T, int H, int Hkv, int D, int max_q_len,
+                                         int max_kv_len) {
+  if (B <= 0 || T <= 0 || T > kMaxCount || !heads_ok(H, Hkv) || (D != 64 && D != 128) ||
+      max_q_len <= 0 || max_kv_len <= 0 || max_kv_len > kMaxCount)
+    return 0;
+  if (max_q_len > T) max_q_len = T;
+  if (!cross_few(B, T, H, Hkv, max_q_len))
+    return pk::grouped_span(H / Hkv) == 0
+               ? 0
+               : pk::grouped_workspace_bytes(B, T, H, Hkv, D, max_kv_len);
+  int pt;
+  const long long parts = cross_parts(B, H, Hkv, D, max_q_len, max_kv_len, &pt);
+  return pk::grouped_decode_in_cluster(B, H * max_q_len, Hkv, parts)
+             ? 0
+             : (size_t)T * H * parts * (D + 2) * sizeof(float);
+}
+
+pa_status pa_cross_attention(const void* q, const void* k, const void* v,
+                             const int32_t* q_offsets, const int32_t* kv_starts,
+                             const int32_t* kv_lens, int B, int T, int Tk, int H, int Hkv, int D,
+                             pa_dtype dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             int max_q_len, int max_kv_len, float scale, void* out,
+                             void* workspace, size_t workspace_bytes, int32_t* status,
+                             pa_stream_t stream) {
+  pa_status st = attention_args(B, H, Hkv, D, dtype);
+  if (st != PA_OK) return st;
+  if (T < 0 || T > kMaxCount || Tk < 0 || Tk > kMaxCount || max_q_len < 0 || max_kv_len < 0 ||
+      max_kv_len > kMaxCount || !isfinite(scale) || !(scale > 0.f))
+    return PA_ERR_INVALID;
+  if (max_q_len > T) max_q_len = T;
+  const bool few = cross_few(B, T, H, Hkv, max_q_len);
+  if (!few && pk::grouped_span(H / Hkv) == 0) return PA_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return PA_OK;
+  if (!q_offsets || !kv_starts || !kv_lens || !out || !aligned16(out) || !rows_ok(q, q_stride, H, D))
+    return PA_ERR_INVALID;
+  if (Tk == 0) {  // no request has states: a map over the queries, of which nothing is read
+    k = v = q;
+    k_stride = v_stride = q_stride;
+  }
+  if (!rows_ok(k, k_stride, Hkv, D) || !rows_ok(v, v_stride, Hkv, D)) return PA_ERR_INVALID;
+  if (workspace != nullptr) {
+    if (!aligned16(workspace)) return PA_ERR_INVALID;
+    if (workspace_bytes <
+        pa_cross_attention_workspace_size(B, T, H, Hkv, D, max_q_len, max_kv_len))
+      return PA_ERR_WORKSPACE;
+  }
+  if (few) {
+    pk::GroupedDecodeArgs a = {};
+    long long parts = cross_parts(B, H, Hkv, D, max_q_len, max_kv_len, &a.part_tokens);
+    if (!pk::grouped_decode_in_cluster(B, H * max_q_len, Hkv, parts)) {
+      if (workspace == nullptr) {  // whole
+        a.part_tokens = (max_kv_len + 63) / 64 * 64;
+        parts = 1;
+      } else {
+        a.ws_o = static_cast<float*>(workspace);
+        a.ws_ml = a.ws_o + (size_t)T * H * parts * D;
+      }
+    }
+    a.num_parts = (int)parts;
+    a.q = q;
+    a.q_offsets = q_offsets;
+    a.kv_starts = kv_starts;
+    a.context_lens = kv_lens;
+    a.out = out;
+    a.status = status;
+    a.B = B;
+    a.T = T;
+    a.Tk = Tk;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.G = H / Hkv;
+    a.D = D;
+    a.max_q = max_q_len;
+    a.max_context = max_kv_len;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a.bf16 = dtype == PA_BF16;
+    const cudaError_t e =
+        pk::launch_grouped_decode(a, k, v, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaErrorInvalidValue ? PA_ERR_INVALID : launched(e);
+  }
+  pk::GroupedArgs a = {};
+  a.split = workspace != nullptr ? pk::grouped_split(B, T, H, Hkv, max_kv_len) : 1;
+  a.q_offsets = q_offsets;
+  a.kv_starts = kv_starts;
+  a.context_lens = kv_lens;
+  a.out = out;
+  a.ws = static_cast<float*>(workspace);
+  a.status = status;
+  a.B = B;
+  a.T = T;
+  a.Tk = Tk;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.max_q = max_q_len;
+  a.max_context = max_kv_len;
+  a.bf16 = dtype == PA_BF16;
+  return packed_impl(a, q, k, v, q_stride, k_stride, v_stride, scale, max_kv_len, stream);
+}
+
 static int decode_partition(int B, int H, int Hkv, int D, int max_context,
                             int partition_tokens) {
   if (max_context < 1) max_context = 1;  // every row is empty: one partition

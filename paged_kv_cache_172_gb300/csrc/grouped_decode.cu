@@ -63,11 +63,14 @@ constexpr int kSpan = kWarps * kKeys;   // keys the CTA takes a round
 constexpr int kMaxPart = 32 * kSpan;    // a warp's table entries sit one per lane
 constexpr int kMaxCluster = 8;          // partitions that merge in a cluster, at most
 
-template <int D>
+// A stage's atoms (8 keys x 64 dims, 1 KB): paged, by key group and then by half, as blocks'
+// boxes land; rows of another array (CROSS), by half and then by key group.
+template <int D, bool CROSS = false>
 struct DCfg {
   static constexpr int HALVES = D / 64;
-  static constexpr int GROUP = HALVES * 1024;  // 8 keys: the atoms of dims 0-63, 64-127
-  static constexpr int TILE = 2 * GROUP;       // K (or V) of a stage
+  static constexpr int GROUP = CROSS ? 1024 : HALVES * 1024;  // to the next 8 keys
+  static constexpr int HALF = CROSS ? 2048 : 1024;            // from dims 0-63 to dims 64-127
+  static constexpr int TILE = HALVES * 2048;                  // K (or V) of a stage
   static constexpr int STAGE = 2 * TILE;
   static constexpr int RING_BYTES = kWarps * kRing * STAGE;
 };
@@ -161,12 +164,13 @@ __device__ __forceinline__ T round_to(float x) {
 
 // NT column tiles of 8 heads; grid (Hkv * head chunks, B, partitions).  CL: the
 // partitions of a sequence are one cluster and merge through each other's shared
-// memory; otherwise through the workspace.
-template <typename T, int D, int NT, bool CL>
+// memory; otherwise through the workspace.  CROSS: the columns are a request's
+// (query, head) pairs, ql * G of them, and its keys are consecutive rows.
+template <typename T, int D, int NT, bool CL, bool CROSS>
 __global__ void __launch_bounds__(kThreads)
     grouped_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap, const GroupedDecodeArgs a) {
-  using C = DCfg<D>;
+  using C = DCfg<D, CROSS>;
   constexpr int HEADS = NT * 8;
   constexpr int KS = D / 16;  // 16-dim steps of either product
   extern __shared__ uint8_t smem_dyn[];
@@ -183,11 +187,17 @@ __global__ void __launch_bounds__(kThreads)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRoom + kWarps * HEADS * 8);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int chunks = (a.G + HEADS - 1) / HEADS;
+  const int chunks = ((CROSS ? a.max_q : 1) * a.G + HEADS - 1) / HEADS;
   const int hkv = blockIdx.x / chunks, g0 = (blockIdx.x % chunks) * HEADS;
-  const int heads = min(HEADS, a.G - g0);  // live columns
-  const int h0 = hkv * a.G + g0;           // first query head
   const int b = blockIdx.y, part = blockIdx.z;
+  int heads = min(HEADS, a.G - g0);  // live columns
+  int q0 = b;                        // first query of the sequence
+  // The row of column g of this CTA among all (query, head) pairs.
+  auto row_at = [&](int g) {
+    if (!CROSS) return (size_t)b * a.H + hkv * a.G + g0 + g;
+    const int tok = (g0 + g) / a.G;
+    return (size_t)(q0 + tok) * a.H + hkv * a.G + (g0 + g - tok * a.G);
+  };
   uint64_t* bar = bars + warp * kRing;
 
   if (lane == 0) {
@@ -203,22 +213,36 @@ __global__ void __launch_bounds__(kThreads)
   // a CTA's start is two trips to memory instead of three.
   const int bs = a.block_size, k0 = part * a.part_tokens;
   const int my_key = k0 + (warp + kWarps * lane) * kKeys;
-  const int32_t* row_of = a.block_tables + (size_t)b * a.max_blocks;
+  const int32_t* row_of = CROSS ? nullptr : a.block_tables + (size_t)b * a.max_blocks;
   int ent_lo = 0, ent_hi = 0;
-  if ((warp + kWarps * lane) * kKeys < a.part_tokens) {
+  if (!CROSS && (warp + kWarps * lane) * kKeys < a.part_tokens) {
     const int blk = my_key / bs;
     if (blk < a.max_blocks) ent_lo = row_of[blk];
     if (bs < kKeys && blk + 1 < a.max_blocks) ent_hi = row_of[blk + 1];
   }
-  int n = a.context_lens[b];
-  if (n < 0 || n > a.max_context) {
+  int n = a.context_lens[b], kv0 = 0;
+  bool bad = n < 0 || n > a.max_context;
+  if constexpr (CROSS) {
+    q0 = a.q_offsets[b];
+    kv0 = a.kv_starts[b];
+    const int end = a.q_offsets[b + 1];
+    const bool lost = q0 < 0 || end < q0 || end > a.T;  // its rows do not exist
+    const int ql = lost ? 0 : end - q0;
+    bad = ql > a.max_q || ((bad || kv0 < 0 || (long long)kv0 + n > a.Tk) && ql > 0);
+    if ((bad || lost) && threadIdx.x == 0 && part == 0)
+      flag_status(a.status, PA_DEV_BAD_CONTEXT);
+    if (bad) n = 0;
+    if ((long long)ql * a.G <= g0) return;
+    // (columns past the last chunk's: of a bad request, whose rows are zeros)
+    heads = bad && g0 / HEADS == chunks - 1 ? ql * a.G - g0 : min(HEADS, ql * a.G - g0);
+  } else if (bad) {
     if (threadIdx.x == 0 && part == 0) flag_status(a.status, PA_DEV_BAD_CONTEXT);
     n = n < 0 ? 0 : a.max_context;
   }
   if (k0 >= n) {
     if (part == 0)  // an empty context: zero rows
-      for (int i = threadIdx.x; i < heads * D; i += kThreads)
-        static_cast<T*>(a.out)[((size_t)b * a.H + h0) * D + i] = round_to<T>(0.f);
+      for (long long i = threadIdx.x; i < (long long)heads * D; i += kThreads)
+        static_cast<T*>(a.out)[row_at((int)(i / D)) * D + i % D] = round_to<T>(0.f);
     return;
   }
   const int k1 = min(n, k0 + a.part_tokens);
@@ -230,7 +254,7 @@ __global__ void __launch_bounds__(kThreads)
   // Lane i holds the pool row of the first slot of the warp's i-th stage, and
   // for 8-token blocks that of its second half.
   int row_lo = 0, row_hi = 0;
-  if (lane < mine) {
+  if (!CROSS && lane < mine) {
     auto pool_row = [&](int key, int phys) {
       if (key >= n) return a.num_blocks * bs * a.Hkv;  // past the sequence: outside the map
       if (phys < 0 || phys >= a.num_blocks) {
@@ -246,6 +270,17 @@ __global__ void __launch_bounds__(kThreads)
 
   uint8_t* ring = smem + warp * kRing * C::STAGE;
   auto request = [&](int i) {
+    if constexpr (CROSS) {  // 16 rows of one head; rows past the array read as zeros
+      if (elect_one()) {
+        uint8_t* st = ring + (i % kRing) * C::STAGE;
+        uint64_t* full = &bar[i % kRing];
+        const int row = kv0 + k0 + (warp + kWarps * i) * kKeys;
+        mbar_arrive_expect_tx(full, C::STAGE);
+        tma_load_4d(st, &kmap, 0, row, 0, hkv, full);
+        tma_load_4d(st + C::TILE, &vmap, 0, row, 0, hkv, full);
+      }
+      return;
+    }
     const int lo = __shfl_sync(kAll, row_lo, i), hi = __shfl_sync(kAll, row_hi, i);
     if (elect_one()) {
       uint8_t* st = ring + (i % kRing) * C::STAGE;
@@ -272,7 +307,14 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int g = t * 8 + col;
-    const T* qr = static_cast<const T*>(a.q) + ((size_t)b * a.H + h0 + g) * D + two;
+    const T* qr = static_cast<const T*>(a.q) + two;
+    if (CROSS) {
+      const int tok = (g0 + g) / a.G;
+      if (g < heads)
+        qr += (size_t)(q0 + tok) * a.q_stride + (size_t)(hkv * a.G + g0 + g - tok * a.G) * D;
+    } else {
+      qr += row_at(g) * D;
+    }
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -306,7 +348,7 @@ __global__ void __launch_bounds__(kThreads)
       // V rows past the keys hold anything, and 0 * NaN is NaN: zero them.
       for (int i = lane; i < (kKeys - live) * (D / 8); i += 32) {
         const int r = live + i / (D / 8), c = i % (D / 8);
-        *reinterpret_cast<uint4*>(st + C::TILE + (r >> 3) * C::GROUP + (c >> 3) * 1024 +
+        *reinterpret_cast<uint4*>(st + C::TILE + (r >> 3) * C::GROUP + (c >> 3) * C::HALF +
                                   (r & 7) * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
       __syncwarp();
@@ -319,7 +361,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int ks = 0; ks < KS; ++ks) {
       const int c = 2 * ks + (mi >> 1);
       uint32_t kf[4];  // keys 0-7 / 8-15 (mi & 1), dims 0-7 / 8-15 (mi >> 1)
-      ldsm4(kb + (mi & 1) * C::GROUP + (c >> 3) * 1024 + rr * 128 + (((c & 7) ^ rr) << 4), kf);
+      ldsm4(kb + (mi & 1) * C::GROUP + (c >> 3) * C::HALF + rr * 128 + (((c & 7) ^ rr) << 4), kf);
 #pragma unroll
       for (int t = 0; t < NT; ++t) mma<T>(s[t], kf, qf[t][ks][0], qf[t][ks][1]);
     }
@@ -367,7 +409,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int ks = 0; ks < KS; ++ks) {
       const int c = 2 * ks + (mi & 1);
       uint32_t vf[4];  // dims 0-7 / 8-15 (mi & 1), keys 0-7 / 8-15 (mi >> 1), transposed
-      ldsm4_t(vb + (mi >> 1) * C::GROUP + (c >> 3) * 1024 + rr * 128 + (((c & 7) ^ rr) << 4), vf);
+      ldsm4_t(vb + (mi >> 1) * C::GROUP + (c >> 3) * C::HALF + rr * 128 + (((c & 7) ^ rr) << 4), vf);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         mma<T>(o[t][ks], vf, pf[t][0][0], pf[t][0][1]);
@@ -433,7 +475,7 @@ __global__ void __launch_bounds__(kThreads)
       x += wgt * v.x;
       y += wgt * v.y;
     }
-    const size_t row = (size_t)b * a.H + h0 + g;
+    const size_t row = row_at(g);
     if (alone) {
       const float inv = L != 0.f ? 1.f / L : 0.f;
       *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D + d) =
@@ -477,25 +519,35 @@ __global__ void __launch_bounds__(kThreads)
         y += wgt * v[p].y;
       }
       const float inv = L != 0.f ? 1.f / L : 0.f;
-      *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) +
-                                   ((size_t)b * a.H + h0 + g) * D + dd) =
+      *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row_at(g) * D + dd) =
           pack<T>(x * inv, y * inv);
     }
     cluster.sync();  // nobody leaves while another reads its shared memory
   }
 }
 
-// Merges the partitions of a (sequence, head): W warps take every W-th one.
-template <typename T, int D, int W>
+// Merges the partitions of a (sequence, head), CROSS of a (query, head) whose request is
+// blockIdx.y: W warps take every W-th one.
+template <typename T, int D, int W, bool CROSS>
 __global__ void __launch_bounds__(32 * W) grouped_decode_merge(const GroupedDecodeArgs a) {
   constexpr int EPL = D / 32;
   __shared__ float s_o[W][D];
   __shared__ float2 s_ml[W];
-  const size_t row = blockIdx.x;
+  size_t row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The lengths come from before the first kernel, which let this one start only when
   // all its blocks had waited for them: they are read while it still runs.
-  const int n = min(max(a.context_lens[row / a.H], 0), a.max_context);
+  int n = a.context_lens[CROSS ? blockIdx.y : row / a.H];
+  if constexpr (CROSS) {
+    const int q0 = a.q_offsets[blockIdx.y], end = a.q_offsets[blockIdx.y + 1];
+    const int kv0 = a.kv_starts[blockIdx.y], tok = blockIdx.x / a.H;
+    if (q0 < 0 || end < q0 || end > a.T || end - q0 > a.max_q || tok >= end - q0 ||
+        n > a.max_context || kv0 < 0 || (long long)kv0 + n > a.Tk)
+      n = 0;
+    row += (size_t)q0 * a.H;
+  } else {
+    n = min(max(n, 0), a.max_context);
+  }
   pdl_wait();
   pdl_launch_dependents();
   if (n <= a.part_tokens) return;  // written by its only partition (or empty)
@@ -562,12 +614,21 @@ __global__ void __launch_bounds__(32 * W) grouped_decode_merge(const GroupedDeco
     *reinterpret_cast<uint32_t*>(dst + e) = pack<T>(o[e] * inv, o[e + 1] * inv);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool CROSS>
 cudaError_t launch_t(const GroupedDecodeArgs& a, const void* k_cache, const void* v_cache,
                      cudaStream_t stream) {
-  using C = DCfg<D>;
+  using C = DCfg<D, CROSS>;
   using u64 = unsigned long long;
   CUtensorMap kmap, vmap;
+  cudaError_t e = cudaSuccess;
+  if constexpr (CROSS) {
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+      const u64 dims[4] = {64, (u64)(a.Tk > 0 ? a.Tk : 1), (u64)C::HALVES, (u64)a.Hkv};
+      const u64 st[3] = {(u64)(i ? a.v_stride : a.k_stride) * 2, 128, (u64)D * 2};
+      const unsigned box[4] = {64, kKeys, (unsigned)C::HALVES, 1};
+      e = make_map_4d(i ? &vmap : &kmap, i ? v_cache : k_cache, dims, st, box, true);
+    }
+  } else {
   // Rows (slot, head) of D values; inside a block (64 dims, 8 keys, halves, key
   // groups), at its first slot's row.
   const u64 rowb = (u64)D * 2, tok = rowb * a.Hkv;
@@ -575,12 +636,14 @@ cudaError_t launch_t(const GroupedDecodeArgs& a, const void* k_cache, const void
                        (u64)a.num_blocks * a.block_size * a.Hkv};
   const u64 st[4] = {tok, 128, 8 * tok, rowb};
   const unsigned box[5] = {64, 8, (unsigned)C::HALVES, a.block_size >= kKeys ? 2u : 1u, 1};
-  cudaError_t e = make_map_5d(&kmap, k_cache, dims, st, box, true);
+  e = make_map_5d(&kmap, k_cache, dims, st, box, true);
   if (e == cudaSuccess) e = make_map_5d(&vmap, v_cache, dims, st, box, true);
+  }
   if (e != cudaSuccess) return e;
   constexpr int smem = smem_bytes<D, NT>();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.Hkv * ((a.G + 8 * NT - 1) / (8 * NT)), a.B, a.num_parts);
+  const int cols = (CROSS ? a.max_q : 1) * a.G;  // of a sequence and a K/V head
+  cfg.gridDim = dim3(a.Hkv * ((cols + 8 * NT - 1) / (8 * NT)), a.B, a.num_parts);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -589,8 +652,8 @@ cudaError_t launch_t(const GroupedDecodeArgs& a, const void* k_cache, const void
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (a.num_parts > 1 && grouped_decode_in_cluster(a.B, a.H, a.Hkv, a.num_parts)) {
-    constexpr auto kern = grouped_decode_kernel<T, D, NT, true>;
+  if (a.num_parts > 1 && grouped_decode_in_cluster(a.B, cols * a.Hkv, a.Hkv, a.num_parts)) {
+    constexpr auto kern = grouped_decode_kernel<T, D, NT, true, CROSS>;
     e = ensure_dynamic_smem<kern>(smem);
     if (e != cudaSuccess) return e;
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -598,19 +661,19 @@ cudaError_t launch_t(const GroupedDecodeArgs& a, const void* k_cache, const void
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, a);
   }
-  constexpr auto kern = grouped_decode_kernel<T, D, NT, false>;
+  constexpr auto kern = grouped_decode_kernel<T, D, NT, false, CROSS>;
   e = ensure_dynamic_smem<kern>(smem);
   if (e != cudaSuccess) return e;
   e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, a);
   if (e != cudaSuccess || a.num_parts == 1) return e;
-  cfg.gridDim = dim3(a.B * a.H);
+  cfg.gridDim = CROSS ? dim3(a.max_q * a.H, a.B) : dim3(a.B * a.H);
   cfg.dynamicSmemBytes = 0;
   if (a.num_parts <= 16) {
     cfg.blockDim = dim3(32);
-    return cudaLaunchKernelEx(&cfg, grouped_decode_merge<T, D, 1>, a);
+    return cudaLaunchKernelEx(&cfg, grouped_decode_merge<T, D, 1, CROSS>, a);
   }
   cfg.blockDim = dim3(32 * 8);
-  return cudaLaunchKernelEx(&cfg, grouped_decode_merge<T, D, 8>, a);
+  return cudaLaunchKernelEx(&cfg, grouped_decode_merge<T, D, 8, CROSS>, a);
 }
 
 }  // namespace
@@ -671,9 +734,13 @@ bool grouped_decode_in_cluster(int B, int H, int Hkv, long long parts) {
 
 cudaError_t launch_grouped_decode(const GroupedDecodeArgs& a, const void* k_cache,
                                   const void* v_cache, cudaStream_t stream) {
-#define PK_GD(TT, DD)                                                  \
-  (a.G <= 8 ? launch_t<TT, DD, 1>(a, k_cache, v_cache, stream)         \
-            : launch_t<TT, DD, 2>(a, k_cache, v_cache, stream))
+  const int cols = (a.kv_starts != nullptr ? a.max_q : 1) * a.G;
+#define PK_GD(TT, DD)                                                               \
+  (a.kv_starts != nullptr                                                           \
+       ? (cols <= 8 ? launch_t<TT, DD, 1, true>(a, k_cache, v_cache, stream)        \
+                    : launch_t<TT, DD, 2, true>(a, k_cache, v_cache, stream))       \
+   : cols <= 8 ? launch_t<TT, DD, 1, false>(a, k_cache, v_cache, stream)            \
+               : launch_t<TT, DD, 2, false>(a, k_cache, v_cache, stream))
   if (a.bf16) return a.D == 128 ? PK_GD(__nv_bfloat16, 128) : PK_GD(__nv_bfloat16, 64);
   return a.D == 128 ? PK_GD(__half, 128) : PK_GD(__half, 64);
 #undef PK_GD

@@ -92,6 +92,10 @@ constexpr float kLazy = 8.0f;            // log2 of the growth that forces a res
 template <typename T>
 constexpr float kRaiseLog2 = std::is_same<T, __half>::value ? 6.0f : 0.0f;
 
+// Where the keys are and who sees them: a prompt's own rows up to itself, the paged
+// cache up to itself, or rows of another array, all of them.
+enum Form { kPrompt, kChunk, kCross };
+
 // Layout of a K or V tile in shared memory.  Paged: key groups of 8 keys x D
 // dims, each the 1 KB atoms of dims 0-63 and 64-127 (the order in which a
 // block's box lands).  Contiguous rows: two slabs of 128 keys x 64 dims.
@@ -131,6 +135,7 @@ __host__ __device__ constexpr uint32_t operand_type() {
 // A sequence of the packed step, as every CTA sees it.
 struct Seq {
   int start, ql, n;  // first packed row, new tokens, keys
+  int kv;            // kCross: first row of its keys
   int nu;            // units
   bool bad;          // its rows are zeros
   bool lost;         // its rows do not exist: nothing to write
@@ -140,9 +145,10 @@ __device__ __forceinline__ int divide(int x, DivBy d) {
   return (int)(((unsigned long long)(unsigned)x * d.m) >> (31 + d.s));
 }
 
-template <bool PAGED>
+template <Form F>
 __device__ __forceinline__ Seq sequence(const GroupedArgs& a, int b) {
   Seq s;
+  s.kv = 0;
   s.start = a.q_offsets[b];
   const int end = a.q_offsets[b + 1];
   s.ql = end - s.start;
@@ -150,7 +156,17 @@ __device__ __forceinline__ Seq sequence(const GroupedArgs& a, int b) {
   if (s.lost) s.ql = 0;
   s.n = s.ql;
   s.bad = s.lost;
-  if (PAGED && s.ql > 0) {
+  if (F == kCross && s.ql > 0) {
+    const int n = a.context_lens[b], kv = a.kv_starts[b];
+    s.n = 0;
+    if (s.ql > a.max_q || n < 0 || n > a.max_context || kv < 0 || (long long)kv + n > a.Tk) {
+      s.bad = true;
+    } else {
+      s.n = n;
+      s.kv = kv;
+    }
+  }
+  if (F == kChunk && s.ql > 0) {
     const int n = a.context_lens[b];
     if (n < s.ql || n > a.max_context)
       s.bad = true;
@@ -161,13 +177,18 @@ __device__ __forceinline__ Seq sequence(const GroupedArgs& a, int b) {
   return s;
 }
 
-// Key tiles that unit i (tokens i * span .. ) of a sequence reads.
+// Key tiles that unit i (tokens i * span .. ) of a sequence reads (at least one, so that
+// a unit without keys is found too and its rows are written).
+template <Form F>
 __device__ __forceinline__ int unit_tiles(const Seq& s, int span, int i) {
+  if (F == kCross) return max(1, (int)((unsigned)(s.n + kTile - 1) / kTile));
   return (int)((unsigned)(s.n - s.ql + min((i + 1) * span, s.ql) + kTile - 1) / kTile);
 }
 
 // Units of a sequence that read at least t (>= 1) key tiles: the last ones.
+template <Form F>
 __device__ __forceinline__ int units_from(const GroupedArgs& a, const Seq& s, int t) {
+  if (F == kCross) return t <= unit_tiles<F>(s, 0, 0) ? s.nu : 0;
   const int k = (t - 1) * kTile + 1;  // keys such a unit needs at least
   if (s.n < k) return 0;  // (an empty sequence too)
   const int over = k - (s.n - s.ql);  // its tokens needed at least
@@ -181,7 +202,7 @@ __device__ __forceinline__ int unit_parts(int tiles, int split) {
 }
 
 // Walks the units by key tiles, longest first (one warp, all lanes alike).
-template <bool PAGED>
+template <Form F>
 struct Units {
   const GroupedArgs& a;
   Seq mine;          // the lane's among the first 32 sequences, read once
@@ -191,16 +212,17 @@ struct Units {
   __device__ Units(const GroupedArgs& args)
       : a(args), bound(args.max_tiles + 1), above(0), tiles(0), base0(0), before(0) {
     const int lane = threadIdx.x & 31;
-    mine = lane < a.B ? sequence<PAGED>(a, lane) : Seq{0, 0, 0, 0, true, true};
+    mine = lane < a.B ? sequence<F>(a, lane) : Seq{0, 0, 0, 0, 0, true, true};
   }
 
   // Sequence b, the same for all lanes.
   __device__ Seq get(int b) const {
-    if (b >= 32) return sequence<PAGED>(a, b);
+    if (b >= 32) return sequence<F>(a, b);
     Seq s;
     s.start = __shfl_sync(kAll, mine.start, b);
     s.ql = __shfl_sync(kAll, mine.ql, b);
     s.n = __shfl_sync(kAll, mine.n, b);
+    s.kv = F == kCross ? __shfl_sync(kAll, mine.kv, b) : 0;
     s.nu = 0;  // (not asked for)
     s.bad = __shfl_sync(kAll, (int)mine.bad, b);
     s.lost = false;  // (a lost one has no units)
@@ -222,8 +244,8 @@ struct Units {
 #pragma unroll 1
       for (int b = lane; b < a.B; b += 32) {
         Seq s = mine;
-        if (b >= 32) s = sequence<PAGED>(a, b);
-        c += units_from(a, s, t);
+        if (b >= 32) s = sequence<F>(a, b);
+        c += units_from<F>(a, s, t);
       }
       c = __reduce_add_sync(kAll, c);
       if (c > rank) {
@@ -248,9 +270,9 @@ struct Units {
       int c = 0, upper = 0, nu = 0;
       if (b < a.B) {
         Seq s = mine;
-        if (b >= 32) s = sequence<PAGED>(a, b);
-        upper = units_from(a, s, lo + 1);
-        c = units_from(a, s, lo) - upper;
+        if (b >= 32) s = sequence<F>(a, b);
+        upper = units_from<F>(a, s, lo + 1);
+        c = units_from<F>(a, s, lo) - upper;
         nu = s.nu;
       }
       int x = c;  // inclusive scan
@@ -316,18 +338,19 @@ struct Item {
   int valid;             // 0: no more items
   int row0, hkv;         // packed row of tile A's first token; K/V head
   int toks_a, toks_b;    // tokens of the tiles in this sequence
-  int pos_a;             // position of tile A's first token
+  int pos_a;             // position of tile A's first token; kCross: first row of the keys
   int kt0, n_kv;         // first key tile, key tiles
   int ntile_a, ntile_b;  // of those, the ones each tile reads
   int parts, part;
   int b, n;              // sequence and its keys
 };
 
-template <typename T, int D, bool PAGED>
+template <typename T, int D, Form F>
 __global__ void __launch_bounds__(kThreadsG, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const GroupedArgs a) {
+  constexpr bool PAGED = F == kChunk;
   using C = Cfg<D, PAGED>;
   constexpr int kRing = C::RING;
   // P is handed over in halves for contiguous rows, so that its product with V starts
@@ -433,10 +456,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     int stages = 0;  // of those, stages
     Item it;
     for (int k = 0; take(k, it); ++k) {
-      const int pos0 = it.pos_a + (x ? tpt : 0);
+      const int pos0 = F == kCross ? it.n - 1 : it.pos_a + (x ? tpt : 0);
       const int ntile = x ? it.ntile_b : it.ntile_a;
       const bool live = my_tok < (x ? it.toks_b : it.toks_a);  // a row of this sequence
-      const int pos = pos0 + my_tok;
+      const int pos = F == kCross ? pos0 : pos0 + my_tok;  // last key that the row sees
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < ntile; ++j, ++done) {
         if (!(ok = __all_sync(kAll, mbar_wait(&s_full[x], done & 1)))) break;
@@ -628,7 +651,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   } else if (warp == kWarpSched) {
     // ------------------------------------------------------------ scheduler, Q loads
     reg_dec();
-    Units<PAGED> units(a);
+    Units<F> units(a);
     const unsigned n_items = (unsigned)a.max_units * a.Hkv * a.split;  // below 2^31
     unsigned round = 0;
     int last_rank = -1, b = 0, unit = 0;
@@ -650,7 +673,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         last_rank = rank;
         const Seq s = units.get(b);
         const int tok0 = unit * a.span;
-        const int all = unit_tiles(s, a.span, unit);
+        const int all = unit_tiles<F>(s, a.span, unit);
         it.parts = unit_parts(all, a.split);
         if (it.part >= it.parts) continue;
         it.valid = 1;
@@ -659,7 +682,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         it.row0 = s.start + tok0;
         it.toks_a = min(tpt, s.ql - tok0);
         it.toks_b = max(0, min(tpt, s.ql - tok0 - tpt));
-        it.pos_a = s.n - s.ql + tok0;
+        it.pos_a = F == kCross ? s.kv : s.n - s.ql + tok0;
         it.kt0 = 0;
         it.n_kv = all;
         if (it.parts > 1) {  // (at most 32 parts of 2^24 tiles)
@@ -668,13 +691,14 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           it.n_kv = (int)((at + all) / parts) - it.kt0;
         }
         auto reads = [&](int pos, int toks) {
+          if (F == kCross) return toks > 0 ? it.n_kv : 0;
           const int t = toks > 0 ? (int)((unsigned)(pos + toks - 1) / kTile) + 1 : 0;
           return min(max(t - it.kt0, 0), it.n_kv);
         };
         it.ntile_a = reads(it.pos_a, it.toks_a);
         it.ntile_b = reads(it.pos_a + tpt, it.toks_b);
-        if (s.bad) {  // no keys: zero rows, written by the first part
-          if (lane == 0) flag_status(a.status, PA_DEV_BAD_CONTEXT);
+        if (s.bad || (F == kCross && s.n == 0)) {  // no keys: zero rows, by the first part
+          if (s.bad && lane == 0) flag_status(a.status, PA_DEV_BAD_CONTEXT);
           if (it.part > 0) {
             it.valid = 0;
             continue;
@@ -729,7 +753,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     }
     if (blockIdx.x == 0)
       for (int i = lane; i < a.B; i += 32)
-        if (sequence<PAGED>(a, i).lost) flag_status(a.status, PA_DEV_BAD_CONTEXT);
+        if (sequence<F>(a, i).lost) flag_status(a.status, PA_DEV_BAD_CONTEXT);
   } else if (warp == kWarpLoad) {
     // ------------------------------------------------------------ K and V
     reg_dec();
@@ -739,7 +763,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     Item it;
     for (int k = 0; take(k, it); ++k) {
       const int nblk = PAGED ? (it.n + a.block_size - 1) / a.block_size : 0;
-      const int row = PAGED ? 0 : it.row0 - it.pos_a;  // first packed row of the sequence
+      // first row of the sequence's keys
+      const int row = PAGED ? 0 : F == kCross ? it.pos_a : it.row0 - it.pos_a;
       int win = -kWindow;
       auto load_tile = [&](int t, bool v) {
         const int lb0 = (it.kt0 + t) * bpt;
@@ -978,7 +1003,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 // then D / 8 columns each, four parts' loads in flight.  (One thread to a row
 // with all its parts one after the other: 64 us for 32 parts, all latency.)
 constexpr int kMergeWarps = 8;
-template <typename T, int D>
+template <typename T, int D, Form F>
 __global__ void __launch_bounds__(32 * kMergeWarps) grouped_merge_kernel(const GroupedArgs a) {
   constexpr int kC = D / 4 / kMergeWarps;  // groups of four columns of a warp
   __shared__ float s_w[kGroupedMaxSplit][32];     // m, then the weight of a part
@@ -1001,7 +1026,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) grouped_merge_kernel(const G
       else
         hi = mid;
     }
-    s = sequence<true>(a, lo);
+    s = sequence<F>(a, lo);
   }
   // A row of no sequence, or one beside offsets that fall: the sequences that these
   // belong to are not computed, but the others are, and looking at all finds theirs.
@@ -1009,10 +1034,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) grouped_merge_kernel(const G
     int falls = 0;
     for (int b = lane; b < a.B; b += 32) falls |= a.q_offsets[b] > a.q_offsets[b + 1];
     if (__any_sync(kAll, falls) && t >= 0)
-      for (int b = 0; b < a.B && !holds(); ++b) s = sequence<true>(a, b);
+      for (int b = 0; b < a.B && !holds(); ++b) s = sequence<F>(a, b);
   }
   if (t >= 0 && !s.bad && holds())
-    parts = unit_parts(unit_tiles(s, a.span, divide(t - s.start, a.by_span)), a.split);
+    parts = unit_parts(unit_tiles<F>(s, a.span, divide(t - s.start, a.by_span)), a.split);
   if (parts == 1) parts = 0;  // (written by its only part)
   pdl_wait();
   pdl_launch_dependents();
@@ -1086,10 +1111,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) grouped_merge_kernel(const G
   }
 }
 
-template <typename T, int D, bool PAGED>
+template <typename T, int D, Form F>
 cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const void* v,
                      long long q_stride, long long k_stride, long long v_stride,
                      cudaStream_t stream) {
+  constexpr bool PAGED = F == kChunk;
   using C = Cfg<D, PAGED>;
   using u64 = unsigned long long;
   CUtensorMap qmap, kmap, vmap;
@@ -1113,14 +1139,14 @@ cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const v
       const unsigned box[5] = {64, 8, (unsigned)C::HALVES, (unsigned)a.block_size / 8, 1};
       e = make_map_5d(map, i ? v : k, dims, st, box, true);
     } else {
-      const u64 dims[4] = {64, (u64)a.T, (u64)C::HALVES, (u64)a.Hkv};
+      const u64 dims[4] = {64, (u64)(F == kCross ? (a.Tk > 0 ? a.Tk : 1) : a.T), (u64)C::HALVES, (u64)a.Hkv};
       const u64 st[3] = {(u64)(i ? v_stride : k_stride) * 2, 128, (u64)D * 2};
       const unsigned box[4] = {64, kTile, (unsigned)C::HALVES, 1};
       e = make_map_4d(map, i ? v : k, dims, st, box, true);
     }
     if (e != cudaSuccess) return e;
   }
-  constexpr auto kern = grouped_kernel<T, D, PAGED>;
+  constexpr auto kern = grouped_kernel<T, D, F>;
   cudaError_t e = ensure_dynamic_smem<kern>(C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1137,13 +1163,13 @@ cudaError_t launch_t(const GroupedArgs& a, const void* q, const void* k, const v
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, qmap, kmap, vmap, a);
-  if constexpr (PAGED) {
+  if constexpr (F != kPrompt) {
     if (e != cudaSuccess || a.split == 1) return e;
     cudaLaunchConfig_t cm = cfg;
     cm.gridDim = dim3((unsigned)(((long long)a.T * a.G + 31) / 32), a.Hkv);
     cm.blockDim = dim3(32 * kMergeWarps);
     cm.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cm, grouped_merge_kernel<T, D>, a);
+    e = cudaLaunchKernelEx(&cm, grouped_merge_kernel<T, D, F>, a);
   }
   return e;
 }
@@ -1197,9 +1223,11 @@ cudaError_t launch_grouped(const GroupedArgs& a, const void* q, const void* k, c
                            long long q_stride, long long k_stride, long long v_stride,
                            cudaStream_t stream) {
 #define PK_GROUPED(TT, DD)                                                                     \
-  (a.block_tables != nullptr                                                                   \
-       ? launch_t<TT, DD, true>(a, q, k, v, q_stride, k_stride, v_stride, stream)              \
-       : launch_t<TT, DD, false>(a, q, k, v, q_stride, k_stride, v_stride, stream))
+  (a.kv_starts != nullptr                                                                      \
+       ? launch_t<TT, DD, kCross>(a, q, k, v, q_stride, k_stride, v_stride, stream)            \
+   : a.block_tables != nullptr                                                                 \
+       ? launch_t<TT, DD, kChunk>(a, q, k, v, q_stride, k_stride, v_stride, stream)            \
+       : launch_t<TT, DD, kPrompt>(a, q, k, v, q_stride, k_stride, v_stride, stream))
   if (a.bf16) return a.D == 128 ? PK_GROUPED(__nv_bfloat16, 128) : PK_GROUPED(__nv_bfloat16, 64);
   return a.D == 128 ? PK_GROUPED(__half, 128) : PK_GROUPED(__half, 64);
 #undef PK_GROUPED

@@ -65,10 +65,12 @@ inline DivBy div_by(int n) {
 }
 
 // Attention of packed new tokens (grouped_prompt.cu): prompts over their own
-// rows (block_tables null) or chunks over the paged cache.
+// rows (block_tables and kv_starts null), chunks over the paged cache, or queries over
+// rows of another array.
 struct GroupedArgs {
   const int32_t* q_offsets;     // [B + 1]
-  const int32_t* context_lens;  // [B], paged
+  const int32_t* context_lens;  // [B], paged and cross
+  const int32_t* kv_starts;     // [B], cross: first row of a request's keys
   const int32_t* block_tables;  // [B, max_blocks], paged
   void* out;                    // [T, H, D]
   float* ws;                    // parts of split units, split * T * H * (D + 2) floats
@@ -81,6 +83,7 @@ struct GroupedArgs {
   int split;      // parts of a unit, at most
   DivBy by_span, by_split, by_hkv;
   int block_size, num_blocks, max_blocks, max_context;
+  int max_q, Tk;  // cross: queries of a request, at most; rows of the keys
   float scale_log2;
   bool bf16;
 };
@@ -93,20 +96,27 @@ cudaError_t launch_grouped(const GroupedArgs& a, const void* q, const void* k, c
                            long long q_stride, long long k_stride, long long v_stride,
                            cudaStream_t stream);
 
-// Grouped decode (grouped_decode.cu): one query token per sequence.
+// Grouped decode (grouped_decode.cu): one query token per sequence over the paged cache,
+// or few queries a request over rows of another array (kv_starts set).
 struct GroupedDecodeArgs {
-  const void* q;  // [B, H, D]
+  const void* q;  // [B, H, D], cross: [T, H, D]
   const int32_t* block_tables;
   const int32_t* context_lens;
   void* out;
-  float* ws_o;   // [B, H, num_parts, D] unnormalised outputs of the parts
+  float* ws_o;   // [B, H, num_parts, D] unnormalised outputs of the parts (cross: T for B)
   float* ws_ml;  // [B, H, num_parts, 2] their (max, normaliser), log2 domain
   int32_t* status;
   int B, H, Hkv, G, D, block_size, num_blocks, max_blocks, max_context;
   int part_tokens, num_parts;
+  // cross: requests' rows and keys; a request's max_q * G columns at most
+  const int32_t* q_offsets;
+  const int32_t* kv_starts;
+  long long q_stride, k_stride, v_stride;
+  int T, Tk, max_q;
   float scale_log2;
   bool bf16;
 };
+constexpr int kCrossFewColumns = 16;  // (query, head) pairs of a request and K/V head
 int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context);
 // Whether that many partitions merge inside the launch, without a workspace.
 bool grouped_decode_in_cluster(int B, int H, int Hkv, long long parts);

@@ -359,6 +359,51 @@ PyObject* decode_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// q, k, v, q_offsets, kv_starts, kv_lens, out, workspace (True: one is allocated for the
+// call), status, max_q_len, max_kv_len, scale, stream
+PyObject* cross_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> int {
+    const at::Tensor *q = tensor(a[0]), *k = tensor(a[1]), *v = tensor(a[2]), *off = tensor(a[3]),
+                     *start = tensor(a[4]), *len = tensor(a[5]), *out = tensor(a[6]);
+    int max_q, max_kv;
+    float scale;
+    pa_dtype type;
+    pa_stream_t s;
+    void* ws;
+    size_t ws_bytes;
+    if (!number(a[9], &max_q) || !number(a[10], &max_kv) || !number(a[11], &scale)) return kUnfit;
+    if (q == nullptr || !q->is_cuda() || q->dim() != 3 || k == nullptr || k->dim() != 3 ||
+        off == nullptr || off->dim() != 1 || !half_type(q, &type))
+      return kUnfit;
+    const int dev = q->get_device();
+    const ScalarType t = q->scalar_type();
+    const int64_t T = q->size(0), H = q->size(1), D = q->size(2), Tk = k->size(0),
+                  Hkv = k->size(1), B = off->size(0) - 1;
+    if (T > INT32_MAX || Tk > INT32_MAX || H > INT32_MAX || Hkv > INT32_MAX || D > INT32_MAX ||
+        B > INT32_MAX || !rows(q, t, dev, T, H, D) || !rows(k, t, dev, Tk, Hkv, D) ||
+        !rows(v, t, dev, Tk, Hkv, D) || !dense(off, ScalarType::Int, dev, {B + 1}) ||
+        !dense(start, ScalarType::Int, dev, {B}) || !dense(len, ScalarType::Int, dev, {B}) ||
+        !dense(out, t, dev, {T, H, D}) || !workspace_fits(a[7], dev, &ws, &ws_bytes) ||
+        !status_fits(a[8], dev) || !stream_of(a[12], dev, &s))
+      return kUnfit;
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    at::Tensor own;
+    if (a[7] == Py_True) {
+      ws_bytes = pa_cross_attention_workspace_size(
+          (int)B, (int)T, (int)H, (int)Hkv, (int)D, max_q, max_kv);
+      if (ws_bytes > 0) {
+        own = workspace_for(ws_bytes, dev, a[12], s);
+        ws = own.data_ptr();
+      }
+    }
+    return pa_cross_attention(data<void>(q), data<void>(k), data<void>(v), data<int32_t>(off),
+                              data<int32_t>(start), data<int32_t>(len), (int)B, (int)T, (int)Tk,
+                              (int)H, (int)Hkv, (int)D, type, stride(q), stride(k), stride(v),
+                              max_q, max_kv, scale, data<void>(out), ws, ws_bytes,
+                              status_of(a[8]), s);
+  });
+}
+
 PyMethodDef methods[] = {
     {"step_plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(step_plan)),
      METH_FASTCALL, nullptr},
@@ -370,6 +415,9 @@ PyMethodDef methods[] = {
      nullptr},
     {"chunk_attention",
      reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(chunk_attention)), METH_FASTCALL,
+     nullptr},
+    {"cross_attention",
+     reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cross_attention)), METH_FASTCALL,
      nullptr},
     {"decode_grouped",
      reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_grouped)), METH_FASTCALL,

@@ -257,6 +257,52 @@ def pa_chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_offset
     return out
 
 
+def pa_cross_attention_workspace_size(B, T, H, Hkv, D, max_q_len, max_kv_len):
+    """Bytes of workspace pa_cross_attention uses on the current device."""
+    return lib().pa_cross_attention_workspace_size(B, T, H, Hkv, D, max_q_len, max_kv_len)
+
+
+def pa_cross_attention(q, k, v, q_offsets, kv_starts, kv_lens, scale, max_q_len=None,
+                       max_kv_len=None, out=None, workspace=None, split=True, status=None,
+                       stream=None):
+    """Attention of packed queries over other rows, all of which each query sees: a
+    decoder's tokens over an encoder's states, or (k, v, offsets of its own) an encoder's
+    over themselves.  q [T,H,D]; k and v [Tk,Hkv,D] (views of one projection's output are
+    fine); request b's queries are rows q_offsets[b] .. q_offsets[b+1]-1 (the beams of a
+    request are queries of it) and its keys rows kv_starts[b] .. kv_starts[b]+kv_lens[b]-1,
+    all int32, [B+1], [B] and [B].  ``max_q_len`` and ``max_kv_len`` bound the lengths
+    (None: T and Tk); with a few queries a request the first says that the kernel of
+    single tokens serves them.  A workspace for the split of long keys is allocated when
+    not given; split=False passes none.  Returns ``out`` [T,H,D]; rows outside the
+    requests are left as they were, rows of a request without keys are zeros."""
+    name = "pa_cross_attention"
+    if not isinstance(q, torch.Tensor):
+        raise TypeError(f"{name}: q must be a torch.Tensor")
+    if max_q_len is None:
+        max_q_len = _size(q, 0) or 0
+    if max_kv_len is None:
+        max_kv_len = _size(k, 0) or 0
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    own = split and workspace is None  # (allocated by the binding)
+    if not split:
+        workspace = None
+    rc = _binding().cross_attention(q, k, v, q_offsets, kv_starts, kv_lens, out,
+                                    own or workspace, status, max_q_len, max_kv_len, scale,
+                                    _handle(name, stream, q))
+    if rc:
+        B = None if _size(q_offsets, 0) is None else q_offsets.shape[0] - 1
+        D, Tk, Hkv = _size(q, 2), _size(k, 0), _size(k, 1)
+        _failed(rc, name, q,
+                (("q_offsets", q_offsets, torch.int32, (None,)),
+                 ("kv_starts", kv_starts, torch.int32, (B,)),
+                 ("kv_lens", kv_lens, torch.int32, (B,)),
+                 ("out", out, None, tuple(q.shape)), *_workspace_arg(workspace)),
+                (("q", q, None, (None, None, None)), ("k", k, None, (None, None, D)),
+                 ("v", v, None, (Tk, Hkv, D))), status)
+    return out
+
+
 def _cache_args(q, k_cache, v_cache, block_tables, context_lens, B):
     pool = (_size(k_cache, 0), _size(k_cache, 1), _size(k_cache, 2), _size(q, 2))
     return (("k_cache", k_cache, None, pool), ("v_cache", v_cache, None, pool),
