@@ -71,11 +71,14 @@ typedef enum pa_status {
 #define PA_DEV_BAD_PAIR 0x8       /* a copy pair outside [0, num_blocks) */
 #define PA_DEV_TIMEOUT 0x10       /* a bounded wait inside a kernel gave up */
 #define PA_DEV_NO_BLOCKS 0x20     /* the free ring holds fewer blocks than a step needs */
+#define PA_DEV_BAD_BEAM 0x40      /* a parent or beam outside [0, W), a length past the steps */
+#define PA_DEV_BAD_LOGITS 0x80    /* NaN or +inf among a live beam's logits */
 
-/* Element type of the calls that take one (2 bytes each). */
+/* Element type of the calls that take one: 2 bytes each, and 4 of logits. */
 typedef enum pa_dtype {
-    PA_F16 = 0, /* IEEE binary16 */
-    PA_BF16 = 1 /* bfloat16 */
+    PA_F16 = 0,  /* IEEE binary16 */
+    PA_BF16 = 1, /* bfloat16 */
+    PA_F32 = 2   /* IEEE binary32, pa_beam_select's logits only */
 } pa_dtype;
 
 /* Human-readable name of a status code (static storage). */
@@ -657,6 +660,124 @@ pa_status pa_decode_grouped(const void *q, const void *k_cache, const void *v_ca
                             int num_blocks, int max_blocks_per_seq, int max_context_len,
                             int partition_tokens, float scale, void *out, void *workspace,
                             size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/* ===========================================================================
+ * Beam search over the paged cache.
+ *
+ * A request has W beams (1 .. 32): sequences b * W .. b * W + W-1 of the calls
+ * above, which share blocks until they part (study notes "4. PagedAttention
+ * 带来的核心红利": a block is copied when one of them writes).  A step of a decoder:
+ * pa_step_plan, pa_rope_cache_write, pa_decode_grouped over all B * W sequences
+ * (and pa_cross_attention, the beams being queries of their request), then
+ * pa_beam_select on the logits, pa_beam_reorder of the tables, and pa_block_copy
+ * with its pairs in every layer's cache.  The steps' tokens and parents are kept,
+ * [S, B, W] each (an output of pa_beam_select may be a slice of them), and
+ * pa_beam_backtrack gathers sequences from them.  B * W is at most 2^20.  None of
+ * these calls keeps anything between calls; a workspace belongs to one call at a
+ * time.
+ * ========================================================================= */
+
+/* ---------------------------------------------------------------------------
+ * Beam selection: the best continuations over beams and vocabulary.
+ *
+ * With x_w the logits of beam w of a request, candidate (w, v) has the score
+ *     c(w, v) = scores[w] + x_w[v] - log sum_u exp(x_w[u])
+ * (log-probabilities in place of logits give the same).  The W best candidates
+ * with v != eos_token are the next beams, best first; of equal ones the lowest
+ * (w, v) comes first.  Candidates are compared as the definition has them: two of
+ * one beam by their logits, two of different beams in 64 bits.  Written [B, W]:
+ *   tokens, parents  v and w of each
+ *   new_scores       c, rounded once; may be scores itself
+ *   ended_scores     by beam w: c(w, eos_token) if it is better than the last of
+ *                    the W chosen (the hypothesis of beam w ends here), else -inf
+ * eos_token -1: no candidate ends.  A score of -inf (any that is not finite) is a
+ * beam that is not there: the first step has one of 0 and W - 1 of -inf, a request that
+ * is done W of them; its logits are not read.  A logit of -inf is never chosen.  A
+ * place that no candidate fills gets pad_token, its own index as parent and -inf.  A
+ * beam with NaN or +inf among its logits gives no candidate, flagged PA_DEV_BAD_LOGITS.
+ *
+ * logits [B * W] rows of V in dtype (PA_F32 too), row_stride >= V elements apart
+ * scores [B, W] float32; V below 2^31 - 32768; eos_token below V
+ * workspace: at least pa_beam_select_workspace_size(B, W, V) bytes, 16-byte aligned,
+ * else PA_ERR_WORKSPACE; the size depends on the SM count of the current device.
+ * W above 32 returns PA_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+size_t pa_beam_select_workspace_size(int B, int W, int V);
+
+pa_status pa_beam_select(const void *logits, pa_dtype dtype, int64_t row_stride,
+                         const float *scores, int B, int W, int V, int eos_token,
+                         int pad_token, int32_t *tokens, int32_t *parents,
+                         float *new_scores, float *ended_scores, void *workspace,
+                         size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Beam reorder: block tables that follow the chosen beams.
+ *
+ * Beam w of request b goes on from its beam p = parents[b][w]: row b * W + w of
+ * tables_out gets the ceil(n / block_size) first entries of row b * W + p, n =
+ * context_lens[b * W + p], and -1 in all others; context_lens_out gets n.  p = -1
+ * ends the beam: an empty row, length 0.
+ *
+ * Copy-on-write: when n is no multiple of block_size, the beam's next token goes into
+ * the row's last block.  The first beam of the request with that block keeps it; every
+ * further one gets a block from the free list (the ring of pa_step_plan, first in, first
+ * out, beams in order) in its place, and copy_pairs[b * W + w] = (old, new) for
+ * pa_block_copy; of all other beams the pair is (0, 0), which copies nothing.  When n is
+ * a multiple, pa_step_plan gives each beam its next block.
+ *
+ * Back to the list: a block that rows of the request held at a column, and that none of
+ * them holds there any more, is written to the ring behind the last one, requests in
+ * order, then columns, then beams (so equal inputs give equal rings); columns below
+ * shared_lens[b] / block_size are left out (NULL: none).  No counts of holders are
+ * needed while a request's beams have grown from one sequence: blocks that requests
+ * share are then of a prefix which all beams hold, so that they come back only when all
+ * beams of a request end; such a request names its shared tokens in shared_lens.
+ *
+ * free_state_out: blocks taken and put after the call.  All or nothing: when the blocks
+ * needed exceed those held before the call, or free_state is none that a ring of
+ * num_blocks can have, PA_DEV_NO_BLOCKS is flagged and everything stays as it was
+ * (copied, where outputs are other arrays; no pairs).  A request with a parent outside
+ * [-1, W) (PA_DEV_BAD_BEAM), a length that its rows cannot hold or a negative shared
+ * length (PA_DEV_BAD_CONTEXT) stays as it was, too.  An id outside [0, num_blocks) in a
+ * last block, in the ring (the entry is then -1) or among those that would come back is
+ * flagged PA_DEV_BAD_BLOCK_ID and neither copied nor put; others are moved unseen.
+ *
+ * parents [B, W], block_tables and tables_out [B * W, max_blocks_per_seq], context_lens
+ * and context_lens_out [B * W], shared_lens [B] int32, copy_pairs [B * W, 2] int64;
+ * free_blocks and free_state as for pa_step_plan.  tables_out may be block_tables,
+ * context_lens_out context_lens, and free_state_out free_state.
+ * W at most 32, block_size in {4, 8, 16, 32} (else PA_ERR_UNSUPPORTED);
+ * max_blocks_per_seq * block_size below 2^31 - 64.  workspace: at least
+ * pa_beam_reorder_workspace_size(...) bytes (0 for small batches), 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+size_t pa_beam_reorder_workspace_size(int B, int W, int max_blocks_per_seq);
+
+pa_status pa_beam_reorder(const int32_t *parents, const int32_t *block_tables,
+                          const int32_t *context_lens, const int32_t *shared_lens, int B,
+                          int W, int block_size, int num_blocks, int max_blocks_per_seq,
+                          int32_t *free_blocks, const int64_t *free_state,
+                          int32_t *tables_out, int32_t *context_lens_out,
+                          int64_t *free_state_out, int64_t *copy_pairs, void *workspace,
+                          size_t workspace_bytes, int32_t *status, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Beam backtrack: hypotheses' tokens from the steps' tokens and parents.
+ *
+ * Hypothesis k of request b has n = lengths[b][k] tokens and ends in beam beams[b][k]:
+ *     beam(n - 1) = beams[b][k],  beam(s - 1) = parents[s][b][beam(s)],
+ *     out[b][k][s] = tokens[s][b][beam(s)] for s < n, pad_token behind
+ * (one that ended with eos_token at step s, by ended_scores of its beam w, has length s
+ * and beam w; its end is no token of it).
+ *
+ * tokens, parents [S, B, W] int32; lengths, beams [B, K] int32; out [B, K, S] int32.
+ * A length outside [0, S] or a beam outside [0, W) gives pad_token alone, a parent outside
+ * [0, W) pad_token in the steps before it; both flagged PA_DEV_BAD_BEAM.  W and K at most
+ * 32 (else PA_ERR_UNSUPPORTED), S below 2^26 - 1024.
+ * ------------------------------------------------------------------------- */
+pa_status pa_beam_backtrack(const int32_t *tokens, const int32_t *parents,
+                            const int32_t *lengths, const int32_t *beams, int S, int B,
+                            int W, int K, int pad_token, int32_t *out, int32_t *status,
+                            pa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -20,6 +20,8 @@ PA_DEV_BAD_SLOT = 0x4
 PA_DEV_BAD_PAIR = 0x8
 PA_DEV_TIMEOUT = 0x10
 PA_DEV_NO_BLOCKS = 0x20
+PA_DEV_BAD_BEAM = 0x40
+PA_DEV_BAD_LOGITS = 0x80
 
 # Every symbol include/pagedkv.h declares.
 EXPORTS = (
@@ -34,6 +36,8 @@ EXPORTS = (
     "pa_chunk_attention_workspace_size", "pa_chunk_attention",
     "pa_decode_grouped_workspace_size", "pa_decode_grouped",
     "pa_cross_attention_workspace_size", "pa_cross_attention",
+    "pa_beam_select_workspace_size", "pa_beam_select",
+    "pa_beam_reorder_workspace_size", "pa_beam_reorder", "pa_beam_backtrack",
 )
 
 # Size of the fixed scratch array behind pa_decode_static (PA_DECODE_STATIC_SCRATCH_BYTES).
@@ -123,6 +127,16 @@ def _bind(lib):
     lib.pa_cross_attention.argtypes = [_P] * 6 + [_I] * 7 + [_L] * 3 + [_I] * 2 + [
         ctypes.c_float, _P, _P, _SZ, _P, _P]
     lib.pa_cross_attention.restype = _I
+    lib.pa_beam_select_workspace_size.argtypes = [_I] * 3
+    lib.pa_beam_select_workspace_size.restype = _SZ
+    lib.pa_beam_select.argtypes = [_P, _I, _L, _P] + [_I] * 5 + [_P] * 5 + [_SZ, _P, _P]
+    lib.pa_beam_select.restype = _I
+    lib.pa_beam_reorder_workspace_size.argtypes = [_I] * 3
+    lib.pa_beam_reorder_workspace_size.restype = _SZ
+    lib.pa_beam_reorder.argtypes = [_P] * 4 + [_I] * 5 + [_P] * 7 + [_SZ, _P, _P]
+    lib.pa_beam_reorder.restype = _I
+    lib.pa_beam_backtrack.argtypes = [_P] * 4 + [_I] * 5 + [_P] * 3
+    lib.pa_beam_backtrack.restype = _I
     return lib
 
 

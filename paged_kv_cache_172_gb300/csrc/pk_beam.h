@@ -1,0 +1,61 @@
+// pk_beam.h -- declarations shared between the C-ABI layer and the kernels of beam
+// search (host side).
+#pragma once
+
+#include "pk_internal.h"
+
+namespace pk {
+
+constexpr int kMaxBeams = 32;
+
+// Beam selection (beam_select.cu).
+struct BeamSelectArgs {
+  const void* logits;  // rows of V, row_stride elements apart
+  long long row_stride;
+  const float* scores;  // [B, W]
+  int32_t* tokens;      // [B, W] the chosen continuations, best first
+  int32_t* parents;
+  float* new_scores;
+  float* ended;  // [B, W] by beam
+  // Per row and split: its W best (keys of 64 bits, in order), its maximum and sum.
+  unsigned long long* ws_keys;  // [B * W][splits][W]
+  double* ws_sum;               // [B * W][splits]
+  float* ws_max;                // [B * W][splits]
+  int32_t* status;
+  int B, W, V, eos, pad, dtype;
+  int splits;
+};
+int beam_select_splits(int B, int W, int V);
+cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t stream);
+
+// Block tables that follow the beams (beam_tables.cu).
+struct BeamReorderArgs {
+  const int32_t* parents;       // [B, W]
+  const int32_t* block_tables;  // [B * W, M]
+  const int32_t* context_lens;  // [B * W]
+  const int32_t* shared_lens;   // [B] or null
+  int32_t* ring;                // [num_blocks]
+  const int64_t* free_state;    // [2]
+  int32_t* tables_out;
+  int32_t* lens_out;
+  int64_t* free_state_out;
+  int64_t* pairs;   // [B * W, 2]
+  int64_t* counts;  // [B + 1, 2] workspace of the launch by requests, or null
+  int32_t* status;
+  int B, W, M, bs_log2, num_blocks;
+};
+bool beam_reorder_in_one(int B, int W, int M);
+cudaError_t launch_beam_reorder(const BeamReorderArgs& a, cudaStream_t stream);
+
+struct BeamBacktrackArgs {
+  const int32_t* tokens;   // [S, B, W]
+  const int32_t* parents;  // [S, B, W]
+  const int32_t* lengths;  // [B, K]
+  const int32_t* beams;    // [B, K]
+  int32_t* out;            // [B, K, S]
+  int32_t* status;
+  int S, B, W, K, pad;
+};
+cudaError_t launch_beam_backtrack(const BeamBacktrackArgs& a, cudaStream_t stream);
+
+}  // namespace pk

@@ -1,4 +1,5 @@
-// py_grouped.cpp -- the Python binding of a serving step with grouped K/V heads.
+// py_grouped.cpp -- the Python binding of a serving step with grouped K/V heads, and of
+// beam search.
 //
 // The kernels of a single-token step take 2 to 6 us; checking ten to seventeen
 // tensor arguments and marshalling them through ctypes took 7 to 9 us of host
@@ -7,7 +8,7 @@
 // tensors' device's current one where none is given), makes that device current
 // and calls the C entry point of the same name (include/pagedkv.h).  It returns
 // the entry point's status, or -1 where an argument does not fit: the caller
-// (grouped.py) then looks for the one to complain about.
+// (grouped.py, beam.py) then looks for the one to complain about.
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <ATen/ops/empty.h>
@@ -404,7 +405,134 @@ PyObject* cross_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// logits, scores, tokens, parents, new_scores, ended_scores, workspace (None: one is
+// allocated), status, eos_token, pad_token, stream
+PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> int {
+    const at::Tensor *x = tensor(a[0]), *sc = tensor(a[1]), *tok = tensor(a[2]),
+                     *par = tensor(a[3]), *ns = tensor(a[4]), *end = tensor(a[5]);
+    int eos, pad;
+    pa_stream_t s;
+    void* ws;
+    size_t ws_bytes;
+    if (!number(a[8], &eos) || !number(a[9], &pad)) return kUnfit;
+    if (x == nullptr || !x->is_cuda() || x->dim() != 2 || sc == nullptr || sc->dim() != 2 ||
+        a[6] == Py_True)
+      return kUnfit;
+    pa_dtype type;
+    if (x->scalar_type() == ScalarType::Float)
+      type = PA_F32;
+    else if (!half_type(x, &type))
+      return kUnfit;
+    const int dev = x->get_device();
+    const int64_t B = sc->size(0), W = sc->size(1), V = x->size(1);
+    const int64_t step = x->size(0) > 1 ? x->stride(0) : V;
+    if (B > INT32_MAX || W > INT32_MAX || V > INT32_MAX || x->size(0) != B * W ||
+        (V > 1 && x->stride(1) != 1) || !dense(sc, ScalarType::Float, dev, {B, W}) ||
+        !dense(tok, ScalarType::Int, dev, {B, W}) || !dense(par, ScalarType::Int, dev, {B, W}) ||
+        !dense(ns, ScalarType::Float, dev, {B, W}) ||
+        !dense(end, ScalarType::Float, dev, {B, W}) ||
+        !workspace_fits(a[6], dev, &ws, &ws_bytes) || !status_fits(a[7], dev) ||
+        !stream_of(a[10], dev, &s))
+      return kUnfit;
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    at::Tensor own;
+    if (a[6] == Py_None) {
+      ws_bytes = pa_beam_select_workspace_size((int)B, (int)W, (int)V);
+      if (ws_bytes > 0) {
+        own = workspace_for(ws_bytes, dev, a[10], s);
+        ws = own.data_ptr();
+      }
+    }
+    return pa_beam_select(data<void>(x), type, step, data<float>(sc), (int)B, (int)W, (int)V,
+                          eos, pad, data<int32_t>(tok), data<int32_t>(par), data<float>(ns),
+                          data<float>(end), ws, ws_bytes, status_of(a[7]), s);
+  });
+}
+
+// parents, block_tables, context_lens, free_blocks, free_state, shared_lens (or None),
+// tables_out, context_lens_out, free_state_out, copy_pairs, workspace (None: one is
+// allocated where the call needs it), status, block_size, stream
+PyObject* beam_reorder(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> int {
+    const at::Tensor *par = tensor(a[0]), *bt = tensor(a[1]), *ctx = tensor(a[2]),
+                     *ring = tensor(a[3]), *st = tensor(a[4]), *sh = tensor(a[5]),
+                     *bo = tensor(a[6]), *co = tensor(a[7]), *so = tensor(a[8]),
+                     *pairs = tensor(a[9]);
+    int bs;
+    pa_stream_t s;
+    void* ws;
+    size_t ws_bytes;
+    if (!number(a[12], &bs)) return kUnfit;
+    if (par == nullptr || !par->is_cuda() || par->dim() != 2 || bt == nullptr ||
+        bt->dim() != 2 || ring == nullptr || ring->dim() != 1 || a[10] == Py_True)
+      return kUnfit;
+    const int dev = par->get_device();
+    const int64_t B = par->size(0), W = par->size(1), M = bt->size(1), NB = ring->size(0);
+    if (B > INT32_MAX || W > INT32_MAX || M > INT32_MAX || NB > INT32_MAX ||
+        !dense(par, ScalarType::Int, dev, {B, W}) ||
+        !dense(bt, ScalarType::Int, dev, {B * W, M}) ||
+        !dense(ctx, ScalarType::Int, dev, {B * W}) || !dense(ring, ScalarType::Int, dev, {NB}) ||
+        !dense(st, ScalarType::Long, dev, {2}) ||
+        (a[5] != Py_None && !dense(sh, ScalarType::Int, dev, {B})) ||
+        !dense(bo, ScalarType::Int, dev, {B * W, M}) ||
+        !dense(co, ScalarType::Int, dev, {B * W}) || !dense(so, ScalarType::Long, dev, {2}) ||
+        !dense(pairs, ScalarType::Long, dev, {B * W, 2}) ||
+        !workspace_fits(a[10], dev, &ws, &ws_bytes) || !status_fits(a[11], dev) ||
+        !stream_of(a[13], dev, &s))
+      return kUnfit;
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    at::Tensor own;
+    if (a[10] == Py_None) {
+      ws_bytes = pa_beam_reorder_workspace_size((int)B, (int)W, (int)M);
+      if (ws_bytes > 0) {
+        own = workspace_for(ws_bytes, dev, a[13], s);
+        ws = own.data_ptr();
+      }
+    }
+    return pa_beam_reorder(data<int32_t>(par), data<int32_t>(bt), data<int32_t>(ctx),
+                           data<int32_t>(sh), (int)B, (int)W, bs, (int)NB, (int)M,
+                           data<int32_t>(ring), data<int64_t>(st), data<int32_t>(bo),
+                           data<int32_t>(co), data<int64_t>(so), data<int64_t>(pairs), ws,
+                           ws_bytes, status_of(a[11]), s);
+  });
+}
+
+// tokens, parents, lengths, beams, out, status, pad_token, stream
+PyObject* beam_backtrack(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> int {
+    const at::Tensor *tok = tensor(a[0]), *par = tensor(a[1]), *len = tensor(a[2]),
+                     *beam = tensor(a[3]), *out = tensor(a[4]);
+    int pad;
+    pa_stream_t s;
+    if (!number(a[6], &pad)) return kUnfit;
+    if (tok == nullptr || !tok->is_cuda() || tok->dim() != 3 || len == nullptr ||
+        len->dim() != 2)
+      return kUnfit;
+    const int dev = tok->get_device();
+    const int64_t S = tok->size(0), B = tok->size(1), W = tok->size(2), K = len->size(1);
+    if (S > INT32_MAX || B > INT32_MAX || W > INT32_MAX || K > INT32_MAX ||
+        !dense(tok, ScalarType::Int, dev, {S, B, W}) ||
+        !dense(par, ScalarType::Int, dev, {S, B, W}) ||
+        !dense(len, ScalarType::Int, dev, {B, K}) || !dense(beam, ScalarType::Int, dev, {B, K}) ||
+        !dense(out, ScalarType::Int, dev, {B, K, S}) || !status_fits(a[5], dev) ||
+        !stream_of(a[7], dev, &s))
+      return kUnfit;
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    return pa_beam_backtrack(data<int32_t>(tok), data<int32_t>(par), data<int32_t>(len),
+                             data<int32_t>(beam), (int)S, (int)B, (int)W, (int)K, pad,
+                             data<int32_t>(out), status_of(a[5]), s);
+  });
+}
+
 PyMethodDef methods[] = {
+    {"beam_select", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(beam_select)),
+     METH_FASTCALL, nullptr},
+    {"beam_reorder", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(beam_reorder)),
+     METH_FASTCALL, nullptr},
+    {"beam_backtrack",
+     reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(beam_backtrack)), METH_FASTCALL,
+     nullptr},
     {"step_plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(step_plan)),
      METH_FASTCALL, nullptr},
     {"rope_cache_write",
