@@ -27,7 +27,7 @@ extern "C" {
 size_t pa_beam_select_workspace_size(int B, int W, int V) {
   if (B <= 0 || !beams_ok(B, W) || W > pk::kMaxBeams || V <= 0 || V > kMaxCount) return 0;
   const size_t lists = (size_t)B * W * pk::beam_select_splits(B, W, V);
-  return lists * (W * 8 + 8 + 4);
+  return lists * (W * 8 + 4 + 4);
 }
 
 pa_status pa_beam_select(const void* logits, pa_dtype dtype, int64_t row_stride,
@@ -65,8 +65,8 @@ pa_status pa_beam_select(const void* logits, pa_dtype dtype, int64_t row_stride,
   a.splits = pk::beam_select_splits(B, W, V);
   const size_t lists = (size_t)B * W * a.splits;
   a.ws_keys = static_cast<unsigned long long*>(workspace);
-  a.ws_sum = reinterpret_cast<double*>(a.ws_keys + lists * W);
-  a.ws_max = reinterpret_cast<float*>(a.ws_sum + lists);
+  a.ws_sum = reinterpret_cast<float*>(a.ws_keys + lists * W);
+  a.ws_max = a.ws_sum + lists;
   return launched(pk::launch_beam_select(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -67,6 +67,15 @@ __device__ __forceinline__ Key warp_max(Key k) {
   return ((Key)top << 32) | lo;
 }
 
+// The warp's sums l relative to maxima m, relative to M, added in 64 bits.  (A lane
+// without values has m = -inf and l = 0; a NaN among l stays one.)
+__device__ __forceinline__ double add_up(float l, float m, float M) {
+  double x = l != 0.f ? l * ex2_approx((m - M) * kLog2e) : 0.f;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
+  return x;
+}
+
 template <typename T>
 __device__ __forceinline__ float to_float(T x) {
   if constexpr (std::is_same<T, float>::value)
@@ -126,7 +135,7 @@ struct Shared {
   Key list[kList];
   Key sorted[kMaxBeams];
   uint32_t group[kGroups];
-  double sum[kThreads / 32];
+  float sum[kThreads / 32];
   float max[kThreads / 32];
   Key best[kThreads / 32];
   int count;
@@ -291,15 +300,24 @@ __global__ void __launch_bounds__(kThreads, 2) beam_rows_kernel(const BeamSelect
     s.sum[warp] = l;
   }
   __syncthreads();
-  if (tid == 0) {
-    float M = -INFINITY;
-    for (int w = 0; w < kThreads / 32; ++w) M = fmaxf(M, s.max[w]);
-    double L = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w)
-      if (s.sum[w] != 0.0) L += s.sum[w] * exp((double)s.max[w] - (double)M);
+  if (warp > 0) return;
+  m = lane < kThreads / 32 ? s.max[lane] : -INFINITY;
+  l = lane < kThreads / 32 ? s.sum[lane] : 0.f;
+  const float M = unordered(__reduce_max_sync(kAll, ordered(m)));
+  const double L = add_up(l, m, M);
+  if (lane == 0) {
     a.ws_max[at] = M;
-    a.ws_sum[at] = L;
+    a.ws_sum[at] = (float)L;
   }
+}
+
+// Order of doubles as unsigned numbers.
+__device__ __forceinline__ double unordered(Key o) {
+  return __longlong_as_double((long long)(o ^ ((o >> 63) ? 1ull << 63 : ~0ull)));
+}
+__device__ __forceinline__ Key ordered(double x) {
+  const Key u = (Key)__double_as_longlong(x);
+  return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
 }
 
 // One CTA to a request, a warp to a beam.
@@ -321,11 +339,9 @@ __global__ void beam_merge_kernel(const BeamSelectArgs a) {
     const Key* keys = a.ws_keys + (size_t)row * S * W;
     for (int i = lane; i < S * W; i += 32) s_keys[(size_t)w * S * W + i] = keys[i];
     const float m = lane < S ? a.ws_max[(size_t)row * S + lane] : -INFINITY;
-    double l = lane < S ? a.ws_sum[(size_t)row * S + lane] : 0.0;
+    const float part = lane < S ? a.ws_sum[(size_t)row * S + lane] : 0.f;
     const float M = unordered(__reduce_max_sync(kAll, ordered(m)));
-    l = l != 0.0 ? l * exp((double)m - (double)M) : 0.0;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(kAll, l, d);
+    const double l = add_up(part, m, M);
     // Nothing allowed (l = 0) gives no candidate; NaN or +inf among the logits neither.
     if (isnan(l)) {
       if (lane == 0) flag_status(a.status, PA_DEV_BAD_LOGITS);
@@ -352,57 +368,47 @@ __global__ void beam_merge_kernel(const BeamSelectArgs a) {
   const float sc = lane < W ? a.scores[b * W + lane] : -INFINITY;
   const double ls = lane < W ? s_lse[lane] : -INFINITY;
   const bool here = ls > -INFINITY;
-  auto candidate = [&](float x) { return (double)sc + ((double)x - ls); };
+  auto candidate = [&](float x) { return (double)sc + ((double)x - ls) + 0.0; };
   at = 0;
   Key k = here ? s_top[lane * W] : 0;
-  double c = k != 0 ? candidate(value_of(k)) : -INFINITY;
+  // (0: none; what a finite number is ordered as is not)
+  Key c = k != 0 ? ordered(candidate(value_of(k))) : 0;
   Key my_key = 0;  // of place `lane`
   int my_beam = lane;
-  double my_c = -INFINITY, last_c = -INFINITY;
+  Key my_c = 0, last_c = 0, last_key = 0;
   int last_beam = 0;
-  Key last_key = 0;
   for (int r = 0; r < W; ++r) {
-    double best = c;
-    int who = lane;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
-      const double oc = __shfl_xor_sync(kAll, best, d);
-      const int ow = __shfl_xor_sync(kAll, who, d);
-      if (oc > best || (oc == best && ow < who)) {
-        best = oc;
-        who = ow;
-      }
-    }
+    const Key best = warp_max(c);
     last_c = best;
-    last_beam = who;
-    last_key = __shfl_sync(kAll, k, who);
-    if (best == -INFINITY) break;
+    if (best == 0) break;
+    last_beam = __ffs(__ballot_sync(kAll, c == best)) - 1;
+    last_key = __shfl_sync(kAll, k, last_beam);
     if (lane == r) {
       my_c = best;
-      my_beam = who;
+      my_beam = last_beam;
       my_key = last_key;
     }
-    if (lane == who) {
+    if (lane == last_beam) {
       ++at;
       k = at < W ? s_top[lane * W + at] : 0;
-      c = k != 0 ? candidate(value_of(k)) : -INFINITY;
+      c = k != 0 ? ordered(candidate(value_of(k))) : 0;
     }
   }
   if (lane >= W) return;
   const int o = b * W + lane;
   a.tokens[o] = my_key != 0 ? index_of(my_key) : a.pad;
   a.parents[o] = my_beam;
-  a.new_scores[o] = (float)my_c;
+  a.new_scores[o] = my_c != 0 ? (float)unordered(my_c) : -INFINITY;
   // ---- ends that are better than the last one chosen
   float ended = -INFINITY;
   if (here && a.eos >= 0) {
     const float x = to_float<T>(
         static_cast<const T*>(a.logits)[(long long)o * a.row_stride + a.eos]) + 0.f;
-    const double e = candidate(x);
-    const bool ahead = lane == last_beam && last_c > -INFINITY
+    const Key e = ordered(candidate(x));
+    const bool ahead = last_c != 0 && lane == last_beam
                            ? key_of(x, a.eos) > last_key
                            : e > last_c || (e == last_c && lane < last_beam);
-    if (e > -INFINITY && ahead) ended = (float)e;
+    if (x > -INFINITY && ahead) ended = (float)unordered(e);
   }
   a.ended[o] = ended;
 }

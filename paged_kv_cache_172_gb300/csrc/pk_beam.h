@@ -19,7 +19,7 @@ struct BeamSelectArgs {
   float* ended;  // [B, W] by beam
   // Per row and split: its W best (keys of 64 bits, in order), its maximum and sum.
   unsigned long long* ws_keys;  // [B * W][splits][W]
-  double* ws_sum;               // [B * W][splits]
+  float* ws_sum;                // [B * W][splits]
   float* ws_max;                // [B * W][splits]
   int32_t* status;
   int B, W, V, eos, pad, dtype;
