@@ -26,8 +26,7 @@ extern "C" {
 
 size_t pa_beam_select_workspace_size(int B, int W, int V) {
   if (B <= 0 || !beams_ok(B, W) || W > pk::kMaxBeams || V <= 0 || V > kMaxCount) return 0;
-  const size_t lists = (size_t)B * W * pk::beam_select_splits(B, W, V);
-  return lists * (W * 8 + 4 + 4);
+  return 0;
 }
 
 pa_status pa_beam_select(const void* logits, pa_dtype dtype, int64_t row_stride,
@@ -44,9 +43,6 @@ pa_status pa_beam_select(const void* logits, pa_dtype dtype, int64_t row_stride,
   if (!logits || !scores || !tokens || !parents || !new_scores || !ended_scores ||
       !aligned(logits, dtype == PA_F32 ? 4 : 2))
     return PA_ERR_INVALID;
-  if (!workspace || workspace_bytes < pa_beam_select_workspace_size(B, W, V))
-    return PA_ERR_WORKSPACE;
-  if (!aligned(workspace, 16)) return PA_ERR_INVALID;
   pk::BeamSelectArgs a;
   a.logits = logits;
   a.row_stride = row_stride;
@@ -62,11 +58,7 @@ pa_status pa_beam_select(const void* logits, pa_dtype dtype, int64_t row_stride,
   a.eos = eos_token;
   a.pad = pad_token;
   a.dtype = dtype;
-  a.splits = pk::beam_select_splits(B, W, V);
-  const size_t lists = (size_t)B * W * a.splits;
-  a.ws_keys = static_cast<unsigned long long*>(workspace);
-  a.ws_sum = reinterpret_cast<float*>(a.ws_keys + lists * W);
-  a.ws_max = a.ws_sum + lists;
+  a.ranks = pk::beam_select_ranks(B, W, V);
   return launched(pk::launch_beam_select(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -5,25 +5,27 @@
 // the W largest with v != eos are chosen, best first, ties to the lowest (w, v).
 //
 // Only a row's own W best can be among them, and they are found while the row's sum is:
-// one pass over the logits.  A CTA takes a row, or one of its `splits` ranges, in chunks
-// of 8,192 that its threads hold in registers, with the next chunk's loads in flight.
-// Every thread keeps a running maximum and sum of its own.  Of the first chunk the W-th
-// largest of 64 groups' maxima is a threshold that W values reach and few others; values
-// that reach it go to a list in shared memory as (ordered value, ~index) keys, of which
-// the W best are kept by counting for each how many are above it.  The W-th of them is
-// the threshold of the chunks behind.  Where a chunk has more values over it than the
-// list holds (logits that rise along the row) its own threshold is taken, and where that
-// does not help (equal values) W rounds of the largest key below the last one.  A second
-// launch, one CTA to a request, merges the ranges' lists and then the beams', both in
-// order, by as many rounds as there are beams.
+// one pass over the logits, one launch.  A request is a cluster of CTAs whose warps share
+// out its live beams' rows, a piece of a row to each; no warp waits for another until all
+// pieces are done.  A warp takes its piece in chunks of 512 values that its lanes hold in
+// registers, with the next chunk's loads in flight, and keeps a running maximum and sum in
+// every lane.  Of the first chunk the W-th largest of the lanes' maxima is a threshold that
+// W values reach and few others.  Values that reach it go to a list in shared memory as
+// (ordered value, ~index) keys; when the list is full, its W best are kept by counting for
+// each key how many are above it, and the W-th becomes the threshold, of the other warps
+// of the CTA on that row too.  The cluster's first CTA then merges the pieces' lists by
+// beam and the beams' lists, in order, by as many rounds of a maximum over the lanes as
+// there are beams.
 //
-// Rounding: sums in fp32 by thread and in 64 bits from there, candidates in 64 bits (two
-// beams' can be nearer than fp32 tells apart), the scores once to fp32.  A sum goes by
-// the values' index and not by the row's alignment, so equal rows have equal sums.
+// Rounding: sums in fp32, candidates in 64 bits (two beams' can be nearer than fp32 tells
+// apart), the scores once to fp32.  A sum goes by the values' index and not by the row's
+// alignment, so equal rows have equal sums.
 //
-// Bound: HBM, or the trip from the logits to the threshold to the list and the second
-// launch, for few rows.
+// Bound: HBM, or the trip from the logits to the lists to the merge, for few rows, where
+// the code itself comes from memory: it is kept short.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math.h>
 
 #include <type_traits>
@@ -35,18 +37,19 @@ namespace pk {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kThreads = 512;
-constexpr int kEach = 16;                 // values of a thread and chunk
-constexpr int kChunk = kThreads * kEach;  // values of a chunk
-constexpr int kGroups = kThreads / 8;     // lanes whose maxima make the threshold
-constexpr int kList = 2048;               // keys that reached the threshold, at most
-constexpr int kSlack = 64;                // keys past the W best before they are sorted out
-constexpr int kMaxSplits = 32;
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kEach = 16;           // values of a lane and chunk
+constexpr int kChunk = 32 * kEach;  // values of a warp's chunk
+constexpr int kList = 128;          // keys of a warp's list
+constexpr int kMaxPieces = 64;      // of a row: two lists to a lane of the merge
+constexpr int kMaxCluster = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 using Key = unsigned long long;
 
-// Order of floats as unsigned numbers.  (-0 is taken as +0 before: equal values tie.)
+// Order of floats and doubles as unsigned numbers.
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x);
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
@@ -54,9 +57,16 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
-// Larger values first, then lower indices; 0 stands for none.
+__device__ __forceinline__ Key ordered(double x) {
+  const Key u = (Key)__double_as_longlong(x);
+  return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double unordered(Key o) {
+  return __longlong_as_double((long long)(o ^ ((o >> 63) ? 1ull << 63 : ~0ull)));
+}
+// Larger values first, then lower indices; 0 stands for none.  (-0 is +0: they tie.)
 __device__ __forceinline__ Key key_of(float x, int i) {
-  return ((Key)ordered(x) << 32) | (uint32_t)~i;
+  return ((Key)ordered(x + 0.f) << 32) | (uint32_t)~i;
 }
 __device__ __forceinline__ float value_of(Key k) { return unordered((uint32_t)(k >> 32)); }
 __device__ __forceinline__ int index_of(Key k) { return (int)~(uint32_t)k; }
@@ -67,10 +77,10 @@ __device__ __forceinline__ Key warp_max(Key k) {
   return ((Key)top << 32) | lo;
 }
 
-// The warp's sums l relative to maxima m, relative to M, added in 64 bits.  (A lane
-// without values has m = -inf and l = 0; a NaN among l stays one.)
-__device__ __forceinline__ double add_up(float l, float m, float M) {
-  double x = l != 0.f ? l * ex2_approx((m - M) * kLog2e) : 0.f;
+// The warp's sums l relative to its maxima m, relative to M.  (A lane without values has
+// m = -inf and l = 0; a NaN among l stays one.)
+__device__ __forceinline__ float add_up(float l, float m, float M) {
+  float x = l != 0.f ? l * ex2_approx((m - M) * kLog2e) : 0.f;
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
   return x;
@@ -86,7 +96,7 @@ __device__ __forceinline__ float to_float(T x) {
     return __bfloat162float(x);
 }
 
-// A thread's values of a chunk as they come from memory.  VEC: 16-byte pieces, every row
+// A lane's values of a chunk as they come from memory.  VEC: 16-byte pieces, every row
 // being aligned; otherwise one value after the other, neighbours in neighbouring lanes.
 template <typename T, bool VEC>
 struct Raw {
@@ -96,13 +106,13 @@ struct Raw {
       VEC, uint4, typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type>::type;
   Piece p[P];
 
-  static __device__ __forceinline__ int index(int base, int k, int j) {  // of value j, piece k
-    return base + (k * kThreads + (int)threadIdx.x) * N + j;
+  static __device__ __forceinline__ int index(int base, int i) {  // of value i of the lane
+    return base + (i / N * 32 + (int)(threadIdx.x & 31)) * N + i % N;
   }
   __device__ __forceinline__ void load(const T* row, int base, int end) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      const int i = index(base, k, 0);
+      const int i = index(base, k * N);
       if (VEC ? i + N <= end : i < end)
         p[k] = __ldcs(reinterpret_cast<const Piece*>(row + i));
     }
@@ -111,287 +121,213 @@ struct Raw {
   __device__ __forceinline__ void get(const T* row, int base, int end, float (&x)[kEach]) const {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      const int i = index(base, k, 0);
-      if constexpr (VEC) {
-        T v[N];
-        *reinterpret_cast<uint4*>(v) = p[k];
+      T v[N];
+      *reinterpret_cast<Piece*>(v) = p[k];
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[k * N + j] = to_float<T>(v[j]) + 0.f;
-        if (i + N > end) {  // the row's last piece, or none of it
+      for (int j = 0; j < N; ++j) x[k * N + j] = to_float<T>(v[j]);
+    }
+    if (base + kChunk > end) {  // a piece's last chunk
 #pragma unroll
-          for (int j = 0; j < N; ++j)
-            x[k * N + j] = i + j < end ? to_float<T>(row[i + j]) + 0.f : -INFINITY;
-        }
-      } else {
-        T v;
-        *reinterpret_cast<Piece*>(&v) = p[k];
-        x[k] = i < end ? to_float<T>(v) + 0.f : -INFINITY;
+      for (int i = 0; i < kEach; ++i) {
+        const int at = index(base, i);
+        if (at >= end)
+          x[i] = -INFINITY;
+        else if (VEC && at - i % N + N > end)
+          x[i] = to_float<T>(row[at]);
       }
     }
   }
 };
 
-struct Shared {
-  Key list[kList];
-  Key sorted[kMaxBeams];
-  uint32_t group[kGroups];
-  float sum[kThreads / 32];
-  float max[kThreads / 32];
-  Key best[kThreads / 32];
-  int count;
-  uint32_t threshold;  // ordered
-};
-
-// The W best of the list's n keys, in order, to its front and to `sorted`; all threads.
-// Keys differ, so that each one's place is the number of those above it.
-__device__ __forceinline__ int sort_out(Shared& s, int n, int W) {
-  const int keep = min(n, W);
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const Key k = s.list[i];
-    int above = 0;
-    for (int j = 0; j < n; ++j) above += s.list[j] > k;
-    if (above < W) s.sorted[above] = k;
+// The W best of a warp's n <= kList keys, in order, to the list's front.  Keys differ, so
+// that each one's place is the number of those above it.
+__device__ __noinline__ int sort_out(Key* list, int n, int W) {
+  constexpr int kMine = kList / 32;
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  Key k[kMine];
+  int above[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    k[j] = lane + 32 * j < n ? list[lane + 32 * j] : 0;
+    above[j] = 0;
   }
-  __syncthreads();
-  if (threadIdx.x < keep) s.list[threadIdx.x] = s.sorted[threadIdx.x];
-  if (threadIdx.x == 0) {
-    s.count = keep;
-    // below any value until there are W
-    s.threshold = keep == W ? (uint32_t)(s.sorted[W - 1] >> 32) : 0u;
+#pragma unroll 1
+  for (int q = 0; q < n; ++q) {
+    const Key o = list[q];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) above[j] += o > k[j];
   }
-  __syncthreads();
-  return keep;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kMine; ++j)
+    if (k[j] != 0 && above[j] < W) list[above[j]] = k[j];
+  __syncwarp();
+  return min(n, W);
 }
 
+// A warp's piece [begin, end) of a row: its W best to the list (0 behind the last), its
+// maximum and sum returned.  shared: a threshold that W values of the row reach.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) beam_rows_kernel(const BeamSelectArgs a) {
-  __shared__ Shared s;
-  const int row = blockIdx.x, split = blockIdx.y, W = a.W;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
-  pdl_launch_dependents();
-  if (!isfinite(a.scores[row])) return;  // a dead beam: the second launch knows it
-  const T* x0 = static_cast<const T*>(a.logits) + (long long)row * a.row_stride;
-  const int chunks = (a.V - 1) / kChunk + 1;
-  const int c0 = (int)((long long)split * chunks / a.splits);
-  const int c1 = (int)((long long)(split + 1) * chunks / a.splits);
-
-  Raw<T, VEC> raw;
-  if (c0 < c1) raw.load(x0, c0 * kChunk, a.V);
-  if (tid == 0) {
-    s.count = 0;
-    s.threshold = 0;
-  }
+__device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos, int W,
+                                       Key* list, uint32_t* shared) {
+  const int lane = threadIdx.x & 31;
   float m = -INFINITY, l = 0.f;
-  int kept = 0;  // of the list's keys, those that were sorted out
-  int held = 0;  // keys of the chunks before
-  constexpr uint32_t kNone = 0x007fffffu;  // ordered(-inf): no candidate
-  for (int c = c0; c < c1; ++c) {
-    const int base = c * kChunk;
+  float t = -FLT_MAX;  // values from it on are candidates (-inf and NaN never)
+  int n = 0;
+  Raw<T, VEC> raw;
+  raw.load(row, begin, end);
+#pragma unroll 1
+  for (int base = begin; base < end; base += kChunk) {
     float x[kEach];
-    raw.get(x0, base, a.V, x);
-    if (c + 1 < c1) raw.load(x0, base + kChunk, a.V);
-    // ---- running maximum and sum
-    float mt = x[0];
+    raw.get(row, base, end, x);
+    if (base + kChunk < end) raw.load(row, base + kChunk, end);
+    float mt = fmaxf(x[0], x[1]);
 #pragma unroll
-    for (int i = 1; i < kEach; ++i) mt = fmaxf(mt, x[i]);
+    for (int i = 2; i < kEach; i += 2) mt = max3f(mt, x[i], x[i + 1]);
     if (mt > m) {
       l *= ex2_approx((m - mt) * kLog2e);  // (m = -inf: l is 0)
       m = mt;
     }
-    const float ref = m == -INFINITY ? 0.f : m;
+    const float ref = m == -INFINITY ? 0.f : -m;
+    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) l += ex2_approx((x[i] - ref) * kLog2e);
-    // ---- candidates: the end is none
-    constexpr int N = Raw<T, VEC>::N;
-    if (a.eos >= base && a.eos - base < kChunk) {
+    for (int i = 0; i < kEach; i += 2) {
+      float a, b;
+      add_f32x2(a, b, x[i], x[i + 1], ref, ref);
+      add_f32x2(s0, s1, s0, s1, ex2_approx(a * kLog2e), ex2_approx(b * kLog2e));
+    }
+    l += s0 + s1;
+    if (eos >= base && eos - base < kChunk) {  // the end is no candidate
 #pragma unroll
       for (int i = 0; i < kEach; ++i)
-        if (Raw<T, VEC>::index(base, i / N, i % N) == a.eos) x[i] = -INFINITY;
+        if (Raw<T, VEC>::index(base, i) == eos) x[i] = -INFINITY;
       mt = x[0];
 #pragma unroll
       for (int i = 1; i < kEach; ++i) mt = fmaxf(mt, x[i]);
     }
-    const uint32_t top = ordered(mt);
-    // Keys from `t` on (behind the first chunk: above it, an equal one comes too late).
-    auto push = [&](uint32_t t) {
-      if (top < t || top <= kNone) return;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const uint32_t o = ordered(x[i]);
-        if (o >= t && o > kNone && !isnan(x[i])) {
-          const int at = atomicAdd(&s.count, 1);
-          if (at < kList) s.list[at] = key_of(x[i], Raw<T, VEC>::index(base, i / N, i % N));
-        }
+    if (base == begin) {
+      // The W-th largest of the lanes' maxima, which W values reach.
+      const uint32_t mine = ordered(mt);
+      int above = 0;
+#pragma unroll 4
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t o = __shfl_sync(kAll, mine, j);
+        above += o > mine || (o == mine && j < lane);
       }
-    };
-    // The W-th largest of the groups' maxima, which W of this chunk's values reach.
-    auto own_threshold = [&]() {
-      uint32_t g = top;
-      g = max(g, __shfl_xor_sync(kAll, g, 1));
-      g = max(g, __shfl_xor_sync(kAll, g, 2));
-      g = max(g, __shfl_xor_sync(kAll, g, 4));
-      if ((lane & 7) == 0) s.group[tid >> 3] = g;
-      __syncthreads();
-      if (tid < kGroups) {
-        const uint32_t mine = s.group[tid];
-        int above = 0;
-#pragma unroll 8
-        for (int j = 0; j < kGroups; ++j) {
-          const uint32_t o = s.group[j];
-          above += o > mine || (o == mine && j < tid);
-        }
-        if (above == W - 1) s.threshold = mine;
-      }
-      __syncthreads();
-      return s.threshold;
-    };
-    if (c == c0) {
-      push(own_threshold());
-    } else {
-      const uint32_t t = s.threshold;
-      push(kept == W ? t + 1 : t);
+      const unsigned at = __ballot_sync(kAll, above == W - 1);
+      t = fmaxf(t, __shfl_sync(kAll, mt, __ffs(at) - 1));
     }
-    __syncthreads();
-    int n = s.count;
-    __syncthreads();
-    const bool full = n > kList;
-    if (full) {
-      if (tid == 0) s.count = held;
-      const uint32_t before = kept == W ? s.threshold + 1 : 0u;
-      const uint32_t mine = own_threshold();
-      push(max(mine, before));
-      __syncthreads();
-      n = s.count;
-      if (n > kList) {
-        Key last = ~0ull;
-        for (int r = 0; r < W; ++r) {
-          Key k = 0;
+    t = fmaxf(t, unordered(*(volatile uint32_t*)shared));
+    const bool last = base + kChunk >= end;
+    bool full = false;
+    if (__any_sync(kAll, mt >= t)) {
+      uint32_t hits = 0;
 #pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            const Key o = key_of(x[i], Raw<T, VEC>::index(base, i / N, i % N));
-            if (ordered(x[i]) > kNone && !isnan(x[i]) && o < last && o > k) k = o;
-          }
-          k = warp_max(k);
-          if (lane == 0) s.best[warp] = k;
-          __syncthreads();
-          k = warp_max(lane < kThreads / 32 ? s.best[lane] : 0);
-          if (tid == 0) s.list[held + r] = k;
-          last = k;
-          __syncthreads();
+      for (int i = 0; i < kEach; ++i) hits |= x[i] >= t ? 1u << i : 0u;
+      // All of them at once, or, where the list has no room, two of a lane at a time.
+      full = n + __reduce_add_sync(kAll, (unsigned)__popc(hits)) > kList;
+      const int width = full ? 2 : kEach;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kEach; i0 += width) {
+        if (full) n = sort_out(list, n, W);
+        const uint32_t part = hits & (((1u << width) - 1) << i0);
+        int at = __popc(part);  // inclusive sum over the lanes
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(kAll, at, d);
+          if (lane >= d) at += y;
         }
-        n = held + W;  // (0 where there was none: below every key)
-        while (n > held && s.list[n - 1] == 0) --n;
-      }
-      __syncthreads();
-    }
-    if (c == c0 || full || n > W + kSlack || c + 1 == c1) n = kept = sort_out(s, n, W);
-    held = n;
-  }
-  // ---- the row's (or range's) keys, maximum and sum
-  const size_t at = (size_t)row * a.splits + split;
-  if (tid < W) a.ws_keys[at * W + tid] = tid < kept ? s.sorted[tid] : 0ull;
-  const float mw = unordered(__reduce_max_sync(kAll, ordered(m)));
-  l *= ex2_approx((m == -INFINITY ? -INFINITY : m - mw) * kLog2e);
+        Key* to = list + n + at - __popc(part);
+        n += __shfl_sync(kAll, at, 31);
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(kAll, l, d);
-  if (lane == 0) {
-    s.max[warp] = mw;
-    s.sum[warp] = l;
+        for (int i = 0; i < kEach; ++i)
+          if (part >> i & 1) *to++ = key_of(x[i], Raw<T, VEC>::index(base, i));
+      }
+    }
+    if (full || last || n > W + 32) {
+      n = sort_out(list, n, W);
+      if (n == W && !last) {  // an equal value of a later chunk comes too late
+        const uint32_t lowest = (uint32_t)(list[W - 1] >> 32);
+        t = fmaxf(t, unordered(lowest + 1));
+        if (lane == 0) atomicMax(shared, lowest);
+      }
+    }
   }
-  __syncthreads();
-  if (warp > 0) return;
-  m = lane < kThreads / 32 ? s.max[lane] : -INFINITY;
-  l = lane < kThreads / 32 ? s.sum[lane] : 0.f;
+  if (lane >= n && lane < W) list[lane] = 0;
   const float M = unordered(__reduce_max_sync(kAll, ordered(m)));
-  const double L = add_up(l, m, M);
-  if (lane == 0) {
-    a.ws_max[at] = M;
-    a.ws_sum[at] = (float)L;
-  }
+  return make_float2(M, add_up(l, m, M));
 }
 
-// Order of doubles as unsigned numbers.
-__device__ __forceinline__ double unordered(Key o) {
-  return __longlong_as_double((long long)(o ^ ((o >> 63) ? 1ull << 63 : ~0ull)));
-}
-__device__ __forceinline__ Key ordered(double x) {
-  const Key u = (Key)__double_as_longlong(x);
-  return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+// What the merge holds: per row (beam) of the cluster its best keys, maximum and sum.
+struct Rows {
+  Key* top;   // [W][W]
+  float2* ml;  // [W]
+};
+
+// log x of a sum, to 2^-25: e log 2 + log f, x = 2^e f with f in [1 / sqrt 2, sqrt 2), so
+// that fp32's half steps are those of a number below 0.35.
+__device__ __forceinline__ double log_of(float x) {
+  int e;
+  float f = frexpf(x, &e);
+  if (f < 0.70710678f) {
+    f *= 2.f;
+    --e;
+  }
+  return e * 0.69314718055994531 + (double)logf(f);
 }
 
-// One CTA to a request, a warp to a beam.
-template <typename T>
-__global__ void beam_merge_kernel(const BeamSelectArgs a) {
-  extern __shared__ Key s_keys[];  // [W][splits * W], then [W][W] sorted
-  __shared__ double s_lse[kMaxBeams];
-  const int W = a.W, S = a.splits, b = blockIdx.x;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Key* s_top = s_keys + (size_t)W * S * W;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int row = b * W + w;
-  const float score = a.scores[row];
-  const bool alive = isfinite(score);
-  // ---- a warp's beam: its log-sum-exp, and its W best in order
-  double lse = -INFINITY;
-  if (alive) {
-    const Key* keys = a.ws_keys + (size_t)row * S * W;
-    for (int i = lane; i < S * W; i += 32) s_keys[(size_t)w * S * W + i] = keys[i];
-    const float m = lane < S ? a.ws_max[(size_t)row * S + lane] : -INFINITY;
-    const float part = lane < S ? a.ws_sum[(size_t)row * S + lane] : 0.f;
-    const float M = unordered(__reduce_max_sync(kAll, ordered(m)));
-    const double l = add_up(part, m, M);
-    // Nothing allowed (l = 0) gives no candidate; NaN or +inf among the logits neither.
-    if (isnan(l)) {
-      if (lane == 0) flag_status(a.status, PA_DEV_BAD_LOGITS);
-    } else if (l > 0.0) {
-      lse = (double)M + log(l);
-    }
-  }
-  __syncwarp();
-  const bool some = lse > -INFINITY;
-  int at = 0;  // the lane's place in its range's list
-  Key head = some && lane < S ? s_keys[((size_t)w * S + lane) * W] : 0;
-  for (int r = 0; r < W; ++r) {
-    const Key k = warp_max(head);
-    if (lane == 0) s_top[w * W + r] = k;
-    if (k != 0 && head == k) {
-      ++at;
-      head = at < W ? s_keys[((size_t)w * S + lane) * W + at] : 0;
-    }
-  }
-  if (lane == 0) s_lse[w] = lse;
-  __syncthreads();
-  if (w > 0) return;
-  // ---- all beams: lane i holds the next candidate of beam i
+// The best over the beams, one CTA to a request; alive: the beams whose rows were taken.
+__device__ __forceinline__ void choose(const BeamSelectArgs& a, int b, uint32_t alive, Rows r,
+                                       Key* cand, double* s_lse, float end_x) {
+  const int W = a.W, tid = threadIdx.x, lane = tid & 31;
   const float sc = lane < W ? a.scores[b * W + lane] : -INFINITY;
-  const double ls = lane < W ? s_lse[lane] : -INFINITY;
-  const bool here = ls > -INFINITY;
-  auto candidate = [&](float x) { return (double)sc + ((double)x - ls) + 0.0; };
-  at = 0;
-  Key k = here ? s_top[lane * W] : 0;
-  // (0: none; what a finite number is ordered as is not)
-  Key c = k != 0 ? ordered(candidate(value_of(k))) : 0;
-  Key my_key = 0;  // of place `lane`
-  int my_beam = lane;
-  Key my_c = 0, last_c = 0, last_key = 0;
-  int last_beam = 0;
-  for (int r = 0; r < W; ++r) {
+  if (tid < 32) {
+    double lse = -INFINITY;
+    if (alive >> lane & 1) {
+      const float2 ml = r.ml[lane];
+      // Nothing allowed (a sum of 0) gives no candidate; NaN or +inf among the logits neither.
+      if (isnan(ml.y))
+        flag_status(a.status, PA_DEV_BAD_LOGITS);
+      else if (ml.y > 0.f)
+        lse = (double)ml.x + log_of(ml.y);
+    }
+    s_lse[lane] = lse;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = tid; i < W * W; i += kThreads) {
+    const int w = i / W;
+    const Key k = (alive >> w & 1) ? r.top[i] : 0;
+    const double lse = s_lse[w];
+    // (0: none; what a finite number is ordered as is not)
+    cand[i] = k != 0 && lse > -INFINITY
+                  ? ordered((double)a.scores[b * W + w] + ((double)value_of(k) - lse) + 0.0)
+                  : 0;
+  }
+  __syncthreads();
+  if (tid >= 32) return;
+  // Lane i holds the next candidate of beam i.
+  int at = 0;
+  Key c = lane < W ? cand[lane * W] : 0;
+  Key my_c = 0, my_key = 0, last_c = 0, last_key = 0;  // of place `lane`; of the last place
+  int my_beam = lane, last_beam = 0;
+#pragma unroll 1
+  for (int j = 0; j < W; ++j) {
     const Key best = warp_max(c);
     last_c = best;
     if (best == 0) break;
     last_beam = __ffs(__ballot_sync(kAll, c == best)) - 1;
-    last_key = __shfl_sync(kAll, k, last_beam);
-    if (lane == r) {
+    const int place = __shfl_sync(kAll, at, last_beam);
+    last_key = r.top[last_beam * W + place];
+    if (lane == j) {
       my_c = best;
       my_beam = last_beam;
       my_key = last_key;
     }
     if (lane == last_beam) {
       ++at;
-      k = at < W ? s_top[lane * W + at] : 0;
-      c = k != 0 ? ordered(candidate(value_of(k))) : 0;
+      c = at < W ? cand[lane * W + at] : 0;
     }
   }
   if (lane >= W) return;
@@ -399,61 +335,170 @@ __global__ void beam_merge_kernel(const BeamSelectArgs a) {
   a.tokens[o] = my_key != 0 ? index_of(my_key) : a.pad;
   a.parents[o] = my_beam;
   a.new_scores[o] = my_c != 0 ? (float)unordered(my_c) : -INFINITY;
-  // ---- ends that are better than the last one chosen
+  // Ends that are better than the last one chosen.
   float ended = -INFINITY;
-  if (here && a.eos >= 0) {
-    const float x = to_float<T>(
-        static_cast<const T*>(a.logits)[(long long)o * a.row_stride + a.eos]) + 0.f;
-    const Key e = ordered(candidate(x));
+  const double lse = s_lse[lane];
+  if (lse > -INFINITY && a.eos >= 0) {
+    const double e = (double)sc + ((double)end_x - lse) + 0.0;
+    const Key eo = ordered(e);
     const bool ahead = last_c != 0 && lane == last_beam
-                           ? key_of(x, a.eos) > last_key
-                           : e > last_c || (e == last_c && lane < last_beam);
-    if (x > -INFINITY && ahead) ended = (float)unordered(e);
+                           ? key_of(end_x, a.eos) > last_key
+                           : eo > last_c || (eo == last_c && lane < last_beam);
+    if (end_x > -INFINITY && ahead) ended = (float)e;
   }
   a.ended[o] = ended;
+}
+
+// The beam of the i-th live row.
+__device__ __forceinline__ int live_beam(uint32_t alive, int i) {
+#pragma unroll 1
+  for (; i > 0; --i) alive &= alive - 1;
+  return __ffs(alive) - 1;
+}
+
+// A cluster to a request.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
+  extern __shared__ Key s_dyn[];
+  __shared__ Key s_list[kWarps][kList];
+  __shared__ float2 s_ml[kWarps];
+  __shared__ uint32_t s_threshold[kMaxBeams];
+  __shared__ double s_lse[32];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = a.ranks, b = blockIdx.x / ranks, rank = blockIdx.x - b * ranks, W = a.W;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < kMaxBeams) s_threshold[tid] = 0;  // below any value
+  pdl_wait();
+  pdl_launch_dependents();
+  // A beam whose score is not finite is not there.
+  const uint32_t alive =
+      __ballot_sync(kAll, lane < W && isfinite(a.scores[b * W + (lane < W ? lane : 0)]));
+  const int rows = __popc(alive);
+  // What the choice needs of the beams, a lane to each.
+  float end_x = -INFINITY;
+  if (rank == 0 && warp == 0 && (alive >> lane & 1) && a.eos >= 0)
+    end_x = to_float<T>(
+        static_cast<const T*>(a.logits)[(long long)(b * W + lane) * a.row_stride + a.eos]);
+  // Pieces of a row: whole 16-byte pieces each, the last ones may be empty.
+  const int pieces = min(kMaxPieces, ranks * kWarps / max(rows, 1));
+  const int length = ((a.V + pieces - 1) / pieces + 15) / 16 * 16;
+  __syncthreads();
+  const int task = warp * ranks + rank;  // (few pieces: spread over the CTAs)
+  if (task < rows * pieces) {
+    const int r = task / pieces, w = live_beam(alive, r);
+    const int begin = (int)min((long long)(task - r * pieces) * length, (long long)a.V);
+    const int end = (int)min((long long)begin + length, (long long)a.V);
+    const T* x = static_cast<const T*>(a.logits) + (long long)(b * W + w) * a.row_stride;
+    const float2 ml = scan<T, VEC>(x, begin, end, a.eos, W, s_list[warp], &s_threshold[w]);
+    if (lane == 0) s_ml[warp] = ml;
+  }
+  if (ranks > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  if (rank == 0) {
+    // All lists, [row][piece][W], and their maxima and sums.
+    Key* keys = s_dyn;
+    const int lists = rows * pieces;
+    float2* ml = reinterpret_cast<float2*>(keys + (size_t)ranks * kWarps * W);
+    Rows r = {reinterpret_cast<Key*>(ml + ranks * kWarps), nullptr};
+    r.ml = reinterpret_cast<float2*>(r.top + W * W);
+    Key* cand = reinterpret_cast<Key*>(r.ml + kMaxBeams);
+    auto at_rank = [&](auto* p, int r) { return ranks > 1 ? cluster.map_shared_rank(p, r) : p; };
+#pragma unroll 1
+    for (int i = tid; i < lists * W; i += kThreads) {
+      const int q = i / W;
+      keys[i] = *at_rank(&s_list[q / ranks][i - q * W], q % ranks);
+    }
+#pragma unroll 1
+    for (int q = tid; q < lists; q += kThreads) ml[q] = *at_rank(&s_ml[q / ranks], q % ranks);
+    __syncthreads();
+    // A warp to a beam: rounds of the largest head of its lists, two to a lane.
+#pragma unroll 1
+    for (int i = warp; i < rows; i += kWarps) {
+      const int w = live_beam(alive, i);
+      const Key* mine = keys + (size_t)i * pieces * W;
+      int at[2] = {0, 0};
+      Key head[2];
+      float m[2], l[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int q = lane + 32 * e;
+        const bool has = q < pieces;
+        head[e] = has ? mine[(size_t)q * W] : 0;
+        const float2 v = has ? ml[i * pieces + q] : make_float2(-INFINITY, 0.f);
+        m[e] = v.x;
+        l[e] = v.y;
+      }
+      const float M = unordered(__reduce_max_sync(kAll, max(ordered(m[0]), ordered(m[1]))));
+      const float L = add_up(l[0], m[0], M) + add_up(l[1], m[1], M);
+      if (lane == 0) r.ml[w] = make_float2(M, L);
+#pragma unroll 1
+      for (int j = 0; j < W; ++j) {
+        const Key k = warp_max(max(head[0], head[1]));
+        if (lane == 0) r.top[w * W + j] = k;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (k != 0 && head[e] == k) {
+            ++at[e];
+            head[e] = at[e] < W ? mine[(size_t)(lane + 32 * e) * W + at[e]] : 0;
+          }
+      }
+    }
+    __syncthreads();
+    choose(a, b, alive, r, cand, s_lse, end_x);
+  }
+  if (ranks > 1) cluster.sync();  // nobody leaves while its lists are read
+}
+
+int dynamic_bytes(int W, int ranks) {
+  return ranks * kWarps * (W + 1) * 8 + (2 * W * W + kMaxBeams) * 8;
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
+  constexpr auto kern = beam_select_kernel<T, VEC>;
+  const int smem = dynamic_bytes(a.W, a.ranks);
+  if (smem > 30 * 1024) {
+    const cudaError_t e = ensure_dynamic_smem<kern>(dynamic_bytes(kMaxBeams, kMaxCluster));
+    if (e != cudaSuccess) return e;
+  }
+  if (a.ranks > 8) {
+    const cudaError_t e = ensure_large_cluster<kern>();
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.ranks * a.B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)a.ranks, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = a.ranks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <typename T>
 cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
   const bool vec = (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 &&
                    (a.B * a.W == 1 || a.row_stride * (int)sizeof(T) % 16 == 0);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.B * a.W, a.splits);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, beam_rows_kernel<T, true>, a)
-                      : cudaLaunchKernelEx(&cfg, beam_rows_kernel<T, false>, a);
-  if (e != cudaSuccess) return e;
-  const int smem = (a.W * a.splits * a.W + a.W * a.W) * (int)sizeof(Key);
-  constexpr auto merge = beam_merge_kernel<T>;
-  if (smem > 40 * 1024) {
-    e = ensure_dynamic_smem<merge>(80 * 1024);
-    if (e != cudaSuccess) return e;
-  }
-  cfg.gridDim = dim3(a.B);
-  cfg.blockDim = dim3(32 * a.W);
-  cfg.dynamicSmemBytes = smem;
-  return cudaLaunchKernelEx(&cfg, merge, a);
+  return vec ? launch_t<T, true>(a, stream) : launch_t<T, false>(a, stream);
 }
 
 }  // namespace
 
-// Ranges of a row: as many as fill two CTAs to an SM, a chunk each at least, and no more
-// than the second launch can hold the keys of (64 KB).
-int beam_select_splits(int B, int W, int V) {
-  const long long rows = (long long)B * W;
+// CTAs of a request: as many as the GPU holds at two to an SM, and as there are chunks of
+// its rows for their warps.
+int beam_select_ranks(int B, int W, int V) {
   const int nsm = sm_count() > 0 ? sm_count() : 152;
-  const int chunks = (V - 1) / kChunk + 1;
-  long long s = (2LL * nsm + rows - 1) / rows;
-  if (s > chunks) s = chunks;
-  if (s > kMaxSplits) s = kMaxSplits;
-  if (s > 8192 / (W * W)) s = 8192 / (W * W);
-  return s > 1 ? (int)s : 1;
+  const long long warps = (long long)W * ((V - 1) / kChunk + 1);
+  int c = W > kWarps ? 2 : 1;  // (a warp to a row at least)
+  while (c < kMaxCluster && 2LL * c * B <= 2 * nsm && c * kWarps < warps) c *= 2;
+  return c;
 }
 
 cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t stream) {

@@ -73,6 +73,7 @@ __device__ __forceinline__ Request look_at(const BeamReorderArgs& a, int b) {
       r.flags |= PA_DEV_BAD_BLOCK_ID;
   }
   bool again = false;  // an earlier beam holds it as its last block
+#pragma unroll 1
   for (int u = 0; u < W; ++u) {
     const int t = __shfl_sync(kAll, r.tail, u), id = __shfl_sync(kAll, r.tail_id, u);
     again |= u < lane && t >= 0 && t == r.tail && id == r.tail_id;
@@ -110,10 +111,12 @@ struct Column {
       }
     }
     if (held == 0) return;
+#pragma unroll 1
     for (int w = 0; w < W; ++w)
       if (parent[w] >= 0) used |= 1u << parent[w];
     used &= held;
     if (col < r.first || used == held) return;
+#pragma unroll 1
     for (uint32_t left = held & ~used; left != 0; left &= left - 1) {
       const int w = __ffs(left) - 1, id = at[(size_t)w * a.M];
       // held by a parent, or given back by an earlier beam
@@ -141,24 +144,22 @@ __device__ __forceinline__ long long blocks_held(long long head, long long tail,
 template <int kThreads>
 __device__ __forceinline__ int block_scan(int x, int* s_warp, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int y = x;
+  auto warp_scan = [&](int y) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int z = __shfl_up_sync(kAll, y, d);
-    if (lane >= d) y += z;
-  }
+    for (int d = 1; d < 32; d <<= 1) {
+      const int z = __shfl_up_sync(kAll, y, d);
+      if (lane >= d) y += z;
+    }
+    return y;
+  };
+  const int y = warp_scan(x);
   if (lane == 31) s_warp[warp] = y;
   __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int t = s_warp[w];
-    if (w < warp) before += t;
-    total += t;
-  }
+  const int w = warp_scan(lane < kThreads / 32 ? s_warp[lane] : 0);
   __syncthreads();
-  return before + y - x;
+  total = __shfl_sync(kAll, w, 31);
+  const int before = __shfl_sync(kAll, w, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0) + y - x;
 }
 
 enum Pass { kInOne, kCount, kWrite };
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   const long long head = state[0], tail = state[1];
   const long long held = blocks_held(head, tail, a.num_blocks);
   // ---- the requests: parents, lengths, last blocks
+#pragma unroll 1
   for (int i = warp; i < nb; i += kThreads / 32) {
     const Request r = look_at(a, b0 + i);
     if (lane < W) {
@@ -205,6 +207,7 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   long long taken = 0, dropped = 0;  // dropped: those of requests before (kWrite)
   if constexpr (P == kInOne) {
     int done = 0;
+#pragma unroll 1
     for (int base = 0; base < nb; base += kThreads) {
       const int i = base + tid;
       int total;
@@ -219,6 +222,7 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   long long before = 0, all_dropped = 0;
   if constexpr (P == kWrite) {
     long long t = 0, d = 0, ta = 0, da = 0;
+#pragma unroll 1
     for (int b = tid; b < a.B; b += kThreads) {
       const long long x = a.counts[2 * b], y = a.counts[2 * b + 1];
       ta += x;
@@ -234,6 +238,7 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
       if (lane == 0) s_sum[warp] = x;
       __syncthreads();
       long long y = 0;
+#pragma unroll 1
       for (int w = 0; w < kThreads / 32; ++w) y += s_sum[w];
       __syncthreads();
       return y;
@@ -244,12 +249,17 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
     all_dropped = sum(da);
   }
   const bool fits = P == kCount || taken <= held;
+  // Places in the ring, less than num_blocks past these (a ring that does not fit is left).
+  const unsigned NB = (unsigned)a.num_blocks;
+  const unsigned head0 = fits && held >= 0 ? (unsigned)((unsigned long long)head % NB) : 0;
+  const unsigned tail0 = fits && held >= 0 ? (unsigned)((unsigned long long)tail % NB) : 0;
   if (P != kCount && !fits && tid == 0 && blockIdx.x == 0)
     flag_status(a.status, PA_DEV_NO_BLOCKS);
   // ---- the columns
   const int items = nb * a.M;  // (one CTA: few; one request: M)
   long long put = dropped;     // blocks given back so far
   int mine = 0;                // (kCount)
+#pragma unroll 1
   for (int base = 0; base < items; base += kThreads) {
     const int i = base + tid, q = i / a.M, col = i - q * a.M;
     Column<WM> c;
@@ -270,19 +280,21 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
     long long at = put + block_scan<kThreads>(__popc(c.drop), s_warp, total);
     put += total;
     if (i >= items) continue;
-#pragma unroll
-    for (int w = 0; w < WM; ++w)
-      if (c.drop >> w & 1) {
-        // (a ring that would hold more than there are: its state was wrong)
-        if (held + at < a.num_blocks)
-          a.ring[(unsigned long long)(tail + at) % (unsigned)a.num_blocks] = c.old[w];
-        else
-          flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
-        ++at;
-      }
     const size_t row0 = (size_t)r.b * W * a.M + col;
+#pragma unroll 1
+    for (uint32_t left = c.drop; left != 0; left &= left - 1, ++at) {
+      // (a ring that would hold more than there are: its state was wrong)
+      if (held + at < NB) {
+        unsigned to = tail0 + (unsigned)at;
+        if (to >= NB) to -= NB;
+        a.ring[to] = a.block_tables[row0 + (size_t)(__ffs(left) - 1) * a.M];
+      } else {
+        flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+      }
+    }
     if (r.bad || !fits) {
       if (a.tables_out != a.block_tables)
+#pragma unroll 1
         for (int w = 0; w < W; ++w)
           a.tables_out[row0 + (size_t)w * a.M] = a.block_tables[row0 + (size_t)w * a.M];
       continue;
@@ -294,23 +306,23 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
       if (w < W && col < s_has[q * W + w])
         now[w] = a.block_tables[row0 + (size_t)s_parent[q * W + w] * a.M];
     }
-    if (r.need != 0) {
-#pragma unroll
-      for (int w = 0; w < WM; ++w)
-        if ((r.need >> w & 1) && col == s_has[q * W + w] - 1) {
-          const int k = r.before + __popc(r.need & ((1u << w) - 1));
-          const int id = a.ring[(unsigned long long)(head + k) % (unsigned)a.num_blocks];
-          const bool ok = id >= 0 && id < a.num_blocks;
-          if (!ok) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
-          now[w] = ok ? id : -1;
-          int64_t* pair = a.pairs + 2 * ((size_t)r.b * W + w);
-          pair[0] = ok ? s_tail[q * W + w] : 0;
-          pair[1] = ok ? id : 0;
-        }
-    }
 #pragma unroll
     for (int w = 0; w < WM; ++w)
       if (w < W) a.tables_out[row0 + (size_t)w * a.M] = now[w];
+#pragma unroll 1
+    for (uint32_t left = r.need; left != 0; left &= left - 1) {
+      const int w = __ffs(left) - 1;
+      if (col != s_has[q * W + w] - 1) continue;
+      unsigned from = head0 + (unsigned)(r.before + __popc(r.need & ((1u << w) - 1)));
+      if (from >= NB) from -= NB;
+      const int id = a.ring[from];
+      const bool ok = id >= 0 && id < a.num_blocks;
+      if (!ok) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+      a.tables_out[row0 + (size_t)w * a.M] = ok ? id : -1;
+      int64_t* pair = a.pairs + 2 * ((size_t)r.b * W + w);
+      pair[0] = ok ? s_tail[q * W + w] : 0;
+      pair[1] = ok ? id : 0;
+    }
   }
   if constexpr (P == kCount) {
     int total;
@@ -325,6 +337,7 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
     }
   } else {
     // ---- the pairs of beams that need no copy, and the lengths
+#pragma unroll 1
     for (int i = tid; i < nb * W; i += kThreads) {
       const int q = i / W, w = i - q * W;
       const size_t o = (size_t)b0 * W + i;
@@ -332,6 +345,7 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
       if (!moved || !(s_bits[q] >> w & 1)) a.pairs[2 * o] = a.pairs[2 * o + 1] = 0;
     }
     // (in place: a parent's length is read by the warp that replaces it)
+#pragma unroll 1
     for (int i = warp; i < nb; i += kThreads / 32) {
       const size_t o = (size_t)(b0 + i) * W + lane;
       const int l = lane < W ? a.context_lens[o] : 0;
@@ -413,6 +427,7 @@ __global__ void __launch_bounds__(kBackThreads)
   __syncthreads();
   const size_t plane = (size_t)a.B * W;
   int32_t* out = a.out + (size_t)b * K * a.S;
+#pragma unroll 1
   for (int i = tid; i < K * (a.S - s_most); i += kBackThreads) {  // behind all of them
     const int k = i / (a.S - s_most);
     out[(size_t)k * a.S + s_most + (i - k * (a.S - s_most))] = a.pad;
@@ -420,6 +435,7 @@ __global__ void __launch_bounds__(kBackThreads)
   for (int hi = s_most; hi > 0; hi -= steps) {  // steps lo .. hi - 1
     const int lo = hi > steps ? hi - steps : 0, n = hi - lo;
     const int np = (n + kPiece - 1) / kPiece;
+#pragma unroll 4
     for (int i = tid; i < n * W; i += kBackThreads) {
       const int s = i / W, w = i - s * W;
       const int p = a.parents[(size_t)(lo + s) * plane + (size_t)b * W + w];
@@ -427,9 +443,11 @@ __global__ void __launch_bounds__(kBackThreads)
     }
     __syncthreads();
     // the beam below each piece, from each of its last step's
+#pragma unroll 1
     for (int i = tid; i < np * W; i += kBackThreads) {
       const int p = i / W;
       int w = i - p * W;
+#pragma unroll 1
       for (int s = min(n, (p + 1) * kPiece) - 1; s >= p * kPiece && w != kOff; --s)
         w = s_parent[s * W + w];
       s_map[i] = (uint8_t)w;
@@ -442,7 +460,9 @@ __global__ void __launch_bounds__(kBackThreads)
       if (end > 0) {
         int p = (end - 1) / kPiece;
         s_at[tid * pieces + p] = (uint8_t)w;
+#pragma unroll 1
         for (int s = end - 1; s >= p * kPiece && w != kOff; --s) w = s_parent[s * W + w];
+#pragma unroll 1
         for (--p; p >= 0; --p) {
           s_at[tid * pieces + p] = (uint8_t)w;
           if (w != kOff) w = s_map[p * W + w];
@@ -452,10 +472,12 @@ __global__ void __launch_bounds__(kBackThreads)
     }
     __syncthreads();
     // all pieces of all hypotheses
+#pragma unroll 1
     for (int i = tid; i < K * np; i += kBackThreads) {
       const int k = i / np, p = i - k * np;
       const int end = min(s_n[k] - lo, n), last = min(n, (p + 1) * kPiece) - 1;
       int w = p * kPiece < end ? s_at[k * pieces + p] : kOff;
+#pragma unroll 1
       for (int s = last; s >= p * kPiece; --s) {
         const bool in = s < end && w != kOff;
         s_beam[(size_t)k * steps + s] = in ? (uint8_t)w : kOff;
@@ -464,6 +486,7 @@ __global__ void __launch_bounds__(kBackThreads)
       }
     }
     __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < K * n; i += kBackThreads) {
       const int k = i / n, s = i - k * n, w = s_beam[(size_t)k * steps + s];
       out[(size_t)k * a.S + lo + s] =

@@ -17,15 +17,11 @@ struct BeamSelectArgs {
   int32_t* parents;
   float* new_scores;
   float* ended;  // [B, W] by beam
-  // Per row and split: its W best (keys of 64 bits, in order), its maximum and sum.
-  unsigned long long* ws_keys;  // [B * W][splits][W]
-  float* ws_sum;                // [B * W][splits]
-  float* ws_max;                // [B * W][splits]
   int32_t* status;
   int B, W, V, eos, pad, dtype;
-  int splits;
+  int ranks;  // CTAs of a request
 };
-int beam_select_splits(int B, int W, int V);
+int beam_select_ranks(int B, int W, int V);
 cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t stream);
 
 // Block tables that follow the beams (beam_tables.cu).

@@ -31,6 +31,20 @@ cudaError_t ensure_dynamic_smem(int bytes) {
   return e;
 }
 
+// Lets Kern be launched in clusters of more than 8 CTAs on the current device, likewise.
+template <auto Kern>
+cudaError_t ensure_large_cluster() {
+  static std::atomic<unsigned long long> done{0};  // bit d: set on device d
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && bit != 0) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // Multiprocessor count of the current device (cached per device; 0 when the
 // query fails).
 int sm_count();
