@@ -139,38 +139,56 @@ struct Raw {
   }
 };
 
-// The W best of a warp's n <= kList keys, in order, to the list's front.  Keys differ, so
-// that each one's place is the number of those above it.
-__device__ __noinline__ int sort_out(Key* list, int n, int W) {
-  constexpr int kMine = kList / 32;
+// The W best of a warp's n <= kList keys, in order, to the list's front (by way of `room`).
+// Keys differ, so that each one's place is the number of those above it.
+__device__ __forceinline__ int sort_out(Key* list, Key* room, int n, int W) {
   const int lane = threadIdx.x & 31;
   __syncwarp();
-  Key k[kMine];
-  int above[kMine];
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    k[j] = lane + 32 * j < n ? list[lane + 32 * j] : 0;
-    above[j] = 0;
-  }
 #pragma unroll 1
-  for (int q = 0; q < n; ++q) {
-    const Key o = list[q];
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) above[j] += o > k[j];
+  for (int i = lane; i < (n + 31) / 32 * 32; i += 32) {
+    const Key k = i < n ? list[i] : ~0ull;
+    int above = 0;
+#pragma unroll 4
+    for (int q = 0; q < n; ++q) above += list[q] > k;
+    if (i < n && above < W) room[above] = k;
   }
   __syncwarp();
-#pragma unroll
-  for (int j = 0; j < kMine; ++j)
-    if (k[j] != 0 && above[j] < W) list[above[j]] = k[j];
+  n = min(n, W);
+  if (lane < n) list[lane] = room[lane];
   __syncwarp();
-  return min(n, W);
+  return n;
+}
+
+// x[i] for an i known at run time only, without a trip through memory.
+__device__ __forceinline__ float pick(const float (&x)[kEach], int i) {
+  float y[kEach / 2];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = i & 8 ? x[j + 8] : x[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = i & 4 ? y[j + 4] : y[j];
+  y[0] = i & 2 ? y[2] : y[0];
+  y[1] = i & 2 ? y[3] : y[1];
+  return i & 1 ? y[1] : y[0];
+}
+
+// The W-th largest of the lanes' x: a bitonic sort over the lanes, largest first.
+__device__ __forceinline__ uint32_t nth_largest(uint32_t x, int W) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const uint32_t y = __shfl_xor_sync(kAll, x, j);
+      x = ((lane & k) == 0) == ((lane & j) == 0) ? max(x, y) : min(x, y);
+    }
+  return __shfl_sync(kAll, x, W - 1);
 }
 
 // A warp's piece [begin, end) of a row: its W best to the list (0 behind the last), its
 // maximum and sum returned.  shared: a threshold that W values of the row reach.
 template <typename T, bool VEC>
 __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos, int W,
-                                       Key* list, uint32_t* shared) {
+                                       Key* list, Key* room, uint32_t* shared) {
   const int lane = threadIdx.x & 31;
   float m = -INFINITY, l = 0.f;
   float t = -FLT_MAX;  // values from it on are candidates (-inf and NaN never)
@@ -179,9 +197,10 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
   raw.load(row, begin, end);
 #pragma unroll 1
   for (int base = begin; base < end; base += kChunk) {
+    const bool last = base + kChunk >= end;
     float x[kEach];
     raw.get(row, base, end, x);
-    if (base + kChunk < end) raw.load(row, base + kChunk, end);
+    if (!last) raw.load(row, base + kChunk, end);
     float mt = fmaxf(x[0], x[1]);
 #pragma unroll
     for (int i = 2; i < kEach; i += 2) mt = max3f(mt, x[i], x[i + 1]);
@@ -207,51 +226,41 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
       for (int i = 1; i < kEach; ++i) mt = fmaxf(mt, x[i]);
     }
     if (base == begin) {
-      // The W-th largest of the lanes' maxima, which W values reach.
-      const uint32_t mine = ordered(mt);
-      int above = 0;
-#pragma unroll 4
-      for (int j = 0; j < 32; ++j) {
-        const uint32_t o = __shfl_sync(kAll, mine, j);
-        above += o > mine || (o == mine && j < lane);
-      }
-      const unsigned at = __ballot_sync(kAll, above == W - 1);
-      t = fmaxf(t, __shfl_sync(kAll, mt, __ffs(at) - 1));
+      // The W-th largest of the lanes' maxima is reached by W values (an order of NaN's
+      // does not matter: their row has no candidates).
+      const uint32_t o = nth_largest(ordered(mt), W);
+      t = fmaxf(t, unordered(o));
+      if (lane == 0 && o > ordered(-FLT_MAX)) atomicMax(shared, o);
     }
     t = fmaxf(t, unordered(*(volatile uint32_t*)shared));
-    const bool last = base + kChunk >= end;
-    bool full = false;
-    if (__any_sync(kAll, mt >= t)) {
-      uint32_t hits = 0;
+    uint32_t hits = 0;  // of the lane's values, those that reach t
+    if (mt >= t) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) hits |= x[i] >= t ? 1u << i : 0u;
-      // All of them at once, or, where the list has no room, two of a lane at a time.
-      full = n + __reduce_add_sync(kAll, (unsigned)__popc(hits)) > kList;
-      const int width = full ? 2 : kEach;
-#pragma unroll 1
-      for (int i0 = 0; i0 < kEach; i0 += width) {
-        if (full) n = sort_out(list, n, W);
-        const uint32_t part = hits & (((1u << width) - 1) << i0);
-        int at = __popc(part);  // inclusive sum over the lanes
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int y = __shfl_up_sync(kAll, at, d);
-          if (lane >= d) at += y;
-        }
-        Key* to = list + n + at - __popc(part);
-        n += __shfl_sync(kAll, at, 31);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-          if (part >> i & 1) *to++ = key_of(x[i], Raw<T, VEC>::index(base, i));
-      }
     }
-    if (full || last || n > W + 32) {
-      n = sort_out(list, n, W);
-      if (n == W && !last) {  // an equal value of a later chunk comes too late
-        const uint32_t lowest = (uint32_t)(list[W - 1] >> 32);
-        t = fmaxf(t, unordered(lowest + 1));
-        if (lane == 0) atomicMax(shared, lowest);
+    bool full = false;
+#pragma unroll 1
+    for (;;) {  // one of a lane at a time
+      const unsigned mask = __ballot_sync(kAll, hits != 0);
+      if (mask != 0 ? n + __popc(mask) > kList : full || last || n > W + 32) {
+        n = sort_out(list, room, n, W);
+        if (n == W) {
+          // An equal value of a later chunk comes too late (of this one it may not: its
+          // values come in no order of their indices).
+          const uint32_t lowest = (uint32_t)(list[W - 1] >> 32);
+          if (mask == 0) t = fmaxf(t, unordered(lowest + 1));
+          if (lane == 0) atomicMax(shared, lowest);
+        }
+        full = true;
       }
+      if (mask == 0) break;
+      if (hits != 0) {
+        const int i = __ffs(hits) - 1;
+        list[n + __popc(mask & ((1u << lane) - 1))] =
+            key_of(pick(x, i), Raw<T, VEC>::index(base, i));
+        hits &= hits - 1;
+      }
+      n += __popc(mask);
     }
   }
   if (lane >= n && lane < W) list[lane] = 0;
@@ -361,6 +370,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
   extern __shared__ Key s_dyn[];
   __shared__ Key s_list[kWarps][kList];
+  __shared__ Key s_room[kWarps][kMaxBeams];
   __shared__ float2 s_ml[kWarps];
   __shared__ uint32_t s_threshold[kMaxBeams];
   __shared__ double s_lse[32];
@@ -383,13 +393,15 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
   const int pieces = min(kMaxPieces, ranks * kWarps / max(rows, 1));
   const int length = ((a.V + pieces - 1) / pieces + 15) / 16 * 16;
   __syncthreads();
-  const int task = warp * ranks + rank;  // (few pieces: spread over the CTAs)
-  if (task < rows * pieces) {
+  // A row's pieces go to neighbouring warps, which share a threshold.
+  const int per = (rows * pieces + ranks - 1) / ranks, task = rank * per + warp;
+  if (warp < per && task < rows * pieces) {
     const int r = task / pieces, w = live_beam(alive, r);
     const int begin = (int)min((long long)(task - r * pieces) * length, (long long)a.V);
     const int end = (int)min((long long)begin + length, (long long)a.V);
     const T* x = static_cast<const T*>(a.logits) + (long long)(b * W + w) * a.row_stride;
-    const float2 ml = scan<T, VEC>(x, begin, end, a.eos, W, s_list[warp], &s_threshold[w]);
+    const float2 ml = scan<T, VEC>(x, begin, end, a.eos, W, s_list[warp], s_room[warp],
+                                    &s_threshold[w]);
     if (lane == 0) s_ml[warp] = ml;
   }
   if (ranks > 1)
@@ -407,11 +419,12 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
     auto at_rank = [&](auto* p, int r) { return ranks > 1 ? cluster.map_shared_rank(p, r) : p; };
 #pragma unroll 1
     for (int i = tid; i < lists * W; i += kThreads) {
-      const int q = i / W;
-      keys[i] = *at_rank(&s_list[q / ranks][i - q * W], q % ranks);
+      const int q = i / W, from = q / per;
+      keys[i] = *at_rank(&s_list[q - from * per][i - q * W], from);
     }
 #pragma unroll 1
-    for (int q = tid; q < lists; q += kThreads) ml[q] = *at_rank(&s_ml[q / ranks], q % ranks);
+    for (int q = tid; q < lists; q += kThreads)
+      ml[q] = *at_rank(&s_ml[q % per], q / per);
     __syncthreads();
     // A warp to a beam: rounds of the largest head of its lists, two to a lane.
 #pragma unroll 1
