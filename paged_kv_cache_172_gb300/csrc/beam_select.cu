@@ -44,6 +44,7 @@ constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kEach = 16;           // values of a lane and chunk
 constexpr int kChunk = 32 * kEach;  // values of a warp's chunk
 constexpr int kList = 128;          // keys of a warp's list
+constexpr int kSlack = 8;           // keys past the W best before they are sorted out
 constexpr int kMaxPieces = 64;      // of a row: two lists to a lane of the merge
 constexpr int kMaxCluster = 16;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -75,6 +76,15 @@ __device__ __forceinline__ Key warp_max(Key k) {
   const uint32_t hi = (uint32_t)(k >> 32), top = __reduce_max_sync(kAll, hi);
   const uint32_t lo = __reduce_max_sync(kAll, hi == top ? (uint32_t)k : 0u);
   return ((Key)top << 32) | lo;
+}
+
+__device__ __forceinline__ void mul_f32x2(float& d0, float& d1, float a0, float a1, float b0,
+                                          float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
 // The warp's sums l relative to its maxima m, relative to M.  (A lane without values has
@@ -214,7 +224,8 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
     for (int i = 0; i < kEach; i += 2) {
       float a, b;
       add_f32x2(a, b, x[i], x[i + 1], ref, ref);
-      add_f32x2(s0, s1, s0, s1, ex2_approx(a * kLog2e), ex2_approx(b * kLog2e));
+      mul_f32x2(a, b, a, b, kLog2e, kLog2e);
+      add_f32x2(s0, s1, s0, s1, ex2_approx(a), ex2_approx(b));
     }
     l += s0 + s1;
     if (eos >= base && eos - base < kChunk) {  // the end is no candidate
@@ -242,7 +253,7 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
 #pragma unroll 1
     for (;;) {  // one of a lane at a time
       const unsigned mask = __ballot_sync(kAll, hits != 0);
-      if (mask != 0 ? n + __popc(mask) > kList : full || last || n > W + 32) {
+      if (mask != 0 ? n + __popc(mask) > kList : full || last || n >= W + kSlack) {
         n = sort_out(list, room, n, W);
         if (n == W) {
           // An equal value of a later chunk comes too late (of this one it may not: its
@@ -472,7 +483,7 @@ template <typename T, bool VEC>
 cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
   constexpr auto kern = beam_select_kernel<T, VEC>;
   const int smem = dynamic_bytes(a.W, a.ranks);
-  if (smem > 30 * 1024) {
+  if (smem > 24 * 1024) {  // (with the lists more than 48 KB)
     const cudaError_t e = ensure_dynamic_smem<kern>(dynamic_bytes(kMaxBeams, kMaxCluster));
     if (e != cudaSuccess) return e;
   }
