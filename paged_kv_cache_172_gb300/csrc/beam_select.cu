@@ -7,26 +7,26 @@
 // Only a row's own W best can be among them, and they are found while the row's sum is:
 // one pass over the logits, one launch.  A request is a cluster of CTAs whose warps share
 // out its live beams' rows, a piece of a row to each; no warp waits for another until all
-// pieces are done.  A warp takes its piece in chunks of 512 values that its lanes hold in
-// registers, with the next chunk's loads in flight, and keeps a running maximum and sum in
-// every lane.  Of the first chunk the W-th largest of the lanes' maxima is a threshold that
-// W values reach and few others.  Values that reach it go to a list in shared memory as
-// (ordered value, ~index) keys; when the list is full, its W best are kept by counting for
-// each key how many are above it, and the W-th becomes the threshold, of the other warps
-// of the CTA on that row too.  The cluster's first CTA then merges the pieces' lists by
-// beam and the beams' lists, in order, by as many rounds of a maximum over the lanes as
-// there are beams.
+// pieces are done.  A warp's piece comes through a ring of its own in shared memory
+// (asynchronous copies of 16 bytes a lane), so that its loop takes few registers and
+// little code; every lane keeps a running maximum and sum.  Of the first pieces in the
+// ring the W-th largest of the lanes' maxima is a threshold that W values reach and few
+// others.  Values that reach it go to a list as (ordered value, ~index) keys; when that is
+// full, its W best are kept by counting for each key how many are above it, and the W-th
+// becomes the threshold, of the other warps of the CTA on that row too.  The cluster's
+// first CTA then merges the pieces' lists by beam and the beams' lists, in order, by as
+// many rounds of a maximum over the lanes as there are beams.
 //
 // Rounding: sums in fp32, candidates in 64 bits (two beams' can be nearer than fp32 tells
 // apart), the scores once to fp32.  A sum goes by the values' index and not by the row's
 // alignment, so equal rows have equal sums.
 //
-// Bound: HBM, or the trip from the logits to the lists to the merge, for few rows, where
-// the code itself comes from memory: it is kept short.
-#include <cooperative_groups.h>
+// Bound: HBM, or, for few rows, the trip from the logits to the lists to the merge, on
+// which the code itself comes from memory: it is kept short.
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
+#include <string.h>
 
 #include <type_traits>
 
@@ -37,16 +37,16 @@ namespace pk {
 
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kEach = 16;           // values of a lane and chunk
 constexpr int kChunk = 32 * kEach;  // values of a warp's chunk
+constexpr int kRing = 4160;         // bytes of a warp's ring: two or four chunks and 16 each
 constexpr int kList = 128;          // keys of a warp's list
 constexpr int kSlack = 8;           // keys past the W best before they are sorted out
 constexpr int kMaxPieces = 64;      // of a row: two lists to a lane of the merge
 constexpr int kMaxCluster = 16;
+constexpr int kShortest = 512;      // values that are a warp's piece of their own
 constexpr float kLog2e = 1.4426950408889634f;
 using Key = unsigned long long;
 
@@ -106,45 +106,68 @@ __device__ __forceinline__ float to_float(T x) {
     return __bfloat162float(x);
 }
 
-// A lane's values of a chunk as they come from memory.  VEC: 16-byte pieces, every row
-// being aligned; otherwise one value after the other, neighbours in neighbouring lanes.
-template <typename T, bool VEC>
-struct Raw {
-  static constexpr int N = VEC ? 16 / (int)sizeof(T) : 1;  // values of a piece
-  static constexpr int P = kEach / N;
-  using Piece = typename std::conditional<
-      VEC, uint4, typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type>::type;
-  Piece p[P];
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;"); }
+// Waits until at most `left` of the lane's groups are still under way.
+template <int left>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(left) : "memory");
+}
 
-  static __device__ __forceinline__ int index(int base, int i) {  // of value i of the lane
-    return base + (i / N * 32 + (int)(threadIdx.x & 31)) * N + i % N;
+// A piece of a row in a warp's ring, chunk by chunk.  The copies are of whole 16 bytes, from
+// `lead` bytes before the piece on where rows are not aligned (the 16 bytes that hold the
+// first value; a chunk then ends in 16 bytes more).  A lane's values: VEC, every row being
+// aligned, 16 bytes each time; otherwise one at a time, neighbours in neighbouring lanes.
+template <typename T, bool VEC>
+struct Piece {
+  static constexpr int N = 16 / (int)sizeof(T);  // values of 16 bytes
+  static constexpr int kCopies = kEach / N, kBytes = kChunk * (int)sizeof(T);
+  static constexpr int kSlot = kBytes + 16, kSlots = kRing / kSlot;
+  const T* from;    // the first value's 16 bytes
+  int lead, bytes;  // before the first value, in all
+  uint8_t* ring;
+
+  static __device__ __forceinline__ int index(int base, int j) {  // of value j of the lane
+    const int lane = threadIdx.x & 31;
+    return VEC ? base + (j / N * 32 + lane) * N + j % N : base + j * 32 + lane;
   }
-  __device__ __forceinline__ void load(const T* row, int base, int end) {
+  // Requests chunk i, if there is one; a group in any case.
+  __device__ __forceinline__ void request(int i) const {
+    const int lane = threadIdx.x & 31, at = i * kBytes + lane * 16;
+    const uint32_t to = smem_u32(ring) + i % kSlots * kSlot + lane * 16;
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(from) + at;
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      const int i = index(base, k * N);
-      if (VEC ? i + N <= end : i < end)
-        p[k] = __ldcs(reinterpret_cast<const Piece*>(row + i));
-    }
+    for (int q = 0; q < kCopies; ++q)
+      if (at + q * 512 < bytes) copy_async(to + q * 512, src + q * 512, min(bytes - at - q * 512, 16));
+    if (!VEC && lane == 0 && at + kBytes < bytes)
+      copy_async(to + kBytes, src + kBytes, min(bytes - at - kBytes, 16));
+    copy_commit();
   }
-  // (values past the end read as -inf)
-  __device__ __forceinline__ void get(const T* row, int base, int end, float (&x)[kEach]) const {
+  // Values from index `end` on read as -inf.
+  __device__ __forceinline__ void get(int i, int base, int end, float (&x)[kEach]) const {
+    const int lane = threadIdx.x & 31;
+    const uint8_t* slot = ring + i % kSlots * kSlot;
+    if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      T v[N];
-      *reinterpret_cast<Piece*>(v) = p[k];
+      for (int q = 0; q < kCopies; ++q) {
+        T v[N];
+        *reinterpret_cast<uint4*>(v) =
+            *reinterpret_cast<const uint4*>(slot + q * 512 + lane * 16);
 #pragma unroll
-      for (int j = 0; j < N; ++j) x[k * N + j] = to_float<T>(v[j]);
-    }
-    if (base + kChunk > end) {  // a piece's last chunk
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int at = index(base, i);
-        if (at >= end)
-          x[i] = -INFINITY;
-        else if (VEC && at - i % N + N > end)
-          x[i] = to_float<T>(row[at]);
+        for (int j = 0; j < N; ++j) x[q * N + j] = to_float<T>(v[j]);
       }
+    } else {
+      const T* v = reinterpret_cast<const T*>(slot + lead) + lane;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) x[j] = to_float<T>(v[j * 32]);
+    }
+    if (base + kChunk > end) {
+#pragma unroll
+      for (int j = 0; j < kEach; ++j)
+        if (index(base, j) >= end) x[j] = -INFINITY;
     }
   }
 };
@@ -181,39 +204,61 @@ __device__ __forceinline__ float pick(const float (&x)[kEach], int i) {
   return i & 1 ? y[1] : y[0];
 }
 
-// The W-th largest of the lanes' x: a bitonic sort over the lanes, largest first.
-__device__ __forceinline__ uint32_t nth_largest(uint32_t x, int W) {
+// A bitonic sort over the lanes, largest first.
+__device__ __forceinline__ uint32_t sort_lanes(uint32_t x) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
+#pragma unroll 1
   for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
+#pragma unroll 1
     for (int j = k >> 1; j > 0; j >>= 1) {
       const uint32_t y = __shfl_xor_sync(kAll, x, j);
       x = ((lane & k) == 0) == ((lane & j) == 0) ? max(x, y) : min(x, y);
     }
-  return __shfl_sync(kAll, x, W - 1);
+  return x;
 }
 
+__device__ __forceinline__ float largest(const float (&x)[kEach]) {
+  float m = fmaxf(x[0], x[1]);
+#pragma unroll
+  for (int j = 2; j < kEach; j += 2) m = max3f(m, x[j], x[j + 1]);
+  return m;
+}
+
+// What the warps of a CTA on one row know of it, as ordered values; 0: nothing yet.
+struct Known {
+  uint32_t* reached;  // W values of the row reach it
+  uint32_t* kth;      // by warp, from the row's first: k of the warp's values reach it
+  int warps, k;       // warps * k >= W: so W values reach the least of them
+};
+
 // A warp's piece [begin, end) of a row: its W best to the list (0 behind the last), its
-// maximum and sum returned.  shared: a threshold that W values of the row reach.
+// maximum and sum returned.  me: the warp among those of its row.
 template <typename T, bool VEC>
 __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos, int W,
-                                       Key* list, Key* room, uint32_t* shared) {
+                                       uint8_t* ring, Key* list, Key* room, Known known, int me) {
+  using P = Piece<T, VEC>;
   const int lane = threadIdx.x & 31;
+  P p;
+  p.ring = ring;
+  p.lead = VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(row + begin) & 15);
+  p.from = row + begin - p.lead / (int)sizeof(T);
+  p.bytes = begin < end ? p.lead + (end - begin) * (int)sizeof(T) : 0;
+#pragma unroll 1
+  for (int i = 0; i < P::kSlots; ++i) p.request(i);
   float m = -INFINITY, l = 0.f;
   float t = -FLT_MAX;  // values from it on are candidates (-inf and NaN never)
+  constexpr uint32_t kLeast = 0x00800000u;  // ordered(-FLT_MAX)
   int n = 0;
-  Raw<T, VEC> raw;
-  raw.load(row, begin, end);
 #pragma unroll 1
-  for (int base = begin; base < end; base += kChunk) {
+  for (int i = 0, base = begin; base < end; ++i, base += kChunk) {
     const bool last = base + kChunk >= end;
+    copy_wait<P::kSlots - 1>();
+    __syncwarp();
     float x[kEach];
-    raw.get(row, base, end, x);
-    if (!last) raw.load(row, base + kChunk, end);
-    float mt = fmaxf(x[0], x[1]);
-#pragma unroll
-    for (int i = 2; i < kEach; i += 2) mt = max3f(mt, x[i], x[i + 1]);
+    p.get(i, base, end, x);
+    __syncwarp();
+    p.request(i + P::kSlots);  // (into the room of this chunk, which all lanes have read)
+    float mt = largest(x);
     if (mt > m) {
       l *= ex2_approx((m - mt) * kLog2e);  // (m = -inf: l is 0)
       m = mt;
@@ -221,59 +266,61 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
     const float ref = m == -INFINITY ? 0.f : -m;
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < kEach; i += 2) {
+    for (int j = 0; j < kEach; j += 2) {
       float a, b;
-      add_f32x2(a, b, x[i], x[i + 1], ref, ref);
+      add_f32x2(a, b, x[j], x[j + 1], ref, ref);
       mul_f32x2(a, b, a, b, kLog2e, kLog2e);
       add_f32x2(s0, s1, s0, s1, ex2_approx(a), ex2_approx(b));
     }
     l += s0 + s1;
-    if (eos >= base && eos - base < kChunk) {  // the end is no candidate
+    if ((unsigned)(eos - base) < (unsigned)kChunk) {  // the end is no candidate
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (Raw<T, VEC>::index(base, i) == eos) x[i] = -INFINITY;
-      mt = x[0];
-#pragma unroll
-      for (int i = 1; i < kEach; ++i) mt = fmaxf(mt, x[i]);
+      for (int j = 0; j < kEach; ++j)
+        if (P::index(base, j) == eos) x[j] = -INFINITY;
+      mt = largest(x);
     }
-    if (base == begin) {
-      // The W-th largest of the lanes' maxima is reached by W values (an order of NaN's
-      // does not matter: their row has no candidates).
-      const uint32_t o = nth_largest(ordered(mt), W);
-      t = fmaxf(t, unordered(o));
-      if (lane == 0 && o > ordered(-FLT_MAX)) atomicMax(shared, o);
+    if (i == 0) {
+      // The lanes' maxima: as many values reach the j-th largest as there are before it.
+      const uint32_t o = sort_lanes(ordered(mt));
+      if (lane == W - 1) atomicMax(known.reached, o);
+      if (lane == known.k - 1) known.kth[me] = o;
+      __syncwarp();
     }
-    t = fmaxf(t, unordered(*(volatile uint32_t*)shared));
+    const uint32_t all = lane < known.warps ? *(volatile uint32_t*)(known.kth + lane) : ~0u;
+    const uint32_t reached =
+        max(__reduce_min_sync(kAll, all), *(volatile uint32_t*)known.reached);
+    t = fmaxf(t, unordered(max(reached, kLeast)));
     uint32_t hits = 0;  // of the lane's values, those that reach t
     if (mt >= t) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) hits |= x[i] >= t ? 1u << i : 0u;
+      for (int j = 0; j < kEach; ++j) hits |= x[j] >= t ? 1u << j : 0u;
     }
-    bool full = false;
+    bool sorted = false;
 #pragma unroll 1
     for (;;) {  // one of a lane at a time
       const unsigned mask = __ballot_sync(kAll, hits != 0);
-      if (mask != 0 ? n + __popc(mask) > kList : full || last || n >= W + kSlack) {
+      if (mask != 0 ? n + __popc(mask) > kList : sorted || last || n >= W + kSlack) {
         n = sort_out(list, room, n, W);
+        if (n >= known.k && lane == 0) known.kth[me] = (uint32_t)(list[known.k - 1] >> 32);
         if (n == W) {
-          // An equal value of a later chunk comes too late (of this one it may not: its
-          // values come in no order of their indices).
+          // An equal value of a later chunk comes too late (of this one it may not: a
+          // lane's values come in no order of their indices).
           const uint32_t lowest = (uint32_t)(list[W - 1] >> 32);
           if (mask == 0) t = fmaxf(t, unordered(lowest + 1));
-          if (lane == 0) atomicMax(shared, lowest);
+          if (lane == 0) atomicMax(known.reached, lowest);
         }
-        full = true;
+        sorted = true;
       }
       if (mask == 0) break;
       if (hits != 0) {
-        const int i = __ffs(hits) - 1;
-        list[n + __popc(mask & ((1u << lane) - 1))] =
-            key_of(pick(x, i), Raw<T, VEC>::index(base, i));
+        const int j = __ffs(hits) - 1;
+        list[n + __popc(mask & ((1u << lane) - 1))] = key_of(pick(x, j), P::index(base, j));
         hits &= hits - 1;
       }
       n += __popc(mask);
     }
   }
+  copy_wait<0>();
   if (lane >= n && lane < W) list[lane] = 0;
   const float M = unordered(__reduce_max_sync(kAll, ordered(m)));
   return make_float2(M, add_up(l, m, M));
@@ -285,14 +332,15 @@ struct Rows {
   float2* ml;  // [W]
 };
 
-// log x of a sum, to 2^-25: e log 2 + log f, x = 2^e f with f in [1 / sqrt 2, sqrt 2), so
-// that fp32's half steps are those of a number below 0.35.
+// log x of a sum, x >= 1, to 2^-25: e log 2 + log f, x = 2^e f with f in [1 / sqrt 2,
+// sqrt 2), so that fp32's half steps are those of a number below 0.35.
 __device__ __forceinline__ double log_of(float x) {
-  int e;
-  float f = frexpf(x, &e);
-  if (f < 0.70710678f) {
-    f *= 2.f;
-    --e;
+  const uint32_t u = __float_as_uint(x);
+  int e = (int)(u >> 23) - 127;
+  float f = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+  if (f >= 1.41421356f) {
+    f *= 0.5f;
+    ++e;
   }
   return e * 0.69314718055994531 + (double)logf(f);
 }
@@ -369,6 +417,24 @@ __device__ __forceinline__ void choose(const BeamSelectArgs& a, int b, uint32_t 
   a.ended[o] = ended;
 }
 
+// All threads of the cluster meet; what they wrote to shared memory is seen behind it.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+// Shared memory of CTA `rank` of the cluster.
+template <typename X>
+__device__ __forceinline__ X at_rank(const X* p, int rank) {
+  static_assert(sizeof(X) == 8, "one load");
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  unsigned long long x;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(at) : "memory");
+  X y;
+  memcpy(&y, &x, 8);
+  return y;
+}
+
 // The beam of the i-th live row.
 __device__ __forceinline__ int live_beam(uint32_t alive, int i) {
 #pragma unroll 1
@@ -379,16 +445,16 @@ __device__ __forceinline__ int live_beam(uint32_t alive, int i) {
 // A cluster to a request.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
-  extern __shared__ Key s_dyn[];
+  extern __shared__ __align__(16) uint8_t s_dyn[];  // the warps' rings, then what is merged
   __shared__ Key s_list[kWarps][kList];
   __shared__ Key s_room[kWarps][kMaxBeams];
   __shared__ float2 s_ml[kWarps];
-  __shared__ uint32_t s_threshold[kMaxBeams];
+  __shared__ uint32_t s_reached[kMaxBeams], s_kth[kWarps];
   __shared__ double s_lse[32];
-  const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = a.ranks, b = blockIdx.x / ranks, rank = blockIdx.x - b * ranks, W = a.W;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < kMaxBeams) s_threshold[tid] = 0;  // below any value
+  if (tid < kMaxBeams) s_reached[tid] = 0;
+  if (tid < kWarps) s_kth[tid] = 0;
   pdl_wait();
   pdl_launch_dependents();
   // A beam whose score is not finite is not there.
@@ -411,31 +477,34 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
     const int begin = (int)min((long long)(task - r * pieces) * length, (long long)a.V);
     const int end = (int)min((long long)begin + length, (long long)a.V);
     const T* x = static_cast<const T*>(a.logits) + (long long)(b * W + w) * a.row_stride;
-    const float2 ml = scan<T, VEC>(x, begin, end, a.eos, W, s_list[warp], s_room[warp],
-                                    &s_threshold[w]);
+    // The row's warps of this CTA (its pieces may begin or go on in a neighbour).
+    const int first = max(r * pieces - rank * per, 0);
+    const int warps = min(min((r + 1) * pieces, rows * pieces) - rank * per, per) - first;
+    const Known known = {&s_reached[w], &s_kth[first], warps, (W + warps - 1) / warps};
+    const float2 ml = scan<T, VEC>(x, begin, end, a.eos, W, s_dyn + warp * kRing,
+                                    s_list[warp], s_room[warp], known, warp - first);
     if (lane == 0) s_ml[warp] = ml;
   }
   if (ranks > 1)
-    cluster.sync();
+    cluster_meet();
   else
     __syncthreads();
   if (rank == 0) {
     // All lists, [row][piece][W], and their maxima and sums.
-    Key* keys = s_dyn;
+    Key* keys = reinterpret_cast<Key*>(s_dyn);
     const int lists = rows * pieces;
     float2* ml = reinterpret_cast<float2*>(keys + (size_t)ranks * kWarps * W);
     Rows r = {reinterpret_cast<Key*>(ml + ranks * kWarps), nullptr};
     r.ml = reinterpret_cast<float2*>(r.top + W * W);
     Key* cand = reinterpret_cast<Key*>(r.ml + kMaxBeams);
-    auto at_rank = [&](auto* p, int r) { return ranks > 1 ? cluster.map_shared_rank(p, r) : p; };
 #pragma unroll 1
     for (int i = tid; i < lists * W; i += kThreads) {
       const int q = i / W, from = q / per;
-      keys[i] = *at_rank(&s_list[q - from * per][i - q * W], from);
+      keys[i] = at_rank(&s_list[q - from * per][i - q * W], from);
     }
 #pragma unroll 1
     for (int q = tid; q < lists; q += kThreads)
-      ml[q] = *at_rank(&s_ml[q % per], q / per);
+      ml[q] = at_rank(&s_ml[q % per], q / per);
     __syncthreads();
     // A warp to a beam: rounds of the largest head of its lists, two to a lane.
 #pragma unroll 1
@@ -472,23 +541,22 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
     __syncthreads();
     choose(a, b, alive, r, cand, s_lse, end_x);
   }
-  if (ranks > 1) cluster.sync();  // nobody leaves while its lists are read
+  if (ranks > 1) cluster_meet();  // nobody leaves while its lists are read
 }
 
 int dynamic_bytes(int W, int ranks) {
-  return ranks * kWarps * (W + 1) * 8 + (2 * W * W + kMaxBeams) * 8;
+  const int merge = ranks * kWarps * (W + 1) * 8 + (2 * W * W + kMaxBeams) * 8;
+  return merge > kWarps * kRing ? merge : kWarps * kRing;
 }
 
 template <typename T, bool VEC>
 cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
   constexpr auto kern = beam_select_kernel<T, VEC>;
   const int smem = dynamic_bytes(a.W, a.ranks);
-  if (smem > 24 * 1024) {  // (with the lists more than 48 KB)
-    const cudaError_t e = ensure_dynamic_smem<kern>(dynamic_bytes(kMaxBeams, kMaxCluster));
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = ensure_dynamic_smem<kern>(dynamic_bytes(kMaxBeams, kMaxCluster));
+  if (e != cudaSuccess) return e;
   if (a.ranks > 8) {
-    const cudaError_t e = ensure_large_cluster<kern>();
+    e = ensure_large_cluster<kern>();
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -519,7 +587,7 @@ cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
 // its rows for their warps.
 int beam_select_ranks(int B, int W, int V) {
   const int nsm = sm_count() > 0 ? sm_count() : 152;
-  const long long warps = (long long)W * ((V - 1) / kChunk + 1);
+  const long long warps = (long long)W * ((V - 1) / kShortest + 1);
   int c = W > kWarps ? 2 : 1;  // (a warp to a row at least)
   while (c < kMaxCluster && 2LL * c * B <= 2 * nsm && c * kWarps < warps) c *= 2;
   return c;
