@@ -697,7 +697,7 @@ pa_status pa_decode_grouped(const void *q, const void *k_cache, const void *v_ca
  * beam with NaN or +inf among its logits gives no candidate, flagged PA_DEV_BAD_LOGITS.
  *
  * logits [B * W] rows of V in dtype (PA_F32 too), row_stride >= V elements apart
- * scores [B, W] float32; V below 2^31 - 32768; eos_token below V
+ * scores [B, W] float32; V at most 2^28; eos_token below V
  * workspace: at least pa_beam_select_workspace_size(B, W, V) bytes, 16-byte aligned,
  * else PA_ERR_WORKSPACE; the size depends on the SM count of the current device.
  * W above 32 returns PA_ERR_UNSUPPORTED.

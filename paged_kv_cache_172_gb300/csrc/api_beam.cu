@@ -13,6 +13,7 @@ pa_status launched(cudaError_t e) {
 
 constexpr int kMaxCount = INT32_MAX - 32768;
 constexpr int kMaxRows = 1 << 20;  // beams of a call
+constexpr int kMaxVocabulary = 1 << 28;  // (a row's bytes in 31 bits)
 
 bool beams_ok(int B, int W) { return B >= 0 && W > 0 && (long long)B * W <= kMaxRows; }
 
@@ -25,7 +26,7 @@ bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p
 extern "C" {
 
 size_t pa_beam_select_workspace_size(int B, int W, int V) {
-  if (B <= 0 || !beams_ok(B, W) || W > pk::kMaxBeams || V <= 0 || V > kMaxCount) return 0;
+  if (B <= 0 || !beams_ok(B, W) || W > pk::kMaxBeams || V <= 0 || V > kMaxVocabulary) return 0;
   return 0;
 }
 
@@ -34,7 +35,7 @@ pa_status pa_beam_select(const void* logits, pa_dtype dtype, int64_t row_stride,
                          int32_t* tokens, int32_t* parents, float* new_scores,
                          float* ended_scores, void* workspace, size_t workspace_bytes,
                          int32_t* status, pa_stream_t stream) {
-  if (!beams_ok(B, W) || V <= 0 || V > kMaxCount || eos_token < -1 || eos_token >= V ||
+  if (!beams_ok(B, W) || V <= 0 || V > kMaxVocabulary || eos_token < -1 || eos_token >= V ||
       row_stride < V || row_stride >= (1LL << 40))
     return PA_ERR_INVALID;
   if (dtype != PA_F16 && dtype != PA_BF16 && dtype != PA_F32) return PA_ERR_INVALID;

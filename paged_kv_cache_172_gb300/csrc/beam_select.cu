@@ -43,7 +43,7 @@ constexpr int kEach = 16;           // values of a lane and chunk
 constexpr int kChunk = 32 * kEach;  // values of a warp's chunk
 constexpr int kRing = 4160;         // bytes of a warp's ring: two or four chunks and 16 each
 constexpr int kList = 128;          // keys of a warp's list
-constexpr int kSlack = 8;           // keys past the W best before they are sorted out
+constexpr int kSlack = 4;           // keys past the W best before they are sorted out
 constexpr int kMaxPieces = 64;      // of a row: two lists to a lane of the merge
 constexpr int kMaxCluster = 16;
 constexpr int kShortest = 512;      // values that are a warp's piece of their own
@@ -204,19 +204,6 @@ __device__ __forceinline__ float pick(const float (&x)[kEach], int i) {
   return i & 1 ? y[1] : y[0];
 }
 
-// A bitonic sort over the lanes, largest first.
-__device__ __forceinline__ uint32_t sort_lanes(uint32_t x) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll 1
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      const uint32_t y = __shfl_xor_sync(kAll, x, j);
-      x = ((lane & k) == 0) == ((lane & j) == 0) ? max(x, y) : min(x, y);
-    }
-  return x;
-}
-
 __device__ __forceinline__ float largest(const float (&x)[kEach]) {
   float m = fmaxf(x[0], x[1]);
 #pragma unroll
@@ -231,11 +218,12 @@ struct Known {
   int warps, k;       // warps * k >= W: so W values reach the least of them
 };
 
-// A warp's piece [begin, end) of a row: its W best to the list (0 behind the last), its
+// A warp's piece [begin, end) of a row: its `count` <= W best to the list, in order, its
 // maximum and sum returned.  me: the warp among those of its row.
 template <typename T, bool VEC>
 __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos, int W,
-                                       uint8_t* ring, Key* list, Key* room, Known known, int me) {
+                                       uint8_t* ring, Key* list, Key* room, Known known, int me,
+                                       int& count) {
   using P = Piece<T, VEC>;
   const int lane = threadIdx.x & 31;
   P p;
@@ -280,10 +268,18 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
       mt = largest(x);
     }
     if (i == 0) {
-      // The lanes' maxima: as many values reach the j-th largest as there are before it.
-      const uint32_t o = sort_lanes(ordered(mt));
-      if (lane == W - 1) atomicMax(known.reached, o);
-      if (lane == known.k - 1) known.kth[me] = o;
+      // The lanes' maxima, largest first: j + 1 values reach the j-th.
+      uint32_t o = ordered(mt);
+#pragma unroll 1
+      for (int j = 0; j < W; ++j) {
+        const uint32_t top = __reduce_max_sync(kAll, o);
+        const int who = __ffs(__ballot_sync(kAll, o == top)) - 1;
+        if (lane == who) {
+          o = 0;
+          if (j + 1 == known.k) known.kth[me] = top;
+          if (j + 1 == W) atomicMax(known.reached, top);
+        }
+      }
       __syncwarp();
     }
     const uint32_t all = lane < known.warps ? *(volatile uint32_t*)(known.kth + lane) : ~0u;
@@ -321,16 +317,10 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
     }
   }
   copy_wait<0>();
-  if (lane >= n && lane < W) list[lane] = 0;
+  count = n;
   const float M = unordered(__reduce_max_sync(kAll, ordered(m)));
   return make_float2(M, add_up(l, m, M));
 }
-
-// What the merge holds: per row (beam) of the cluster its best keys, maximum and sum.
-struct Rows {
-  Key* top;   // [W][W]
-  float2* ml;  // [W]
-};
 
 // log x of a sum, x >= 1, to 2^-25: e log 2 + log f, x = 2^e f with f in [1 / sqrt 2,
 // sqrt 2), so that fp32's half steps are those of a number below 0.35.
@@ -345,39 +335,159 @@ __device__ __forceinline__ double log_of(float x) {
   return e * 0.69314718055994531 + (double)logf(f);
 }
 
-// The best over the beams, one CTA to a request; alive: the beams whose rows were taken.
-__device__ __forceinline__ void choose(const BeamSelectArgs& a, int b, uint32_t alive, Rows r,
-                                       Key* cand, double* s_lse, float end_x) {
-  const int W = a.W, tid = threadIdx.x, lane = tid & 31;
-  const float sc = lane < W ? a.scores[b * W + lane] : -INFINITY;
-  if (tid < 32) {
-    double lse = -INFINITY;
-    if (alive >> lane & 1) {
-      const float2 ml = r.ml[lane];
-      // Nothing allowed (a sum of 0) gives no candidate; NaN or +inf among the logits neither.
-      if (isnan(ml.y))
-        flag_status(a.status, PA_DEV_BAD_LOGITS);
-      else if (ml.y > 0.f)
-        lse = (double)ml.x + log_of(ml.y);
-    }
-    s_lse[lane] = lse;
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores 8 bytes to shared memory of the cluster's first CTA.
+template <typename X>
+__device__ __forceinline__ void store_first(X* p, X x) {
+  static_assert(sizeof(X) == 8, "one store");
+  uint32_t at;
+  unsigned long long y;
+  memcpy(&y, &x, 8);
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(p)));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(y) : "memory");
+}
+
+// a / b, rounded down, of small numbers, b > 0 (the quotient's error is far below 0.5 / b).
+__device__ __forceinline__ int small_div(int a, int b) {
+  return (int)__fdividef((float)a + 0.5f, (float)b);
+}
+
+// A cluster to a request.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
+  extern __shared__ __align__(16) uint8_t s_dyn[];  // the warps' rings, then what is merged
+  __shared__ Key s_list[kWarps][kList];
+  __shared__ Key s_room[kWarps][kMaxBeams];
+  __shared__ uint32_t s_reached[kMaxBeams], s_kth[kWarps];
+  __shared__ double s_lse[32];
+  __shared__ float s_score[32];
+  const int ranks = a.ranks, b = blockIdx.x / ranks, rank = blockIdx.x - b * ranks, W = a.W;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (ranks > 1) cluster_arrive();  // (nobody stores to a CTA that has not begun)
+  if (tid < kMaxBeams) s_reached[tid] = 0;
+  if (tid < kWarps) s_kth[tid] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  // A beam whose score is not finite is not there.
+  const float score = lane < W ? a.scores[b * W + lane] : -INFINITY;
+  const bool here = isfinite(score);
+  const uint32_t alive = __ballot_sync(kAll, here);
+  const int rows = __popc(alive);
+  // What the choice needs of the beams, a lane to each.
+  float end_x = -INFINITY;
+  if (rank == 0 && warp == 0) {
+    s_score[lane] = score;
+    if (here && a.eos >= 0)
+      end_x = to_float<T>(
+          static_cast<const T*>(a.logits)[(long long)(b * W + lane) * a.row_stride + a.eos]);
   }
+  // The beam of the i-th live row.
+  const int nth = __popc(alive & ((1u << lane) - 1));
+  auto live_beam = [&](int i) { return __ffs(__ballot_sync(kAll, here && nth == i)) - 1; };
+  // Pieces of a row, multiples of 16 values, the last ones may be empty.
+  const int pieces = min(kMaxPieces, small_div(ranks * kWarps, max(rows, 1)));
+  const int length = ((int)(__fdividef((float)a.V, (float)pieces) * 1.000001f) + 16) & ~15;
+  // What is merged, in the first CTA: per list, [row][piece], its keys, maximum and sum;
+  // per beam its best keys and what they are as candidates.
+  Key* keys = reinterpret_cast<Key*>(s_dyn + kWarps * kRing);
+  float2* mls = reinterpret_cast<float2*>(keys + (size_t)ranks * kWarps * W);
+  Key* top = reinterpret_cast<Key*>(mls + ranks * kWarps);
+  Key* cand = top + W * W;
   __syncthreads();
+  // A row's pieces go to neighbouring warps, which share thresholds.
+  const int per = small_div(rows * pieces + ranks - 1, ranks), task = rank * per + warp;
+  const bool work = warp < per && task < rows * pieces;
+  if (work) {
+    const int r = small_div(task, pieces), w = live_beam(r);
+    const int begin = (int)min((long long)(task - r * pieces) * length, (long long)a.V);
+    const int end = (int)min((long long)begin + length, (long long)a.V);
+    const T* x = static_cast<const T*>(a.logits) + (long long)(b * W + w) * a.row_stride;
+    // The row's warps of this CTA (its pieces may begin or go on in a neighbour).
+    const int first = max(r * pieces - rank * per, 0);
+    const int warps = min((r + 1) * pieces - rank * per, per) - first;
+    const Known known = {&s_reached[w], &s_kth[first], warps, small_div(W + warps - 1, warps)};
+    int n;
+    const float2 ml = scan<T, VEC>(x, begin, end, a.eos, W, s_dyn + warp * kRing, s_list[warp],
+                                   s_room[warp], known, warp - first, n);
+    if (ranks > 1) cluster_wait();
+    if (lane < W) store_first(keys + task * W + lane, lane < n ? s_list[warp][lane] : (Key)0);
+    if (lane == 0) store_first(mls + task, ml);
+  } else if (ranks > 1) {
+    cluster_wait();
+  }
+  if (ranks > 1) {
+    cluster_arrive();
+    cluster_wait();
+    if (rank > 0) return;
+  } else {
+    __syncthreads();
+  }
+  // ---- the first CTA: by row a warp for the keys and one for the sum
 #pragma unroll 1
-  for (int i = tid; i < W * W; i += kThreads) {
-    const int w = i / W;
-    const Key k = (alive >> w & 1) ? r.top[i] : 0;
-    const double lse = s_lse[w];
-    // (0: none; what a finite number is ordered as is not)
-    cand[i] = k != 0 && lse > -INFINITY
-                  ? ordered((double)a.scores[b * W + w] + ((double)value_of(k) - lse) + 0.0)
-                  : 0;
+  for (int i = warp; i < 2 * rows; i += kWarps) {
+    const bool sums = i >= rows;
+    const int r = sums ? i - rows : i, w = live_beam(r);
+    if (sums) {
+      float2 v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        v[e] = lane + 32 * e < pieces ? mls[r * pieces + lane + 32 * e]
+                                      : make_float2(-INFINITY, 0.f);
+      const float M = unordered(__reduce_max_sync(kAll, ordered(fmaxf(v[0].x, v[1].x))));
+      float l = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (v[e].y != 0.f) l += v[e].y * ex2_approx((v[e].x - M) * kLog2e);
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(kAll, l, d);
+      // Nothing allowed (a sum of 0) gives no candidate; NaN or +inf among the logits neither.
+      if (isnan(l) && lane == 0) flag_status(a.status, PA_DEV_BAD_LOGITS);
+      if (lane == 0) s_lse[w] = l > 0.f ? (double)M + log_of(l) : -INFINITY;
+    } else {
+      // Rounds of the largest head of the row's lists, two to a lane.
+      const Key* mine = keys + r * pieces * W;
+      int at[2] = {lane * W, (lane + 32) * W};
+      Key head[2], kept = 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) head[e] = lane + 32 * e < pieces ? mine[at[e]] : 0;
+#pragma unroll 1
+      for (int j = 0; j < W; ++j) {
+        const Key k = warp_max(max(head[0], head[1]));
+        if (lane == j) kept = k;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (k != 0 && head[e] == k) {
+            ++at[e];
+            head[e] = at[e] < (lane + 32 * e + 1) * W ? mine[at[e]] : 0;
+          }
+      }
+      if (lane < W) top[w * W + lane] = kept;
+    }
   }
   __syncthreads();
-  if (tid >= 32) return;
-  // Lane i holds the next candidate of beam i.
-  int at = 0;
-  Key c = lane < W ? cand[lane * W] : 0;
+  // ---- candidates (0: none; what a finite number is ordered as is not)
+#pragma unroll 1
+  for (int i = warp; i < rows; i += kWarps) {
+    const int w = live_beam(i);
+    const double lse = s_lse[w];
+    if (lane < W) {
+      const Key k = top[w * W + lane];
+      cand[w * W + lane] =
+          k != 0 && lse > -INFINITY
+              ? ordered((double)s_score[w] + ((double)value_of(k) - lse) + 0.0)
+              : 0;
+    }
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  // ---- the choice: lane i holds the next candidate of beam i
+  int at = lane * W;
+  Key c = here ? cand[at] : 0, k = here ? top[at] : 0;
   Key my_c = 0, my_key = 0, last_c = 0, last_key = 0;  // of place `lane`; of the last place
   int my_beam = lane, last_beam = 0;
 #pragma unroll 1
@@ -386,8 +496,7 @@ __device__ __forceinline__ void choose(const BeamSelectArgs& a, int b, uint32_t 
     last_c = best;
     if (best == 0) break;
     last_beam = __ffs(__ballot_sync(kAll, c == best)) - 1;
-    const int place = __shfl_sync(kAll, at, last_beam);
-    last_key = r.top[last_beam * W + place];
+    last_key = __shfl_sync(kAll, k, last_beam);
     if (lane == j) {
       my_c = best;
       my_beam = last_beam;
@@ -395,7 +504,8 @@ __device__ __forceinline__ void choose(const BeamSelectArgs& a, int b, uint32_t 
     }
     if (lane == last_beam) {
       ++at;
-      c = at < W ? cand[lane * W + at] : 0;
+      c = at < (lane + 1) * W ? cand[at] : 0;
+      k = at < (lane + 1) * W ? top[at] : 0;
     }
   }
   if (lane >= W) return;
@@ -405,148 +515,20 @@ __device__ __forceinline__ void choose(const BeamSelectArgs& a, int b, uint32_t 
   a.new_scores[o] = my_c != 0 ? (float)unordered(my_c) : -INFINITY;
   // Ends that are better than the last one chosen.
   float ended = -INFINITY;
-  const double lse = s_lse[lane];
-  if (lse > -INFINITY && a.eos >= 0) {
-    const double e = (double)sc + ((double)end_x - lse) + 0.0;
+  const double lse = here ? s_lse[lane] : -INFINITY;
+  if (lse > -INFINITY && end_x > -INFINITY) {
+    const double e = (double)score + ((double)end_x - lse) + 0.0;
     const Key eo = ordered(e);
     const bool ahead = last_c != 0 && lane == last_beam
                            ? key_of(end_x, a.eos) > last_key
                            : eo > last_c || (eo == last_c && lane < last_beam);
-    if (end_x > -INFINITY && ahead) ended = (float)e;
+    if (ahead) ended = (float)e;
   }
   a.ended[o] = ended;
 }
 
-// All threads of the cluster meet; what they wrote to shared memory is seen behind it.
-__device__ __forceinline__ void cluster_meet() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-}
-// Shared memory of CTA `rank` of the cluster.
-template <typename X>
-__device__ __forceinline__ X at_rank(const X* p, int rank) {
-  static_assert(sizeof(X) == 8, "one load");
-  uint32_t at;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  unsigned long long x;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(at) : "memory");
-  X y;
-  memcpy(&y, &x, 8);
-  return y;
-}
-
-// The beam of the i-th live row.
-__device__ __forceinline__ int live_beam(uint32_t alive, int i) {
-#pragma unroll 1
-  for (; i > 0; --i) alive &= alive - 1;
-  return __ffs(alive) - 1;
-}
-
-// A cluster to a request.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
-  extern __shared__ __align__(16) uint8_t s_dyn[];  // the warps' rings, then what is merged
-  __shared__ Key s_list[kWarps][kList];
-  __shared__ Key s_room[kWarps][kMaxBeams];
-  __shared__ float2 s_ml[kWarps];
-  __shared__ uint32_t s_reached[kMaxBeams], s_kth[kWarps];
-  __shared__ double s_lse[32];
-  const int ranks = a.ranks, b = blockIdx.x / ranks, rank = blockIdx.x - b * ranks, W = a.W;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < kMaxBeams) s_reached[tid] = 0;
-  if (tid < kWarps) s_kth[tid] = 0;
-  pdl_wait();
-  pdl_launch_dependents();
-  // A beam whose score is not finite is not there.
-  const uint32_t alive =
-      __ballot_sync(kAll, lane < W && isfinite(a.scores[b * W + (lane < W ? lane : 0)]));
-  const int rows = __popc(alive);
-  // What the choice needs of the beams, a lane to each.
-  float end_x = -INFINITY;
-  if (rank == 0 && warp == 0 && (alive >> lane & 1) && a.eos >= 0)
-    end_x = to_float<T>(
-        static_cast<const T*>(a.logits)[(long long)(b * W + lane) * a.row_stride + a.eos]);
-  // Pieces of a row: whole 16-byte pieces each, the last ones may be empty.
-  const int pieces = min(kMaxPieces, ranks * kWarps / max(rows, 1));
-  const int length = ((a.V + pieces - 1) / pieces + 15) / 16 * 16;
-  __syncthreads();
-  // A row's pieces go to neighbouring warps, which share a threshold.
-  const int per = (rows * pieces + ranks - 1) / ranks, task = rank * per + warp;
-  if (warp < per && task < rows * pieces) {
-    const int r = task / pieces, w = live_beam(alive, r);
-    const int begin = (int)min((long long)(task - r * pieces) * length, (long long)a.V);
-    const int end = (int)min((long long)begin + length, (long long)a.V);
-    const T* x = static_cast<const T*>(a.logits) + (long long)(b * W + w) * a.row_stride;
-    // The row's warps of this CTA (its pieces may begin or go on in a neighbour).
-    const int first = max(r * pieces - rank * per, 0);
-    const int warps = min(min((r + 1) * pieces, rows * pieces) - rank * per, per) - first;
-    const Known known = {&s_reached[w], &s_kth[first], warps, (W + warps - 1) / warps};
-    const float2 ml = scan<T, VEC>(x, begin, end, a.eos, W, s_dyn + warp * kRing,
-                                    s_list[warp], s_room[warp], known, warp - first);
-    if (lane == 0) s_ml[warp] = ml;
-  }
-  if (ranks > 1)
-    cluster_meet();
-  else
-    __syncthreads();
-  if (rank == 0) {
-    // All lists, [row][piece][W], and their maxima and sums.
-    Key* keys = reinterpret_cast<Key*>(s_dyn);
-    const int lists = rows * pieces;
-    float2* ml = reinterpret_cast<float2*>(keys + (size_t)ranks * kWarps * W);
-    Rows r = {reinterpret_cast<Key*>(ml + ranks * kWarps), nullptr};
-    r.ml = reinterpret_cast<float2*>(r.top + W * W);
-    Key* cand = reinterpret_cast<Key*>(r.ml + kMaxBeams);
-#pragma unroll 1
-    for (int i = tid; i < lists * W; i += kThreads) {
-      const int q = i / W, from = q / per;
-      keys[i] = at_rank(&s_list[q - from * per][i - q * W], from);
-    }
-#pragma unroll 1
-    for (int q = tid; q < lists; q += kThreads)
-      ml[q] = at_rank(&s_ml[q % per], q / per);
-    __syncthreads();
-    // A warp to a beam: rounds of the largest head of its lists, two to a lane.
-#pragma unroll 1
-    for (int i = warp; i < rows; i += kWarps) {
-      const int w = live_beam(alive, i);
-      const Key* mine = keys + (size_t)i * pieces * W;
-      int at[2] = {0, 0};
-      Key head[2];
-      float m[2], l[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int q = lane + 32 * e;
-        const bool has = q < pieces;
-        head[e] = has ? mine[(size_t)q * W] : 0;
-        const float2 v = has ? ml[i * pieces + q] : make_float2(-INFINITY, 0.f);
-        m[e] = v.x;
-        l[e] = v.y;
-      }
-      const float M = unordered(__reduce_max_sync(kAll, max(ordered(m[0]), ordered(m[1]))));
-      const float L = add_up(l[0], m[0], M) + add_up(l[1], m[1], M);
-      if (lane == 0) r.ml[w] = make_float2(M, L);
-#pragma unroll 1
-      for (int j = 0; j < W; ++j) {
-        const Key k = warp_max(max(head[0], head[1]));
-        if (lane == 0) r.top[w * W + j] = k;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (k != 0 && head[e] == k) {
-            ++at[e];
-            head[e] = at[e] < W ? mine[(size_t)(lane + 32 * e) * W + at[e]] : 0;
-          }
-      }
-    }
-    __syncthreads();
-    choose(a, b, alive, r, cand, s_lse, end_x);
-  }
-  if (ranks > 1) cluster_meet();  // nobody leaves while its lists are read
-}
-
 int dynamic_bytes(int W, int ranks) {
-  const int merge = ranks * kWarps * (W + 1) * 8 + (2 * W * W + kMaxBeams) * 8;
-  return merge > kWarps * kRing ? merge : kWarps * kRing;
+  return kWarps * kRing + ranks * kWarps * (W + 1) * 8 + 2 * W * W * 8;
 }
 
 template <typename T, bool VEC>

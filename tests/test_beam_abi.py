@@ -64,7 +64,7 @@ def select(lib, **kw):
 def test_select_refusals(lib):
     for kw in (dict(x=None), dict(x=P + 2), dict(dt=1, x=P + 1), dict(dt=3), dict(dt=-1),
                dict(stride=99), dict(stride=2 ** 40), dict(s=None), dict(B=-1), dict(W=0),
-               dict(B=2 ** 19, W=4), dict(V=0), dict(V=2 ** 31 - 1, stride=2 ** 31),
+               dict(B=2 ** 19, W=4), dict(V=0), dict(V=2 ** 28 + 1, stride=2 ** 31),
                dict(eos=100), dict(eos=-2), dict(t=None), dict(p=None), dict(n=None),
                dict(e=None)):
         assert select(lib, **kw) == pk.PA_ERR_INVALID, kw
