@@ -9,13 +9,13 @@
 // out its live beams' rows, a piece of a row to each; no warp waits for another until all
 // pieces are done.  A warp's piece comes through a ring of its own in shared memory
 // (asynchronous copies of 16 bytes a lane), so that its loop takes few registers and
-// little code; every lane keeps a running maximum and sum.  Of the first pieces in the
-// ring the W-th largest of the lanes' maxima is a threshold that W values reach and few
-// others.  Values that reach it go to a list as (ordered value, ~index) keys; when that is
-// full, its W best are kept by counting for each key how many are above it, and the W-th
-// becomes the threshold, of the other warps of the CTA on that row too.  The cluster's
-// first CTA then merges the pieces' lists by beam and the beams' lists, in order, by as
-// many rounds of a maximum over the lanes as there are beams.
+// little code; every lane keeps a running maximum and sum.  The piece's W best are a
+// sorted list of (ordered value, ~index) keys over the lanes, into which values that reach
+// a threshold are inserted one by one: the W-th of the list, or what the row's other warps
+// of the CTA know, and in a chunk where many values reach that (the first one) the W-th
+// largest of the lanes' maxima.  The cluster's first CTA then merges the pieces' lists by
+// beam and the beams' lists, in order, by as many rounds of a maximum over the lanes as
+// there are beams.
 //
 // Rounding: sums in fp32, candidates in 64 bits (two beams' can be nearer than fp32 tells
 // apart), the scores once to fp32.  A sum goes by the values' index and not by the row's
@@ -42,8 +42,7 @@ constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kEach = 16;           // values of a lane and chunk
 constexpr int kChunk = 32 * kEach;  // values of a warp's chunk
 constexpr int kRing = 4160;         // bytes of a warp's ring: two or four chunks and 16 each
-constexpr int kList = 128;          // keys of a warp's list
-constexpr int kSlack = 4;           // keys past the W best before they are sorted out
+constexpr int kMany = 64;           // values of a chunk that are too many to be inserted
 constexpr int kMaxPieces = 64;      // of a row: two lists to a lane of the merge
 constexpr int kMaxCluster = 16;
 constexpr int kShortest = 512;      // values that are a warp's piece of their own
@@ -87,8 +86,8 @@ __device__ __forceinline__ void mul_f32x2(float& d0, float& d1, float a0, float 
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-// The warp's sums l relative to its maxima m, relative to M.  (A lane without values has
-// m = -inf and l = 0; a NaN among l stays one.)
+// The sum over the lanes of l relative to maximum m, relative to M.  (A lane without
+// values has m = -inf and l = 0; a NaN among l stays one.)
 __device__ __forceinline__ float add_up(float l, float m, float M) {
   float x = l != 0.f ? l * ex2_approx((m - M) * kLog2e) : 0.f;
 #pragma unroll
@@ -172,26 +171,6 @@ struct Piece {
   }
 };
 
-// The W best of a warp's n <= kList keys, in order, to the list's front (by way of `room`).
-// Keys differ, so that each one's place is the number of those above it.
-__device__ __forceinline__ int sort_out(Key* list, Key* room, int n, int W) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
-#pragma unroll 1
-  for (int i = lane; i < (n + 31) / 32 * 32; i += 32) {
-    const Key k = i < n ? list[i] : ~0ull;
-    int above = 0;
-#pragma unroll 4
-    for (int q = 0; q < n; ++q) above += list[q] > k;
-    if (i < n && above < W) room[above] = k;
-  }
-  __syncwarp();
-  n = min(n, W);
-  if (lane < n) list[lane] = room[lane];
-  __syncwarp();
-  return n;
-}
-
 // x[i] for an i known at run time only, without a trip through memory.
 __device__ __forceinline__ float pick(const float (&x)[kEach], int i) {
   float y[kEach / 2];
@@ -211,19 +190,18 @@ __device__ __forceinline__ float largest(const float (&x)[kEach]) {
   return m;
 }
 
-// What the warps of a CTA on one row know of it, as ordered values; 0: nothing yet.
+// What the warps of a CTA on one row know of it, as ordered values by warp; 0: nothing yet.
 struct Known {
-  uint32_t* reached;  // W values of the row reach it
-  uint32_t* kth;      // by warp, from the row's first: k of the warp's values reach it
-  int warps, k;       // warps * k >= W: so W values reach the least of them
+  uint32_t* wth;  // W of the warp's values reach it
+  uint32_t* kth;  // k of them do
+  int warps, k;   // warps * k >= W: so W values of the row reach the least of these
 };
 
-// A warp's piece [begin, end) of a row: its `count` <= W best to the list, in order, its
-// maximum and sum returned.  me: the warp among those of its row.
+// A warp's piece [begin, end) of a row: its W best, in order, a lane to each (0: none), and
+// its maximum and sum.  me: the warp among those of its row.
 template <typename T, bool VEC>
-__device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos, int W,
-                                       uint8_t* ring, Key* list, Key* room, Known known, int me,
-                                       int& count) {
+__device__ __forceinline__ Key scan(const T* row, int begin, int end, int eos, int W,
+                                    uint8_t* ring, Known known, int me, float2& max_sum) {
   using P = Piece<T, VEC>;
   const int lane = threadIdx.x & 31;
   P p;
@@ -233,13 +211,11 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
   p.bytes = begin < end ? p.lead + (end - begin) * (int)sizeof(T) : 0;
 #pragma unroll 1
   for (int i = 0; i < P::kSlots; ++i) p.request(i);
+  Key mine = 0;
   float m = -INFINITY, l = 0.f;
   float t = -FLT_MAX;  // values from it on are candidates (-inf and NaN never)
-  constexpr uint32_t kLeast = 0x00800000u;  // ordered(-FLT_MAX)
-  int n = 0;
 #pragma unroll 1
   for (int i = 0, base = begin; base < end; ++i, base += kChunk) {
-    const bool last = base + kChunk >= end;
     copy_wait<P::kSlots - 1>();
     __syncwarp();
     float x[kEach];
@@ -251,6 +227,7 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
       l *= ex2_approx((m - mt) * kLog2e);  // (m = -inf: l is 0)
       m = mt;
     }
+    // (From the maximum first: a product of its own would round, or overflow, before.)
     const float ref = m == -INFINITY ? 0.f : -m;
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -267,59 +244,52 @@ __device__ __forceinline__ float2 scan(const T* row, int begin, int end, int eos
         if (P::index(base, j) == eos) x[j] = -INFINITY;
       mt = largest(x);
     }
-    if (i == 0) {
-      // The lanes' maxima, largest first: j + 1 values reach the j-th.
+    if (!__any_sync(kAll, mt >= t)) continue;
+    const bool other = lane < known.warps;
+    const uint32_t least =
+        __reduce_min_sync(kAll, other ? *(volatile uint32_t*)(known.kth + lane) : ~0u);
+    uint32_t reached =
+        max(__reduce_max_sync(kAll, other ? *(volatile uint32_t*)(known.wth + lane) : 0u), least);
+    uint32_t hits;  // of the lane's values, those that reach t
+#pragma unroll 1
+    for (bool again = true;; again = false) {
+      t = fmaxf(t, unordered(max(reached, ordered(-FLT_MAX))));
+      hits = 0;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) hits |= x[j] >= t ? 1u << j : 0u;
+      if (!again || __reduce_add_sync(kAll, (unsigned)__popc(hits)) <= kMany) break;
+      // The lanes' maxima, largest first: W values reach the W-th.
       uint32_t o = ordered(mt);
 #pragma unroll 1
       for (int j = 0; j < W; ++j) {
-        const uint32_t top = __reduce_max_sync(kAll, o);
-        const int who = __ffs(__ballot_sync(kAll, o == top)) - 1;
-        if (lane == who) {
-          o = 0;
-          if (j + 1 == known.k) known.kth[me] = top;
-          if (j + 1 == W) atomicMax(known.reached, top);
-        }
+        reached = __reduce_max_sync(kAll, o);
+        if (lane == __ffs(__ballot_sync(kAll, o == reached)) - 1) o = 0;
       }
-      __syncwarp();
     }
-    const uint32_t all = lane < known.warps ? *(volatile uint32_t*)(known.kth + lane) : ~0u;
-    const uint32_t reached =
-        max(__reduce_min_sync(kAll, all), *(volatile uint32_t*)known.reached);
-    t = fmaxf(t, unordered(max(reached, kLeast)));
-    uint32_t hits = 0;  // of the lane's values, those that reach t
-    if (mt >= t) {
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) hits |= x[j] >= t ? 1u << j : 0u;
-    }
-    bool sorted = false;
 #pragma unroll 1
-    for (;;) {  // one of a lane at a time
-      const unsigned mask = __ballot_sync(kAll, hits != 0);
-      if (mask != 0 ? n + __popc(mask) > kList : sorted || last || n >= W + kSlack) {
-        n = sort_out(list, room, n, W);
-        if (n >= known.k && lane == 0) known.kth[me] = (uint32_t)(list[known.k - 1] >> 32);
-        if (n == W) {
-          // An equal value of a later chunk comes too late (of this one it may not: a
-          // lane's values come in no order of their indices).
-          const uint32_t lowest = (uint32_t)(list[W - 1] >> 32);
-          if (mask == 0) t = fmaxf(t, unordered(lowest + 1));
-          if (lane == 0) atomicMax(known.reached, lowest);
-        }
-        sorted = true;
+    for (unsigned mask; (mask = __ballot_sync(kAll, hits != 0)) != 0;) {
+      const int j = hits != 0 ? __ffs(hits) - 1 : 0;
+      const Key key = key_of(pick(x, j), P::index(base, j));
+      hits &= hits - 1;
+#pragma unroll 1
+      for (; mask != 0; mask &= mask - 1) {
+        const Key k = __shfl_sync(kAll, key, __ffs(mask) - 1);
+        const int above = __popc(__ballot_sync(kAll, mine > k));
+        const Key up = __shfl_up_sync(kAll, mine, 1);
+        mine = lane < above ? mine : lane == above ? k : up;
       }
-      if (mask == 0) break;
-      if (hits != 0) {
-        const int j = __ffs(hits) - 1;
-        list[n + __popc(mask & ((1u << lane) - 1))] = key_of(pick(x, j), P::index(base, j));
-        hits &= hits - 1;
-      }
-      n += __popc(mask);
     }
+    const uint32_t value = (uint32_t)(mine >> 32);
+    if (lane == known.k - 1) known.kth[me] = value;
+    if (lane == W - 1) known.wth[me] = value;
+    // (an equal value of a later chunk comes too late)
+    const uint32_t last = __shfl_sync(kAll, value, W - 1);
+    if (last != 0) t = fmaxf(t, unordered(last + 1));
   }
   copy_wait<0>();
-  count = n;
   const float M = unordered(__reduce_max_sync(kAll, ordered(m)));
-  return make_float2(M, add_up(l, m, M));
+  max_sum = make_float2(M, add_up(l, m, M));
+  return lane < W ? mine : 0;
 }
 
 // log x of a sum, x >= 1, to 2^-25: e log 2 + log f, x = 2^e f with f in [1 / sqrt 2,
@@ -361,16 +331,13 @@ __device__ __forceinline__ int small_div(int a, int b) {
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
   extern __shared__ __align__(16) uint8_t s_dyn[];  // the warps' rings, then what is merged
-  __shared__ Key s_list[kWarps][kList];
-  __shared__ Key s_room[kWarps][kMaxBeams];
-  __shared__ uint32_t s_reached[kMaxBeams], s_kth[kWarps];
+  __shared__ uint32_t s_wth[kWarps], s_kth[kWarps];
   __shared__ double s_lse[32];
   __shared__ float s_score[32];
   const int ranks = a.ranks, b = blockIdx.x / ranks, rank = blockIdx.x - b * ranks, W = a.W;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (ranks > 1) cluster_arrive();  // (nobody stores to a CTA that has not begun)
-  if (tid < kMaxBeams) s_reached[tid] = 0;
-  if (tid < kWarps) s_kth[tid] = 0;
+  if (tid < kWarps) s_wth[tid] = s_kth[tid] = 0;
   pdl_wait();
   pdl_launch_dependents();
   // A beam whose score is not finite is not there.
@@ -410,12 +377,12 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
     // The row's warps of this CTA (its pieces may begin or go on in a neighbour).
     const int first = max(r * pieces - rank * per, 0);
     const int warps = min((r + 1) * pieces - rank * per, per) - first;
-    const Known known = {&s_reached[w], &s_kth[first], warps, small_div(W + warps - 1, warps)};
-    int n;
-    const float2 ml = scan<T, VEC>(x, begin, end, a.eos, W, s_dyn + warp * kRing, s_list[warp],
-                                   s_room[warp], known, warp - first, n);
+    const Known known = {&s_wth[first], &s_kth[first], warps, small_div(W + warps - 1, warps)};
+    float2 ml;
+    const Key mine = scan<T, VEC>(x, begin, end, a.eos, W, s_dyn + warp * kRing, known,
+                                  warp - first, ml);
     if (ranks > 1) cluster_wait();
-    if (lane < W) store_first(keys + task * W + lane, lane < n ? s_list[warp][lane] : (Key)0);
+    if (lane < W) store_first(keys + task * W + lane, mine);
     if (lane == 0) store_first(mls + task, ml);
   } else if (ranks > 1) {
     cluster_wait();

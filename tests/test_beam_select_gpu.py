@@ -174,6 +174,10 @@ def test_masked(V):
     x, s = made(2, W, V, F32, seed=5)
     x[:, 5:] = lowest  # the type's lowest value is a value
     check(x, s, eos=2)
+    for dtype in (F32, BF16, FP16):  # a row of nothing else is one of equal values
+        x[:] = torch.finfo(dtype).min
+        x[1, V // 2] = torch.finfo(dtype).max
+        check(x.to(dtype), s, eos=2)
 
 
 def test_no_numbers():
