@@ -38,14 +38,13 @@ namespace pk {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kWarps = 16;          // of a CTA
 constexpr int kEach = 16;           // values of a lane and chunk
 constexpr int kChunk = 32 * kEach;  // values of a warp's chunk
-constexpr int kRing = 4160;         // bytes of a warp's ring: two or four chunks and 16 each
+constexpr int kRing = 8320;         // bytes of a warp's ring: four or eight chunks and 16 each
 constexpr int kMany = 64;           // values of a chunk that are too many to be inserted
 constexpr int kMaxPieces = 64;      // of a row: two lists to a lane of the merge
 constexpr int kMaxCluster = 16;
-constexpr int kShortest = 512;      // values that are a warp's piece of their own
 constexpr float kLog2e = 1.4426950408889634f;
 using Key = unsigned long long;
 
@@ -329,15 +328,15 @@ __device__ __forceinline__ int small_div(int a, int b) {
 
 // A cluster to a request.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamSelectArgs a) {
   extern __shared__ __align__(16) uint8_t s_dyn[];  // the warps' rings, then what is merged
   __shared__ uint32_t s_wth[kWarps], s_kth[kWarps];
   __shared__ double s_lse[32];
   __shared__ float s_score[32];
   const int ranks = a.ranks, b = blockIdx.x / ranks, rank = blockIdx.x - b * ranks, W = a.W;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (ranks > 1) cluster_arrive();  // (nobody stores to a CTA that has not begun)
-  if (tid < kWarps) s_wth[tid] = s_kth[tid] = 0;
+  if (lane == 0) s_wth[warp] = s_kth[warp] = 0;
   pdl_wait();
   pdl_launch_dependents();
   // A beam whose score is not finite is not there.
@@ -362,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
   // What is merged, in the first CTA: per list, [row][piece], its keys, maximum and sum;
   // per beam its best keys and what they are as candidates.
   Key* keys = reinterpret_cast<Key*>(s_dyn + kWarps * kRing);
-  float2* mls = reinterpret_cast<float2*>(keys + (size_t)ranks * kWarps * W);
+  float2* mls = reinterpret_cast<float2*>(keys + ranks * kWarps * W);
   Key* top = reinterpret_cast<Key*>(mls + ranks * kWarps);
   Key* cand = top + W * W;
   __syncthreads();
@@ -376,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
     const T* x = static_cast<const T*>(a.logits) + (long long)(b * W + w) * a.row_stride;
     // The row's warps of this CTA (its pieces may begin or go on in a neighbour).
     const int first = max(r * pieces - rank * per, 0);
-    const int warps = min((r + 1) * pieces - rank * per, per) - first;
-    const Known known = {&s_wth[first], &s_kth[first], warps, small_div(W + warps - 1, warps)};
+    const int n = min((r + 1) * pieces - rank * per, per) - first;
+    const Known known = {&s_wth[first], &s_kth[first], n, small_div(W + n - 1, n)};
     float2 ml;
     const Key mine = scan<T, VEC>(x, begin, end, a.eos, W, s_dyn + warp * kRing, known,
                                   warp - first, ml);
@@ -510,7 +509,7 @@ cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.ranks * a.B);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -532,14 +531,17 @@ cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// CTAs of a request: as many as the GPU holds at two to an SM, and as there are chunks of
-// its rows for their warps.
+// CTAs of a request: as many as give every SM one, which their rings see to as well (two
+// to an SM share its issue slots, and the second may come to lie beside the first while
+// other SMs are idle), and no more than there are chunks for their warps.  Clusters of 16
+// take one GPU's processing cluster each: for few requests.
 int beam_select_ranks(int B, int W, int V) {
   const int nsm = sm_count() > 0 ? sm_count() : 152;
-  const long long warps = (long long)W * ((V - 1) / kShortest + 1);
-  int c = W > kWarps ? 2 : 1;  // (a warp to a row at least)
-  while (c < kMaxCluster && 2LL * c * B <= 2 * nsm && c * kWarps < warps) c *= 2;
-  return c;
+  const long long chunks = (long long)W * ((V - 1) / kChunk + 1);
+  const int limit = B <= 4 ? kMaxCluster : 8, least = W > kWarps ? 2 : 1;  // a warp to a row
+  long long c = (chunks + kWarps - 1) / kWarps;
+  if (c > nsm / B) c = nsm / B;
+  return c > limit ? limit : c > least ? (int)c : least;
 }
 
 cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t stream) {
