@@ -9,13 +9,15 @@
 // none holds there any more goes back to the ring.  Requests in order, in each one the
 // rows' columns in order, in each one the beams: equal inputs give equal tables.
 //
-// Every thread takes a column of a request, reads its W entries and writes the new ones,
-// so that a table may be its own output; what a request needs and gives back has to be
-// known before, for the places in the ring.  Few entries: one CTA takes all requests and
-// its scan over the columns carries the places along.  Many: one CTA to a request counts,
-// a second launch adds up the counts before its request and writes.
+// A CTA brings its requests' rows to shared memory while it reads parents and lengths
+// (rows that do not fit stay where they are); then every thread takes a column of a
+// request, looks at its W entries and writes the new ones, so that a table may be its own
+// output.  What a request needs and gives back has to be known before, for the places in
+// the ring.  Few entries: one CTA takes all requests and its scan over the columns carries
+// the places along.  Many: one CTA to a request counts, a second launch adds up the counts
+// before its request and writes.
 //
-// Bound: the launches and the trips parents, lengths, last blocks, entries.
+// Bound: the launches, and the one trip to memory that parents, lengths and entries share.
 //
 // Backtrack.  Tokens of hypothesis k: beam(n - 1) = beams[k], token(s) = tokens[s][beam(s)],
 // beam(s - 1) = parents[s][beam(s)].  A walk of S steps is a chain of S loads, so each
@@ -35,73 +37,19 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 
 // ---------------------------------------------------------------- reorder
-// What a warp finds out about a request, a lane to a beam.
-struct Request {
-  int p;         // parent of the lane's beam, -1: none
-  int had, has;  // blocks of the old and of the new row
-  int len;       // new length
-  int tail;      // column of the last block, half full and an entry of the pool; -1: none
-  int tail_id;
-  uint32_t need;  // beams that get a copy of their last block
-  bool bad;       // left as it is
-  int flags;      // what is wrong with it, for the status
-};
-
-__device__ __forceinline__ Request look_at(const BeamReorderArgs& a, int b) {
-  const int lane = threadIdx.x & 31, W = a.W, bs = 1 << a.bs_log2;
-  Request r;
-  const bool here = lane < W;
-  r.p = here ? a.parents[b * W + lane] : -1;
-  const int old_len = here ? a.context_lens[b * W + lane] : 0;
-  const int shared = a.shared_lens != nullptr ? a.shared_lens[b] : 0;
-  const bool lost = here && (r.p < -1 || r.p >= W);
-  const bool off = here && (old_len < 0 || ((long long)old_len + bs - 1) >> a.bs_log2 > a.M);
-  r.flags = (lost ? PA_DEV_BAD_BEAM : 0) | (off || shared < 0 ? PA_DEV_BAD_CONTEXT : 0);
-  r.bad = __any_sync(kAll, r.flags != 0);
-  const int src = r.p >= 0 && r.p < W ? r.p : lane;
-  const int l = __shfl_sync(kAll, old_len, src);
-  r.len = r.p >= 0 ? l : 0;
-  r.had = r.bad ? 0 : (int)(((long long)old_len + bs - 1) >> a.bs_log2);
-  r.has = r.bad ? 0 : (int)(((long long)r.len + bs - 1) >> a.bs_log2);
-  r.tail = -1;
-  r.tail_id = -1;
-  if (!r.bad && here && r.has > 0 && (r.len & (bs - 1)) != 0) {
-    r.tail_id = a.block_tables[((size_t)b * W + src) * a.M + r.has - 1];
-    if (r.tail_id >= 0 && r.tail_id < a.num_blocks)
-      r.tail = r.has - 1;
-    else
-      r.flags |= PA_DEV_BAD_BLOCK_ID;
-  }
-  bool again = false;  // an earlier beam holds it as its last block
-#pragma unroll 1
-  for (int u = 0; u < W; ++u) {
-    const int t = __shfl_sync(kAll, r.tail, u), id = __shfl_sync(kAll, r.tail_id, u);
-    again |= u < lane && t >= 0 && t == r.tail && id == r.tail_id;
-  }
-  r.need = __ballot_sync(kAll, again);
-  return r;
-}
-
-// A request as the columns' threads see it.
-struct Rows {
-  int b, first;  // first: the first column whose blocks are the request's own
-  uint32_t need;
-  int before;  // blocks that requests before it take
-  bool bad;
-};
-
+// A column of a request: the entries of its beams there.
 template <int WM>
 struct Column {
-  int old[WM];          // entries; meaningful for beams that hold one
   uint32_t held, used;  // beams that hold an entry here; of those, the parents of one
   uint32_t drop;        // beams whose entry goes back
 
-  // had: blocks of the old rows
-  __device__ __forceinline__ void read(const BeamReorderArgs& a, const Rows& r, int col,
-                                       const int* had, const int* parent) {
+  // at: the column in the request's first row; had: blocks of the old rows; parents: the
+  // beams that are a parent.
+  __device__ __forceinline__ void look(const BeamReorderArgs& a, const int32_t* at, int col,
+                                       const int* had, uint32_t parents, int first) {
     const int W = a.W;
-    held = used = drop = 0;
-    const int32_t* at = a.block_tables + (size_t)r.b * W * a.M + col;
+    held = drop = 0;
+    int old[WM];
 #pragma unroll
     for (int w = 0; w < WM; ++w) {
       old[w] = -1;
@@ -110,12 +58,8 @@ struct Column {
         held |= 1u << w;
       }
     }
-    if (held == 0) return;
-#pragma unroll 1
-    for (int w = 0; w < W; ++w)
-      if (parent[w] >= 0) used |= 1u << parent[w];
-    used &= held;
-    if (col < r.first || used == held) return;
+    used = held & parents;
+    if (col < first || used == held) return;
 #pragma unroll 1
     for (uint32_t left = held & ~used; left != 0; left &= left - 1) {
       const int w = __ffs(left) - 1, id = at[(size_t)w * a.M];
@@ -133,7 +77,7 @@ struct Column {
   }
 };
 
-constexpr int kMaxInOne = 1024;  // requests of the launch by one CTA
+constexpr int kMaxInOne = 256;  // requests of the launch by one CTA
 
 // Blocks in the ring; -1 for a state that no ring of this size can have.
 __device__ __forceinline__ long long blocks_held(long long head, long long tail, int NB) {
@@ -164,62 +108,122 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int& total) {
 
 enum Pass { kInOne, kCount, kWrite };
 
+// A CTA's shared memory: its requests' rows (staged), then for each beam its parent, its
+// old and its new blocks and the last one where it is to be copied, and for each request
+// the beams that need a copy, the blocks taken before it, the beams that are a parent and
+// its first column of its own (-1: a request that stays as it is).
+int reorder_bytes(int nb, int W, int M, bool staged) {
+  return (staged ? nb * W * M * 4 : 0) + nb * W * 16 + nb * 16;
+}
+
 template <int WM, Pass P, int kThreads>
-__global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorderArgs a) {
-  // parents and blocks of a CTA's requests: one, or all of them
-  extern __shared__ int s_rows[];
+__global__ void __launch_bounds__(kThreads)
+    beam_reorder_kernel(const BeamReorderArgs a, bool staged) {
+  extern __shared__ __align__(16) int s_dyn[];
   __shared__ int s_warp[kThreads / 32];
   __shared__ long long s_sum[kThreads / 32];
-  __shared__ uint32_t s_bits[P == kInOne ? kMaxInOne : 1];  // need
-  __shared__ int s_before[P == kInOne ? kMaxInOne : 1];
-  __shared__ uint8_t s_bad[P == kInOne ? kMaxInOne : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int W = a.W;
+  const int W = a.W, M = a.M, bs = 1 << a.bs_log2;
   const int b0 = P == kInOne ? 0 : blockIdx.x, nb = P == kInOne ? a.B : 1;
-  int* s_parent = s_rows;        // [nb][W]
-  int* s_had = s_rows + nb * W;  // [nb][W]
-  int* s_has = s_had + nb * W;   // [nb][W]
-  int* s_tail = s_has + nb * W;  // [nb][W] id of a last block to copy
+  int* s_tab = s_dyn;
+  int* s_parent = s_tab + (staged ? nb * W * M : 0);  // [nb][W]
+  int* s_had = s_parent + nb * W;
+  int* s_has = s_had + nb * W;
+  int* s_tail = s_has + nb * W;
+  int* s_need = s_tail + nb * W;  // [nb]
+  int* s_before = s_need + nb;
+  int* s_used = s_before + nb;
+  int* s_first = s_used + nb;
   pdl_wait();
   pdl_launch_dependents();
+  // ---- everything from memory at once
+  const int32_t* from = a.block_tables + (size_t)b0 * W * M;
+  if (staged) {
+    const int n = nb * W * M;
+    const bool wide = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
+    const int n4 = wide ? n / 4 : 0;
+#pragma unroll 4
+    for (int i = tid; i < n4; i += kThreads)
+      reinterpret_cast<int4*>(s_tab)[i] = reinterpret_cast<const int4*>(from)[i];
+#pragma unroll 4
+    for (int i = 4 * n4 + tid; i < n; i += kThreads) s_tab[i] = from[i];
+  }
   // (By requests the second launch may replace the state while others still read it.)
   const int64_t* state = P == kWrite ? a.counts + 2 * a.B : a.free_state;
   const long long head = state[0], tail = state[1];
+#pragma unroll 1
+  for (int i = tid; i < nb * W; i += kThreads) {
+    s_parent[i] = a.parents[b0 * W + i];
+    s_had[i] = a.context_lens[b0 * W + i];  // (the length, for now)
+  }
+#pragma unroll 1
+  for (int i = tid; i < nb; i += kThreads)
+    s_first[i] = a.shared_lens != nullptr ? a.shared_lens[b0 + i] : 0;
+  __syncthreads();
   const long long held = blocks_held(head, tail, a.num_blocks);
-  // ---- the requests: parents, lengths, last blocks
+  const int32_t* tab = staged ? s_tab : from;
+  // ---- the requests, a warp to each, a lane to a beam
 #pragma unroll 1
   for (int i = warp; i < nb; i += kThreads / 32) {
-    const Request r = look_at(a, b0 + i);
-    if (lane < W) {
-      s_parent[i * W + lane] = r.bad ? lane : r.p;
-      s_had[i * W + lane] = r.had;
-      s_has[i * W + lane] = r.has;
-      s_tail[i * W + lane] = r.tail_id;
+    const bool here = lane < W;
+    const int p = here ? s_parent[i * W + lane] : -1, l = here ? s_had[i * W + lane] : 0;
+    const int shared = s_first[i];
+    const bool lost = p < -1 || p >= W;
+    const bool off = l < 0 || (int)(((long long)l + bs - 1) >> a.bs_log2) > M || shared < 0;
+    int flags = (lost ? PA_DEV_BAD_BEAM : 0) | (off ? PA_DEV_BAD_CONTEXT : 0);
+    const bool bad = __any_sync(kAll, flags != 0);
+    const int src = p >= 0 && p < W ? p : lane;
+    const int l_src = __shfl_sync(kAll, l, src);
+    const int len = p >= 0 ? l_src : 0;
+    const int had = bad ? 0 : (int)(((long long)l + bs - 1) >> a.bs_log2);
+    const int has = bad ? 0 : (int)(((long long)len + bs - 1) >> a.bs_log2);
+    int col = -1, id = -1;  // of the last block, half full and an entry of the pool
+    if (here && has > 0 && (len & (bs - 1)) != 0) {
+      id = tab[((size_t)i * W + src) * M + has - 1];
+      if (id >= 0 && id < a.num_blocks)
+        col = has - 1;
+      else
+        flags |= PA_DEV_BAD_BLOCK_ID;
+    }
+    bool again = false;  // an earlier beam holds it as its last block
+#pragma unroll 1
+    for (int u = 0; u < W; ++u) {
+      const int ucol = __shfl_sync(kAll, col, u), uid = __shfl_sync(kAll, id, u);
+      again |= u < lane && ucol >= 0 && ucol == col && uid == id;
+    }
+    const uint32_t need = __ballot_sync(kAll, again);
+    const uint32_t used = __reduce_or_sync(kAll, here && p >= 0 && !bad ? 1u << p : 0u);
+    __syncwarp();
+    if (here) {
+      s_parent[i * W + lane] = bad ? lane : p;
+      s_had[i * W + lane] = had;
+      s_has[i * W + lane] = has;
+      s_tail[i * W + lane] = id;
     }
     if (lane == 0) {
-      s_bits[i] = r.need;
-      s_bad[i] = r.bad;
+      s_need[i] = (int)need;
+      s_used[i] = (int)used;
+      s_first[i] = bad ? -1 : shared >> a.bs_log2;
     }
-    if (P != kWrite && r.flags != 0) flag_status(a.status, r.flags);
+    if (P != kWrite && flags != 0) flag_status(a.status, flags);
   }
   __syncthreads();
   // ---- blocks to take: before each request, and in all
   long long taken = 0, dropped = 0;  // dropped: those of requests before (kWrite)
+  long long all_dropped = 0;
   if constexpr (P == kInOne) {
     int done = 0;
 #pragma unroll 1
     for (int base = 0; base < nb; base += kThreads) {
       const int i = base + tid;
       int total;
-      const int x = i < nb ? __popc(s_bits[i]) : 0;
-      const int at = block_scan<kThreads>(x, s_warp, total);
+      const int at = block_scan<kThreads>(i < nb ? __popc(s_need[i]) : 0, s_warp, total);
       if (i < nb) s_before[i] = done + at;
       done += total;
     }
     taken = done;
     __syncthreads();
   }
-  long long before = 0, all_dropped = 0;
   if constexpr (P == kWrite) {
     long long t = 0, d = 0, ta = 0, da = 0;
 #pragma unroll 1
@@ -243,10 +247,13 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
       __syncthreads();
       return y;
     };
-    before = sum(t);
+    // (at most 2^20 blocks taken, 2^46 given back)
+    const long long before = sum(t << 32 | ta);
     dropped = sum(d);
-    taken = sum(ta);
     all_dropped = sum(da);
+    taken = before & 0xffffffffll;
+    if (tid == 0) s_before[0] = (int)(before >> 32);
+    __syncthreads();
   }
   const bool fits = P == kCount || taken <= held;
   // Places in the ring, less than num_blocks past these (a ring that does not fit is left).
@@ -256,22 +263,18 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   if (P != kCount && !fits && tid == 0 && blockIdx.x == 0)
     flag_status(a.status, PA_DEV_NO_BLOCKS);
   // ---- the columns
-  const int items = nb * a.M;  // (one CTA: few; one request: M)
-  long long put = dropped;     // blocks given back so far
-  int mine = 0;                // (kCount)
+  const int items = nb * M;  // (one CTA: few; one request: M)
+  long long put = dropped;   // blocks given back so far
+  int mine = 0;              // (kCount)
 #pragma unroll 1
   for (int base = 0; base < items; base += kThreads) {
-    const int i = base + tid, q = i / a.M, col = i - q * a.M;
+    const int i = base + tid, q = P == kInOne ? i / M : 0, col = i - q * M;
+    const int32_t* at_col = tab + (size_t)q * W * M + col;
     Column<WM> c;
-    c.held = c.used = c.drop = 0;
-    Rows r = {b0 + q, 0, 0, 0, true};
-    if (i < items) {
-      r.bad = s_bad[q];
-      r.need = s_bits[q];
-      r.before = P == kInOne ? s_before[q] : (int)before;
-      r.first = a.shared_lens != nullptr && !r.bad ? a.shared_lens[r.b] >> a.bs_log2 : 0;
-      if (!r.bad && fits) c.read(a, r, col, s_had + q * W, s_parent + q * W);
-    }
+    c.drop = 0;
+    const int first = i < items ? s_first[q] : -1;
+    if (first >= 0 && fits)
+      c.look(a, at_col, col, s_had + q * W, (uint32_t)s_used[q], first);
     if constexpr (P == kCount) {
       mine += __popc(c.drop);
       continue;
@@ -280,46 +283,45 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
     long long at = put + block_scan<kThreads>(__popc(c.drop), s_warp, total);
     put += total;
     if (i >= items) continue;
-    const size_t row0 = (size_t)r.b * W * a.M + col;
 #pragma unroll 1
     for (uint32_t left = c.drop; left != 0; left &= left - 1, ++at) {
       // (a ring that would hold more than there are: its state was wrong)
       if (held + at < NB) {
         unsigned to = tail0 + (unsigned)at;
         if (to >= NB) to -= NB;
-        a.ring[to] = a.block_tables[row0 + (size_t)(__ffs(left) - 1) * a.M];
+        a.ring[to] = at_col[(size_t)(__ffs(left) - 1) * M];
       } else {
         flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
       }
     }
-    if (r.bad || !fits) {
+    int32_t* out = a.tables_out + ((size_t)(b0 + q) * W) * M + col;
+    if (first < 0 || !fits) {
       if (a.tables_out != a.block_tables)
 #pragma unroll 1
-        for (int w = 0; w < W; ++w)
-          a.tables_out[row0 + (size_t)w * a.M] = a.block_tables[row0 + (size_t)w * a.M];
+        for (int w = 0; w < W; ++w) out[(size_t)w * M] = at_col[(size_t)w * M];
       continue;
     }
     int now[WM];
 #pragma unroll
     for (int w = 0; w < WM; ++w) {
       now[w] = -1;
-      if (w < W && col < s_has[q * W + w])
-        now[w] = a.block_tables[row0 + (size_t)s_parent[q * W + w] * a.M];
+      if (w < W && col < s_has[q * W + w]) now[w] = at_col[(size_t)s_parent[q * W + w] * M];
     }
 #pragma unroll
     for (int w = 0; w < WM; ++w)
-      if (w < W) a.tables_out[row0 + (size_t)w * a.M] = now[w];
+      if (w < W) out[(size_t)w * M] = now[w];
+    const uint32_t need = (uint32_t)s_need[q];
 #pragma unroll 1
-    for (uint32_t left = r.need; left != 0; left &= left - 1) {
+    for (uint32_t left = need; left != 0; left &= left - 1) {
       const int w = __ffs(left) - 1;
       if (col != s_has[q * W + w] - 1) continue;
-      unsigned from = head0 + (unsigned)(r.before + __popc(r.need & ((1u << w) - 1)));
-      if (from >= NB) from -= NB;
-      const int id = a.ring[from];
+      unsigned from_at = head0 + (unsigned)(s_before[q] + __popc(need & ((1u << w) - 1)));
+      if (from_at >= NB) from_at -= NB;
+      const int id = a.ring[from_at];
       const bool ok = id >= 0 && id < a.num_blocks;
       if (!ok) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
-      a.tables_out[row0 + (size_t)w * a.M] = ok ? id : -1;
-      int64_t* pair = a.pairs + 2 * ((size_t)r.b * W + w);
+      out[(size_t)w * M] = ok ? id : -1;
+      int64_t* pair = a.pairs + 2 * ((size_t)(b0 + q) * W + w);
       pair[0] = ok ? s_tail[q * W + w] : 0;
       pair[1] = ok ? id : 0;
     }
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
     int total;
     block_scan<kThreads>(mine, s_warp, total);
     if (tid == 0) {
-      a.counts[2 * b0] = __popc(s_bits[0]);
+      a.counts[2 * b0] = __popc(s_need[0]);
       a.counts[2 * b0 + 1] = total;
       if (b0 == 0) {
         a.counts[2 * a.B] = head;
@@ -338,20 +340,15 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   } else {
     // ---- the pairs of beams that need no copy, and the lengths
 #pragma unroll 1
-    for (int i = tid; i < nb * W; i += kThreads) {
-      const int q = i / W, w = i - q * W;
-      const size_t o = (size_t)b0 * W + i;
-      const bool moved = fits && !s_bad[q];
-      if (!moved || !(s_bits[q] >> w & 1)) a.pairs[2 * o] = a.pairs[2 * o + 1] = 0;
-    }
-    // (in place: a parent's length is read by the warp that replaces it)
-#pragma unroll 1
     for (int i = warp; i < nb; i += kThreads / 32) {
       const size_t o = (size_t)(b0 + i) * W + lane;
-      const int l = lane < W ? a.context_lens[o] : 0;
-      const int p = lane < W ? s_parent[i * W + lane] : lane;
-      const int from = __shfl_sync(kAll, l, p >= 0 ? p : lane);
-      if (lane < W) a.lens_out[o] = !fits || s_bad[i] ? l : p >= 0 ? from : 0;
+      const bool here = lane < W, moved = fits && s_first[i] >= 0;
+      const int l = here ? a.context_lens[o] : 0;  // (in place: all of a request's first)
+      const int p = here ? s_parent[i * W + lane] : lane;
+      const int l_src = __shfl_sync(kAll, l, p >= 0 ? p : lane);
+      if (!here) continue;
+      a.lens_out[o] = !moved ? l : p >= 0 ? l_src : 0;
+      if (!moved || !((uint32_t)s_need[i] >> lane & 1)) a.pairs[2 * o] = a.pairs[2 * o + 1] = 0;
     }
     if (tid == 0 && blockIdx.x == 0) {
       const long long gave = P == kInOne ? put : all_dropped;
@@ -362,8 +359,11 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   }
 }
 
+constexpr int kStageBytes = 160 * 1024;  // rows that are brought to shared memory
+
 template <int WM>
 cudaError_t launch_reorder_t(const BeamReorderArgs& a, cudaStream_t stream) {
+  constexpr int kMost = 224 * 1024;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -375,26 +375,28 @@ cudaError_t launch_reorder_t(const BeamReorderArgs& a, cudaStream_t stream) {
     constexpr auto kern = beam_reorder_kernel<WM, kInOne, 1024>;
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(1024);
-    cfg.dynamicSmemBytes = 16 * a.B * a.W;
-    if (cfg.dynamicSmemBytes > 32 * 1024) {
-      const cudaError_t e = ensure_dynamic_smem<kern>(200 * 1024);
-      if (e != cudaSuccess) return e;
-    }
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    cfg.dynamicSmemBytes = reorder_bytes(a.B, a.W, a.M, true);
+    const cudaError_t e = ensure_dynamic_smem<kern>(kMost);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kern, a, true);
   }
   constexpr int kThreads = 256;
+  const bool staged = (long long)a.W * a.M * 4 <= kStageBytes;
+  constexpr auto count = beam_reorder_kernel<WM, kCount, kThreads>;
+  constexpr auto write = beam_reorder_kernel<WM, kWrite, kThreads>;
   cfg.gridDim = dim3(a.B);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 16 * a.W;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, beam_reorder_kernel<WM, kCount, kThreads>, a);
-  if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, beam_reorder_kernel<WM, kWrite, kThreads>, a);
+  cfg.dynamicSmemBytes = reorder_bytes(1, a.W, a.M, staged);
+  cudaError_t e = ensure_dynamic_smem<count>(kMost);
+  if (e == cudaSuccess) e = ensure_dynamic_smem<write>(kMost);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, count, a, staged);
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, write, a, staged);
 }
 
 // ---------------------------------------------------------------- backtrack
-constexpr int kBackThreads = 512;
+constexpr int kBackThreads = 1024;
 constexpr int kPiece = 32;              // steps of a piece
 constexpr int kBackBytes = 160 * 1024;  // parents and beams of the steps held at a time
+constexpr int kBatch = 8;               // loads of a thread in flight
 constexpr uint8_t kOff = 255;           // a parent that is none of the beams
 
 __global__ void __launch_bounds__(kBackThreads)
@@ -427,19 +429,31 @@ __global__ void __launch_bounds__(kBackThreads)
   __syncthreads();
   const size_t plane = (size_t)a.B * W;
   int32_t* out = a.out + (size_t)b * K * a.S;
+  const int behind = a.S - s_most;
 #pragma unroll 1
-  for (int i = tid; i < K * (a.S - s_most); i += kBackThreads) {  // behind all of them
-    const int k = i / (a.S - s_most);
-    out[(size_t)k * a.S + s_most + (i - k * (a.S - s_most))] = a.pad;
+  for (int i = tid; i < K * behind; i += kBackThreads) {
+    const int k = i / behind;
+    out[(size_t)k * a.S + s_most + (i - k * behind)] = a.pad;
   }
+  // (a thread's parents: of one beam, every `rows`-th step)
+  const int rows = kBackThreads / W, my_s = tid / W, my_w = tid - my_s * W;
+#pragma unroll 1
   for (int hi = s_most; hi > 0; hi -= steps) {  // steps lo .. hi - 1
     const int lo = hi > steps ? hi - steps : 0, n = hi - lo;
     const int np = (n + kPiece - 1) / kPiece;
-#pragma unroll 4
-    for (int i = tid; i < n * W; i += kBackThreads) {
-      const int s = i / W, w = i - s * W;
-      const int p = a.parents[(size_t)(lo + s) * plane + (size_t)b * W + w];
-      s_parent[i] = p >= 0 && p < W ? (uint8_t)p : kOff;
+    if (my_s < rows) {
+      const int32_t* from = a.parents + (size_t)lo * plane + (size_t)b * W + my_w;
+#pragma unroll 1
+      for (int s = my_s; s < n; s += kBatch * rows) {
+        int p[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          p[j] = s + j * rows < n ? from[(size_t)(s + j * rows) * plane] : -1;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (s + j * rows < n)
+            s_parent[(s + j * rows) * W + my_w] = p[j] >= 0 && p[j] < W ? (uint8_t)p[j] : kOff;
+      }
     }
     __syncthreads();
     // the beam below each piece, from each of its last step's
@@ -486,11 +500,22 @@ __global__ void __launch_bounds__(kBackThreads)
       }
     }
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < K * n; i += kBackThreads) {
-      const int k = i / n, s = i - k * n, w = s_beam[(size_t)k * steps + s];
-      out[(size_t)k * a.S + lo + s] =
-          w != kOff ? a.tokens[(size_t)(lo + s) * plane + (size_t)b * W + w] : a.pad;
+#pragma unroll 1
+    for (int i0 = tid; i0 < K * n; i0 += kBatch * kBackThreads) {
+      int token[kBatch], at[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * kBackThreads;
+        if (i < K * n) {
+          const int k = i / n, s = i - k * n, w = s_beam[(size_t)k * steps + s];
+          at[j] = k * a.S + lo + s;
+          token[j] =
+              w != kOff ? a.tokens[(size_t)(lo + s) * plane + (size_t)b * W + w] : a.pad;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i0 + j * kBackThreads < K * n) out[at[j]] = token[j];
     }
     __syncthreads();
   }
@@ -500,7 +525,7 @@ __global__ void __launch_bounds__(kBackThreads)
 
 // One CTA or one to a request: its rounds over 1,024 columns against a second launch.
 bool beam_reorder_in_one(int B, int W, int M) {
-  return B <= kMaxInOne && (long long)B * W <= 8192 && (long long)B * M <= 4096;
+  return B <= kMaxInOne && (long long)B * M <= 4096 && (long long)B * W * M * 4 <= kStageBytes;
 }
 
 cudaError_t launch_beam_reorder(const BeamReorderArgs& a, cudaStream_t stream) {
