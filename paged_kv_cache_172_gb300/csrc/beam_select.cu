@@ -26,7 +26,6 @@
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
-#include <string.h>
 
 #include <type_traits>
 
@@ -304,23 +303,6 @@ __device__ __forceinline__ double log_of(float x) {
   return e * 0.69314718055994531 + (double)logf(f);
 }
 
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Stores 8 bytes to shared memory of the cluster's first CTA.
-template <typename X>
-__device__ __forceinline__ void store_first(X* p, X x) {
-  static_assert(sizeof(X) == 8, "one store");
-  uint32_t at;
-  unsigned long long y;
-  memcpy(&y, &x, 8);
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(p)));
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(y) : "memory");
-}
-
 // a / b, rounded down, of small numbers, b > 0 (the quotient's error is far below 0.5 / b).
 __device__ __forceinline__ int small_div(int a, int b) {
   return (int)__fdividef((float)a + 0.5f, (float)b);
@@ -381,8 +363,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamS
     const Key mine = scan<T, VEC>(x, begin, end, a.eos, W, s_dyn + warp * kRing, known,
                                   warp - first, ml);
     if (ranks > 1) cluster_wait();
-    if (lane < W) store_first(keys + task * W + lane, mine);
-    if (lane == 0) store_first(mls + task, ml);
+    if (lane < W) store_cluster(keys + task * W + lane, 0, mine);
+    if (lane == 0) store_cluster(mls + task, 0, ml);
   } else if (ranks > 1) {
     cluster_wait();
   }

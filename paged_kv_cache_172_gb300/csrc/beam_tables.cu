@@ -9,15 +9,16 @@
 // none holds there any more goes back to the ring.  Requests in order, in each one the
 // rows' columns in order, in each one the beams: equal inputs give equal tables.
 //
-// A CTA brings its requests' rows to shared memory while it reads parents and lengths
-// (rows that do not fit stay where they are); then every thread takes a column of a
-// request, looks at its W entries and writes the new ones, so that a table may be its own
-// output.  What a request needs and gives back has to be known before, for the places in
-// the ring.  Few entries: one CTA takes all requests and its scan over the columns carries
-// the places along.  Many: one CTA to a request counts, a second launch adds up the counts
-// before its request and writes.
+// A CTA brings its requests' rows to shared memory while it reads parents and lengths, so
+// that a table may be its own output.  Its threads look at a column each for the blocks
+// that go back, and its warps write a new row each.  What a request needs and gives back
+// has to be known before, for the places in the ring: a small batch is one cluster, whose
+// CTAs share out the requests and tell each other their numbers; a larger one takes a CTA
+// to a request and two launches, the first to count, the second to add up the counts
+// before its request and write.  Rows that do not fit shared memory are read where they
+// are, and written by column, every entry of which a thread then holds.
 //
-// Bound: the launches, and the one trip to memory that parents, lengths and entries share.
+// Bound: the launches, and the trips to memory (entries, then the ring).
 //
 // Backtrack.  Tokens of hypothesis k: beam(n - 1) = beams[k], token(s) = tokens[s][beam(s)],
 // beam(s - 1) = parents[s][beam(s)].  A walk of S steps is a chain of S loads, so each
@@ -37,47 +38,38 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 
 // ---------------------------------------------------------------- reorder
-// A column of a request: the entries of its beams there.
+// The beams of a request whose entry at a column goes back: those that are no beam's
+// parent, hold one there that no parent holds, and no earlier one of them.  at: the column
+// in the request's first row; had: blocks of the old rows; parents: the beams that are one.
 template <int WM>
-struct Column {
-  uint32_t held, used;  // beams that hold an entry here; of those, the parents of one
-  uint32_t drop;        // beams whose entry goes back
-
-  // at: the column in the request's first row; had: blocks of the old rows; parents: the
-  // beams that are a parent.
-  __device__ __forceinline__ void look(const BeamReorderArgs& a, const int32_t* at, int col,
-                                       const int* had, uint32_t parents, int first) {
-    const int W = a.W;
-    held = drop = 0;
-    int old[WM];
+__device__ __forceinline__ uint32_t given_back(const BeamReorderArgs& a, const int32_t* at,
+                                               int col, const int* had, uint32_t parents) {
+  const int W = a.W;
+  uint32_t held = 0, drop = 0;
+  int old[WM];
 #pragma unroll
-    for (int w = 0; w < WM; ++w) {
-      old[w] = -1;
-      if (w < W && col < had[w]) {
-        old[w] = at[(size_t)w * a.M];
-        held |= 1u << w;
-      }
-    }
-    used = held & parents;
-    if (col < first || used == held) return;
-#pragma unroll 1
-    for (uint32_t left = held & ~used; left != 0; left &= left - 1) {
-      const int w = __ffs(left) - 1, id = at[(size_t)w * a.M];
-      // held by a parent, or given back by an earlier beam
-      const uint32_t others = used | (held & ((1u << w) - 1));
-      bool keep = false;
-#pragma unroll
-      for (int u = 0; u < WM; ++u) keep |= (others >> u & 1) && old[u] == id;
-      if (keep) continue;
-      if (id >= 0 && id < a.num_blocks)
-        drop |= 1u << w;
-      else
-        flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+  for (int w = 0; w < WM; ++w) {
+    old[w] = -1;
+    if (w < W && col < had[w]) {
+      old[w] = at[(size_t)w * a.M];
+      held |= 1u << w;
     }
   }
-};
-
-constexpr int kMaxInOne = 256;  // requests of the launch by one CTA
+#pragma unroll 1
+  for (uint32_t left = held & ~parents; left != 0; left &= left - 1) {
+    const int w = __ffs(left) - 1, id = at[(size_t)w * a.M];
+    const uint32_t others = (held & parents) | (held & ((1u << w) - 1));
+    bool keep = false;
+#pragma unroll
+    for (int u = 0; u < WM; ++u) keep |= (others >> u & 1) && old[u] == id;
+    if (keep) continue;
+    if (id >= 0 && id < a.num_blocks)
+      drop |= 1u << w;
+    else
+      flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+  }
+  return drop;
+}
 
 // Blocks in the ring; -1 for a state that no ring of this size can have.
 __device__ __forceinline__ long long blocks_held(long long head, long long tail, int NB) {
@@ -106,42 +98,50 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int& total) {
   return (warp > 0 ? before : 0) + y - x;
 }
 
-enum Pass { kInOne, kCount, kWrite };
+constexpr int kThreads = 512;
+constexpr int kMaxRanks = 8;              // CTAs of a small batch
+constexpr int kRounds = 2;                // columns of a thread there
+constexpr int kStageBytes = 160 * 1024;   // rows that are brought to shared memory
 
-// A CTA's shared memory: its requests' rows (staged), then for each beam its parent, its
-// old and its new blocks and the last one where it is to be copied, and for each request
-// the beams that need a copy, the blocks taken before it, the beams that are a parent and
-// its first column of its own (-1: a request that stays as it is).
+enum Pass { kCluster, kCount, kWrite };
+
+// A CTA's shared memory: its requests' rows (STAGED), then for each beam its parent, its
+// old and its new blocks, its new length and the last block where it is to be copied, and
+// for each request the beams that need a copy, the blocks taken before it, the beams that
+// are a parent and its first column of its own (-1: a request that stays as it is).
 int reorder_bytes(int nb, int W, int M, bool staged) {
-  return (staged ? nb * W * M * 4 : 0) + nb * W * 16 + nb * 16;
+  return (staged ? nb * W * M * 4 : 0) + nb * W * 20 + nb * 16;
 }
 
-template <int WM, Pass P, int kThreads>
-__global__ void __launch_bounds__(kThreads)
-    beam_reorder_kernel(const BeamReorderArgs a, bool staged) {
+template <int WM, Pass P, bool STAGED>
+__global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorderArgs a) {
   extern __shared__ __align__(16) int s_dyn[];
   __shared__ int s_warp[kThreads / 32];
   __shared__ long long s_sum[kThreads / 32];
+  __shared__ int2 s_rank[kMaxRanks];  // blocks that a CTA's requests take and give back
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = a.W, M = a.M, bs = 1 << a.bs_log2;
-  const int b0 = P == kInOne ? 0 : blockIdx.x, nb = P == kInOne ? a.B : 1;
+  const int rank = blockIdx.x, ranks = gridDim.x;
+  const int b0 = P == kCluster ? rank * a.B / ranks : rank;
+  const int nb = P == kCluster ? (rank + 1) * a.B / ranks - b0 : 1;
   int* s_tab = s_dyn;
-  int* s_parent = s_tab + (staged ? nb * W * M : 0);  // [nb][W]
+  int* s_parent = s_tab + (STAGED ? nb * W * M : 0);  // [nb][W]
   int* s_had = s_parent + nb * W;
   int* s_has = s_had + nb * W;
-  int* s_tail = s_has + nb * W;
+  int* s_len = s_has + nb * W;
+  int* s_tail = s_len + nb * W;
   int* s_need = s_tail + nb * W;  // [nb]
   int* s_before = s_need + nb;
   int* s_used = s_before + nb;
   int* s_first = s_used + nb;
+  if (P == kCluster) cluster_arrive();  // (nobody stores to a CTA that has not begun)
   pdl_wait();
   pdl_launch_dependents();
   // ---- everything from memory at once
   const int32_t* from = a.block_tables + (size_t)b0 * W * M;
-  if (staged) {
+  if (STAGED) {
     const int n = nb * W * M;
-    const bool wide = (reinterpret_cast<uintptr_t>(from) & 15) == 0;
-    const int n4 = wide ? n / 4 : 0;
+    const int n4 = (reinterpret_cast<uintptr_t>(from) & 15) == 0 ? n / 4 : 0;
 #pragma unroll 4
     for (int i = tid; i < n4; i += kThreads)
       reinterpret_cast<int4*>(s_tab)[i] = reinterpret_cast<const int4*>(from)[i];
@@ -159,9 +159,22 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll 1
   for (int i = tid; i < nb; i += kThreads)
     s_first[i] = a.shared_lens != nullptr ? a.shared_lens[b0 + i] : 0;
+  long long t = 0, d = 0, ta = 0, da = 0;  // kWrite: before this request and in all
+  if (P == kWrite) {
+#pragma unroll 1
+    for (int b = tid; b < a.B; b += kThreads) {
+      const long long x = a.counts[2 * b], y = a.counts[2 * b + 1];
+      ta += x;
+      da += y;
+      if (b < b0) {
+        t += x;
+        d += y;
+      }
+    }
+  }
   __syncthreads();
   const long long held = blocks_held(head, tail, a.num_blocks);
-  const int32_t* tab = staged ? s_tab : from;
+  const int32_t* tab = STAGED ? s_tab : from;
   // ---- the requests, a warp to each, a lane to a beam
 #pragma unroll 1
   for (int i = warp; i < nb; i += kThreads / 32) {
@@ -174,7 +187,7 @@ __global__ void __launch_bounds__(kThreads)
     const bool bad = __any_sync(kAll, flags != 0);
     const int src = p >= 0 && p < W ? p : lane;
     const int l_src = __shfl_sync(kAll, l, src);
-    const int len = p >= 0 ? l_src : 0;
+    const int len = bad ? l : p >= 0 ? l_src : 0;
     const int had = bad ? 0 : (int)(((long long)l + bs - 1) >> a.bs_log2);
     const int has = bad ? 0 : (int)(((long long)len + bs - 1) >> a.bs_log2);
     int col = -1, id = -1;  // of the last block, half full and an entry of the pool
@@ -185,19 +198,17 @@ __global__ void __launch_bounds__(kThreads)
       else
         flags |= PA_DEV_BAD_BLOCK_ID;
     }
-    bool again = false;  // an earlier beam holds it as its last block
-#pragma unroll 1
-    for (int u = 0; u < W; ++u) {
-      const int ucol = __shfl_sync(kAll, col, u), uid = __shfl_sync(kAll, id, u);
-      again |= u < lane && ucol >= 0 && ucol == col && uid == id;
-    }
-    const uint32_t need = __ballot_sync(kAll, again);
+    // An earlier beam holds it as its last block.
+    const unsigned same =
+        __match_any_sync(kAll, (unsigned long long)(unsigned)col << 32 | (unsigned)id);
+    const uint32_t need =
+        __ballot_sync(kAll, col >= 0 && (same & ((1u << lane) - 1)) != 0);
     const uint32_t used = __reduce_or_sync(kAll, here && p >= 0 && !bad ? 1u << p : 0u);
-    __syncwarp();
     if (here) {
       s_parent[i * W + lane] = bad ? lane : p;
       s_had[i * W + lane] = had;
       s_has[i * W + lane] = has;
+      s_len[i * W + lane] = len;
       s_tail[i * W + lane] = id;
     }
     if (lane == 0) {
@@ -208,123 +219,72 @@ __global__ void __launch_bounds__(kThreads)
     if (P != kWrite && flags != 0) flag_status(a.status, flags);
   }
   __syncthreads();
-  // ---- blocks to take: before each request, and in all
-  long long taken = 0, dropped = 0;  // dropped: those of requests before (kWrite)
-  long long all_dropped = 0;
-  if constexpr (P == kInOne) {
-    int done = 0;
-#pragma unroll 1
-    for (int base = 0; base < nb; base += kThreads) {
-      const int i = base + tid;
-      int total;
-      const int at = block_scan<kThreads>(i < nb ? __popc(s_need[i]) : 0, s_warp, total);
-      if (i < nb) s_before[i] = done + at;
-      done += total;
+  // ---- the blocks that go back, a thread to a column
+  const int items = nb * M;
+  auto column = [&](int i, int& q, int& col) {  // item i: a column of request q
+    q = P == kCluster ? i / M : 0;
+    col = i - q * M;
+  };
+  auto drops = [&](int i) -> uint32_t {
+    if (i >= items) return 0u;
+    int q, col;
+    column(i, q, col);
+    const int first = s_first[q];
+    const uint32_t used = (uint32_t)s_used[q];
+    if (first < 0 || col < first || used == (1u << (W - 1) << 1) - 1) return 0u;
+    return given_back<WM>(a, tab + (size_t)q * W * M + col, col, s_had + q * W, used);
+  };
+  uint32_t drop[kRounds];  // (kCluster)
+  int mine = 0;
+  if constexpr (P == kCluster) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      drop[r] = drops(r * kThreads + tid);
+      mine += __popc(drop[r]);
     }
-    taken = done;
-    __syncthreads();
   }
-  if constexpr (P == kWrite) {
-    long long t = 0, d = 0, ta = 0, da = 0;
+  if constexpr (P == kCount) {
 #pragma unroll 1
-    for (int b = tid; b < a.B; b += kThreads) {
-      const long long x = a.counts[2 * b], y = a.counts[2 * b + 1];
-      ta += x;
-      da += y;
-      if (b < b0) {
-        t += x;
-        d += y;
+    for (int i = tid; i < items; i += kThreads) mine += __popc(drops(i));
+  }
+  // ---- what is taken and given back before this CTA's requests, and in all
+  long long taken = 0, dropped = 0, all_dropped = 0;
+  if constexpr (P == kCluster) {
+    int total, needs = 0;
+    block_scan<kThreads>(mine, s_warp, total);
+    if (warp == 0) {
+#pragma unroll 1
+      for (int base = 0; base < nb; base += 32) {
+        const int i = base + lane, x = i < nb ? __popc(s_need[i]) : 0;
+        int y = x;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const int z = __shfl_up_sync(kAll, y, k);
+          if (lane >= k) y += z;
+        }
+        if (i < nb) s_before[i] = needs + y - x;
+        needs += __shfl_sync(kAll, y, 31);
       }
     }
-    auto sum = [&](long long x) {
-#pragma unroll
-      for (int k = 16; k >= 1; k >>= 1) x += __shfl_xor_sync(kAll, x, k);
-      if (lane == 0) s_sum[warp] = x;
-      __syncthreads();
-      long long y = 0;
+    cluster_wait();
+    if (warp == 0 && lane < ranks) store_cluster(&s_rank[rank], lane, make_int2(needs, total));
+    cluster_arrive();
+    cluster_wait();
+    int before = 0;
 #pragma unroll 1
-      for (int w = 0; w < kThreads / 32; ++w) y += s_sum[w];
-      __syncthreads();
-      return y;
-    };
-    // (at most 2^20 blocks taken, 2^46 given back)
-    const long long before = sum(t << 32 | ta);
-    dropped = sum(d);
-    all_dropped = sum(da);
-    taken = before & 0xffffffffll;
-    if (tid == 0) s_before[0] = (int)(before >> 32);
-    __syncthreads();
-  }
-  const bool fits = P == kCount || taken <= held;
-  // Places in the ring, less than num_blocks past these (a ring that does not fit is left).
-  const unsigned NB = (unsigned)a.num_blocks;
-  const unsigned head0 = fits && held >= 0 ? (unsigned)((unsigned long long)head % NB) : 0;
-  const unsigned tail0 = fits && held >= 0 ? (unsigned)((unsigned long long)tail % NB) : 0;
-  if (P != kCount && !fits && tid == 0 && blockIdx.x == 0)
-    flag_status(a.status, PA_DEV_NO_BLOCKS);
-  // ---- the columns
-  const int items = nb * M;  // (one CTA: few; one request: M)
-  long long put = dropped;   // blocks given back so far
-  int mine = 0;              // (kCount)
-#pragma unroll 1
-  for (int base = 0; base < items; base += kThreads) {
-    const int i = base + tid, q = P == kInOne ? i / M : 0, col = i - q * M;
-    const int32_t* at_col = tab + (size_t)q * W * M + col;
-    Column<WM> c;
-    c.drop = 0;
-    const int first = i < items ? s_first[q] : -1;
-    if (first >= 0 && fits)
-      c.look(a, at_col, col, s_had + q * W, (uint32_t)s_used[q], first);
-    if constexpr (P == kCount) {
-      mine += __popc(c.drop);
-      continue;
-    }
-    int total;
-    long long at = put + block_scan<kThreads>(__popc(c.drop), s_warp, total);
-    put += total;
-    if (i >= items) continue;
-#pragma unroll 1
-    for (uint32_t left = c.drop; left != 0; left &= left - 1, ++at) {
-      // (a ring that would hold more than there are: its state was wrong)
-      if (held + at < NB) {
-        unsigned to = tail0 + (unsigned)at;
-        if (to >= NB) to -= NB;
-        a.ring[to] = at_col[(size_t)(__ffs(left) - 1) * M];
-      } else {
-        flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+    for (int r = 0; r < ranks; ++r) {
+      const int2 x = s_rank[r];
+      taken += x.x;
+      all_dropped += x.y;
+      if (r < rank) {
+        before += x.x;
+        dropped += x.y;
       }
     }
-    int32_t* out = a.tables_out + ((size_t)(b0 + q) * W) * M + col;
-    if (first < 0 || !fits) {
-      if (a.tables_out != a.block_tables)
+    __syncthreads();
 #pragma unroll 1
-        for (int w = 0; w < W; ++w) out[(size_t)w * M] = at_col[(size_t)w * M];
-      continue;
-    }
-    int now[WM];
-#pragma unroll
-    for (int w = 0; w < WM; ++w) {
-      now[w] = -1;
-      if (w < W && col < s_has[q * W + w]) now[w] = at_col[(size_t)s_parent[q * W + w] * M];
-    }
-#pragma unroll
-    for (int w = 0; w < WM; ++w)
-      if (w < W) out[(size_t)w * M] = now[w];
-    const uint32_t need = (uint32_t)s_need[q];
-#pragma unroll 1
-    for (uint32_t left = need; left != 0; left &= left - 1) {
-      const int w = __ffs(left) - 1;
-      if (col != s_has[q * W + w] - 1) continue;
-      unsigned from_at = head0 + (unsigned)(s_before[q] + __popc(need & ((1u << w) - 1)));
-      if (from_at >= NB) from_at -= NB;
-      const int id = a.ring[from_at];
-      const bool ok = id >= 0 && id < a.num_blocks;
-      if (!ok) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
-      out[(size_t)w * M] = ok ? id : -1;
-      int64_t* pair = a.pairs + 2 * ((size_t)(b0 + q) * W + w);
-      pair[0] = ok ? s_tail[q * W + w] : 0;
-      pair[1] = ok ? id : 0;
-    }
+    for (int i = tid; i < nb; i += kThreads) s_before[i] += before;
+    __syncthreads();
   }
   if constexpr (P == kCount) {
     int total;
@@ -337,59 +297,160 @@ __global__ void __launch_bounds__(kThreads)
         a.counts[2 * a.B + 1] = tail;
       }
     }
-  } else {
-    // ---- the pairs of beams that need no copy, and the lengths
+    return;
+  }
+  if constexpr (P == kWrite) {
+    auto sum = [&](long long x) {
+#pragma unroll
+      for (int k = 16; k >= 1; k >>= 1) x += __shfl_xor_sync(kAll, x, k);
+      if (lane == 0) s_sum[warp] = x;
+      __syncthreads();
+      long long y = 0;
 #pragma unroll 1
-    for (int i = warp; i < nb; i += kThreads / 32) {
-      const size_t o = (size_t)(b0 + i) * W + lane;
-      const bool here = lane < W, moved = fits && s_first[i] >= 0;
-      const int l = here ? a.context_lens[o] : 0;  // (in place: all of a request's first)
-      const int p = here ? s_parent[i * W + lane] : lane;
-      const int l_src = __shfl_sync(kAll, l, p >= 0 ? p : lane);
-      if (!here) continue;
-      a.lens_out[o] = !moved ? l : p >= 0 ? l_src : 0;
-      if (!moved || !((uint32_t)s_need[i] >> lane & 1)) a.pairs[2 * o] = a.pairs[2 * o + 1] = 0;
+      for (int w = 0; w < kThreads / 32; ++w) y += s_sum[w];
+      __syncthreads();
+      return y;
+    };
+    const long long takes = sum(t << 32 | ta);  // (at most 2^20 each)
+    dropped = sum(d);
+    all_dropped = sum(da);
+    taken = takes & 0xffffffffll;
+    if (tid == 0) s_before[0] = (int)(takes >> 32);
+    __syncthreads();
+  }
+  const bool fits = taken <= held;
+  // Places in the ring, less than num_blocks past these (a ring that does not fit is left).
+  const unsigned NB = (unsigned)a.num_blocks;
+  const unsigned head0 = fits ? (unsigned)((unsigned long long)head % NB) : 0;
+  const unsigned tail0 = fits ? (unsigned)((unsigned long long)tail % NB) : 0;
+  if (rank == 0 && tid == 0) {
+    if (!fits) flag_status(a.status, PA_DEV_NO_BLOCKS);
+    const long long room = a.num_blocks - held;
+    a.free_state_out[0] = head + (fits ? taken : 0);
+    a.free_state_out[1] = tail + (!fits ? 0 : all_dropped < room ? all_dropped : room);
+  }
+  // ---- the ring
+  if (fits) {
+    long long put = dropped;
+#pragma unroll
+    for (int r = 0; r < (P == kCluster ? kRounds : 1); ++r) {
+#pragma unroll 1
+      for (int base = r * kThreads; base < items; base += kThreads) {
+        const int i = base + tid;
+        uint32_t left = P == kCluster ? drop[r] : drops(i);
+        int total, q, col;
+        long long at = put + block_scan<kThreads>(__popc(left), s_warp, total);
+        put += total;
+        column(i, q, col);
+#pragma unroll 1
+        for (; left != 0; left &= left - 1, ++at) {
+          // (a ring that would hold more than there are: its state was wrong)
+          if (held + at < NB) {
+            unsigned to = tail0 + (unsigned)at;
+            if (to >= NB) to -= NB;
+            a.ring[to] = tab[((size_t)q * W + __ffs(left) - 1) * M + col];
+          } else {
+            flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+          }
+        }
+        if (P == kCluster) break;
+      }
     }
-    if (tid == 0 && blockIdx.x == 0) {
-      const long long gave = P == kInOne ? put : all_dropped;
-      const long long room = a.num_blocks - held;
-      a.free_state_out[0] = head + (fits ? taken : 0);
-      a.free_state_out[1] = tail + (!fits ? 0 : gave < room ? gave : room);
+  }
+  // A fresh block for beam w of a request, -1 where the ring's entry is none; its pair.
+  auto fresh = [&](int q, int w) {
+    const uint32_t need = (uint32_t)s_need[q];
+    unsigned at = head0 + (unsigned)(s_before[q] + __popc(need & ((1u << w) - 1)));
+    if (at >= NB) at -= NB;
+    const int id = a.ring[at];
+    return id >= 0 && id < a.num_blocks ? id : -1;
+  };
+  // ---- rows (by warp), lengths and pairs
+#pragma unroll 1
+  for (int i = warp; i < nb * W; i += kThreads / 32) {
+    const int q = P == kCluster ? i / W : 0, w = i - q * W;
+    const size_t o = (size_t)b0 * W + i;
+    const bool moves = fits && s_first[q] >= 0;
+    int id = -2;  // of a last block that is new
+    if (moves && ((uint32_t)s_need[q] >> w & 1)) id = fresh(q, w);
+    if (lane == 0) {
+      // (what was not moved keeps the length that it came with; of one that was, s_len's)
+      a.lens_out[o] = moves || s_first[q] < 0 ? s_len[i] : a.context_lens[o];
+      a.pairs[2 * o] = id >= 0 ? s_tail[i] : 0;
+      a.pairs[2 * o + 1] = id >= 0 ? id : 0;
+      if (id == -1) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+    }
+    if (!STAGED || (!moves && a.tables_out == a.block_tables)) continue;
+    const int has = moves ? s_has[i] : M, p = moves ? s_parent[i] : w;
+    const int32_t* src = tab + (q * W + (p >= 0 ? p : 0)) * M;
+    int32_t* out = a.tables_out + o * M;
+#pragma unroll 4
+    for (int col = lane; col < M; col += 32)
+      out[col] = col < has ? (id != -2 && col == has - 1 ? id : src[col]) : -1;
+  }
+  // ---- rows that were not staged, a thread to a column
+  if constexpr (!STAGED) {
+    const bool moves = fits && s_first[0] >= 0;
+    if (!moves && a.tables_out == a.block_tables) return;
+    const uint32_t need = moves ? (uint32_t)s_need[0] : 0u;
+#pragma unroll 1
+    for (int col = tid; col < M; col += kThreads) {
+      int now[WM];
+#pragma unroll
+      for (int w = 0; w < WM; ++w) {
+        now[w] = -1;
+        if (w < W && (!moves || col < s_has[w]))
+          now[w] = tab[(size_t)(moves ? s_parent[w] : w) * M + col];
+      }
+      int32_t* out = a.tables_out + (size_t)b0 * W * M + col;
+#pragma unroll
+      for (int w = 0; w < WM; ++w)
+        if (w < W) out[(size_t)w * M] = now[w];
+#pragma unroll 1
+      for (uint32_t left = need; left != 0; left &= left - 1) {
+        const int w = __ffs(left) - 1;
+        if (col == s_has[w] - 1) out[(size_t)w * M] = fresh(0, w);
+      }
     }
   }
 }
-
-constexpr int kStageBytes = 160 * 1024;  // rows that are brought to shared memory
 
 template <int WM>
 cudaError_t launch_reorder_t(const BeamReorderArgs& a, cudaStream_t stream) {
   constexpr int kMost = 224 * 1024;
   cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (a.counts == nullptr) {
-    constexpr auto kern = beam_reorder_kernel<WM, kInOne, 1024>;
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(1024);
-    cfg.dynamicSmemBytes = reorder_bytes(a.B, a.W, a.M, true);
+    constexpr auto kern = beam_reorder_kernel<WM, kCluster, true>;
+    const int ranks = a.B < kMaxRanks ? std::max(a.B, 1) : kMaxRanks;
+    cfg.gridDim = dim3(ranks);
+    cfg.dynamicSmemBytes = reorder_bytes((a.B + ranks - 1) / ranks, a.W, a.M, true);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)ranks, 1, 1};
+    cfg.numAttrs = 2;
     const cudaError_t e = ensure_dynamic_smem<kern>(kMost);
-    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kern, a, true);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kern, a);
   }
-  constexpr int kThreads = 256;
-  const bool staged = (long long)a.W * a.M * 4 <= kStageBytes;
-  constexpr auto count = beam_reorder_kernel<WM, kCount, kThreads>;
-  constexpr auto write = beam_reorder_kernel<WM, kWrite, kThreads>;
   cfg.gridDim = dim3(a.B);
-  cfg.blockDim = dim3(kThreads);
+  auto both = [&](auto count, auto write) {
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, count, a);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, write, a);
+  };
+  const bool staged = (long long)a.W * a.M * 4 <= kStageBytes;
   cfg.dynamicSmemBytes = reorder_bytes(1, a.W, a.M, staged);
+  if (!staged)
+    return both(beam_reorder_kernel<WM, kCount, false>, beam_reorder_kernel<WM, kWrite, false>);
+  constexpr auto count = beam_reorder_kernel<WM, kCount, true>;
+  constexpr auto write = beam_reorder_kernel<WM, kWrite, true>;
   cudaError_t e = ensure_dynamic_smem<count>(kMost);
   if (e == cudaSuccess) e = ensure_dynamic_smem<write>(kMost);
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, count, a, staged);
-  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, write, a, staged);
+  return e != cudaSuccess ? e : both(count, write);
 }
 
 // ---------------------------------------------------------------- backtrack
@@ -523,9 +584,10 @@ __global__ void __launch_bounds__(kBackThreads)
 
 }  // namespace
 
-// One CTA or one to a request: its rounds over 1,024 columns against a second launch.
+// One cluster, or a CTA to a request and two launches: what the cluster's CTAs hold.
 bool beam_reorder_in_one(int B, int W, int M) {
-  return B <= kMaxInOne && (long long)B * M <= 4096 && (long long)B * W * M * 4 <= kStageBytes;
+  const long long each = (B + kMaxRanks - 1) / kMaxRanks;  // requests of a CTA
+  return each * M <= kRounds * kThreads && each <= 64 && each * W * M * 4 <= kStageBytes;
 }
 
 cudaError_t launch_beam_reorder(const BeamReorderArgs& a, cudaStream_t stream) {

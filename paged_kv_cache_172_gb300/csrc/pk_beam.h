@@ -1,8 +1,13 @@
 // pk_beam.h -- declarations shared between the C-ABI layer and the kernels of beam
-// search (host side).
+// search (host side), and the device wrappers that only these kernels use.
 #pragma once
 
 #include "pk_internal.h"
+#ifdef __CUDACC__
+#include <string.h>
+
+#include "pk_common.cuh"
+#endif
 
 namespace pk {
 
@@ -53,5 +58,26 @@ struct BeamBacktrackArgs {
   int S, B, W, K, pad;
 };
 cudaError_t launch_beam_backtrack(const BeamBacktrackArgs& a, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// The cluster's barrier in two halves, for all threads of all CTAs: what was written to
+// shared memory before the first is seen behind the second.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores 8 bytes to what p is in the shared memory of the cluster's CTA `rank`.
+template <typename X>
+__device__ __forceinline__ void store_cluster(X* p, int rank, X x) {
+  static_assert(sizeof(X) == 8, "one store");
+  uint32_t at;
+  unsigned long long y;
+  memcpy(&y, &x, 8);
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(y) : "memory");
+}
+#endif
 
 }  // namespace pk
