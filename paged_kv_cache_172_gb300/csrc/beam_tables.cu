@@ -25,7 +25,8 @@
 // request's CTA keeps its parents in shared memory, cuts the steps into pieces of 32 and
 // walks all pieces from all W beams at once; a walk over the pieces' results then gives
 // each piece's beam, and all pieces are walked again for their beams.  That makes three
-// walks of 32 steps and one of S / 32 out of one of S.
+// walks of 32 steps and one of S / 32 out of one of S.  Bound: those chains, and the trips
+// to parents and tokens.
 #include <algorithm>
 
 #include "pk_beam.h"
@@ -117,7 +118,7 @@ template <int WM, Pass P, bool STAGED>
 __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorderArgs a) {
   extern __shared__ __align__(16) int s_dyn[];
   __shared__ int s_warp[kThreads / 32];
-  __shared__ long long s_sum[kThreads / 32];
+  __shared__ long long s_sum[3][kThreads / 32];
   __shared__ int2 s_rank[kMaxRanks];  // blocks that a CTA's requests take and give back
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = a.W, M = a.M, bs = 1 << a.bs_log2;
@@ -160,7 +161,9 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   for (int i = tid; i < nb; i += kThreads)
     s_first[i] = a.shared_lens != nullptr ? a.shared_lens[b0 + i] : 0;
   long long t = 0, d = 0, ta = 0, da = 0;  // kWrite: before this request and in all
+  uint32_t first_mask = 0;                 // ... and of the thread's first column
   if (P == kWrite) {
+    if (tid < M) first_mask = a.masks[(size_t)b0 * M + tid];
 #pragma unroll 1
     for (int b = tid; b < a.B; b += kThreads) {
       const long long x = a.counts[2 * b], y = a.counts[2 * b + 1];
@@ -245,7 +248,11 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   }
   if constexpr (P == kCount) {
 #pragma unroll 1
-    for (int i = tid; i < items; i += kThreads) mine += __popc(drops(i));
+    for (int i = tid; i < items; i += kThreads) {
+      const uint32_t x = drops(i);
+      a.masks[(size_t)b0 * M + i] = x;
+      mine += __popc(x);
+    }
   }
   // ---- what is taken and given back before this CTA's requests, and in all
   long long taken = 0, dropped = 0, all_dropped = 0;
@@ -300,20 +307,25 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
     return;
   }
   if constexpr (P == kWrite) {
-    auto sum = [&](long long x) {
+    // Three sums at once: of the warps, then of all by every warp.
+    long long x[3] = {t << 32 | ta, d, da};  // (at most 2^20 taken)
 #pragma unroll
-      for (int k = 16; k >= 1; k >>= 1) x += __shfl_xor_sync(kAll, x, k);
-      if (lane == 0) s_sum[warp] = x;
-      __syncthreads();
-      long long y = 0;
-#pragma unroll 1
-      for (int w = 0; w < kThreads / 32; ++w) y += s_sum[w];
-      __syncthreads();
-      return y;
-    };
-    const long long takes = sum(t << 32 | ta);  // (at most 2^20 each)
-    dropped = sum(d);
-    all_dropped = sum(da);
+    for (int k = 16; k >= 1; k >>= 1)
+#pragma unroll
+      for (int e = 0; e < 3; ++e) x[e] += __shfl_xor_sync(kAll, x[e], k);
+    if (lane == 0)
+#pragma unroll
+      for (int e = 0; e < 3; ++e) s_sum[e][warp] = x[e];
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 3; ++e) x[e] = s_sum[e][lane % (kThreads / 32)];
+#pragma unroll
+    for (int k = kThreads / 64; k >= 1; k >>= 1)
+#pragma unroll
+      for (int e = 0; e < 3; ++e) x[e] += __shfl_xor_sync(kAll, x[e], k);
+    const long long takes = x[0];
+    dropped = x[1];
+    all_dropped = x[2];
     taken = takes & 0xffffffffll;
     if (tid == 0) s_before[0] = (int)(takes >> 32);
     __syncthreads();
@@ -337,7 +349,10 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
 #pragma unroll 1
       for (int base = r * kThreads; base < items; base += kThreads) {
         const int i = base + tid;
-        uint32_t left = P == kCluster ? drop[r] : drops(i);
+        uint32_t left = P == kCluster ? drop[r]
+                        : base == 0 ? first_mask
+                        : i < items ? a.masks[(size_t)b0 * M + i]
+                                    : 0u;
         int total, q, col;
         long long at = put + block_scan<kThreads>(__popc(left), s_warp, total);
         put += total;
@@ -455,20 +470,32 @@ cudaError_t launch_reorder_t(const BeamReorderArgs& a, cudaStream_t stream) {
 
 // ---------------------------------------------------------------- backtrack
 constexpr int kBackThreads = 1024;
-constexpr int kPiece = 32;              // steps of a piece
+constexpr int kPiece = 32;              // steps of a piece, a lane to each in the end
 constexpr int kBackBytes = 160 * 1024;  // parents and beams of the steps held at a time
 constexpr int kBatch = 8;               // loads of a thread in flight
-constexpr uint8_t kOff = 255;           // a parent that is none of the beams
+
+// Bytes of a step's parents: one for each beam and one for "none", which W stands for and
+// which is its own parent, so that a walk asks nothing.
+__host__ __device__ constexpr int step_bytes(int W) { return W + 1; }
+
+// Shared memory for `steps` steps: parents; the hypotheses' beams, four steps to a word;
+// for each piece the beam below it from each of its last step's, and the hypotheses' beams
+// at its last step.
+int back_bytes(int steps, int W, int K) {
+  return steps * (step_bytes(W) + K) + steps / kPiece * (step_bytes(W) + K);
+}
 
 __global__ void __launch_bounds__(kBackThreads)
     beam_backtrack_kernel(const BeamBacktrackArgs a, int steps) {
-  extern __shared__ uint8_t s_back[];
-  const int W = a.W, K = a.K, b = blockIdx.x, tid = threadIdx.x;
-  const int pieces = (steps + kPiece - 1) / kPiece;
-  uint8_t* s_parent = s_back;                   // [steps][W]
-  uint8_t* s_beam = s_parent + steps * W;       // [K][steps], kOff: no token
-  uint8_t* s_map = s_beam + (size_t)K * steps;  // [pieces][W] beam below a piece
-  uint8_t* s_at = s_map + pieces * W;           // [K][pieces] beam at a piece's last step
+  extern __shared__ __align__(16) uint8_t s_back[];
+  const int W = a.W, K = a.K, SW = step_bytes(W), b = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pieces = steps / kPiece;
+  // [K][piece of steps / 4][pieces]: neighbouring pieces in neighbouring words
+  uint32_t* s_beam = reinterpret_cast<uint32_t*>(s_back);
+  uint8_t* s_parent = s_back + K * steps;   // [steps][SW]
+  uint8_t* s_map = s_parent + steps * SW;   // [pieces][SW]
+  uint8_t* s_at = s_map + pieces * SW;      // [K][pieces]
   __shared__ int s_n[kMaxBeams];        // the hypotheses' lengths
   __shared__ uint8_t s_cur[kMaxBeams];  // their beam at the last step still to walk
   __shared__ int s_most;
@@ -484,18 +511,16 @@ __global__ void __launch_bounds__(kBackThreads)
       n = 0;
     }
     s_n[tid] = n;
-    s_cur[tid] = n > 0 ? (uint8_t)w : kOff;
+    s_cur[tid] = n > 0 ? (uint8_t)w : (uint8_t)W;
     atomicMax(&s_most, n);
   }
   __syncthreads();
   const size_t plane = (size_t)a.B * W;
   int32_t* out = a.out + (size_t)b * K * a.S;
-  const int behind = a.S - s_most;
 #pragma unroll 1
-  for (int i = tid; i < K * behind; i += kBackThreads) {
-    const int k = i / behind;
-    out[(size_t)k * a.S + s_most + (i - k * behind)] = a.pad;
-  }
+  for (int k = 0; k < K; ++k)  // behind all of them
+#pragma unroll 1
+    for (int s = s_most + tid; s < a.S; s += kBackThreads) out[(size_t)k * a.S + s] = a.pad;
   // (a thread's parents: of one beam, every `rows`-th step)
   const int rows = kBackThreads / W, my_s = tid / W, my_w = tid - my_s * W;
 #pragma unroll 1
@@ -503,80 +528,100 @@ __global__ void __launch_bounds__(kBackThreads)
     const int lo = hi > steps ? hi - steps : 0, n = hi - lo;
     const int np = (n + kPiece - 1) / kPiece;
     if (my_s < rows) {
-      const int32_t* from = a.parents + (size_t)lo * plane + (size_t)b * W + my_w;
+      const int32_t* from = a.parents + (size_t)(lo + my_s) * plane + (size_t)b * W + my_w;
+      const size_t next = rows * plane;
 #pragma unroll 1
-      for (int s = my_s; s < n; s += kBatch * rows) {
+      for (int s = my_s; s < n; s += kBatch * rows, from += kBatch * next) {
         int p[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          p[j] = s + j * rows < n ? from[(size_t)(s + j * rows) * plane] : -1;
+        for (int j = 0; j < kBatch; ++j) p[j] = s + j * rows < n ? from[j * next] : -1;
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
           if (s + j * rows < n)
-            s_parent[(s + j * rows) * W + my_w] = p[j] >= 0 && p[j] < W ? (uint8_t)p[j] : kOff;
+            s_parent[(s + j * rows) * SW + my_w] = (uint8_t)min((unsigned)p[j], (unsigned)W);
       }
     }
+#pragma unroll 1
+    for (int s = tid; s < n; s += kBackThreads) s_parent[s * SW + W] = (uint8_t)W;
     __syncthreads();
-    // the beam below each piece, from each of its last step's
+    // ---- the beam below each piece, from each of its last step's
 #pragma unroll 1
-    for (int i = tid; i < np * W; i += kBackThreads) {
-      const int p = i / W;
-      int w = i - p * W;
-#pragma unroll 1
-      for (int s = min(n, (p + 1) * kPiece) - 1; s >= p * kPiece && w != kOff; --s)
-        w = s_parent[s * W + w];
+    for (int i = tid; i < np * SW; i += kBackThreads) {
+      const int p = i / SW;
+      int w = i - p * SW;
+      const uint8_t* at = s_parent + (min(n, (p + 1) * kPiece) - 1) * SW;
+#pragma unroll 4
+      for (int s = min(n - p * kPiece, kPiece); s > 0; --s, at -= SW) w = at[w];
       s_map[i] = (uint8_t)w;
     }
     __syncthreads();
-    // each hypothesis over the pieces (it may begin inside one)
+    // ---- each hypothesis over the pieces (it may begin inside one)
     if (tid < K) {
       const int end = min(s_n[tid] - lo, n);  // its steps here
       int w = s_cur[tid];
       if (end > 0) {
         int p = (end - 1) / kPiece;
         s_at[tid * pieces + p] = (uint8_t)w;
-#pragma unroll 1
-        for (int s = end - 1; s >= p * kPiece && w != kOff; --s) w = s_parent[s * W + w];
-#pragma unroll 1
+        const uint8_t* at = s_parent + (end - 1) * SW;
+#pragma unroll 4
+        for (int s = end - p * kPiece; s > 0; --s, at -= SW) w = at[w];
+#pragma unroll 4
         for (--p; p >= 0; --p) {
           s_at[tid * pieces + p] = (uint8_t)w;
-          if (w != kOff) w = s_map[p * W + w];
+          w = s_map[p * SW + w];
         }
         s_cur[tid] = (uint8_t)w;
       }
     }
     __syncthreads();
-    // all pieces of all hypotheses
+    // ---- all pieces of all hypotheses: their beams, W where there is no token
 #pragma unroll 1
     for (int i = tid; i < K * np; i += kBackThreads) {
       const int k = i / np, p = i - k * np;
-      const int end = min(s_n[k] - lo, n), last = min(n, (p + 1) * kPiece) - 1;
-      int w = p * kPiece < end ? s_at[k * pieces + p] : kOff;
+      const int end = min(s_n[k] - lo, n) - p * kPiece;  // steps of it in this piece
+      int w = end > 0 ? s_at[k * pieces + p] : W;
+      const uint8_t* at = s_parent + p * kPiece * SW;
+      uint32_t* to = s_beam + k * (kPiece / 4) * pieces + p;
+      bool off = false;
 #pragma unroll 1
-      for (int s = last; s >= p * kPiece; --s) {
-        const bool in = s < end && w != kOff;
-        s_beam[(size_t)k * steps + s] = in ? (uint8_t)w : kOff;
-        if (in) w = s_parent[s * W + w];
-        if (in && w == kOff && lo + s > 0) flag_status(a.status, PA_DEV_BAD_BEAM);
+      for (int q = kPiece / 4 - 1; q >= 0; --q) {
+        uint32_t four = 0;
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          const int s = 4 * q + e;
+          const bool in = s < end;
+          four |= (uint32_t)(in ? w : W) << (8 * e);
+          const int below = in ? at[s * SW + w] : w;
+          off |= below == W && w != W && lo + p * kPiece + s > 0;
+          w = below;
+        }
+        to[q * pieces] = four;
       }
+      if (off) flag_status(a.status, PA_DEV_BAD_BEAM);
     }
     __syncthreads();
+    // ---- the tokens, a warp to a piece of a hypothesis, a lane to a step
 #pragma unroll 1
-    for (int i0 = tid; i0 < K * n; i0 += kBatch * kBackThreads) {
-      int token[kBatch], at[kBatch];
+    for (int i0 = warp; i0 < K * np; i0 += kBatch * (kBackThreads / 32)) {
+      int token[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * kBackThreads;
-        if (i < K * n) {
-          const int k = i / n, s = i - k * n, w = s_beam[(size_t)k * steps + s];
-          at[j] = k * a.S + lo + s;
-          token[j] =
-              w != kOff ? a.tokens[(size_t)(lo + s) * plane + (size_t)b * W + w] : a.pad;
+        const int i = i0 + j * (kBackThreads / 32), k = i / np, p = i - k * np;
+        token[j] = a.pad;
+        if (i < K * np && p * kPiece + lane < n) {
+          const uint32_t four = s_beam[(k * (kPiece / 4) + (lane >> 2)) * pieces + p];
+          const int w = four >> (8 * (lane & 3)) & 255;
+          if (w < W)
+            token[j] =
+                a.tokens[(size_t)(lo + p * kPiece + lane) * plane + (size_t)b * W + w];
         }
       }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (i0 + j * kBackThreads < K * n) out[at[j]] = token[j];
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * (kBackThreads / 32), k = i / np, p = i - k * np;
+        if (i < K * np && p * kPiece + lane < n)
+          out[(size_t)k * a.S + lo + p * kPiece + lane] = token[j];
+      }
     }
     __syncthreads();
   }
@@ -597,11 +642,10 @@ cudaError_t launch_beam_reorder(const BeamReorderArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_beam_backtrack(const BeamBacktrackArgs& a, cudaStream_t stream) {
-  // steps whose parents and beams (and the pieces' of 32) fit shared memory
-  int steps = kBackBytes / (a.W + a.K) / kPiece * kPiece;
+  int steps = kBackBytes / (step_bytes(a.W) + a.K) / kPiece * kPiece;
   steps = std::min(steps, (a.S + kPiece - 1) / kPiece * kPiece);
-  const int smem = steps * (a.W + a.K) + steps / kPiece * (a.W + a.K);
-  const cudaError_t e = ensure_dynamic_smem<beam_backtrack_kernel>(kBackBytes * 33 / 32);
+  const int smem = back_bytes(steps, a.W, a.K);
+  const cudaError_t e = ensure_dynamic_smem<beam_backtrack_kernel>(kBackBytes / 32 * 33);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.B);

@@ -41,7 +41,10 @@ struct BeamReorderArgs {
   int32_t* lens_out;
   int64_t* free_state_out;
   int64_t* pairs;   // [B * W, 2]
-  int64_t* counts;  // [B + 1, 2] workspace of the launch by requests, or null
+  // Workspace of the launches by requests, or null: [B + 1, 2] blocks that each request
+  // takes and gives back, then the ring's state; [B, M] beams whose entry goes back.
+  int64_t* counts;
+  uint32_t* masks;
   int32_t* status;
   int B, W, M, bs_log2, num_blocks;
 };
