@@ -478,11 +478,17 @@ constexpr int kBatch = 8;               // loads of a thread in flight
 // which is its own parent, so that a walk asks nothing.
 __host__ __device__ constexpr int step_bytes(int W) { return W + 1; }
 
-// Shared memory for `steps` steps: parents; the hypotheses' beams, four steps to a word;
-// for each piece the beam below it from each of its last step's, and the hypotheses' beams
-// at its last step.
+// Shared memory for `steps` steps: tokens; the hypotheses' beams, four steps to a word;
+// parents; for each piece the beam below it from each of its last step's, and the
+// hypotheses' beams at its last step.
 int back_bytes(int steps, int W, int K) {
-  return steps * (step_bytes(W) + K) + steps / kPiece * (step_bytes(W) + K);
+  return steps * (4 * W + step_bytes(W) + K) + steps / kPiece * (step_bytes(W) + K);
+}
+
+// Copies 4 bytes to shared memory, not awaited.
+__device__ __forceinline__ void copy_word(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from)
+               : "memory");
 }
 
 __global__ void __launch_bounds__(kBackThreads)
@@ -492,8 +498,9 @@ __global__ void __launch_bounds__(kBackThreads)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pieces = steps / kPiece;
   // [K][piece of steps / 4][pieces]: neighbouring pieces in neighbouring words
-  uint32_t* s_beam = reinterpret_cast<uint32_t*>(s_back);
-  uint8_t* s_parent = s_back + K * steps;   // [steps][SW]
+  int32_t* s_token = reinterpret_cast<int32_t*>(s_back);  // [steps][W]
+  uint32_t* s_beam = reinterpret_cast<uint32_t*>(s_token + steps * W);
+  uint8_t* s_parent = s_back + 4 * steps * W + K * steps;  // [steps][SW]
   uint8_t* s_map = s_parent + steps * SW;   // [pieces][SW]
   uint8_t* s_at = s_map + pieces * SW;      // [K][pieces]
   __shared__ int s_n[kMaxBeams];        // the hypotheses' lengths
@@ -528,8 +535,12 @@ __global__ void __launch_bounds__(kBackThreads)
     const int lo = hi > steps ? hi - steps : 0, n = hi - lo;
     const int np = (n + kPiece - 1) / kPiece;
     if (my_s < rows) {
-      const int32_t* from = a.parents + (size_t)(lo + my_s) * plane + (size_t)b * W + my_w;
-      const size_t next = rows * plane;
+      const size_t at = (size_t)(lo + my_s) * plane + (size_t)b * W + my_w, next = rows * plane;
+      const int32_t* from = a.tokens + at;
+#pragma unroll 4
+      for (int s = my_s; s < n; s += rows, from += next)  // (awaited at the end)
+        copy_word(s_token + s * W + my_w, from);
+      from = a.parents + at;
 #pragma unroll 1
       for (int s = my_s; s < n; s += kBatch * rows, from += kBatch * next) {
         int p[kBatch];
@@ -599,28 +610,19 @@ __global__ void __launch_bounds__(kBackThreads)
       }
       if (off) flag_status(a.status, PA_DEV_BAD_BEAM);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     // ---- the tokens, a warp to a piece of a hypothesis, a lane to a step
 #pragma unroll 1
-    for (int i0 = warp; i0 < K * np; i0 += kBatch * (kBackThreads / 32)) {
-      int token[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * (kBackThreads / 32), k = i / np, p = i - k * np;
-        token[j] = a.pad;
-        if (i < K * np && p * kPiece + lane < n) {
-          const uint32_t four = s_beam[(k * (kPiece / 4) + (lane >> 2)) * pieces + p];
-          const int w = four >> (8 * (lane & 3)) & 255;
-          if (w < W)
-            token[j] =
-                a.tokens[(size_t)(lo + p * kPiece + lane) * plane + (size_t)b * W + w];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * (kBackThreads / 32), k = i / np, p = i - k * np;
-        if (i < K * np && p * kPiece + lane < n)
-          out[(size_t)k * a.S + lo + p * kPiece + lane] = token[j];
+    for (int k = 0; k < K; ++k) {
+      const uint32_t* fours = s_beam + (k * (kPiece / 4) + (lane >> 2)) * pieces;
+      int32_t* to = out + (size_t)k * a.S + lo + lane;
+#pragma unroll 2
+      for (int p = warp; p < np; p += kBackThreads / 32) {
+        const int s = p * kPiece + lane;
+        if (s >= n) continue;
+        const int w = fours[p] >> (8 * (lane & 3)) & 255;
+        to[p * kPiece] = w < W ? s_token[s * W + w] : a.pad;
       }
     }
     __syncthreads();
@@ -642,7 +644,7 @@ cudaError_t launch_beam_reorder(const BeamReorderArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_beam_backtrack(const BeamBacktrackArgs& a, cudaStream_t stream) {
-  int steps = kBackBytes / (step_bytes(a.W) + a.K) / kPiece * kPiece;
+  int steps = kBackBytes / (4 * a.W + step_bytes(a.W) + a.K) / kPiece * kPiece;
   steps = std::min(steps, (a.S + kPiece - 1) / kPiece * kPiece);
   const int smem = back_bytes(steps, a.W, a.K);
   const cudaError_t e = ensure_dynamic_smem<beam_backtrack_kernel>(kBackBytes / 32 * 33);
