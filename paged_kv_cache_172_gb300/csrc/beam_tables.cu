@@ -21,12 +21,12 @@
 // Bound: the launches, and the trips to memory (entries, then the ring).
 //
 // Backtrack.  Tokens of hypothesis k: beam(n - 1) = beams[k], token(s) = tokens[s][beam(s)],
-// beam(s - 1) = parents[s][beam(s)].  A walk of S steps is a chain of S loads, so each
-// request's CTA keeps its parents in shared memory, cuts the steps into pieces of 32 and
-// walks all pieces from all W beams at once; a walk over the pieces' results then gives
-// each piece's beam, and all pieces are walked again for their beams.  That makes three
-// walks of 32 steps and one of S / 32 out of one of S.  Bound: those chains, and the trips
-// to parents and tokens.
+// beam(s - 1) = parents[s][beam(s)].  A walk of S steps is a chain of S loads, so a
+// request's CTAs, a cluster that shares out the steps, keep parents and tokens in shared
+// memory, cut the steps into pieces of 32 and walk all pieces from all W beams at once; a
+// walk over the pieces' results then gives each piece's beam, and all pieces are walked
+// again for their beams.  That makes three walks of 32 steps and one of S / 32 out of one
+// of S.  Bound: those chains, and the trips to parents and tokens, W words a step.
 #include <algorithm>
 
 #include "pk_beam.h"
@@ -478,11 +478,11 @@ constexpr int kBatch = 8;               // loads of a thread in flight
 // which is its own parent, so that a walk asks nothing.
 __host__ __device__ constexpr int step_bytes(int W) { return W + 1; }
 
-// Shared memory for `steps` steps: tokens; the hypotheses' beams, four steps to a word;
-// parents; for each piece the beam below it from each of its last step's, and the
-// hypotheses' beams at its last step.
-int back_bytes(int steps, int W, int K) {
-  return steps * (4 * W + step_bytes(W) + K) + steps / kPiece * (step_bytes(W) + K);
+// A CTA's shared memory for `steps` steps: tokens; the hypotheses' beams, four steps to a
+// word; parents; the hypotheses' beams at its pieces' last steps; and, of all the cluster's
+// pieces, the beam below each from each of its last step's.
+int back_bytes(int steps, int ranks, int W, int K) {
+  return steps * (4 * W + step_bytes(W) + K) + steps / kPiece * (ranks * step_bytes(W) + K);
 }
 
 // Copies 4 bytes to shared memory, not awaited.
@@ -492,20 +492,23 @@ __device__ __forceinline__ void copy_word(void* to, const void* from) {
 }
 
 __global__ void __launch_bounds__(kBackThreads)
-    beam_backtrack_kernel(const BeamBacktrackArgs a, int steps) {
+    beam_backtrack_kernel(const BeamBacktrackArgs a, int steps, int ranks) {
   extern __shared__ __align__(16) uint8_t s_back[];
-  const int W = a.W, K = a.K, SW = step_bytes(W), b = blockIdx.x;
+  const int W = a.W, K = a.K, SW = step_bytes(W);
+  const int b = blockIdx.x / ranks, rank = blockIdx.x - b * ranks;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pieces = steps / kPiece;
   // [K][piece of steps / 4][pieces]: neighbouring pieces in neighbouring words
   int32_t* s_token = reinterpret_cast<int32_t*>(s_back);  // [steps][W]
   uint32_t* s_beam = reinterpret_cast<uint32_t*>(s_token + steps * W);
   uint8_t* s_parent = s_back + 4 * steps * W + K * steps;  // [steps][SW]
-  uint8_t* s_map = s_parent + steps * SW;   // [pieces][SW]
-  uint8_t* s_at = s_map + pieces * SW;      // [K][pieces]
-  __shared__ int s_n[kMaxBeams];        // the hypotheses' lengths
-  __shared__ uint8_t s_cur[kMaxBeams];  // their beam at the last step still to walk
+  uint8_t* s_at = s_parent + steps * SW;                   // [K][pieces]
+  uint8_t* s_map = s_at + K * pieces;                      // [ranks * pieces][SW]
+  __shared__ int s_n[kMaxBeams];         // the hypotheses' lengths
+  __shared__ uint8_t s_cur[kMaxBeams];   // their beam at the last step still to walk
+  __shared__ uint8_t s_part[kMaxBeams];  // ... and below the piece that they begin in
   __shared__ int s_most;
+  cluster_arrive();  // (nobody stores to a CTA that has not begun)
   pdl_wait();
   pdl_launch_dependents();
   if (tid == 0) s_most = 0;
@@ -527,15 +530,19 @@ __global__ void __launch_bounds__(kBackThreads)
 #pragma unroll 1
   for (int k = 0; k < K; ++k)  // behind all of them
 #pragma unroll 1
-    for (int s = s_most + tid; s < a.S; s += kBackThreads) out[(size_t)k * a.S + s] = a.pad;
+    for (int s = s_most + rank * kBackThreads + tid; s < a.S; s += ranks * kBackThreads)
+      out[(size_t)k * a.S + s] = a.pad;
   // (a thread's parents: of one beam, every `rows`-th step)
   const int rows = kBackThreads / W, my_s = tid / W, my_w = tid - my_s * W;
+  // Steps lo .. hi - 1 in the cluster, base .. base + n - 1 in this CTA.
 #pragma unroll 1
-  for (int hi = s_most; hi > 0; hi -= steps) {  // steps lo .. hi - 1
-    const int lo = hi > steps ? hi - steps : 0, n = hi - lo;
-    const int np = (n + kPiece - 1) / kPiece;
+  for (int hi = s_most, lo; hi > 0; hi = lo) {
+    lo = max(0, hi - ranks * steps);
+    const int base = lo + rank * steps, n = min(max(hi - base, 0), steps);
+    const int np = (n + kPiece - 1) / kPiece, p0 = rank * pieces;
     if (my_s < rows) {
-      const size_t at = (size_t)(lo + my_s) * plane + (size_t)b * W + my_w, next = rows * plane;
+      const size_t at = (size_t)(base + my_s) * plane + (size_t)b * W + my_w;
+      const size_t next = rows * plane;
       const int32_t* from = a.tokens + at;
 #pragma unroll 4
       for (int s = my_s; s < n; s += rows, from += next)  // (awaited at the end)
@@ -555,41 +562,58 @@ __global__ void __launch_bounds__(kBackThreads)
 #pragma unroll 1
     for (int s = tid; s < n; s += kBackThreads) s_parent[s * SW + W] = (uint8_t)W;
     __syncthreads();
-    // ---- the beam below each piece, from each of its last step's
+    cluster_wait();  // (the other CTAs are done with their last maps)
+    // ---- the beam below each piece from each of its last step's, and below the piece
+    // that a hypothesis begins in from its own: told to all CTAs
 #pragma unroll 1
-    for (int i = tid; i < np * SW; i += kBackThreads) {
-      const int p = i / SW;
-      int w = i - p * SW;
-      const uint8_t* at = s_parent + (min(n, (p + 1) * kPiece) - 1) * SW;
+    for (int i = tid; i < np * SW + K; i += kBackThreads) {
+      uint8_t* to;
+      int p, w, last;  // piece of this CTA, beam at the last of so many steps of it
+      if (i < np * SW) {
+        p = i / SW;
+        w = i - p * SW;
+        last = min(n - p * kPiece, kPiece);
+        to = s_map + p0 * SW + i;
+      } else {
+        const int k = i - np * SW, end = min(s_n[k], hi) - base;  // its steps from base on
+        if (end <= 0 || end > n) continue;
+        p = (end - 1) / kPiece;
+        w = s_cur[k];
+        last = end - p * kPiece;
+        to = s_part + k;
+      }
+      const uint8_t* at = s_parent + (p * kPiece + last - 1) * SW;
 #pragma unroll 4
-      for (int s = min(n - p * kPiece, kPiece); s > 0; --s, at -= SW) w = at[w];
-      s_map[i] = (uint8_t)w;
+      for (int s = last; s > 0; --s, at -= SW) w = at[w];
+#pragma unroll 1
+      for (int r = 0; r < ranks; ++r) store_cluster_byte(to, r, w);
     }
-    __syncthreads();
-    // ---- each hypothesis over the pieces (it may begin inside one)
+    cluster_arrive();
+    cluster_wait();
+    // ---- each hypothesis over the cluster's pieces
     if (tid < K) {
-      const int end = min(s_n[tid] - lo, n);  // its steps here
+      const int end = min(s_n[tid], hi) - lo;
       int w = s_cur[tid];
       if (end > 0) {
         int p = (end - 1) / kPiece;
-        s_at[tid * pieces + p] = (uint8_t)w;
-        const uint8_t* at = s_parent + (end - 1) * SW;
-#pragma unroll 4
-        for (int s = end - p * kPiece; s > 0; --s, at -= SW) w = at[w];
+        uint8_t* at = s_at + tid * pieces - p0;  // (of this CTA's pieces only)
+        if (p >= p0 && p < p0 + pieces) at[p] = (uint8_t)w;
+        w = s_part[tid];
 #pragma unroll 4
         for (--p; p >= 0; --p) {
-          s_at[tid * pieces + p] = (uint8_t)w;
+          if (p >= p0 && p < p0 + pieces) at[p] = (uint8_t)w;
           w = s_map[p * SW + w];
         }
         s_cur[tid] = (uint8_t)w;
       }
     }
     __syncthreads();
+    cluster_arrive();
     // ---- all pieces of all hypotheses: their beams, W where there is no token
 #pragma unroll 1
     for (int i = tid; i < K * np; i += kBackThreads) {
       const int k = i / np, p = i - k * np;
-      const int end = min(s_n[k] - lo, n) - p * kPiece;  // steps of it in this piece
+      const int end = min(s_n[k], hi) - base - p * kPiece;  // steps of it from this piece on
       int w = end > 0 ? s_at[k * pieces + p] : W;
       const uint8_t* at = s_parent + p * kPiece * SW;
       uint32_t* to = s_beam + k * (kPiece / 4) * pieces + p;
@@ -603,7 +627,7 @@ __global__ void __launch_bounds__(kBackThreads)
           const bool in = s < end;
           four |= (uint32_t)(in ? w : W) << (8 * e);
           const int below = in ? at[s * SW + w] : w;
-          off |= below == W && w != W && lo + p * kPiece + s > 0;
+          off |= below == W && w != W && base + p * kPiece + s > 0;
           w = below;
         }
         to[q * pieces] = four;
@@ -616,7 +640,7 @@ __global__ void __launch_bounds__(kBackThreads)
 #pragma unroll 1
     for (int k = 0; k < K; ++k) {
       const uint32_t* fours = s_beam + (k * (kPiece / 4) + (lane >> 2)) * pieces;
-      int32_t* to = out + (size_t)k * a.S + lo + lane;
+      int32_t* to = out + (size_t)k * a.S + base + lane;
 #pragma unroll 2
       for (int p = warp; p < np; p += kBackThreads / 32) {
         const int s = p * kPiece + lane;
@@ -627,6 +651,7 @@ __global__ void __launch_bounds__(kBackThreads)
     }
     __syncthreads();
   }
+  cluster_wait();
 }
 
 }  // namespace
@@ -644,22 +669,29 @@ cudaError_t launch_beam_reorder(const BeamReorderArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_beam_backtrack(const BeamBacktrackArgs& a, cudaStream_t stream) {
-  int steps = kBackBytes / (4 * a.W + step_bytes(a.W) + a.K) / kPiece * kPiece;
-  steps = std::min(steps, (a.S + kPiece - 1) / kPiece * kPiece);
-  const int smem = back_bytes(steps, a.W, a.K);
-  const cudaError_t e = ensure_dynamic_smem<beam_backtrack_kernel>(kBackBytes / 32 * 33);
+  // CTAs of a request: as many as give every SM one, 256 steps each at least.  (An SM has
+  // some 500 of its pieces of a step under way at a time, whatever their size.)
+  const int nsm = sm_count() > 0 ? sm_count() : 152;
+  const int ranks = std::min({kMaxRanks, std::max(nsm / a.B, 1), (a.S + 255) / 256});
+  // Their steps: what fits shared memory.
+  const int each = 4 * a.W + 2 * step_bytes(a.W) + 2 * a.K;  // (a bound: ranks <= kPiece)
+  int steps = kBackBytes / each / kPiece * kPiece;
+  steps = std::min(steps, ((a.S + ranks - 1) / ranks + kPiece - 1) / kPiece * kPiece);
+  const cudaError_t e = ensure_dynamic_smem<beam_backtrack_kernel>(kBackBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.B);
+  cfg.gridDim = dim3((unsigned)a.B * ranks);
   cfg.blockDim = dim3(kBackThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = back_bytes(steps, ranks, a.W, a.K);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)ranks, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, beam_backtrack_kernel, a, steps);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, beam_backtrack_kernel, a, steps, ranks);
 }
 
 }  // namespace pk

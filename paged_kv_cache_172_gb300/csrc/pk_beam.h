@@ -81,6 +81,11 @@ __device__ __forceinline__ void store_cluster(X* p, int rank, X x) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(y) : "memory");
 }
+__device__ __forceinline__ void store_cluster_byte(uint8_t* p, int rank, int x) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
 #endif
 
 }  // namespace pk
