@@ -20,7 +20,8 @@
 //   warp 10         issues O += P V (one thread);
 //   warp 11         schedules, and requests Q.
 // Tensor memory: S [0, 128) shared by both tiles, P_A [128, 192), P_B
-// [192, 256) as 16-bit pairs, O_A, O_B from column 256 (D columns each).  Q
+// [192, 256) as 16-bit pairs, O_A, O_B from column 256 (D columns each); cross attention
+// at D = 64 has room for an S of each tile, [0, 256), and the others 128 further on.  Q
 // stays in shared memory (A operand of the S products) and P in tensor memory
 // (A operand of the P V products): the placement that asks least of the shared
 // memory's bandwidth, as in the fp16 chunk kernel of this library.
@@ -81,7 +82,6 @@ constexpr int kThreadsG = 384;           // 8 softmax warps, K/V loads, 2 MMA is
 constexpr int kWarpLoad = 8, kWarpS = 9, kWarpPv = 10, kWarpSched = 11;
 constexpr int kItems = 3;                // items posted ahead
 constexpr int kCols = 512;               // tensor memory columns
-constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr int kWindow = 256;             // block-table entries staged at a time
 constexpr int kMaxRing = 8;
 constexpr int kBars = 4 * kMaxRing + 14 + 2 * kItems + 1;
@@ -95,6 +95,17 @@ constexpr float kRaiseLog2 = std::is_same<T, __half>::value ? 6.0f : 0.0f;
 // Where the keys are and who sees them: a prompt's own rows up to itself, the paged
 // cache up to itself, or rows of another array, all of them.
 enum Form { kPrompt, kChunk, kCross };
+
+// Tensor memory: whether each tile has an S region of its own (where O leaves room), then
+// the columns of S, P and O.
+template <int D, Form F>
+constexpr bool kOwnS = F == kCross && D == 64;
+template <int D, Form F>
+struct Col {
+  static constexpr uint32_t S = 0, P = kOwnS<D, F> ? 256 : 128, O = P + kTile;
+  static constexpr uint32_t nextS = kOwnS<D, F> ? kTile : 0;  // from tile A's S to tile B's
+  static_assert(O + 2 * D <= kCols, "tensor memory");
+};
 
 // Layout of a K or V tile in shared memory.  Paged: key groups of 8 keys x D
 // dims, each the 1 KB atoms of dims 0-63 and 64-127 (the order in which a
@@ -353,6 +364,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   constexpr bool PAGED = F == kChunk;
   using C = Cfg<D, PAGED>;
   constexpr int kRing = C::RING;
+  constexpr uint32_t kColS = Col<D, F>::S, kColP = Col<D, F>::P, kColO = Col<D, F>::O;
+  constexpr uint32_t kNextS = Col<D, F>::nextS;
   // P is handed over in halves for contiguous rows, so that its product with V starts
   // 64 keys early (one prompt of 8,192 353 -> 343 us); with the paged loader's code
   // beside it the longer loops cost more than that (16 x 2,048 keys 457 -> 470 us).
@@ -449,7 +462,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     const int row = quarter * 32 + lane;
     const int my_tok = (row * a.g_magic) >> 16;  // row / G
     const uint32_t t_lane = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_s = tmem + t_lane + kColS, t_o = tmem + t_lane + kColO + x * D;
+    const uint32_t t_s = tmem + t_lane + kColS + x * kNextS, t_o = tmem + t_lane + kColO + x * D;
     const float sl2 = a.scale_log2;
     int done = 0;    // key tiles of the items before and of this one
     int u0 = 0;      // ring slots of the items before
@@ -881,13 +894,16 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             if (t >= nt[x] || !ok) continue;
             if (!q_there[x] && !(ok = q_there[x] = mbar_wait(&q_full[x], k & 1))) continue;
             const uint64_t da = dq + x * (kQRoom >> 4);
-            // S is free once the softmax of the product before has loaded it.
-            if (last_free != nullptr && !(ok = mbar_wait(last_free, last_phase))) continue;
+            // S is free once the softmax of the product before has loaded it (of the
+            // tile's own product where it has a region of its own).
+            if (kOwnS<D, F> ? done[x] > 0 && !(ok = mbar_wait(&s_free[x], (done[x] - 1) & 1))
+                            : last_free != nullptr && !(ok = mbar_wait(last_free, last_phase)))
+              continue;
             if (!PAGED && !(ok = mbar_wait(&k_full[ki % kRing], (ki / kRing) & 1))) continue;
             tc::fence_after_sync();
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              tc::mma_f16(tmem + kColS, da + (((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
+              tc::mma_f16(tmem + kColS + x * kNextS, da + (((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
                           db + (((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4), kIdS, kk > 0);
             tc::commit(&s_full[x]);
             if (t + 1 == nt[x]) tc::commit(&q_free[x]);
