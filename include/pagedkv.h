@@ -614,9 +614,10 @@ pa_status pa_chunk_attention(const void *q, const void *k_cache, const void *v_c
  * max_q_len, max_kv_len  host-side bounds on the requests' lengths: a request past one
  *           of them, or whose keys leave [0, Tk), is flagged PA_DEV_BAD_CONTEXT and its
  *           rows are zeros (max_q_len above T counts as T)
- * D in {64, 128}; scale > 0.  With max_q_len * H / Hkv at most 16 (and B at most 65535)
- * the kernel of pa_decode_grouped serves the call, to its precision; otherwise that of
- * pa_prompt_attention, to its, and H / Hkv is at most 128 (else PA_ERR_UNSUPPORTED).
+ * D in {64, 128}; scale > 0.  With max_q_len * H / Hkv at most 16 (up to 48 in small
+ * calls; B at most 65535) the kernel of pa_decode_grouped serves the call, to its
+ * precision; otherwise that of pa_prompt_attention, to its, and H / Hkv is at most 128
+ * (else PA_ERR_UNSUPPORTED).
  *
  * workspace (16-byte aligned, may be NULL): with at least
  * pa_cross_attention_workspace_size(...) bytes few queries over many keys are cut into
@@ -698,8 +699,9 @@ pa_status pa_decode_grouped(const void *q, const void *k_cache, const void *v_ca
  *
  * logits [B * W] rows of V in dtype (PA_F32 too), row_stride >= V elements apart
  * scores [B, W] float32; V at most 2^28; eos_token below V
- * workspace: at least pa_beam_select_workspace_size(B, W, V) bytes, 16-byte aligned,
- * else PA_ERR_WORKSPACE; the size depends on the SM count of the current device.
+ * workspace: at least pa_beam_select_workspace_size(B, W, V) bytes, 16-byte aligned, else
+ * PA_ERR_WORKSPACE; the size is 0 but for few requests with many beams and a large
+ * vocabulary, and depends on the SM count of the current device.
  * W above 32 returns PA_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 size_t pa_beam_select_workspace_size(int B, int W, int V);

@@ -27,7 +27,9 @@ extern "C" {
 
 size_t pa_beam_select_workspace_size(int B, int W, int V) {
   if (B <= 0 || !beams_ok(B, W) || W > pk::kMaxBeams || V <= 0 || V > kMaxVocabulary) return 0;
-  return 0;
+  int groups, ranks;
+  pk::beam_select_shape(B, W, V, &groups, &ranks);
+  return groups == 1 ? 0 : (size_t)B * W * (W * 8 + 8);
 }
 
 pa_status pa_beam_select(const void* logits, pa_dtype dtype, int64_t row_stride,
@@ -44,6 +46,11 @@ pa_status pa_beam_select(const void* logits, pa_dtype dtype, int64_t row_stride,
   if (!logits || !scores || !tokens || !parents || !new_scores || !ended_scores ||
       !aligned(logits, dtype == PA_F32 ? 4 : 2))
     return PA_ERR_INVALID;
+  const size_t need = pa_beam_select_workspace_size(B, W, V);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return PA_ERR_INVALID;
+  }
   pk::BeamSelectArgs a;
   a.logits = logits;
   a.row_stride = row_stride;
@@ -59,7 +66,9 @@ pa_status pa_beam_select(const void* logits, pa_dtype dtype, int64_t row_stride,
   a.eos = eos_token;
   a.pad = pad_token;
   a.dtype = dtype;
-  a.ranks = pk::beam_select_ranks(B, W, V);
+  pk::beam_select_shape(B, W, V, &a.groups, &a.ranks);
+  a.ws_top = static_cast<unsigned long long*>(workspace);
+  a.ws_lse = reinterpret_cast<double*>(a.ws_top + (size_t)B * W * W);
   return launched(pk::launch_beam_select(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -275,13 +275,6 @@ pa_status pa_chunk_attention(const void* q, const void* k_cache, const void* v_c
   return packed_impl(a, q, k_cache, v_cache, q_stride, 0, 0, scale, max_context_len, stream);
 }
 
-// Cross attention: whether a request's rows, max_q_len * G to a K/V head, go to the kernel
-// of single tokens, which reads the keys once for every 16 of them.
-static bool cross_few(int B, int T, int H, int Hkv, int max_q) {
-  return (long long)max_q * (H / Hkv) <= pk::kCrossFewColumns && B <= 65535 &&
-         (long long)T * H < (1LL << 31);
-}
-
 static long long cross_parts(int B, int H, int Hkv, int D, int max_q, int max_kv, int* partition) {
   const int kv = max_kv > 0 ? max_kv : 1;
   // (a request's queries are further heads of the group)
@@ -292,13 +285,27 @@ static long long cross_parts(int B, int H, int Hkv, int D, int max_q, int max_kv
   return ((long long)kv + *partition - 1) / *partition;
 }
 
+// Cross attention: whether a request's rows, max_q_len * G to a K/V head, go to the kernel
+// of single tokens, which reads the keys once for every 16 of them.  Up to 16 they do (32
+// requests of 4 on up to 1,500 keys, 16 heads, D = 64: 23 us and 43 by tiles of 128 rows; of
+// 16 alike); up to 48 where all its CTAs run at once, as it begins and ends quicker (one
+// request of 32 on 1,500 keys 7.9 and 12.6 us; eight on 4,000 keys 38.8 and 35.2).
+static bool cross_few(int B, int T, int H, int Hkv, int D, int max_q, int max_kv) {
+  const long long cols = (long long)max_q * (H / Hkv);
+  if (B > 65535 || (long long)T * H >= (1LL << 31) || cols > pk::kCrossFewMost) return false;
+  if (cols <= pk::kCrossFew) return true;
+  int pt;
+  const long long parts = cross_parts(B, H, Hkv, D, max_q, max_kv, &pt);
+  return B <= 2 && pk::grouped_decode_in_cluster(B, H * max_q, Hkv, parts > 1 ? parts : 2);
+}
+
 size_t pa_cross_attention_workspace_size(int B, int T, int H, int Hkv, int D, int max_q_len,
                                          int max_kv_len) {
   if (B <= 0 || T <= 0 || T > kMaxCount || !heads_ok(H, Hkv) || (D != 64 && D != 128) ||
       max_q_len <= 0 || max_kv_len <= 0 || max_kv_len > kMaxCount)
     return 0;
   if (max_q_len > T) max_q_len = T;
-  if (!cross_few(B, T, H, Hkv, max_q_len))
+  if (!cross_few(B, T, H, Hkv, D, max_q_len, max_kv_len))
     return pk::grouped_span(H / Hkv) == 0
                ? 0
                : pk::grouped_workspace_bytes(B, T, H, Hkv, D, max_kv_len);
@@ -322,7 +329,7 @@ pa_status pa_cross_attention(const void* q, const void* k, const void* v,
       max_kv_len > kMaxCount || !isfinite(scale) || !(scale > 0.f))
     return PA_ERR_INVALID;
   if (max_q_len > T) max_q_len = T;
-  const bool few = cross_few(B, T, H, Hkv, max_q_len);
+  const bool few = cross_few(B, T, H, Hkv, D, max_q_len, max_kv_len);
   if (!few && pk::grouped_span(H / Hkv) == 0) return PA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return PA_OK;
   if (!q_offsets || !kv_starts || !kv_lens || !out || !aligned16(out) || !rows_ok(q, q_stride, H, D))

@@ -308,14 +308,79 @@ __device__ __forceinline__ int small_div(int a, int b) {
   return (int)__fdividef((float)a + 0.5f, (float)b);
 }
 
-// A cluster to a request.
+// What is chosen from the beams' best keys, top [W][W], and the logarithms of their sums; a
+// lane of the first warp has its beam's score and the logit of its end.  cand: room for
+// [W][W]; all threads of a CTA, a barrier ahead of it.
+__device__ __forceinline__ void choose(const BeamSelectArgs& a, int b, uint32_t alive,
+                                       const Key* top, Key* cand, const double* s_lse,
+                                       const float* s_score, float score, float end_x) {
+  const int W = a.W, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool here = alive >> lane & 1;
+  // ---- candidates (0: none; what a finite number is ordered as is not)
+#pragma unroll 1
+  for (int w = warp; w < W; w += kWarps) {
+    const double lse = s_lse[w];
+    if (lane < W && (alive >> w & 1)) {
+      const Key k = top[w * W + lane];
+      cand[w * W + lane] =
+          k != 0 && lse > -INFINITY
+              ? ordered((double)s_score[w] + ((double)value_of(k) - lse) + 0.0)
+              : 0;
+    }
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  // ---- the choice: lane i holds the next candidate of beam i
+  int at = lane * W;
+  Key c = here ? cand[at] : 0, k = here ? top[at] : 0;
+  Key my_c = 0, my_key = 0, last_c = 0, last_key = 0;  // of place `lane`; of the last place
+  int my_beam = lane, last_beam = 0;
+#pragma unroll 1
+  for (int j = 0; j < W; ++j) {
+    const Key best = warp_max(c);
+    last_c = best;
+    if (best == 0) break;
+    last_beam = __ffs(__ballot_sync(kAll, c == best)) - 1;
+    last_key = __shfl_sync(kAll, k, last_beam);
+    if (lane == j) {
+      my_c = best;
+      my_beam = last_beam;
+      my_key = last_key;
+    }
+    if (lane == last_beam) {
+      ++at;
+      c = at < (lane + 1) * W ? cand[at] : 0;
+      k = at < (lane + 1) * W ? top[at] : 0;
+    }
+  }
+  if (lane >= W) return;
+  const int o = b * W + lane;
+  a.tokens[o] = my_key != 0 ? index_of(my_key) : a.pad;
+  a.parents[o] = my_beam;
+  a.new_scores[o] = my_c != 0 ? (float)unordered(my_c) : -INFINITY;
+  // Ends that are better than the last one chosen.
+  float ended = -INFINITY;
+  const double lse = here ? s_lse[lane] : -INFINITY;
+  if (lse > -INFINITY && end_x > -INFINITY) {
+    const double e = (double)score + ((double)end_x - lse) + 0.0;
+    const Key eo = ordered(e);
+    const bool ahead = last_c != 0 && lane == last_beam
+                           ? key_of(end_x, a.eos) > last_key
+                           : eo > last_c || (eo == last_c && lane < last_beam);
+    if (ahead) ended = (float)e;
+  }
+  a.ended[o] = ended;
+}
+
+// A cluster to a request, or to a group of its rows.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamSelectArgs a) {
   extern __shared__ __align__(16) uint8_t s_dyn[];  // the warps' rings, then what is merged
   __shared__ uint32_t s_wth[kWarps], s_kth[kWarps];
   __shared__ double s_lse[32];
   __shared__ float s_score[32];
-  const int ranks = a.ranks, b = blockIdx.x / ranks, rank = blockIdx.x - b * ranks, W = a.W;
+  const int ranks = a.ranks, cluster = blockIdx.x / ranks, rank = blockIdx.x - cluster * ranks;
+  const int b = cluster / a.groups, group = cluster - b * a.groups, W = a.W;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (ranks > 1) cluster_arrive();  // (nobody stores to a CTA that has not begun)
   if (lane == 0) s_wth[warp] = s_kth[warp] = 0;
@@ -323,8 +388,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamS
   pdl_launch_dependents();
   // A beam whose score is not finite is not there.
   const float score = lane < W ? a.scores[b * W + lane] : -INFINITY;
-  const bool here = isfinite(score);
-  const uint32_t alive = __ballot_sync(kAll, here);
+  bool here = isfinite(score);
+  uint32_t alive = __ballot_sync(kAll, here);
+  if (a.groups > 1) {  // every groups-th of them
+    const int nth = __popc(alive & ((1u << lane) - 1));
+    here = here && nth % a.groups == group;
+    alive = __ballot_sync(kAll, here);
+  }
   const int rows = __popc(alive);
   // What the choice needs of the beams, a lane to each.
   float end_x = -INFINITY;
@@ -418,61 +488,43 @@ __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamS
     }
   }
   __syncthreads();
-  // ---- candidates (0: none; what a finite number is ordered as is not)
+  if (a.groups > 1) {  // to be chosen from when all groups are done
 #pragma unroll 1
-  for (int i = warp; i < rows; i += kWarps) {
-    const int w = live_beam(i);
-    const double lse = s_lse[w];
-    if (lane < W) {
-      const Key k = top[w * W + lane];
-      cand[w * W + lane] =
-          k != 0 && lse > -INFINITY
-              ? ordered((double)s_score[w] + ((double)value_of(k) - lse) + 0.0)
-              : 0;
+    for (int i = warp; i < rows; i += kWarps) {
+      const int w = live_beam(i);
+      if (lane < W) a.ws_top[(size_t)(b * W + w) * W + lane] = top[w * W + lane];
+      if (lane == 0) a.ws_lse[b * W + w] = s_lse[w];
     }
+    return;
   }
+  choose(a, b, alive, top, cand, s_lse, s_score, score, end_x);
+}
+
+// The choice where the rows of a request were shared out among several clusters.
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps) beam_choose_kernel(const BeamSelectArgs a) {
+  __shared__ Key s_top[kMaxBeams * kMaxBeams], s_cand[kMaxBeams * kMaxBeams];
+  __shared__ double s_lse[32];
+  __shared__ float s_score[32];
+  const int b = blockIdx.x, W = a.W, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  const float score = lane < W ? a.scores[b * W + lane] : -INFINITY;
+  const bool here = isfinite(score);
+  const uint32_t alive = __ballot_sync(kAll, here);
+  float end_x = -INFINITY;
+  if (warp == 0) {
+    s_score[lane] = score;
+    s_lse[lane] = here ? a.ws_lse[b * W + lane] : -INFINITY;
+    if (here && a.eos >= 0)
+      end_x = to_float<T>(
+          static_cast<const T*>(a.logits)[(long long)(b * W + lane) * a.row_stride + a.eos]);
+  }
+#pragma unroll 1
+  for (int w = warp; w < W; w += kWarps)
+    if (lane < W && (alive >> w & 1)) s_top[w * W + lane] = a.ws_top[(size_t)(b * W + w) * W + lane];
   __syncthreads();
-  if (warp > 0) return;
-  // ---- the choice: lane i holds the next candidate of beam i
-  int at = lane * W;
-  Key c = here ? cand[at] : 0, k = here ? top[at] : 0;
-  Key my_c = 0, my_key = 0, last_c = 0, last_key = 0;  // of place `lane`; of the last place
-  int my_beam = lane, last_beam = 0;
-#pragma unroll 1
-  for (int j = 0; j < W; ++j) {
-    const Key best = warp_max(c);
-    last_c = best;
-    if (best == 0) break;
-    last_beam = __ffs(__ballot_sync(kAll, c == best)) - 1;
-    last_key = __shfl_sync(kAll, k, last_beam);
-    if (lane == j) {
-      my_c = best;
-      my_beam = last_beam;
-      my_key = last_key;
-    }
-    if (lane == last_beam) {
-      ++at;
-      c = at < (lane + 1) * W ? cand[at] : 0;
-      k = at < (lane + 1) * W ? top[at] : 0;
-    }
-  }
-  if (lane >= W) return;
-  const int o = b * W + lane;
-  a.tokens[o] = my_key != 0 ? index_of(my_key) : a.pad;
-  a.parents[o] = my_beam;
-  a.new_scores[o] = my_c != 0 ? (float)unordered(my_c) : -INFINITY;
-  // Ends that are better than the last one chosen.
-  float ended = -INFINITY;
-  const double lse = here ? s_lse[lane] : -INFINITY;
-  if (lse > -INFINITY && end_x > -INFINITY) {
-    const double e = (double)score + ((double)end_x - lse) + 0.0;
-    const Key eo = ordered(e);
-    const bool ahead = last_c != 0 && lane == last_beam
-                           ? key_of(end_x, a.eos) > last_key
-                           : eo > last_c || (eo == last_c && lane < last_beam);
-    if (ahead) ended = (float)e;
-  }
-  a.ended[o] = ended;
+  choose(a, b, alive, s_top, s_cand, s_lse, s_score, score, end_x);
 }
 
 int dynamic_bytes(int W, int ranks) {
@@ -490,7 +542,7 @@ cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.ranks * a.B);
+  cfg.gridDim = dim3((unsigned)a.ranks * a.groups * a.B);
   cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -501,7 +553,12 @@ cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim = {(unsigned)a.ranks, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = a.ranks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess || a.groups == 1) return e;
+  cfg.gridDim = dim3(a.B);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, beam_choose_kernel<T>, a);
 }
 
 template <typename T>
@@ -513,17 +570,26 @@ cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// CTAs of a request: as many as give every SM one, which their rings see to as well (two
-// to an SM share its issue slots, and the second may come to lie beside the first while
-// other SMs are idle), and no more than there are chunks for their warps.  Clusters of 16
-// take one GPU's processing cluster each: for few requests.
-int beam_select_ranks(int B, int W, int V) {
+// Clusters of a request, their CTAs.  As many CTAs as give every SM one, which their rings
+// see to as well (two to an SM share its issue slots, and the second may come to lie beside
+// the first while other SMs are idle), and no more than there are chunks for their warps.
+// A cluster of 16 takes one of the GPU's processing clusters, few of which have that many
+// SMs: for few requests.  Where its warps would have four chunks or more, clusters of 8 take
+// a part of the rows each, which are chosen from in a second launch (one request of 16 x
+// 256,000 logits 27 us by clusters of 16).
+void beam_select_shape(int B, int W, int V, int* groups, int* ranks) {
   const int nsm = sm_count() > 0 ? sm_count() : 152;
   const long long chunks = (long long)W * ((V - 1) / kChunk + 1);
   const int limit = B <= 4 ? kMaxCluster : 8, least = W > kWarps ? 2 : 1;  // a warp to a row
   long long c = (chunks + kWarps - 1) / kWarps;
   if (c > nsm / B) c = nsm / B;
-  return c > limit ? limit : c > least ? (int)c : least;
+  *ranks = c > limit ? limit : c > least ? (int)c : least;
+  *groups = 1;
+  if (*ranks == kMaxCluster && chunks >= 4 * kMaxCluster * kWarps) {
+    const int most = nsm / (8 * B), rows = (W + most - 1) / most;  // of a cluster
+    *groups = (W + rows - 1) / rows;
+    if (*groups > 1) *ranks = 8;
+  }
 }
 
 cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t stream) {

@@ -24,9 +24,12 @@ struct BeamSelectArgs {
   float* ended;  // [B, W] by beam
   int32_t* status;
   int B, W, V, eos, pad, dtype;
-  int ranks;  // CTAs of a request
+  int ranks, groups;  // CTAs of a cluster, clusters of a request
+  // With groups > 1, per beam: its best keys and the logarithm of its sum.
+  unsigned long long* ws_top;  // [B * W][W]
+  double* ws_lse;              // [B * W]
 };
-int beam_select_ranks(int B, int W, int V);
+void beam_select_shape(int B, int W, int V, int* groups, int* ranks);
 cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t stream);
 
 // Block tables that follow the beams (beam_tables.cu).

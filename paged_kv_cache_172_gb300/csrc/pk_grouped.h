@@ -116,7 +116,9 @@ struct GroupedDecodeArgs {
   float scale_log2;
   bool bf16;
 };
-constexpr int kCrossFewColumns = 16;  // (query, head) pairs of a request and K/V head
+// (query, head) pairs of a request and K/V head that the kernel of single tokens serves in
+// cross attention: always, and where its CTAs run at once.
+constexpr int kCrossFew = 16, kCrossFewMost = 48;
 int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context);
 // Whether that many partitions merge inside the launch, without a workspace.
 bool grouped_decode_in_cluster(int B, int H, int Hkv, long long parts);

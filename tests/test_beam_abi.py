@@ -69,8 +69,13 @@ def test_select_refusals(lib):
                dict(e=None)):
         assert select(lib, **kw) == pk.PA_ERR_INVALID, kw
     assert select(lib, W=33) == pk.PA_ERR_UNSUPPORTED
-    need = lib.pa_beam_select_workspace_size(2, 4, 100)
-    assert need == 0
+    assert lib.pa_beam_select_workspace_size(2, 4, 100) == 0
+    need = lib.pa_beam_select_workspace_size(1, 16, 200000)
+    wide = dict(B=1, W=16, V=200000, stride=200000)
+    if need > 0:  # (on a GPU of many SMs, as without one)
+        assert select(lib, ws=None, **wide) == pk.PA_ERR_WORKSPACE
+        assert select(lib, wsb=need - 1, **wide) == pk.PA_ERR_WORKSPACE
+        assert select(lib, ws=P + 8, **wide) == pk.PA_ERR_INVALID
     assert select(lib, B=0, x=None) == pk.PA_OK
     for a in ((0, 4, 100), (2, 33, 100), (2, 4, 0), (-1, 4, 100), (2 ** 20, 2, 100)):
         assert lib.pa_beam_select_workspace_size(*a) == 0, a

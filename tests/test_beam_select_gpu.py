@@ -77,6 +77,7 @@ def test_beams(W, dtype):
 @pytest.mark.parametrize("B,W,V,stride", [(1, 4, 32000, None), (7, 4, 50001, None),
                                          (2, 5, 50001, 50048), (2, 3, 128000, 128001),
                                          (1, 1, 300000, None), (1, 32, 100003, None),
+                                         (2, 16, 140001, None), (1, 24, 260000, None),
                                          (40, 16, 4099, None), (300, 2, 513, 520)])
 def test_vocabularies(B, W, V, stride, dtype):
     """One row cut into ranges, rows of several chunks, rows that begin anywhere."""
@@ -246,6 +247,20 @@ def test_in_place_and_history():
             assert torch.equal(out.ended_scores, end[i])
             now = out.scores
         assert torch.equal(now, live)
+
+
+def test_groups_of_rows():
+    """Few requests, many beams: rows shared out among clusters, some of them dead."""
+    B, W, V = 1, 16, 140000
+    need = pk.pa_beam_select_workspace_size(B, W, V)
+    assert need > 0
+    for dead in ([], [0], [15], [3, 4, 7, 8, 11], list(range(1, 16)), list(range(16))):
+        x, s = made(B, W, V, BF16, seed=len(dead))
+        s[0, dead] = -INF
+        check(x, s, eos=7)
+    with pytest.raises(pk.PagedKVError) as e:
+        run(x, s, workspace=torch.empty(need - 8, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == pk.PA_ERR_WORKSPACE
 
 
 def test_deterministic_and_streams():
