@@ -12,10 +12,13 @@
 // little code; every lane keeps a running maximum and sum.  The piece's W best are a
 // sorted list of (ordered value, ~index) keys over the lanes, into which values that reach
 // a threshold are inserted one by one: the W-th of the list, or what the row's other warps
-// of the CTA know, and in a chunk where many values reach that (the first one) the W-th
-// largest of the lanes' maxima.  The cluster's first CTA then merges the pieces' lists by
-// beam and the beams' lists, in order, by as many rounds of a maximum over the lanes as
-// there are beams.
+// of the CTA know.  In a chunk where many values reach that (the first one) it is raised to
+// the W-th largest of the lanes' maxima first (W rounds), or, for more than 8 beams, these
+// are merged into the list as a whole until few are left (W rounds and the insertions after
+// them against the merges: 32 beams of 260,000 logits 66 -> 43 us, 16 of 256,000 27.6 ->
+// 25.4, 32 requests of 16 83.6 -> 82.2; a kernel of its own, since its code costs the small
+// calls 0.2 us).  The cluster's first CTA then merges the pieces' lists by beam and the
+// beams' lists, in order, by as many rounds of a maximum over the lanes as there are beams.
 //
 // Rounding: sums in fp32, candidates in 64 bits (two beams' can be nearer than fp32 tells
 // apart), the scores once to fp32.  A sum goes by the values' index and not by the row's
@@ -42,6 +45,7 @@ constexpr int kEach = 16;           // values of a lane and chunk
 constexpr int kChunk = 32 * kEach;  // values of a warp's chunk
 constexpr int kRing = 8320;         // bytes of a warp's ring: four or eight chunks and 16 each
 constexpr int kMany = 64;           // values of a chunk that are too many to be inserted
+constexpr int kFewBeams = 8;        // most for which W rounds of a maximum are done
 constexpr int kMaxPieces = 64;      // of a row: two lists to a lane of the merge
 constexpr int kMaxCluster = 16;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -181,6 +185,27 @@ __device__ __forceinline__ float pick(const float (&x)[kEach], int i) {
   return i & 1 ? y[1] : y[0];
 }
 
+// The 32 largest of two keys a lane, in order: mine in order, other not.  A bitonic sort of
+// the others, the larger of every pair of opposite places, a bitonic merge.
+__device__ __forceinline__ Key merge_lanes(Key mine, Key other) {
+  const int lane = threadIdx.x & 31;
+  Key x = other;
+#pragma unroll 1
+  for (int k = 2; k <= 64; k <<= 1) {
+    if (k == 64) {
+      const Key y = __shfl_xor_sync(kAll, x, 31);
+      x = mine > y ? mine : y;
+    }
+#pragma unroll 1
+    for (int j = min(k, 32) >> 1; j > 0; j >>= 1) {
+      const Key y = __shfl_xor_sync(kAll, x, j);
+      const bool larger = ((lane & k) == 0) == ((lane & j) == 0);
+      x = (x > y) == larger ? x : y;
+    }
+  }
+  return x;
+}
+
 __device__ __forceinline__ float largest(const float (&x)[kEach]) {
   float m = fmaxf(x[0], x[1]);
 #pragma unroll
@@ -197,7 +222,7 @@ struct Known {
 
 // A warp's piece [begin, end) of a row: its W best, in order, a lane to each (0: none), and
 // its maximum and sum.  me: the warp among those of its row.
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool FEW>
 __device__ __forceinline__ Key scan(const T* row, int begin, int end, int eos, int W,
                                     uint8_t* ring, Known known, int me, float2& max_sum) {
   using P = Piece<T, VEC>;
@@ -250,18 +275,36 @@ __device__ __forceinline__ Key scan(const T* row, int begin, int end, int eos, i
         max(__reduce_max_sync(kAll, other ? *(volatile uint32_t*)(known.wth + lane) : 0u), least);
     uint32_t hits;  // of the lane's values, those that reach t
 #pragma unroll 1
-    for (bool again = true;; again = false) {
+    for (;;) {
       t = fmaxf(t, unordered(max(reached, ordered(-FLT_MAX))));
       hits = 0;
 #pragma unroll
       for (int j = 0; j < kEach; ++j) hits |= x[j] >= t ? 1u << j : 0u;
-      if (!again || __reduce_add_sync(kAll, (unsigned)__popc(hits)) <= kMany) break;
-      // The lanes' maxima, largest first: W values reach the W-th.
-      uint32_t o = ordered(mt);
+      if (__reduce_add_sync(kAll, (unsigned)__popc(hits)) <= kMany) break;
+      if constexpr (FEW) {
+        // The lanes' maxima, largest first: W values reach the W-th.
+        uint32_t o = ordered(mt);
 #pragma unroll 1
-      for (int j = 0; j < W; ++j) {
-        reached = __reduce_max_sync(kAll, o);
-        if (lane == __ffs(__ballot_sync(kAll, o == reached)) - 1) o = 0;
+        for (int j = 0; j < W; ++j) {
+          reached = __reduce_max_sync(kAll, o);
+          if (lane == __ffs(__ballot_sync(kAll, o == reached)) - 1) o = 0;
+        }
+        if (unordered(reached) <= t) break;  // (equal ones: all of them)
+      } else {
+        // The lanes' maxima into the list at once.
+        int at = 0;
+#pragma unroll
+        for (int j = kEach - 1; j >= 0; --j) at = x[j] == mt ? j : at;
+        const Key key = mt >= t ? key_of(mt, P::index(base, at)) : 0;
+        if (!__any_sync(kAll, key > __shfl_sync(kAll, mine, W - 1))) {
+          hits = 0;  // (equal ones, behind those that are held)
+          break;
+        }
+        mine = merge_lanes(mine, key);
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) x[j] = j == at ? -INFINITY : x[j];
+        mt = largest(x);
+        reached = (uint32_t)(__shfl_sync(kAll, mine, W - 1) >> 32);
       }
     }
 #pragma unroll 1
@@ -373,7 +416,7 @@ __device__ __forceinline__ void choose(const BeamSelectArgs& a, int b, uint32_t 
 }
 
 // A cluster to a request, or to a group of its rows.
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool FEW>
 __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamSelectArgs a) {
   extern __shared__ __align__(16) uint8_t s_dyn[];  // the warps' rings, then what is merged
   __shared__ uint32_t s_wth[kWarps], s_kth[kWarps];
@@ -430,7 +473,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamS
     const int n = min((r + 1) * pieces - rank * per, per) - first;
     const Known known = {&s_wth[first], &s_kth[first], n, small_div(W + n - 1, n)};
     float2 ml;
-    const Key mine = scan<T, VEC>(x, begin, end, a.eos, W, s_dyn + warp * kRing, known,
+    const Key mine = scan<T, VEC, FEW>(x, begin, end, a.eos, W, s_dyn + warp * kRing, known,
                                   warp - first, ml);
     if (ranks > 1) cluster_wait();
     if (lane < W) store_cluster(keys + task * W + lane, 0, mine);
@@ -531,9 +574,9 @@ int dynamic_bytes(int W, int ranks) {
   return kWarps * kRing + ranks * kWarps * (W + 1) * 8 + 2 * W * W * 8;
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool FEW>
 cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
-  constexpr auto kern = beam_select_kernel<T, VEC>;
+  constexpr auto kern = beam_select_kernel<T, VEC, FEW>;
   const int smem = dynamic_bytes(a.W, a.ranks);
   cudaError_t e = ensure_dynamic_smem<kern>(dynamic_bytes(kMaxBeams, kMaxCluster));
   if (e != cudaSuccess) return e;
@@ -565,7 +608,9 @@ template <typename T>
 cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
   const bool vec = (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 &&
                    (a.B * a.W == 1 || a.row_stride * (int)sizeof(T) % 16 == 0);
-  return vec ? launch_t<T, true>(a, stream) : launch_t<T, false>(a, stream);
+  if (a.W <= kFewBeams)
+    return vec ? launch_t<T, true, true>(a, stream) : launch_t<T, false, true>(a, stream);
+  return vec ? launch_t<T, true, false>(a, stream) : launch_t<T, false, false>(a, stream);
 }
 
 }  // namespace
@@ -575,8 +620,7 @@ cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
 // the first while other SMs are idle), and no more than there are chunks for their warps.
 // A cluster of 16 takes one of the GPU's processing clusters, few of which have that many
 // SMs: for few requests.  Where its warps would have four chunks or more, clusters of 8 take
-// a part of the rows each, which are chosen from in a second launch (one request of 16 x
-// 256,000 logits 27 us by clusters of 16).
+// a part of the rows each, which are chosen from in a second launch.
 void beam_select_shape(int B, int W, int V, int* groups, int* ranks) {
   const int nsm = sm_count() > 0 ? sm_count() : 152;
   const long long chunks = (long long)W * ((V - 1) / kChunk + 1);
