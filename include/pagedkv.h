@@ -419,7 +419,8 @@ pa_status pa_kv_cache_write(const pa_half *k, const pa_half *v,
  * becomes a bit-exact copy of block pairs[i][0] (all block_size * H * D
  * values).  Destinations must be distinct and no destination may be the
  * source of another pair in the same call (otherwise the result is
- * undefined); src == dst is a no-op.
+ * undefined); src == dst is a no-op.  The values are copied as 16 bits each, so the
+ * bf16 pools of the calls with grouped heads (H: their K/V heads) are copied as well.
  *
  * pairs [N, 2] int64 (src, dst).
  * ------------------------------------------------------------------------- */

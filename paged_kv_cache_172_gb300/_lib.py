@@ -530,9 +530,10 @@ def pa_kv_cache_write(k, v, slot_mapping, k_cache, v_cache, status=None, stream=
 
 @_one_device
 def pa_block_copy(k_cache, v_cache, pairs, status=None, stream=None):
-    """Copy whole physical blocks: pairs [N,2] int64 (src, dst)."""
-    _need(k_cache, torch.float16, "k_cache", 4)
-    _need(v_cache, torch.float16, "v_cache", 4)
+    """Copy whole physical blocks of fp16 or bf16 pools: pairs [N,2] int64 (src, dst)."""
+    half = torch.bfloat16 if getattr(k_cache, "dtype", None) == torch.bfloat16 else torch.float16
+    _need(k_cache, half, "k_cache", 4)
+    _need(v_cache, half, "v_cache", 4)
     _need(pairs, torch.int64, "pairs", 2)
     NB, bs, H, D = k_cache.shape
     if v_cache.shape != k_cache.shape or pairs.shape[1] != 2:

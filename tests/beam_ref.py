@@ -1,19 +1,27 @@
 """Plain implementations of the beam calls, one element after the other, in 64 bits.
 
 pa_beam_select against them.  Which candidates are chosen is exact within a beam; between
-beams the kernel's log-sum-exp is off by at most lse_error(V): each weight by 2^-21 (the
-exponential) and 2^-23 a nat (the difference from the maximum and its product with log2 e,
-2^-24 each, of at most 24 nats that still count), a thread's sum of V / 512 weights and its
-rescalings by 2^-24 a step, a warp's by 5 of those, all relative to the sum.  So a chosen
-list that differs from the reference is right when every place's score is within that of
-the reference's; scores are compared with it and half a step of fp32."""
+beams the kernel's log-sum-exp is off by at most lse_error(V).  Relative to the sum:
+  24 * 2^-23       a weight's argument: the difference from the maximum and its product with
+                   log2 e, 2^-24 each, of at most 24 nats that still count, whether taken at
+                   once or in the steps of its rescalings
+  2^-22 + 2^-24    each exponential, with its product: a weight's own, one to each rise of its
+                   lane's maximum (one a chunk of 512 at most; 24 are not seen in a lane of
+                   values in random order), one where lanes are joined and one where pieces are
+  2^-24            each addition: 8 within a chunk, V / 512 chunks and 1, 5 where lanes are
+                   joined and 6 where pieces are
+and 2^-25 of the logarithm.  So a chosen list that differs from the reference is right when
+every place's score is within that of the reference's; scores are compared with it and half
+a step of fp32."""
 import math
 
 import numpy as np
 
 
-def lse_error(V):
-    return 24 * 2.0 ** -23 + 2.0 ** -21 + (V / 512 + 16 + 5) * 2.0 ** -24
+def lse_error(V, rises=24):
+    chunks = V // 512 + 1
+    return (24 * 2.0 ** -23 + (3 + min(rises, chunks)) * (2.0 ** -22 + 2.0 ** -24)
+            + (chunks + 20) * 2.0 ** -24 + 2.0 ** -25)
 
 
 def select(logits, scores, eos=-1, pad=0):
@@ -51,6 +59,37 @@ def select(logits, scores, eos=-1, pad=0):
             if len(cand) < W or e < cand[-1]:
                 ended[b, e[1]] = -e[0]
     return dict(tokens=tokens, parents=parents, scores=best, ended=ended, bad=bad)
+
+
+def compare(out, logits, scores, eos, pad, rises=24):
+    """What pa_beam_select gave (tensors) against select()."""
+    x, s = logits.double().cpu().numpy(), scores.cpu().numpy()
+    ref = select(x, s, eos, pad)
+    V = logits.shape[1]
+    tol = lse_error(V, rises)
+    got = [t.cpu().numpy() for t in out]
+    fine = np.isfinite(ref["scores"])
+    assert (np.isfinite(got[2]) == fine).all()
+    top = np.abs(ref["scores"], where=fine, out=np.zeros_like(ref["scores"])).max()
+    half = 2.0 ** -24 * top + tol
+    assert (np.abs(got[2][fine] - ref["scores"][fine]) <= half).all()
+    # a different choice only where two beams' candidates are as near as the sums' error
+    B, W = s.shape
+    for b, j in zip(*np.nonzero((got[0] != ref["tokens"]) | (got[1] != ref["parents"]))):
+        w, v = int(got[1][b, j]), int(got[0][b, j])
+        assert fine[b, j] and 0 <= v < V and v != eos, (b, j, w, v)
+        row = x[b * W + w]
+        m = row.max()
+        c = s[b, w] + (row[v] - (m + math.log(np.exp(row - m).sum())))
+        assert abs(c - ref["scores"][b, j]) <= 2 * tol, (b, j, w, v)
+        assert len({(int(p), int(t)) for p, t in zip(got[1][b], got[0][b])}) == W
+    ends = np.isfinite(ref["ended"])
+    off = ends != np.isfinite(got[3])
+    if off.any():
+        b, w = (i[0] for i in np.nonzero(off))
+        assert False, (b, w, got[3][b], ref["ended"][b], ref["scores"][b])
+    top = np.abs(ref["ended"], where=ends, out=np.zeros_like(ref["ended"])).max()
+    assert (np.abs(got[3][ends] - ref["ended"][ends]) <= 2.0 ** -24 * top + tol).all()
 
 
 def reorder(parents, tables, lens, ring, state, bs, shared=None):

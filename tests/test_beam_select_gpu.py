@@ -1,12 +1,11 @@
 """pa_beam_select against a plain implementation in 64 bits (beam_ref)."""
 import math
 
-import numpy as np
 import pytest
 import torch
 
-import beam_ref
 import paged_kv_cache_172_gb300 as pk
+from beam_ref import compare
 
 pytestmark = pytest.mark.gpu
 F32, BF16, FP16 = torch.float32, torch.bfloat16, torch.float16
@@ -19,41 +18,11 @@ def run(logits, scores, eos=-1, pad=-7, **kw):
     return out, status.item()
 
 
-def check(logits, scores, eos=-1, pad=-7, flags=0, **kw):
+def check(logits, scores, eos=-1, pad=-7, flags=0, rises=24, **kw):
     out, got = run(logits, scores, eos, pad, **kw)
     assert got == flags
-    compare(out, logits, scores, eos, pad)
+    compare(out, logits, scores, eos, pad, rises)
     return out
-
-
-def compare(out, logits, scores, eos, pad):
-    x, s = logits.double().cpu().numpy(), scores.cpu().numpy()
-    ref = beam_ref.select(x, s, eos, pad)
-    V = logits.shape[1]
-    tol = beam_ref.lse_error(V)
-    got = [t.cpu().numpy() for t in out]
-    fine = np.isfinite(ref["scores"])
-    assert (np.isfinite(got[2]) == fine).all()
-    top = np.abs(ref["scores"], where=fine, out=np.zeros_like(ref["scores"])).max()
-    half = 2.0 ** -24 * top + tol
-    assert (np.abs(got[2][fine] - ref["scores"][fine]) <= half).all()
-    # a different choice only where two beams' candidates are as near as the sums' error
-    B, W = s.shape
-    for b, j in zip(*np.nonzero((got[0] != ref["tokens"]) | (got[1] != ref["parents"]))):
-        w, v = int(got[1][b, j]), int(got[0][b, j])
-        assert fine[b, j] and 0 <= v < V and v != eos, (b, j, w, v)
-        row = x[b * W + w]
-        m = row.max()
-        c = s[b, w] + (row[v] - (m + math.log(np.exp(row - m).sum())))
-        assert abs(c - ref["scores"][b, j]) <= 2 * tol, (b, j, w, v)
-        assert len({(int(p), int(t)) for p, t in zip(got[1][b], got[0][b])}) == W
-    ends = np.isfinite(ref["ended"])
-    off = ends != np.isfinite(got[3])
-    if off.any():
-        b, w = (i[0] for i in np.nonzero(off))
-        assert False, (b, w, got[3][b], ref["ended"][b], ref["scores"][b])
-    top = np.abs(ref["ended"], where=ends, out=np.zeros_like(ref["ended"])).max()
-    assert (np.abs(got[3][ends] - ref["ended"][ends]) <= 2.0 ** -24 * top + tol).all()
 
 
 def made(B, W, V, dtype, seed, stride=None, first=0.0):
@@ -148,13 +117,13 @@ def test_orders_that_fill_the_list(dtype):
                         torch.sin(ramp)]).to(dtype)
     for W in (2, 4, 8):
         s = -torch.arange(8, device="cuda").float().reshape(8 // W, W) * 0.0137
-        check(rows, s, eos=V - 1)
+        check(rows, s, eos=V - 1, rises=V)
     for W in (1, 32):
         for r in rows:
             x = r.repeat(W, 1)
             s = torch.full((1, W), -INF, device="cuda")
             s[0, W - 1] = -1.0
-            check(x, s, eos=17)
+            check(x, s, eos=17, rises=V)
 
 
 @pytest.mark.parametrize("V", [40, 20000])
