@@ -701,8 +701,8 @@ pa_status pa_decode_grouped(const void *q, const void *k_cache, const void *v_ca
  * logits [B * W] rows of V in dtype (PA_F32 too), row_stride >= V elements apart
  * scores [B, W] float32; V at most 2^28; eos_token below V
  * workspace: at least pa_beam_select_workspace_size(B, W, V) bytes, 16-byte aligned, else
- * PA_ERR_WORKSPACE; the size is 0 but for few requests with many beams and a large
- * vocabulary, and depends on the SM count of the current device.
+ * PA_ERR_WORKSPACE; the size is 0 but for small batches with several beams and a large
+ * vocabulary, and depends on the current device.
  * W above 32 returns PA_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 size_t pa_beam_select_workspace_size(int B, int W, int V);
