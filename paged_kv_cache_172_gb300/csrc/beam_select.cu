@@ -617,9 +617,7 @@ cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// How many clusters of `ranks` CTAs the current device holds at once, an SM to a CTA (its
-// processing clusters have SMs left over; kept per device).
-static int clusters_at_once(int ranks) {
+int clusters_at_once(int ranks) {
   static std::atomic<int> cached[64][kMaxCluster + 1];
   const int nsm = sm_count() > 0 ? sm_count() : 152;
   int dev = 0, n = 0;

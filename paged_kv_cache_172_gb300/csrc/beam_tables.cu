@@ -669,10 +669,10 @@ cudaError_t launch_beam_reorder(const BeamReorderArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_beam_backtrack(const BeamBacktrackArgs& a, cudaStream_t stream) {
-  // CTAs of a request: as many as give every SM one, 256 steps each at least.  (An SM has
+  // CTAs of a request: as many as find an SM each, 256 steps each at least.  (An SM has
   // some 500 of its pieces of a step under way at a time, whatever their size.)
-  const int nsm = sm_count() > 0 ? sm_count() : 152;
-  const int ranks = std::min({kMaxRanks, std::max(nsm / a.B, 1), (a.S + 255) / 256});
+  int ranks = std::min(kMaxRanks, (a.S + 255) / 256);
+  while (ranks > 1 && clusters_at_once(ranks) < a.B) --ranks;
   // Their steps: what fits shared memory.
   const int each = 4 * a.W + 2 * step_bytes(a.W) + 2 * a.K;  // (a bound: ranks <= kPiece)
   int steps = kBackBytes / each / kPiece * kPiece;

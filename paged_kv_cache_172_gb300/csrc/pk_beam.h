@@ -29,6 +29,9 @@ struct BeamSelectArgs {
   unsigned long long* ws_top;  // [B * W][W]
   double* ws_lse;              // [B * W]
 };
+// How many clusters of `ranks` CTAs the current device holds at once, an SM to each CTA (its
+// processing clusters have SMs left over); kept per device.
+int clusters_at_once(int ranks);
 void beam_select_shape(int B, int W, int V, int* groups, int* ranks);
 cudaError_t launch_beam_select(const BeamSelectArgs& a, cudaStream_t stream);
 

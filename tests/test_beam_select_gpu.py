@@ -232,6 +232,16 @@ def test_groups_of_rows():
     assert e.value.code == pk.PA_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("B,W,V", [(1, 32, 33000), (2, 16, 60001), (8, 32, 20001), (5, 8, 40000),
+                                   (12, 8, 30000), (18, 4, 64000), (20, 5, 50257), (40, 8, 20000),
+                                   (80, 16, 5001), (100, 3, 9000)])
+def test_shares_of_the_device(B, W, V):
+    """Requests that take clusters of different sizes, several or a part of one each, and more
+    than the device holds at once."""
+    x, s = made(B, W, V, BF16 if B % 2 else F32, seed=B + W, first=0.3)
+    check(x, s, eos=V - 2)
+
+
 def test_deterministic_and_streams():
     x, s = made(16, 8, 60001, BF16, seed=9)
     first, _ = run(x, s, eos=5)
