@@ -370,6 +370,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   // 64 keys early (one prompt of 8,192 353 -> 343 us); with the paged loader's code
   // beside it the longer loops cost more than that (16 x 2,048 keys 457 -> 470 us).
   constexpr int kHalves = PAGED ? 1 : 2;
+  // With an S region to each tile the softmax is the longest chain, which the second
+  // handing over lengthens: P is stored in halves there, but waited for and told once
+  // (8 encoder sequences of 500-4,096, 16 heads, 177.3 -> 166.9 us; stored at once 169.2).
+  constexpr bool kTold = kHalves > 1 && !kOwnS<D, F>;  // in halves
   constexpr float kRaise = kRaiseLog2<T>;
   constexpr uint32_t kIdS = tc::idesc_f16_f32(kTile, kTile, false, false) | operand_type<T>();
   constexpr uint32_t kIdO = tc::idesc_f16_f32(kTile, D, false, true) | operand_type<T>();
@@ -474,6 +478,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       const bool live = my_tok < (x ? it.toks_b : it.toks_a);  // a row of this sequence
       const int pos = F == kCross ? pos0 : pos0 + my_tok;  // last key that the row sees
       float m = -INFINITY, l = 0.f;
+      // (Where there are registers for it, summed up behind the last tile: 166.9 -> 164.7.)
+      float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       for (int j = 0; j < ntile; ++j, ++done) {
         if (!(ok = __all_sync(kAll, mbar_wait(&s_full[x], done & 1)))) break;
         tc::fence_after_sync();
@@ -518,12 +524,19 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           alpha = ex2_approx(m - m_new);
           m = m_new;
           l *= alpha;
+          if constexpr (kOwnS<D, F>) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) rs[i] *= alpha;
+          }
         }
         // A row that has seen masked keys alone (a part whose range starts past
         // its position) has m = -inf, and -inf + inf is NaN: taken with maximum 0
         // its weights are all zero and its partial row is empty.
         const float neg_m = m == -INFINITY ? 0.f : kRaise - m;
-        float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if constexpr (!kOwnS<D, F>) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) rs[i] = 0.f;
+        }
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
           constexpr int kC = 4 / kHalves;
@@ -558,15 +571,19 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 #pragma unroll
           for (int c = kC * h; c < kC * h + kC; ++c)  // the packed pairs, as in the registers
             tc::st_32x16(tmem + t_lane + kColP + x * (kTile / 2) + c * 16, r[c]);
+          if (!kTold && h + 1 < kHalves) continue;
           tc::wait_st();
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(h + 1 == kHalves ? &p_full[x] : &p_half[x]);
         }
         if (!ok) break;
-        l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+        if constexpr (!kOwnS<D, F>)
+          l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
       }
       if (!ok) break;
+      if constexpr (kOwnS<D, F>)
+        l = ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
       if (ntile > 0) {  // the last P V
         if (!(ok = __all_sync(kAll, mbar_wait(&pv_done[x], (done - 1) & 1)))) break;
         tc::fence_after_sync();
@@ -963,11 +980,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
               const uint32_t ta = tmem + kColP + x * (kTile / 2);
               // (P of an item's first tile is stored behind the item before's last
               // read of O by the same warps: O may then be overwritten.)
-              if (!(ok = mbar_wait(kHalves > 1 ? &p_half[x] : &p_full[x], done[x] & 1))) continue;
+              if (!(ok = mbar_wait(kTold ? &p_half[x] : &p_full[x], done[x] & 1))) continue;
               tc::fence_after_sync();
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk) {
-                if (kHalves > 1 && kk == kTile / 32) {
+                if (kTold && kk == kTile / 32) {
                   if (!(ok = mbar_wait(&p_full[x], done[x] & 1))) break;
                   tc::fence_after_sync();
                 }
