@@ -614,7 +614,7 @@ pa_status pa_chunk_attention(const void *q, const void *k_cache, const void *v_c
  * q_offsets [B+1] int32 as for pa_prompt_attention; kv_starts, kv_lens [B] int32
  * max_q_len, max_kv_len  host-side bounds on the requests' lengths: a request past one
  *           of them, or whose keys leave [0, Tk), is flagged PA_DEV_BAD_CONTEXT and its
- *           rows are zeros (max_q_len above T counts as T)
+ *           rows are zeros (max_q_len above T counts as T, 0 as 1)
  * D in {64, 128}; scale > 0.  With max_q_len * H / Hkv at most 16 (up to 48 in small
  * calls; B at most 65535) the kernel of pa_decode_grouped serves the call, to its
  * precision; otherwise that of pa_prompt_attention, to its, and H / Hkv is at most 128

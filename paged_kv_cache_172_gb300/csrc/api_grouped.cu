@@ -302,9 +302,9 @@ static bool cross_few(int B, int T, int H, int Hkv, int D, int max_q, int max_kv
 size_t pa_cross_attention_workspace_size(int B, int T, int H, int Hkv, int D, int max_q_len,
                                          int max_kv_len) {
   if (B <= 0 || T <= 0 || T > kMaxCount || !heads_ok(H, Hkv) || (D != 64 && D != 128) ||
-      max_q_len <= 0 || max_kv_len <= 0 || max_kv_len > kMaxCount)
+      max_q_len < 0 || max_kv_len <= 0 || max_kv_len > kMaxCount)
     return 0;
-  if (max_q_len > T) max_q_len = T;
+  max_q_len = max_q_len > T ? T : max_q_len > 0 ? max_q_len : 1;
   if (!cross_few(B, T, H, Hkv, D, max_q_len, max_kv_len))
     return pk::grouped_span(H / Hkv) == 0
                ? 0
@@ -328,7 +328,7 @@ pa_status pa_cross_attention(const void* q, const void* k, const void* v,
   if (T < 0 || T > kMaxCount || Tk < 0 || Tk > kMaxCount || max_q_len < 0 || max_kv_len < 0 ||
       max_kv_len > kMaxCount || !isfinite(scale) || !(scale > 0.f))
     return PA_ERR_INVALID;
-  if (max_q_len > T) max_q_len = T;
+  max_q_len = max_q_len > T ? T : max_q_len > 0 ? max_q_len : 1;
   const bool few = cross_few(B, T, H, Hkv, D, max_q_len, max_kv_len);
   if (!few && pk::grouped_span(H / Hkv) == 0) return PA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return PA_OK;

@@ -205,6 +205,21 @@ def test_no_states_at_all(H, Hkv):
     assert (out == 0).all() and status.item() == pk.PA_DEV_BAD_CONTEXT
 
 
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (40, 2)])
+def test_no_queries(H, Hkv):
+    """Requests without queries under a bound of none: nothing is written.  (One query counts
+    as within it.)"""
+    c = Cross([0, 0, 0], [300, 5000, 1], H, Hkv, 64, BF16, behind=4, seed=18)
+    out = torch.full_like(c.q, 7.0)
+    c.run(max_q=0, out=out)
+    assert (out == 7).all() and c.status.item() == 0
+    c = Cross([1, 0, 2], [300, 5000, 1], H, Hkv, 64, BF16, seed=19)
+    c.run(max_q=0, out=out[:3])
+    c.check(out[:3], skip=(2,))
+    assert (out[1:3] == 0).all() and (out[3] == 7).all()
+    assert c.status.item() == pk.PA_DEV_BAD_CONTEXT
+
+
 @pytest.mark.parametrize("qlen", [4, 150])
 def test_strided_queries(qlen):
     c = Cross([qlen, qlen], [777, 130], 8, 8, 64, FP16, seed=13)
