@@ -76,7 +76,7 @@ size_t pa_beam_reorder_workspace_size(int B, int W, int max_blocks_per_seq) {
   if (B <= 0 || !beams_ok(B, W) || max_blocks_per_seq <= 0 ||
       pk::beam_reorder_in_one(B, W, max_blocks_per_seq))
     return 0;
-  return ((size_t)B + 1) * 16 + (size_t)B * max_blocks_per_seq * 4;
+  return ((size_t)B + 2) * 16 + (size_t)B * max_blocks_per_seq * 4;
 }
 
 pa_status pa_beam_reorder(const int32_t* parents, const int32_t* block_tables,
@@ -113,7 +113,7 @@ pa_status pa_beam_reorder(const int32_t* parents, const int32_t* block_tables,
   a.free_state_out = free_state_out;
   a.pairs = copy_pairs;
   a.counts = need > 0 ? static_cast<int64_t*>(workspace) : nullptr;
-  a.masks = need > 0 ? reinterpret_cast<uint32_t*>(a.counts + 2 * ((size_t)B + 1)) : nullptr;
+  a.masks = need > 0 ? reinterpret_cast<uint32_t*>(a.counts + 2 * ((size_t)B + 2)) : nullptr;
   a.status = status;
   a.B = B;
   a.W = W;

@@ -657,6 +657,8 @@ int clusters_at_once(int ranks) {
 void beam_select_shape(int B, int W, int V, int* groups, int* ranks) {
   const long long chunks = (V - 1) / kChunk + 1;  // of a row
   long long least = LLONG_MAX;
+  *groups = 1;
+  *ranks = W > kWarps ? 2 : 1;
   for (int r = 1; r <= kMaxCluster; r = r == 8 ? kMaxCluster : r + 1) {
     const int fit = clusters_at_once(r);
     if (fit == 0) continue;

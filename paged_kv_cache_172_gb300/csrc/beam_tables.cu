@@ -104,6 +104,8 @@ constexpr int kMaxRanks = 8;              // CTAs of a small batch
 constexpr int kRounds = 2;                // columns of a thread there
 constexpr int kStageBytes = 160 * 1024;   // rows that are brought to shared memory
 
+constexpr int kScanFrom = 4096;           // requests whose counts are summed up once
+
 enum Pass { kCluster, kCount, kWrite };
 
 // A CTA's shared memory: its requests' rows (STAGED), then for each beam its parent, its
@@ -164,8 +166,14 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   uint32_t first_mask = 0;                 // ... and of the thread's first column
   if (P == kWrite) {
     if (tid < M) first_mask = a.masks[(size_t)b0 * M + tid];
+    if (a.B >= kScanFrom && tid == 0) {  // (summed up: see beam_scan_kernel)
+      t = a.counts[2 * b0];
+      d = a.counts[2 * b0 + 1];
+      ta = a.counts[2 * a.B + 2];
+      da = a.counts[2 * a.B + 3];
+    }
 #pragma unroll 1
-    for (int b = tid; b < a.B; b += kThreads) {
+    for (int b = tid; b < a.B && a.B < kScanFrom; b += kThreads) {
       const long long x = a.counts[2 * b], y = a.counts[2 * b + 1];
       ta += x;
       da += y;
@@ -430,6 +438,53 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   }
 }
 
+// Many requests' counts to those of the requests before each, and of all behind the state;
+// neighbouring requests to a thread.  (Every CTA of the second launch adding them up took
+// 69.4 us for 4,096 requests of 8 beams, this 67.5, and 4,054 and 836 for 65,536 of one; for fewer the launch
+// costs 1.5 us more than it gives.)
+constexpr int kScanThreads = 1024;
+__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamReorderArgs a) {
+  __shared__ long long s_sum[2][kScanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int each = (a.B + kScanThreads - 1) / kScanThreads;
+  const int b0 = min(tid * each, a.B), b1 = min(b0 + each, a.B);
+  long long own[2] = {0, 0}, x[2];
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) own[e] += a.counts[2 * (size_t)b + e];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {  // of the threads up to this one, then of the warps before
+    x[e] = own[e];
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long y = __shfl_up_sync(kAll, x[e], k);
+      if (lane >= k) x[e] += y;
+    }
+    if (lane == 31) s_sum[e][warp] = x[e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    long long y = lane < warp ? s_sum[e][lane] : 0;
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) y += __shfl_xor_sync(kAll, y, k);
+    x[e] += y;
+    if (tid == kScanThreads - 1) a.counts[2 * (size_t)a.B + 2 + e] = x[e];
+    x[e] -= own[e];
+  }
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long y = a.counts[2 * (size_t)b + e];
+      a.counts[2 * (size_t)b + e] = x[e];
+      x[e] += y;
+    }
+}
+
 template <int WM>
 cudaError_t launch_reorder_t(const BeamReorderArgs& a, cudaStream_t stream) {
   constexpr int kMost = 224 * 1024;
@@ -454,7 +509,14 @@ cudaError_t launch_reorder_t(const BeamReorderArgs& a, cudaStream_t stream) {
   }
   cfg.gridDim = dim3(a.B);
   auto both = [&](auto count, auto write) {
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, count, a);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, count, a);
+    if (e == cudaSuccess && a.B >= kScanFrom) {
+      cudaLaunchConfig_t one = cfg;
+      one.gridDim = dim3(1);
+      one.blockDim = dim3(kScanThreads);
+      one.dynamicSmemBytes = 0;
+      e = cudaLaunchKernelEx(&one, beam_scan_kernel, a);
+    }
     return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, write, a);
   };
   const bool staged = (long long)a.W * a.M * 4 <= kStageBytes;
@@ -656,10 +718,13 @@ __global__ void __launch_bounds__(kBackThreads)
 
 }  // namespace
 
-// One cluster, or a CTA to a request and two launches: what the cluster's CTAs hold.
+// One cluster, or a CTA to a request and two launches (6 to 7 us): the cluster is quicker
+// while a CTA has at most 32 rows of 4,096 entries in all (a batch of 32 requests of 4 beams
+// 4.9 us in one and 5.9 in two, of 64 5.8 and 6.1, of 80 7.3 and 6.1; 16 of 8 beams in 256
+// columns 5.8 and 6.9, 24 7.7 and 6.9).
 bool beam_reorder_in_one(int B, int W, int M) {
   const long long each = (B + kMaxRanks - 1) / kMaxRanks;  // requests of a CTA
-  return each * M <= kRounds * kThreads && each <= 64 && each * W * M * 4 <= kStageBytes;
+  return each * M <= kRounds * kThreads && each * W <= 32 && each * W * M <= 4096;
 }
 
 cudaError_t launch_beam_reorder(const BeamReorderArgs& a, cudaStream_t stream) {

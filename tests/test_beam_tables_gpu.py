@@ -102,7 +102,9 @@ def test_reorder(W, bs, in_place):
 @pytest.mark.parametrize("B,W,longest,M", [(64, 4, 2000, None), (1, 8, 80000, 6000),
                                           (300, 2, 300, 40), (1100, 1, 40, 4),
                                           (40, 32, 1000, None), (1024, 8, 30, 4),
-                                          (1025, 8, 30, 4)])
+                                          (1025, 8, 30, 4), (511, 2, 700, 50),
+                                          (512, 2, 700, 50), (2500, 4, 100, 9),
+                                          (20000, 1, 40, 3)])
 def test_reorder_by_requests(B, W, longest, M, in_place):
     """Batches past one CTA, and at its border."""
     rng = np.random.default_rng(B)
