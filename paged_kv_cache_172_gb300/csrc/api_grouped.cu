@@ -332,7 +332,8 @@ pa_status pa_cross_attention(const void* q, const void* k, const void* v,
   const bool few = cross_few(B, T, H, Hkv, D, max_q_len, max_kv_len);
   if (!few && pk::grouped_span(H / Hkv) == 0) return PA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return PA_OK;
-  if (!q_offsets || !kv_starts || !kv_lens || !out || !aligned16(out) || !rows_ok(q, q_stride, H, D))
+  if (!q_offsets || !kv_starts || !kv_lens || !out || !aligned16(out) ||
+      !rows_ok(q, q_stride, H, D))
     return PA_ERR_INVALID;
   if (Tk == 0) {  // no request has states: a map over the queries, of which nothing is read
     k = v = q;

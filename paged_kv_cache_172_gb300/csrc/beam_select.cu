@@ -25,7 +25,13 @@
 // alignment, so equal rows have equal sums.
 //
 // Bound: HBM, or, for few rows, the trip from the logits to the lists to the merge, on
-// which the code itself comes from memory: it is kept short.
+// which the code itself comes from memory: it is kept short (24 to 31 KB a kernel).  A warp
+// takes 0.65 us to a chunk of 512 values, whatever their type, where an SM has 16 warps.
+// Measured (GB300, in a replayed graph): one request of 4 beams and 32,000 fp32 logits
+// 6.0 us; 64 of 4 and 50,001 bf16 in rows of odd lengths 14.7 us; 32 of 16 and 255,999
+// fp32, of which 430 MB are live beams', 82 us, 5.2 TB/s, 0.77 of the copy rate (clusters
+// of 4 on 128 SMs, each at the 50 bytes a ns that an SM takes in).  There chunks of 256
+// values took 143 us, chunks without a ring 116, two CTAs to an SM with half the ring 84.
 #include <cuda_bf16.h>
 #include <float.h>
 #include <limits.h>
@@ -144,7 +150,8 @@ struct Piece {
     const uint8_t* src = reinterpret_cast<const uint8_t*>(from) + at;
 #pragma unroll
     for (int q = 0; q < kCopies; ++q)
-      if (at + q * 512 < bytes) copy_async(to + q * 512, src + q * 512, min(bytes - at - q * 512, 16));
+      if (at + q * 512 < bytes)
+        copy_async(to + q * 512, src + q * 512, min(bytes - at - q * 512, 16));
     if (!VEC && lane == 0 && at + kBytes < bytes)
       copy_async(to + kBytes, src + kBytes, min(bytes - at - kBytes, 16));
     copy_commit();
@@ -567,7 +574,8 @@ __global__ void __launch_bounds__(32 * kWarps) beam_choose_kernel(const BeamSele
   }
 #pragma unroll 1
   for (int w = warp; w < W; w += kWarps)
-    if (lane < W && (alive >> w & 1)) s_top[w * W + lane] = a.ws_top[(size_t)(b * W + w) * W + lane];
+    if (lane < W && (alive >> w & 1))
+      s_top[w * W + lane] = a.ws_top[(size_t)(b * W + w) * W + lane];
   __syncthreads();
   choose(a, b, alive, s_top, s_cand, s_lse, s_score, score, end_x);
 }
