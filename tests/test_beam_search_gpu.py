@@ -324,3 +324,58 @@ def test_block_copy_of_bf16_pools():
         pk.pa_block_copy(k, v.half(), ints([[0, 5]], torch.int64))
     with pytest.raises(TypeError):
         pk.pa_block_copy(k.float(), v.float(), ints([[0, 5]], torch.int64))
+
+
+def test_two_calls_at_once():
+    """Calls on two streams at a time, each with outputs and a workspace of its own, give what
+    they give alone."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    sides = []
+    for i in range(2):
+        W, V, bs = 16, 140000, 16
+        logits = torch.randn(W, V, generator=g, device=DEV)
+        scores = -torch.rand(1, W, generator=g, device=DEV)
+        q = torch.randn(700, 8, 64, generator=g, device=DEV).half()
+        k, v = (torch.randn(9000, 4, 64, generator=g, device=DEV).half() for _ in range(2))
+        B, M = 300, 40
+        tables = torch.randperm(B * 4 * M, generator=torch.Generator().manual_seed(i)).int()
+        tables = tables.view(B * 4, M).to(DEV)
+        lens = torch.randint(1, M * bs, (B,), generator=g, device=DEV).int().repeat_interleave(4)
+        ring, state = ints(np.arange(B * 4 * M)), ints([0, 0], torch.int64)
+        parents = torch.randint(0, 4, (B, 4), generator=g, device=DEV).int()
+        # blocks of other rows for the copies: all of them are held, so the ring is empty
+        lens = lens // bs * bs
+
+        def call(out, stream, logits=logits, scores=scores, q=q, k=k, v=v, tables=tables,
+                 lens=lens, ring=ring, state=state, parents=parents):
+            step, att, few, moved, ws = out
+            pk.pa_beam_select(logits, scores, 3, out=step, workspace=ws[0], stream=stream)
+            for x, n, w in ((att, 700, ws[1]), (few, 2, ws[2])):
+                pk.pa_cross_attention(q[:n], k, v, ints([0, n]), ints([0]), ints([9000]), 0.125,
+                                      n, 9000, out=x, workspace=w, stream=stream)
+            pk.pa_beam_reorder(parents, tables, lens, ring.clone(), state, bs, out=moved,
+                               workspace=ws[3], stream=stream)
+
+        def room():
+            sizes = (pk.pa_beam_select_workspace_size(1, W, V),
+                     pk.pa_cross_attention_workspace_size(1, 700, 8, 4, 64, 700, 9000),
+                     pk.pa_cross_attention_workspace_size(1, 2, 8, 4, 64, 2, 9000),
+                     pk.pa_beam_reorder_workspace_size(B, 4, M))
+            return (pk.BeamStep.empty(1, W, DEV), torch.empty_like(q), torch.empty_like(q[:2]),
+                    pk.BeamTables.empty(B * 4, M, DEV),
+                    [torch.empty(max(16, n), dtype=torch.uint8, device=DEV) for n in sizes])
+        sides.append((call, room(), room(), torch.cuda.Stream()))
+
+    def results(out):
+        return [*out[0], out[1], out[2], *out[3]]
+    for call, alone, _, _ in sides:
+        call(alone, None)
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for call, _, out, stream in sides:
+            with torch.cuda.stream(stream):
+                call(out, stream)
+    torch.cuda.synchronize()
+    for _, alone, out, _ in sides:
+        for x, y in zip(results(alone), results(out)):
+            assert torch.equal(x, y)
