@@ -43,10 +43,10 @@
 // room, every tile's next S is computed while its softmax still works on the last one, and
 // the softmax bounds the steady state: 2,000 cycles a pair of tiles, where its exponentials,
 // sums and conversions are 1,196 of a scheduler's, the rest loads, stores and waits, and the
-// four products 1,080 of the tensor core's.  8 encoder sequences of 500-4,096, 16 heads: 169 us, 1,060 TFLOP/s,
-// 0.55 of the burst rate (one S region 180 us, P told in halves 178; the same at D = 128
-// takes 225).  Two threads to a row, 16 softmax warps, took 204 us, the next S loaded while
-// P is stored 185: loads then wait for the products.  16 requests of
+// four products 1,080 of the tensor core's.  8 encoder sequences of 500-4,096, 16 heads:
+// 169 us, 1,060 TFLOP/s, 0.55 of the burst rate (one S region 180 us, P told in halves 178;
+// the same at D = 128 takes 225).  Two threads to a row, 16 softmax warps, took 204 us, the
+// next S loaded while P is stored 185: loads then wait for the products.  16 requests of
 // 1-400 queries on 0-4,096 keys, 40 on 8, D = 128: 145 us, 1,160 TFLOP/s (0.60): S chain,
 // start (10,000 cycles), three to four units a CTA of unequal length.
 //
