@@ -53,6 +53,7 @@ constexpr int kEach = 16;           // values of a lane and chunk
 constexpr int kChunk = 32 * kEach;  // values of a warp's chunk
 constexpr int kRing = 8320;         // bytes of a warp's ring: four or eight chunks and 16 each
 constexpr int kMany = 64;           // values of a chunk that are too many to be inserted
+constexpr int kManyLanes = 8;       // lanes whose values are merged rather than inserted
 constexpr int kFewBeams = 8;        // most for which W rounds of a maximum are done
 constexpr int kMaxPieces = 64;      // of a row: two lists to a lane of the merge
 constexpr int kMaxCluster = 16;
@@ -194,25 +195,32 @@ __device__ __forceinline__ float pick(const float (&x)[kEach], int i) {
   return i & 1 ? y[1] : y[0];
 }
 
-// The 32 largest of two keys a lane, in order: mine in order, other not.  A bitonic sort of
-// the others, the larger of every pair of opposite places, a bitonic merge.
+// The 32 largest of two keys a lane, in order: mine in order, rising the other way round: the
+// larger of every two, a bitonic merge.
+__device__ __forceinline__ Key merge_sorted(Key mine, Key rising) {
+  const int lane = threadIdx.x & 31;
+  Key x = mine > rising ? mine : rising;
+#pragma unroll 1
+  for (int j = 16; j > 0; j >>= 1) {
+    const Key y = __shfl_xor_sync(kAll, x, j);
+    x = (x > y) == ((lane & j) == 0) ? x : y;
+  }
+  return x;
+}
+
+// The same with the others in any order: a bitonic sort ahead of it.
 __device__ __forceinline__ Key merge_lanes(Key mine, Key other) {
   const int lane = threadIdx.x & 31;
   Key x = other;
 #pragma unroll 1
-  for (int k = 2; k <= 64; k <<= 1) {
-    if (k == 64) {
-      const Key y = __shfl_xor_sync(kAll, x, 31);
-      x = mine > y ? mine : y;
-    }
+  for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll 1
-    for (int j = min(k, 32) >> 1; j > 0; j >>= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
       const Key y = __shfl_xor_sync(kAll, x, j);
-      const bool larger = ((lane & k) == 0) == ((lane & j) == 0);
-      x = (x > y) == larger ? x : y;
+      const bool smaller = ((lane & k & 31) == 0) == ((lane & j) == 0);
+      x = (x < y) == smaller ? x : y;
     }
-  }
-  return x;
+  return merge_sorted(mine, x);
 }
 
 __device__ __forceinline__ float largest(const float (&x)[kEach]) {
@@ -289,7 +297,9 @@ __device__ __forceinline__ Key scan(const T* row, int begin, int end, int eos, i
       hits = 0;
 #pragma unroll
       for (int j = 0; j < kEach; ++j) hits |= x[j] >= t ? 1u << j : 0u;
-      if (__reduce_add_sync(kAll, (unsigned)__popc(hits)) <= kMany) break;
+      if (FEW ? __reduce_add_sync(kAll, (unsigned)__popc(hits)) <= kMany
+              : __popc(__ballot_sync(kAll, hits != 0)) <= kManyLanes)
+        break;
       if constexpr (FEW) {
         // The lanes' maxima, largest first: W values reach the W-th.
         uint32_t o = ordered(mt);
@@ -518,9 +528,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamS
       // Nothing allowed (a sum of 0) gives no candidate; NaN or +inf among the logits neither.
       if (isnan(l) && lane == 0) flag_status(a.status, PA_DEV_BAD_LOGITS);
       if (lane == 0) s_lse[w] = l > 0.f ? (double)M + log_of(l) : -INFINITY;
+    } else if (const Key* mine = keys + r * pieces * W; !FEW && pieces < W) {
+      // One after the other.
+      Key kept = lane < W ? mine[lane] : 0;
+#pragma unroll 1
+      for (int p = 1; p < pieces; ++p)
+        kept = merge_sorted(kept, 31 - lane < W ? mine[p * W + 31 - lane] : 0);
+      if (lane < W) top[w * W + lane] = kept;
     } else {
       // Rounds of the largest head of the row's lists, two to a lane.
-      const Key* mine = keys + r * pieces * W;
       int at[2] = {lane * W, (lane + 32) * W};
       Key head[2], kept = 0;
 #pragma unroll
