@@ -14,11 +14,12 @@
 // a threshold are inserted one by one: the W-th of the list, or what the row's other warps
 // of the CTA know.  In a chunk where many values reach that (the first one) it is raised to
 // the W-th largest of the lanes' maxima first (W rounds), or, for more than 8 beams, these
-// are merged into the list as a whole until few are left (W rounds and the insertions after
-// them against the merges: 32 beams of 260,000 logits 66 -> 43 us, 16 of 256,000 27.6 ->
-// 25.4, 32 requests of 16 83.6 -> 82.2; a kernel of its own, since its code costs the small
-// calls 0.2 us).  The cluster's first CTA then merges the pieces' lists by beam and the
-// beams' lists, in order, by as many rounds of a maximum over the lanes as there are beams.
+// are merged into the list as a whole until few lanes are left.  The cluster's first CTA then
+// merges the pieces' lists by beam and the beams' lists, in order: by as many rounds of a
+// maximum over the lists' heads as there are beams, or, for more than 8, by bitonic merges.
+// (The merges against rounds, with the lanes' maxima merged either way: 32 beams of 32,000
+// bf16 logits 21.7 -> 16.3 us, 156 requests of 32 x 1,152 fp32 88 -> 50, 2 of 16 x 140,000
+// bf16 17.2 -> 16.6; a kernel of its own, since its code costs the small calls 0.2 us.)
 //
 // Rounding: sums in fp32, candidates in 64 bits (two beams' can be nearer than fp32 tells
 // apart), the scores once to fp32.  A sum goes by the values' index and not by the row's
@@ -370,50 +371,114 @@ __device__ __forceinline__ int small_div(int a, int b) {
   return (int)__fdividef((float)a + 0.5f, (float)b);
 }
 
+// The 32 best of two lists of candidates, (value, beam and place), over the lanes, the second
+// one the other way round: the better of every two, a bitonic merge.
+__device__ __forceinline__ void merge_best(Key& c, uint32_t& id, Key other, uint32_t other_id) {
+  const int lane = threadIdx.x & 31;
+  auto ahead = [](Key a, uint32_t i, Key b, uint32_t j) { return a > b || (a == b && i < j); };
+  if (ahead(other, other_id, c, id)) {
+    c = other;
+    id = other_id;
+  }
+#pragma unroll 1
+  for (int j = 16; j > 0; j >>= 1) {
+    const Key y = __shfl_xor_sync(kAll, c, j);
+    const uint32_t yi = __shfl_xor_sync(kAll, id, j);
+    if (ahead(c, id, y, yi) != ((lane & j) == 0)) {
+      c = y;
+      id = yi;
+    }
+  }
+}
+
 // What is chosen from the beams' best keys, top [W][W], and the logarithms of their sums; a
 // lane of the first warp has its beam's score and the logit of its end.  cand: room for
-// [W][W]; all threads of a CTA, a barrier ahead of it.
+// kCand keys; all threads of a CTA, a barrier ahead of it.  Few beams' lists by W rounds of a
+// maximum over their heads, more of them by merges: a warp's two, then four warps' each, then
+// all (32 beams 8,600 cycles in rounds).
+constexpr int kCand = kWarps * 32 * 3 / 2;
+template <bool FEW>
 __device__ __forceinline__ void choose(const BeamSelectArgs& a, int b, uint32_t alive,
                                        const Key* top, Key* cand, const double* s_lse,
                                        const float* s_score, float score, float end_x) {
   const int W = a.W, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool here = alive >> lane & 1;
   // ---- candidates (0: none; what a finite number is ordered as is not)
-#pragma unroll 1
-  for (int w = warp; w < W; w += kWarps) {
+  auto candidate = [&](int w) -> Key {
     const double lse = s_lse[w];
-    if (lane < W && (alive >> w & 1)) {
-      const Key k = top[w * W + lane];
-      cand[w * W + lane] =
-          k != 0 && lse > -INFINITY
-              ? ordered((double)s_score[w] + ((double)value_of(k) - lse) + 0.0)
-              : 0;
-    }
-  }
-  __syncthreads();
-  if (warp > 0) return;
-  // ---- the choice: lane i holds the next candidate of beam i
-  int at = lane * W;
-  Key c = here ? cand[at] : 0, k = here ? top[at] : 0;
+    const Key k = lane < W && (alive >> w & 1) ? top[w * W + lane] : 0;
+    return k != 0 && lse > -INFINITY
+               ? ordered((double)s_score[w] + ((double)value_of(k) - lse) + 0.0)
+               : 0;
+  };
   Key my_c = 0, my_key = 0, last_c = 0, last_key = 0;  // of place `lane`; of the last place
   int my_beam = lane, last_beam = 0;
+  if constexpr (FEW) {
+    if (warp < W) {
+      const Key c = candidate(warp);
+      if (lane < W) cand[warp * W + lane] = c;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    // ---- the choice: lane i holds the next candidate of beam i
+    int at = lane * W;
+    Key c = here ? cand[at] : 0, k = here ? top[at] : 0;
 #pragma unroll 1
-  for (int j = 0; j < W; ++j) {
-    const Key best = warp_max(c);
-    last_c = best;
-    if (best == 0) break;
-    last_beam = __ffs(__ballot_sync(kAll, c == best)) - 1;
-    last_key = __shfl_sync(kAll, k, last_beam);
-    if (lane == j) {
-      my_c = best;
-      my_beam = last_beam;
-      my_key = last_key;
+    for (int j = 0; j < W; ++j) {
+      const Key best = warp_max(c);
+      last_c = best;
+      if (best == 0) break;
+      last_beam = __ffs(__ballot_sync(kAll, c == best)) - 1;
+      last_key = __shfl_sync(kAll, k, last_beam);
+      if (lane == j) {
+        my_c = best;
+        my_beam = last_beam;
+        my_key = last_key;
+      }
+      if (lane == last_beam) {
+        ++at;
+        c = at < (lane + 1) * W ? cand[at] : 0;
+        k = at < (lane + 1) * W ? top[at] : 0;
+      }
     }
-    if (lane == last_beam) {
-      ++at;
-      c = at < (lane + 1) * W ? cand[at] : 0;
-      k = at < (lane + 1) * W ? top[at] : 0;
+  } else {
+    uint32_t* ids = reinterpret_cast<uint32_t*>(cand + kWarps * 32);
+    const int lists = min(W, kWarps);
+    uint32_t id = warp << 5 | lane;
+    if (warp < lists) {
+      my_c = candidate(warp);
+      if (warp + kWarps < W) {
+        const Key c = candidate(warp + kWarps);
+        merge_best(my_c, id, __shfl_xor_sync(kAll, c, 31), (warp + kWarps) << 5 | (31 - lane));
+      }
+      cand[warp * 32 + lane] = my_c;
+      ids[warp * 32 + lane] = id;
     }
+    __syncthreads();
+#pragma unroll 1
+    for (int step = 1; step < kWarps; step *= 4) {  // lists `step` apart, four to a warp
+      const int first = warp * 4 * step;
+      if (first < lists) {
+        my_c = cand[first * 32 + lane];
+        id = ids[first * 32 + lane];
+#pragma unroll 1
+        for (int i = 1; i < 4 && first + i * step < lists; ++i) {
+          const int from = (first + i * step) * 32 + 31 - lane;
+          merge_best(my_c, id, cand[from], ids[from]);
+        }
+        cand[first * 32 + lane] = my_c;
+        ids[first * 32 + lane] = id;
+      }
+      __syncthreads();
+    }
+    if (warp > 0) return;
+    if (my_c != 0) {
+      my_beam = (int)(id >> 5);
+      my_key = top[my_beam * W + (id & 31)];
+    }
+    last_c = __shfl_sync(kAll, my_c, W - 1);
+    last_key = __shfl_sync(kAll, my_key, W - 1);
+    last_beam = __shfl_sync(kAll, my_beam, W - 1);
   }
   if (lane >= W) return;
   const int o = b * W + lane;
@@ -477,7 +542,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamS
   Key* keys = reinterpret_cast<Key*>(s_dyn + kWarps * kRing);
   float2* mls = reinterpret_cast<float2*>(keys + ranks * kWarps * W);
   Key* top = reinterpret_cast<Key*>(mls + ranks * kWarps);
-  Key* cand = top + W * W;
+  Key* cand = reinterpret_cast<Key*>(s_dyn);  // (over the rings)
   __syncthreads();
   // A row's pieces go to neighbouring warps, which share thresholds.
   const int per = small_div(rows * pieces + ranks - 1, ranks), task = rank * per + warp;
@@ -565,13 +630,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamS
     }
     return;
   }
-  choose(a, b, alive, top, cand, s_lse, s_score, score, end_x);
+  choose<FEW>(a, b, alive, top, cand, s_lse, s_score, score, end_x);
 }
 
 // The choice where the rows of a request were shared out among several clusters.
-template <typename T>
+template <typename T, bool FEW>
 __global__ void __launch_bounds__(32 * kWarps) beam_choose_kernel(const BeamSelectArgs a) {
-  __shared__ Key s_top[kMaxBeams * kMaxBeams], s_cand[kMaxBeams * kMaxBeams];
+  __shared__ Key s_top[kMaxBeams * kMaxBeams], s_cand[kCand];
   __shared__ double s_lse[32];
   __shared__ float s_score[32];
   const int b = blockIdx.x, W = a.W, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -593,11 +658,11 @@ __global__ void __launch_bounds__(32 * kWarps) beam_choose_kernel(const BeamSele
     if (lane < W && (alive >> w & 1))
       s_top[w * W + lane] = a.ws_top[(size_t)(b * W + w) * W + lane];
   __syncthreads();
-  choose(a, b, alive, s_top, s_cand, s_lse, s_score, score, end_x);
+  choose<FEW>(a, b, alive, s_top, s_cand, s_lse, s_score, score, end_x);
 }
 
 int dynamic_bytes(int W, int ranks) {
-  return kWarps * kRing + ranks * kWarps * (W + 1) * 8 + 2 * W * W * 8;
+  return kWarps * kRing + ranks * kWarps * (W + 1) * 8 + W * W * 8;
 }
 
 template <typename T, bool VEC, bool FEW>
@@ -627,7 +692,7 @@ cudaError_t launch_t(const BeamSelectArgs& a, cudaStream_t stream) {
   cfg.gridDim = dim3(a.B);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, beam_choose_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, beam_choose_kernel<T, FEW>, a);
 }
 
 template <typename T>
@@ -673,13 +738,14 @@ int clusters_at_once(int ranks) {
 // of 0.05 us, by what was measured: for every time that the GPU is filled with clusters, the
 // chunks of a warp (the more warps an SM has, the longer) and what comes before and after
 // them, which grows with the beams; and the second launch.  What it chooses is within 8 % of
-// the best of up to 25 others over 31 sizes (one request of one beam and 32,000 logits to 80
-// of 16 x 128,000).  Against the largest cluster a request whose CTAs find an SM each: one
-// request of 32 x 260,000 fp32 logits 56.8 -> 28.8 us (32 clusters of 4), one of 16 x 256,000
-// 28.5 -> 18.3, 8 of 32 x 260,000 84.6 -> 62.5, 16 of these 159 -> 101; 80 requests of
-// 16 x 128,000 bf16, more than half of the SMs, 121 -> 113 (clusters of 3, twice).
+// the best of up to 25 others over 40 sizes (one request of one beam and 32,000 logits to 80
+// of 16 x 128,000).  Against the largest cluster a request with an SM to each CTA: one
+// request of 32 x 260,000 fp32 logits 48 -> 24 us (32 clusters of 4), one of 16 x 256,000
+// 28 -> 17.2, 8 of 32 x 260,000 74 -> 56.6, 16 of these 150 (two fills) -> 95; 80 requests
+// of 16 x 128,000 bf16, more than half of the SMs, 119 -> 108 (clusters of 3, two fills).
 void beam_select_shape(int B, int W, int V, int* groups, int* ranks) {
   const long long chunks = (V - 1) / kChunk + 1;  // of a row
+  const int around = 9 * W < 100 + 5 * W / 2 ? 70 + 9 * W : 170 + 5 * W / 2;
   long long least = LLONG_MAX;
   *groups = 1;
   *ranks = W > kWarps ? 2 : 1;
@@ -697,8 +763,8 @@ void beam_select_shape(int B, int W, int V, int* groups, int* ranks) {
       const long long fills = ((long long)B * g - 1) / fit + 1;
       const int warps = (rows * pieces - 1) / r + 1;  // of a CTA
       const long long time =
-          fills * (80 + 10 * W + (10 + warps) * ((chunks - 1) / pieces + 1) / 2) +
-          (g > 1 ? 40 : 0);
+          fills * (around + 5 * rows / 2 + (10 + warps) * ((chunks - 1) / pieces + 1) / 2) +
+          (fills - 1) * 60 + (g > 1 ? 40 : 0);
       if (time < least) {
         least = time;
         *groups = g;
