@@ -302,14 +302,17 @@ __device__ __forceinline__ Key scan(const T* row, int begin, int end, int eos, i
               : __popc(__ballot_sync(kAll, hits != 0)) <= kManyLanes)
         break;
       if constexpr (FEW) {
-        // The lanes' maxima, largest first: W values reach the W-th.
-        uint32_t o = ordered(mt);
+        // The lanes' maxima, largest first: W values reach the W-th.  (A lane whose values do
+        // not reach t, or are all NaN, has none.)
+        uint32_t o = mt >= t ? ordered(mt) : 0;
 #pragma unroll 1
         for (int j = 0; j < W; ++j) {
           reached = __reduce_max_sync(kAll, o);
           if (lane == __ffs(__ballot_sync(kAll, o == reached)) - 1) o = 0;
         }
-        if (unordered(reached) <= t) break;  // (equal ones: all of them)
+        // Equal ones: all of them.  So are those of fewer than W lanes, whose W-th is 0, a NaN.
+        // (Every other turn raises t, and to what it finds again: the second is the last.)
+        if (!(unordered(reached) > t)) break;
       } else {
         // The lanes' maxima into the list at once.
         int at = 0;
