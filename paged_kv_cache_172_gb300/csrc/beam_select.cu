@@ -22,8 +22,8 @@
 // bf16 17.2 -> 16.6; a kernel of its own, since its code costs the small calls 0.2 us.)
 //
 // Rounding: sums in fp32, candidates in 64 bits (two beams' can be nearer than fp32 tells
-// apart), the scores once to fp32.  A sum goes by the values' index and not by the row's
-// alignment, so equal rows have equal sums.
+// apart), the scores once to fp32.  A sum goes by the values' index, and not by the row's
+// alignment or by the cluster that takes it, so equal rows of a request have equal sums.
 //
 // Bound: HBM, or, for few rows, the trip from the logits to the lists to the merge, on
 // which the code itself comes from memory: it is kept short (24 to 31 KB a kernel).  A warp
@@ -520,7 +520,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamS
   const float score = lane < W ? a.scores[b * W + lane] : -INFINITY;
   bool here = isfinite(score);
   uint32_t alive = __ballot_sync(kAll, here);
+  // Rows of a cluster, at most: the pieces go by these, so that all rows of a request are cut
+  // alike and equal ones have equal sums.
+  int most = __popc(alive);
   if (a.groups > 1) {  // every groups-th of them
+    most = small_div(most + a.groups - 1, a.groups);
     const int nth = __popc(alive & ((1u << lane) - 1));
     here = here && nth % a.groups == group;
     alive = __ballot_sync(kAll, here);
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) beam_select_kernel(const BeamS
   const int nth = __popc(alive & ((1u << lane) - 1));
   auto live_beam = [&](int i) { return __ffs(__ballot_sync(kAll, here && nth == i)) - 1; };
   // Pieces of a row, multiples of 16 values, the last ones may be empty.
-  const int pieces = min(kMaxPieces, small_div(ranks * kWarps, max(rows, 1)));
+  const int pieces = min(kMaxPieces, small_div(ranks * kWarps, max(most, 1)));
   const int length = ((int)(__fdividef((float)a.V, (float)pieces) * 1.000001f) + 16) & ~15;
   // What is merged, in the first CTA: per list, [row][piece], its keys, maximum and sum;
   // per beam its best keys and what they are as candidates.
