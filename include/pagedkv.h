@@ -615,10 +615,11 @@ pa_status pa_chunk_attention(const void *q, const void *k_cache, const void *v_c
  * max_q_len, max_kv_len  host-side bounds on the requests' lengths: a request past one
  *           of them, or whose keys leave [0, Tk), is flagged PA_DEV_BAD_CONTEXT and its
  *           rows are zeros (max_q_len above T counts as T, 0 as 1)
- * D in {64, 128}; scale > 0.  With max_q_len * H / Hkv at most 16 (up to 48 in small
- * calls; B at most 65535) the kernel of pa_decode_grouped serves the call, to its
- * precision; otherwise that of pa_prompt_attention, to its, and H / Hkv is at most 128
- * (else PA_ERR_UNSUPPORTED).
+ * D in {64, 128}; scale > 0.  With max_q_len * H / Hkv at most 16 (up to 48 where B is 1
+ * or 2 and all its CTAs run at once; B at most 65535) the kernel of pa_decode_grouped
+ * serves the call, to its precision; otherwise that of pa_prompt_attention, to its, and
+ * H / Hkv is at most 128 (else PA_ERR_UNSUPPORTED).  So a request's last bits go by the
+ * call that it is in.
  *
  * workspace (16-byte aligned, may be NULL): with at least
  * pa_cross_attention_workspace_size(...) bytes few queries over many keys are cut into
@@ -686,8 +687,12 @@ pa_status pa_decode_grouped(const void *q, const void *k_cache, const void *v_ca
  *     c(w, v) = scores[w] + x_w[v] - log sum_u exp(x_w[u])
  * (log-probabilities in place of logits give the same).  The W best candidates
  * with v != eos_token are the next beams, best first; of equal ones the lowest
- * (w, v) comes first.  Candidates are compared as the definition has them: two of
- * one beam by their logits, two of different beams in 64 bits.  Written [B, W]:
+ * (w, v) comes first.  Two candidates of one beam are compared by their logits, two
+ * of different beams by their c in 64 bits, of which the sum under the logarithm is
+ * taken in fp32: equal rows of a request have equal sums, but different beams'
+ * candidates nearer than its error (at most 1.3e-5 + V * 2^-33 for logits in no
+ * particular order) can change places, and its last bits go by B, W, V, the beams that
+ * are there and the alignment of logits and row_stride.  Written [B, W]:
  *   tokens, parents  v and w of each
  *   new_scores       c, rounded once; may be scores itself
  *   ended_scores     by beam w: c(w, eos_token) if it is better than the last of
@@ -726,7 +731,10 @@ pa_status pa_beam_select(const void *logits, pa_dtype dtype, int64_t row_stride,
  * further one gets a block from the free list (the ring of pa_step_plan, first in, first
  * out, beams in order) in its place, and copy_pairs[b * W + w] = (old, new) for
  * pa_block_copy; of all other beams the pair is (0, 0), which copies nothing.  When n is
- * a multiple, pa_step_plan gives each beam its next block.
+ * a multiple, pa_step_plan gives each beam its next block.  This is for beams that are
+ * of one length, as a search's are: only last blocks are looked at, so that a half-full
+ * last block which a longer beam of the request holds as a full one is not copied for
+ * it, and the shorter beam's next token would be written among the longer one's.
  *
  * Back to the list: a block that rows of the request held at a column, and that none of
  * them holds there any more, is written to the ring behind the last one, requests in
@@ -773,9 +781,9 @@ pa_status pa_beam_reorder(const int32_t *parents, const int32_t *block_tables,
  * and beam w; its end is no token of it).
  *
  * tokens, parents [S, B, W] int32; lengths, beams [B, K] int32; out [B, K, S] int32.
- * A length outside [0, S] or a beam outside [0, W) gives pad_token alone, a parent outside
- * [0, W) pad_token in the steps before it; both flagged PA_DEV_BAD_BEAM.  W and K at most
- * 32 (else PA_ERR_UNSUPPORTED), S below 2^26 - 1024.
+ * A length outside [0, S] or, where there are tokens, a beam outside [0, W) gives
+ * pad_token alone, a parent outside [0, W) pad_token in the steps before it; both flagged
+ * PA_DEV_BAD_BEAM.  W and K at most 32 (else PA_ERR_UNSUPPORTED), S below 2^26 - 1024.
  * ------------------------------------------------------------------------- */
 pa_status pa_beam_backtrack(const int32_t *tokens, const int32_t *parents,
                             const int32_t *lengths, const int32_t *beams, int S, int B,

@@ -55,7 +55,8 @@ def pa_beam_select(logits, scores, eos_token=-1, pad_token=0, out=None, workspac
     parents slices of a history): tokens and parents of the next beams, best first,
     their scores, and by beam the score of its end with ``eos_token`` where that is
     better than the last of them (-inf elsewhere).  Places that nothing fills hold
-    ``pad_token``, their own index and -inf."""
+    ``pad_token``, their own index and -inf.  A beam with NaN or +inf among its logits
+    gives no candidate and is flagged."""
     name = "pa_beam_select"
     if out is None:
         if not isinstance(scores, torch.Tensor):
@@ -101,7 +102,9 @@ def pa_beam_reorder(parents, block_tables, context_lens, free_blocks, free_state
     of half-full last blocks are taken from; columns that hold the first shared_lens [B]
     tokens stay out of it.  Returns a BeamTables, in ``out`` when given (its tables,
     lengths and state may be the ones passed in); its copy_pairs [B*W, 2] go to
-    pa_block_copy before the next token is written."""
+    pa_block_copy before the next token is written.  The beams of a request are of one
+    length (of others, a half-full last block that a longer beam holds as a full one is
+    not copied)."""
     name = "pa_beam_reorder"
     if out is None:
         if not isinstance(block_tables, torch.Tensor):

@@ -288,8 +288,10 @@ static long long cross_parts(int B, int H, int Hkv, int D, int max_q, int max_kv
 // Cross attention: whether a request's rows, max_q_len * G to a K/V head, go to the kernel
 // of single tokens, which reads the keys once for every 16 of them.  Up to 16 they do (32
 // requests of 4 on up to 1,500 keys, 16 heads, D = 64: 23 us and 43 by tiles of 128 rows; of
-// 16 alike); up to 48 where all its CTAs run at once, as it begins and ends quicker (one
-// request of 32 on 1,500 keys 7.9 and 12.6 us; eight on 4,000 keys 38.8 and 35.2).
+// 16 alike); up to 48 for one or two requests where all its CTAs run at once, as it begins
+// and ends quicker (one request of 32 on 1,500 keys 7.1 us and 12.6).  From three requests on
+// it goes either way by the keys, and tiles serve them (three of 32 on 100 keys 4.1 us and
+// 6.0, on 1,500 11.4 and 14.8; four of 32 on 1,500 18.7 and 14.8, of 48 23.7 and 15.4).
 static bool cross_few(int B, int T, int H, int Hkv, int D, int max_q, int max_kv) {
   const long long cols = (long long)max_q * (H / Hkv);
   if (B > 65535 || (long long)T * H >= (1LL << 31) || cols > pk::kCrossFewMost) return false;

@@ -29,8 +29,8 @@
 // which the code itself comes from memory: it is kept short (24 to 31 KB a kernel).  A warp
 // takes 0.65 us to a chunk of 512 values, whatever their type, where an SM has 16 warps.
 // Measured (GB300, in a replayed graph): one request of 4 beams and 32,000 fp32 logits
-// 6.0 us; 64 of 4 and 50,001 bf16 in rows of odd lengths 14.7 us; 32 of 16 and 255,999
-// fp32, of which 430 MB are live beams', 81 us, 5.3 TB/s, 0.78 of the copy rate (clusters
+// 6.1 us; 64 of 4 and 50,001 bf16 in rows of odd lengths 14.8 us; 32 of 16 and 255,999
+// fp32, of which 430 MB are live beams', 80 us, 5.4 TB/s, 0.79 of the copy rate (clusters
 // of 4 on 128 SMs, each at the 50 bytes a ns that an SM takes in).  There chunks of 256
 // values took 143 us, chunks without a ring 116, two CTAs to an SM with half the ring 84.
 #include <cuda_bf16.h>

@@ -117,7 +117,7 @@ struct GroupedDecodeArgs {
   bool bf16;
 };
 // (query, head) pairs of a request and K/V head that the kernel of single tokens serves in
-// cross attention: always, and where its CTAs run at once.
+// cross attention: always, and for one or two requests where its CTAs run at once.
 constexpr int kCrossFew = 16, kCrossFewMost = 48;
 int grouped_decode_partition(int B, int H, int Hkv, int D, int max_context);
 // Whether that many partitions merge inside the launch, without a workspace.
